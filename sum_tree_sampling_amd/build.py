@@ -12,7 +12,8 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libper.so")
-SOURCES = ["per_api.hip", "tree_kernels.hip", "sample_kernels.hip", "rank_kernels.hip"]
+SOURCES = ["per_api.hip", "tree_kernels.hip", "sample_kernels.hip", "rank_kernels.hip",
+           "train_api.hip", "rows_kernels.hip", "scan_kernels.hip", "distill_kernels.hip"]
 PROBE_SRC = os.path.join(HERE, "probe", "latency_probe.hip")
 PROBE_LIB = os.path.join(HERE, "libper_probe.so")
 STAMPS_LIB = os.path.join(HERE, "libper_stamps.so")

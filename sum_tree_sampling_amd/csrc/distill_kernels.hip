@@ -1,0 +1,661 @@
+// distill_kernels.hip -- distillation from a teacher's top logits: per-row loss
+// and its gradient by the student's logits.
+//
+// With m the row's largest logit, S = sum exp((z - m) / tau) over all tokens
+// and S_r the same over the tokens of the rest, the gradient by z_j is
+//   w tau (e_j / S - p_j)             at a token of the teacher's top,
+//   w tau e_j (1 / S - p_r / S_r)     at the others (p_r = 0 without a rest),
+// so one coefficient serves the whole row and K places are put right after.
+//
+// A row is read in 16-byte chunks aligned in memory; chunk j holds the tokens
+// [j * kVec - mis, (j + 1) * kVec - mis).  The tokens of the top are marked in
+// a bitmap in LDS, so sums over the rest leave them out instead of
+// subtracting them, and repeated entries are found.
+
+#include "elem.h"
+#include "lanes.h"
+#include "train_internal.h"
+
+namespace per {
+namespace {
+
+constexpr float kNegInf = -__builtin_inff();
+
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ float ex2(float v) { return __builtin_amdgcn_exp2f(v); }
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int s = 0; s < 6; ++s) v = fmaxf(v, xor_lanes(v, s));
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int s = 0; s < 6; ++s) v += xor_lanes(v, s);
+  return v;
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int s = 0; s < 6; ++s) v += __shfl_xor(v, 1 << s);
+  return v;
+}
+
+// A row of logits as aligned chunks.
+template <typename T>
+struct Row {
+  const T* z;
+  int mis;        // tokens between the aligned address before the row and the row
+  uint32_t V;
+  uint32_t chunks;
+};
+template <typename T>
+__device__ __forceinline__ Row<T> row_of(const DistillArgs& a, int64_t n) {
+  Row<T> r;
+  r.z = static_cast<const T*>(a.z) + n * a.stride;
+  r.mis = (int)((reinterpret_cast<uintptr_t>(r.z) & 15) / sizeof(T));
+  r.V = (uint32_t)a.V;
+  r.chunks = (r.V + r.mis + kVec<T> - 1) / kVec<T>;
+  return r;
+}
+
+template <typename T>
+using Chunk = Pack<T, kVec<T>>;
+
+// Chunk j; -Inf where it reaches outside the row.
+template <typename T>
+__device__ __forceinline__ Chunk<T> load_chunk(const Row<T>& r, uint32_t j) {
+  const int64_t i0 = (int64_t)j * kVec<T> - r.mis;
+  Chunk<T> v;
+  if (i0 >= 0 && i0 + kVec<T> <= r.V) {
+    const T* p = static_cast<const T*>(__builtin_assume_aligned(r.z + i0, 16));
+    __builtin_memcpy(&v, p, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e)
+      v.v[e] = i0 + e >= 0 && i0 + e < r.V ? r.z[i0 + e] : (T)kNegInf;
+  }
+  return v;
+}
+
+// Hides where a chunk came from, so that the compiler keeps it packed between
+// two passes over it instead of holding its values as f32 (a row of 17 chunks
+// per thread would not fit the registers).
+template <typename T>
+__device__ __forceinline__ void keep_packed(Chunk<T>& v) {
+  uint4 u;
+  __builtin_memcpy(&u, &v, 16);
+  asm volatile("" : "+v"(u.x), "+v"(u.y), "+v"(u.z), "+v"(u.w));
+  __builtin_memcpy(&v, &u, 16);
+}
+
+// Stores kVec gradients at chunk j of a row of V tokens.
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* grad, const Row<T>& r, uint32_t j,
+                                            const float (&g)[kVec<T>]) {
+  const int64_t i0 = (int64_t)j * kVec<T> - r.mis;
+  if (i0 >= 0 && i0 + kVec<T> <= r.V) {
+    store_vals<T, kVec<T>>(grad + i0, g);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e)
+      if (i0 + e >= 0 && i0 + e < r.V) grad[i0 + e] = (T)g[e];
+  }
+}
+
+// ------------------------------------------------------------------ the teacher
+//
+// LDS of a workgroup: the K entries, then a bitmap over the tokens of chunks
+// [c0, c1) of the row.
+struct Lds {
+  int* idx;        // token, -1 where absent
+  float* p;        // teacher's probability (its logit before)
+  float* z;        // student's logit
+  uint32_t* bits;  // bit i - c0 * kVec + mis of token i
+};
+__device__ __forceinline__ Lds lds_of(char* mem, int K) {
+  Lds l;
+  l.idx = reinterpret_cast<int*>(mem);
+  l.p = reinterpret_cast<float*>(mem) + K;
+  l.z = reinterpret_cast<float*>(mem) + 2 * K;
+  l.bits = reinterpret_cast<uint32_t*>(mem) + 3 * K;
+  return l;
+}
+
+__device__ __forceinline__ float teacher_logit(const DistillArgs& a, int64_t at) {
+  if (a.t_type == 0) return static_cast<const float*>(a.t)[at];
+  if (a.t_type == 1) return (float)static_cast<const bf16_t*>(a.t)[at];
+  return (float)static_cast<const f16_t*>(a.t)[at];
+}
+
+struct Teacher {
+  double h;     // sum p log p
+  double ps;    // sum p
+  double rest;  // p_r
+  bool any;     // an entry is present
+  bool dup;     // two entries name one token of [c0, c1)
+};
+
+// One whole wave: entries to LDS, the bitmap of chunks [c0, c1), and the sums.
+// The K exponentials are taken in f64: the rest 1 - sum p would lose its digits
+// in f32 where the top holds nearly everything.
+template <typename T, bool TAIL>
+__device__ __forceinline__ Teacher teacher(const DistillArgs& a, const Row<T>& r, int64_t n,
+                                           const Lds& l, uint32_t c0, uint32_t c1) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t words = ((c1 - c0) * kVec<T> + 31) / 32;
+  for (uint32_t w = lane; w < words; w += 64) l.bits[w] = 0;
+  const int64_t lo = (int64_t)c0 * kVec<T> - r.mis;
+  const int64_t hi = (int64_t)c1 * kVec<T> - r.mis;
+  float tm = kNegInf;
+  bool dup = false, any = false;
+  for (int k = lane; k < a.K; k += 64) {
+    int i = a.tidx[n * a.K + k];
+    const float t = teacher_logit(a, n * a.K + k);
+    if (i < 0 || i >= (int64_t)r.V) i = -1;
+    l.idx[k] = i;
+    l.p[k] = t;
+    l.z[k] = i >= 0 ? (float)r.z[i] : 0.0f;
+    if (i >= 0) {
+      any = true;
+      tm = fmaxf(tm, t);
+      if (i >= lo && i < hi) {
+        const uint32_t bit = (uint32_t)(i - lo);
+        dup |= (atomicOr(&l.bits[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u;
+      }
+    }
+  }
+  tm = wave_max(tm);
+  double norm = 0.0;  // log of the normaliser of t / tau, relative to `ref`
+  const double ref = TAIL ? 0.0 : (tm == kNegInf ? 0.0 : (double)tm);
+  if (TAIL) {
+    norm = (double)a.tlse[n];
+  } else {
+    double s = 0.0;
+    for (int k = lane; k < a.K; k += 64)
+      if (l.idx[k] >= 0) s += exp(((double)l.p[k] - ref) * a.inv_tau);
+    norm = log(wave_sum(s));
+  }
+  Teacher o = {0.0, 0.0, 0.0, false, false};
+  for (int k = lane; k < a.K; k += 64) {
+    double p = 0.0;
+    if (l.idx[k] >= 0) {
+      const double lp = ((double)l.p[k] - ref) * a.inv_tau - norm;
+      p = exp(lp);
+      if (!(p == 0.0)) {
+        o.h += p * lp;
+        o.ps += p;
+      }
+    }
+    l.p[k] = (float)p;
+  }
+  o.h = wave_sum(o.h);
+  o.ps = wave_sum(o.ps);
+  if (TAIL) {
+    o.rest = 1.0 - o.ps;
+    if (o.rest < 0.0) o.rest = 0.0;
+  }
+  o.any = __any(any) && o.ps != 0.0;  // entries at -Inf are none
+  o.dup = __any(dup);
+  return o;
+}
+
+// The row's loss from the teacher's sums and the student's statistics, by one
+// whole wave.  The differences z - m are taken before they are summed, so that
+// logits at the type's lowest value cancel.
+__device__ __forceinline__ float row_loss(const DistillArgs& a, const Lds& l, const Teacher& t,
+                                          float m, float S, float Sr, bool tail) {
+  double d = 0.0;
+  for (int k = threadIdx.x & 63; k < a.K; k += 64)
+    if (l.idx[k] >= 0 && !(l.p[k] == 0.0f)) d += (double)l.p[k] * ((double)l.z[k] - (double)m);
+  const double logS = log((double)S);
+  double v = t.h + t.ps * logS - wave_sum(d) * a.inv_tau;
+  if (tail && t.rest > 0.0 && Sr != 0.0f) v += t.rest * (log(t.rest) - log((double)Sr) + logS);
+  return (float)(v * (double)a.tau * (double)a.tau);
+}
+
+// Puts right the gradient at the teacher's tokens within [lo, hi).
+template <typename T>
+__device__ __forceinline__ void patch_top(const DistillArgs& a, const Lds& l, T* grad, float m,
+                                          float S, float scale, bool dup, int64_t lo, int64_t hi) {
+  for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
+    const int i = l.idx[k];
+    if (i < 0 || i < lo || i >= hi) continue;
+    float p = l.p[k];
+    if (dup) {  // every entry of the token writes the same sum
+      p = 0.0f;
+      for (int q = 0; q < a.K; ++q)
+        if (l.idx[q] == i) p += l.p[q];
+    }
+    grad[i] = (T)(scale * (ex2((l.z[k] - m) * a.c) / S - p));
+  }
+}
+
+// Marks of chunk j (bit e: its token e is in the top), j counted from c0.
+template <typename T>
+__device__ __forceinline__ uint32_t chunk_bits(const uint32_t* bits, uint32_t j) {
+  const uint32_t at = j * kVec<T>;
+  return (bits[at >> 5] >> (at & 31)) & ((1u << kVec<T>) - 1);
+}
+
+// Adds exp((z - m) / tau) of a chunk to the rest's sum, or to the top's.
+template <typename T, bool TAIL>
+__device__ __forceinline__ void add_chunk(const Chunk<T>& v, float m, float c, uint32_t marks,
+                                          float& rest, float& top) {
+  float z[kVec<T>];
+  unpack(v, z);
+  if (!TAIL || marks == 0) {
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e) rest += ex2((z[e] - m) * c);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e) {
+      const float x = ex2((z[e] - m) * c);
+      if ((marks >> e) & 1u) top += x;
+      else rest += x;
+    }
+  }
+}
+
+// ------------------------------------------------- one workgroup holds the row
+template <typename T, int NT, int R, bool TAIL>
+__global__ __launch_bounds__(NT) void distill_row_kernel(DistillArgs a) {
+  extern __shared__ char mem[];
+  __shared__ float red[3][NT / 64];
+  __shared__ Teacher t;  // kept here, not in registers across the passes
+  const int64_t n = blockIdx.x;
+  const int tid = threadIdx.x, wv = tid >> 6;
+  const Row<T> r = row_of<T>(a, n);
+  T* grad = static_cast<T*>(a.grad) + n * a.grad_stride;
+  const float w = a.weight ? a.weight[n] : 1.0f;
+  if (w == 0.0f) {
+    const float zero[kVec<T>] = {};
+    for (uint32_t j = tid; j < r.chunks; j += NT) store_chunk(grad, r, j, zero);
+    if (tid == 0) a.loss[n] = 0.0f;
+    return;
+  }
+  const Lds l = lds_of(mem, a.K);
+  auto read_teacher = [&] {
+    if (wv != 0) return;
+    const Teacher o = teacher<T, TAIL>(a, r, n, l, 0, r.chunks);
+    if (tid == 0) t = o;
+  };
+  // The row's loads come first, so that they are in flight meanwhile, unless
+  // they would take the registers the first wave needs for the teacher.
+  if (R > 12) read_teacher();
+  Chunk<T> v[R];
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const uint32_t j = tid + q * NT;
+    if (j < r.chunks) {
+      v[q] = load_chunk(r, j);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kVec<T>; ++e) v[q].v[e] = (T)kNegInf;
+    }
+  }
+  if (R <= 12) read_teacher();
+  float m = kNegInf;
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    float z[kVec<T>];
+    unpack(v[q], z);
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e) m = fmaxf(m, z[e]);
+    keep_packed<T>(v[q]);
+  }
+  m = wave_max(m);
+  if ((tid & 63) == 0) red[0][wv] = m;
+  __syncthreads();
+  m = red[0][0];
+#pragma unroll
+  for (int q = 1; q < NT / 64; ++q) m = fmaxf(m, red[0][q]);
+  if (m == kNegInf) m = 0.0f;
+  float rest = 0.0f, top = 0.0f;
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const uint32_t j = tid + q * NT;
+    if (j < r.chunks)
+      add_chunk<T, TAIL>(v[q], m, a.c, TAIL ? chunk_bits<T>(l.bits, j) : 0u, rest, top);
+    keep_packed<T>(v[q]);
+  }
+  rest = wave_sum(rest);
+  if (TAIL) top = wave_sum(top);
+  if ((tid & 63) == 0) {
+    red[1][wv] = rest;
+    red[2][wv] = top;
+  }
+  __syncthreads();
+  rest = top = 0.0f;
+#pragma unroll
+  for (int q = 0; q < NT / 64; ++q) {
+    rest += red[1][q];
+    if (TAIL) top += red[2][q];
+  }
+  const float S = rest + top;
+  const bool dead = S == 0.0f || (!TAIL && !t.any);
+  const float scale = dead ? 0.0f : w * a.tau;
+  // 1 / S - p_r / S_r as one rounded difference over the product
+  float coef = 0.0f;
+  if (!dead)
+    coef = TAIL ? (rest == 0.0f ? 0.0f : scale * (__builtin_fmaf(-(float)t.rest, S, rest) / (S * rest)))
+                : scale / S;
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const uint32_t j = tid + q * NT;
+    if (j < r.chunks) {
+      float z[kVec<T>], g[kVec<T>];
+      unpack(v[q], z);
+#pragma unroll
+      for (int e = 0; e < kVec<T>; ++e) g[e] = dead ? 0.0f : coef * ex2((z[e] - m) * a.c);
+      store_chunk(grad, r, j, g);
+    }
+  }
+  __syncthreads();
+  if (!dead) patch_top(a, l, grad, m, S, scale, t.dup, 0, (int64_t)r.V);
+  if (wv == 0) {
+    const float loss = dead ? 0.0f : row_loss(a, l, t, m, S, rest, TAIL);
+    if (tid == 0) a.loss[n] = loss;
+  }
+}
+
+// ------------------------------------------------------ rows taken in parts
+constexpr int kPartThreads = 256;
+constexpr int kBatch = 4;  // chunks a thread loads at once
+
+// Chunks [c0, c1) of the workgroup's part.
+struct Span {
+  int64_t n;
+  int split;
+  uint32_t c0, c1;
+};
+template <typename T>
+__device__ __forceinline__ Span span_of(const DistillArgs& a, const Row<T>& r, int64_t n,
+                                        int split) {
+  const uint32_t per = (r.chunks + a.splits - 1) / a.splits;
+  Span s;
+  s.n = n;
+  s.split = split;
+  s.c0 = (uint32_t)split * per < r.chunks ? (uint32_t)split * per : r.chunks;
+  s.c1 = s.c0 + per < r.chunks ? s.c0 + per : r.chunks;
+  return s;
+}
+
+// Largest logit and sums of one part of a row.
+template <typename T, bool TAIL>
+__global__ __launch_bounds__(kPartThreads) void distill_part_kernel(DistillArgs a) {
+  extern __shared__ char mem[];
+  __shared__ float red[3][kPartThreads / 64];
+  const int64_t n = blockIdx.x / (uint32_t)a.splits;
+  const int tid = threadIdx.x, wv = tid >> 6;
+  float* part = a.part + (int64_t)blockIdx.x * 4;
+  if (a.weight && a.weight[n] == 0.0f) {
+    if (tid == 0) part[0] = kNegInf, part[1] = part[2] = 0.0f;
+    return;
+  }
+  const Row<T> r = row_of<T>(a, n);
+  const Span s = span_of(a, r, n, (int)(blockIdx.x % (uint32_t)a.splits));
+  uint32_t* bits = reinterpret_cast<uint32_t*>(mem);
+  if (TAIL) {
+    const uint32_t words = ((s.c1 - s.c0) * kVec<T> + 31) / 32;
+    for (uint32_t q = tid; q < words; q += kPartThreads) bits[q] = 0;
+    __syncthreads();
+    const int64_t lo = (int64_t)s.c0 * kVec<T> - r.mis, hi = (int64_t)s.c1 * kVec<T> - r.mis;
+    for (int k = tid; k < a.K; k += kPartThreads) {
+      const int i = a.tidx[n * a.K + k];
+      if (i >= 0 && i < (int64_t)r.V && i >= lo && i < hi) {
+        const uint32_t bit = (uint32_t)(i - lo);
+        atomicOr(&bits[bit >> 5], 1u << (bit & 31));
+      }
+    }
+    __syncthreads();
+  }
+  float m = kNegInf, rest = 0.0f, top = 0.0f;
+  for (uint32_t j0 = s.c0 + tid; j0 < s.c1; j0 += kBatch * kPartThreads) {
+    Chunk<T> v[kBatch];
+    float mb = m;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const uint32_t j = j0 + q * kPartThreads;
+      if (j < s.c1) {
+        v[q] = load_chunk(r, j);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e) v[q].v[e] = (T)kNegInf;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      float z[kVec<T>];
+      unpack(v[q], z);
+#pragma unroll
+      for (int e = 0; e < kVec<T>; ++e) mb = fmaxf(mb, z[e]);
+    }
+    if (mb > m) {
+      const float k = m == kNegInf ? 0.0f : ex2((m - mb) * a.c);
+      rest *= k;
+      top *= k;
+      m = mb;
+    }
+    const float ms = m == kNegInf ? 0.0f : m;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const uint32_t j = j0 + q * kPartThreads;
+      if (j < s.c1)
+        add_chunk<T, TAIL>(v[q], ms, a.c, TAIL ? chunk_bits<T>(bits, j - s.c0) : 0u, rest, top);
+    }
+  }
+  float mw = wave_max(m);
+  if ((tid & 63) == 0) red[0][wv] = mw;
+  __syncthreads();
+  mw = red[0][0];
+#pragma unroll
+  for (int q = 1; q < kPartThreads / 64; ++q) mw = fmaxf(mw, red[0][q]);
+  const float k = m == kNegInf ? (rest == rest ? 0.0f : 1.0f) : ex2((m - mw) * a.c);
+  rest = wave_sum(rest * k);
+  top = wave_sum(top * k);
+  if ((tid & 63) == 0) {
+    red[1][wv] = rest;
+    red[2][wv] = top;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    rest = top = 0.0f;
+    for (int q = 0; q < kPartThreads / 64; ++q) {
+      rest += red[1][q];
+      top += red[2][q];
+    }
+    part[0] = mw;
+    part[1] = rest;
+    part[2] = top;
+  }
+}
+
+// Joins a row's parts; one wave per row.
+template <typename T, bool TAIL>
+__global__ __launch_bounds__(64) void distill_join_kernel(DistillArgs a) {
+  extern __shared__ char mem[];
+  const int64_t n = blockIdx.x;
+  const int lane = threadIdx.x;
+  const float* part = a.part + n * a.splits * 4;
+  const bool off = a.weight && a.weight[n] == 0.0f;
+  float m = kNegInf, rest = 0.0f, top = 0.0f;
+  for (int q = lane; q < a.splits; q += 64) m = fmaxf(m, part[4 * q]);
+  m = wave_max(m);
+  for (int q = lane; q < a.splits; q += 64) {
+    const float pm = part[4 * q], pr = part[4 * q + 1], pt = part[4 * q + 2];
+    const float k = pm == kNegInf ? (pr == pr ? 0.0f : 1.0f) : ex2((pm - m) * a.c);
+    rest += pr * k;
+    top += pt * k;
+  }
+  rest = wave_sum(rest);
+  top = wave_sum(top);
+  if (m == kNegInf) m = 0.0f;
+  float S = rest + top;
+  float loss = 0.0f, p_rest = 0.0f;
+  if (!off) {
+    const Row<T> r = row_of<T>(a, n);
+    const Lds l = lds_of(mem, a.K);
+    const Teacher t = teacher<T, TAIL>(a, r, n, l, 0, 0);
+    const bool dead = S == 0.0f || (!TAIL && !t.any);
+    if (dead) S = rest = 0.0f;
+    loss = dead ? 0.0f : row_loss(a, l, t, m, S, rest, TAIL);
+    p_rest = (float)t.rest;
+  }
+  if (lane == 0) {
+    a.loss[n] = loss;
+    if (a.saved) {
+      float* s = a.saved + n * 4;
+      s[0] = m;
+      s[1] = S;
+      s[2] = rest;
+      s[3] = p_rest;
+    }
+  }
+}
+
+// Gradient of one part of a row from its saved statistics.
+template <typename T, bool TAIL>
+__global__ __launch_bounds__(kPartThreads) void distill_grad_kernel(DistillArgs a) {
+  extern __shared__ char mem[];
+  __shared__ uint32_t sh_dup;
+  const int64_t n = blockIdx.x / (uint32_t)a.splits;
+  const int tid = threadIdx.x, wv = tid >> 6;
+  const Row<T> r = row_of<T>(a, n);
+  const Span s = span_of(a, r, n, (int)(blockIdx.x % (uint32_t)a.splits));
+  T* grad = static_cast<T*>(a.grad) + n * a.grad_stride;
+  const float w = a.weight ? a.weight[n] : 1.0f;
+  const float m = a.saved[4 * n], S = a.saved[4 * n + 1], rest = a.saved[4 * n + 2];
+  if (w == 0.0f || S == 0.0f) {
+    const float zero[kVec<T>] = {};
+    for (uint32_t j = s.c0 + tid; j < s.c1; j += kPartThreads) store_chunk(grad, r, j, zero);
+    return;
+  }
+  const Lds l = lds_of(mem, a.K);
+  if (wv == 0) {
+    const Teacher t = teacher<T, TAIL>(a, r, n, l, s.c0, s.c1);
+    if (tid == 0) sh_dup = t.dup;
+  }
+  __syncthreads();  // the top's logits are read before they may be overwritten
+  const float scale = w * a.tau;
+  const float coef =
+      TAIL ? (rest == 0.0f ? 0.0f
+                           : scale * (__builtin_fmaf(-a.saved[4 * n + 3], S, rest) / (S * rest)))
+           : scale / S;
+  for (uint32_t j0 = s.c0 + tid; j0 < s.c1; j0 += kBatch * kPartThreads) {
+    Chunk<T> v[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const uint32_t j = j0 + q * kPartThreads;
+      if (j < s.c1) v[q] = load_chunk(r, j);
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const uint32_t j = j0 + q * kPartThreads;
+      if (j < s.c1) {
+        float z[kVec<T>], g[kVec<T>];
+        unpack(v[q], z);
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e) g[e] = coef * ex2((z[e] - m) * a.c);
+        store_chunk(grad, r, j, g);
+      }
+    }
+  }
+  __syncthreads();
+  patch_top(a, l, grad, m, S, scale, sh_dup != 0, (int64_t)s.c0 * kVec<T> - r.mis,
+            (int64_t)s.c1 * kVec<T> - r.mis);
+}
+
+size_t lds_bytes(int K, int64_t tokens) {
+  return (size_t)K * 12 + (size_t)((tokens + 31) / 32) * 4;
+}
+
+int elem_size(int type) { return type == 0 ? 4 : 2; }
+
+// Tokens of the largest part, whole chunks.
+int64_t part_tokens(const DistillArgs& a, int type) {
+  const int vec = 16 / elem_size(type);
+  const int64_t chunks = (a.V + vec - 1 + vec - 1) / vec;
+  return (chunks + a.splits - 1) / a.splits * vec;
+}
+
+template <typename T, int NT, int R>
+hipError_t row_launch(const DistillArgs& a, hipStream_t s) {
+  const size_t lds = lds_bytes(a.K, a.V + 2 * kVec<T>);
+  if (a.tlse)
+    return launch_kernel(distill_row_kernel<T, NT, R, true>, dim3((uint32_t)a.N), dim3(NT), lds, s,
+                         a);
+  return launch_kernel(distill_row_kernel<T, NT, R, false>, dim3((uint32_t)a.N), dim3(NT), lds, s,
+                       a);
+}
+
+template <typename T>
+hipError_t row_typed(const DistillArgs& a, hipStream_t s) {
+  const int64_t chunks = (a.V + 2 * kVec<T> - 2) / kVec<T>;  // at most, for any alignment
+  if (chunks <= 64 * 4) return row_launch<T, 64, 4>(a, s);
+  if (chunks <= 256 * 4) return row_launch<T, 256, 4>(a, s);
+  if (chunks <= 512 * 8) return row_launch<T, 512, 8>(a, s);
+  if (chunks <= 1024 * 9) return row_launch<T, 1024, 9>(a, s);
+  return row_launch<T, 1024, 17>(a, s);
+}
+
+template <typename T>
+hipError_t stats_typed(const DistillArgs& a, int type, hipStream_t s) {
+  const dim3 grid((uint32_t)(a.N * a.splits));
+  const size_t lds = lds_bytes(0, part_tokens(a, type));
+  hipError_t e = a.tlse ? launch_kernel(distill_part_kernel<T, true>, grid, dim3(kPartThreads), lds,
+                                        s, a)
+                        : launch_kernel(distill_part_kernel<T, false>, grid, dim3(kPartThreads), 0,
+                                        s, a);
+  if (e != hipSuccess) return e;
+  return a.tlse ? launch_kernel(distill_join_kernel<T, true>, dim3((uint32_t)a.N), dim3(64),
+                                lds_bytes(a.K, 0), s, a)
+                : launch_kernel(distill_join_kernel<T, false>, dim3((uint32_t)a.N), dim3(64),
+                                lds_bytes(a.K, 0), s, a);
+}
+
+template <typename T>
+hipError_t grad_typed(const DistillArgs& a, int type, hipStream_t s) {
+  const dim3 grid((uint32_t)(a.N * a.splits));
+  const size_t lds = lds_bytes(a.K, part_tokens(a, type));
+  return a.tlse ? launch_kernel(distill_grad_kernel<T, true>, grid, dim3(kPartThreads), lds, s, a)
+                : launch_kernel(distill_grad_kernel<T, false>, grid, dim3(kPartThreads), lds, s, a);
+}
+
+}  // namespace
+
+bool distill_resident(int64_t N, int64_t V, int type) {
+  const int vec = 16 / elem_size(type);
+  const int64_t chunks = (V + 2 * vec - 2) / vec;
+  return chunks <= 1024 * 17 && (N >= 128 || chunks <= 256 * 4);
+}
+
+int distill_splits(int64_t N, int64_t V, int type) {
+  const int vec = 16 / elem_size(type);
+  const int64_t chunks = (V + 2 * vec - 2) / vec;
+  const int64_t most = (chunks + kPartThreads * kBatch - 1) / (kPartThreads * kBatch);
+  int64_t n = (1024 + N - 1) / N;
+  if (n > most) n = most;
+  // the bitmap of a part lies in LDS
+  const int64_t least = (V + (1 << 18) - 1) >> 18;
+  if (n < least) n = least;
+  return (int)(n < 1 ? 1 : n);
+}
+
+hipError_t launch_distill_fused(const DistillArgs& a, int type, hipStream_t s) {
+  return type == 0 ? row_typed<float>(a, s) : type == 1 ? row_typed<bf16_t>(a, s)
+                                                        : row_typed<f16_t>(a, s);
+}
+
+hipError_t launch_distill_forward(const DistillArgs& a, int type, hipStream_t s) {
+  return type == 0 ? stats_typed<float>(a, type, s)
+                   : type == 1 ? stats_typed<bf16_t>(a, type, s) : stats_typed<f16_t>(a, type, s);
+}
+
+hipError_t launch_distill_backward(const DistillArgs& a, int type, hipStream_t s) {
+  return type == 0 ? grad_typed<float>(a, type, s)
+                   : type == 1 ? grad_typed<bf16_t>(a, type, s) : grad_typed<f16_t>(a, type, s);
+}
+
+}  // namespace per

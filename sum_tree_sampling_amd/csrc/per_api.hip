@@ -145,6 +145,9 @@ namespace per {
 
 KernelTiming& kernel_timing() { return g_timing; }
 
+int api_fail(int code, const char* what) { return fail(code, "%s", what); }
+int api_ok() { return ok(); }
+
 // The bucketed update's scratch for np partitions and max_batch entries,
 // laid out from `base` (256-byte aligned) with the workspace's rules; the
 // layout's end is returned in *end.

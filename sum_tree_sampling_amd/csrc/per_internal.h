@@ -18,6 +18,11 @@ struct KernelTiming {
 };
 KernelTiming& kernel_timing();
 
+// How an entry point outside per_api.hip returns: sets (or clears) the
+// thread's error text and drops a pending timing request.
+int api_fail(int code, const char* what);
+int api_ok();
+
 // Every kernel of the library is launched through here.
 template <typename... KArgs, typename... Args>
 hipError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t lds, hipStream_t s,

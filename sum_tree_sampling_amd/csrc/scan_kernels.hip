@@ -1,0 +1,632 @@
+// scan_kernels.hip -- the gated linear recurrence h_t = f_t h'_{t-1} +
+// (1 - f_t) x_t with f = sigmoid(g), forward, backward and one step.
+//
+// A workgroup takes 64 C channels of one sequence (C per lane) and walks the
+// time axis in tiles of kSteps steps per wave: each wave loads its steps,
+// reduces them to one affine map h -> A h + B, the maps meet in LDS, every
+// wave folds those before it into the state it starts from, and then runs its
+// steps.  So the inputs are read once, with as many loads in flight as a wave
+// has steps, and the time axis still has kWaves-fold parallelism inside a
+// workgroup.  Where batch and channels alone do not fill the chip the time
+// axis is cut into segments: a first kernel reduces each segment to its map,
+// and each workgroup of the second folds the maps of the segments before it.
+//
+// A reset makes its map ignore the state (a flag beside A = 0), so an infinite
+// or NaN state before it does not leak through 0 * Inf.
+
+#include "elem.h"
+#include "train_internal.h"
+
+namespace per {
+namespace {
+
+constexpr int kSteps = 16;                 // steps of a wave in one tile
+constexpr int kWaves = 8;                  // waves of a workgroup, at most
+constexpr int kChunk = kSteps * kWaves;    // PER_SCAN_CHUNK
+constexpr int kMaxSeg = 128;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// f = sigmoid(g) and 1 - f, each to f32 precision.
+__device__ __forceinline__ void gate(float g, float& f, float& i) {
+  const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(g) * kLog2e);
+  const float large = __builtin_amdgcn_rcpf(1.0f + e);
+  const float small = e * large;
+  f = g >= 0.0f ? large : small;
+  i = g >= 0.0f ? small : large;
+  if (g != g) f = i = g;
+}
+
+// Position of a workgroup: sequence, segment, first channel of the lane.
+struct Place {
+  int64_t b, d;
+  int seg;
+  int64_t t_begin, t_end;  // steps of the segment
+  int64_t live;            // steps before min(t_end, length)
+};
+
+template <int C>
+__device__ __forceinline__ Place place(const ScanArgs& a) {
+  const uint32_t nct = (uint32_t)((a.D + 64 * C - 1) / (64 * C));
+  uint32_t id = blockIdx.x;
+  Place p;
+  p.d = (int64_t)(id % nct) * (64 * C) + (threadIdx.x & 63) * C;
+  id /= nct;
+  p.seg = (int)(id % (uint32_t)a.nseg);
+  p.b = id / (uint32_t)a.nseg;
+  int64_t len = a.T;
+  if (a.length) {
+    len = a.length[p.b];
+    len = len < 0 ? 0 : len > a.T ? a.T : len;
+  }
+  p.t_begin = (int64_t)p.seg * a.seg_steps;
+  p.t_end = p.t_begin + a.seg_steps < a.T ? p.t_begin + a.seg_steps : a.T;
+  p.live = len < p.t_end ? len : p.t_end;
+  return p;
+}
+
+// Steps of [ts, ts + kSteps) before `live`.
+__device__ __forceinline__ int steps_at(int64_t ts, int64_t live) {
+  const int64_t n = live - ts;
+  return n < 0 ? 0 : n > kSteps ? kSteps : (int)n;
+}
+
+// Bit s: an episode begins at step ts + s (s < n), the same in every lane.
+__device__ __forceinline__ uint32_t reset_mask(const uint8_t* reset, int64_t ts, int n) {
+  if (!reset) return 0;
+  const int lane = threadIdx.x & 63;
+  return (uint32_t)__ballot(lane < n && reset[ts + lane] != 0);
+}
+
+// kSteps rows of C channels from row ts of a [T x D] matrix; rows past the
+// last live one are loaded from it and not used.
+template <typename T, int C>
+__device__ __forceinline__ void load_steps(const T* p, int64_t st, int64_t ts, int n,
+                                           Pack<T, C> (&v)[kSteps]) {
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s)
+    v[s] = load_pack<T, C>(p + (ts + (s < n ? s : n - 1)) * st);
+}
+
+template <typename T, int C>
+__global__ __launch_bounds__(kWaves * 64) void scan_forward_kernel(ScanArgs a) {
+  __shared__ float sA[2][kWaves][C][64], sB[2][kWaves][C][64];
+  __shared__ uint32_t sF[2][kWaves];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nw = blockDim.x >> 6;
+  const Place p = place<C>(a);
+  const bool in = p.d < a.D;
+  const T* x = static_cast<const T*>(a.x) + p.b * a.x_sb + p.d;
+  const T* g = static_cast<const T*>(a.g) + p.b * a.g_sb + p.d;
+  T* y = static_cast<T*>(a.y) + p.b * a.y_sb + p.d;
+  const uint8_t* reset = a.reset ? a.reset + p.b * a.T : nullptr;
+  float h[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) h[c] = a.h0 && in ? a.h0[p.b * a.D + p.d + c] : 0.0f;
+
+  if (p.seg > 0) {  // fold the segments before this one: a run per wave, then the waves
+    const int run = (p.seg + nw - 1) / nw;
+    float A[C], B[C];
+    uint32_t flag = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
+    for (int s = wv * run; s < (wv + 1) * run && s < p.seg; ++s) {
+      const int64_t at = p.b * a.nseg + s;
+      const uint32_t f = a.agg_flag[at];
+      const float* m = a.agg + at * 2 * a.D + p.d;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const float sa = in ? m[c] : 0.0f, sb = in ? m[a.D + c] : 0.0f;
+        B[c] = f ? sb : __builtin_fmaf(sa, B[c], sb);
+        A[c] *= sa;
+      }
+      flag |= f;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) sA[1][wv][c][lane] = A[c], sB[1][wv][c][lane] = B[c];
+    if (lane == 0) sF[1][wv] = flag;
+    __syncthreads();
+    for (int w = 0; w < nw; ++w) {
+      const bool f = sF[1][w] != 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        h[c] = f ? sB[1][w][c][lane] : __builtin_fmaf(sA[1][w][c][lane], h[c], sB[1][w][c][lane]);
+    }
+  }
+
+  int buf = 0;
+  for (int64_t t0 = p.t_begin; t0 < p.t_end; t0 += nw * kSteps, buf ^= 1) {
+    const int64_t ts = t0 + wv * kSteps;
+    const int n = steps_at(ts, p.live);
+    const uint32_t mask = reset_mask(reset, ts, n);
+    if (a.carries && wv == 0 && in) {
+      float* c0 = a.carries + (p.b * ((a.T + kChunk - 1) / kChunk) + t0 / kChunk) * a.D + p.d;
+#pragma unroll
+      for (int c = 0; c < C; ++c) c0[c] = h[c];
+    }
+    float f[kSteps][C], ix[kSteps][C];
+    float A[C], B[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
+    if (n > 0 && in) {
+      Pack<T, C> gx[kSteps], gg[kSteps];
+      load_steps<T, C>(x, a.x_st, ts, n, gx);
+      load_steps<T, C>(g, a.g_st, ts, n, gg);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        float xv[C], gv[C];
+        unpack(gx[s], xv);
+        unpack(gg[s], gv);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          float i;
+          gate(gv[c], f[s][c], i);
+          ix[s][c] = i * xv[c];
+          if (s < n) {
+            const bool r = (mask >> s) & 1u;
+            B[c] = r ? ix[s][c] : __builtin_fmaf(f[s][c], B[c], ix[s][c]);
+            A[c] = r ? 0.0f : A[c] * f[s][c];
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) sA[buf][wv][c][lane] = A[c], sB[buf][wv][c][lane] = B[c];
+    if (lane == 0) sF[buf][wv] = mask;
+    __syncthreads();
+    float hs[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) hs[c] = h[c];
+    for (int w = 0; w < nw; ++w) {
+      const bool fl = sF[buf][w] != 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (w == wv) hs[c] = h[c];
+        const float wb = sB[buf][w][c][lane];
+        h[c] = fl ? wb : __builtin_fmaf(sA[buf][w][c][lane], h[c], wb);
+      }
+    }
+    if (in) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        if (s < n) {
+          const bool r = (mask >> s) & 1u;
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+            hs[c] = r ? ix[s][c] : __builtin_fmaf(f[s][c], hs[c], ix[s][c]);
+          store_vals<T, C>(y + (ts + s) * a.y_st, hs);
+        } else if (ts + s < p.t_end) {
+          const float zero[C] = {};
+          store_vals<T, C>(y + (ts + s) * a.y_st, zero);
+        }
+      }
+    }
+  }
+  if (a.h_last && p.t_end == a.T && p.seg == a.nseg - 1 && wv == 0 && in) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) a.h_last[p.b * a.D + p.d + c] = h[c];
+  }
+}
+
+// The map of one segment: forward h -> A h + B, or (REV) of the gradient that
+// flows back through it, E -> A E + B.  Waves take runs of whole tiles.
+template <typename T, int C, bool REV>
+__global__ __launch_bounds__(kWaves * 64) void scan_segment_kernel(ScanArgs a) {
+  __shared__ float sA[kWaves][C][64], sB[kWaves][C][64];
+  __shared__ uint32_t sF[kWaves];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Place p = place<C>(a);
+  const bool in = p.d < a.D;
+  const T* v = REV ? static_cast<const T*>(a.dy) + p.b * a.dy_sb + p.d
+                   : static_cast<const T*>(a.x) + p.b * a.x_sb + p.d;
+  const int64_t v_st = REV ? a.dy_st : a.x_st;
+  const T* g = static_cast<const T*>(a.g) + p.b * a.g_sb + p.d;
+  const uint8_t* reset = a.reset ? a.reset + p.b * a.T : nullptr;
+  const int64_t run = a.seg_steps / kWaves;  // a multiple of kSteps
+  float A[C], B[C];
+  uint32_t flag = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
+  for (int64_t k = 0; k < run; k += kSteps) {
+    const int64_t ts = p.t_begin + wv * run + (REV ? run - kSteps - k : k);
+    const int n = steps_at(ts, p.live);
+    if (n == 0) continue;
+    const uint32_t mask = reset_mask(reset, ts, n);
+    flag |= mask;
+    if (!in) continue;
+    Pack<T, C> gv[kSteps], gg[kSteps];
+    load_steps<T, C>(v, v_st, ts, n, gv);
+    load_steps<T, C>(g, a.g_st, ts, n, gg);
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const int s = REV ? kSteps - 1 - q : q;
+      if (s < n) {
+        const bool r = (mask >> s) & 1u;
+        float vv[C], gf[C];
+        unpack(gv[s], vv);
+        unpack(gg[s], gf);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          float f, i;
+          gate(gf[c], f, i);
+          if (REV) {
+            B[c] = r ? 0.0f : f * (B[c] + vv[c]);
+          } else {
+            const float b = i * vv[c];
+            B[c] = r ? b : __builtin_fmaf(f, B[c], b);
+          }
+          A[c] = r ? 0.0f : A[c] * f;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) sA[wv][c][lane] = A[c], sB[wv][c][lane] = B[c];
+  if (lane == 0) sF[wv] = flag;
+  __syncthreads();
+  if (wv != 0) return;
+  uint32_t any = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
+#pragma unroll
+  for (int q = 0; q < kWaves; ++q) {
+    const int w = REV ? kWaves - 1 - q : q;
+    const bool fl = sF[w] != 0;
+    any |= sF[w];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      B[c] = fl ? sB[w][c][lane] : __builtin_fmaf(sA[w][c][lane], B[c], sB[w][c][lane]);
+      A[c] *= sA[w][c][lane];
+    }
+  }
+  const int64_t at = p.b * a.nseg + p.seg;
+  if (in) {
+    float* m = a.agg + at * 2 * a.D + p.d;
+#pragma unroll
+    for (int c = 0; c < C; ++c) m[c] = A[c], m[a.D + c] = B[c];
+  }
+  if (p.d == 0) a.agg_flag[at] = any;
+  if (!REV && a.h0 && p.seg == 0 && in) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) a.h0_copy[p.b * a.D + p.d + c] = a.h0[p.b * a.D + p.d + c];
+  }
+}
+
+// E_t = f_t (E_{t+1} + dy_t) is the gradient that reaches the state before
+// step t (0 where an episode begins at t); full_t = E_{t+1} + dy_t that of h_t:
+//   dx = full (1 - f),  dg = full (h' - x) f (1 - f).
+// The states of a chunk are computed again from its carry.
+template <typename T, int C>
+__global__ __launch_bounds__(kWaves * 64) void scan_backward_kernel(ScanArgs a) {
+  __shared__ float sA[2][kWaves][C][64], sB[2][kWaves][C][64], sQ[2][kWaves][C][64];
+  __shared__ uint32_t sF[2][kWaves];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nw = blockDim.x >> 6;
+  const Place p = place<C>(a);
+  const bool in = p.d < a.D;
+  const T* x = static_cast<const T*>(a.x) + p.b * a.x_sb + p.d;
+  const T* g = static_cast<const T*>(a.g) + p.b * a.g_sb + p.d;
+  const T* dy = static_cast<const T*>(a.dy) + p.b * a.dy_sb + p.d;
+  T* dx = static_cast<T*>(a.dx) + p.b * a.dx_sb + p.d;
+  T* dg = static_cast<T*>(a.dg) + p.b * a.dg_sb + p.d;
+  const uint8_t* reset = a.reset ? a.reset + p.b * a.T : nullptr;
+  float E[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) E[c] = a.dh_last && in ? a.dh_last[p.b * a.D + p.d + c] : 0.0f;
+
+  if (p.seg < a.nseg - 1) {  // fold the segments after this one
+    const int later = a.nseg - 1 - p.seg;
+    const int run = (later + nw - 1) / nw;
+    float A[C], B[C];
+    uint32_t flag = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
+    // wave nw - 1 takes the last segments, each run from its end
+    int hi = p.seg + 1 + (wv + 1) * run;
+    if (hi > a.nseg) hi = a.nseg;
+    for (int s = hi - 1; s >= p.seg + 1 + wv * run; --s) {
+      const int64_t at = p.b * a.nseg + s;
+      const uint32_t f = a.agg_flag[at];
+      const float* m = a.agg + at * 2 * a.D + p.d;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const float sa = in ? m[c] : 0.0f, sb = in ? m[a.D + c] : 0.0f;
+        B[c] = f ? sb : __builtin_fmaf(sa, B[c], sb);
+        A[c] *= sa;
+      }
+      flag |= f;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) sA[1][wv][c][lane] = A[c], sB[1][wv][c][lane] = B[c];
+    if (lane == 0) sF[1][wv] = flag;
+    __syncthreads();
+    for (int w = nw - 1; w >= 0; --w) {
+      const bool f = sF[1][w] != 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        E[c] = f ? sB[1][w][c][lane] : __builtin_fmaf(sA[1][w][c][lane], E[c], sB[1][w][c][lane]);
+    }
+  }
+
+  const int64_t tile = nw * kSteps;
+  const int64_t tiles = p.t_end > p.t_begin ? (p.t_end - p.t_begin + tile - 1) / tile : 0;
+  float Eo[C];  // what flows out of the wave's own steps, run one by one
+#pragma unroll
+  for (int c = 0; c < C; ++c) Eo[c] = E[c];
+  int buf = 0;
+  for (int64_t k = tiles - 1; k >= 0; --k, buf ^= 1) {
+    const int64_t t0 = p.t_begin + k * tile;
+    const int64_t ts = t0 + wv * kSteps;
+    const int n = steps_at(ts, p.live);
+    const uint32_t mask = reset_mask(reset, ts, n);
+    float f[kSteps][C], i[kSteps][C], xv[kSteps][C];
+    Pack<T, C> pd[kSteps];
+    float h[C], A[C], B[C], Q[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      A[c] = 1.0f;
+      B[c] = Q[c] = 0.0f;
+      h[c] = in ? a.carries[(p.b * ((a.T + kChunk - 1) / kChunk) + t0 / kChunk) * a.D + p.d + c]
+                : 0.0f;
+    }
+    if (n > 0 && in) {
+      Pack<T, C> px[kSteps], pg[kSteps];
+      load_steps<T, C>(x, a.x_st, ts, n, px);
+      load_steps<T, C>(g, a.g_st, ts, n, pg);
+      load_steps<T, C>(dy, a.dy_st, ts, n, pd);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        float gv[C];
+        unpack(px[s], xv[s]);
+        unpack(pg[s], gv);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          gate(gv[c], f[s][c], i[s][c]);
+          if (s < n) {
+            const bool r = (mask >> s) & 1u;
+            const float b = i[s][c] * xv[s][c];
+            B[c] = r ? b : __builtin_fmaf(f[s][c], B[c], b);
+            A[c] = r ? 0.0f : A[c] * f[s][c];
+          }
+        }
+      }
+#pragma unroll
+      for (int s = kSteps - 1; s >= 0; --s) {
+        if (s < n) {
+          const bool r = (mask >> s) & 1u;
+          float dv[C];
+          unpack(pd[s], dv);
+#pragma unroll
+          for (int c = 0; c < C; ++c) Q[c] = r ? 0.0f : f[s][c] * (Q[c] + dv[c]);
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      sA[buf][wv][c][lane] = A[c];
+      sB[buf][wv][c][lane] = B[c];
+      sQ[buf][wv][c][lane] = Q[c];
+    }
+    if (lane == 0) sF[buf][wv] = mask;
+    __syncthreads();
+    for (int w = 0; w < wv; ++w) {
+      const bool fl = sF[buf][w] != 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        h[c] = fl ? sB[buf][w][c][lane]
+                  : __builtin_fmaf(sA[buf][w][c][lane], h[c], sB[buf][w][c][lane]);
+    }
+    float Es[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) Es[c] = E[c];
+    for (int w = nw - 1; w >= 0; --w) {
+      const bool fl = sF[buf][w] != 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (w == wv) Es[c] = E[c];
+        const float q = sQ[buf][w][c][lane];
+        E[c] = fl ? q : __builtin_fmaf(sA[buf][w][c][lane], E[c], q);
+      }
+    }
+    if (in) {
+      if (n > 0) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          if (s < n) {
+            const bool r = (mask >> s) & 1u;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+              const float hp = r ? 0.0f : h[c];
+              const float b = i[s][c] * xv[s][c];
+              h[c] = r ? b : __builtin_fmaf(f[s][c], h[c], b);
+              xv[s][c] = (hp - xv[s][c]) * f[s][c] * i[s][c];
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int s = kSteps - 1; s >= 0; --s) {
+        if (s < n) {
+          const bool r = (mask >> s) & 1u;
+          float dv[C], ox[C], og[C];
+          unpack(pd[s], dv);
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const float full = Es[c] + dv[c];
+            ox[c] = full * i[s][c];
+            og[c] = full * xv[s][c];
+            Es[c] = r ? 0.0f : full * f[s][c];
+          }
+          store_vals<T, C>(dx + (ts + s) * a.dx_st, ox);
+          store_vals<T, C>(dg + (ts + s) * a.dg_st, og);
+        } else if (ts + s < p.t_end) {
+          const float zero[C] = {};
+          store_vals<T, C>(dx + (ts + s) * a.dx_st, zero);
+          store_vals<T, C>(dg + (ts + s) * a.dg_st, zero);
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) Eo[c] = Es[c];
+  }
+  if (a.dh0 && p.seg == 0 && wv == 0 && in) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) a.dh0[p.b * a.D + p.d + c] = Eo[c];
+  }
+}
+
+// One step of B sequences: 2^lg threads per row, C channels per thread and
+// step of the loop.
+template <typename T, int C>
+__global__ __launch_bounds__(256) void scan_step_kernel(StepArgs a, int lg) {
+  const int64_t b = (int64_t)blockIdx.x * (256 >> lg) + (threadIdx.x >> lg);
+  if (b >= a.B) return;
+  const bool r = a.reset && a.reset[b] != 0;
+  const int64_t step = (int64_t)C << lg;
+  for (int64_t d = blockIdx.y * step + (threadIdx.x & ((1 << lg) - 1)) * C; d < a.D;
+       d += gridDim.y * step) {
+    float x[C], g[C], h[C], o[C];
+    unpack(load_pack<T, C>(static_cast<const T*>(a.x) + b * a.x_st + d), x);
+    unpack(load_pack<T, C>(static_cast<const T*>(a.g) + b * a.g_st + d), g);
+    unpack(load_pack<float, C>(a.h + b * a.D + d), h);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float f, i;
+      gate(g[c], f, i);
+      const float ix = i * x[c];
+      o[c] = r ? ix : __builtin_fmaf(f, h[c], ix);
+    }
+    store_vals<float, C>(a.h_out + b * a.D + d, o);
+    store_vals<T, C>(static_cast<T*>(a.y) + b * a.y_st + d, o);
+  }
+}
+
+// Two channels per lane where they fill a wave's lanes and D is even, else one.
+bool two_channels(int64_t D) { return D % 2 == 0 && D > 64; }
+
+int64_t channel_tiles(int64_t D) {
+  const int64_t w = two_channels(D) ? 128 : 64;
+  return (D + w - 1) / w;
+}
+
+template <typename T, int C>
+hipError_t forward_typed(ScanArgs a, uint32_t blocks, int waves, hipStream_t s) {
+  if (a.nseg > 1) {
+    const hipError_t e = launch_kernel(scan_segment_kernel<T, C, false>, dim3(blocks),
+                                       dim3(kWaves * 64), 0, s, a);
+    if (e != hipSuccess) return e;
+    // The last segment's workgroup may write h_last = h0 before others start.
+    if (a.h0) a.h0 = a.h0_copy;
+  }
+  return launch_kernel(scan_forward_kernel<T, C>, dim3(blocks), dim3(64 * waves), 0, s, a);
+}
+
+template <typename T, int C>
+hipError_t backward_typed(const ScanArgs& a, uint32_t blocks, int waves, hipStream_t s) {
+  if (a.nseg > 1) {
+    const hipError_t e = launch_kernel(scan_segment_kernel<T, C, true>, dim3(blocks),
+                                       dim3(kWaves * 64), 0, s, a);
+    if (e != hipSuccess) return e;
+  }
+  return launch_kernel(scan_backward_kernel<T, C>, dim3(blocks), dim3(64 * waves), 0, s, a);
+}
+
+int waves_for(int64_t T) {
+  const int64_t w = (T + kSteps - 1) / kSteps;
+  return w < 1 ? 1 : w > kWaves ? kWaves : (int)w;
+}
+
+// Segments and their steps (whole chunks).
+struct Split {
+  int n;
+  int64_t steps;
+};
+Split split_time(int64_t B, int64_t T, int64_t D) {
+  const int64_t blocks = B * channel_tiles(D);
+  const int64_t chunks = (T + kChunk - 1) / kChunk;
+  Split s = {1, T};
+  if (blocks >= 256 || chunks < 2) return s;
+  int64_t n = (512 + blocks - 1) / blocks;
+  if (n > kMaxSeg) n = kMaxSeg;
+  if (n > chunks) n = chunks;
+  s.steps = (chunks + n - 1) / n * kChunk;
+  s.n = (int)((T + s.steps - 1) / s.steps);
+  return s;
+}
+
+void set_split(ScanArgs& a) {
+  const Split s = split_time(a.B, a.T, a.D);
+  a.nseg = s.n;
+  a.seg_steps = s.steps;
+  if (s.n > 1) {
+    a.h0_copy = a.agg + a.B * s.n * 2 * a.D;
+    a.agg_flag = reinterpret_cast<uint32_t*>(a.h0_copy + a.B * a.D);
+  }
+}
+
+}  // namespace
+
+int64_t scan_blocks(int64_t B, int64_t T, int64_t D) {
+  return B * split_time(B, T, D).n * channel_tiles(D);
+}
+
+size_t scan_workspace(int64_t B, int64_t T, int64_t D) {
+  const int n = split_time(B, T, D).n;
+  return n == 1 ? 0 : (size_t)(B * n * 2 * D + B * D + B * n) * 4;
+}
+
+hipError_t launch_scan_forward(ScanArgs a, int type, hipStream_t s) {
+  set_split(a);
+  const uint32_t blocks = (uint32_t)(a.B * a.nseg * channel_tiles(a.D));
+  const int waves = waves_for(a.T);
+  const bool two = two_channels(a.D);
+  if (type == 0)
+    return two ? forward_typed<float, 2>(a, blocks, waves, s)
+               : forward_typed<float, 1>(a, blocks, waves, s);
+  if (type == 1)
+    return two ? forward_typed<bf16_t, 2>(a, blocks, waves, s)
+               : forward_typed<bf16_t, 1>(a, blocks, waves, s);
+  return two ? forward_typed<f16_t, 2>(a, blocks, waves, s)
+             : forward_typed<f16_t, 1>(a, blocks, waves, s);
+}
+
+hipError_t launch_scan_backward(ScanArgs a, int type, hipStream_t s) {
+  set_split(a);
+  const uint32_t blocks = (uint32_t)(a.B * a.nseg * channel_tiles(a.D));
+  const int waves = waves_for(a.T);
+  const bool two = two_channels(a.D);
+  if (type == 0)
+    return two ? backward_typed<float, 2>(a, blocks, waves, s)
+               : backward_typed<float, 1>(a, blocks, waves, s);
+  if (type == 1)
+    return two ? backward_typed<bf16_t, 2>(a, blocks, waves, s)
+               : backward_typed<bf16_t, 1>(a, blocks, waves, s);
+  return two ? backward_typed<f16_t, 2>(a, blocks, waves, s)
+             : backward_typed<f16_t, 1>(a, blocks, waves, s);
+}
+
+template <typename T, int C>
+static hipError_t step_launch(const StepArgs& a, hipStream_t s) {
+  const int64_t units = a.D / C;
+  int lg = 0;
+  while (lg < 8 && (int64_t(1) << lg) < units) ++lg;
+  const int64_t cols = (units + (1 << lg) - 1) >> lg;
+  const int64_t rows = (a.B + (256 >> lg) - 1) / (256 >> lg);
+  return launch_kernel(scan_step_kernel<T, C>,
+                       dim3((uint32_t)rows, (uint32_t)(cols < 65535 ? cols : 65535)), dim3(256), 0,
+                       s, a, lg);
+}
+
+template <typename T>
+static hipError_t step_typed(const StepArgs& a, hipStream_t s) {
+  return a.D % 4 == 0 ? step_launch<T, 4>(a, s) : step_launch<T, 1>(a, s);
+}
+
+hipError_t launch_scan_step(const StepArgs& a, int type, hipStream_t s) {
+  return type == 0 ? step_typed<float>(a, s) : type == 1 ? step_typed<bf16_t>(a, s)
+                                                         : step_typed<f16_t>(a, s);
+}
+
+}  // namespace per

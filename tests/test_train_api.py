@@ -1,0 +1,208 @@
+"""The sequence operators' ABI (include/per_train.h): every declared function is
+exported and bound, and bad arguments are refused on the host before anything
+is enqueued (no GPU is needed: the pointers below are never used)."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "per_train.h")
+P = 0x100000  # an aligned address
+EINVAL, ENOSPC = -1, -2
+
+
+@pytest.fixture(scope="module")
+def call():
+    from sum_tree_sampling_amd import build, per, train
+    if not os.path.exists(per.LIB_PATH):
+        build.build()
+    per.load()
+
+    def f(name, *args):
+        rc = train._get(name)(*args)
+        if rc:
+            assert per.per_last_error()
+        return rc
+    return f
+
+
+def declared():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    return sorted(set(re.findall(r"\b(per_[a-z_]+)\s*\(", text)))
+
+
+def test_declared_exported_bound(call):
+    import sum_tree_sampling_amd as pkg
+    from sum_tree_sampling_amd import per, train
+    out = subprocess.run(["nm", "-D", "--defined-only", per.LIB_PATH], capture_output=True, text=True,
+                         check=True).stdout
+    exported = set(re.findall(r"\bT (per_\w+)$", out, flags=re.M))
+    names = declared()
+    assert len(names) == 11
+    for n in names:
+        assert n in exported and hasattr(pkg, n) and n in train._SIG, n
+        args = re.search(r"\b%s\s*\((.*?)\)" % n, re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S),
+                         flags=re.S).group(1)
+        assert len(args.split(",")) == len(train._SIG[n]), n
+
+
+ROWS = dict(capacity=64, dim=100, format=0, group=32, codes=P, cs=128, scales=P, ss=4)
+
+
+def rows(**kw):
+    a = dict(ROWS)
+    a.update({k: v for k, v in kw.items() if k in a})
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(capacity=0), dict(capacity=-1), dict(capacity=(1 << 30) + 1), dict(dim=0), dict(dim=(1 << 20) + 1),
+    dict(format=2), dict(format=-1), dict(group=16), dict(group=-32), dict(group=256), dict(codes=None),
+    dict(scales=None), dict(scales=P + 2), dict(cs=99), dict(cs=-128), dict(ss=3), dict(cs=1 << 41),
+    dict(count=-1), dict(count=65), dict(first=-1), dict(first=64), dict(src=None), dict(src=P + 2),
+    dict(type=3), dict(type=-1), dict(stride=99), dict(stride=1 << 41)])
+def test_rows_write_refuses(call, kw):
+    a = dict(count=8, first=0, src=P, type=0, stride=100)
+    a.update({k: v for k, v in kw.items() if k in a})
+    assert call("per_rows_write", *rows(**kw), *a.values(), None) == EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(count=-1), dict(count=1 << 31), dict(slots=None), dict(slots=P + 4),
+                                dict(claims=None), dict(claims=P + 2), dict(src=None), dict(type=7),
+                                dict(stride=5), dict(dim=0), dict(cs=1)])
+def test_rows_write_at_refuses(call, kw):
+    a = dict(count=8, slots=P, claims=P, src=P, type=1, stride=100)
+    a.update({k: v for k, v in kw.items() if k in a})
+    assert call("per_rows_write_at", *rows(**kw), *a.values(), None) == EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(B=-1), dict(window=0), dict(window=-1), dict(B=1 << 20, window=1 << 20),
+                                dict(B=1 << 62, window=4), dict(idx=None), dict(idx=P + 4), dict(out=None),
+                                dict(out=P + 1), dict(type=3), dict(stride=99), dict(group=5)])
+def test_rows_read_refuses(call, kw):
+    a = dict(B=8, idx=P, window=2, out=P, type=1, stride=100)
+    a.update({k: v for k, v in kw.items() if k in a})
+    assert call("per_rows_read", *rows(**kw), *a.values(), None) == EINVAL
+
+
+def test_empty_calls_enqueue_nothing(call):
+    assert call("per_rows_write", *rows(), 0, 0, None, 0, 100, None) == 0
+    assert call("per_rows_write_at", *rows(), 0, None, None, None, 0, 100, None) == 0
+    assert call("per_rows_read", *rows(), 0, None, 1, None, 0, 100, None) == 0
+    assert call("per_scan_step", 0, 8, 0, None, 8, None, 8, None, None, None, None, 8, None) == 0
+    z = [None, 0, 0]
+    assert call("per_scan_forward", 0, 5, 8, 0, *z, *z, None, None, None, *z, None, None, None, 0, None) == 0
+    assert call("per_scan_backward", 0, 5, 8, 0, *z, *z, None, None, None, *z, None, *z, *z, None, None, 0,
+                None) == 0
+    top = [0, 100, 4, 0, None, 100, None, None, 0, None, 1.0]
+    assert call("per_distill", *top, None, None, None, 100, None, 0, None) == 0
+    assert call("per_distill_forward", *top, None, None, None, 0, None) == 0
+    assert call("per_distill_backward", *top, None, None, None, 100, None) == 0
+
+
+FWD = dict(B=2, T=40, D=16, type=0, x=P, x_sb=640, x_st=16, g=P, g_sb=640, g_st=16, reset=None, length=None,
+           h0=None, y=P, y_sb=640, y_st=16, h_last=None, carries=None, ws=None, ws_bytes=0)
+BWD = dict(B=2, T=40, D=16, type=0, x=P, x_sb=640, x_st=16, g=P, g_sb=640, g_st=16, reset=None, length=None,
+           carries=P, dy=P, dy_sb=640, dy_st=16, dh_last=None, dx=P, dx_sb=640, dx_st=16, dg=P, dg_sb=640,
+           dg_st=16, dh0=None, ws=None, ws_bytes=0)
+SEQ_BAD = [dict(B=-1), dict(T=-1), dict(D=0), dict(D=-4), dict(type=3), dict(x=None), dict(x=P + 2),
+           dict(g=None), dict(x_sb=-1), dict(g_st=-1), dict(length=P + 4), dict(B=1 << 31), dict(T=1 << 41),
+           dict(D=1 << 32), dict(B=(1 << 31) - 1, D=1 << 20)]
+
+
+@pytest.mark.parametrize("kw", SEQ_BAD + [
+    dict(y=None), dict(y=P + 1), dict(y_st=15), dict(y_sb=16), dict(y_sb=639), dict(y_sb=-640), dict(h0=P + 2),
+    dict(h_last=P + 1), dict(carries=P + 2), dict(T=1000, x_sb=16000, g_sb=16000, y_sb=16000)])
+def test_scan_forward_refuses(call, kw):
+    assert call("per_scan_forward", *{**FWD, **kw}.values(), None) == EINVAL
+
+
+@pytest.mark.parametrize("kw", SEQ_BAD + [
+    dict(dy=None), dict(dx=None), dict(dg=None), dict(dx_st=8), dict(dg_sb=100), dict(carries=None),
+    dict(carries=P + 2), dict(dh_last=P + 2), dict(dh0=P + 1), dict(dy_st=-1),
+    dict(T=1000, x_sb=16000, g_sb=16000, dy_sb=16000, dx_sb=16000, dg_sb=16000)])
+def test_scan_backward_refuses(call, kw):
+    assert call("per_scan_backward", *{**BWD, **kw}.values(), None) == EINVAL
+
+
+def test_scan_workspace(call):
+    from sum_tree_sampling_amd import per_scan_workspace_bytes as need
+    assert need(2, 40, 16) == 0 and need(0, 5000, 16) == 0 and need(256, 5000, 128) == 0
+    n = need(1, 5000, 16)
+    assert n > 0
+    kw = dict(B=1, T=5000, x_sb=0, g_sb=0, y_sb=0, ws=P)
+    assert call("per_scan_forward", *{**FWD, **kw, "ws_bytes": n - 1}.values(), None) == ENOSPC
+    assert call("per_scan_forward", *{**FWD, **kw, "ws": P + 8, "ws_bytes": n}.values(), None) == EINVAL
+    for bad in ((-1, 5, 5), (1, -1, 5), (1, 1, 0)):
+        with pytest.raises(RuntimeError):
+            need(*bad)
+
+
+@pytest.mark.parametrize("kw", [dict(B=-1), dict(D=0), dict(type=3), dict(x=None), dict(g=None), dict(h=None),
+                                dict(h_out=None), dict(y=None), dict(x_st=-1), dict(y_st=7), dict(h=P + 2),
+                                dict(y=P + 2), dict(h_out=P + 1)])
+def test_scan_step_refuses(call, kw):
+    a = dict(B=4, D=8, type=0, x=P, x_st=8, g=P, g_st=8, reset=None, h=P, h_out=P, y=P, y_st=8)
+    assert call("per_scan_step", *{**a, **kw}.values(), None) == EINVAL
+
+
+TOP = dict(N=4, V=100, K=8, type=1, z=P, stride=100, tidx=P, t=P, t_type=0, tlse=None, tau=1.0)
+TOP_BAD = [dict(N=-1), dict(N=1 << 31), dict(V=0), dict(V=(1 << 24) + 1), dict(K=0), dict(K=1025), dict(type=3),
+           dict(t_type=-1), dict(z=None), dict(z=P + 1), dict(tidx=None), dict(tidx=P + 2), dict(t=None),
+           dict(t=P + 2), dict(stride=99), dict(tlse=P + 1), dict(tau=0.0), dict(tau=-1.0),
+           dict(tau=float("nan")), dict(tau=float("inf")), dict(tau=1e-9)]
+
+
+@pytest.mark.parametrize("kw", TOP_BAD + [dict(weight=P + 2), dict(loss=None), dict(loss=P + 2), dict(grad=None),
+                                          dict(grad=P + 1), dict(gs=99), dict(grad=P, gs=104)])
+def test_distill_refuses(call, kw):
+    a = dict(TOP, weight=None, loss=P, grad=2 * P, gs=100, ws=None, ws_bytes=0)
+    assert call("per_distill", *{**a, **kw}.values(), None) == EINVAL
+
+
+@pytest.mark.parametrize("kw", TOP_BAD + [dict(loss=None), dict(saved=P + 2), dict(ws=None), dict(ws=P + 4)])
+def test_distill_forward_refuses(call, kw):
+    a = dict(TOP, loss=P, saved=P, ws=P, ws_bytes=1 << 20)
+    assert call("per_distill_forward", *{**a, **kw}.values(), None) == EINVAL
+
+
+@pytest.mark.parametrize("kw", TOP_BAD + [dict(saved=None), dict(gloss=None), dict(gloss=P + 2), dict(grad=None),
+                                          dict(gs=10), dict(grad=P, gs=104)])
+def test_distill_backward_refuses(call, kw):
+    a = dict(TOP, saved=P, gloss=P, grad=2 * P, gs=100)
+    assert call("per_distill_backward", *{**a, **kw}.values(), None) == EINVAL
+
+
+def test_distill_workspace(call):
+    from sum_tree_sampling_amd import per_distill_workspace_bytes as need
+    n = need(4, 200000, 1)
+    assert n > 0 and need(0, 100, 0) == 0
+    a = dict(TOP, V=200000, stride=200000, loss=P, saved=P, ws=P, ws_bytes=15)
+    assert call("per_distill_forward", *a.values(), None) == ENOSPC
+    a = dict(TOP, V=200000, stride=200000, weight=None, loss=P, grad=2 * P, gs=200000, ws=P, ws_bytes=n - 1)
+    assert call("per_distill", *a.values(), None) == ENOSPC
+    for bad in ((-1, 5, 0), (1, 0, 0), (1, 5, 3)):
+        with pytest.raises(RuntimeError):
+            need(*bad)
+
+
+def test_binding_refuses_host_tensors():
+    from sum_tree_sampling_amd import per_distill, per_rows_write, per_scan_forward, per_scan_step, rows_alloc
+    codes, scales = rows_alloc(16, 40, device="cpu")
+    assert codes.shape == (16, 40) and scales.shape == (16, 1) and codes.dtype == torch.float8_e4m3fn
+    with pytest.raises(ValueError):
+        per_rows_write(codes, scales, torch.zeros(4, 40))
+    with pytest.raises(ValueError):
+        per_scan_forward(torch.zeros(1, 2, 3), torch.zeros(1, 2, 3))
+    with pytest.raises(ValueError):
+        per_scan_step(torch.zeros(2, 3), torch.zeros(2, 3), torch.zeros(2, 3))
+    with pytest.raises(ValueError):
+        per_distill(torch.zeros(2, 30), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3))
+    with pytest.raises(ValueError):
+        rows_alloc(16, 40, dtype=torch.float16, device="cpu")
+    with pytest.raises(ValueError):
+        rows_alloc(16, 40, group=48, device="cpu")
