@@ -38,7 +38,12 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
-  for (int s = 0; s < 6; ++s) v += __shfl_xor(v, 1 << s);
+  for (int s = 0; s < 6; ++s) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __float_as_uint(xor_lanes(__uint_as_float((uint32_t)u), s));
+    const uint32_t hi = __float_as_uint(xor_lanes(__uint_as_float((uint32_t)(u >> 32)), s));
+    v += __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+  }
   return v;
 }
 
@@ -63,14 +68,18 @@ __device__ __forceinline__ Row<T> row_of(const DistillArgs& a, int64_t n) {
 template <typename T>
 using Chunk = Pack<T, kVec<T>>;
 
-// Chunk j; -Inf where it reaches outside the row.
-template <typename T>
+// Chunk j; -Inf where it reaches outside the row.  ONCE: past the caches.
+template <typename T, bool ONCE = false>
 __device__ __forceinline__ Chunk<T> load_chunk(const Row<T>& r, uint32_t j) {
   const int64_t i0 = (int64_t)j * kVec<T> - r.mis;
   Chunk<T> v;
   if (i0 >= 0 && i0 + kVec<T> <= r.V) {
-    const T* p = static_cast<const T*>(__builtin_assume_aligned(r.z + i0, 16));
-    __builtin_memcpy(&v, p, 16);
+    if (ONCE) {
+      v = load_once<Chunk<T>>(r.z + i0);
+    } else {
+      const T* p = static_cast<const T*>(__builtin_assume_aligned(r.z + i0, 16));
+      __builtin_memcpy(&v, p, 16);
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < kVec<T>; ++e)
@@ -96,7 +105,7 @@ __device__ __forceinline__ void store_chunk(T* grad, const Row<T>& r, uint32_t j
                                             const float (&g)[kVec<T>]) {
   const int64_t i0 = (int64_t)j * kVec<T> - r.mis;
   if (i0 >= 0 && i0 + kVec<T> <= r.V) {
-    store_vals<T, kVec<T>>(grad + i0, g);
+    store_once<T, kVec<T>>(grad + i0, g);
   } else {
 #pragma unroll
     for (int e = 0; e < kVec<T>; ++e)
@@ -106,20 +115,28 @@ __device__ __forceinline__ void store_chunk(T* grad, const Row<T>& r, uint32_t j
 
 // ------------------------------------------------------------------ the teacher
 //
-// LDS of a workgroup: the K entries, then a bitmap over the tokens of chunks
-// [c0, c1) of the row.
+// LDS of a workgroup: a bitmap, then the K entries.  With a rest the bitmap
+// marks the tokens of chunks [c0, c1) of the row; without one it only has to
+// find repeated entries, and marks them modulo its size (tokens that merely
+// meet there cost a second look in patch_top, no more).
+constexpr uint32_t kHashWords = 1024;
+__host__ __device__ inline uint32_t mark_words(bool tail, int64_t tokens) {
+  const uint32_t w = (uint32_t)((tokens + 127) / 128 * 4);
+  return !tail && w > kHashWords ? kHashWords : w;
+}
+
 struct Lds {
-  int* idx;        // token, -1 where absent
-  float* p;        // teacher's probability (its logit before)
-  float* z;        // student's logit
   uint32_t* bits;  // bit i - c0 * kVec + mis of token i
+  int* idx;        // token, -1 where absent
+  float* p;        // teacher's probability
+  float* z;        // student's logit
 };
-__device__ __forceinline__ Lds lds_of(char* mem, int K) {
+__device__ __forceinline__ Lds lds_of(char* mem, int K, uint32_t words) {
   Lds l;
-  l.idx = reinterpret_cast<int*>(mem);
-  l.p = reinterpret_cast<float*>(mem) + K;
-  l.z = reinterpret_cast<float*>(mem) + 2 * K;
-  l.bits = reinterpret_cast<uint32_t*>(mem) + 3 * K;
+  l.bits = reinterpret_cast<uint32_t*>(mem);
+  l.idx = reinterpret_cast<int*>(l.bits + words);
+  l.p = reinterpret_cast<float*>(l.idx + K);
+  l.z = l.p + K;
   return l;
 }
 
@@ -134,49 +151,61 @@ struct Teacher {
   double ps;    // sum p
   double rest;  // p_r
   bool any;     // an entry is present
-  bool dup;     // two entries name one token of [c0, c1)
+  bool dup;     // two entries may name one token of [c0, c1)
 };
+
+// The lane's first entry, loaded ahead of the row.
+struct Entry {
+  int i;
+  float t;
+};
+__device__ __forceinline__ Entry first_entry(const DistillArgs& a, int64_t n) {
+  const int k = threadIdx.x & 63;
+  Entry e = {-1, 0.0f};
+  if (k < a.K) {
+    e.i = a.tidx[n * a.K + k];
+    e.t = teacher_logit(a, n * a.K + k);
+  }
+  return e;
+}
 
 // One whole wave: entries to LDS, the bitmap of chunks [c0, c1), and the sums.
 // The K exponentials are taken in f64: the rest 1 - sum p would lose its digits
 // in f32 where the top holds nearly everything.
 template <typename T, bool TAIL>
 __device__ __forceinline__ Teacher teacher(const DistillArgs& a, const Row<T>& r, int64_t n,
-                                           const Lds& l, uint32_t c0, uint32_t c1) {
+                                           const Lds& l, uint32_t words, uint32_t c0, uint32_t c1,
+                                           Entry e) {
   const int lane = threadIdx.x & 63;
-  const uint32_t words = ((c1 - c0) * kVec<T> + 31) / 32;
-  for (uint32_t w = lane; w < words; w += 64) l.bits[w] = 0;
+  for (uint32_t w = 4 * lane; w < words; w += 256)
+    *reinterpret_cast<uint4*>(l.bits + w) = make_uint4(0, 0, 0, 0);
   const int64_t lo = (int64_t)c0 * kVec<T> - r.mis;
   const int64_t hi = (int64_t)c1 * kVec<T> - r.mis;
   float tm = kNegInf;
   bool dup = false, any = false;
   for (int k = lane; k < a.K; k += 64) {
-    int i = a.tidx[n * a.K + k];
-    const float t = teacher_logit(a, n * a.K + k);
-    if (i < 0 || i >= (int64_t)r.V) i = -1;
+    if (k != lane) {
+      e.i = a.tidx[n * a.K + k];
+      e.t = teacher_logit(a, n * a.K + k);
+    }
+    const int i = e.i < 0 || e.i >= (int64_t)r.V ? -1 : e.i;
     l.idx[k] = i;
-    l.p[k] = t;
+    l.p[k] = e.t;
     l.z[k] = i >= 0 ? (float)r.z[i] : 0.0f;
     if (i >= 0) {
       any = true;
-      tm = fmaxf(tm, t);
+      tm = fmaxf(tm, e.t);
       if (i >= lo && i < hi) {
-        const uint32_t bit = (uint32_t)(i - lo);
+        uint32_t bit = (uint32_t)(i - lo);
+        if (!TAIL) bit &= 32 * kHashWords - 1;
         dup |= (atomicOr(&l.bits[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u;
       }
     }
   }
   tm = wave_max(tm);
-  double norm = 0.0;  // log of the normaliser of t / tau, relative to `ref`
-  const double ref = TAIL ? 0.0 : (tm == kNegInf ? 0.0 : (double)tm);
-  if (TAIL) {
-    norm = (double)a.tlse[n];
-  } else {
-    double s = 0.0;
-    for (int k = lane; k < a.K; k += 64)
-      if (l.idx[k] >= 0) s += exp(((double)l.p[k] - ref) * a.inv_tau);
-    norm = log(wave_sum(s));
-  }
+  // Without a rest: e = exp((t - largest) / tau), p = e / sum e.
+  const double ref = TAIL || tm == kNegInf ? 0.0 : (double)tm;
+  const double norm = TAIL ? (double)a.tlse[n] : 0.0;
   Teacher o = {0.0, 0.0, 0.0, false, false};
   for (int k = lane; k < a.K; k += 64) {
     double p = 0.0;
@@ -192,12 +221,18 @@ __device__ __forceinline__ Teacher teacher(const DistillArgs& a, const Row<T>& r
   }
   o.h = wave_sum(o.h);
   o.ps = wave_sum(o.ps);
+  o.any = __any(any) && o.ps != 0.0;  // entries at -Inf are none
+  o.dup = __any(dup);
   if (TAIL) {
     o.rest = 1.0 - o.ps;
     if (o.rest < 0.0) o.rest = 0.0;
+  } else if (o.any) {
+    const double inv = 1.0 / o.ps;
+    const float scale = (float)inv;
+    for (int k = lane; k < a.K; k += 64) l.p[k] *= scale;
+    o.h = o.h * inv - log(o.ps);
+    o.ps = 1.0;
   }
-  o.any = __any(any) && o.ps != 0.0;  // entries at -Inf are none
-  o.dup = __any(dup);
   return o;
 }
 
@@ -259,8 +294,8 @@ __device__ __forceinline__ void add_chunk(const Chunk<T>& v, float m, float c, u
 }
 
 // ------------------------------------------------- one workgroup holds the row
-template <typename T, int NT, int R, bool TAIL>
-__global__ __launch_bounds__(NT) void distill_row_kernel(DistillArgs a) {
+template <typename T, int NT, int R, bool TAIL, bool ONCE>
+__global__ __launch_bounds__(NT, NT >= 512 ? 4 : 1) void distill_row_kernel(DistillArgs a) {
   extern __shared__ char mem[];
   __shared__ float red[3][NT / 64];
   __shared__ Teacher t;  // kept here, not in registers across the passes
@@ -275,10 +310,13 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(DistillArgs a) {
     if (tid == 0) a.loss[n] = 0.0f;
     return;
   }
-  const Lds l = lds_of(mem, a.K);
+  const uint32_t words = mark_words(TAIL, (int64_t)r.chunks * kVec<T>);
+  const Lds l = lds_of(mem, a.K, words);
+  Entry first = {-1, 0.0f};
+  if (wv == 0) first = first_entry(a, n);
   auto read_teacher = [&] {
     if (wv != 0) return;
-    const Teacher o = teacher<T, TAIL>(a, r, n, l, 0, r.chunks);
+    const Teacher o = teacher<T, TAIL>(a, r, n, l, words, 0, r.chunks, first);
     if (tid == 0) t = o;
   };
   // The row's loads come first, so that they are in flight meanwhile, unless
@@ -289,7 +327,7 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(DistillArgs a) {
   for (int q = 0; q < R; ++q) {
     const uint32_t j = tid + q * NT;
     if (j < r.chunks) {
-      v[q] = load_chunk(r, j);
+      v[q] = load_chunk<T, ONCE>(r, j);
     } else {
 #pragma unroll
       for (int e = 0; e < kVec<T>; ++e) v[q].v[e] = (T)kNegInf;
@@ -398,7 +436,7 @@ __global__ __launch_bounds__(kPartThreads) void distill_part_kernel(DistillArgs 
   const Span s = span_of(a, r, n, (int)(blockIdx.x % (uint32_t)a.splits));
   uint32_t* bits = reinterpret_cast<uint32_t*>(mem);
   if (TAIL) {
-    const uint32_t words = ((s.c1 - s.c0) * kVec<T> + 31) / 32;
+    const uint32_t words = mark_words(true, (int64_t)(s.c1 - s.c0) * kVec<T>);
     for (uint32_t q = tid; q < words; q += kPartThreads) bits[q] = 0;
     __syncthreads();
     const int64_t lo = (int64_t)s.c0 * kVec<T> - r.mis, hi = (int64_t)s.c1 * kVec<T> - r.mis;
@@ -496,8 +534,8 @@ __global__ __launch_bounds__(64) void distill_join_kernel(DistillArgs a) {
   float loss = 0.0f, p_rest = 0.0f;
   if (!off) {
     const Row<T> r = row_of<T>(a, n);
-    const Lds l = lds_of(mem, a.K);
-    const Teacher t = teacher<T, TAIL>(a, r, n, l, 0, 0);
+    const Lds l = lds_of(mem, a.K, 0);
+    const Teacher t = teacher<T, TAIL>(a, r, n, l, 0, 0, 0, first_entry(a, n));
     const bool dead = S == 0.0f || (!TAIL && !t.any);
     if (dead) S = rest = 0.0f;
     loss = dead ? 0.0f : row_loss(a, l, t, m, S, rest, TAIL);
@@ -532,9 +570,10 @@ __global__ __launch_bounds__(kPartThreads) void distill_grad_kernel(DistillArgs 
     for (uint32_t j = s.c0 + tid; j < s.c1; j += kPartThreads) store_chunk(grad, r, j, zero);
     return;
   }
-  const Lds l = lds_of(mem, a.K);
+  const uint32_t words = mark_words(TAIL, (int64_t)(s.c1 - s.c0) * kVec<T>);
+  const Lds l = lds_of(mem, a.K, words);
   if (wv == 0) {
-    const Teacher t = teacher<T, TAIL>(a, r, n, l, s.c0, s.c1);
+    const Teacher t = teacher<T, TAIL>(a, r, n, l, words, s.c0, s.c1, first_entry(a, n));
     if (tid == 0) sh_dup = t.dup;
   }
   __syncthreads();  // the top's logits are read before they may be overwritten
@@ -567,8 +606,8 @@ __global__ __launch_bounds__(kPartThreads) void distill_grad_kernel(DistillArgs 
             (int64_t)s.c1 * kVec<T> - r.mis);
 }
 
-size_t lds_bytes(int K, int64_t tokens) {
-  return (size_t)K * 12 + (size_t)((tokens + 31) / 32) * 4;
+size_t lds_bytes(int K, bool tail, int64_t tokens) {
+  return (size_t)K * 12 + (size_t)mark_words(tail, tokens) * 4;
 }
 
 int elem_size(int type) { return type == 0 ? 4 : 2; }
@@ -580,14 +619,13 @@ int64_t part_tokens(const DistillArgs& a, int type) {
   return (chunks + a.splits - 1) / a.splits * vec;
 }
 
-template <typename T, int NT, int R>
+template <typename T, int NT, int R, bool ONCE = false>
 hipError_t row_launch(const DistillArgs& a, hipStream_t s) {
-  const size_t lds = lds_bytes(a.K, a.V + 2 * kVec<T>);
+  const size_t lds = lds_bytes(a.K, a.tlse != nullptr, a.V + 2 * kVec<T>);
+  const dim3 grid((uint32_t)a.N);
   if (a.tlse)
-    return launch_kernel(distill_row_kernel<T, NT, R, true>, dim3((uint32_t)a.N), dim3(NT), lds, s,
-                         a);
-  return launch_kernel(distill_row_kernel<T, NT, R, false>, dim3((uint32_t)a.N), dim3(NT), lds, s,
-                       a);
+    return launch_kernel(distill_row_kernel<T, NT, R, true, ONCE>, grid, dim3(NT), lds, s, a);
+  return launch_kernel(distill_row_kernel<T, NT, R, false, ONCE>, grid, dim3(NT), lds, s, a);
 }
 
 template <typename T>
@@ -595,30 +633,36 @@ hipError_t row_typed(const DistillArgs& a, hipStream_t s) {
   const int64_t chunks = (a.V + 2 * kVec<T> - 2) / kVec<T>;  // at most, for any alignment
   if (chunks <= 64 * 4) return row_launch<T, 64, 4>(a, s);
   if (chunks <= 256 * 4) return row_launch<T, 256, 4>(a, s);
-  if (chunks <= 512 * 8) return row_launch<T, 512, 8>(a, s);
-  if (chunks <= 1024 * 9) return row_launch<T, 1024, 9>(a, s);
-  return row_launch<T, 1024, 17>(a, s);
+  // Logits that fill half of the 256 MB Infinity Cache are loaded past it
+  // (128 MB of bf16 logits at 32768 tokens: 70.5 -> 68.6 us, 1 GB at 65536: 468
+  // -> 460 us; 64 MB the other way: 34.5 -> 37.9 us).
+  const bool once = a.N * a.V * (int64_t)sizeof(T) >= (int64_t(1) << 27);
+  if (chunks <= 512 * 9)
+    return once ? row_launch<T, 512, 9, true>(a, s) : row_launch<T, 512, 9>(a, s);
+  if (chunks <= 512 * 17)
+    return once ? row_launch<T, 512, 17, true>(a, s) : row_launch<T, 512, 17>(a, s);
+  return once ? row_launch<T, 1024, 17, true>(a, s) : row_launch<T, 1024, 17>(a, s);
 }
 
 template <typename T>
 hipError_t stats_typed(const DistillArgs& a, int type, hipStream_t s) {
   const dim3 grid((uint32_t)(a.N * a.splits));
-  const size_t lds = lds_bytes(0, part_tokens(a, type));
+  const size_t lds = lds_bytes(0, true, part_tokens(a, type));
   hipError_t e = a.tlse ? launch_kernel(distill_part_kernel<T, true>, grid, dim3(kPartThreads), lds,
                                         s, a)
                         : launch_kernel(distill_part_kernel<T, false>, grid, dim3(kPartThreads), 0,
                                         s, a);
   if (e != hipSuccess) return e;
   return a.tlse ? launch_kernel(distill_join_kernel<T, true>, dim3((uint32_t)a.N), dim3(64),
-                                lds_bytes(a.K, 0), s, a)
+                                lds_bytes(a.K, true, 0), s, a)
                 : launch_kernel(distill_join_kernel<T, false>, dim3((uint32_t)a.N), dim3(64),
-                                lds_bytes(a.K, 0), s, a);
+                                lds_bytes(a.K, true, 0), s, a);
 }
 
 template <typename T>
 hipError_t grad_typed(const DistillArgs& a, int type, hipStream_t s) {
   const dim3 grid((uint32_t)(a.N * a.splits));
-  const size_t lds = lds_bytes(a.K, part_tokens(a, type));
+  const size_t lds = lds_bytes(a.K, a.tlse != nullptr, part_tokens(a, type));
   return a.tlse ? launch_kernel(distill_grad_kernel<T, true>, grid, dim3(kPartThreads), lds, s, a)
                 : launch_kernel(distill_grad_kernel<T, false>, grid, dim3(kPartThreads), lds, s, a);
 }

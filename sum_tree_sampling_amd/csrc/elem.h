@@ -55,4 +55,28 @@ __device__ __forceinline__ void store_vals(T* p, const float (&in)[N]) {
   __builtin_memcpy(p, &r, sizeof r);
 }
 
+// The same, past the caches: for output that this kernel does not read again.
+template <typename T, int N>
+__device__ __forceinline__ void store_once(T* p, const float (&in)[N]) {
+  typedef float fvec __attribute__((ext_vector_type(N)));
+  typedef T tvec __attribute__((ext_vector_type(N)));
+  typedef tvec tvec_u __attribute__((aligned(sizeof(T))));
+  fvec f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = in[i];
+  __builtin_nontemporal_store(__builtin_convertvector(f, tvec), reinterpret_cast<tvec_u*>(p));
+}
+
+// 16 bytes at a 16-byte aligned address that no later access is expected to
+// find in a cache.
+template <typename P>
+__device__ __forceinline__ P load_once(const void* p) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  const u4 u = __builtin_nontemporal_load(static_cast<const u4*>(p));
+  P r;
+  static_assert(sizeof(P) == 16, "16 bytes");
+  __builtin_memcpy(&r, &u, 16);
+  return r;
+}
+
 }  // namespace per

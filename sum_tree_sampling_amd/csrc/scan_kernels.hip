@@ -19,6 +19,14 @@
 
 namespace per {
 namespace {
+#ifndef LB
+#define LB 1
+#endif
+#ifdef NTS
+#define ST store_once
+#else
+#define ST store_vals
+#endif
 
 constexpr int kSteps = 16;                 // steps of a wave in one tile
 constexpr int kWaves = 8;                  // waves of a workgroup, at most
@@ -194,10 +202,10 @@ __global__ __launch_bounds__(kWaves * 64) void scan_forward_kernel(ScanArgs a) {
 #pragma unroll
           for (int c = 0; c < C; ++c)
             hs[c] = r ? ix[s][c] : __builtin_fmaf(f[s][c], hs[c], ix[s][c]);
-          store_vals<T, C>(y + (ts + s) * a.y_st, hs);
+          ST<T, C>(y + (ts + s) * a.y_st, hs);
         } else if (ts + s < p.t_end) {
           const float zero[C] = {};
-          store_vals<T, C>(y + (ts + s) * a.y_st, zero);
+          ST<T, C>(y + (ts + s) * a.y_st, zero);
         }
       }
     }
@@ -298,7 +306,7 @@ __global__ __launch_bounds__(kWaves * 64) void scan_segment_kernel(ScanArgs a) {
 //   dx = full (1 - f),  dg = full (h' - x) f (1 - f).
 // The states of a chunk are computed again from its carry.
 template <typename T, int C>
-__global__ __launch_bounds__(kWaves * 64) void scan_backward_kernel(ScanArgs a) {
+__global__ __launch_bounds__(kWaves * 64, LB) void scan_backward_kernel(ScanArgs a) {
   __shared__ float sA[2][kWaves][C][64], sB[2][kWaves][C][64], sQ[2][kWaves][C][64];
   __shared__ uint32_t sF[2][kWaves];
   const int lane = threadIdx.x & 63;
@@ -459,12 +467,12 @@ __global__ __launch_bounds__(kWaves * 64) void scan_backward_kernel(ScanArgs a) 
             og[c] = full * xv[s][c];
             Es[c] = r ? 0.0f : full * f[s][c];
           }
-          store_vals<T, C>(dx + (ts + s) * a.dx_st, ox);
-          store_vals<T, C>(dg + (ts + s) * a.dg_st, og);
+          ST<T, C>(dx + (ts + s) * a.dx_st, ox);
+          ST<T, C>(dg + (ts + s) * a.dg_st, og);
         } else if (ts + s < p.t_end) {
           const float zero[C] = {};
-          store_vals<T, C>(dx + (ts + s) * a.dx_st, zero);
-          store_vals<T, C>(dg + (ts + s) * a.dg_st, zero);
+          ST<T, C>(dx + (ts + s) * a.dx_st, zero);
+          ST<T, C>(dg + (ts + s) * a.dg_st, zero);
         }
       }
     }

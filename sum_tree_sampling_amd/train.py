@@ -11,11 +11,13 @@ autograd.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 
 import torch
 
-from .per import _check, _stream, load
+from .per import PerError, load
 
 PER_F32, PER_BF16, PER_F16 = 0, 1, 2
 PER_E4M3, PER_I8 = 0, 1
@@ -45,6 +47,8 @@ _SIG = {
     "per_distill_backward": _TOPK + [_vp, _vp, _vp, _i64, _vp],
 }
 _fn: dict = {}
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _get(name):
@@ -56,77 +60,96 @@ def _get(name):
     return f
 
 
+def _fail(rc):
+    raise PerError(rc, load().per_last_error().decode())
+
+
 # ------------------------------------------------------------------ arguments
+#
+# The smallest calls take about as long on the host as on the device, so the
+# checks below ask a tensor for as little as they can; what is wrong is found
+# out only once something is.
 
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
-def _on_device(t, name):
-    _need(t.is_cuda and t.device.index == torch.cuda.current_device(),
-          "%s must be a tensor on the current device" % name)
+def _current():
+    """The current device, as tensors' get_device() gives it (which is -1 on the host)."""
+    return _device() if torch.cuda.is_initialized() else -2
 
 
-def _dense(t, name, dtype, *shape):
+def _stream(stream, dev):
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream):
+    """Allocations inside belong to the call's stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _empty(stream, shape, dtype, dev):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _refuse(t, name, dtype, shape, dev):
+    _need(isinstance(t, torch.Tensor), "%s must be a tensor" % name)
+    _need(t.get_device() == dev, "%s must be a tensor on the current device" % name)
+    _need(t.dtype is dtype, "%s has type %s, expected %s" % (name, t.dtype, dtype))
+    _need(tuple(t.shape) == tuple(shape),
+          "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    _need(False, "%s must be contiguous" % name)
+
+
+def _dense(t, name, dtype, shape, dev):
     """Pointer of a dense tensor of this type and shape (NULL for None)."""
     if t is None:
         return None
-    _on_device(t, name)
-    _need(t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype,
-          "%s has type %s" % (name, t.dtype))
-    _need(tuple(t.shape) == shape, "%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
-    _need(t.is_contiguous(), "%s must be contiguous" % name)
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
     return t.data_ptr()
+
+
+def _flags(t, name, shape, dev):
+    return None if t is None else _dense(t, name, torch.uint8 if t.dtype is torch.uint8 else torch.bool,
+                                         shape, dev)
 
 
 def _row_stride(t, name):
     """Stride between the rows of a matrix with unit column stride."""
+    s0, s1 = t.stride()
     n, d = t.shape
-    _need(d <= 1 or t.stride(1) == 1, "%s must have unit stride in its last dimension" % name)
-    return t.stride(0) if n > 1 else max(d, t.stride(0))
+    if s1 != 1 and d > 1:
+        raise ValueError("%s must have unit stride in its last dimension" % name)
+    return s0 if n > 1 else max(d, s0)
 
 
-def _view(t, name, dtype, shape):
+def _matrix(t, name, dtype, shape, dev):
+    """(pointer, row stride) of a matrix."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr(), _row_stride(t, name)
+
+
+def _view(t, name, dtype, shape, dev):
     """(pointer, stride between sequences, between steps) of a [B x T x D] view."""
-    _on_device(t, name)
-    _need(t.dtype == dtype, "%s has type %s, expected %s" % (name, t.dtype, dtype))
-    _need(t.shape == shape, "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    s = t.stride()
-    _need(shape[2] <= 1 or s[2] == 1, "%s must have unit stride in its last dimension" % name)
-    return t.data_ptr(), s[0], s[1]
-
-
-def _flags(t, name, *shape):
-    return _dense(t, name, (torch.bool, torch.uint8), *shape)
-
-
-class _On:
-    """Allocations inside belong to the call's stream."""
-
-    def __init__(self, stream):
-        self.cm = None
-        if stream is not None:
-            s = stream
-            if not isinstance(s, torch.cuda.Stream):
-                s = torch.cuda.ExternalStream(int(s))
-            self.cm = torch.cuda.stream(s)
-
-    def __enter__(self):
-        if self.cm is not None:
-            self.cm.__enter__()
-
-    def __exit__(self, *a):
-        if self.cm is not None:
-            self.cm.__exit__(*a)
-
-
-def _scratch(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, dtype, shape, dev)
+    sb, st, sd = t.stride()
+    if sd != 1 and shape[2] > 1:
+        raise ValueError("%s must have unit stride in its last dimension" % name)
+    return t.data_ptr(), sb, st
 
 
 # ------------------------------------------------------------ 8-bit row store
@@ -143,77 +166,85 @@ def rows_alloc(capacity, dim, dtype=torch.float8_e4m3fn, group=128, device="cuda
     return raw[:, :dim].view(dtype), raw.view(torch.float32)[:, at // 4:at // 4 + ng]
 
 
-def _store(codes, scales, group):
-    _on_device(codes, "codes")
-    _on_device(scales, "scales")
+def _store(codes, scales, group, dev):
     fmt = _FORMAT.get(codes.dtype)
-    _need(fmt is not None and codes.dim() == 2, "codes must be [capacity x dim], float8_e4m3fn or int8")
-    _need(group in (0, 32, 64, 128), "group is 0 (the row), 32, 64 or 128")
-    cap, dim = codes.shape
-    ng = 1 if group == 0 else -(-dim // group)
-    _need(scales.dtype == torch.float32 and tuple(scales.shape) == (cap, ng),
-          "scales must be [capacity x %d] float32" % ng)
-    return (cap, dim, fmt, group, codes.data_ptr(), _row_stride(codes, "codes"), scales.data_ptr(),
-            _row_stride(scales, "scales"))
+    if fmt is None or codes.dim() != 2:
+        raise ValueError("codes must be [capacity x dim], float8_e4m3fn or int8")
+    if group not in (0, 32, 64, 128):
+        raise ValueError("group is 0 (the row), 32, 64 or 128")
+    cap, dim = shape = codes.shape
+    return (cap, dim, fmt, group, *_matrix(codes, "codes", codes.dtype, shape, dev),
+            *_matrix(scales, "scales", torch.float32, (cap, -(-dim // group) if group else 1), dev))
 
 
-def _source(src, dim):
-    _on_device(src, "src")
+def _source(src, dim, dev):
     t = _TYPE.get(src.dtype)
-    _need(t is not None and src.dim() == 2 and src.shape[1] == dim,
-          "src must be [count x %d] of float32, bfloat16 or float16" % dim)
-    return src.data_ptr(), t, _row_stride(src, "src")
+    if t is None or src.dim() != 2:
+        raise ValueError("src must be [count x %d] of float32, bfloat16 or float16" % dim)
+    p, st = _matrix(src, "src", src.dtype, (src.shape[0], dim), dev)
+    return p, t, st
 
 
 def per_rows_write(codes, scales, src, first=0, group=128, stream=None):
     """Quantise the rows of src into the ring's slots first, first + 1, ..."""
-    st = _store(codes, scales, group)
-    s = _source(src, st[1])
-    _check(_get("per_rows_write")(*st, src.shape[0], int(first), *s, _stream(stream)))
+    dev = _current()
+    st = _store(codes, scales, group, dev)
+    rc = _get("per_rows_write")(*st, src.shape[0], first, *_source(src, st[1], dev),
+                                _stream(stream, dev))
+    if rc:
+        _fail(rc)
 
 
 def per_rows_write_at(codes, scales, src, slots, claims, group=128, stream=None):
     """Quantise row j of src into slot slots[j]; of a repeated slot the last
     position wins.  claims: [capacity] int32 zeros, zero again afterwards."""
-    st = _store(codes, scales, group)
-    s = _source(src, st[1])
+    dev = _current()
+    st = _store(codes, scales, group, dev)
+    s = _source(src, st[1], dev)
     n = src.shape[0]
-    _check(_get("per_rows_write_at")(*st, n, _dense(slots, "slots", torch.int64, n),
-                                     _dense(claims, "claims", torch.int32, st[0]), *s,
-                                     _stream(stream)))
+    rc = _get("per_rows_write_at")(*st, n, _dense(slots, "slots", torch.int64, (n,), dev),
+                                   _dense(claims, "claims", torch.int32, (st[0],), dev), *s,
+                                   _stream(stream, dev))
+    if rc:
+        _fail(rc)
 
 
 def per_rows_read(codes, scales, idx, window=1, group=128, out=None, dtype=torch.float32,
                   stream=None):
     """[B x window x dim]: the rows of slots idx[b], idx[b] + 1, ... of the ring."""
-    st = _store(codes, scales, group)
-    _need(idx.dim() == 1, "idx must be [B]")
-    B, window, dim = idx.shape[0], int(window), st[1]
+    dev = _current()
+    st = _store(codes, scales, group, dev)
+    B, dim = idx.shape[0], st[1]
     _need(window >= 1, "window is at least 1")
-    p = _dense(idx, "idx", torch.int64, B)
     if out is None:
-        with _On(stream):
-            out = torch.empty(B, window, dim, dtype=dtype, device=codes.device)
-    o, t = _dense(out, "out", (torch.float32, torch.bfloat16, torch.float16), B, window, dim), \
-        _TYPE[out.dtype]
-    _check(_get("per_rows_read")(*st, B, p, window, o, t, dim, _stream(stream)))
+        out = _empty(stream, (B, window, dim), dtype, dev)
+    t = _TYPE.get(out.dtype)
+    _need(t is not None, "out has type %s" % out.dtype)
+    rc = _get("per_rows_read")(*st, B, _dense(idx, "idx", torch.int64, (B,), dev), window,
+                               _dense(out, "out", out.dtype, (B, window, dim), dev), t, dim,
+                               _stream(stream, dev))
+    if rc:
+        _fail(rc)
     return out
 
 
 # ----------------------------------------------------- gated linear recurrence
 
+@functools.lru_cache(maxsize=1024)
 def per_scan_workspace_bytes(B, T, D) -> int:
     out = _sz(0)
-    _check(_get("per_scan_workspace_bytes")(int(B), int(T), int(D), ctypes.byref(out)))
+    rc = _get("per_scan_workspace_bytes")(B, T, D, ctypes.byref(out))
+    if rc:
+        _fail(rc)
     return out.value
 
 
-def _seq(x, g):
-    _need(x.dim() == 3, "x must be [B x T x D]")
+def _seq(x, g, dev):
     t = _TYPE.get(x.dtype)
-    _need(t is not None, "x has type %s" % x.dtype)
+    if t is None or x.dim() != 3:
+        raise ValueError("x must be [B x T x D] of float32, bfloat16 or float16")
     shape = x.shape
-    return shape, t, _view(x, "x", x.dtype, shape), _view(g, "g", x.dtype, shape)
+    return shape, t, _view(x, "x", x.dtype, shape, dev), _view(g, "g", x.dtype, shape, dev)
 
 
 def per_scan_forward(x, g, reset=None, length=None, h0=None, y=None, h_last=None, carries=None,
@@ -221,106 +252,103 @@ def per_scan_forward(x, g, reset=None, length=None, h0=None, y=None, h_last=None
     """h_t = f h_{t-1} + (1 - f) x_t with f = sigmoid(g_t) along dim 1 of x, g
     [B x T x D].  Returns (y [B x T x D], h_last [B x D] f32, carries: the f32
     states that per_scan_backward takes)."""
-    shape, t, vx, vg = _seq(x, g)
+    dev = _current()
+    shape, t, vx, vg = _seq(x, g, dev)
     B, T, D = shape
-    dev = x.device
-    r, n = _flags(reset, "reset", B, T), _dense(length, "length", torch.int64, B)
-    p0 = _dense(h0, "h0", torch.float32, B, D)
-    nbytes = per_scan_workspace_bytes(B, T, D) if T > PER_SCAN_CHUNK else 0
-    nch = -(-T // PER_SCAN_CHUNK)
-    with _On(stream):
-        if y is None:
-            y = torch.empty(B, T, D, dtype=x.dtype, device=dev)
-        if h_last is None:
-            h_last = torch.empty(B, D, dtype=torch.float32, device=dev)
-        if carries is None:
-            carries = torch.empty(B, nch, D, dtype=torch.float32, device=dev)
-        ws = _scratch(nbytes, dev)
-    _check(_get("per_scan_forward")(
-        B, T, D, t, *vx, *vg, r, n, p0, *_view(y, "y", x.dtype, shape),
-        _dense(h_last, "h_last", torch.float32, B, D),
-        _dense(carries, "carries", torch.float32, B, nch, D), _ptr(ws), nbytes, _stream(stream)))
+    f32 = torch.float32
+    chunks = (B, -(-T // PER_SCAN_CHUNK), D)
+    nbytes = per_scan_workspace_bytes(B, T, D)
+    if y is None:
+        y = _empty(stream, shape, x.dtype, dev)
+    if h_last is None:
+        h_last = _empty(stream, (B, D), f32, dev)
+    if carries is None:
+        carries = _empty(stream, chunks, f32, dev)
+    ws = _empty(stream, nbytes, torch.uint8, dev) if nbytes else None
+    rc = _get("per_scan_forward")(
+        B, T, D, t, *vx, *vg, _flags(reset, "reset", (B, T), dev),
+        _dense(length, "length", torch.int64, (B,), dev), _dense(h0, "h0", f32, (B, D), dev),
+        *_view(y, "y", x.dtype, shape, dev), _dense(h_last, "h_last", f32, (B, D), dev),
+        _dense(carries, "carries", f32, chunks, dev), ws.data_ptr() if nbytes else None, nbytes,
+        _stream(stream, dev))
+    if rc:
+        _fail(rc)
     return y, h_last, carries
 
 
 def per_scan_backward(x, g, carries, dy, reset=None, length=None, dh_last=None, dx=None, dg=None,
                       dh0=None, stream=None):
     """Gradients (dx, dg, dh0) of per_scan_forward from dy and dh_last."""
-    shape, t, vx, vg = _seq(x, g)
+    dev = _current()
+    shape, t, vx, vg = _seq(x, g, dev)
     B, T, D = shape
-    dev = x.device
-    r, n = _flags(reset, "reset", B, T), _dense(length, "length", torch.int64, B)
-    nbytes = per_scan_workspace_bytes(B, T, D) if T > PER_SCAN_CHUNK else 0
-    c = _dense(carries, "carries", torch.float32, B, -(-T // PER_SCAN_CHUNK), D)
-    vdy = _view(dy, "dy", x.dtype, shape)
-    pl = _dense(dh_last, "dh_last", torch.float32, B, D)
-    with _On(stream):
-        if dx is None:
-            dx = torch.empty(B, T, D, dtype=x.dtype, device=dev)
-        if dg is None:
-            dg = torch.empty(B, T, D, dtype=x.dtype, device=dev)
-        if dh0 is None:
-            dh0 = torch.empty(B, D, dtype=torch.float32, device=dev)
-        ws = _scratch(nbytes, dev)
-    _check(_get("per_scan_backward")(
-        B, T, D, t, *vx, *vg, r, n, c, *vdy, pl, *_view(dx, "dx", x.dtype, shape),
-        *_view(dg, "dg", x.dtype, shape), _dense(dh0, "dh0", torch.float32, B, D), _ptr(ws), nbytes,
-        _stream(stream)))
+    f32 = torch.float32
+    nbytes = per_scan_workspace_bytes(B, T, D)
+    if dx is None:
+        dx = _empty(stream, shape, x.dtype, dev)
+    if dg is None:
+        dg = _empty(stream, shape, x.dtype, dev)
+    if dh0 is None:
+        dh0 = _empty(stream, (B, D), f32, dev)
+    ws = _empty(stream, nbytes, torch.uint8, dev) if nbytes else None
+    rc = _get("per_scan_backward")(
+        B, T, D, t, *vx, *vg, _flags(reset, "reset", (B, T), dev),
+        _dense(length, "length", torch.int64, (B,), dev),
+        _dense(carries, "carries", f32, (B, -(-T // PER_SCAN_CHUNK), D), dev),
+        *_view(dy, "dy", x.dtype, shape, dev), _dense(dh_last, "dh_last", f32, (B, D), dev),
+        *_view(dx, "dx", x.dtype, shape, dev), *_view(dg, "dg", x.dtype, shape, dev),
+        _dense(dh0, "dh0", f32, (B, D), dev), ws.data_ptr() if nbytes else None, nbytes,
+        _stream(stream, dev))
+    if rc:
+        _fail(rc)
     return dx, dg, dh0
 
 
 def per_scan_step(x, g, h, reset=None, h_out=None, y=None, stream=None):
     """One step of B sequences: x, g [B x D], h [B x D] f32 (updated in place
     without h_out).  Returns (y, h_out)."""
-    _need(x.dim() == 2 and x.dtype in _TYPE, "x must be [B x D] of float32, bfloat16 or float16")
-    B, D = x.shape
-    _on_device(x, "x")
-    _on_device(g, "g")
-    _need(g.shape == x.shape and g.dtype == x.dtype, "g must have the shape and type of x")
+    dev = _current()
+    t = _TYPE.get(x.dtype)
+    if t is None or x.dim() != 2:
+        raise ValueError("x must be [B x D] of float32, bfloat16 or float16")
+    dt, shape = x.dtype, x.shape
+    mx, mg = _matrix(x, "x", dt, shape, dev), _matrix(g, "g", dt, shape, dev)
     if h_out is None:
         h_out = h
     if y is None:
-        with _On(stream):
-            y = torch.empty(B, D, dtype=x.dtype, device=x.device)
-    _on_device(y, "y")
-    _need(y.shape == x.shape and y.dtype == x.dtype, "y must have the shape and type of x")
-    _check(_get("per_scan_step")(
-        B, D, _TYPE[x.dtype], x.data_ptr(), _row_stride(x, "x"), g.data_ptr(), _row_stride(g, "g"),
-        _flags(reset, "reset", B), _dense(h, "h", torch.float32, B, D),
-        _dense(h_out, "h_out", torch.float32, B, D), y.data_ptr(), _row_stride(y, "y"),
-        _stream(stream)))
+        y = _empty(stream, shape, dt, dev)
+    rc = _get("per_scan_step")(
+        *shape, t, *mx, *mg,
+        _flags(reset, "reset", shape[:1], dev), _dense(h, "h", torch.float32, shape, dev),
+        _dense(h_out, "h_out", torch.float32, shape, dev), *_matrix(y, "y", dt, shape, dev),
+        _stream(stream, dev))
+    if rc:
+        _fail(rc)
     return y, h_out
 
 
 # ----------------------------------------------------------------- distillation
 
+@functools.lru_cache(maxsize=1024)
 def per_distill_workspace_bytes(N, V, type) -> int:  # noqa: A002
     out = _sz(0)
-    _check(_get("per_distill_workspace_bytes")(int(N), int(V), int(type), ctypes.byref(out)))
+    rc = _get("per_distill_workspace_bytes")(N, V, type, ctypes.byref(out))
+    if rc:
+        _fail(rc)
     return out.value
 
 
-def _top(logits, tidx, tlogit, tlse, temperature):
-    _on_device(logits, "logits")
-    _need(logits.dim() == 2 and logits.dtype in _TYPE,
-          "logits must be [N x V] of float32, bfloat16 or float16")
-    N, V = logits.shape
-    _need(tidx.dim() == 2 and tidx.shape[0] == N, "tidx must be [N x K]")
-    K = tidx.shape[1]
-    return (N, V, K, _TYPE[logits.dtype], logits.data_ptr(), _row_stride(logits, "logits"),
-            _dense(tidx, "tidx", torch.int32, N, K),
-            _dense(tlogit, "tlogit", (torch.float32, torch.bfloat16, torch.float16), N, K),
-            _TYPE[tlogit.dtype], _dense(tlse, "tlse", torch.float32, N), float(temperature))
-
-
-def _grad(grad, logits, stream):
-    if grad is None:
-        with _On(stream):
-            grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    _on_device(grad, "grad")
-    _need(grad.shape == logits.shape and grad.dtype == logits.dtype,
-          "grad must have the shape and type of logits")
-    return grad, _row_stride(grad, "grad")
+def _top(logits, tidx, tlogit, tlse, temperature, dev):
+    t = _TYPE.get(logits.dtype)
+    if t is None or logits.dim() != 2 or tidx.dim() != 2:
+        raise ValueError("logits must be [N x V] of float32, bfloat16 or float16, tidx [N x K]")
+    N, V = shape = logits.shape
+    top = (N, tidx.shape[1])
+    tt = _TYPE.get(tlogit.dtype)
+    _need(tt is not None, "tlogit has type %s" % tlogit.dtype)
+    return (N, V, top[1], t, *_matrix(logits, "logits", logits.dtype, shape, dev),
+            _dense(tidx, "tidx", torch.int32, top, dev), _dense(tlogit, "tlogit", tlogit.dtype, top, dev),
+            tt, _dense(tlse, "tlse", torch.float32, (N,), dev), temperature)
 
 
 def per_distill(logits, tidx, tlogit, tlse=None, temperature=1.0, weight=None, loss=None, grad=None,
@@ -328,45 +356,55 @@ def per_distill(logits, tidx, tlogit, tlse=None, temperature=1.0, weight=None, l
     """Per-row distillation loss [N] (not weighted) and its gradient by the
     logits [N x V] (weighted), against the teacher's logits tlogit [N x K] at
     tokens tidx [N x K] int32.  grad may be logits."""
-    a = _top(logits, tidx, tlogit, tlse, temperature)
-    N = a[0]
-    w = _dense(weight, "weight", torch.float32, N)
-    grad, gs = _grad(grad, logits, stream)
+    dev = _current()
+    a = _top(logits, tidx, tlogit, tlse, temperature, dev)
+    N, f32 = a[0], torch.float32
     nbytes = per_distill_workspace_bytes(N, a[1], a[3])
-    with _On(stream):
-        if loss is None:
-            loss = torch.empty(N, dtype=torch.float32, device=logits.device)
-        ws = _scratch(nbytes, logits.device)
-    _check(_get("per_distill")(*a, w, _dense(loss, "loss", torch.float32, N), grad.data_ptr(), gs,
-                               _ptr(ws), nbytes, _stream(stream)))
+    if grad is None:
+        grad = _empty(stream, logits.shape, logits.dtype, dev)
+    if loss is None:
+        loss = _empty(stream, (N,), f32, dev)
+    ws = _empty(stream, nbytes, torch.uint8, dev) if nbytes else None
+    rc = _get("per_distill")(
+        *a, _dense(weight, "weight", f32, (N,), dev), _dense(loss, "loss", f32, (N,), dev),
+        *_matrix(grad, "grad", logits.dtype, logits.shape, dev), ws.data_ptr() if nbytes else None,
+        nbytes, _stream(stream, dev))
+    if rc:
+        _fail(rc)
     return loss, grad
 
 
 def per_distill_forward(logits, tidx, tlogit, tlse=None, temperature=1.0, loss=None, saved=None,
                         stream=None):
     """Per-row loss [N], and the row statistics per_distill_backward takes."""
-    a = _top(logits, tidx, tlogit, tlse, temperature)
-    N = a[0]
+    dev = _current()
+    a = _top(logits, tidx, tlogit, tlse, temperature, dev)
+    N, f32 = a[0], torch.float32
     nbytes = per_distill_workspace_bytes(N, a[1], a[3])
-    with _On(stream):
-        if loss is None:
-            loss = torch.empty(N, dtype=torch.float32, device=logits.device)
-        if saved is None:
-            saved = torch.empty(N, 4, dtype=torch.float32, device=logits.device)
-        ws = _scratch(nbytes, logits.device)
-    _check(_get("per_distill_forward")(*a, _dense(loss, "loss", torch.float32, N),
-                                       _dense(saved, "saved", torch.float32, N, 4), _ptr(ws),
-                                       nbytes, _stream(stream)))
+    if loss is None:
+        loss = _empty(stream, (N,), f32, dev)
+    if saved is None:
+        saved = _empty(stream, (N, 4), f32, dev)
+    ws = _empty(stream, nbytes, torch.uint8, dev) if nbytes else None
+    rc = _get("per_distill_forward")(
+        *a, _dense(loss, "loss", f32, (N,), dev), _dense(saved, "saved", f32, (N, 4), dev),
+        ws.data_ptr() if nbytes else None, nbytes, _stream(stream, dev))
+    if rc:
+        _fail(rc)
     return loss, saved
 
 
 def per_distill_backward(logits, tidx, tlogit, saved, gloss, tlse=None, temperature=1.0, grad=None,
                          stream=None):
     """Gradient by the logits from the gradient by each row's loss."""
-    a = _top(logits, tidx, tlogit, tlse, temperature)
-    N = a[0]
-    grad, gs = _grad(grad, logits, stream)
-    _check(_get("per_distill_backward")(*a, _dense(saved, "saved", torch.float32, N, 4),
-                                        _dense(gloss, "gloss", torch.float32, N), grad.data_ptr(),
-                                        gs, _stream(stream)))
+    dev = _current()
+    a = _top(logits, tidx, tlogit, tlse, temperature, dev)
+    N, f32 = a[0], torch.float32
+    if grad is None:
+        grad = _empty(stream, logits.shape, logits.dtype, dev)
+    rc = _get("per_distill_backward")(
+        *a, _dense(saved, "saved", f32, (N, 4), dev), _dense(gloss, "gloss", f32, (N,), dev),
+        *_matrix(grad, "grad", logits.dtype, logits.shape, dev), _stream(stream, dev))
+    if rc:
+        _fail(rc)
     return grad
