@@ -43,7 +43,7 @@ extern "C" {
 #define PER_MAX_ROW_DIM (1LL << 20)
 #define PER_MAX_TOP 1024
 #define PER_MAX_VOCAB (1LL << 24)
-#define PER_SCAN_CHUNK 128
+#define PER_SCAN_CHUNK 64
 
 /*
  * The row store.  Row r of a store of `capacity` rows of `dim` values holds
@@ -103,7 +103,7 @@ int per_rows_read(int64_t capacity, int64_t dim, int32_t format, int32_t group,
  * States (h0, h_last, dh_last, dh0) are dense [B x D] f32.
  *
  * per_scan_forward writes y, d_h_last (or NULL), the state after the last
- *   step of each sequence, and d_carries (or NULL), [B x ceil(T / 128) x D]
+ *   step of each sequence, and d_carries (or NULL), [B x ceil(T / 64) x D]
  *   f32: the state before each chunk of PER_SCAN_CHUNK steps, for the backward
  *   pass.  d_h_last may be d_h0.
  * per_scan_backward takes those carries, dy, and d_dh_last, the gradient of

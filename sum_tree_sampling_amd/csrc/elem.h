@@ -58,13 +58,17 @@ __device__ __forceinline__ void store_vals(T* p, const float (&in)[N]) {
 // The same, past the caches: for output that this kernel does not read again.
 template <typename T, int N>
 __device__ __forceinline__ void store_once(T* p, const float (&in)[N]) {
-  typedef float fvec __attribute__((ext_vector_type(N)));
-  typedef T tvec __attribute__((ext_vector_type(N)));
-  typedef tvec tvec_u __attribute__((aligned(sizeof(T))));
-  fvec f;
+  if constexpr (N == 1) {
+    __builtin_nontemporal_store((T)in[0], p);
+  } else {
+    typedef float fvec __attribute__((ext_vector_type(N)));
+    typedef T tvec __attribute__((ext_vector_type(N)));
+    typedef tvec tvec_u __attribute__((aligned(sizeof(T))));
+    fvec f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = in[i];
-  __builtin_nontemporal_store(__builtin_convertvector(f, tvec), reinterpret_cast<tvec_u*>(p));
+    for (int i = 0; i < N; ++i) f[i] = in[i];
+    __builtin_nontemporal_store(__builtin_convertvector(f, tvec), reinterpret_cast<tvec_u*>(p));
+  }
 }
 
 // 16 bytes at a 16-byte aligned address that no later access is expected to

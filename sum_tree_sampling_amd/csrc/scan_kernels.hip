@@ -14,34 +14,43 @@
 // A reset makes its map ignore the state (a flag beside A = 0), so an infinite
 // or NaN state before it does not leak through 0 * Inf.
 
+#include <type_traits>
+
 #include "elem.h"
 #include "train_internal.h"
 
 namespace per {
 namespace {
-#ifndef LB
-#define LB 1
-#endif
-#ifdef NTS
-#define ST store_once
-#else
-#define ST store_vals
-#endif
 
-constexpr int kSteps = 16;                 // steps of a wave in one tile
+// Steps of a wave in one tile.  The backward pass keeps four values of a step
+// (f, 1 - f, the packed inputs, the gate's weight), so that 16 steps of two
+// channels would not leave two workgroups' registers to a CU.
+#ifndef LBB
+#define LBB 4
+#endif
+#ifndef LBF
+#define LBF 4
+#endif
+#ifndef SF
+#define SF 16
+#endif
+#ifndef SB
+#define SB 8
+#endif
+constexpr int kForward = SF;
+constexpr int kBackward = SB;
 constexpr int kWaves = 8;                  // waves of a workgroup, at most
-constexpr int kChunk = kSteps * kWaves;    // PER_SCAN_CHUNK
+constexpr int kChunk = 64;                 // PER_SCAN_CHUNK
+constexpr int kSegment = 128;              // segments are multiples of it
 constexpr int kMaxSeg = 128;
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// f = sigmoid(g) and 1 - f, each to f32 precision.
+// f = sigmoid(g) = 1 / (1 + e) and 1 - f = e / (1 + e), each to f32 precision;
+// e = exp(-g) is kept finite so that the second does not become Inf * 0.
 __device__ __forceinline__ void gate(float g, float& f, float& i) {
-  const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(g) * kLog2e);
-  const float large = __builtin_amdgcn_rcpf(1.0f + e);
-  const float small = e * large;
-  f = g >= 0.0f ? large : small;
-  i = g >= 0.0f ? small : large;
-  if (g != g) f = i = g;
+  const float e = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(-kLog2e * g, 126.0f));
+  f = __builtin_amdgcn_rcpf(1.0f + e);
+  i = e * f;
 }
 
 // Position of a workgroup: sequence, segment, first channel of the lane.
@@ -72,10 +81,11 @@ __device__ __forceinline__ Place place(const ScanArgs& a) {
   return p;
 }
 
-// Steps of [ts, ts + kSteps) before `live`.
+// Steps of [ts, ts + S) before `live`.
+template <int S>
 __device__ __forceinline__ int steps_at(int64_t ts, int64_t live) {
   const int64_t n = live - ts;
-  return n < 0 ? 0 : n > kSteps ? kSteps : (int)n;
+  return n < 0 ? 0 : n > S ? S : (int)n;
 }
 
 // Bit s: an episode begins at step ts + s (s < n), the same in every lane.
@@ -85,18 +95,29 @@ __device__ __forceinline__ uint32_t reset_mask(const uint8_t* reset, int64_t ts,
   return (uint32_t)__ballot(lane < n && reset[ts + lane] != 0);
 }
 
-// kSteps rows of C channels from row ts of a [T x D] matrix; rows past the
-// last live one are loaded from it and not used.
-template <typename T, int C>
-__device__ __forceinline__ void load_steps(const T* p, int64_t st, int64_t ts, int n,
-                                           Pack<T, C> (&v)[kSteps]) {
+// A [T x D] matrix of one sequence: the row's address is the same in every
+// lane, the lane's channel an offset from it.
+template <typename T>
+struct Rows {
+  T* p;
+  int64_t st;
+  uint32_t d;
+  __device__ __forceinline__ T* at(int64_t t) const { return p + t * st + d; }
+};
+
+// S rows of C channels from row ts.  Without FULL only the first n are
+// live: the others are loaded from the last of them and not used.
+template <typename T, int C, bool FULL, int S>
+__device__ __forceinline__ void load_steps(const Rows<const T>& r, int64_t ts, int n,
+                                           Pack<T, C> (&v)[S]) {
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s)
-    v[s] = load_pack<T, C>(p + (ts + (s < n ? s : n - 1)) * st);
+  for (int s = 0; s < S; ++s)
+    v[s] = load_pack<T, C>(r.at(ts + (FULL || s < n ? s : n - 1)));
 }
 
 template <typename T, int C>
-__global__ __launch_bounds__(kWaves * 64) void scan_forward_kernel(ScanArgs a) {
+__global__ __launch_bounds__(kWaves * 64, LBF) void scan_forward_kernel(ScanArgs a) {
+  constexpr int S = kForward;
   __shared__ float sA[2][kWaves][C][64], sB[2][kWaves][C][64];
   __shared__ uint32_t sF[2][kWaves];
   const int lane = threadIdx.x & 63;
@@ -104,9 +125,10 @@ __global__ __launch_bounds__(kWaves * 64) void scan_forward_kernel(ScanArgs a) {
   const int nw = blockDim.x >> 6;
   const Place p = place<C>(a);
   const bool in = p.d < a.D;
-  const T* x = static_cast<const T*>(a.x) + p.b * a.x_sb + p.d;
-  const T* g = static_cast<const T*>(a.g) + p.b * a.g_sb + p.d;
-  T* y = static_cast<T*>(a.y) + p.b * a.y_sb + p.d;
+  const uint32_t d32 = (uint32_t)p.d;
+  const Rows<const T> x = {static_cast<const T*>(a.x) + p.b * a.x_sb, a.x_st, d32};
+  const Rows<const T> g = {static_cast<const T*>(a.g) + p.b * a.g_sb, a.g_st, d32};
+  const Rows<T> y = {static_cast<T*>(a.y) + p.b * a.y_sb, a.y_st, d32};
   const uint8_t* reset = a.reset ? a.reset + p.b * a.T : nullptr;
   float h[C];
 #pragma unroll
@@ -143,41 +165,42 @@ __global__ __launch_bounds__(kWaves * 64) void scan_forward_kernel(ScanArgs a) {
   }
 
   int buf = 0;
-  for (int64_t t0 = p.t_begin; t0 < p.t_end; t0 += nw * kSteps, buf ^= 1) {
-    const int64_t ts = t0 + wv * kSteps;
-    const int n = steps_at(ts, p.live);
+  for (int64_t t0 = p.t_begin; t0 < p.t_end; t0 += nw * S, buf ^= 1) {
+    const int64_t ts = t0 + wv * S;
+    const int n = steps_at<S>(ts, p.live);
     const uint32_t mask = reset_mask(reset, ts, n);
-    if (a.carries && wv == 0 && in) {
-      float* c0 = a.carries + (p.b * ((a.T + kChunk - 1) / kChunk) + t0 / kChunk) * a.D + p.d;
-#pragma unroll
-      for (int c = 0; c < C; ++c) c0[c] = h[c];
-    }
-    float f[kSteps][C], ix[kSteps][C];
+    float f[S][C], ix[S][C];
     float A[C], B[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
-    if (n > 0 && in) {
-      Pack<T, C> gx[kSteps], gg[kSteps];
-      load_steps<T, C>(x, a.x_st, ts, n, gx);
-      load_steps<T, C>(g, a.g_st, ts, n, gg);
+    // Whole tiles without an episode's begin, nearly all of a long sequence,
+    // go without the per-step conditions.
+    const bool full = n == S && mask == 0;
+    auto reduce = [&](auto is_full) {
+      constexpr bool FULL = decltype(is_full)::value;
+      Pack<T, C> px[S], pg[S];
+      load_steps<T, C, FULL, S>(x, ts, n, px);
+      load_steps<T, C, FULL, S>(g, ts, n, pg);
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
+      for (int s = 0; s < S; ++s) {
         float xv[C], gv[C];
-        unpack(gx[s], xv);
-        unpack(gg[s], gv);
+        unpack(px[s], xv);
+        unpack(pg[s], gv);
+        const bool r = !FULL && ((mask >> s) & 1u);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           float i;
           gate(gv[c], f[s][c], i);
           ix[s][c] = i * xv[c];
-          if (s < n) {
-            const bool r = (mask >> s) & 1u;
+          if (FULL || s < n) {
             B[c] = r ? ix[s][c] : __builtin_fmaf(f[s][c], B[c], ix[s][c]);
             A[c] = r ? 0.0f : A[c] * f[s][c];
           }
         }
       }
-    }
+    };
+    if (in && full) reduce(std::true_type{});
+    else if (in && n > 0) reduce(std::false_type{});
 #pragma unroll
     for (int c = 0; c < C; ++c) sA[buf][wv][c][lane] = A[c], sB[buf][wv][c][lane] = B[c];
     if (lane == 0) sF[buf][wv] = mask;
@@ -194,18 +217,30 @@ __global__ __launch_bounds__(kWaves * 64) void scan_forward_kernel(ScanArgs a) {
         h[c] = fl ? wb : __builtin_fmaf(sA[buf][w][c][lane], h[c], wb);
       }
     }
-    if (in) {
+    if (a.carries && in && ts % kChunk == 0 && ts < p.t_end) {
+      float* c0 = a.carries + (p.b * ((a.T + kChunk - 1) / kChunk) + ts / kChunk) * a.D + p.d;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
+      for (int c = 0; c < C; ++c) c0[c] = hs[c];
+    }
+    if (in && full) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) hs[c] = __builtin_fmaf(f[s][c], hs[c], ix[s][c]);
+        store_once<T, C>(y.at(ts + s), hs);
+      }
+    } else if (in) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
         if (s < n) {
           const bool r = (mask >> s) & 1u;
 #pragma unroll
           for (int c = 0; c < C; ++c)
             hs[c] = r ? ix[s][c] : __builtin_fmaf(f[s][c], hs[c], ix[s][c]);
-          ST<T, C>(y + (ts + s) * a.y_st, hs);
+          store_once<T, C>(y.at(ts + s), hs);
         } else if (ts + s < p.t_end) {
           const float zero[C] = {};
-          ST<T, C>(y + (ts + s) * a.y_st, zero);
+          store_once<T, C>(y.at(ts + s), zero);
         }
       }
     }
@@ -220,40 +255,44 @@ __global__ __launch_bounds__(kWaves * 64) void scan_forward_kernel(ScanArgs a) {
 // flows back through it, E -> A E + B.  Waves take runs of whole tiles.
 template <typename T, int C, bool REV>
 __global__ __launch_bounds__(kWaves * 64) void scan_segment_kernel(ScanArgs a) {
+  constexpr int S = kForward;
   __shared__ float sA[kWaves][C][64], sB[kWaves][C][64];
   __shared__ uint32_t sF[kWaves];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Place p = place<C>(a);
   const bool in = p.d < a.D;
-  const T* v = REV ? static_cast<const T*>(a.dy) + p.b * a.dy_sb + p.d
-                   : static_cast<const T*>(a.x) + p.b * a.x_sb + p.d;
-  const int64_t v_st = REV ? a.dy_st : a.x_st;
-  const T* g = static_cast<const T*>(a.g) + p.b * a.g_sb + p.d;
+  const uint32_t d32 = (uint32_t)p.d;
+  const Rows<const T> v =
+      REV ? Rows<const T>{static_cast<const T*>(a.dy) + p.b * a.dy_sb, a.dy_st, d32}
+          : Rows<const T>{static_cast<const T*>(a.x) + p.b * a.x_sb, a.x_st, d32};
+  const Rows<const T> g = {static_cast<const T*>(a.g) + p.b * a.g_sb, a.g_st, d32};
   const uint8_t* reset = a.reset ? a.reset + p.b * a.T : nullptr;
-  const int64_t run = a.seg_steps / kWaves;  // a multiple of kSteps
+  const int64_t run = a.seg_steps / kWaves;  // a multiple of S
   float A[C], B[C];
   uint32_t flag = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
-  for (int64_t k = 0; k < run; k += kSteps) {
-    const int64_t ts = p.t_begin + wv * run + (REV ? run - kSteps - k : k);
-    const int n = steps_at(ts, p.live);
+  for (int64_t k = 0; k < run; k += S) {
+    const int64_t ts = p.t_begin + wv * run + (REV ? run - S - k : k);
+    const int n = steps_at<S>(ts, p.live);
     if (n == 0) continue;
     const uint32_t mask = reset_mask(reset, ts, n);
     flag |= mask;
     if (!in) continue;
-    Pack<T, C> gv[kSteps], gg[kSteps];
-    load_steps<T, C>(v, v_st, ts, n, gv);
-    load_steps<T, C>(g, a.g_st, ts, n, gg);
+    auto reduce = [&](auto is_full) {
+      constexpr bool FULL = decltype(is_full)::value;
+      Pack<T, C> pv[S], pg[S];
+      load_steps<T, C, FULL, S>(v, ts, n, pv);
+      load_steps<T, C, FULL, S>(g, ts, n, pg);
 #pragma unroll
-    for (int q = 0; q < kSteps; ++q) {
-      const int s = REV ? kSteps - 1 - q : q;
-      if (s < n) {
-        const bool r = (mask >> s) & 1u;
+      for (int q = 0; q < S; ++q) {
+        const int s = REV ? S - 1 - q : q;
+        if (!FULL && s >= n) continue;
+        const bool r = !FULL && ((mask >> s) & 1u);
         float vv[C], gf[C];
-        unpack(gv[s], vv);
-        unpack(gg[s], gf);
+        unpack(pv[s], vv);
+        unpack(pg[s], gf);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           float f, i;
@@ -267,7 +306,9 @@ __global__ __launch_bounds__(kWaves * 64) void scan_segment_kernel(ScanArgs a) {
           A[c] = r ? 0.0f : A[c] * f;
         }
       }
-    }
+    };
+    if (n == S && mask == 0) reduce(std::true_type{});
+    else reduce(std::false_type{});
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) sA[wv][c][lane] = A[c], sB[wv][c][lane] = B[c];
@@ -306,7 +347,8 @@ __global__ __launch_bounds__(kWaves * 64) void scan_segment_kernel(ScanArgs a) {
 //   dx = full (1 - f),  dg = full (h' - x) f (1 - f).
 // The states of a chunk are computed again from its carry.
 template <typename T, int C>
-__global__ __launch_bounds__(kWaves * 64, LB) void scan_backward_kernel(ScanArgs a) {
+__global__ __launch_bounds__(kWaves * 64, LBB) void scan_backward_kernel(ScanArgs a) {
+  constexpr int S = kBackward;
   __shared__ float sA[2][kWaves][C][64], sB[2][kWaves][C][64], sQ[2][kWaves][C][64];
   __shared__ uint32_t sF[2][kWaves];
   const int lane = threadIdx.x & 63;
@@ -314,11 +356,12 @@ __global__ __launch_bounds__(kWaves * 64, LB) void scan_backward_kernel(ScanArgs
   const int nw = blockDim.x >> 6;
   const Place p = place<C>(a);
   const bool in = p.d < a.D;
-  const T* x = static_cast<const T*>(a.x) + p.b * a.x_sb + p.d;
-  const T* g = static_cast<const T*>(a.g) + p.b * a.g_sb + p.d;
-  const T* dy = static_cast<const T*>(a.dy) + p.b * a.dy_sb + p.d;
-  T* dx = static_cast<T*>(a.dx) + p.b * a.dx_sb + p.d;
-  T* dg = static_cast<T*>(a.dg) + p.b * a.dg_sb + p.d;
+  const uint32_t d32 = (uint32_t)p.d;
+  const Rows<const T> x = {static_cast<const T*>(a.x) + p.b * a.x_sb, a.x_st, d32};
+  const Rows<const T> g = {static_cast<const T*>(a.g) + p.b * a.g_sb, a.g_st, d32};
+  const Rows<const T> dy = {static_cast<const T*>(a.dy) + p.b * a.dy_sb, a.dy_st, d32};
+  const Rows<T> dx = {static_cast<T*>(a.dx) + p.b * a.dx_sb, a.dx_st, d32};
+  const Rows<T> dg = {static_cast<T*>(a.dg) + p.b * a.dg_sb, a.dg_st, d32};
   const uint8_t* reset = a.reset ? a.reset + p.b * a.T : nullptr;
   float E[C];
 #pragma unroll
@@ -358,7 +401,7 @@ __global__ __launch_bounds__(kWaves * 64, LB) void scan_backward_kernel(ScanArgs
     }
   }
 
-  const int64_t tile = nw * kSteps;
+  const int64_t tile = nw * S;
   const int64_t tiles = p.t_end > p.t_begin ? (p.t_end - p.t_begin + tile - 1) / tile : 0;
   float Eo[C];  // what flows out of the wave's own steps, run one by one
 #pragma unroll
@@ -366,11 +409,11 @@ __global__ __launch_bounds__(kWaves * 64, LB) void scan_backward_kernel(ScanArgs
   int buf = 0;
   for (int64_t k = tiles - 1; k >= 0; --k, buf ^= 1) {
     const int64_t t0 = p.t_begin + k * tile;
-    const int64_t ts = t0 + wv * kSteps;
-    const int n = steps_at(ts, p.live);
+    const int64_t ts = t0 + wv * S;
+    const int n = steps_at<S>(ts, p.live);
     const uint32_t mask = reset_mask(reset, ts, n);
-    float f[kSteps][C], i[kSteps][C], xv[kSteps][C];
-    Pack<T, C> pd[kSteps];
+    float f[S][C], i[S][C];
+    Pack<T, C> px[S], pd[S];
     float h[C], A[C], B[C], Q[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -379,38 +422,41 @@ __global__ __launch_bounds__(kWaves * 64, LB) void scan_backward_kernel(ScanArgs
       h[c] = in ? a.carries[(p.b * ((a.T + kChunk - 1) / kChunk) + t0 / kChunk) * a.D + p.d + c]
                 : 0.0f;
     }
-    if (n > 0 && in) {
-      Pack<T, C> px[kSteps], pg[kSteps];
-      load_steps<T, C>(x, a.x_st, ts, n, px);
-      load_steps<T, C>(g, a.g_st, ts, n, pg);
-      load_steps<T, C>(dy, a.dy_st, ts, n, pd);
+    const bool full = n == S && mask == 0;
+    auto reduce = [&](auto is_full) {
+      constexpr bool FULL = decltype(is_full)::value;
+      Pack<T, C> pg[S];
+      load_steps<T, C, FULL, S>(g, ts, n, pg);
+      load_steps<T, C, FULL, S>(x, ts, n, px);
+      load_steps<T, C, FULL, S>(dy, ts, n, pd);
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        float gv[C];
-        unpack(px[s], xv[s]);
+      for (int s = 0; s < S; ++s) {
+        float gv[C], xv[C];
+        unpack(px[s], xv);
         unpack(pg[s], gv);
+        const bool r = !FULL && ((mask >> s) & 1u);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           gate(gv[c], f[s][c], i[s][c]);
-          if (s < n) {
-            const bool r = (mask >> s) & 1u;
-            const float b = i[s][c] * xv[s][c];
+          if (FULL || s < n) {
+            const float b = i[s][c] * xv[c];
             B[c] = r ? b : __builtin_fmaf(f[s][c], B[c], b);
             A[c] = r ? 0.0f : A[c] * f[s][c];
           }
         }
       }
 #pragma unroll
-      for (int s = kSteps - 1; s >= 0; --s) {
-        if (s < n) {
-          const bool r = (mask >> s) & 1u;
-          float dv[C];
-          unpack(pd[s], dv);
+      for (int s = S - 1; s >= 0; --s) {
+        if (!FULL && s >= n) continue;
+        const bool r = !FULL && ((mask >> s) & 1u);
+        float dv[C];
+        unpack(pd[s], dv);
 #pragma unroll
-          for (int c = 0; c < C; ++c) Q[c] = r ? 0.0f : f[s][c] * (Q[c] + dv[c]);
-        }
+        for (int c = 0; c < C; ++c) Q[c] = r ? 0.0f : f[s][c] * (Q[c] + dv[c]);
       }
-    }
+    };
+    if (in && full) reduce(std::true_type{});
+    else if (in && n > 0) reduce(std::false_type{});
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       sA[buf][wv][c][lane] = A[c];
@@ -438,44 +484,47 @@ __global__ __launch_bounds__(kWaves * 64, LB) void scan_backward_kernel(ScanArgs
         E[c] = fl ? q : __builtin_fmaf(sA[buf][w][c][lane], E[c], q);
       }
     }
-    if (in) {
-      if (n > 0) {
+    auto finish = [&](auto is_full) {
+      constexpr bool FULL = decltype(is_full)::value;
+      float w[S][C];  // (h' - x) f (1 - f)
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          if (s < n) {
-            const bool r = (mask >> s) & 1u;
+      for (int s = 0; s < S; ++s) {
+        if (!FULL && s >= n) continue;
+        const bool r = !FULL && ((mask >> s) & 1u);
+        float xv[C];
+        unpack(px[s], xv);
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-              const float hp = r ? 0.0f : h[c];
-              const float b = i[s][c] * xv[s][c];
-              h[c] = r ? b : __builtin_fmaf(f[s][c], h[c], b);
-              xv[s][c] = (hp - xv[s][c]) * f[s][c] * i[s][c];
-            }
-          }
+        for (int c = 0; c < C; ++c) {
+          const float hp = r ? 0.0f : h[c];
+          const float b = i[s][c] * xv[c];
+          h[c] = r ? b : __builtin_fmaf(f[s][c], h[c], b);
+          w[s][c] = (hp - xv[c]) * (f[s][c] * i[s][c]);
         }
       }
 #pragma unroll
-      for (int s = kSteps - 1; s >= 0; --s) {
-        if (s < n) {
-          const bool r = (mask >> s) & 1u;
+      for (int s = S - 1; s >= 0; --s) {
+        if (FULL || s < n) {
+          const bool r = !FULL && ((mask >> s) & 1u);
           float dv[C], ox[C], og[C];
           unpack(pd[s], dv);
 #pragma unroll
           for (int c = 0; c < C; ++c) {
-            const float full = Es[c] + dv[c];
-            ox[c] = full * i[s][c];
-            og[c] = full * xv[s][c];
-            Es[c] = r ? 0.0f : full * f[s][c];
+            const float full_t = Es[c] + dv[c];
+            ox[c] = full_t * i[s][c];
+            og[c] = full_t * w[s][c];
+            Es[c] = r ? 0.0f : full_t * f[s][c];
           }
-          ST<T, C>(dx + (ts + s) * a.dx_st, ox);
-          ST<T, C>(dg + (ts + s) * a.dg_st, og);
+          store_once<T, C>(dx.at(ts + s), ox);
+          store_once<T, C>(dg.at(ts + s), og);
         } else if (ts + s < p.t_end) {
           const float zero[C] = {};
-          ST<T, C>(dx + (ts + s) * a.dx_st, zero);
-          ST<T, C>(dg + (ts + s) * a.dg_st, zero);
+          store_once<T, C>(dx.at(ts + s), zero);
+          store_once<T, C>(dg.at(ts + s), zero);
         }
       }
-    }
+    };
+    if (in && full) finish(std::true_type{});
+    else if (in) finish(std::false_type{});
 #pragma unroll
     for (int c = 0; c < C; ++c) Eo[c] = Es[c];
   }
@@ -541,25 +590,25 @@ hipError_t backward_typed(const ScanArgs& a, uint32_t blocks, int waves, hipStre
   return launch_kernel(scan_backward_kernel<T, C>, dim3(blocks), dim3(64 * waves), 0, s, a);
 }
 
-int waves_for(int64_t T) {
-  const int64_t w = (T + kSteps - 1) / kSteps;
+int waves_for(int64_t T, int steps) {
+  const int64_t w = (T + steps - 1) / steps;
   return w < 1 ? 1 : w > kWaves ? kWaves : (int)w;
 }
 
-// Segments and their steps (whole chunks).
+// Segments and their steps (multiples of kSegment).
 struct Split {
   int n;
   int64_t steps;
 };
 Split split_time(int64_t B, int64_t T, int64_t D) {
   const int64_t blocks = B * channel_tiles(D);
-  const int64_t chunks = (T + kChunk - 1) / kChunk;
+  const int64_t chunks = (T + kSegment - 1) / kSegment;
   Split s = {1, T};
   if (blocks >= 256 || chunks < 2) return s;
   int64_t n = (512 + blocks - 1) / blocks;
   if (n > kMaxSeg) n = kMaxSeg;
   if (n > chunks) n = chunks;
-  s.steps = (chunks + n - 1) / n * kChunk;
+  s.steps = (chunks + n - 1) / n * kSegment;
   s.n = (int)((T + s.steps - 1) / s.steps);
   return s;
 }
@@ -588,7 +637,7 @@ size_t scan_workspace(int64_t B, int64_t T, int64_t D) {
 hipError_t launch_scan_forward(ScanArgs a, int type, hipStream_t s) {
   set_split(a);
   const uint32_t blocks = (uint32_t)(a.B * a.nseg * channel_tiles(a.D));
-  const int waves = waves_for(a.T);
+  const int waves = waves_for(a.T, kForward);
   const bool two = two_channels(a.D);
   if (type == 0)
     return two ? forward_typed<float, 2>(a, blocks, waves, s)
@@ -603,7 +652,7 @@ hipError_t launch_scan_forward(ScanArgs a, int type, hipStream_t s) {
 hipError_t launch_scan_backward(ScanArgs a, int type, hipStream_t s) {
   set_split(a);
   const uint32_t blocks = (uint32_t)(a.B * a.nseg * channel_tiles(a.D));
-  const int waves = waves_for(a.T);
+  const int waves = waves_for(a.T, kBackward);
   const bool two = two_channels(a.D);
   if (type == 0)
     return two ? backward_typed<float, 2>(a, blocks, waves, s)

@@ -21,7 +21,7 @@ from .per import PerError, load
 
 PER_F32, PER_BF16, PER_F16 = 0, 1, 2
 PER_E4M3, PER_I8 = 0, 1
-PER_SCAN_CHUNK = 128
+PER_SCAN_CHUNK = 64
 
 _TYPE = {torch.float32: PER_F32, torch.bfloat16: PER_BF16, torch.float16: PER_F16}
 _FORMAT = {torch.float8_e4m3fn: PER_E4M3, torch.int8: PER_I8}

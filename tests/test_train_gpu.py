@@ -571,7 +571,7 @@ def state(p):
         s[k] = torch.empty(4, 200, 96, device=DEV)
     for k in ("h0", "h", "h2", "y2", "dh0"):
         s[k] = torch.zeros(4, 96, device=DEV)
-    s["c"] = torch.empty(4, 2, 96, device=DEV)
+    s["c"] = torch.empty(4, -(-200 // p.train.PER_SCAN_CHUNK), 96, device=DEV)
     s["dz"] = torch.empty(800, 96, device=DEV)
     s["tidx"] = torch.stack([torch.randperm(96, generator=gen(k))[:7] for k in range(800)]).to(torch.int32).cuda()
     t = torch.randn(800, 7, generator=gen(3))
