@@ -1,12 +1,14 @@
 """Compile the HIP library (libper.so), the latency probe (libper_probe.so)
 and the library's phase-stamped measurement build (libper_stamps.so) for
-gfx950, in-tree, with hipcc."""
+gfx950, in-tree, with hipcc, and the Python binding of include/per_train.h
+(_marshal.so) with the host compiler."""
 from __future__ import annotations
 
 import os
 import re
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,8 @@ SOURCES = ["per_api.hip", "tree_kernels.hip", "sample_kernels.hip", "rank_kernel
 PROBE_SRC = os.path.join(HERE, "probe", "latency_probe.hip")
 PROBE_LIB = os.path.join(HERE, "libper_probe.so")
 STAMPS_LIB = os.path.join(HERE, "libper_stamps.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL_LIB = os.path.join(HERE, "_marshal.so")
 STAMPED = ("tree_kernels.hip", "sample_kernels.hip")  # sources whose kernels carry stamps
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -71,10 +75,26 @@ def _compile(src: str, obj: str, defines: tuple = ()) -> None:
         sys.stderr.write("\n".join(noise) + "\n")
 
 
+def _build_marshal() -> None:
+    """_marshal.so: host code against torch's headers."""
+    import torch
+    t = os.path.dirname(torch.__file__)
+    tmp = MARSHAL_LIB + ".tmp"
+    subprocess.check_call([
+        os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+        "-Wall", "-Wno-unknown-pragmas", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+        "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+        "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(t, "include"), "-isystem",
+        os.path.join(t, "include", "torch", "csrc", "api", "include"), "-isystem",
+        "/opt/rocm/include", MARSHAL_SRC, "-o", tmp, "-L" + os.path.join(t, "lib"), "-lc10",
+        "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python"])
+    os.replace(tmp, MARSHAL_LIB)
+
+
 def build() -> str:
-    """Compile every source and link libper.so, libper_probe.so and
+    """Compile every source and link libper.so, libper_probe.so,
     libper_stamps.so (libper.so with PER_PHASE_STAMPS in the STAMPED sources)
-    next to this file."""
+    and _marshal.so next to this file."""
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     srcs = [os.path.join(CSRC, s) for s in SOURCES] + [PROBE_SRC]
@@ -84,8 +104,10 @@ def build() -> str:
     jobs = [(s, o, ()) for s, o in zip(srcs, objs)]
     jobs += [(os.path.join(CSRC, f), stamped[f.replace(".hip", ".o")], ("PER_PHASE_STAMPS",))
              for f in STAMPED]
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        binding = ex.submit(_build_marshal)
         list(ex.map(lambda job: _compile(*job), jobs))
+        binding.result()
     lib_objs = objs[:-1]
     stamps_objs = [stamped.get(os.path.basename(o), o) for o in lib_objs]
     for lib, lib_objs in ((LIB, lib_objs), (PROBE_LIB, objs[-1:]), (STAMPS_LIB, stamps_objs)):

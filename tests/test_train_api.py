@@ -14,16 +14,40 @@ HEADER = os.path.join(ROOT, "include", "per_train.h")
 P = 0x100000  # an aligned address
 EINVAL, ENOSPC = -1, -2
 
+_i64, _i32, _f64, _vp, _sz = (ctypes.c_int64, ctypes.c_int32, ctypes.c_double, ctypes.c_void_p,
+                              ctypes.c_size_t)
+_VIEW = [_vp, _i64, _i64]
+_ROWS = [_i64, _i64, _i32, _i32, _vp, _i64, _vp, _i64]
+_TOPK = [_i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _f64]
+SIG = {
+    "per_rows_write": _ROWS + [_i64, _i64, _vp, _i32, _i64, _vp],
+    "per_rows_write_at": _ROWS + [_i64, _vp, _vp, _vp, _i32, _i64, _vp],
+    "per_rows_read": _ROWS + [_i64, _vp, _i64, _vp, _i32, _i64, _vp],
+    "per_scan_workspace_bytes": [_i64, _i64, _i64, ctypes.POINTER(_sz)],
+    "per_scan_forward": [_i64, _i64, _i64, _i32] + 2 * _VIEW + [_vp, _vp, _vp] + _VIEW
+    + [_vp, _vp, _vp, _sz, _vp],
+    "per_scan_backward": [_i64, _i64, _i64, _i32] + 2 * _VIEW + [_vp, _vp, _vp] + _VIEW + [_vp]
+    + 2 * _VIEW + [_vp, _vp, _sz, _vp],
+    "per_scan_step": [_i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp],
+    "per_distill_workspace_bytes": [_i64, _i64, _i32, ctypes.POINTER(_sz)],
+    "per_distill": _TOPK + [_vp, _vp, _vp, _i64, _vp, _sz, _vp],
+    "per_distill_forward": _TOPK + [_vp, _vp, _vp, _sz, _vp],
+    "per_distill_backward": _TOPK + [_vp, _vp, _vp, _i64, _vp],
+}
+
 
 @pytest.fixture(scope="module")
 def call():
-    from sum_tree_sampling_amd import build, per, train
-    if not os.path.exists(per.LIB_PATH):
+    from sum_tree_sampling_amd import build, per
+    if not os.path.exists(per.LIB_PATH) or not os.path.exists(build.MARSHAL_LIB):
         build.build()
+    lib = ctypes.CDLL(per.LIB_PATH)
     per.load()
+    for name, args in SIG.items():
+        getattr(lib, name).argtypes = args
 
     def f(name, *args):
-        rc = train._get(name)(*args)
+        rc = getattr(lib, name)(*args)
         if rc:
             assert per.per_last_error()
         return rc
@@ -44,10 +68,10 @@ def test_declared_exported_bound(call):
     names = declared()
     assert len(names) == 11
     for n in names:
-        assert n in exported and hasattr(pkg, n) and n in train._SIG, n
+        assert n in exported and callable(getattr(pkg, n)) and n in train.NAMES, n
         args = re.search(r"\b%s\s*\((.*?)\)" % n, re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S),
                          flags=re.S).group(1)
-        assert len(args.split(",")) == len(train._SIG[n]), n
+        assert len(args.split(",")) == len(SIG[n]), n
 
 
 ROWS = dict(capacity=64, dim=100, format=0, group=32, codes=P, cs=128, scales=P, ss=4)
@@ -190,19 +214,36 @@ def test_distill_workspace(call):
             need(*bad)
 
 
-def test_binding_refuses_host_tensors():
-    from sum_tree_sampling_amd import per_distill, per_rows_write, per_scan_forward, per_scan_step, rows_alloc
+def test_binding_refuses(call):
+    """The binding's own checks, on host tensors and wrong arguments."""
+    from sum_tree_sampling_amd import (per_distill, per_distill_workspace_bytes, per_rows_read, per_rows_write,
+                                       per_scan_forward, per_scan_step, rows_alloc)
     codes, scales = rows_alloc(16, 40, device="cpu")
     assert codes.shape == (16, 40) and scales.shape == (16, 1) and codes.dtype == torch.float8_e4m3fn
-    with pytest.raises(ValueError):
-        per_rows_write(codes, scales, torch.zeros(4, 40))
-    with pytest.raises(ValueError):
-        per_scan_forward(torch.zeros(1, 2, 3), torch.zeros(1, 2, 3))
-    with pytest.raises(ValueError):
-        per_scan_step(torch.zeros(2, 3), torch.zeros(2, 3), torch.zeros(2, 3))
-    with pytest.raises(ValueError):
-        per_distill(torch.zeros(2, 30), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3))
+    x, z = torch.zeros(1, 2, 3), torch.zeros(2, 30)
+    ti, t = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3)
+    for f, args, kw in [
+            (per_rows_write, (codes, scales, torch.zeros(4, 40)), {}),
+            (per_rows_read, (codes, scales, torch.zeros(4, dtype=torch.int64)), {}),
+            (per_scan_forward, (x, x), {}), (per_scan_step, (z, z, z), {}), (per_distill, (z, ti, t), {}),
+            (per_rows_write, (codes, scales), {}), (per_rows_write, (codes, scales, None), {}),
+            (per_rows_write, (codes, scales, 3), {}), (per_scan_forward, (3, x), {}),
+            (per_distill, (z, ti, t), {"nothing": 1}), (per_distill, (z, ti, t), {"logits": z}),
+            (per_distill, (z,) * 12, {}), (per_distill_workspace_bytes, (2.5, 10, 0), {}),
+            (per_distill_workspace_bytes, (1 << 70, 10, 0), {})]:
+        with pytest.raises(ValueError):
+            f(*args, **kw)
     with pytest.raises(ValueError):
         rows_alloc(16, 40, dtype=torch.float16, device="cpu")
     with pytest.raises(ValueError):
         rows_alloc(16, 40, group=48, device="cpu")
+
+
+def test_build_before_binding():
+    """A tree without the binding still imports, builds, and says what is missing."""
+    code = ("import sys; sys.modules['sum_tree_sampling_amd._marshal'] = None\n"
+            "import sum_tree_sampling_amd as p\n"
+            "from sum_tree_sampling_amd import build\n"
+            "try:\n    p.per_distill()\nexcept ImportError as e:\n    print('said', e)\n")
+    out = subprocess.run(["python3", "-c", code], cwd=ROOT, capture_output=True, text=True, check=True).stdout
+    assert "said _marshal.so is not built" in out
