@@ -158,14 +158,16 @@ int per_scan_step(int64_t B, int64_t D, int32_t type, const void* d_x, int64_t x
  *   the losses are not weighted, the gradient is; a row of weight 0 is not
  *   read and gets loss 0 and gradient 0.  d_grad may be d_logits (with the
  *   same stride).
- * per_distill_forward: the losses, and d_saved [N x 4] f32 (or NULL): largest
- *   logit m, sum of exp((z - m) / tau), the same over the rest, and 0.
+ * per_distill_forward: the losses, and d_saved [N x (4 + K)] f32 (or NULL):
+ *   largest logit m, S = sum of exp((z - m) / tau) (0 for a row without loss),
+ *   the same over the rest, p_r, and the K probabilities p_k.
  * per_distill_backward: the gradient from d_saved, weighted by d_gloss [N]
  *   f32, the gradient by each row's loss; d_grad may be d_logits.
  * per_distill_workspace_bytes: device workspace of per_distill and
- *   per_distill_forward (may be 0), 16-byte aligned, scratch of one call.
+ *   per_distill_forward, 16-byte aligned, scratch of one call.  per_distill
+ *   needs none where a workgroup holds a whole row, and does not look at it.
  */
-int per_distill_workspace_bytes(int64_t N, int64_t V, int32_t type, size_t* out);
+int per_distill_workspace_bytes(int64_t N, int64_t V, int64_t K, int32_t type, size_t* out);
 int per_distill(int64_t N, int64_t V, int64_t K, int32_t type, const void* d_logits,
                 int64_t stride, const int32_t* d_tidx, const void* d_tlogit, int32_t tlogit_type,
                 const float* d_tlse, double temperature, const float* d_weight, float* d_loss,

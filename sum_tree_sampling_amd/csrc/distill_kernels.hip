@@ -146,15 +146,8 @@ __device__ __forceinline__ float teacher_logit(const DistillArgs& a, int64_t at)
   return (float)static_cast<const f16_t*>(a.t)[at];
 }
 
-struct Teacher {
-  double h;     // sum p log p
-  double ps;    // sum p
-  double rest;  // p_r
-  bool any;     // an entry is present
-  bool dup;     // two entries may name one token of [c0, c1)
-};
-
-// The lane's first entry, loaded ahead of the row.
+// An entry of the lane: token and teacher's logit (or probability).  The first
+// one is loaded ahead of the row.
 struct Entry {
   int i;
   float t;
@@ -169,6 +162,20 @@ __device__ __forceinline__ Entry first_entry(const DistillArgs& a, int64_t n) {
   return e;
 }
 
+// Clears the bitmap, by one whole wave.
+__device__ __forceinline__ void clear_marks(uint32_t* bits, uint32_t words) {
+  for (uint32_t w = 4 * (threadIdx.x & 63); w < words; w += 256)
+    *reinterpret_cast<uint4*>(bits + w) = make_uint4(0, 0, 0, 0);
+}
+// Marks token i if it lies in [lo, hi); whether it was marked before.
+template <bool TAIL>
+__device__ __forceinline__ bool mark(uint32_t* bits, int i, int64_t lo, int64_t hi) {
+  if (i < lo || i >= hi) return false;
+  uint32_t bit = (uint32_t)(i - lo);
+  if (!TAIL) bit &= 32 * kHashWords - 1;
+  return (atomicOr(&bits[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u;
+}
+
 // One whole wave: entries to LDS, the bitmap of chunks [c0, c1), and the sums.
 // The K exponentials are taken in f64: the rest 1 - sum p would lose its digits
 // in f32 where the top holds nearly everything.
@@ -177,11 +184,10 @@ __device__ __forceinline__ Teacher teacher(const DistillArgs& a, const Row<T>& r
                                            const Lds& l, uint32_t words, uint32_t c0, uint32_t c1,
                                            Entry e) {
   const int lane = threadIdx.x & 63;
-  for (uint32_t w = 4 * lane; w < words; w += 256)
-    *reinterpret_cast<uint4*>(l.bits + w) = make_uint4(0, 0, 0, 0);
+  clear_marks(l.bits, words);
   const int64_t lo = (int64_t)c0 * kVec<T> - r.mis;
   const int64_t hi = (int64_t)c1 * kVec<T> - r.mis;
-  float tm = kNegInf;
+  float tm = kNegInf, z0 = kNegInf;
   bool dup = false, any = false;
   for (int k = lane; k < a.K; k += 64) {
     if (k != lane) {
@@ -189,24 +195,24 @@ __device__ __forceinline__ Teacher teacher(const DistillArgs& a, const Row<T>& r
       e.t = teacher_logit(a, n * a.K + k);
     }
     const int i = e.i < 0 || e.i >= (int64_t)r.V ? -1 : e.i;
+    const float z = i >= 0 ? (float)r.z[i] : kNegInf;
     l.idx[k] = i;
     l.p[k] = e.t;
-    l.z[k] = i >= 0 ? (float)r.z[i] : 0.0f;
+    l.z[k] = z;
     if (i >= 0) {
       any = true;
       tm = fmaxf(tm, e.t);
-      if (i >= lo && i < hi) {
-        uint32_t bit = (uint32_t)(i - lo);
-        if (!TAIL) bit &= 32 * kHashWords - 1;
-        dup |= (atomicOr(&l.bits[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u;
-      }
+      z0 = fmaxf(z0, z);
+      if (words) dup |= mark<TAIL>(l.bits, i, lo, hi);
     }
   }
   tm = wave_max(tm);
+  z0 = wave_max(z0);
+  if (z0 == kNegInf) z0 = 0.0f;
   // Without a rest: e = exp((t - largest) / tau), p = e / sum e.
   const double ref = TAIL || tm == kNegInf ? 0.0 : (double)tm;
   const double norm = TAIL ? (double)a.tlse[n] : 0.0;
-  Teacher o = {0.0, 0.0, 0.0, false, false};
+  Teacher o = {0.0, 0.0, 0.0, 0.0, z0, false, false};
   for (int k = lane; k < a.K; k += 64) {
     double p = 0.0;
     if (l.idx[k] >= 0) {
@@ -215,12 +221,15 @@ __device__ __forceinline__ Teacher teacher(const DistillArgs& a, const Row<T>& r
       if (!(p == 0.0)) {
         o.h += p * lp;
         o.ps += p;
+        // the difference first: logits at the type's lowest value cancel
+        o.pz += p * ((double)l.z[k] - (double)z0);
       }
     }
     l.p[k] = (float)p;
   }
   o.h = wave_sum(o.h);
   o.ps = wave_sum(o.ps);
+  o.pz = wave_sum(o.pz);
   o.any = __any(any) && o.ps != 0.0;  // entries at -Inf are none
   o.dup = __any(dup);
   if (TAIL) {
@@ -231,21 +240,18 @@ __device__ __forceinline__ Teacher teacher(const DistillArgs& a, const Row<T>& r
     const float scale = (float)inv;
     for (int k = lane; k < a.K; k += 64) l.p[k] *= scale;
     o.h = o.h * inv - log(o.ps);
+    o.pz *= inv;
     o.ps = 1.0;
   }
   return o;
 }
 
-// The row's loss from the teacher's sums and the student's statistics, by one
-// whole wave.  The differences z - m are taken before they are summed, so that
-// logits at the type's lowest value cancel.
-__device__ __forceinline__ float row_loss(const DistillArgs& a, const Lds& l, const Teacher& t,
-                                          float m, float S, float Sr, bool tail) {
-  double d = 0.0;
-  for (int k = threadIdx.x & 63; k < a.K; k += 64)
-    if (l.idx[k] >= 0 && !(l.p[k] == 0.0f)) d += (double)l.p[k] * ((double)l.z[k] - (double)m);
+// The row's loss from the teacher's sums and the student's statistics.
+__device__ __forceinline__ float row_loss(const DistillArgs& a, const Teacher& t, float m, float S,
+                                          float Sr, bool tail) {
   const double logS = log((double)S);
-  double v = t.h + t.ps * logS - wave_sum(d) * a.inv_tau;
+  double v = t.h + t.ps * logS;
+  if (t.ps != 0.0) v -= (t.pz + t.ps * ((double)t.z0 - (double)m)) * a.inv_tau;
   if (tail && t.rest > 0.0 && Sr != 0.0f) v += t.rest * (log(t.rest) - log((double)Sr) + logS);
   return (float)(v * (double)a.tau * (double)a.tau);
 }
@@ -294,75 +300,95 @@ __device__ __forceinline__ void add_chunk(const Chunk<T>& v, float m, float c, u
 }
 
 // ------------------------------------------------- one workgroup holds the row
+//
+// NT threads hold the row, R chunks each.  In the small workgroups one more
+// wave reads the teacher beside them (its chain of loads and f64 exponentials
+// is as long as the row's own); in the large ones, whose registers are full,
+// the first wave does.
+template <int NT>
+constexpr bool kSideWave = NT <= 256;
+template <int NT>
+constexpr int kRowThreads = kSideWave<NT> ? NT + 64 : NT;
+
 template <typename T, int NT, int R, bool TAIL, bool ONCE>
-__global__ __launch_bounds__(NT, NT >= 512 ? 4 : 1) void distill_row_kernel(DistillArgs a) {
+__global__ __launch_bounds__(kRowThreads<NT>, NT >= 512 ? 4 : 1) void distill_row_kernel(
+    DistillArgs a) {
   extern __shared__ char mem[];
   __shared__ float red[3][NT / 64];
   __shared__ Teacher t;  // kept here, not in registers across the passes
   const int64_t n = blockIdx.x;
   const int tid = threadIdx.x, wv = tid >> 6;
+  const bool row_wave = !kSideWave<NT> || wv < NT / 64;
+  const bool teacher_wave = wv == (kSideWave<NT> ? NT / 64 : 0);
   const Row<T> r = row_of<T>(a, n);
   T* grad = static_cast<T*>(a.grad) + n * a.grad_stride;
+  Entry first = {-1, 0.0f};
+  if (teacher_wave) first = first_entry(a, n);
   const float w = a.weight ? a.weight[n] : 1.0f;
   if (w == 0.0f) {
     const float zero[kVec<T>] = {};
-    for (uint32_t j = tid; j < r.chunks; j += NT) store_chunk(grad, r, j, zero);
+    for (uint32_t j = tid; j < r.chunks; j += kRowThreads<NT>) store_chunk(grad, r, j, zero);
     if (tid == 0) a.loss[n] = 0.0f;
     return;
   }
   const uint32_t words = mark_words(TAIL, (int64_t)r.chunks * kVec<T>);
   const Lds l = lds_of(mem, a.K, words);
-  Entry first = {-1, 0.0f};
-  if (wv == 0) first = first_entry(a, n);
   auto read_teacher = [&] {
-    if (wv != 0) return;
+    if (!teacher_wave) return;
     const Teacher o = teacher<T, TAIL>(a, r, n, l, words, 0, r.chunks, first);
-    if (tid == 0) t = o;
+    if ((tid & 63) == 0) t = o;
   };
   // The row's loads come first, so that they are in flight meanwhile, unless
   // they would take the registers the first wave needs for the teacher.
   if (R > 12) read_teacher();
   Chunk<T> v[R];
+  if (row_wave) {
 #pragma unroll
-  for (int q = 0; q < R; ++q) {
-    const uint32_t j = tid + q * NT;
-    if (j < r.chunks) {
-      v[q] = load_chunk<T, ONCE>(r, j);
-    } else {
+    for (int q = 0; q < R; ++q) {
+      const uint32_t j = tid + q * NT;
+      if (j < r.chunks) {
+        v[q] = load_chunk<T, ONCE>(r, j);
+      } else {
 #pragma unroll
-      for (int e = 0; e < kVec<T>; ++e) v[q].v[e] = (T)kNegInf;
+        for (int e = 0; e < kVec<T>; ++e) v[q].v[e] = (T)kNegInf;
+      }
     }
   }
   if (R <= 12) read_teacher();
   float m = kNegInf;
+  if (row_wave) {
 #pragma unroll
-  for (int q = 0; q < R; ++q) {
-    float z[kVec<T>];
-    unpack(v[q], z);
+    for (int q = 0; q < R; ++q) {
+      float z[kVec<T>];
+      unpack(v[q], z);
 #pragma unroll
-    for (int e = 0; e < kVec<T>; ++e) m = fmaxf(m, z[e]);
-    keep_packed<T>(v[q]);
+      for (int e = 0; e < kVec<T>; ++e) m = fmaxf(m, z[e]);
+      keep_packed<T>(v[q]);
+    }
+    m = wave_max(m);
+    if ((tid & 63) == 0) red[0][wv] = m;
   }
-  m = wave_max(m);
-  if ((tid & 63) == 0) red[0][wv] = m;
+  // The side wave's marks are needed only by the sums over the rest.
   __syncthreads();
   m = red[0][0];
 #pragma unroll
   for (int q = 1; q < NT / 64; ++q) m = fmaxf(m, red[0][q]);
   if (m == kNegInf) m = 0.0f;
   float rest = 0.0f, top = 0.0f;
+  if (row_wave) {
 #pragma unroll
-  for (int q = 0; q < R; ++q) {
-    const uint32_t j = tid + q * NT;
-    if (j < r.chunks)
-      add_chunk<T, TAIL>(v[q], m, a.c, TAIL ? chunk_bits<T>(l.bits, j) : 0u, rest, top);
-    keep_packed<T>(v[q]);
-  }
-  rest = wave_sum(rest);
-  if (TAIL) top = wave_sum(top);
-  if ((tid & 63) == 0) {
-    red[1][wv] = rest;
-    red[2][wv] = top;
+    for (int q = 0; q < R; ++q) {
+      const uint32_t j = tid + q * NT;
+      if (j < r.chunks)
+        add_chunk<T, TAIL>(v[q], m, a.c, TAIL ? chunk_bits<T>(l.bits, j) : 0u, rest, top);
+      keep_packed<T>(v[q]);
+    }
+    rest = wave_sum(rest);
+    if (TAIL) top = wave_sum(top);
+    if ((tid & 63) == 0) {
+      red[1][wv] = rest;
+      red[2][wv] = top;
+    }
   }
   __syncthreads();
   rest = top = 0.0f;
@@ -377,125 +403,143 @@ __global__ __launch_bounds__(NT, NT >= 512 ? 4 : 1) void distill_row_kernel(Dist
   // 1 / S - p_r / S_r as one rounded difference over the product
   float coef = 0.0f;
   if (!dead)
-    coef = TAIL ? (rest == 0.0f ? 0.0f : scale * (__builtin_fmaf(-(float)t.rest, S, rest) / (S * rest)))
+    coef = TAIL ? (rest == 0.0f ? 0.0f
+                                : scale * (__builtin_fmaf(-(float)t.rest, S, rest) / (S * rest)))
                 : scale / S;
+  if (row_wave) {
 #pragma unroll
-  for (int q = 0; q < R; ++q) {
-    const uint32_t j = tid + q * NT;
-    if (j < r.chunks) {
-      float z[kVec<T>], g[kVec<T>];
-      unpack(v[q], z);
+    for (int q = 0; q < R; ++q) {
+      const uint32_t j = tid + q * NT;
+      if (j < r.chunks) {
+        float z[kVec<T>], g[kVec<T>];
+        unpack(v[q], z);
 #pragma unroll
-      for (int e = 0; e < kVec<T>; ++e) g[e] = dead ? 0.0f : coef * ex2((z[e] - m) * a.c);
-      store_chunk(grad, r, j, g);
+        for (int e = 0; e < kVec<T>; ++e) g[e] = dead ? 0.0f : coef * ex2((z[e] - m) * a.c);
+        store_chunk(grad, r, j, g);
+      }
     }
+  }
+  if (teacher_wave) {
+    const float loss = dead ? 0.0f : row_loss(a, t, m, S, rest, TAIL);
+    if ((tid & 63) == 0) a.loss[n] = loss;
   }
   __syncthreads();
   if (!dead) patch_top(a, l, grad, m, S, scale, t.dup, 0, (int64_t)r.V);
-  if (wv == 0) {
-    const float loss = dead ? 0.0f : row_loss(a, l, t, m, S, rest, TAIL);
-    if (tid == 0) a.loss[n] = loss;
-  }
 }
 
 // ------------------------------------------------------ rows taken in parts
+//
+// 256 threads go over a part's chunks, one more wave takes the entries.
 constexpr int kPartThreads = 256;
 constexpr int kBatch = 4;  // chunks a thread loads at once
 
 // Chunks [c0, c1) of the workgroup's part.
 struct Span {
-  int64_t n;
-  int split;
   uint32_t c0, c1;
 };
 template <typename T>
-__device__ __forceinline__ Span span_of(const DistillArgs& a, const Row<T>& r, int64_t n,
-                                        int split) {
+__device__ __forceinline__ Span span_of(const DistillArgs& a, const Row<T>& r, int split) {
   const uint32_t per = (r.chunks + a.splits - 1) / a.splits;
   Span s;
-  s.n = n;
-  s.split = split;
   s.c0 = (uint32_t)split * per < r.chunks ? (uint32_t)split * per : r.chunks;
   s.c1 = s.c0 + per < r.chunks ? s.c0 + per : r.chunks;
   return s;
 }
 
-// Largest logit and sums of one part of a row.
+template <typename T>
+__device__ __forceinline__ void load_batch(const Row<T>& r, uint32_t j0, uint32_t c1,
+                                           Chunk<T> (&v)[kBatch]) {
+#pragma unroll
+  for (int q = 0; q < kBatch; ++q) {
+    const uint32_t j = j0 + q * kPartThreads;
+    if (j < c1) {
+      v[q] = load_chunk(r, j);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kVec<T>; ++e) v[q].v[e] = (T)kNegInf;
+    }
+  }
+}
+
+// Largest logit and sums of one part of a row; the first part's extra wave
+// reads the teacher.
 template <typename T, bool TAIL>
-__global__ __launch_bounds__(kPartThreads) void distill_part_kernel(DistillArgs a) {
+__global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(DistillArgs a) {
   extern __shared__ char mem[];
   __shared__ float red[3][kPartThreads / 64];
   const int64_t n = blockIdx.x / (uint32_t)a.splits;
+  const int split = (int)(blockIdx.x % (uint32_t)a.splits);
   const int tid = threadIdx.x, wv = tid >> 6;
+  const bool row_wave = wv < kPartThreads / 64;
   float* part = a.part + (int64_t)blockIdx.x * 4;
   if (a.weight && a.weight[n] == 0.0f) {
     if (tid == 0) part[0] = kNegInf, part[1] = part[2] = 0.0f;
     return;
   }
   const Row<T> r = row_of<T>(a, n);
-  const Span s = span_of(a, r, n, (int)(blockIdx.x % (uint32_t)a.splits));
-  uint32_t* bits = reinterpret_cast<uint32_t*>(mem);
-  if (TAIL) {
-    const uint32_t words = mark_words(true, (int64_t)(s.c1 - s.c0) * kVec<T>);
-    for (uint32_t q = tid; q < words; q += kPartThreads) bits[q] = 0;
-    __syncthreads();
-    const int64_t lo = (int64_t)s.c0 * kVec<T> - r.mis, hi = (int64_t)s.c1 * kVec<T> - r.mis;
-    for (int k = tid; k < a.K; k += kPartThreads) {
-      const int i = a.tidx[n * a.K + k];
-      if (i >= 0 && i < (int64_t)r.V && i >= lo && i < hi) {
-        const uint32_t bit = (uint32_t)(i - lo);
-        atomicOr(&bits[bit >> 5], 1u << (bit & 31));
+  const Span s = span_of(a, r, split);
+  const uint32_t words = TAIL ? mark_words(true, (int64_t)(s.c1 - s.c0) * kVec<T>) : 0;
+  const Lds l = lds_of(mem, a.K, words);
+  Chunk<T> v[kBatch];
+  if (row_wave) {
+    load_batch(r, s.c0 + tid, s.c1, v);
+  } else {
+    if (split == 0) {
+      const Teacher t = teacher<T, TAIL>(a, r, n, l, words, s.c0, s.c1, first_entry(a, n));
+      if ((tid & 63) == 0) a.teacher[n] = t;
+      if (a.saved)
+        for (int k = tid & 63; k < a.K; k += 64) a.saved[n * (4 + a.K) + 4 + k] = l.p[k];
+    } else if (TAIL) {
+      clear_marks(l.bits, words);
+      for (int k = tid & 63; k < a.K; k += 64) {
+        const int i = a.tidx[n * a.K + k];
+        if (i >= 0 && i < (int64_t)r.V)
+          mark<true>(l.bits, i, (int64_t)s.c0 * kVec<T> - r.mis, (int64_t)s.c1 * kVec<T> - r.mis);
       }
     }
-    __syncthreads();
   }
+  if (TAIL) __syncthreads();
   float m = kNegInf, rest = 0.0f, top = 0.0f;
-  for (uint32_t j0 = s.c0 + tid; j0 < s.c1; j0 += kBatch * kPartThreads) {
-    Chunk<T> v[kBatch];
-    float mb = m;
+  if (row_wave) {
+    for (uint32_t j0 = s.c0 + tid; j0 < s.c1; j0 += kBatch * kPartThreads) {
+      float mb = m;
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      const uint32_t j = j0 + q * kPartThreads;
-      if (j < s.c1) {
-        v[q] = load_chunk(r, j);
-      } else {
+      for (int q = 0; q < kBatch; ++q) {
+        float z[kVec<T>];
+        unpack(v[q], z);
 #pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) v[q].v[e] = (T)kNegInf;
+        for (int e = 0; e < kVec<T>; ++e) mb = fmaxf(mb, z[e]);
       }
-    }
+      if (mb > m) {
+        const float k = m == kNegInf ? 0.0f : ex2((m - mb) * a.c);
+        rest *= k;
+        top *= k;
+        m = mb;
+      }
+      const float ms = m == kNegInf ? 0.0f : m;
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      float z[kVec<T>];
-      unpack(v[q], z);
-#pragma unroll
-      for (int e = 0; e < kVec<T>; ++e) mb = fmaxf(mb, z[e]);
+      for (int q = 0; q < kBatch; ++q) {
+        const uint32_t j = j0 + q * kPartThreads;
+        if (j < s.c1)
+          add_chunk<T, TAIL>(v[q], ms, a.c, TAIL ? chunk_bits<T>(l.bits, j - s.c0) : 0u, rest, top);
+      }
+      if (j0 + kBatch * kPartThreads < s.c1) load_batch(r, j0 + kBatch * kPartThreads, s.c1, v);
     }
-    if (mb > m) {
-      const float k = m == kNegInf ? 0.0f : ex2((m - mb) * a.c);
-      rest *= k;
-      top *= k;
-      m = mb;
-    }
-    const float ms = m == kNegInf ? 0.0f : m;
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      const uint32_t j = j0 + q * kPartThreads;
-      if (j < s.c1)
-        add_chunk<T, TAIL>(v[q], ms, a.c, TAIL ? chunk_bits<T>(bits, j - s.c0) : 0u, rest, top);
-    }
+    const float mw = wave_max(m);
+    if ((tid & 63) == 0) red[0][wv] = mw;
   }
-  float mw = wave_max(m);
-  if ((tid & 63) == 0) red[0][wv] = mw;
   __syncthreads();
-  mw = red[0][0];
+  float mw = red[0][0];
 #pragma unroll
   for (int q = 1; q < kPartThreads / 64; ++q) mw = fmaxf(mw, red[0][q]);
-  const float k = m == kNegInf ? (rest == rest ? 0.0f : 1.0f) : ex2((m - mw) * a.c);
-  rest = wave_sum(rest * k);
-  top = wave_sum(top * k);
-  if ((tid & 63) == 0) {
-    red[1][wv] = rest;
-    red[2][wv] = top;
+  if (row_wave) {
+    const float k = m == kNegInf ? (rest == rest ? 0.0f : 1.0f) : ex2((m - mw) * a.c);
+    rest = wave_sum(rest * k);
+    top = wave_sum(top * k);
+    if ((tid & 63) == 0) {
+      red[1][wv] = rest;
+      red[2][wv] = top;
+    }
   }
   __syncthreads();
   if (tid == 0) {
@@ -511,13 +555,14 @@ __global__ __launch_bounds__(kPartThreads) void distill_part_kernel(DistillArgs 
 }
 
 // Joins a row's parts; one wave per row.
-template <typename T, bool TAIL>
+template <bool TAIL>
 __global__ __launch_bounds__(64) void distill_join_kernel(DistillArgs a) {
-  extern __shared__ char mem[];
   const int64_t n = blockIdx.x;
   const int lane = threadIdx.x;
   const float* part = a.part + n * a.splits * 4;
   const bool off = a.weight && a.weight[n] == 0.0f;
+  Teacher t = {0.0, 0.0, 0.0, 0.0, 0.0f, false, false};
+  if (!off) t = a.teacher[n];
   float m = kNegInf, rest = 0.0f, top = 0.0f;
   for (int q = lane; q < a.splits; q += 64) m = fmaxf(m, part[4 * q]);
   m = wave_max(m);
@@ -531,79 +576,86 @@ __global__ __launch_bounds__(64) void distill_join_kernel(DistillArgs a) {
   top = wave_sum(top);
   if (m == kNegInf) m = 0.0f;
   float S = rest + top;
-  float loss = 0.0f, p_rest = 0.0f;
-  if (!off) {
-    const Row<T> r = row_of<T>(a, n);
-    const Lds l = lds_of(mem, a.K, 0);
-    const Teacher t = teacher<T, TAIL>(a, r, n, l, 0, 0, 0, first_entry(a, n));
-    const bool dead = S == 0.0f || (!TAIL && !t.any);
-    if (dead) S = rest = 0.0f;
-    loss = dead ? 0.0f : row_loss(a, l, t, m, S, rest, TAIL);
-    p_rest = (float)t.rest;
-  }
+  const bool dead = off || S == 0.0f || (!TAIL && !t.any);
+  if (dead) S = rest = 0.0f;
+  const float loss = dead ? 0.0f : row_loss(a, t, m, S, rest, TAIL);
   if (lane == 0) {
     a.loss[n] = loss;
     if (a.saved) {
-      float* s = a.saved + n * 4;
+      float* s = a.saved + n * (4 + a.K);
       s[0] = m;
       s[1] = S;
       s[2] = rest;
-      s[3] = p_rest;
+      s[3] = (float)t.rest;
     }
   }
 }
 
-// Gradient of one part of a row from its saved statistics.
+// Gradient of one part of a row from its saved statistics and probabilities.
 template <typename T, bool TAIL>
-__global__ __launch_bounds__(kPartThreads) void distill_grad_kernel(DistillArgs a) {
+__global__ __launch_bounds__(kPartThreads + 64) void distill_grad_kernel(DistillArgs a) {
   extern __shared__ char mem[];
   __shared__ uint32_t sh_dup;
   const int64_t n = blockIdx.x / (uint32_t)a.splits;
   const int tid = threadIdx.x, wv = tid >> 6;
+  const bool row_wave = wv < kPartThreads / 64;
   const Row<T> r = row_of<T>(a, n);
-  const Span s = span_of(a, r, n, (int)(blockIdx.x % (uint32_t)a.splits));
+  const Span s = span_of(a, r, (int)(blockIdx.x % (uint32_t)a.splits));
+  const int64_t lo = (int64_t)s.c0 * kVec<T> - r.mis, hi = (int64_t)s.c1 * kVec<T> - r.mis;
   T* grad = static_cast<T*>(a.grad) + n * a.grad_stride;
+  const float* saved = a.saved + n * (4 + a.K);
   const float w = a.weight ? a.weight[n] : 1.0f;
-  const float m = a.saved[4 * n], S = a.saved[4 * n + 1], rest = a.saved[4 * n + 2];
+  const float m = saved[0], S = saved[1], rest = saved[2];
   if (w == 0.0f || S == 0.0f) {
     const float zero[kVec<T>] = {};
-    for (uint32_t j = s.c0 + tid; j < s.c1; j += kPartThreads) store_chunk(grad, r, j, zero);
+    for (uint32_t j = s.c0 + tid; j < s.c1; j += kPartThreads + 64) store_chunk(grad, r, j, zero);
     return;
   }
-  const uint32_t words = mark_words(TAIL, (int64_t)(s.c1 - s.c0) * kVec<T>);
+  const uint32_t words = mark_words(false, (int64_t)(s.c1 - s.c0) * kVec<T>);
   const Lds l = lds_of(mem, a.K, words);
-  if (wv == 0) {
-    const Teacher t = teacher<T, TAIL>(a, r, n, l, words, s.c0, s.c1, first_entry(a, n));
-    if (tid == 0) sh_dup = t.dup;
+  Chunk<T> v[kBatch];
+  if (row_wave) {
+    load_batch(r, s.c0 + tid, s.c1, v);
+  } else {
+    bool dup = false;
+    clear_marks(l.bits, words);
+    for (int k = tid & 63; k < a.K; k += 64) {
+      const int i = a.tidx[n * a.K + k];
+      const float p = saved[4 + k];
+      const bool here = i >= 0 && i < (int64_t)r.V && i >= lo && i < hi;
+      l.idx[k] = here ? i : -1;
+      l.p[k] = p;
+      if (here) {
+        l.z[k] = (float)r.z[i];
+        dup |= mark<false>(l.bits, i, lo, hi);
+      }
+    }
+    const bool any = __any(dup);
+    if ((tid & 63) == 0) sh_dup = any;
   }
   __syncthreads();  // the top's logits are read before they may be overwritten
   const float scale = w * a.tau;
-  const float coef =
-      TAIL ? (rest == 0.0f ? 0.0f
-                           : scale * (__builtin_fmaf(-a.saved[4 * n + 3], S, rest) / (S * rest)))
-           : scale / S;
-  for (uint32_t j0 = s.c0 + tid; j0 < s.c1; j0 += kBatch * kPartThreads) {
-    Chunk<T> v[kBatch];
+  if (row_wave) {
+    const float coef =
+        TAIL ? (rest == 0.0f ? 0.0f : scale * (__builtin_fmaf(-saved[3], S, rest) / (S * rest)))
+             : scale / S;
+    for (uint32_t j0 = s.c0 + tid; j0 < s.c1; j0 += kBatch * kPartThreads) {
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      const uint32_t j = j0 + q * kPartThreads;
-      if (j < s.c1) v[q] = load_chunk(r, j);
-    }
+      for (int q = 0; q < kBatch; ++q) {
+        const uint32_t j = j0 + q * kPartThreads;
+        if (j < s.c1) {
+          float z[kVec<T>], g[kVec<T>];
+          unpack(v[q], z);
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      const uint32_t j = j0 + q * kPartThreads;
-      if (j < s.c1) {
-        float z[kVec<T>], g[kVec<T>];
-        unpack(v[q], z);
-#pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) g[e] = coef * ex2((z[e] - m) * a.c);
-        store_chunk(grad, r, j, g);
+          for (int e = 0; e < kVec<T>; ++e) g[e] = coef * ex2((z[e] - m) * a.c);
+          store_chunk(grad, r, j, g);
+        }
       }
+      if (j0 + kBatch * kPartThreads < s.c1) load_batch(r, j0 + kBatch * kPartThreads, s.c1, v);
     }
   }
   __syncthreads();
-  patch_top(a, l, grad, m, S, scale, sh_dup != 0, (int64_t)s.c0 * kVec<T> - r.mis,
-            (int64_t)s.c1 * kVec<T> - r.mis);
+  patch_top(a, l, grad, m, S, scale, sh_dup != 0, lo, hi);
 }
 
 size_t lds_bytes(int K, bool tail, int64_t tokens) {
@@ -622,10 +674,10 @@ int64_t part_tokens(const DistillArgs& a, int type) {
 template <typename T, int NT, int R, bool ONCE = false>
 hipError_t row_launch(const DistillArgs& a, hipStream_t s) {
   const size_t lds = lds_bytes(a.K, a.tlse != nullptr, a.V + 2 * kVec<T>);
-  const dim3 grid((uint32_t)a.N);
+  const dim3 grid((uint32_t)a.N), block(kRowThreads<NT>);
   if (a.tlse)
-    return launch_kernel(distill_row_kernel<T, NT, R, true, ONCE>, grid, dim3(NT), lds, s, a);
-  return launch_kernel(distill_row_kernel<T, NT, R, false, ONCE>, grid, dim3(NT), lds, s, a);
+    return launch_kernel(distill_row_kernel<T, NT, R, true, ONCE>, grid, block, lds, s, a);
+  return launch_kernel(distill_row_kernel<T, NT, R, false, ONCE>, grid, block, lds, s, a);
 }
 
 template <typename T>
@@ -646,25 +698,25 @@ hipError_t row_typed(const DistillArgs& a, hipStream_t s) {
 
 template <typename T>
 hipError_t stats_typed(const DistillArgs& a, int type, hipStream_t s) {
-  const dim3 grid((uint32_t)(a.N * a.splits));
-  const size_t lds = lds_bytes(0, true, part_tokens(a, type));
-  hipError_t e = a.tlse ? launch_kernel(distill_part_kernel<T, true>, grid, dim3(kPartThreads), lds,
-                                        s, a)
-                        : launch_kernel(distill_part_kernel<T, false>, grid, dim3(kPartThreads), 0,
-                                        s, a);
+  const dim3 grid((uint32_t)(a.N * a.splits)), block(kPartThreads + 64);
+  if (a.tlse) {
+    const hipError_t e = launch_kernel(distill_part_kernel<T, true>, grid, block,
+                                       lds_bytes(a.K, true, part_tokens(a, type)), s, a);
+    if (e != hipSuccess) return e;
+    return launch_kernel(distill_join_kernel<true>, dim3((uint32_t)a.N), dim3(64), 0, s, a);
+  }
+  const hipError_t e = launch_kernel(distill_part_kernel<T, false>, grid, block,
+                                     lds_bytes(a.K, true, 0), s, a);
   if (e != hipSuccess) return e;
-  return a.tlse ? launch_kernel(distill_join_kernel<T, true>, dim3((uint32_t)a.N), dim3(64),
-                                lds_bytes(a.K, true, 0), s, a)
-                : launch_kernel(distill_join_kernel<T, false>, dim3((uint32_t)a.N), dim3(64),
-                                lds_bytes(a.K, true, 0), s, a);
+  return launch_kernel(distill_join_kernel<false>, dim3((uint32_t)a.N), dim3(64), 0, s, a);
 }
 
 template <typename T>
 hipError_t grad_typed(const DistillArgs& a, int type, hipStream_t s) {
-  const dim3 grid((uint32_t)(a.N * a.splits));
-  const size_t lds = lds_bytes(a.K, a.tlse != nullptr, part_tokens(a, type));
-  return a.tlse ? launch_kernel(distill_grad_kernel<T, true>, grid, dim3(kPartThreads), lds, s, a)
-                : launch_kernel(distill_grad_kernel<T, false>, grid, dim3(kPartThreads), lds, s, a);
+  const dim3 grid((uint32_t)(a.N * a.splits)), block(kPartThreads + 64);
+  const size_t lds = lds_bytes(a.K, false, part_tokens(a, type));
+  return a.tlse ? launch_kernel(distill_grad_kernel<T, true>, grid, block, lds, s, a)
+                : launch_kernel(distill_grad_kernel<T, false>, grid, block, lds, s, a);
 }
 
 }  // namespace

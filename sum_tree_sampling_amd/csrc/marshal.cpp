@@ -422,9 +422,9 @@ PyObject* scan_workspace(const Args& a) {
 
 // ----------------------------------------------------------------- distillation
 
-int64_t distill_bytes(int64_t N, int64_t V, int type) {
+int64_t distill_bytes(int64_t N, int64_t V, int64_t K, int type) {
   size_t n = 0;
-  check(api.per_distill_workspace_bytes(N, V, type, &n));
+  check(api.per_distill_workspace_bytes(N, V, K, type, &n));
   return (int64_t)n;
 }
 
@@ -468,7 +468,7 @@ PyObject* distill(const Args& a) {
   const Tensor loss = output(a, 6, {o.N}, at::kFloat, w), grad = output(a, 7, all, o.dtype, w);
   float* pl = dense<float>(loss, "loss", at::kFloat, {o.N}, w);
   const Matrix mg = matrix(grad, "grad", o.dtype, all, w);
-  const int64_t bytes = distill_bytes(o.N, o.V, o.type);
+  const int64_t bytes = distill_bytes(o.N, o.V, o.K, o.type);
   Tensor ws;
   if (bytes) ws = w.empty({bytes}, at::kByte);
   check(api.per_distill(TOP(o), weight, pl, mg.p, mg.stride, bytes ? ws.data_ptr() : nullptr,
@@ -481,10 +481,10 @@ PyObject* distill_forward(const Args& a) {
   const Where w(a.v[7], a.tensor(0), "logits");
   const Top o = top(a, 3, w);
   const Tensor loss = output(a, 5, {o.N}, at::kFloat, w),
-               saved = output(a, 6, {o.N, 4}, at::kFloat, w);
+               saved = output(a, 6, {o.N, 4 + o.K}, at::kFloat, w);
   float* pl = dense<float>(loss, "loss", at::kFloat, {o.N}, w);
-  float* ps = dense<float>(saved, "saved", at::kFloat, {o.N, 4}, w);
-  const int64_t bytes = distill_bytes(o.N, o.V, o.type);
+  float* ps = dense<float>(saved, "saved", at::kFloat, {o.N, 4 + o.K}, w);
+  const int64_t bytes = distill_bytes(o.N, o.V, o.K, o.type);
   Tensor ws;
   if (bytes) ws = w.empty({bytes}, at::kByte);
   check(api.per_distill_forward(TOP(o), pl, ps, bytes ? ws.data_ptr() : nullptr, (size_t)bytes,
@@ -497,7 +497,7 @@ PyObject* distill_backward(const Args& a) {
   const Where w(a.v[8], a.tensor(0), "logits");
   const Top o = top(a, 5, w);
   const int64_t all[] = {o.N, o.V};
-  const auto* saved = dense<const float>(a, 3, at::kFloat, {o.N, 4}, w);
+  const auto* saved = dense<const float>(a, 3, at::kFloat, {o.N, 4 + o.K}, w);
   const auto* gloss = dense<const float>(a, 4, at::kFloat, {o.N}, w);
   const Tensor grad = output(a, 7, all, o.dtype, w);
   const Matrix mg = matrix(grad, "grad", o.dtype, all, w);
@@ -506,7 +506,8 @@ PyObject* distill_backward(const Args& a) {
 }
 
 PyObject* distill_workspace(const Args& a) {
-  return PyLong_FromLongLong(distill_bytes(a.integer(0, 0), a.integer(1, 0), (int)a.integer(2, 0)));
+  return PyLong_FromLongLong(
+      distill_bytes(a.integer(0, 0), a.integer(1, 0), a.integer(2, 0), (int)a.integer(3, 0)));
 }
 
 // ----------------------------------------------------------------- the module
@@ -552,8 +553,8 @@ Function functions[] = {
      "per_scan_step(x, g, h, reset=None, h_out=None, y=None, stream=None)\n\n"
      "One step of B sequences: x, g [B x D], h [B x D] f32 (updated in place without h_out).\n"
      "Returns (y, h_out).", {}},
-    {"per_distill_workspace_bytes", distill_workspace, 3, 3, {"N", "V", "type"},
-     "per_distill_workspace_bytes(N, V, type)", {}},
+    {"per_distill_workspace_bytes", distill_workspace, 4, 4, {"N", "V", "K", "type"},
+     "per_distill_workspace_bytes(N, V, K, type)", {}},
     {"per_distill", distill, 3, 9,
      {"logits", "tidx", "tlogit", "tlse", "temperature", "weight", "loss", "grad", "stream"},
      "per_distill(logits, tidx, tlogit, tlse=None, temperature=1.0, weight=None, loss=None, "

@@ -130,30 +130,35 @@ template <typename T, int FMT, int U, bool ROW>
 __global__ __launch_bounds__(kThreads) void rows_write_kernel(RowsArgs a, int lg) {
   const uint32_t lane = threadIdx.x & ((1u << lg) - 1);
   const uint32_t j = blockIdx.x * (uint32_t)(kThreads >> lg) + (threadIdx.x >> lg);
-  int64_t slot = -1;
-  if (j < a.rows) {
-    bool claimed;
-    slot = slot_of(a, j, &claimed);
-    if (claimed && lane == 0) a.claims[slot] = 0;
-  }
-  const bool live = slot >= 0;
+  const bool row = j < a.rows;
   const T* src = static_cast<const T*>(a.src) + (int64_t)j * a.stride;
-  uint8_t* codes = a.codes + slot * a.cs;
-  float* scales = a.scales + slot * a.ss;
   const uint32_t step = (uint32_t)U << lg;
+  int64_t slot = -1;
+  bool known = false;
   for (uint32_t u0 = blockIdx.y * step; 8 * u0 < a.dim; u0 += gridDim.y * step) {
+    // The row is loaded, and reduced, before its slot and claim are known: most
+    // rows are written, and three dependent loads would cost their latencies.
     float x[U][8];
     uint32_t m[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t u = u0 + ((uint32_t)i << lg) + lane;
-      if (live && 8 * u < a.dim) {
+      if (row && 8 * u < a.dim) {
         load_unit(src, u, a.dim, x[i]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
       }
     }
+    if (!known && row) {
+      bool claimed;
+      slot = slot_of(a, j, &claimed);
+      if (claimed && lane == 0) a.claims[slot] = 0;
+    }
+    known = true;
+    const bool live = slot >= 0;
+    uint8_t* codes = a.codes + slot * a.cs;
+    float* scales = a.scales + slot * a.ss;
     uint32_t all = 0;
 #pragma unroll
     for (int i = 0; i < U; ++i) {

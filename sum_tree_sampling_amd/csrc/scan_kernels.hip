@@ -2,7 +2,7 @@
 // (1 - f_t) x_t with f = sigmoid(g), forward, backward and one step.
 //
 // A workgroup takes 64 C channels of one sequence (C per lane) and walks the
-// time axis in tiles of kSteps steps per wave: each wave loads its steps,
+// time axis in tiles of a few steps per wave: each wave loads its steps,
 // reduces them to one affine map h -> A h + B, the maps meet in LDS, every
 // wave folds those before it into the state it starts from, and then runs its
 // steps.  So the inputs are read once, with as many loads in flight as a wave
@@ -25,21 +25,10 @@ namespace {
 // Steps of a wave in one tile.  The backward pass keeps four values of a step
 // (f, 1 - f, the packed inputs, the gate's weight), so that 16 steps of two
 // channels would not leave two workgroups' registers to a CU.
-#ifndef LBB
-#define LBB 4
-#endif
-#ifndef LBF
-#define LBF 4
-#endif
-#ifndef SF
-#define SF 16
-#endif
-#ifndef SB
-#define SB 8
-#endif
-constexpr int kForward = SF;
-constexpr int kBackward = SB;
-constexpr int kWaves = 8;                  // waves of a workgroup, at most
+constexpr int kForward = 16;
+constexpr int kBackward = 8;
+constexpr int kWaves = 8;                  // waves of a workgroup
+constexpr int kBackWaves = 16;             // in the backward pass, of one tile, at most
 constexpr int kChunk = 64;                 // PER_SCAN_CHUNK
 constexpr int kSegment = 128;              // segments are multiples of it
 constexpr int kMaxSeg = 128;
@@ -88,11 +77,16 @@ __device__ __forceinline__ int steps_at(int64_t ts, int64_t live) {
   return n < 0 ? 0 : n > S ? S : (int)n;
 }
 
-// Bit s: an episode begins at step ts + s (s < n), the same in every lane.
-__device__ __forceinline__ uint32_t reset_mask(const uint8_t* reset, int64_t ts, int n) {
-  if (!reset) return 0;
+// The lane's byte of the resets at step ts + lane, loaded a tile ahead (for the
+// first tile beside the sequence's length); reset_mask then has bit s where an
+// episode begins at ts + s, s < n, the same in every lane.
+template <int S>
+__device__ __forceinline__ uint8_t reset_byte(const uint8_t* reset, int64_t ts, int64_t T) {
   const int lane = threadIdx.x & 63;
-  return (uint32_t)__ballot(lane < n && reset[ts + lane] != 0);
+  return reset && lane < S && ts >= 0 && ts + lane < T ? reset[ts + lane] : 0;
+}
+__device__ __forceinline__ uint32_t reset_mask(uint8_t byte, int n) {
+  return (uint32_t)__ballot(byte != 0) & ((1u << n) - 1);
 }
 
 // A [T x D] matrix of one sequence: the row's address is the same in every
@@ -116,7 +110,7 @@ __device__ __forceinline__ void load_steps(const Rows<const T>& r, int64_t ts, i
 }
 
 template <typename T, int C>
-__global__ __launch_bounds__(kWaves * 64, LBF) void scan_forward_kernel(ScanArgs a) {
+__global__ __launch_bounds__(kWaves * 64, 4) void scan_forward_kernel(ScanArgs a) {
   constexpr int S = kForward;
   __shared__ float sA[2][kWaves][C][64], sB[2][kWaves][C][64];
   __shared__ uint32_t sF[2][kWaves];
@@ -125,11 +119,12 @@ __global__ __launch_bounds__(kWaves * 64, LBF) void scan_forward_kernel(ScanArgs
   const int nw = blockDim.x >> 6;
   const Place p = place<C>(a);
   const bool in = p.d < a.D;
+  const uint8_t* reset = a.reset ? a.reset + p.b * a.T : nullptr;
+  uint8_t begins = reset_byte<S>(reset, p.t_begin + wv * S, a.T);
   const uint32_t d32 = (uint32_t)p.d;
   const Rows<const T> x = {static_cast<const T*>(a.x) + p.b * a.x_sb, a.x_st, d32};
   const Rows<const T> g = {static_cast<const T*>(a.g) + p.b * a.g_sb, a.g_st, d32};
   const Rows<T> y = {static_cast<T*>(a.y) + p.b * a.y_sb, a.y_st, d32};
-  const uint8_t* reset = a.reset ? a.reset + p.b * a.T : nullptr;
   float h[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) h[c] = a.h0 && in ? a.h0[p.b * a.D + p.d + c] : 0.0f;
@@ -168,7 +163,8 @@ __global__ __launch_bounds__(kWaves * 64, LBF) void scan_forward_kernel(ScanArgs
   for (int64_t t0 = p.t_begin; t0 < p.t_end; t0 += nw * S, buf ^= 1) {
     const int64_t ts = t0 + wv * S;
     const int n = steps_at<S>(ts, p.live);
-    const uint32_t mask = reset_mask(reset, ts, n);
+    const uint32_t mask = reset_mask(begins, n);
+    begins = reset_byte<S>(reset, ts + nw * S, a.T);
     float f[S][C], ix[S][C];
     float A[C], B[C];
 #pragma unroll
@@ -227,7 +223,7 @@ __global__ __launch_bounds__(kWaves * 64, LBF) void scan_forward_kernel(ScanArgs
       for (int s = 0; s < S; ++s) {
 #pragma unroll
         for (int c = 0; c < C; ++c) hs[c] = __builtin_fmaf(f[s][c], hs[c], ix[s][c]);
-        store_once<T, C>(y.at(ts + s), hs);
+        store_vals<T, C>(y.at(ts + s), hs);
       }
     } else if (in) {
 #pragma unroll
@@ -237,10 +233,10 @@ __global__ __launch_bounds__(kWaves * 64, LBF) void scan_forward_kernel(ScanArgs
 #pragma unroll
           for (int c = 0; c < C; ++c)
             hs[c] = r ? ix[s][c] : __builtin_fmaf(f[s][c], hs[c], ix[s][c]);
-          store_once<T, C>(y.at(ts + s), hs);
+          store_vals<T, C>(y.at(ts + s), hs);
         } else if (ts + s < p.t_end) {
           const float zero[C] = {};
-          store_once<T, C>(y.at(ts + s), zero);
+          store_vals<T, C>(y.at(ts + s), zero);
         }
       }
     }
@@ -277,7 +273,7 @@ __global__ __launch_bounds__(kWaves * 64) void scan_segment_kernel(ScanArgs a) {
     const int64_t ts = p.t_begin + wv * run + (REV ? run - S - k : k);
     const int n = steps_at<S>(ts, p.live);
     if (n == 0) continue;
-    const uint32_t mask = reset_mask(reset, ts, n);
+    const uint32_t mask = reset_mask(reset_byte<S>(reset, ts, a.T), n);
     flag |= mask;
     if (!in) continue;
     auto reduce = [&](auto is_full) {
@@ -347,10 +343,10 @@ __global__ __launch_bounds__(kWaves * 64) void scan_segment_kernel(ScanArgs a) {
 //   dx = full (1 - f),  dg = full (h' - x) f (1 - f).
 // The states of a chunk are computed again from its carry.
 template <typename T, int C>
-__global__ __launch_bounds__(kWaves * 64, LBB) void scan_backward_kernel(ScanArgs a) {
+__global__ __launch_bounds__(64 * kBackWaves, 4) void scan_backward_kernel(ScanArgs a) {
   constexpr int S = kBackward;
-  __shared__ float sA[2][kWaves][C][64], sB[2][kWaves][C][64], sQ[2][kWaves][C][64];
-  __shared__ uint32_t sF[2][kWaves];
+  __shared__ float sA[2][kBackWaves][C][64], sB[2][kBackWaves][C][64], sQ[2][kBackWaves][C][64];
+  __shared__ uint32_t sF[2][kBackWaves];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = blockDim.x >> 6;
@@ -403,6 +399,7 @@ __global__ __launch_bounds__(kWaves * 64, LBB) void scan_backward_kernel(ScanArg
 
   const int64_t tile = nw * S;
   const int64_t tiles = p.t_end > p.t_begin ? (p.t_end - p.t_begin + tile - 1) / tile : 0;
+  uint8_t begins = reset_byte<S>(reset, p.t_begin + (tiles - 1) * tile + wv * S, a.T);
   float Eo[C];  // what flows out of the wave's own steps, run one by one
 #pragma unroll
   for (int c = 0; c < C; ++c) Eo[c] = E[c];
@@ -411,7 +408,8 @@ __global__ __launch_bounds__(kWaves * 64, LBB) void scan_backward_kernel(ScanArg
     const int64_t t0 = p.t_begin + k * tile;
     const int64_t ts = t0 + wv * S;
     const int n = steps_at<S>(ts, p.live);
-    const uint32_t mask = reset_mask(reset, ts, n);
+    const uint32_t mask = reset_mask(begins, n);
+    begins = reset_byte<S>(reset, ts - tile, a.T);
     float f[S][C], i[S][C];
     Pack<T, C> px[S], pd[S];
     float h[C], A[C], B[C], Q[C];
@@ -590,9 +588,19 @@ hipError_t backward_typed(const ScanArgs& a, uint32_t blocks, int waves, hipStre
   return launch_kernel(scan_backward_kernel<T, C>, dim3(blocks), dim3(64 * waves), 0, s, a);
 }
 
-int waves_for(int64_t T, int steps) {
-  const int64_t w = (T + steps - 1) / steps;
+// Waves of a workgroup: as many as the sequence has steps for, up to 8.  The
+// backward pass takes up to 128 steps in one tile of 16 waves where there are
+// too few workgroups for two to a CU anyway (37 x 81 x 333 f32: 10.7 -> 9.0 us;
+// with 2048 workgroups, 256 x 128 x 1024 bf16, one such workgroup to a CU would
+// leave loads and stores unoverlapped).
+int forward_waves(int64_t T) {
+  const int64_t w = (T + kForward - 1) / kForward;
   return w < 1 ? 1 : w > kWaves ? kWaves : (int)w;
+}
+int backward_waves(int64_t T, uint32_t blocks) {
+  const int64_t w = (T + kBackward - 1) / kBackward;
+  if (w <= kWaves) return w < 1 ? 1 : (int)w;
+  return w <= kBackWaves && blocks < 512 ? (int)w : kWaves;
 }
 
 // Segments and their steps (multiples of kSegment).
@@ -637,7 +645,7 @@ size_t scan_workspace(int64_t B, int64_t T, int64_t D) {
 hipError_t launch_scan_forward(ScanArgs a, int type, hipStream_t s) {
   set_split(a);
   const uint32_t blocks = (uint32_t)(a.B * a.nseg * channel_tiles(a.D));
-  const int waves = waves_for(a.T, kForward);
+  const int waves = forward_waves(a.T);
   const bool two = two_channels(a.D);
   if (type == 0)
     return two ? forward_typed<float, 2>(a, blocks, waves, s)
@@ -652,7 +660,7 @@ hipError_t launch_scan_forward(ScanArgs a, int type, hipStream_t s) {
 hipError_t launch_scan_backward(ScanArgs a, int type, hipStream_t s) {
   set_split(a);
   const uint32_t blocks = (uint32_t)(a.B * a.nseg * channel_tiles(a.D));
-  const int waves = waves_for(a.T, kBackward);
+  const int waves = backward_waves(a.T, blocks);
   const bool two = two_channels(a.D);
   if (type == 0)
     return two ? backward_typed<float, 2>(a, blocks, waves, s)

@@ -144,8 +144,24 @@ int check_distill(per::DistillArgs& a, int64_t N, int64_t V, int64_t K, int32_t 
   return PER_OK;
 }
 
-size_t part_bytes(int64_t N, int64_t V, int32_t type) {
-  return (size_t)N * per::distill_splits(N, V, type) * 16;
+// Workspace of rows taken in parts: the teacher's sums of each row, each part's
+// statistics, and what per_distill saves between its passes.
+struct DistillSpace {
+  size_t part, saved, total;
+};
+DistillSpace distill_space(int64_t N, int64_t V, int64_t K, int32_t type) {
+  DistillSpace s;
+  s.part = (size_t)N * sizeof(per::Teacher);
+  s.saved = s.part + (size_t)N * per::distill_splits(N, V, type) * 16;
+  s.total = s.saved + (size_t)N * (size_t)(4 + K) * 4;
+  return s;
+}
+void set_space(per::DistillArgs& a, void* ws, int32_t type) {
+  const DistillSpace s = distill_space(a.N, a.V, a.K, type);
+  char* base = static_cast<char*>(ws);
+  a.teacher = reinterpret_cast<per::Teacher*>(base);
+  a.part = reinterpret_cast<float*>(base + s.part);
+  a.saved = reinterpret_cast<float*>(base + s.saved);
 }
 
 int check_grad(const void* grad, int64_t stride, int32_t type, int64_t V, const void* z,
@@ -347,12 +363,12 @@ int per_scan_step(int64_t B, int64_t D, int32_t type, const void* d_x, int64_t x
   return done(per::launch_scan_step(a, type, stream), "per_scan_step");
 }
 
-int per_distill_workspace_bytes(int64_t N, int64_t V, int32_t type, size_t* out) {
-  if (N < 0 || N > kMaxGrid || V < 1 || V > PER_MAX_VOCAB) return bad("N or V is out of range");
+int per_distill_workspace_bytes(int64_t N, int64_t V, int64_t K, int32_t type, size_t* out) {
+  if (N < 0 || N > kMaxGrid || V < 1 || V > PER_MAX_VOCAB || K < 1 || K > PER_MAX_TOP)
+    return bad("N, V or K is out of range");
   if (!type_ok(type)) return bad("type %d is none", (int)type);
   if (!out) return bad("out is NULL");
-  // parts, and the saved statistics of per_distill where it takes rows in parts
-  *out = N > 0 ? part_bytes(N, V, type) + (size_t)N * 16 : 0;
+  *out = N > 0 ? distill_space(N, V, K, type).total : 0;
   return per::api_ok();
 }
 
@@ -375,10 +391,8 @@ int per_distill(int64_t N, int64_t V, int64_t K, int32_t type, const void* d_log
   a.grad_stride = grad_stride;
   if (per::distill_resident(N, V, type))
     return done(per::launch_distill_fused(a, type, stream), "per_distill");
-  const size_t parts = part_bytes(N, V, type);
-  if ((rc = check_ws(d_ws, ws_bytes, parts + (size_t)N * 16))) return rc;
-  a.part = static_cast<float*>(d_ws);
-  a.saved = reinterpret_cast<float*>(static_cast<char*>(d_ws) + parts);
+  if ((rc = check_ws(d_ws, ws_bytes, distill_space(N, V, K, type).total))) return rc;
+  set_space(a, d_ws, type);
   hipError_t e = per::launch_distill_forward(a, type, stream);
   if (e == hipSuccess) e = per::launch_distill_backward(a, type, stream);
   return done(e, "per_distill");
@@ -396,10 +410,10 @@ int per_distill_forward(int64_t N, int64_t V, int64_t K, int32_t type, const voi
   if (N == 0) return per::api_ok();
   if (!d_loss || misaligned(d_loss, 4) || misaligned(d_saved, 4))
     return bad("loss is required, loss and saved 4-byte aligned");
-  if ((rc = check_ws(d_ws, ws_bytes, part_bytes(N, V, type)))) return rc;
+  if ((rc = check_ws(d_ws, ws_bytes, distill_space(N, V, K, type).total))) return rc;
+  set_space(a, d_ws, type);
   a.loss = d_loss;
   a.saved = d_saved;
-  a.part = static_cast<float*>(d_ws);
   return done(per::launch_distill_forward(a, type, stream), "per_distill_forward");
 }
 

@@ -68,6 +68,16 @@ struct StepArgs {
 hipError_t launch_scan_step(const StepArgs& a, int type, hipStream_t s);
 
 // --------------------------------------------------------------- distillation
+// What a row's teacher entries sum to.
+struct Teacher {
+  double h;     // sum p log p
+  double ps;    // sum p
+  double pz;    // sum p (z - z0)
+  double rest;  // p_r
+  float z0;     // largest student's logit at an entry
+  bool any;     // an entry is present
+  bool dup;     // two entries may name one token of the part
+};
 struct DistillArgs {
   int64_t N, V;
   int K;
@@ -82,10 +92,11 @@ struct DistillArgs {
   float tau;
   const float* weight;    // NULL: 1
   float* loss;
-  float* saved;           // [N x 4]
+  float* saved;           // [N x (4 + K)]
   void* grad;
   int64_t grad_stride;
   float* part;            // [N x splits x 4]
+  Teacher* teacher;       // [N]
   int splits;
 };
 // Whether one workgroup holds a whole row in registers, and if not, how many

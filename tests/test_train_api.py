@@ -29,7 +29,7 @@ SIG = {
     "per_scan_backward": [_i64, _i64, _i64, _i32] + 2 * _VIEW + [_vp, _vp, _vp] + _VIEW + [_vp]
     + 2 * _VIEW + [_vp, _vp, _sz, _vp],
     "per_scan_step": [_i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp],
-    "per_distill_workspace_bytes": [_i64, _i64, _i32, ctypes.POINTER(_sz)],
+    "per_distill_workspace_bytes": [_i64, _i64, _i64, _i32, ctypes.POINTER(_sz)],
     "per_distill": _TOPK + [_vp, _vp, _vp, _i64, _vp, _sz, _vp],
     "per_distill_forward": _TOPK + [_vp, _vp, _vp, _sz, _vp],
     "per_distill_backward": _TOPK + [_vp, _vp, _vp, _i64, _vp],
@@ -203,13 +203,13 @@ def test_distill_backward_refuses(call, kw):
 
 def test_distill_workspace(call):
     from sum_tree_sampling_amd import per_distill_workspace_bytes as need
-    n = need(4, 200000, 1)
-    assert n > 0 and need(0, 100, 0) == 0
+    n = need(4, 200000, 8, 1)
+    assert n > 0 and need(0, 100, 8, 0) == 0
     a = dict(TOP, V=200000, stride=200000, loss=P, saved=P, ws=P, ws_bytes=15)
     assert call("per_distill_forward", *a.values(), None) == ENOSPC
     a = dict(TOP, V=200000, stride=200000, weight=None, loss=P, grad=2 * P, gs=200000, ws=P, ws_bytes=n - 1)
     assert call("per_distill", *a.values(), None) == ENOSPC
-    for bad in ((-1, 5, 0), (1, 0, 0), (1, 5, 3)):
+    for bad in ((-1, 5, 1, 0), (1, 0, 1, 0), (1, 5, 1, 3), (1, 5, 0, 0), (1, 5, 1025, 0)):
         with pytest.raises(RuntimeError):
             need(*bad)
 
@@ -229,8 +229,8 @@ def test_binding_refuses(call):
             (per_rows_write, (codes, scales), {}), (per_rows_write, (codes, scales, None), {}),
             (per_rows_write, (codes, scales, 3), {}), (per_scan_forward, (3, x), {}),
             (per_distill, (z, ti, t), {"nothing": 1}), (per_distill, (z, ti, t), {"logits": z}),
-            (per_distill, (z,) * 12, {}), (per_distill_workspace_bytes, (2.5, 10, 0), {}),
-            (per_distill_workspace_bytes, (1 << 70, 10, 0), {})]:
+            (per_distill, (z,) * 12, {}), (per_distill_workspace_bytes, (2.5, 10, 1, 0), {}),
+            (per_distill_workspace_bytes, (1 << 70, 10, 1, 0), {})]:
         with pytest.raises(ValueError):
             f(*args, **kw)
     with pytest.raises(ValueError):

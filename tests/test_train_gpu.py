@@ -577,7 +577,7 @@ def state(p):
     t = torch.randn(800, 7, generator=gen(3))
     s["t"], s["tlse"] = t.cuda(), with_rest(t, 1.0, 4).cuda()
     s["w"] = torch.rand(800, generator=gen(5)).cuda()
-    s["saved"] = torch.empty(800, 4, device=DEV)
+    s["saved"] = torch.empty(800, 4 + 7, device=DEV)
     s["loss"], s["loss2"] = torch.empty(800, device=DEV), torch.empty(800, device=DEV)
     return s
 
