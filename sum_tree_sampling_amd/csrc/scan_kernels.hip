@@ -31,7 +31,7 @@ constexpr int kWaves = 8;                  // waves of a workgroup
 constexpr int kBackWaves = 16;             // in the backward pass, of one tile, at most
 constexpr int kChunk = 64;                 // PER_SCAN_CHUNK
 constexpr int kSegment = 128;              // segments are multiples of it
-constexpr int kMaxSeg = 128;
+constexpr int kMaxSeg = 256;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // f = sigmoid(g) = 1 / (1 + e) and 1 - f = e / (1 + e), each to f32 precision;
@@ -558,14 +558,6 @@ __global__ __launch_bounds__(256) void scan_step_kernel(StepArgs a, int lg) {
   }
 }
 
-// Two channels per lane where they fill a wave's lanes and D is even, else one.
-bool two_channels(int64_t D) { return D % 2 == 0 && D > 64; }
-
-int64_t channel_tiles(int64_t D) {
-  const int64_t w = two_channels(D) ? 128 : 64;
-  return (D + w - 1) / w;
-}
-
 template <typename T, int C>
 hipError_t forward_typed(ScanArgs a, uint32_t blocks, int waves, hipStream_t s) {
   if (a.nseg > 1) {
@@ -603,50 +595,72 @@ int backward_waves(int64_t T, uint32_t blocks) {
   return w <= kBackWaves && blocks < 512 ? (int)w : kWaves;
 }
 
-// Segments and their steps (multiples of kSegment).
-struct Split {
+// How a batch is spread over the chip: channels per lane, segments of the time
+// axis, steps of a segment (a multiple of kSegment).
+//
+// The time axis is cut where there are fewer than 192 workgroups without it: a
+// cut costs a second reading of two of the tensors (24 x 300 x 1000 bf16, 192
+// workgroups: 67 us cut, 48 not; 16 x 512 x 1024, 128: 55 and 61).  Two channels
+// per lane are faster once the chip is full (128 x 512 x 1024: 231 against
+// 247 us; 2 x 16384 x 512: 89 against 101) and one below (4 x 512 x 256: 32
+// against 39; 32 x 80 x 512: 14.3 against 15.8), or where it saves the cut (16 x
+// 512 x 1024: 49 against 55).  Forward and backward together.
+struct Plan {
+  bool two;
+  int64_t blocks;  // without the cut
   int n;
   int64_t steps;
 };
-Split split_time(int64_t B, int64_t T, int64_t D) {
-  const int64_t blocks = B * channel_tiles(D);
+constexpr int64_t kFull = 192;
+
+Plan plan_with(int64_t B, int64_t T, int64_t D, bool two) {
+  const int64_t w = two ? 128 : 64;
+  Plan p = {two, B * ((D + w - 1) / w), 1, T};
   const int64_t chunks = (T + kSegment - 1) / kSegment;
-  Split s = {1, T};
-  if (blocks >= 256 || chunks < 2) return s;
-  int64_t n = (512 + blocks - 1) / blocks;
+  if (p.blocks >= kFull || chunks < 2) return p;
+  int64_t n = (512 + p.blocks - 1) / p.blocks;
   if (n > kMaxSeg) n = kMaxSeg;
   if (n > chunks) n = chunks;
-  s.steps = (chunks + n - 1) / n * kSegment;
-  s.n = (int)((T + s.steps - 1) / s.steps);
-  return s;
+  p.steps = (chunks + n - 1) / n * kSegment;
+  p.n = (int)((T + p.steps - 1) / p.steps);
+  return p;
 }
 
-void set_split(ScanArgs& a) {
-  const Split s = split_time(a.B, a.T, a.D);
-  a.nseg = s.n;
-  a.seg_steps = s.steps;
-  if (s.n > 1) {
-    a.h0_copy = a.agg + a.B * s.n * 2 * a.D;
+Plan plan(int64_t B, int64_t T, int64_t D) {
+  if (D % 2 != 0 || D <= 64) return plan_with(B, T, D, false);
+  const Plan two = plan_with(B, T, D, true), one = plan_with(B, T, D, false);
+  if (two.blocks * two.n < kFull || (two.n > 1 && one.n == 1)) return one;
+  return two;
+}
+
+Plan set_plan(ScanArgs& a) {
+  const Plan p = plan(a.B, a.T, a.D);
+  a.nseg = p.n;
+  a.seg_steps = p.steps;
+  if (p.n > 1) {
+    a.h0_copy = a.agg + a.B * p.n * 2 * a.D;
     a.agg_flag = reinterpret_cast<uint32_t*>(a.h0_copy + a.B * a.D);
   }
+  return p;
 }
 
 }  // namespace
 
 int64_t scan_blocks(int64_t B, int64_t T, int64_t D) {
-  return B * split_time(B, T, D).n * channel_tiles(D);
+  const Plan p = plan(B, T, D);
+  return p.blocks * p.n;
 }
 
 size_t scan_workspace(int64_t B, int64_t T, int64_t D) {
-  const int n = split_time(B, T, D).n;
+  const int n = plan(B, T, D).n;
   return n == 1 ? 0 : (size_t)(B * n * 2 * D + B * D + B * n) * 4;
 }
 
 hipError_t launch_scan_forward(ScanArgs a, int type, hipStream_t s) {
-  set_split(a);
-  const uint32_t blocks = (uint32_t)(a.B * a.nseg * channel_tiles(a.D));
+  const Plan p = set_plan(a);
+  const uint32_t blocks = (uint32_t)(p.blocks * p.n);
   const int waves = forward_waves(a.T);
-  const bool two = two_channels(a.D);
+  const bool two = p.two;
   if (type == 0)
     return two ? forward_typed<float, 2>(a, blocks, waves, s)
                : forward_typed<float, 1>(a, blocks, waves, s);
@@ -658,10 +672,10 @@ hipError_t launch_scan_forward(ScanArgs a, int type, hipStream_t s) {
 }
 
 hipError_t launch_scan_backward(ScanArgs a, int type, hipStream_t s) {
-  set_split(a);
-  const uint32_t blocks = (uint32_t)(a.B * a.nseg * channel_tiles(a.D));
+  const Plan p = set_plan(a);
+  const uint32_t blocks = (uint32_t)(p.blocks * p.n);
   const int waves = backward_waves(a.T, blocks);
-  const bool two = two_channels(a.D);
+  const bool two = p.two;
   if (type == 0)
     return two ? backward_typed<float, 2>(a, blocks, waves, s)
                : backward_typed<float, 1>(a, blocks, waves, s);
