@@ -675,3 +675,16 @@ def test_rounding_bound_itself():
     v = torch.randn(10000, dtype=torch.float64, generator=gen(1))
     for t in TYPES.values():
         assert ((v.to(t).double() - v).abs() <= rounding(v, t)).all()
+
+
+def test_example_learns():
+    """The example runs every operator together, and its student learns."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "replay_distill.py")
+    spec = importlib.util.spec_from_file_location("replay_distill", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    losses = m.main(steps=120, say=None)
+    assert torch.isfinite(losses).all()
+    assert losses[-10:].mean() < 0.7 * losses[:5].mean(), losses
