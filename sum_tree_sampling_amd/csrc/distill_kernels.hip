@@ -176,19 +176,21 @@ __device__ __forceinline__ bool mark(uint32_t* bits, int i, int64_t lo, int64_t 
   return (atomicOr(&bits[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u;
 }
 
-// One whole wave: entries to LDS, the bitmap of chunks [c0, c1), and the sums.
-// The K exponentials are taken in f64: the rest 1 - sum p would lose its digits
-// in f32 where the top holds nearly everything.
+// One whole wave: the entries to LDS, with the bitmap of chunks [c0, c1).  What
+// comes back is the lane's own share.
+struct Entries {
+  float tm, z0;  // largest teacher's and student's logits of the entries present
+  bool any, dup;
+};
 template <typename T, bool TAIL>
-__device__ __forceinline__ Teacher teacher(const DistillArgs& a, const Row<T>& r, int64_t n,
-                                           const Lds& l, uint32_t words, uint32_t c0, uint32_t c1,
-                                           Entry e) {
+__device__ __forceinline__ Entries read_entries(const DistillArgs& a, const Row<T>& r, int64_t n,
+                                                const Lds& l, uint32_t words, uint32_t c0,
+                                                uint32_t c1, Entry e) {
   const int lane = threadIdx.x & 63;
   clear_marks(l.bits, words);
   const int64_t lo = (int64_t)c0 * kVec<T> - r.mis;
   const int64_t hi = (int64_t)c1 * kVec<T> - r.mis;
-  float tm = kNegInf, z0 = kNegInf;
-  bool dup = false, any = false;
+  Entries o = {kNegInf, kNegInf, false, false};
   for (int k = lane; k < a.K; k += 64) {
     if (k != lane) {
       e.i = a.tidx[n * a.K + k];
@@ -196,18 +198,28 @@ __device__ __forceinline__ Teacher teacher(const DistillArgs& a, const Row<T>& r
     }
     const int i = e.i < 0 || e.i >= (int64_t)r.V ? -1 : e.i;
     const float z = i >= 0 ? (float)r.z[i] : kNegInf;
+    if (i >= 0) {
+      o.any = true;
+      o.tm = fmaxf(o.tm, e.t);
+      if (words) o.dup |= mark<TAIL>(l.bits, i, lo, hi);
+    }
     l.idx[k] = i;
     l.p[k] = e.t;
     l.z[k] = z;
-    if (i >= 0) {
-      any = true;
-      tm = fmaxf(tm, e.t);
-      z0 = fmaxf(z0, z);
-      if (words) dup |= mark<TAIL>(l.bits, i, lo, hi);
-    }
+    o.z0 = fmaxf(o.z0, z);
   }
-  tm = wave_max(tm);
-  z0 = wave_max(z0);
+  return o;
+}
+
+// The same wave: the probabilities to LDS, and the sums over the entries.  The
+// K exponentials are taken in f64: the rest 1 - sum p would lose its digits in
+// f32 where the top holds nearly everything.
+template <bool TAIL>
+__device__ __forceinline__ Teacher sum_entries(const DistillArgs& a, int64_t n, const Lds& l,
+                                               const Entries& e) {
+  const int lane = threadIdx.x & 63;
+  const float tm = wave_max(e.tm);
+  float z0 = wave_max(e.z0);
   if (z0 == kNegInf) z0 = 0.0f;
   // Without a rest: e = exp((t - largest) / tau), p = e / sum e.
   const double ref = TAIL || tm == kNegInf ? 0.0 : (double)tm;
@@ -230,8 +242,8 @@ __device__ __forceinline__ Teacher teacher(const DistillArgs& a, const Row<T>& r
   o.h = wave_sum(o.h);
   o.ps = wave_sum(o.ps);
   o.pz = wave_sum(o.pz);
-  o.any = __any(any) && o.ps != 0.0;  // entries at -Inf are none
-  o.dup = __any(dup);
+  o.any = __any(e.any) && o.ps != 0.0;  // entries at -Inf are none
+  o.dup = __any(e.dup);
   if (TAIL) {
     o.rest = 1.0 - o.ps;
     if (o.rest < 0.0) o.rest = 0.0;
@@ -333,10 +345,15 @@ __global__ __launch_bounds__(kRowThreads<NT>, NT >= 512 ? 4 : 1) void distill_ro
   }
   const uint32_t words = mark_words(TAIL, (int64_t)r.chunks * kVec<T>);
   const Lds l = lds_of(mem, a.K, words);
+  Entries entries;
+  auto sums = [&] {
+    const Teacher o = sum_entries<TAIL>(a, n, l, entries);
+    if ((tid & 63) == 0) t = o;
+  };
   auto read_teacher = [&] {
     if (!teacher_wave) return;
-    const Teacher o = teacher<T, TAIL>(a, r, n, l, words, 0, r.chunks, first);
-    if ((tid & 63) == 0) t = o;
+    entries = read_entries<T, TAIL>(a, r, n, l, words, 0, r.chunks, first);
+    if (!kSideWave<NT>) sums();
   };
   // The row's loads come first, so that they are in flight meanwhile, unless
   // they would take the registers the first wave needs for the teacher.
@@ -368,8 +385,8 @@ __global__ __launch_bounds__(kRowThreads<NT>, NT >= 512 ? 4 : 1) void distill_ro
     m = wave_max(m);
     if ((tid & 63) == 0) red[0][wv] = m;
   }
-  // The side wave's marks are needed only by the sums over the rest.
   __syncthreads();
+  if (kSideWave<NT> && teacher_wave) sums();  // beside the row's own
   m = red[0][0];
 #pragma unroll
   for (int q = 1; q < NT / 64; ++q) m = fmaxf(m, red[0][q]);
@@ -481,14 +498,12 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
   const uint32_t words = TAIL ? mark_words(true, (int64_t)(s.c1 - s.c0) * kVec<T>) : 0;
   const Lds l = lds_of(mem, a.K, words);
   Chunk<T> v[kBatch];
+  Entries entries;
   if (row_wave) {
     load_batch(r, s.c0 + tid, s.c1, v);
   } else {
     if (split == 0) {
-      const Teacher t = teacher<T, TAIL>(a, r, n, l, words, s.c0, s.c1, first_entry(a, n));
-      if ((tid & 63) == 0) a.teacher[n] = t;
-      if (a.saved)
-        for (int k = tid & 63; k < a.K; k += 64) a.saved[n * (4 + a.K) + 4 + k] = l.p[k];
+      entries = read_entries<T, TAIL>(a, r, n, l, words, s.c0, s.c1, first_entry(a, n));
     } else if (TAIL) {
       clear_marks(l.bits, words);
       for (int k = tid & 63; k < a.K; k += 64) {
@@ -499,6 +514,12 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
     }
   }
   if (TAIL) __syncthreads();
+  if (!row_wave && split == 0) {
+    const Teacher t = sum_entries<TAIL>(a, n, l, entries);
+    if ((tid & 63) == 0) a.teacher[n] = t;
+    if (a.saved)
+      for (int k = tid & 63; k < a.K; k += 64) a.saved[n * (4 + a.K) + 4 + k] = l.p[k];
+  }
   float m = kNegInf, rest = 0.0f, top = 0.0f;
   if (row_wave) {
     for (uint32_t j0 = s.c0 + tid; j0 < s.c1; j0 += kBatch * kPartThreads) {
