@@ -164,8 +164,8 @@ int per_scan_step(int64_t B, int64_t D, int32_t type, const void* d_x, int64_t x
  * per_distill_backward: the gradient from d_saved, weighted by d_gloss [N]
  *   f32, the gradient by each row's loss; d_grad may be d_logits.
  * per_distill_workspace_bytes: device workspace of per_distill and
- *   per_distill_forward, 16-byte aligned, scratch of one call.  per_distill
- *   needs none where a workgroup holds a whole row, and does not look at it.
+ *   per_distill_forward (0 for short rows), 16-byte aligned, scratch of one
+ *   call.  per_distill does not look at it where a workgroup holds a whole row.
  */
 int per_distill_workspace_bytes(int64_t N, int64_t V, int64_t K, int32_t type, size_t* out);
 int per_distill(int64_t N, int64_t V, int64_t K, int32_t type, const void* d_logits,

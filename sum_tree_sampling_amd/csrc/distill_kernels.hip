@@ -26,19 +26,27 @@ constexpr int kVec = 16 / (int)sizeof(T);
 
 __device__ __forceinline__ float ex2(float v) { return __builtin_amdgcn_exp2f(v); }
 
-__device__ __forceinline__ float wave_max(float v) {
+// Over a wave, or over its groups of 2^lg lanes (lg the same in every lane).
+__device__ __forceinline__ float wave_max(float v, int lg = 6) {
 #pragma unroll
-  for (int s = 0; s < 6; ++s) v = fmaxf(v, xor_lanes(v, s));
+  for (int s = 0; s < 6; ++s) {
+    if (s >= lg) break;
+    v = fmaxf(v, xor_lanes(v, s));
+  }
   return v;
+}
+__device__ __forceinline__ bool wave_any(bool b, int lg) {
+  return wave_max(b ? 1.0f : 0.0f, lg) != 0.0f;
 }
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int s = 0; s < 6; ++s) v += xor_lanes(v, s);
   return v;
 }
-__device__ __forceinline__ double wave_sum(double v) {
+__device__ __forceinline__ double wave_sum(double v, int lg = 6) {
 #pragma unroll
   for (int s = 0; s < 6; ++s) {
+    if (s >= lg) break;
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = __float_as_uint(xor_lanes(__uint_as_float((uint32_t)u), s));
     const uint32_t hi = __float_as_uint(xor_lanes(__uint_as_float((uint32_t)(u >> 32)), s));
@@ -146,16 +154,15 @@ __device__ __forceinline__ float teacher_logit(const DistillArgs& a, int64_t at)
   return (float)static_cast<const f16_t*>(a.t)[at];
 }
 
-// An entry of the lane: token and teacher's logit (or probability).  The first
-// one is loaded ahead of the row.
+// An entry of the lane: token and teacher's logit.  The first one is loaded
+// ahead of the row.
 struct Entry {
   int i;
   float t;
 };
-__device__ __forceinline__ Entry first_entry(const DistillArgs& a, int64_t n) {
-  const int k = threadIdx.x & 63;
+__device__ __forceinline__ Entry entry_at(const DistillArgs& a, int64_t n, int k) {
   Entry e = {-1, 0.0f};
-  if (k < a.K) {
+  if (k < a.K && n < a.N) {
     e.i = a.tidx[n * a.K + k];
     e.t = teacher_logit(a, n * a.K + k);
   }
@@ -176,32 +183,29 @@ __device__ __forceinline__ bool mark(uint32_t* bits, int i, int64_t lo, int64_t 
   return (atomicOr(&bits[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u;
 }
 
-// One whole wave: the entries to LDS, with the bitmap of chunks [c0, c1).  What
-// comes back is the lane's own share.
+// 2^lg lanes of a wave: the entries of a row to LDS, marked in its bitmap
+// (cleared before) over chunks [c0, c1).  What comes back is the lane's own share.
 struct Entries {
   float tm, z0;  // largest teacher's and student's logits of the entries present
   bool any, dup;
 };
 template <typename T, bool TAIL>
 __device__ __forceinline__ Entries read_entries(const DistillArgs& a, const Row<T>& r, int64_t n,
-                                                const Lds& l, uint32_t words, uint32_t c0,
-                                                uint32_t c1, Entry e) {
-  const int lane = threadIdx.x & 63;
-  clear_marks(l.bits, words);
+                                                const Lds& l, bool marks, uint32_t c0, uint32_t c1,
+                                                Entry e, int lg = 6) {
+  const int first = threadIdx.x & ((1 << lg) - 1);
   const int64_t lo = (int64_t)c0 * kVec<T> - r.mis;
   const int64_t hi = (int64_t)c1 * kVec<T> - r.mis;
   Entries o = {kNegInf, kNegInf, false, false};
-  for (int k = lane; k < a.K; k += 64) {
-    if (k != lane) {
-      e.i = a.tidx[n * a.K + k];
-      e.t = teacher_logit(a, n * a.K + k);
-    }
+  if (n >= a.N) return o;
+  for (int k = first; k < a.K; k += 1 << lg) {
+    if (k != first) e = entry_at(a, n, k);
     const int i = e.i < 0 || e.i >= (int64_t)r.V ? -1 : e.i;
     const float z = i >= 0 ? (float)r.z[i] : kNegInf;
     if (i >= 0) {
       o.any = true;
       o.tm = fmaxf(o.tm, e.t);
-      if (words) o.dup |= mark<TAIL>(l.bits, i, lo, hi);
+      if (marks) o.dup |= mark<TAIL>(l.bits, i, lo, hi);
     }
     l.idx[k] = i;
     l.p[k] = e.t;
@@ -211,21 +215,22 @@ __device__ __forceinline__ Entries read_entries(const DistillArgs& a, const Row<
   return o;
 }
 
-// The same wave: the probabilities to LDS, and the sums over the entries.  The
+// The same lanes: the probabilities to LDS, and the sums over the entries.  The
 // K exponentials are taken in f64: the rest 1 - sum p would lose its digits in
 // f32 where the top holds nearly everything.
 template <bool TAIL>
 __device__ __forceinline__ Teacher sum_entries(const DistillArgs& a, int64_t n, const Lds& l,
-                                               const Entries& e) {
-  const int lane = threadIdx.x & 63;
-  const float tm = wave_max(e.tm);
-  float z0 = wave_max(e.z0);
+                                               const Entries& e, int lg = 6) {
+  const int first = threadIdx.x & ((1 << lg) - 1);
+  const int K = n < a.N ? a.K : 0;
+  const float tm = wave_max(e.tm, lg);
+  float z0 = wave_max(e.z0, lg);
   if (z0 == kNegInf) z0 = 0.0f;
   // Without a rest: e = exp((t - largest) / tau), p = e / sum e.
   const double ref = TAIL || tm == kNegInf ? 0.0 : (double)tm;
-  const double norm = TAIL ? (double)a.tlse[n] : 0.0;
-  Teacher o = {0.0, 0.0, 0.0, 0.0, z0, false, false};
-  for (int k = lane; k < a.K; k += 64) {
+  const double norm = TAIL && n < a.N ? (double)a.tlse[n] : 0.0;
+  Teacher o = {0.0, 0.0, 0.0, 0.0, 1.0, z0, false, false};
+  for (int k = first; k < K; k += 1 << lg) {
     double p = 0.0;
     if (l.idx[k] >= 0) {
       const double lp = ((double)l.p[k] - ref) * a.inv_tau - norm;
@@ -239,40 +244,44 @@ __device__ __forceinline__ Teacher sum_entries(const DistillArgs& a, int64_t n, 
     }
     l.p[k] = (float)p;
   }
-  o.h = wave_sum(o.h);
-  o.ps = wave_sum(o.ps);
-  o.pz = wave_sum(o.pz);
-  o.any = __any(e.any) && o.ps != 0.0;  // entries at -Inf are none
-  o.dup = __any(e.dup);
+  o.h = wave_sum(o.h, lg);
+  o.ps = wave_sum(o.ps, lg);
+  o.pz = wave_sum(o.pz, lg);
+  o.any = wave_any(e.any, lg) && o.ps != 0.0;  // entries at -Inf are none
+  o.dup = wave_any(e.dup, lg);
   if (TAIL) {
     o.rest = 1.0 - o.ps;
     if (o.rest < 0.0) o.rest = 0.0;
   } else if (o.any) {
     const double inv = 1.0 / o.ps;
     const float scale = (float)inv;
-    for (int k = lane; k < a.K; k += 64) l.p[k] *= scale;
-    o.h = o.h * inv - log(o.ps);
+    for (int k = first; k < K; k += 1 << lg) l.p[k] *= scale;
+    o.h *= inv;
     o.pz *= inv;
+    o.norm = o.ps;
     o.ps = 1.0;
   }
   return o;
 }
 
-// The row's loss from the teacher's sums and the student's statistics.
+// The row's loss from the teacher's sums and the student's statistics:
+//   sum p (log p - log q) = h - log norm + ps log S - sum p (z - m) / tau
+// (norm = 1 with a rest, ps = 1 without one), and the rest's term.
 __device__ __forceinline__ float row_loss(const DistillArgs& a, const Teacher& t, float m, float S,
                                           float Sr, bool tail) {
-  const double logS = log((double)S);
+  const double logS = log((double)S / t.norm);
   double v = t.h + t.ps * logS;
   if (t.ps != 0.0) v -= (t.pz + t.ps * ((double)t.z0 - (double)m)) * a.inv_tau;
-  if (tail && t.rest > 0.0 && Sr != 0.0f) v += t.rest * (log(t.rest) - log((double)Sr) + logS);
+  if (tail && t.rest > 0.0 && Sr != 0.0f) v += t.rest * log(t.rest * (double)S / (double)Sr);
   return (float)(v * (double)a.tau * (double)a.tau);
 }
 
 // Puts right the gradient at the teacher's tokens within [lo, hi).
 template <typename T>
 __device__ __forceinline__ void patch_top(const DistillArgs& a, const Lds& l, T* grad, float m,
-                                          float S, float scale, bool dup, int64_t lo, int64_t hi) {
-  for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
+                                          float S, float scale, bool dup, int64_t lo, int64_t hi,
+                                          int first, int step) {
+  for (int k = first; k < a.K; k += step) {
     const int i = l.idx[k];
     if (i < 0 || i < lo || i >= hi) continue;
     float p = l.p[k];
@@ -335,7 +344,7 @@ __global__ __launch_bounds__(kRowThreads<NT>, NT >= 512 ? 4 : 1) void distill_ro
   const Row<T> r = row_of<T>(a, n);
   T* grad = static_cast<T*>(a.grad) + n * a.grad_stride;
   Entry first = {-1, 0.0f};
-  if (teacher_wave) first = first_entry(a, n);
+  if (teacher_wave) first = entry_at(a, n, tid & 63);
   const float w = a.weight ? a.weight[n] : 1.0f;
   if (w == 0.0f) {
     const float zero[kVec<T>] = {};
@@ -352,7 +361,8 @@ __global__ __launch_bounds__(kRowThreads<NT>, NT >= 512 ? 4 : 1) void distill_ro
   };
   auto read_teacher = [&] {
     if (!teacher_wave) return;
-    entries = read_entries<T, TAIL>(a, r, n, l, words, 0, r.chunks, first);
+    clear_marks(l.bits, words);
+    entries = read_entries<T, TAIL>(a, r, n, l, true, 0, r.chunks, first);
     if (!kSideWave<NT>) sums();
   };
   // The row's loads come first, so that they are in flight meanwhile, unless
@@ -441,14 +451,14 @@ __global__ __launch_bounds__(kRowThreads<NT>, NT >= 512 ? 4 : 1) void distill_ro
     if ((tid & 63) == 0) a.loss[n] = loss;
   }
   __syncthreads();
-  if (!dead) patch_top(a, l, grad, m, S, scale, t.dup, 0, (int64_t)r.V);
+  if (!dead) patch_top(a, l, grad, m, S, scale, t.dup, 0, (int64_t)r.V, tid, blockDim.x);
 }
 
 // ------------------------------------------------------ rows taken in parts
 //
 // 256 threads go over a part's chunks, one more wave takes the entries.
 constexpr int kPartThreads = 256;
-constexpr int kBatch = 4;  // chunks a thread loads at once
+constexpr int kBatch = 2;  // chunks a thread loads at once
 
 // Chunks [c0, c1) of the workgroup's part.
 struct Span {
@@ -503,7 +513,9 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
     load_batch(r, s.c0 + tid, s.c1, v);
   } else {
     if (split == 0) {
-      entries = read_entries<T, TAIL>(a, r, n, l, words, s.c0, s.c1, first_entry(a, n));
+      const Entry first = entry_at(a, n, tid & 63);
+      clear_marks(l.bits, words);
+      entries = read_entries<T, TAIL>(a, r, n, l, TAIL, s.c0, s.c1, first);
     } else if (TAIL) {
       clear_marks(l.bits, words);
       for (int k = tid & 63; k < a.K; k += 64) {
@@ -582,7 +594,7 @@ __global__ __launch_bounds__(64) void distill_join_kernel(DistillArgs a) {
   const int lane = threadIdx.x;
   const float* part = a.part + n * a.splits * 4;
   const bool off = a.weight && a.weight[n] == 0.0f;
-  Teacher t = {0.0, 0.0, 0.0, 0.0, 0.0f, false, false};
+  Teacher t = {0.0, 0.0, 0.0, 0.0, 1.0, 0.0f, false, false};
   if (!off) t = a.teacher[n];
   float m = kNegInf, rest = 0.0f, top = 0.0f;
   for (int q = lane; q < a.splits; q += 64) m = fmaxf(m, part[4 * q]);
@@ -676,7 +688,181 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_grad_kernel(Distill
     }
   }
   __syncthreads();
-  patch_top(a, l, grad, m, S, scale, sh_dup != 0, lo, hi);
+  patch_top(a, l, grad, m, S, scale, sh_dup != 0, lo, hi, tid, blockDim.x);
+}
+
+// ---------------------------------------------------------- one wave per row
+//
+// Rows of up to 256 chunks, four to a workgroup, each within one wave, which
+// needs no barrier for its maximum and sums.  A fifth wave reads the four
+// teachers at once, K entries of a row on the next power of two of lanes: the
+// f64 arithmetic of a row, spent by a whole wave on each, took longer than the
+// row itself (16384 x 500 bf16, K = 16: 27.6 us).
+enum Pass { kFused, kLoss, kGradient };
+constexpr int kWaveRows = 4;
+
+template <typename T, int R, bool TAIL, int PASS>
+__global__ __launch_bounds__(PASS == kGradient ? 64 * kWaveRows : 64 * (kWaveRows + 1))
+void distill_wave_kernel(DistillArgs a, uint32_t words) {
+  extern __shared__ char mem[];
+  __shared__ float stat[kWaveRows][3];
+  __shared__ Teacher teachers[kWaveRows];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * kWaveRows;
+  auto lds_row = [&](int q) {
+    return lds_of(mem + (size_t)q * 4 * (words + 3 * (size_t)((a.K + 3) / 4 * 4)), a.K, words);
+  };
+  if (PASS != kGradient && wv == kWaveRows) {  // the teachers
+    int lg = 0;
+    while (lg < 6 && (1 << lg) < a.K) ++lg;
+    const int per = 64 >> lg;  // rows at once
+    Entries e[kWaveRows];
+    Entry first[kWaveRows];
+#pragma unroll
+    for (int u = 0; u < kWaveRows; ++u) {
+      const int q = u * per + (lane >> lg);
+      if (u * per < kWaveRows)
+        first[u] = entry_at(a, q < kWaveRows ? n0 + q : a.N, lane & ((1 << lg) - 1));
+    }
+#pragma unroll
+    for (int q = 0; q < kWaveRows; ++q) clear_marks(lds_row(q).bits, words);
+#pragma unroll
+    for (int u = 0; u < kWaveRows; ++u) {
+      const int q = u * per + (lane >> lg);
+      if (u * per < kWaveRows) {
+        const int64_t n = q < kWaveRows ? n0 + q : a.N;
+        const Row<T> r = row_of<T>(a, n < a.N ? n : n0);
+        e[u] = read_entries<T, TAIL>(a, r, n, lds_row(q < kWaveRows ? q : 0), true, 0, r.chunks,
+                                     first[u], lg);
+      }
+    }
+    if (TAIL) __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kWaveRows; ++u) {
+      const int q = u * per + (lane >> lg);
+      if (u * per < kWaveRows) {
+        const int64_t n = q < kWaveRows ? n0 + q : a.N;
+        const Lds l = lds_row(q < kWaveRows ? q : 0);
+        const Teacher t = sum_entries<TAIL>(a, n, l, e[u], lg);
+        if (q < kWaveRows && (lane & ((1 << lg) - 1)) == 0) teachers[q] = t;
+        if (PASS == kLoss && a.saved && n < a.N)
+          for (int k = lane & ((1 << lg) - 1); k < a.K; k += 1 << lg)
+            a.saved[n * (4 + a.K) + 4 + k] = l.p[k];
+      }
+    }
+    __syncthreads();
+    const int64_t n = n0 + lane;
+    if (lane < kWaveRows && n < a.N) {
+      const float w = PASS == kFused && a.weight ? a.weight[n] : 1.0f;
+      const float m = stat[lane][0], S = stat[lane][1], Sr = stat[lane][2];
+      const Teacher t = teachers[lane];
+      const bool dead = w == 0.0f || S == 0.0f || (!TAIL && !t.any);
+      a.loss[n] = dead ? 0.0f : row_loss(a, t, m, S, Sr, TAIL);
+      if (PASS == kLoss && a.saved) {
+        float* s = a.saved + n * (4 + a.K);
+        s[0] = m;
+        s[1] = dead ? 0.0f : S;
+        s[2] = Sr;
+        s[3] = (float)t.rest;
+      }
+    }
+    return;
+  }
+
+  const int64_t n = n0 + wv;
+  const bool here = n < a.N;
+  const Row<T> r = row_of<T>(a, here ? n : n0);
+  const Lds l = lds_row(wv);
+  T* grad = static_cast<T*>(a.grad) + n * a.grad_stride;
+  const float w = !here ? 0.0f : PASS != kLoss && a.weight ? a.weight[n] : 1.0f;
+  Chunk<T> v[R];
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const uint32_t j = lane + q * 64;
+    if (w != 0.0f && j < r.chunks) {
+      v[q] = load_chunk(r, j);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kVec<T>; ++e) v[q].v[e] = (T)kNegInf;
+    }
+  }
+  float m, S, rest, p_rest = 0.0f;
+  bool dead, dup;
+  if (PASS == kGradient) {
+    const float* saved = a.saved + (here ? n : 0) * (4 + a.K);
+    m = saved[0];
+    S = saved[1];
+    rest = saved[2];
+    p_rest = saved[3];
+    dead = w == 0.0f || S == 0.0f;
+    dup = false;
+    clear_marks(l.bits, words);
+    for (int k = lane; k < a.K && !dead; k += 64) {
+      const Entry e = {a.tidx[n * a.K + k], saved[4 + k]};
+      const bool ok = e.i >= 0 && e.i < (int64_t)r.V;
+      l.idx[k] = ok ? e.i : -1;
+      l.p[k] = e.t;
+      if (ok) {
+        l.z[k] = (float)r.z[e.i];
+        dup |= mark<false>(l.bits, e.i, 0, (int64_t)r.V);
+      }
+    }
+    dup = __any(dup);
+  } else {
+    m = kNegInf;
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      float z[kVec<T>];
+      unpack(v[q], z);
+#pragma unroll
+      for (int e = 0; e < kVec<T>; ++e) m = fmaxf(m, z[e]);
+    }
+    m = wave_max(m);
+    if (m == kNegInf) m = 0.0f;
+    if (TAIL) __syncthreads();  // the marks
+    float top = 0.0f;
+    rest = 0.0f;
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const uint32_t j = lane + q * 64;
+      if (w != 0.0f && j < r.chunks)
+        add_chunk<T, TAIL>(v[q], m, a.c, TAIL ? chunk_bits<T>(l.bits, j) : 0u, rest, top);
+    }
+    rest = wave_sum(rest);
+    if (TAIL) top = wave_sum(top);
+    S = rest + top;
+    if (lane == 0) {
+      stat[wv][0] = m;
+      stat[wv][1] = S;
+      stat[wv][2] = rest;
+    }
+    __syncthreads();  // the teachers, whose logits are read before they may be overwritten
+    const Teacher t = teachers[wv];
+    dead = w == 0.0f || S == 0.0f || (!TAIL && !t.any);
+    dup = t.dup;
+    p_rest = (float)t.rest;
+  }
+  if (PASS != kLoss && here) {
+    const float scale = dead ? 0.0f : w * a.tau;
+    float coef = 0.0f;
+    if (!dead)
+      coef = TAIL ? (rest == 0.0f ? 0.0f
+                                  : scale * (__builtin_fmaf(-p_rest, S, rest) / (S * rest)))
+                  : scale / S;
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const uint32_t j = lane + q * 64;
+      if (j < r.chunks) {
+        float z[kVec<T>], g[kVec<T>];
+        unpack(v[q], z);
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e) g[e] = dead ? 0.0f : coef * ex2((z[e] - m) * a.c);
+        store_chunk(grad, r, j, g);
+      }
+    }
+    if (!dead) patch_top(a, l, grad, m, S, scale, dup, 0, (int64_t)r.V, lane, 64);
+  }
 }
 
 size_t lds_bytes(int K, bool tail, int64_t tokens) {
@@ -701,10 +887,28 @@ hipError_t row_launch(const DistillArgs& a, hipStream_t s) {
   return launch_kernel(distill_row_kernel<T, NT, R, false, ONCE>, grid, block, lds, s, a);
 }
 
+constexpr int64_t kWaveChunks = 256;
+
+template <typename T, int PASS, bool TAIL>
+hipError_t wave_launch(const DistillArgs& a, hipStream_t s) {
+  const int64_t chunks = (a.V + 2 * kVec<T> - 2) / kVec<T>;  // at most, for any alignment
+  const uint32_t words = mark_words(TAIL, chunks * kVec<T>);
+  const size_t lds = (size_t)kWaveRows * 4 * (words + 3 * (size_t)((a.K + 3) / 4 * 4));
+  const dim3 grid((uint32_t)((a.N + kWaveRows - 1) / kWaveRows));
+  const dim3 block(PASS == kGradient ? 64 * kWaveRows : 64 * (kWaveRows + 1));
+  if (chunks <= 64)
+    return launch_kernel(distill_wave_kernel<T, 1, TAIL, PASS>, grid, block, lds, s, a, words);
+  return launch_kernel(distill_wave_kernel<T, 4, TAIL, PASS>, grid, block, lds, s, a, words);
+}
+template <typename T, int PASS>
+hipError_t wave_typed(const DistillArgs& a, hipStream_t s) {
+  return a.tlse ? wave_launch<T, PASS, true>(a, s) : wave_launch<T, PASS, false>(a, s);
+}
+
 template <typename T>
 hipError_t row_typed(const DistillArgs& a, hipStream_t s) {
-  const int64_t chunks = (a.V + 2 * kVec<T> - 2) / kVec<T>;  // at most, for any alignment
-  if (chunks <= 64 * 4) return row_launch<T, 64, 4>(a, s);
+  const int64_t chunks = (a.V + 2 * kVec<T> - 2) / kVec<T>;
+  if (chunks <= kWaveChunks) return wave_typed<T, kFused>(a, s);
   if (chunks <= 256 * 4) return row_launch<T, 256, 4>(a, s);
   // Logits that fill half of the 256 MB Infinity Cache are loaded past it
   // (128 MB of bf16 logits at 32768 tokens: 70.5 -> 68.6 us, 1 GB at 65536: 468
@@ -719,6 +923,7 @@ hipError_t row_typed(const DistillArgs& a, hipStream_t s) {
 
 template <typename T>
 hipError_t stats_typed(const DistillArgs& a, int type, hipStream_t s) {
+  if (distill_small(a.V, type)) return wave_typed<T, kLoss>(a, s);
   const dim3 grid((uint32_t)(a.N * a.splits)), block(kPartThreads + 64);
   if (a.tlse) {
     const hipError_t e = launch_kernel(distill_part_kernel<T, true>, grid, block,
@@ -734,6 +939,7 @@ hipError_t stats_typed(const DistillArgs& a, int type, hipStream_t s) {
 
 template <typename T>
 hipError_t grad_typed(const DistillArgs& a, int type, hipStream_t s) {
+  if (distill_small(a.V, type)) return wave_typed<T, kGradient>(a, s);
   const dim3 grid((uint32_t)(a.N * a.splits)), block(kPartThreads + 64);
   const size_t lds = lds_bytes(a.K, false, part_tokens(a, type));
   return a.tlse ? launch_kernel(distill_grad_kernel<T, true>, grid, block, lds, s, a)
@@ -741,6 +947,11 @@ hipError_t grad_typed(const DistillArgs& a, int type, hipStream_t s) {
 }
 
 }  // namespace
+
+bool distill_small(int64_t V, int type) {
+  const int vec = 16 / elem_size(type);
+  return (V + 2 * vec - 2) / vec <= kWaveChunks;
+}
 
 bool distill_resident(int64_t N, int64_t V, int type) {
   const int vec = 16 / elem_size(type);
@@ -752,7 +963,7 @@ int distill_splits(int64_t N, int64_t V, int type) {
   const int vec = 16 / elem_size(type);
   const int64_t chunks = (V + 2 * vec - 2) / vec;
   const int64_t most = (chunks + kPartThreads * kBatch - 1) / (kPartThreads * kBatch);
-  int64_t n = (1024 + N - 1) / N;
+    int64_t n = (2048 + N - 1) / N;
   if (n > most) n = most;
   // the bitmap of a part lies in LDS
   const int64_t least = (V + (1 << 18) - 1) >> 18;

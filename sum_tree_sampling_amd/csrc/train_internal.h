@@ -74,6 +74,7 @@ struct Teacher {
   double ps;    // sum p
   double pz;    // sum p (z - z0)
   double rest;  // p_r
+  double norm;  // sum of exp((t - largest) / tau) without a rest, else 1
   float z0;     // largest student's logit at an entry
   bool any;     // an entry is present
   bool dup;     // two entries may name one token of the part
@@ -99,8 +100,10 @@ struct DistillArgs {
   Teacher* teacher;       // [N]
   int splits;
 };
-// Whether one workgroup holds a whole row in registers, and if not, how many
-// parts each row is split into.
+// Whether one wave holds a whole row (then no call needs a workspace), whether
+// one workgroup does in per_distill, and if not, how many parts each row is
+// split into.
+bool distill_small(int64_t V, int type);
 bool distill_resident(int64_t N, int64_t V, int type);
 int distill_splits(int64_t N, int64_t V, int type);
 hipError_t launch_distill_fused(const DistillArgs& a, int type, hipStream_t s);

@@ -188,7 +188,8 @@ def test_distill_refuses(call, kw):
     assert call("per_distill", *{**a, **kw}.values(), None) == EINVAL
 
 
-@pytest.mark.parametrize("kw", TOP_BAD + [dict(loss=None), dict(saved=P + 2), dict(ws=None), dict(ws=P + 4)])
+@pytest.mark.parametrize("kw", TOP_BAD + [dict(loss=None), dict(saved=P + 2),
+                                          dict(V=20000, stride=20000, ws=None), dict(V=20000, stride=20000, ws=P + 4)])
 def test_distill_forward_refuses(call, kw):
     a = dict(TOP, loss=P, saved=P, ws=P, ws_bytes=1 << 20)
     assert call("per_distill_forward", *{**a, **kw}.values(), None) == EINVAL
@@ -204,7 +205,7 @@ def test_distill_backward_refuses(call, kw):
 def test_distill_workspace(call):
     from sum_tree_sampling_amd import per_distill_workspace_bytes as need
     n = need(4, 200000, 8, 1)
-    assert n > 0 and need(0, 100, 8, 0) == 0
+    assert n > 0 and need(0, 20000, 8, 0) == 0 and need(4, 100, 8, 0) == 0
     a = dict(TOP, V=200000, stride=200000, loss=P, saved=P, ws=P, ws_bytes=15)
     assert call("per_distill_forward", *a.values(), None) == ENOSPC
     a = dict(TOP, V=200000, stride=200000, weight=None, loss=P, grad=2 * P, gs=200000, ws=P, ws_bytes=n - 1)

@@ -391,7 +391,7 @@ def check_distill(z, tidx, t, w, tlse, tau, in_place=True):
 
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("V,K", [(1, 1), (2, 2), (9, 3), (250, 8), (1000, 64), (2053, 65), (5000, 200), (9001, 1)])
+@pytest.mark.parametrize("V,K", [(1, 1), (2, 2), (9, 3), (250, 8), (600, 130), (1000, 64), (1000, 20), (2053, 65), (5000, 200), (9001, 1)])
 def test_distill_sizes(V, K, dtype, tail):
     say("distill", V, K, dtype, tail)
     tau = [1.0, 2.0, 0.7][(V + K) % 3]
