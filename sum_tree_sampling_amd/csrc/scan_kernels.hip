@@ -11,8 +11,12 @@
 // axis is cut into segments: a first kernel reduces each segment to its map,
 // and each workgroup of the second folds the maps of the segments before it.
 //
-// A reset makes its map ignore the state (a flag beside A = 0), so an infinite
-// or NaN state before it does not leak through 0 * Inf.
+// A reset makes its map ignore the state, so an infinite or NaN state before it
+// does not leak through 0 * Inf: such a map has A = -0, which no product of gates
+// is, and which stays -0 under further gates.
+//
+// Rows of few channels are packed: the lanes of a wave then take neighbouring
+// channels across sequences, and lengths and resets are each lane's own.
 
 #include <type_traits>
 
@@ -42,28 +46,43 @@ __device__ __forceinline__ void gate(float g, float& f, float& i) {
   i = e * f;
 }
 
-// Position of a workgroup: sequence, segment, first channel of the lane.
+// Position of a lane: sequence, segment, first channel.
 struct Place {
   int64_t b, d;
   int seg;
+  bool in;                 // the lane has channels
   int64_t t_begin, t_end;  // steps of the segment
   int64_t live;            // steps before min(t_end, length)
 };
 
-template <int C>
+template <int C, bool PACK>
 __device__ __forceinline__ Place place(const ScanArgs& a) {
-  const uint32_t nct = (uint32_t)((a.D + 64 * C - 1) / (64 * C));
-  uint32_t id = blockIdx.x;
+  static_assert(!PACK || C == 1, "packed lanes have one channel");
+  const int lane = threadIdx.x & 63;
+  const uint32_t id = blockIdx.x;
   Place p;
-  p.d = (int64_t)(id % nct) * (64 * C) + (threadIdx.x & 63) * C;
-  id /= nct;
-  p.seg = (int)(id % (uint32_t)a.nseg);
-  p.b = id / (uint32_t)a.nseg;
+  if (PACK) {
+    const uint64_t all = (uint64_t)a.B * (uint64_t)a.D;
+    const uint32_t tiles = (uint32_t)((all + 63) / 64);
+    p.seg = (int)(id / tiles);
+    const uint64_t e = (uint64_t)(id % tiles) * 64 + lane;
+    p.in = e < all;
+    p.b = p.in ? (int64_t)(e / (uint64_t)a.D) : 0;
+    p.d = p.in ? (int64_t)(e - (uint64_t)p.b * (uint64_t)a.D) : 0;
+  } else {
+    const uint32_t nct = (uint32_t)((a.D + 64 * C - 1) / (64 * C));
+    const uint32_t r = id / nct;
+    p.d = (int64_t)(id % nct) * (64 * C) + lane * C;
+    p.in = p.d < a.D;
+    p.seg = (int)(r % (uint32_t)a.nseg);
+    p.b = r / (uint32_t)a.nseg;
+  }
   int64_t len = a.T;
   if (a.length) {
     len = a.length[p.b];
     len = len < 0 ? 0 : len > a.T ? a.T : len;
   }
+  if (PACK && !p.in) len = 0;
   p.t_begin = (int64_t)p.seg * a.seg_steps;
   p.t_end = p.t_begin + a.seg_steps < a.T ? p.t_begin + a.seg_steps : a.T;
   p.live = len < p.t_end ? len : p.t_end;
@@ -77,20 +96,58 @@ __device__ __forceinline__ int steps_at(int64_t ts, int64_t live) {
   return n < 0 ? 0 : n > S ? S : (int)n;
 }
 
-// The lane's byte of the resets at step ts + lane, loaded a tile ahead (for the
-// first tile beside the sequence's length); reset_mask then has bit s where an
-// episode begins at ts + s, s < n, the same in every lane.
-template <int S>
-__device__ __forceinline__ uint8_t reset_byte(const uint8_t* reset, int64_t ts, int64_t T) {
-  const int lane = threadIdx.x & 63;
-  return reset && lane < S && ts >= 0 && ts + lane < T ? reset[ts + lane] : 0;
-}
-__device__ __forceinline__ uint32_t reset_mask(uint8_t byte, int n) {
-  return (uint32_t)__ballot(byte != 0) & ((1u << n) - 1);
+// Where episodes begin among the S steps from ts: bytes loaded a tile ahead (for
+// the first tile beside the sequence's length), then bit s for step ts + s < ts +
+// n.  One byte per lane where the lanes share a sequence, S where each has its own.
+template <int S, bool PACK>
+struct Begins {
+  uint32_t w[PACK ? S / 4 : 1];
+  __device__ __forceinline__ void load(const uint8_t* reset, int64_t ts, int64_t T) {
+#pragma unroll
+    for (int k = 0; k < (PACK ? S / 4 : 1); ++k) w[k] = 0;
+    if (!reset || ts < 0) return;
+    if constexpr (!PACK) {
+      const int lane = threadIdx.x & 63;
+      if (lane < S && ts + lane < T) w[0] = reset[ts + lane];
+    } else if (ts + S <= T) {
+      __builtin_memcpy(w, reset + ts, S);
+    } else {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if (ts + s < T) w[s / 4] |= (uint32_t)reset[ts + s] << (8 * (s & 3));
+    }
+  }
+  __device__ __forceinline__ uint32_t mask(int n) const {
+    uint32_t m = 0;
+    if constexpr (!PACK) {
+      m = (uint32_t)__ballot(w[0] != 0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < S / 4; ++k) {  // the top bit of each byte that is not 0, gathered
+        const uint32_t t = (((w[k] & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | w[k]) & 0x80808080u;
+        m |= (((t >> 7) * 0x10204080u) >> 28) << (4 * k);
+      }
+    }
+    return m & ((1u << n) - 1);
+  }
+};
+
+// Whether every lane has a whole tile without an episode's begin: nearly all of
+// a long sequence, and it goes without the per-step conditions.
+template <int S, bool PACK>
+__device__ __forceinline__ bool whole(int n, uint32_t mask) {
+  const bool w = n == S && mask == 0;
+  return PACK ? __all(w) : w;
 }
 
-// A [T x D] matrix of one sequence: the row's address is the same in every
-// lane, the lane's channel an offset from it.
+__device__ __forceinline__ bool ignores(float A) { return __float_as_uint(A) == 0x80000000u; }
+// The map (A, B) on a state.
+__device__ __forceinline__ float apply(float A, float B, float h) {
+  return ignores(A) ? B : __builtin_fmaf(A, h, B);
+}
+
+// A [T x D] matrix of one sequence.  Where the lanes share the sequence a row's
+// address is the same in all of them, the lane's channel an offset from it.
 template <typename T>
 struct Rows {
   T* p;
@@ -100,27 +157,28 @@ struct Rows {
 };
 
 // S rows of C channels from row ts.  Without FULL only the first n are
-// live: the others are loaded from the last of them and not used.
+// live: the others are loaded from the last of them (row 0 if there is none) and
+// not used.
 template <typename T, int C, bool FULL, int S>
 __device__ __forceinline__ void load_steps(const Rows<const T>& r, int64_t ts, int n,
                                            Pack<T, C> (&v)[S]) {
 #pragma unroll
   for (int s = 0; s < S; ++s)
-    v[s] = load_pack<T, C>(r.at(ts + (FULL || s < n ? s : n - 1)));
+    v[s] = load_pack<T, C>(r.at(FULL ? ts + s : n > 0 ? ts + (s < n ? s : n - 1) : 0));
 }
 
-template <typename T, int C>
+template <typename T, int C, bool PACK>
 __global__ __launch_bounds__(kWaves * 64, 4) void scan_forward_kernel(ScanArgs a) {
   constexpr int S = kForward;
   __shared__ float sA[2][kWaves][C][64], sB[2][kWaves][C][64];
-  __shared__ uint32_t sF[2][kWaves];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = blockDim.x >> 6;
-  const Place p = place<C>(a);
-  const bool in = p.d < a.D;
+  const Place p = place<C, PACK>(a);
+  const bool in = p.in;
   const uint8_t* reset = a.reset ? a.reset + p.b * a.T : nullptr;
-  uint8_t begins = reset_byte<S>(reset, p.t_begin + wv * S, a.T);
+  Begins<S, PACK> begins;
+  begins.load(reset, p.t_begin + wv * S, a.T);
   const uint32_t d32 = (uint32_t)p.d;
   const Rows<const T> x = {static_cast<const T*>(a.x) + p.b * a.x_sb, a.x_st, d32};
   const Rows<const T> g = {static_cast<const T*>(a.g) + p.b * a.g_sb, a.g_st, d32};
@@ -132,30 +190,23 @@ __global__ __launch_bounds__(kWaves * 64, 4) void scan_forward_kernel(ScanArgs a
   if (p.seg > 0) {  // fold the segments before this one: a run per wave, then the waves
     const int run = (p.seg + nw - 1) / nw;
     float A[C], B[C];
-    uint32_t flag = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
     for (int s = wv * run; s < (wv + 1) * run && s < p.seg; ++s) {
-      const int64_t at = p.b * a.nseg + s;
-      const uint32_t f = a.agg_flag[at];
-      const float* m = a.agg + at * 2 * a.D + p.d;
+      const float* m = a.agg + (p.b * a.nseg + s) * 2 * a.D + p.d;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const float sa = in ? m[c] : 0.0f, sb = in ? m[a.D + c] : 0.0f;
-        B[c] = f ? sb : __builtin_fmaf(sa, B[c], sb);
-        A[c] *= sa;
+        B[c] = apply(sa, sb, B[c]);
+        A[c] = ignores(sa) ? sa : A[c] * sa;
       }
-      flag |= f;
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) sA[1][wv][c][lane] = A[c], sB[1][wv][c][lane] = B[c];
-    if (lane == 0) sF[1][wv] = flag;
     __syncthreads();
     for (int w = 0; w < nw; ++w) {
-      const bool f = sF[1][w] != 0;
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        h[c] = f ? sB[1][w][c][lane] : __builtin_fmaf(sA[1][w][c][lane], h[c], sB[1][w][c][lane]);
+      for (int c = 0; c < C; ++c) h[c] = apply(sA[1][w][c][lane], sB[1][w][c][lane], h[c]);
     }
   }
 
@@ -163,15 +214,13 @@ __global__ __launch_bounds__(kWaves * 64, 4) void scan_forward_kernel(ScanArgs a
   for (int64_t t0 = p.t_begin; t0 < p.t_end; t0 += nw * S, buf ^= 1) {
     const int64_t ts = t0 + wv * S;
     const int n = steps_at<S>(ts, p.live);
-    const uint32_t mask = reset_mask(begins, n);
-    begins = reset_byte<S>(reset, ts + nw * S, a.T);
+    const uint32_t mask = begins.mask(n);
+    begins.load(reset, ts + nw * S, a.T);
     float f[S][C], ix[S][C];
     float A[C], B[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
-    // Whole tiles without an episode's begin, nearly all of a long sequence,
-    // go without the per-step conditions.
-    const bool full = n == S && mask == 0;
+    const bool full = whole<S, PACK>(n, mask);
     auto reduce = [&](auto is_full) {
       constexpr bool FULL = decltype(is_full)::value;
       Pack<T, C> px[S], pg[S];
@@ -190,27 +239,24 @@ __global__ __launch_bounds__(kWaves * 64, 4) void scan_forward_kernel(ScanArgs a
           ix[s][c] = i * xv[c];
           if (FULL || s < n) {
             B[c] = r ? ix[s][c] : __builtin_fmaf(f[s][c], B[c], ix[s][c]);
-            A[c] = r ? 0.0f : A[c] * f[s][c];
+            A[c] = r ? -0.0f : A[c] * f[s][c];
           }
         }
       }
     };
-    if (in && full) reduce(std::true_type{});
-    else if (in && n > 0) reduce(std::false_type{});
+    if ((PACK || in) && full) reduce(std::true_type{});
+    else if (PACK ? __any(n > 0) : in && n > 0) reduce(std::false_type{});
 #pragma unroll
     for (int c = 0; c < C; ++c) sA[buf][wv][c][lane] = A[c], sB[buf][wv][c][lane] = B[c];
-    if (lane == 0) sF[buf][wv] = mask;
     __syncthreads();
     float hs[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) hs[c] = h[c];
     for (int w = 0; w < nw; ++w) {
-      const bool fl = sF[buf][w] != 0;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         if (w == wv) hs[c] = h[c];
-        const float wb = sB[buf][w][c][lane];
-        h[c] = fl ? wb : __builtin_fmaf(sA[buf][w][c][lane], h[c], wb);
+        h[c] = apply(sA[buf][w][c][lane], sB[buf][w][c][lane], h[c]);
       }
     }
     if (a.carries && in && ts % kChunk == 0 && ts < p.t_end) {
@@ -249,15 +295,14 @@ __global__ __launch_bounds__(kWaves * 64, 4) void scan_forward_kernel(ScanArgs a
 
 // The map of one segment: forward h -> A h + B, or (REV) of the gradient that
 // flows back through it, E -> A E + B.  Waves take runs of whole tiles.
-template <typename T, int C, bool REV>
-__global__ __launch_bounds__(kWaves * 64) void scan_segment_kernel(ScanArgs a) {
-  constexpr int S = kForward;
+template <typename T, int C, bool PACK, bool REV>
+__global__ __launch_bounds__(kWaves * 64, 4) void scan_segment_kernel(ScanArgs a) {
+  constexpr int S = PACK ? kForward / 2 : kForward;  // packed lanes hold an address each
   __shared__ float sA[kWaves][C][64], sB[kWaves][C][64];
-  __shared__ uint32_t sF[kWaves];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Place p = place<C>(a);
-  const bool in = p.d < a.D;
+  const Place p = place<C, PACK>(a);
+  const bool in = p.in;
   const uint32_t d32 = (uint32_t)p.d;
   const Rows<const T> v =
       REV ? Rows<const T>{static_cast<const T*>(a.dy) + p.b * a.dy_sb, a.dy_st, d32}
@@ -266,16 +311,16 @@ __global__ __launch_bounds__(kWaves * 64) void scan_segment_kernel(ScanArgs a) {
   const uint8_t* reset = a.reset ? a.reset + p.b * a.T : nullptr;
   const int64_t run = a.seg_steps / kWaves;  // a multiple of S
   float A[C], B[C];
-  uint32_t flag = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
   for (int64_t k = 0; k < run; k += S) {
     const int64_t ts = p.t_begin + wv * run + (REV ? run - S - k : k);
     const int n = steps_at<S>(ts, p.live);
-    if (n == 0) continue;
-    const uint32_t mask = reset_mask(reset_byte<S>(reset, ts, a.T), n);
-    flag |= mask;
-    if (!in) continue;
+    if (PACK ? !__any(n > 0) : n == 0) continue;
+    Begins<S, PACK> begins;
+    begins.load(reset, ts, a.T);
+    const uint32_t mask = begins.mask(n);
+    if (!PACK && !in) continue;
     auto reduce = [&](auto is_full) {
       constexpr bool FULL = decltype(is_full)::value;
       Pack<T, C> pv[S], pg[S];
@@ -299,39 +344,34 @@ __global__ __launch_bounds__(kWaves * 64) void scan_segment_kernel(ScanArgs a) {
             const float b = i * vv[c];
             B[c] = r ? b : __builtin_fmaf(f, B[c], b);
           }
-          A[c] = r ? 0.0f : A[c] * f;
+          A[c] = r ? -0.0f : A[c] * f;
         }
       }
     };
-    if (n == S && mask == 0) reduce(std::true_type{});
+    if (whole<S, PACK>(n, mask)) reduce(std::true_type{});
     else reduce(std::false_type{});
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) sA[wv][c][lane] = A[c], sB[wv][c][lane] = B[c];
-  if (lane == 0) sF[wv] = flag;
   __syncthreads();
   if (wv != 0) return;
-  uint32_t any = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
 #pragma unroll
   for (int q = 0; q < kWaves; ++q) {
     const int w = REV ? kWaves - 1 - q : q;
-    const bool fl = sF[w] != 0;
-    any |= sF[w];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      B[c] = fl ? sB[w][c][lane] : __builtin_fmaf(sA[w][c][lane], B[c], sB[w][c][lane]);
-      A[c] *= sA[w][c][lane];
+      const float wa = sA[w][c][lane];
+      B[c] = apply(wa, sB[w][c][lane], B[c]);
+      A[c] = ignores(wa) ? wa : A[c] * wa;
     }
   }
-  const int64_t at = p.b * a.nseg + p.seg;
   if (in) {
-    float* m = a.agg + at * 2 * a.D + p.d;
+    float* m = a.agg + (p.b * a.nseg + p.seg) * 2 * a.D + p.d;
 #pragma unroll
     for (int c = 0; c < C; ++c) m[c] = A[c], m[a.D + c] = B[c];
   }
-  if (p.d == 0) a.agg_flag[at] = any;
   if (!REV && a.h0 && p.seg == 0 && in) {
 #pragma unroll
     for (int c = 0; c < C; ++c) a.h0_copy[p.b * a.D + p.d + c] = a.h0[p.b * a.D + p.d + c];
@@ -342,16 +382,15 @@ __global__ __launch_bounds__(kWaves * 64) void scan_segment_kernel(ScanArgs a) {
 // step t (0 where an episode begins at t); full_t = E_{t+1} + dy_t that of h_t:
 //   dx = full (1 - f),  dg = full (h' - x) f (1 - f).
 // The states of a chunk are computed again from its carry.
-template <typename T, int C>
+template <typename T, int C, bool PACK>
 __global__ __launch_bounds__(64 * kBackWaves, 4) void scan_backward_kernel(ScanArgs a) {
   constexpr int S = kBackward;
   __shared__ float sA[2][kBackWaves][C][64], sB[2][kBackWaves][C][64], sQ[2][kBackWaves][C][64];
-  __shared__ uint32_t sF[2][kBackWaves];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = blockDim.x >> 6;
-  const Place p = place<C>(a);
-  const bool in = p.d < a.D;
+  const Place p = place<C, PACK>(a);
+  const bool in = p.in;
   const uint32_t d32 = (uint32_t)p.d;
   const Rows<const T> x = {static_cast<const T*>(a.x) + p.b * a.x_sb, a.x_st, d32};
   const Rows<const T> g = {static_cast<const T*>(a.g) + p.b * a.g_sb, a.g_st, d32};
@@ -367,39 +406,33 @@ __global__ __launch_bounds__(64 * kBackWaves, 4) void scan_backward_kernel(ScanA
     const int later = a.nseg - 1 - p.seg;
     const int run = (later + nw - 1) / nw;
     float A[C], B[C];
-    uint32_t flag = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) A[c] = 1.0f, B[c] = 0.0f;
     // wave nw - 1 takes the last segments, each run from its end
     int hi = p.seg + 1 + (wv + 1) * run;
     if (hi > a.nseg) hi = a.nseg;
     for (int s = hi - 1; s >= p.seg + 1 + wv * run; --s) {
-      const int64_t at = p.b * a.nseg + s;
-      const uint32_t f = a.agg_flag[at];
-      const float* m = a.agg + at * 2 * a.D + p.d;
+      const float* m = a.agg + (p.b * a.nseg + s) * 2 * a.D + p.d;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const float sa = in ? m[c] : 0.0f, sb = in ? m[a.D + c] : 0.0f;
-        B[c] = f ? sb : __builtin_fmaf(sa, B[c], sb);
-        A[c] *= sa;
+        B[c] = apply(sa, sb, B[c]);
+        A[c] = ignores(sa) ? sa : A[c] * sa;
       }
-      flag |= f;
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) sA[1][wv][c][lane] = A[c], sB[1][wv][c][lane] = B[c];
-    if (lane == 0) sF[1][wv] = flag;
     __syncthreads();
     for (int w = nw - 1; w >= 0; --w) {
-      const bool f = sF[1][w] != 0;
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        E[c] = f ? sB[1][w][c][lane] : __builtin_fmaf(sA[1][w][c][lane], E[c], sB[1][w][c][lane]);
+      for (int c = 0; c < C; ++c) E[c] = apply(sA[1][w][c][lane], sB[1][w][c][lane], E[c]);
     }
   }
 
   const int64_t tile = nw * S;
   const int64_t tiles = p.t_end > p.t_begin ? (p.t_end - p.t_begin + tile - 1) / tile : 0;
-  uint8_t begins = reset_byte<S>(reset, p.t_begin + (tiles - 1) * tile + wv * S, a.T);
+  Begins<S, PACK> begins;
+  begins.load(reset, p.t_begin + (tiles - 1) * tile + wv * S, a.T);
   float Eo[C];  // what flows out of the wave's own steps, run one by one
 #pragma unroll
   for (int c = 0; c < C; ++c) Eo[c] = E[c];
@@ -408,8 +441,8 @@ __global__ __launch_bounds__(64 * kBackWaves, 4) void scan_backward_kernel(ScanA
     const int64_t t0 = p.t_begin + k * tile;
     const int64_t ts = t0 + wv * S;
     const int n = steps_at<S>(ts, p.live);
-    const uint32_t mask = reset_mask(begins, n);
-    begins = reset_byte<S>(reset, ts - tile, a.T);
+    const uint32_t mask = begins.mask(n);
+    begins.load(reset, ts - tile, a.T);
     float f[S][C], i[S][C];
     Pack<T, C> px[S], pd[S];
     float h[C], A[C], B[C], Q[C];
@@ -420,7 +453,7 @@ __global__ __launch_bounds__(64 * kBackWaves, 4) void scan_backward_kernel(ScanA
       h[c] = in ? a.carries[(p.b * ((a.T + kChunk - 1) / kChunk) + t0 / kChunk) * a.D + p.d + c]
                 : 0.0f;
     }
-    const bool full = n == S && mask == 0;
+    const bool full = whole<S, PACK>(n, mask);
     auto reduce = [&](auto is_full) {
       constexpr bool FULL = decltype(is_full)::value;
       Pack<T, C> pg[S];
@@ -439,7 +472,7 @@ __global__ __launch_bounds__(64 * kBackWaves, 4) void scan_backward_kernel(ScanA
           if (FULL || s < n) {
             const float b = i[s][c] * xv[c];
             B[c] = r ? b : __builtin_fmaf(f[s][c], B[c], b);
-            A[c] = r ? 0.0f : A[c] * f[s][c];
+            A[c] = r ? -0.0f : A[c] * f[s][c];
           }
         }
       }
@@ -453,33 +486,27 @@ __global__ __launch_bounds__(64 * kBackWaves, 4) void scan_backward_kernel(ScanA
         for (int c = 0; c < C; ++c) Q[c] = r ? 0.0f : f[s][c] * (Q[c] + dv[c]);
       }
     };
-    if (in && full) reduce(std::true_type{});
-    else if (in && n > 0) reduce(std::false_type{});
+    if ((PACK || in) && full) reduce(std::true_type{});
+    else if (PACK ? __any(n > 0) : in && n > 0) reduce(std::false_type{});
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       sA[buf][wv][c][lane] = A[c];
       sB[buf][wv][c][lane] = B[c];
       sQ[buf][wv][c][lane] = Q[c];
     }
-    if (lane == 0) sF[buf][wv] = mask;
     __syncthreads();
     for (int w = 0; w < wv; ++w) {
-      const bool fl = sF[buf][w] != 0;
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        h[c] = fl ? sB[buf][w][c][lane]
-                  : __builtin_fmaf(sA[buf][w][c][lane], h[c], sB[buf][w][c][lane]);
+      for (int c = 0; c < C; ++c) h[c] = apply(sA[buf][w][c][lane], sB[buf][w][c][lane], h[c]);
     }
     float Es[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) Es[c] = E[c];
     for (int w = nw - 1; w >= 0; --w) {
-      const bool fl = sF[buf][w] != 0;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         if (w == wv) Es[c] = E[c];
-        const float q = sQ[buf][w][c][lane];
-        E[c] = fl ? q : __builtin_fmaf(sA[buf][w][c][lane], E[c], q);
+        E[c] = apply(sA[buf][w][c][lane], sQ[buf][w][c][lane], E[c]);
       }
     }
     auto finish = [&](auto is_full) {
@@ -558,33 +585,33 @@ __global__ __launch_bounds__(256) void scan_step_kernel(StepArgs a, int lg) {
   }
 }
 
-template <typename T, int C>
+template <typename T, int C, bool PACK = false>
 hipError_t forward_typed(ScanArgs a, uint32_t blocks, int waves, hipStream_t s) {
   if (a.nseg > 1) {
-    const hipError_t e = launch_kernel(scan_segment_kernel<T, C, false>, dim3(blocks),
+    const hipError_t e = launch_kernel(scan_segment_kernel<T, C, PACK, false>, dim3(blocks),
                                        dim3(kWaves * 64), 0, s, a);
     if (e != hipSuccess) return e;
     // The last segment's workgroup may write h_last = h0 before others start.
     if (a.h0) a.h0 = a.h0_copy;
   }
-  return launch_kernel(scan_forward_kernel<T, C>, dim3(blocks), dim3(64 * waves), 0, s, a);
+  return launch_kernel(scan_forward_kernel<T, C, PACK>, dim3(blocks), dim3(64 * waves), 0, s, a);
 }
 
-template <typename T, int C>
+template <typename T, int C, bool PACK = false>
 hipError_t backward_typed(const ScanArgs& a, uint32_t blocks, int waves, hipStream_t s) {
   if (a.nseg > 1) {
-    const hipError_t e = launch_kernel(scan_segment_kernel<T, C, true>, dim3(blocks),
+    const hipError_t e = launch_kernel(scan_segment_kernel<T, C, PACK, true>, dim3(blocks),
                                        dim3(kWaves * 64), 0, s, a);
     if (e != hipSuccess) return e;
   }
-  return launch_kernel(scan_backward_kernel<T, C>, dim3(blocks), dim3(64 * waves), 0, s, a);
+  return launch_kernel(scan_backward_kernel<T, C, PACK>, dim3(blocks), dim3(64 * waves), 0, s, a);
 }
 
 // Waves of a workgroup: as many as the sequence has steps for, up to 8.  The
 // backward pass takes up to 128 steps in one tile of 16 waves where there are
-// too few workgroups for two to a CU anyway (37 x 81 x 333 f32: 10.7 -> 9.0 us;
-// with 2048 workgroups, 256 x 128 x 1024 bf16, one such workgroup to a CU would
-// leave loads and stores unoverlapped).
+// too few workgroups for two to a CU anyway (37 x 81 x 333 f32, both passes:
+// 15.5 -> 14.2 us); with 2048 workgroups (256 x 128 x 1024 bf16) one such
+// workgroup to a CU leaves loads and stores unoverlapped: 109 us become 116.
 int forward_waves(int64_t T) {
   const int64_t w = (T + kForward - 1) / kForward;
   return w < 1 ? 1 : w > kWaves ? kWaves : (int)w;
@@ -595,18 +622,22 @@ int backward_waves(int64_t T, uint32_t blocks) {
   return w <= kBackWaves && blocks < 512 ? (int)w : kWaves;
 }
 
-// How a batch is spread over the chip: channels per lane, segments of the time
-// axis, steps of a segment (a multiple of kSegment).
+// How a batch is spread over the chip: channels per lane, packed lanes, segments
+// of the time axis and their steps (a multiple of kSegment).  Times below are
+// forward and backward together, bf16 unless said.
 //
-// The time axis is cut where there are fewer than 192 workgroups without it: a
-// cut costs a second reading of two of the tensors (24 x 300 x 1000 bf16, 192
-// workgroups: 67 us cut, 48 not; 16 x 512 x 1024, 128: 55 and 61).  Two channels
-// per lane are faster once the chip is full (128 x 512 x 1024: 231 against
-// 247 us; 2 x 16384 x 512: 89 against 101) and one below (4 x 512 x 256: 32
-// against 39; 32 x 80 x 512: 14.3 against 15.8), or where it saves the cut (16 x
-// 512 x 1024: 49 against 55).  Forward and backward together.
+// The time axis is cut where fewer than 192 workgroups would walk it: a cut
+// reads two of the tensors again (24 x 300 x 1000, 192 workgroups: 61 us cut, 41
+// not), and without one a few workgroups cannot carry the load (2 x 16384 x 512,
+// 8 of them).  Two channels per lane make better use of loads once the chip is
+// full (128 x 512 x 1024: 234 against 241 us; 2 x 16384 x 512: 86 against 97),
+// one below (4 x 512 x 256: 28 against 32; 32 x 80 x 512: 12.7 against 14.6), or
+// where it saves the cut (16 x 512 x 1024: 42 against 50).  Lanes are packed
+// where several sequences share a wave evenly or at least four do (4096 x 128 x
+// 8: 36 against 81 us, x 32: 79 against 97; x 40: 114 against 98, since a packed
+// lane has its own addresses and row ends inside a wave).
 struct Plan {
-  bool two;
+  bool two, packed;
   int64_t blocks;  // without the cut
   int n;
   int64_t steps;
@@ -615,7 +646,9 @@ constexpr int64_t kFull = 192;
 
 Plan plan_with(int64_t B, int64_t T, int64_t D, bool two) {
   const int64_t w = two ? 128 : 64;
-  Plan p = {two, B * ((D + w - 1) / w), 1, T};
+  Plan p = {two, false, B * ((D + w - 1) / w), 1, T};
+  p.packed = D <= 16 || D == 32;
+  if (p.packed) p.blocks = (B * D + 63) / 64;
   const int64_t chunks = (T + kSegment - 1) / kSegment;
   if (p.blocks >= kFull || chunks < 2) return p;
   int64_t n = (512 + p.blocks - 1) / p.blocks;
@@ -633,14 +666,25 @@ Plan plan(int64_t B, int64_t T, int64_t D) {
   return two;
 }
 
+template <typename T>
+hipError_t forward_of(const Plan& p, const ScanArgs& a, uint32_t blocks, int waves, hipStream_t s) {
+  return p.packed ? forward_typed<T, 1, true>(a, blocks, waves, s)
+         : p.two  ? forward_typed<T, 2>(a, blocks, waves, s)
+                  : forward_typed<T, 1>(a, blocks, waves, s);
+}
+template <typename T>
+hipError_t backward_of(const Plan& p, const ScanArgs& a, uint32_t blocks, int waves,
+                       hipStream_t s) {
+  return p.packed ? backward_typed<T, 1, true>(a, blocks, waves, s)
+         : p.two  ? backward_typed<T, 2>(a, blocks, waves, s)
+                  : backward_typed<T, 1>(a, blocks, waves, s);
+}
+
 Plan set_plan(ScanArgs& a) {
   const Plan p = plan(a.B, a.T, a.D);
   a.nseg = p.n;
   a.seg_steps = p.steps;
-  if (p.n > 1) {
-    a.h0_copy = a.agg + a.B * p.n * 2 * a.D;
-    a.agg_flag = reinterpret_cast<uint32_t*>(a.h0_copy + a.B * a.D);
-  }
+  if (p.n > 1) a.h0_copy = a.agg + a.B * p.n * 2 * a.D;
   return p;
 }
 
@@ -653,37 +697,29 @@ int64_t scan_blocks(int64_t B, int64_t T, int64_t D) {
 
 size_t scan_workspace(int64_t B, int64_t T, int64_t D) {
   const int n = plan(B, T, D).n;
-  return n == 1 ? 0 : (size_t)(B * n * 2 * D + B * D + B * n) * 4;
+  return n == 1 ? 0 : (size_t)(B * n * 2 * D + B * D) * 4;
 }
 
 hipError_t launch_scan_forward(ScanArgs a, int type, hipStream_t s) {
   const Plan p = set_plan(a);
   const uint32_t blocks = (uint32_t)(p.blocks * p.n);
   const int waves = forward_waves(a.T);
-  const bool two = p.two;
   if (type == 0)
-    return two ? forward_typed<float, 2>(a, blocks, waves, s)
-               : forward_typed<float, 1>(a, blocks, waves, s);
+    return forward_of<float>(p, a, blocks, waves, s);
   if (type == 1)
-    return two ? forward_typed<bf16_t, 2>(a, blocks, waves, s)
-               : forward_typed<bf16_t, 1>(a, blocks, waves, s);
-  return two ? forward_typed<f16_t, 2>(a, blocks, waves, s)
-             : forward_typed<f16_t, 1>(a, blocks, waves, s);
+    return forward_of<bf16_t>(p, a, blocks, waves, s);
+  return forward_of<f16_t>(p, a, blocks, waves, s);
 }
 
 hipError_t launch_scan_backward(ScanArgs a, int type, hipStream_t s) {
   const Plan p = set_plan(a);
   const uint32_t blocks = (uint32_t)(p.blocks * p.n);
   const int waves = backward_waves(a.T, blocks);
-  const bool two = p.two;
   if (type == 0)
-    return two ? backward_typed<float, 2>(a, blocks, waves, s)
-               : backward_typed<float, 1>(a, blocks, waves, s);
+    return backward_of<float>(p, a, blocks, waves, s);
   if (type == 1)
-    return two ? backward_typed<bf16_t, 2>(a, blocks, waves, s)
-               : backward_typed<bf16_t, 1>(a, blocks, waves, s);
-  return two ? backward_typed<f16_t, 2>(a, blocks, waves, s)
-             : backward_typed<f16_t, 1>(a, blocks, waves, s);
+    return backward_of<bf16_t>(p, a, blocks, waves, s);
+  return backward_of<f16_t>(p, a, blocks, waves, s);
 }
 
 template <typename T, int C>

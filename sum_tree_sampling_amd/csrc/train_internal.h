@@ -45,7 +45,6 @@ struct ScanArgs {
   float* dh0;
   float* agg;             // [B x nseg x 2 x D] maps (A, B) of the segments
   float* h0_copy;         // [B x D] h0 as the first kernel found it (h_last may be h0)
-  uint32_t* agg_flag;     // [B x nseg] whether a reset lies in the segment
   int64_t seg_steps;      // steps of a segment (a multiple of the chunk; T if nseg == 1)
   int nseg;
 };
