@@ -3,7 +3,9 @@
 //
 // A lane holds 8 neighbouring columns (a unit: one 16-byte load of a 16-bit
 // type, 8 bytes of codes); a group of 32, 64 or 128 columns is 4, 8 or 16
-// neighbouring lanes, so its largest magnitude is found by lane exchanges.
+// neighbouring lanes, so its largest magnitude is found by lane exchanges.  Each
+// row is read and written once; what bounds the large calls is HBM, the small
+// ones (400 rows of 64: 2.9 us) the launch.
 
 #include "elem.h"
 #include "lanes.h"
@@ -126,6 +128,10 @@ __device__ __forceinline__ int64_t slot_of(const RowsArgs& a, uint32_t j, bool* 
 // 2^lg lanes per row, U units per lane and step.  ROW: one scale for the row,
 // whose units all lie in one step; else groups of 2^lg_group lanes.  Steps
 // beyond the first are taken by blockIdx.y (ring writes) or by a loop.
+//
+// x / scale is taken as x * (1 / scale), one division per group instead of one
+// per value: at 3 bytes moved a value, ten more instructions would show.
+// 65536 rows of 2048 bf16, groups of 128: 75 us, 5.4 TB/s (a large copy: 4.8).
 template <typename T, int FMT, int U, bool ROW>
 __global__ __launch_bounds__(kThreads) void rows_write_kernel(RowsArgs a, int lg) {
   const uint32_t lane = threadIdx.x & ((1u << lg) - 1);
@@ -278,6 +284,11 @@ __device__ __forceinline__ void decode(uint2 w, float scale, float (&x)[8]) {
 }
 
 // 2^lg lanes per output row, U units per lane, blockIdx.y over column steps.
+//
+// 512 sequences of 80 rows of 1024 to bf16: 26.5 us, 4.8 TB/s, the rate of a large
+// copy.  Stores past the caches take 16.5 us alone, but what reads the rows next
+// then finds none of them: with the recurrence behind it 42.4 us become 44.9, and
+// at twice the sequences 77 become 93.
 template <typename T, int FMT, int U>
 __global__ __launch_bounds__(kThreads) void rows_read_kernel(RowsArgs a, int lg) {
   const uint32_t lane = threadIdx.x & ((1u << lg) - 1);

@@ -11,6 +11,13 @@
 // axis is cut into segments: a first kernel reduces each segment to its map,
 // and each workgroup of the second folds the maps of the segments before it.
 //
+// 128 x 512 x 1024 bf16: forward 80 us (5.0 TB/s), backward 158 us (4.3 TB/s),
+// bound by HBM with the vector units half busy.  2 x 16384 x 512, cut into 64
+// segments: 16 + 21 us forward, 16 + 31 backward, the maps' reading of two tensors
+// being what the cut costs.  Handing maps and states from tile to tile within one
+// launch instead (tickets and polled words) reads everything once, but 512
+// workgroups then load, wait and store in step: 44 and 69 us.
+//
 // A reset makes its map ignore the state, so an infinite or NaN state before it
 // does not leak through 0 * Inf: such a map has A = -0, which no product of gates
 // is, and which stays -0 under further gates.
