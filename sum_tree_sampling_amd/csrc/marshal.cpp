@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -147,6 +148,15 @@ struct Where {
     return at::empty(shape, at::TensorOptions().dtype(dtype).device(at::kCUDA, device));
   }
 };
+
+// Nothing here is recorded for autograd: a call that would silently cut a graph is
+// refused (inside an autograd.Function, and under no_grad, recording is off).
+void unrecorded(const Args& a, int i) {
+  if (a.v[i] && at::GradMode::is_enabled() && a.tensor(i).requires_grad())
+    refuse(std::string(a.names[i]) +
+           " requires grad: call this under torch.no_grad() or from an autograd.Function; its "
+           "gradients come from explicit calls");
+}
 
 std::string text(at::IntArrayRef s) {
   std::string t = "(";
@@ -353,6 +363,7 @@ Sequences sequences(const Args& a, const Where& w) {
 // x, g, reset, length, h0, y, h_last, carries, stream
 PyObject* scan_forward(const Args& a) {
   const Where w(a.v[8], a.tensor(0), "x");
+  for (int i : {0, 1, 4}) unrecorded(a, i);
   const Sequences s = sequences(a, w);
   const int64_t all[] = {s.B, s.T, s.D}, state[] = {s.B, s.D}, carry[] = {s.B, s.chunks, s.D};
   const uint8_t* reset = flags(a, 2, {s.B, s.T}, w);
@@ -400,6 +411,7 @@ PyObject* scan_backward(const Args& a) {
 PyObject* scan_step(const Args& a) {
   const Tensor& x = a.tensor(0);
   const Where w(a.v[6], x, "x");
+  for (int i : {0, 1, 2}) unrecorded(a, i);
   if (x.dim() != 2) refuse("x must be [B x D]");
   const int type = type_of(x, "x");
   const auto dt = x.scalar_type();
@@ -462,6 +474,7 @@ Top top(const Args& a, int lse, const Where& w) {
 // logits, tidx, tlogit, tlse, temperature, weight, loss, grad, stream
 PyObject* distill(const Args& a) {
   const Where w(a.v[8], a.tensor(0), "logits");
+  unrecorded(a, 0);
   const Top o = top(a, 3, w);
   const int64_t all[] = {o.N, o.V};
   const auto* weight = dense<const float>(a, 5, at::kFloat, {o.N}, w);
@@ -479,6 +492,7 @@ PyObject* distill(const Args& a) {
 // logits, tidx, tlogit, tlse, temperature, loss, saved, stream
 PyObject* distill_forward(const Args& a) {
   const Where w(a.v[7], a.tensor(0), "logits");
+  unrecorded(a, 0);
   const Top o = top(a, 3, w);
   const Tensor loss = output(a, 5, {o.N}, at::kFloat, w),
                saved = output(a, 6, {o.N, 4 + o.K}, at::kFloat, w);
@@ -605,6 +619,8 @@ PyObject* call(Function& f, PyObject* const* args, Py_ssize_t nargs, PyObject* k
     PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    PyErr_SetString(PyExc_RuntimeError, "unknown error");
   }
   return nullptr;
 }

@@ -195,7 +195,7 @@ def check_scan(x, g, dy, h0, dl, rs, ln, views=False):
 
 
 @pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 81, 127, 128, 129, 300, 1500])
-@pytest.mark.parametrize("D", [1, 63, 64, 65, 130, 333])
+@pytest.mark.parametrize("D", [1, 8, 15, 32, 63, 64, 65, 130, 333])
 def test_scan_sizes(T, D):
     dtype = TYPES[["f32", "bf16", "f16"][(T + D) % 3]]
     say("scan", T, D, dtype)
@@ -209,6 +209,57 @@ def test_scan_long_time_split(dtype):
     x, g, dy, h0, dl, rs, ln = seq_inputs(2, 9000, 66, TYPES[dtype], 5, 0.0004, False)
     check_scan(x, g, dy, h0, dl, rs, torch.tensor([9000, 4321]))
     check_scan(x[:1], g[:1] + 6, dy[:1], h0[:1], dl[:1], None, None)
+
+
+@pytest.mark.parametrize("D", [5, 32, 100])
+def test_scan_flags_of_bytes(D):
+    """Resets as bytes of any value but 0, on odd rows of them, in sequences that
+    share a wave and in others."""
+    p = per()
+    B, T = 23, 211
+    x, g, dy, h0, dl, _, ln = seq_inputs(B, T, D, torch.float32, D, 0, True)
+    rs = torch.randint(0, 40, (B, T), generator=gen(D))
+    rs = torch.where(rs == 0, torch.randint(1, 256, (B, T), generator=gen(D + 1)), 0).to(torch.uint8)
+    want = scan(x, g, rs != 0, ln, h0, dy, dl)
+    y, h, c = p.per_scan_forward(x.cuda(), g.cuda(), reset=rs.cuda(), length=cu(ln), h0=cu(h0))
+    dx, dg, dh0 = p.per_scan_backward(x.cuda(), g.cuda(), c, dy.cuda(), reset=rs.cuda(), length=cu(ln), dh_last=cu(dl))
+    for n, t in (("y", y), ("h", h), ("dx", dx), ("dg", dg), ("dh0", dh0)):
+        assert_close(t, *want[n], n)
+
+
+def test_recorded_inputs_are_refused():
+    """A call that would cut an autograd graph says so; inside a Function, and
+    under no_grad, it runs."""
+    p = per()
+    x, g = torch.randn(2, 8, 16, device=DEV, requires_grad=True), torch.randn(2, 8, 16, device=DEV)
+    h = torch.zeros(2, 16, device=DEV, requires_grad=True)
+    z = torch.randn(2, 16, device=DEV, requires_grad=True)
+    ti, t = torch.zeros(2, 1, dtype=torch.int32, device=DEV), torch.zeros(2, 1, device=DEV)
+    for f in (lambda: p.per_scan_forward(x, g), lambda: p.per_scan_forward(g, x), lambda: p.per_scan_forward(g, g, h0=h),
+              lambda: p.per_scan_step(g[:, 0], g[:, 0], h), lambda: p.per_distill(z, ti, t),
+              lambda: p.per_distill_forward(z, ti, t)):
+        with pytest.raises(ValueError, match="requires grad"):
+            f()
+        with torch.no_grad():
+            f()
+
+    class Scan(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, a, b):
+            y, _, c = p.per_scan_forward(a, b)
+            ctx.save_for_backward(a, b, c)
+            return y
+
+        @staticmethod
+        def backward(ctx, dy):
+            a, b, c = ctx.saved_tensors
+            return p.per_scan_backward(a, b, c, dy.contiguous())[:2]
+
+    Scan.apply(x, g).square().sum().backward()
+    want = scan(x, g)["y"][0]
+    full = scan(x, g, dy=2 * want)
+    # dy = 2 y is itself off by y's error, at most 1e-5 of values below 4
+    assert_close(x.grad, full["dx"][0], full["dx"][1] + 1e-4, "dx")
 
 
 def test_scan_filled_chip():
