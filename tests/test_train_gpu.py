@@ -40,7 +40,7 @@ def make_rows(n, d, dtype, seed):
     return x.to(dtype)
 
 
-@pytest.mark.parametrize("dim", [1, 7, 8, 33, 64, 333, 512, 1001, 2048, 2049, 5000])
+@pytest.mark.parametrize("dim", [1, 7, 8, 33, 64, 333, 512, 1001, 2048, 2049, 5000, 9001, 33000])
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("fmt", ["e4m3", "i8"])
 def test_rows_round_trip(dim, group, fmt):
@@ -111,7 +111,7 @@ def test_rows_odd_values(fmt, dim, group):
     assert torch.equal(torch.where(nan, 0.0, got.float()), torch.where(nan, 0.0, wc.float()))
 
 
-@pytest.mark.parametrize("dim,group,count", [(40, 32, 1), (1001, 64, 700), (5000, 0, 300), (8, 0, 3000), (300, 0, 257)])
+@pytest.mark.parametrize("dim,group,count", [(40, 32, 1), (1001, 64, 700), (5000, 0, 300), (5000, 128, 300), (33000, 0, 200), (8, 0, 3000), (300, 0, 257)])
 @pytest.mark.parametrize("fmt", ["e4m3", "i8"])
 def test_rows_write_at_last_position_wins(dim, group, count, fmt):
     p = per()
