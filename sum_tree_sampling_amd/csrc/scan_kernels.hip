@@ -39,7 +39,7 @@ namespace {
 constexpr int kForward = 16;
 constexpr int kBackward = 8;
 constexpr int kWaves = 8;                  // waves of a workgroup
-constexpr int kBackWaves = 16;             // in the backward pass, of one tile, at most
+constexpr int kMaxWaves = 16;              // where there is at most one to a CU
 constexpr int kChunk = 64;                 // PER_SCAN_CHUNK
 constexpr int kSegment = 128;              // segments are multiples of it
 constexpr int kMaxSeg = 256;
@@ -81,6 +81,10 @@ __device__ __forceinline__ Place place(const ScanArgs& a) {
     const uint32_t r = id / nct;
     p.d = (int64_t)(id % nct) * (64 * C) + lane * C;
     p.in = p.d < a.D;
+    // Where D is odd the last lane takes the channel before its own as well: it
+    // loads, computes and stores the very values the lane before it does, in step
+    // with it (plan() leaves out the D whose last lane has none before it).
+    if (C > 1 && p.in && p.d > a.D - C) p.d = a.D - C;
     p.seg = (int)(r % (uint32_t)a.nseg);
     p.b = r / (uint32_t)a.nseg;
   }
@@ -175,9 +179,9 @@ __device__ __forceinline__ void load_steps(const Rows<const T>& r, int64_t ts, i
 }
 
 template <typename T, int C, bool PACK>
-__global__ __launch_bounds__(kWaves * 64, 4) void scan_forward_kernel(ScanArgs a) {
+__global__ __launch_bounds__(kMaxWaves * 64, 4) void scan_forward_kernel(ScanArgs a) {
   constexpr int S = kForward;
-  __shared__ float sA[2][kWaves][C][64], sB[2][kWaves][C][64];
+  __shared__ float sA[2][kMaxWaves][C][64], sB[2][kMaxWaves][C][64];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = blockDim.x >> 6;
@@ -390,9 +394,9 @@ __global__ __launch_bounds__(kWaves * 64, 4) void scan_segment_kernel(ScanArgs a
 //   dx = full (1 - f),  dg = full (h' - x) f (1 - f).
 // The states of a chunk are computed again from its carry.
 template <typename T, int C, bool PACK>
-__global__ __launch_bounds__(64 * kBackWaves, 4) void scan_backward_kernel(ScanArgs a) {
+__global__ __launch_bounds__(64 * kMaxWaves, 4) void scan_backward_kernel(ScanArgs a) {
   constexpr int S = kBackward;
-  __shared__ float sA[2][kBackWaves][C][64], sB[2][kBackWaves][C][64], sQ[2][kBackWaves][C][64];
+  __shared__ float sA[2][kMaxWaves][C][64], sB[2][kMaxWaves][C][64], sQ[2][kMaxWaves][C][64];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = blockDim.x >> 6;
@@ -614,19 +618,16 @@ hipError_t backward_typed(const ScanArgs& a, uint32_t blocks, int waves, hipStre
   return launch_kernel(scan_backward_kernel<T, C, PACK>, dim3(blocks), dim3(64 * waves), 0, s, a);
 }
 
-// Waves of a workgroup: as many as the sequence has steps for, up to 8.  The
-// backward pass takes up to 128 steps in one tile of 16 waves where there are
-// too few workgroups for two to a CU anyway (37 x 81 x 333 f32, both passes:
-// 15.5 -> 14.2 us); with 2048 workgroups (256 x 128 x 1024 bf16) one such
-// workgroup to a CU leaves loads and stores unoverlapped: 109 us become 116.
-int forward_waves(int64_t T) {
-  const int64_t w = (T + kForward - 1) / kForward;
-  return w < 1 ? 1 : w > kWaves ? kWaves : (int)w;
-}
-int backward_waves(int64_t T, uint32_t blocks) {
-  const int64_t w = (T + kBackward - 1) / kBackward;
-  if (w <= kWaves) return w < 1 ? 1 : (int)w;
-  return w <= kBackWaves && blocks < 512 ? (int)w : kWaves;
+// Waves of a workgroup: as many as the sequence has steps for, up to 8, or 16 where
+// there is at most one workgroup to a CU and the time axis is whole (forward and
+// backward, 16 against 8: 8 x 512 x 256 bf16 29.7 and 36.1 us, 200 x 200 x 64 19.4
+// and 23.9, 37 x 81 x 333 f32 15.1 and 17.1).  With more workgroups one of 16 waves
+// on a CU leaves its loads and stores unoverlapped (128 x 256 x 333 bf16, 384
+// workgroups: 60 us with 16, 52 with 8).
+int waves_for(int64_t T, int steps, int64_t blocks, bool cut) {
+  const int64_t w = (T + steps - 1) / steps;
+  const int most = !cut && blocks <= 256 ? kMaxWaves : kWaves;
+  return w < 1 ? 1 : w > most ? most : (int)w;
 }
 
 // How a batch is spread over the chip: channels per lane, packed lanes, segments
@@ -636,10 +637,15 @@ int backward_waves(int64_t T, uint32_t blocks) {
 // The time axis is cut where fewer than 192 workgroups would walk it: a cut
 // reads two of the tensors again (24 x 300 x 1000, 192 workgroups: 61 us cut, 41
 // not), and without one a few workgroups cannot carry the load (2 x 16384 x 512,
-// 8 of them).  Two channels per lane make better use of loads once the chip is
-// full (128 x 512 x 1024: 234 against 241 us; 2 x 16384 x 512: 86 against 97),
-// one below (4 x 512 x 256: 28 against 32; 32 x 80 x 512: 12.7 against 14.6), or
-// where it saves the cut (16 x 512 x 1024: 42 against 50).  Lanes are packed
+// 8 of them).  Up to 512 steps the second launch of each pass costs what the cut
+// saves, or more (1 x 186 x 164: 27 us cut, 16 not; 16 x 300 x 400: 35 and 26; 4 x
+// 512 x 1024: 29 and 31; 4 x 762 x 98 f16: 30 and 41).  Two channels per lane make
+// better use of loads once the chip is full (128 x 512 x 1024: 234 against 241 us;
+// 2 x 16384 x 512: 86 against 97), one below (4 x 512 x 256: 28 against 32; 32 x 80
+// x 512: 12.7 against 14.6), or where it saves the cut (16 x 512 x 1024, when it was cut:
+// 42 against 50).  So they do for odd D, whose rows are not aligned to a pair (128 x 256 x 333:
+// 52 against 63; 32 x 388 x 1225: 87 against 97), unless the last tile would hold a
+// lone channel: the lane before it would be another workgroup's.  Lanes are packed
 // where several sequences share a wave evenly or at least four do (4096 x 128 x
 // 8: 36 against 81 us, x 32: 79 against 97; x 40: 114 against 98, since a packed
 // lane has its own addresses and row ends inside a wave).
@@ -650,6 +656,7 @@ struct Plan {
   int64_t steps;
 };
 constexpr int64_t kFull = 192;
+constexpr int64_t kWhole = 512;
 
 Plan plan_with(int64_t B, int64_t T, int64_t D, bool two) {
   const int64_t w = two ? 128 : 64;
@@ -657,7 +664,7 @@ Plan plan_with(int64_t B, int64_t T, int64_t D, bool two) {
   p.packed = D <= 16 || D == 32;
   if (p.packed) p.blocks = (B * D + 63) / 64;
   const int64_t chunks = (T + kSegment - 1) / kSegment;
-  if (p.blocks >= kFull || chunks < 2) return p;
+  if (p.blocks >= kFull || T <= kWhole) return p;
   int64_t n = (512 + p.blocks - 1) / p.blocks;
   if (n > kMaxSeg) n = kMaxSeg;
   if (n > chunks) n = chunks;
@@ -667,7 +674,7 @@ Plan plan_with(int64_t B, int64_t T, int64_t D, bool two) {
 }
 
 Plan plan(int64_t B, int64_t T, int64_t D) {
-  if (D % 2 != 0 || D <= 64) return plan_with(B, T, D, false);
+  if (D <= 64 || D % 128 == 1) return plan_with(B, T, D, false);
   const Plan two = plan_with(B, T, D, true), one = plan_with(B, T, D, false);
   if (two.blocks * two.n < kFull || (two.n > 1 && one.n == 1)) return one;
   return two;
@@ -710,7 +717,7 @@ size_t scan_workspace(int64_t B, int64_t T, int64_t D) {
 hipError_t launch_scan_forward(ScanArgs a, int type, hipStream_t s) {
   const Plan p = set_plan(a);
   const uint32_t blocks = (uint32_t)(p.blocks * p.n);
-  const int waves = forward_waves(a.T);
+  const int waves = waves_for(a.T, kForward, blocks, p.n > 1);
   if (type == 0)
     return forward_of<float>(p, a, blocks, waves, s);
   if (type == 1)
@@ -721,7 +728,7 @@ hipError_t launch_scan_forward(ScanArgs a, int type, hipStream_t s) {
 hipError_t launch_scan_backward(ScanArgs a, int type, hipStream_t s) {
   const Plan p = set_plan(a);
   const uint32_t blocks = (uint32_t)(p.blocks * p.n);
-  const int waves = backward_waves(a.T, blocks);
+  const int waves = waves_for(a.T, kBackward, blocks, p.n > 1);
   if (type == 0)
     return backward_of<float>(p, a, blocks, waves, s);
   if (type == 1)

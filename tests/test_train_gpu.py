@@ -203,6 +203,28 @@ def test_scan_sizes(T, D):
     check_scan(*a, views=T % 3 == 0)
 
 
+@pytest.mark.parametrize("T", [40, 200, 600])
+@pytest.mark.parametrize("D", [127, 129, 131, 255, 257, 333])
+def test_scan_odd_rows_in_pairs(T, D):
+    """Rows of odd length in a batch that fills the chip: the last lane's pair starts
+    a channel early.  h_last may be h0 there too."""
+    dtype = TYPES[["f32", "bf16", "f16"][(T // 40 + D) % 3]]
+    say("scan odd", T, D, dtype)
+    a = seq_inputs(200, T, D, dtype, T + D, 0.03, True)
+    y, h, *_ = check_scan(*a, views=D % 4 == 1)
+    x, g, _, h0, _, rs, ln = a
+    st = h0.cuda()
+    y2, _, _ = per().per_scan_forward(x.cuda(), g.cuda(), reset=rs.cuda(), length=ln.cuda(), h0=st, h_last=st)
+    assert torch.equal(st, h) and torch.equal(y2, y)
+
+
+@pytest.mark.parametrize("shape", [(1, 186, 164), (2, 511, 26), (2, 512, 66), (2, 513, 66), (9, 400, 250)])
+def test_scan_few_sequences(shape):
+    """Few sequences of up to 512 steps, by workgroups of 16 waves, and of one more."""
+    for dtype in TYPES.values():
+        check_scan(*seq_inputs(*shape, dtype, shape[1], 0.01, False))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_scan_long_time_split(dtype):
     """Few channels and a long axis: segments, with resets in some of them."""
