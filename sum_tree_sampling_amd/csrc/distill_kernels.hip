@@ -325,28 +325,22 @@ __device__ __forceinline__ void add_chunk(const Chunk<T>& v, float m, float c, u
 // NT threads hold the row, R chunks each, so it is read once: the largest logit,
 // the sum and the gradient are three passes over registers.  512 threads of 17
 // chunks leave room for two rows to a CU, one loading while the other stores (8192
-// x 65536 bf16, fused: 450-457 us, 4.7 TB/s, the rate of a large copy; with one row of
-// 1024 threads to a CU 637 us).  In the small workgroups one more wave reads the
-// teacher beside them (its chain of loads and f64 exponentials is as long as the
-// row's own); in the large ones, whose registers are full, the first wave does.
+// x 65536 bf16, fused: 409 us, 5.3 TB/s; with one row of 1024 threads to a CU 637
+// us).  With SIDE one more wave reads the teacher beside them (its chain of loads
+// and f64 exponentials is as long as the row's own), else the first wave does.
 // Gradients are stored past the caches: 64 MB 42.8 -> 34.6 us, and the products
 // that read them next take no longer (1 GB with both products of the head: 2915
 // us stored through, 2909 past).
-template <int NT>
-constexpr bool kSideWave = NT <= 256;
-template <int NT>
-constexpr int kRowThreads = kSideWave<NT> ? NT + 64 : NT;
-
-template <typename T, int NT, int R, bool TAIL, bool ONCE>
-__global__ __launch_bounds__(kRowThreads<NT>, NT >= 512 ? 4 : 1) void distill_row_kernel(
-    DistillArgs a) {
+template <typename T, int NT, int R, bool TAIL, bool SIDE>
+__global__ __launch_bounds__(SIDE ? NT + 64 : NT, NT < 512 ? 1 : 4)
+void distill_row_kernel(DistillArgs a) {
   extern __shared__ char mem[];
   __shared__ float red[3][NT / 64];
   __shared__ Teacher t;  // kept here, not in registers across the passes
   const int64_t n = blockIdx.x;
   const int tid = threadIdx.x, wv = tid >> 6;
-  const bool row_wave = !kSideWave<NT> || wv < NT / 64;
-  const bool teacher_wave = wv == (kSideWave<NT> ? NT / 64 : 0);
+  const bool row_wave = !SIDE || wv < NT / 64;
+  const bool teacher_wave = wv == (SIDE ? NT / 64 : 0);
   const Row<T> r = row_of<T>(a, n);
   T* grad = static_cast<T*>(a.grad) + n * a.grad_stride;
   Entry first = {-1, 0.0f};
@@ -354,7 +348,7 @@ __global__ __launch_bounds__(kRowThreads<NT>, NT >= 512 ? 4 : 1) void distill_ro
   const float w = a.weight ? a.weight[n] : 1.0f;
   if (w == 0.0f) {
     const float zero[kVec<T>] = {};
-    for (uint32_t j = tid; j < r.chunks; j += kRowThreads<NT>) store_chunk(grad, r, j, zero);
+    for (uint32_t j = tid; j < r.chunks; j += blockDim.x) store_chunk(grad, r, j, zero);
     if (tid == 0) a.loss[n] = 0.0f;
     return;
   }
@@ -369,7 +363,7 @@ __global__ __launch_bounds__(kRowThreads<NT>, NT >= 512 ? 4 : 1) void distill_ro
     if (!teacher_wave) return;
     clear_marks(l.bits, words);
     entries = read_entries<T, TAIL>(a, r, n, l, true, 0, r.chunks, first);
-    if (!kSideWave<NT>) sums();
+    if (!SIDE) sums();
   };
   // The row's loads come first, so that they are in flight meanwhile, unless
   // they would take the registers the first wave needs for the teacher.
@@ -380,7 +374,7 @@ __global__ __launch_bounds__(kRowThreads<NT>, NT >= 512 ? 4 : 1) void distill_ro
     for (int q = 0; q < R; ++q) {
       const uint32_t j = tid + q * NT;
       if (j < r.chunks) {
-        v[q] = load_chunk<T, ONCE>(r, j);
+        v[q] = a.once ? load_chunk<T, true>(r, j) : load_chunk(r, j);
       } else {
 #pragma unroll
         for (int e = 0; e < kVec<T>; ++e) v[q].v[e] = (T)kNegInf;
@@ -402,7 +396,7 @@ __global__ __launch_bounds__(kRowThreads<NT>, NT >= 512 ? 4 : 1) void distill_ro
     if ((tid & 63) == 0) red[0][wv] = m;
   }
   __syncthreads();
-  if (kSideWave<NT> && teacher_wave) sums();  // beside the row's own
+  if (SIDE && teacher_wave) sums();  // beside the row's own
   m = red[0][0];
 #pragma unroll
   for (int q = 1; q < NT / 64; ++q) m = fmaxf(m, red[0][q]);
@@ -498,12 +492,34 @@ __device__ __forceinline__ void load_batch(const Row<T>& r, uint32_t j0, uint32_
   }
 }
 
+// A row's loss and what its gradient needs, by one wave.
+template <bool TAIL>
+__device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t n, bool off,
+                                           const Teacher& t, float m, float rest, float top) {
+  if (m == kNegInf) m = 0.0f;
+  float S = rest + top;
+  const bool dead = off || S == 0.0f || (!TAIL && !t.any);
+  if (dead) S = rest = 0.0f;
+  const float loss = dead ? 0.0f : row_loss(a, t, m, S, rest, TAIL);
+  if ((threadIdx.x & 63) == 0) {
+    a.loss[n] = loss;
+    if (a.saved) {
+      float* s = a.saved + n * (4 + a.K);
+      s[0] = m;
+      s[1] = S;
+      s[2] = rest;
+      s[3] = (float)t.rest;
+    }
+  }
+}
+
 // Largest logit and sums of one part of a row; the first part's extra wave
 // reads the teacher.
 template <typename T, bool TAIL>
 __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(DistillArgs a) {
   extern __shared__ char mem[];
   __shared__ float red[3][kPartThreads / 64];
+  __shared__ Teacher whole;  // where the part is the row
   const int64_t n = blockIdx.x / (uint32_t)a.splits;
   const int split = (int)(blockIdx.x % (uint32_t)a.splits);
   const int tid = threadIdx.x, wv = tid >> 6;
@@ -511,6 +527,7 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
   float* part = a.part + (int64_t)blockIdx.x * 4;
   if (a.weight && a.weight[n] == 0.0f) {
     if (tid == 0) part[0] = kNegInf, part[1] = part[2] = 0.0f;
+    if (a.splits == 1 && !row_wave) finish_row<TAIL>(a, n, true, Teacher{}, 0.0f, 0.0f, 0.0f);
     return;
   }
   const Row<T> r = row_of<T>(a, n);
@@ -538,7 +555,7 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
   if (TAIL) __syncthreads();
   if (!row_wave && split == 0) {
     const Teacher t = sum_entries<TAIL>(a, n, l, entries);
-    if ((tid & 63) == 0) a.teacher[n] = t;
+    if ((tid & 63) == 0) (a.splits == 1 ? whole : a.teacher[n]) = t;
     if (a.saved)
       for (int k = tid & 63; k < a.K; k += 64) a.saved[n * (4 + a.K) + 4 + k] = l.p[k];
   }
@@ -585,12 +602,16 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    rest = top = 0.0f;
-    for (int q = 0; q < kPartThreads / 64; ++q) {
-      rest += red[1][q];
-      top += red[2][q];
-    }
+  if (a.splits == 1 ? row_wave : tid != 0) return;
+  rest = top = 0.0f;
+#pragma unroll
+  for (int q = 0; q < kPartThreads / 64; ++q) {
+    rest += red[1][q];
+    top += red[2][q];
+  }
+  if (a.splits == 1) {
+    finish_row<TAIL>(a, n, false, whole, mw, rest, top);
+  } else {
     part[0] = mw;
     part[1] = rest;
     part[2] = top;
@@ -617,22 +638,10 @@ __global__ __launch_bounds__(64) void distill_join_kernel(DistillArgs a) {
   }
   rest = wave_sum(rest);
   top = wave_sum(top);
-  if (m == kNegInf) m = 0.0f;
-  float S = rest + top;
-  const bool dead = off || S == 0.0f || (!TAIL && !t.any);
-  if (dead) S = rest = 0.0f;
-  const float loss = dead ? 0.0f : row_loss(a, t, m, S, rest, TAIL);
-  if (lane == 0) {
-    a.loss[n] = loss;
-    if (a.saved) {
-      float* s = a.saved + n * (4 + a.K);
-      s[0] = m;
-      s[1] = S;
-      s[2] = rest;
-      s[3] = (float)t.rest;
-    }
-  }
+  finish_row<TAIL>(a, n, off, t, m, rest, top);
 }
+
+constexpr int kAhead = 4;  // entries a lane loads at once
 
 // Gradient of one part of a row from its saved statistics and probabilities.
 template <typename T, bool TAIL>
@@ -662,15 +671,26 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_grad_kernel(Distill
   } else {
     bool dup = false;
     clear_marks(l.bits, words);
-    for (int k = tid & 63; k < a.K; k += 64) {
-      const int i = a.tidx[n * a.K + k];
-      const float p = saved[4 + k];
-      const bool here = i >= 0 && i < (int64_t)r.V && i >= lo && i < hi;
-      l.idx[k] = here ? i : -1;
-      l.p[k] = p;
-      if (here) {
-        l.z[k] = (float)r.z[i];
-        dup |= mark<false>(l.bits, i, lo, hi);
+    for (int k0 = tid & 63; k0 < a.K; k0 += 64 * kAhead) {
+      int i[kAhead];
+      float p[kAhead], z[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int k = k0 + 64 * u;
+        i[u] = k < a.K ? a.tidx[n * a.K + k] : -1;
+        p[u] = k < a.K ? saved[4 + k] : 0.0f;
+        if (i[u] >= (int64_t)r.V || i[u] < lo || i[u] >= hi) i[u] = -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) z[u] = i[u] >= 0 ? (float)r.z[i[u]] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int k = k0 + 64 * u;
+        if (k >= a.K) break;
+        l.idx[k] = i[u];
+        l.p[k] = p[u];
+        l.z[k] = z[u];
+        if (i[u] >= 0) dup |= mark<false>(l.bits, i[u], lo, hi);
       }
     }
     const bool any = __any(dup);
@@ -703,16 +723,29 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_grad_kernel(Distill
 
 // ---------------------------------------------------------- one wave per row
 //
-// Rows of up to 256 chunks, four to a workgroup, each within one wave, which
-// needs no barrier for its maximum and sums.  A fifth wave reads the four
-// teachers at once, K entries of a row on the next power of two of lanes: the
-// f64 arithmetic of a row, spent by a whole wave on each, took longer than the
-// row itself (16384 x 500 bf16, K = 16: 27.6 us).
+// Rows of up to 256 chunks, or more where there are many, four to a workgroup, each
+// within one wave, which needs no barrier for its maximum and sums.  One more wave
+// reads the four teachers at once, K entries of a row on the next power of two of
+// lanes: the f64 arithmetic of a row, spent by a whole wave on each, took longer
+// than the row itself (16384 x 500 bf16, K = 16: 27.6 -> 21 us).  Where K leaves it
+// fewer than four rows, two or four waves do (610 x 457 f16, K = 102: 13.9 -> 6.4 us,
+// 16384 x 500 bf16 with a rest, K = 64: 55 -> 29).
 enum Pass { kFused, kLoss, kGradient };
 constexpr int kWaveRows = 4;
 
+// Lanes for the K entries of a row (log2), and the waves that take four rows'.
+__host__ __device__ inline int entry_lanes(int K) {
+  int lg = 0;
+  while (lg < 6 && (1 << lg) < K) ++lg;
+  return lg;
+}
+int teacher_waves(int K) {
+  const int per = 64 >> entry_lanes(K);
+  return per >= kWaveRows ? 1 : kWaveRows / per;
+}
+
 template <typename T, int R, bool TAIL, int PASS>
-__global__ __launch_bounds__(PASS == kGradient ? 64 * kWaveRows : 64 * (kWaveRows + 1))
+__global__ __launch_bounds__(PASS == kGradient ? 64 * kWaveRows : 128 * kWaveRows)
 void distill_wave_kernel(DistillArgs a, uint32_t words) {
   extern __shared__ char mem[];
   __shared__ float stat[kWaveRows][3];
@@ -723,50 +756,25 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
   auto lds_row = [&](int q) {
     return lds_of(mem + (size_t)q * 4 * (words + 3 * (size_t)((a.K + 3) / 4 * 4)), a.K, words);
   };
-  if (PASS != kGradient && wv == kWaveRows) {  // the teachers
-    int lg = 0;
-    while (lg < 6 && (1 << lg) < a.K) ++lg;
-    const int per = 64 >> lg;  // rows at once
-    Entries e[kWaveRows];
-    Entry first[kWaveRows];
-#pragma unroll
-    for (int u = 0; u < kWaveRows; ++u) {
-      const int q = u * per + (lane >> lg);
-      if (u * per < kWaveRows)
-        first[u] = entry_at(a, q < kWaveRows ? n0 + q : a.N, lane & ((1 << lg) - 1));
-    }
-#pragma unroll
-    for (int q = 0; q < kWaveRows; ++q) clear_marks(lds_row(q).bits, words);
-#pragma unroll
-    for (int u = 0; u < kWaveRows; ++u) {
-      const int q = u * per + (lane >> lg);
-      if (u * per < kWaveRows) {
-        const int64_t n = q < kWaveRows ? n0 + q : a.N;
-        const Row<T> r = row_of<T>(a, n < a.N ? n : n0);
-        e[u] = read_entries<T, TAIL>(a, r, n, lds_row(q < kWaveRows ? q : 0), true, 0, r.chunks,
-                                     first[u], lg);
-      }
-    }
+  if (PASS != kGradient && wv >= kWaveRows) {  // the teachers
+    const int lg = entry_lanes(a.K), k0 = lane & ((1 << lg) - 1);
+    const int q = ((wv - kWaveRows) << (6 - lg)) + (lane >> lg);
+    const int64_t n = q < kWaveRows ? n0 + q : a.N;
+    const Entry first = entry_at(a, n, k0);
+    const int own = kWaveRows / ((int)(blockDim.x >> 6) - kWaveRows);  // rows of the wave
+    for (int b = 0; b < own; ++b) clear_marks(lds_row((wv - kWaveRows) * own + b).bits, words);
+    const Row<T> r = row_of<T>(a, n < a.N ? n : n0);
+    const Lds l = lds_row(q < kWaveRows ? q : 0);
+    const Entries e = read_entries<T, TAIL>(a, r, n, l, true, 0, r.chunks, first, lg);
     if (TAIL) __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kWaveRows; ++u) {
-      const int q = u * per + (lane >> lg);
-      if (u * per < kWaveRows) {
-        const int64_t n = q < kWaveRows ? n0 + q : a.N;
-        const Lds l = lds_row(q < kWaveRows ? q : 0);
-        const Teacher t = sum_entries<TAIL>(a, n, l, e[u], lg);
-        if (q < kWaveRows && (lane & ((1 << lg) - 1)) == 0) teachers[q] = t;
-        if (PASS == kLoss && a.saved && n < a.N)
-          for (int k = lane & ((1 << lg) - 1); k < a.K; k += 1 << lg)
-            a.saved[n * (4 + a.K) + 4 + k] = l.p[k];
-      }
-    }
+    const Teacher t = sum_entries<TAIL>(a, n, l, e, lg);
+    if (q < kWaveRows && k0 == 0) teachers[q] = t;
+    if (PASS == kLoss && a.saved && n < a.N)
+      for (int k = k0; k < a.K; k += 1 << lg) a.saved[n * (4 + a.K) + 4 + k] = l.p[k];
     __syncthreads();
-    const int64_t n = n0 + lane;
-    if (lane < kWaveRows && n < a.N) {
+    if (q < kWaveRows && k0 == 0 && n < a.N) {
       const float w = PASS == kFused && a.weight ? a.weight[n] : 1.0f;
-      const float m = stat[lane][0], S = stat[lane][1], Sr = stat[lane][2];
-      const Teacher t = teachers[lane];
+      const float m = stat[q][0], S = stat[q][1], Sr = stat[q][2];
       const bool dead = w == 0.0f || S == 0.0f || (!TAIL && !t.any);
       a.loss[n] = dead ? 0.0f : row_loss(a, t, m, S, Sr, TAIL);
       if (PASS == kLoss && a.saved) {
@@ -888,16 +896,21 @@ int64_t part_tokens(const DistillArgs& a, int type) {
   return (chunks + a.splits - 1) / a.splits * vec;
 }
 
-template <typename T, int NT, int R, bool ONCE = false>
+template <typename T, int NT, int R, bool SIDE>
 hipError_t row_launch(const DistillArgs& a, hipStream_t s) {
   const size_t lds = lds_bytes(a.K, a.tlse != nullptr, a.V + 2 * kVec<T>);
-  const dim3 grid((uint32_t)a.N), block(kRowThreads<NT>);
-  if (a.tlse)
-    return launch_kernel(distill_row_kernel<T, NT, R, true, ONCE>, grid, block, lds, s, a);
-  return launch_kernel(distill_row_kernel<T, NT, R, false, ONCE>, grid, block, lds, s, a);
+  const dim3 grid((uint32_t)a.N), block(SIDE ? NT + 64 : NT);
+  return a.tlse ? launch_kernel(distill_row_kernel<T, NT, R, true, SIDE>, grid, block, lds, s, a)
+                : launch_kernel(distill_row_kernel<T, NT, R, false, SIDE>, grid, block, lds, s, a);
 }
 
-constexpr int64_t kWaveChunks = 256;
+// Whether the wave kernel takes rows of so many chunks.  From 1024 rows on there are
+// enough waves to hide its loads: 16384 x 4000 bf16 75 us, 80 by workgroups; 64 x 4000
+// 8 and 6.  The two calls apart gain more, since a row has no parts to join (1500 x
+// 5900 bf16 with a rest 22 us, 30 in parts; 6000 x 5900 69 and 67; fused 46 and 41).
+bool by_waves(int64_t N, int64_t chunks, bool fused) {
+  return chunks <= (N < 1024 ? 256 : fused ? 512 : 768);
+}
 
 template <typename T, int PASS, bool TAIL>
 hipError_t wave_launch(const DistillArgs& a, hipStream_t s) {
@@ -905,9 +918,14 @@ hipError_t wave_launch(const DistillArgs& a, hipStream_t s) {
   const uint32_t words = mark_words(TAIL, chunks * kVec<T>);
   const size_t lds = (size_t)kWaveRows * 4 * (words + 3 * (size_t)((a.K + 3) / 4 * 4));
   const dim3 grid((uint32_t)((a.N + kWaveRows - 1) / kWaveRows));
-  const dim3 block(PASS == kGradient ? 64 * kWaveRows : 64 * (kWaveRows + 1));
+  const dim3 block(64 * (PASS == kGradient ? kWaveRows : kWaveRows + teacher_waves(a.K)));
   if (chunks <= 64)
     return launch_kernel(distill_wave_kernel<T, 1, TAIL, PASS>, grid, block, lds, s, a, words);
+  if constexpr (PASS != kFused)
+    if (chunks > 512)
+      return launch_kernel(distill_wave_kernel<T, 12, TAIL, PASS>, grid, block, lds, s, a, words);
+  if (chunks > 256)
+    return launch_kernel(distill_wave_kernel<T, 8, TAIL, PASS>, grid, block, lds, s, a, words);
   return launch_kernel(distill_wave_kernel<T, 4, TAIL, PASS>, grid, block, lds, s, a, words);
 }
 template <typename T, int PASS>
@@ -916,40 +934,50 @@ hipError_t wave_typed(const DistillArgs& a, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t row_typed(const DistillArgs& a, hipStream_t s) {
+hipError_t row_typed(DistillArgs a, hipStream_t s) {
   const int64_t chunks = (a.V + 2 * kVec<T> - 2) / kVec<T>;
-  if (chunks <= kWaveChunks) return wave_typed<T, kFused>(a, s);
-  if (chunks <= 256 * 4) return row_launch<T, 256, 4>(a, s);
+  if (by_waves(a.N, chunks, true)) return wave_typed<T, kFused>(a, s);
   // Logits that fill half of the 256 MB Infinity Cache are loaded past it
   // (128 MB of bf16 logits at 32768 tokens: 70.5 -> 68.6 us, 1 GB at 65536: 468
   // -> 460 us; 64 MB the other way: 34.5 -> 37.9 us).
-  const bool once = a.N * a.V * (int64_t)sizeof(T) >= (int64_t(1) << 27);
+  a.once = a.N * a.V * (int64_t)sizeof(T) >= (int64_t(1) << 27);
+  // Few chunks to a thread and few threads leave room for more rows on a CU (4096 x
+  // 10000 bf16: 512 x 9 64 us, 512 x 4 48, 256 x 6 43; 4096 x 20000: 512 x 9 93 us,
+  // 512 x 7 76), more threads are faster where each CU has two rows or fewer (512 x
+  // 10000 with a rest: 256 x 8 10.3 us, 512 x 4 9.5).  The teacher's extra wave pays
+  // in the small workgroups and where CUs have registers to spare (256 x 32000 with
+  // a rest: 12.3 us, 14.1 without; 512 x 20000 14.7 and 16.1), and otherwise takes
+  // the second row's place on the CU (4096 x 32768: 161 us, 128 without).
+  if (chunks <= 256 * 4) return row_launch<T, 256, 4, true>(a, s);
+  if (chunks <= 256 * 6 && a.N > 512) return row_launch<T, 256, 6, true>(a, s);
+  if (chunks <= 512 * 4) return row_launch<T, 512, 4, true>(a, s);
+  if (chunks <= 512 * 7)
+    return a.N <= 512 ? row_launch<T, 512, 7, true>(a, s) : row_launch<T, 512, 7, false>(a, s);
   if (chunks <= 512 * 9)
-    return once ? row_launch<T, 512, 9, true>(a, s) : row_launch<T, 512, 9>(a, s);
-  if (chunks <= 512 * 17)
-    return once ? row_launch<T, 512, 17, true>(a, s) : row_launch<T, 512, 17>(a, s);
-  return once ? row_launch<T, 1024, 17, true>(a, s) : row_launch<T, 1024, 17>(a, s);
+    return a.N <= 256 ? row_launch<T, 512, 9, true>(a, s) : row_launch<T, 512, 9, false>(a, s);
+  return chunks <= 512 * 17 ? row_launch<T, 512, 17, false>(a, s)
+                            : row_launch<T, 1024, 17, false>(a, s);
 }
 
 template <typename T>
 hipError_t stats_typed(const DistillArgs& a, int type, hipStream_t s) {
-  if (distill_small(a.V, type)) return wave_typed<T, kLoss>(a, s);
+  if (distill_small(a.N, a.V, type)) return wave_typed<T, kLoss>(a, s);
   const dim3 grid((uint32_t)(a.N * a.splits)), block(kPartThreads + 64);
   if (a.tlse) {
     const hipError_t e = launch_kernel(distill_part_kernel<T, true>, grid, block,
                                        lds_bytes(a.K, true, part_tokens(a, type)), s, a);
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || a.splits == 1) return e;
     return launch_kernel(distill_join_kernel<true>, dim3((uint32_t)a.N), dim3(64), 0, s, a);
   }
   const hipError_t e = launch_kernel(distill_part_kernel<T, false>, grid, block,
                                      lds_bytes(a.K, true, 0), s, a);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || a.splits == 1) return e;
   return launch_kernel(distill_join_kernel<false>, dim3((uint32_t)a.N), dim3(64), 0, s, a);
 }
 
 template <typename T>
 hipError_t grad_typed(const DistillArgs& a, int type, hipStream_t s) {
-  if (distill_small(a.V, type)) return wave_typed<T, kGradient>(a, s);
+  if (distill_small(a.N, a.V, type)) return wave_typed<T, kGradient>(a, s);
   const dim3 grid((uint32_t)(a.N * a.splits)), block(kPartThreads + 64);
   const size_t lds = lds_bytes(a.K, false, part_tokens(a, type));
   return a.tlse ? launch_kernel(distill_grad_kernel<T, true>, grid, block, lds, s, a)
@@ -958,22 +986,31 @@ hipError_t grad_typed(const DistillArgs& a, int type, hipStream_t s) {
 
 }  // namespace
 
-bool distill_small(int64_t V, int type) {
+bool distill_small(int64_t N, int64_t V, int type) {
   const int vec = 16 / elem_size(type);
-  return (V + 2 * vec - 2) / vec <= kWaveChunks;
+  return by_waves(N, (V + 2 * vec - 2) / vec, false);
 }
 
+// A workgroup takes the whole row where it fits the registers: from 128 rows on, and
+// below where 512 threads of 9 chunks do (5 x 11692 f32 with a rest 5.8 us, 11.6 in
+// parts; 60 x 32000 bf16 9.0 and 13.5; of longer rows, 5 x 60000 16.7 and 11.3).
 bool distill_resident(int64_t N, int64_t V, int type) {
   const int vec = 16 / elem_size(type);
   const int64_t chunks = (V + 2 * vec - 2) / vec;
-  return chunks <= 1024 * 17 && (N >= 128 || chunks <= 256 * 4);
+  return chunks <= 1024 * 17 && (N >= 128 || chunks <= 512 * 9);
 }
+
+// Up to five workgroups to a CU: with more, the last of them start when the others
+// are done (147 x 120926 bf16 with a rest, both calls: 34.0 us, 35.7 of up to 2048
+// workgroups, 45 of 4096; 300 x 131071 51.6, 53.5 of 1024), and a row in one part
+// needs no join (700 x 8000: 20.1 -> 15.0 us).
+constexpr int64_t kPartGroups = 1280;
 
 int distill_splits(int64_t N, int64_t V, int type) {
   const int vec = 16 / elem_size(type);
   const int64_t chunks = (V + 2 * vec - 2) / vec;
   const int64_t most = (chunks + kPartThreads * kBatch - 1) / (kPartThreads * kBatch);
-    int64_t n = (2048 + N - 1) / N;
+  int64_t n = N ? kPartGroups / N : 1;
   if (n > most) n = most;
   // the bitmap of a part lies in LDS
   const int64_t least = (V + (1 << 18) - 1) >> 18;

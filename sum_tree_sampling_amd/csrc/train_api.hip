@@ -151,7 +151,7 @@ struct DistillSpace {
 };
 DistillSpace distill_space(int64_t N, int64_t V, int64_t K, int32_t type) {
   DistillSpace s = {0, 0, 0};
-  if (per::distill_small(V, type)) return s;
+  if (per::distill_small(N, V, type)) return s;
   s.part = (size_t)N * sizeof(per::Teacher);
   s.saved = s.part + (size_t)N * per::distill_splits(N, V, type) * 16;
   s.total = s.saved + (size_t)N * (size_t)(4 + K) * 4;

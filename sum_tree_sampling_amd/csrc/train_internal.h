@@ -98,11 +98,12 @@ struct DistillArgs {
   float* part;            // [N x splits x 4]
   Teacher* teacher;       // [N]
   int splits;
+  bool once;              // logits are loaded past the caches
 };
 // Whether one wave holds a whole row (then no call needs a workspace), whether
 // one workgroup does in per_distill, and if not, how many parts each row is
 // split into.
-bool distill_small(int64_t V, int type);
+bool distill_small(int64_t N, int64_t V, int type);
 bool distill_resident(int64_t N, int64_t V, int type);
 int distill_splits(int64_t N, int64_t V, int type);
 hipError_t launch_distill_fused(const DistillArgs& a, int type, hipStream_t s);

@@ -474,6 +474,61 @@ def test_distill_sizes(V, K, dtype, tail):
 
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("chunks", [300, 512, 700, 769, 1100, 1537, 2048, 2300, 3584, 4000])
+def test_distill_many_rows(chunks, dtype, tail):
+    """Rows by one wave each, by workgroups of each size, and the two calls apart in
+    one part: every row of many is the row of a small batch."""
+    p = per()
+    V, K, tau = chunks * (4 if dtype == "f32" else 8) - 11, 70, 1.3
+    z, tidx, t, w = top_inputs(4, V, K, TYPES[dtype], chunks, tail)
+    tl = with_rest(t, tau, V) if tail else None
+    want = distill(z, tidx, t, tl, tau, w, z.dtype)
+    for N in (257, 1029) if chunks <= 2048 else (257, 517):
+        say("distill rows", N, V, dtype, tail)
+        at = torch.arange(N) % 4
+        gz, gi, gt, gw, gl = z[at].cuda(), tidx[at].cuda(), t[at].cuda(), w[at].cuda(), cu(None if tl is None else tl[at])
+        loss, grad = p.per_distill(gz, gi, gt, tlse=gl, temperature=tau, weight=gw)
+        l2, saved = p.per_distill_forward(gz, gi, gt, tlse=gl, temperature=tau)
+        g2 = p.per_distill_backward(gz, gi, gt, saved, gw, tlse=gl, temperature=tau)
+        assert_close(loss[:4], *want["loss"], "loss")
+        assert_close(grad[:4], *want["grad"], "grad")
+        assert_close(g2[:4], *want["grad"], "backward grad")
+        assert_close(l2[:4], *distill(z, tidx, t, tl, tau, None, z.dtype)["loss"], "forward loss")
+        # rows are aligned to 16 bytes in different ways, so sums are in four orders
+        for q in range(4, 24):
+            k = q % 4
+            assert_close(loss[q], *(b[k] for b in want["loss"]), "loss")
+            assert_close(grad[q], *(b[k] for b in want["grad"]), "grad")
+            assert_close(g2[q], *(b[k] for b in want["grad"]), "backward grad")
+        span = 16  # 16 rows of any length begin alike again
+        for got in (loss, grad, l2, saved, g2):
+            head = got[:span]
+            for q in range(span, N, span):
+                m = min(span, N - q)
+                assert torch.equal(got[q:q + m], head[:m])
+
+
+@pytest.mark.parametrize("chunks", [4000, 8192])
+def test_distill_logits_past_the_caches(chunks):
+    """Batches of 128 MB and more give the bits of smaller ones."""
+    p = per()
+    V, K, part = chunks * 8, 64, 520
+    N = (1 << 27) // (V * 2) + 9
+    g = torch.Generator(device=DEV).manual_seed(chunks)
+    z = torch.randn(N, V, generator=g, device=DEV).to(torch.bfloat16) * 3
+    tidx = torch.randint(0, V, (N, K), generator=g, device=DEV, dtype=torch.int32)
+    t = torch.randn(N, K, generator=g, device=DEV)
+    loss, grad = p.per_distill(z, tidx, t)
+    for q in range(0, N, part):
+        m = min(part, N - q)
+        if m < part:
+            q, m = N - part, part
+        l2, g2 = p.per_distill(z[q:q + m], tidx[q:q + m], t[q:q + m])
+        assert torch.equal(loss[q:q + m], l2) and torch.equal(grad[q:q + m], g2)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("N,V", [(130, 20000), (130, 40001), (129, 66000), (3, 131071), (2, 300001)])
 def test_distill_large_rows(N, V, dtype, tail):
     """Rows in one workgroup's registers, in parts, and past both."""
