@@ -125,12 +125,15 @@ __device__ __forceinline__ void store_chunk(T* grad, const Row<T>& r, uint32_t j
 //
 // LDS of a workgroup: a bitmap, then the K entries.  With a rest the bitmap
 // marks the tokens of chunks [c0, c1) of the row; without one it only has to
-// find repeated entries, and marks them modulo its size (tokens that merely
-// meet there cost a second look in patch_top, no more).
-constexpr uint32_t kHashWords = 1024;
-__host__ __device__ inline uint32_t mark_words(bool tail, int64_t tokens) {
-  const uint32_t w = (uint32_t)((tokens + 127) / 128 * 4);
-  return !tail && w > kHashWords ? kHashWords : w;
+// find repeated entries, and marks them modulo its size.  Tokens that merely meet
+// there cost patch_top a second look, K^2 of LDS reads (10 us of a row with K = 239),
+// so the size grows with K: at most one row in four has such a pair up to K = 256.
+__host__ __device__ inline uint32_t hash_words(int K) {
+  return K <= 128 ? 1024 : K <= 181 ? 2048 : 4096;
+}
+__host__ __device__ inline uint32_t mark_words(bool tail, int64_t tokens, int K) {
+  const uint32_t w = (uint32_t)((tokens + 127) / 128 * 4), h = hash_words(K);
+  return !tail && w > h ? h : w;
 }
 
 struct Lds {
@@ -148,23 +151,27 @@ __device__ __forceinline__ Lds lds_of(char* mem, int K, uint32_t words) {
   return l;
 }
 
-__device__ __forceinline__ float teacher_logit(const DistillArgs& a, int64_t at) {
-  if (a.t_type == 0) return static_cast<const float*>(a.t)[at];
-  if (a.t_type == 1) return (float)static_cast<const bf16_t*>(a.t)[at];
-  return (float)static_cast<const f16_t*>(a.t)[at];
-}
-
-// An entry of the lane: token and teacher's logit.  The first one is loaded
-// ahead of the row.
+// An entry of the lane: token and teacher's logit, whose bits are converted where
+// it is used, since that waits for the load.  The first one is loaded ahead of the
+// row.
 struct Entry {
   int i;
-  float t;
+  uint32_t bits;
 };
+__device__ __forceinline__ uint32_t teacher_bits(const DistillArgs& a, int64_t at) {
+  return a.t_type == 0 ? static_cast<const uint32_t*>(a.t)[at]
+                       : (uint32_t) static_cast<const uint16_t*>(a.t)[at];
+}
+__device__ __forceinline__ float teacher_logit(const DistillArgs& a, uint32_t bits) {
+  if (a.t_type == 0) return __uint_as_float(bits);
+  if (a.t_type == 1) return __uint_as_float(bits << 16);
+  return (float)__builtin_bit_cast(f16_t, (uint16_t)bits);
+}
 __device__ __forceinline__ Entry entry_at(const DistillArgs& a, int64_t n, int k) {
-  Entry e = {-1, 0.0f};
+  Entry e = {-1, 0};
   if (k < a.K && n < a.N) {
     e.i = a.tidx[n * a.K + k];
-    e.t = teacher_logit(a, n * a.K + k);
+    e.bits = teacher_bits(a, n * a.K + k);
   }
   return e;
 }
@@ -176,10 +183,10 @@ __device__ __forceinline__ void clear_marks(uint32_t* bits, uint32_t words) {
 }
 // Marks token i if it lies in [lo, hi); whether it was marked before.
 template <bool TAIL>
-__device__ __forceinline__ bool mark(uint32_t* bits, int i, int64_t lo, int64_t hi) {
+__device__ __forceinline__ bool mark(uint32_t* bits, int K, int i, int64_t lo, int64_t hi) {
   if (i < lo || i >= hi) return false;
   uint32_t bit = (uint32_t)(i - lo);
-  if (!TAIL) bit &= 32 * kHashWords - 1;
+  if (!TAIL) bit &= 32 * hash_words(K) - 1;
   return (atomicOr(&bits[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u;
 }
 
@@ -202,13 +209,14 @@ __device__ __forceinline__ Entries read_entries(const DistillArgs& a, const Row<
     if (k != first) e = entry_at(a, n, k);
     const int i = e.i < 0 || e.i >= (int64_t)r.V ? -1 : e.i;
     const float z = i >= 0 ? (float)r.z[i] : kNegInf;
+    const float t = teacher_logit(a, e.bits);
     if (i >= 0) {
       o.any = true;
-      o.tm = fmaxf(o.tm, e.t);
-      if (marks) o.dup |= mark<TAIL>(l.bits, i, lo, hi);
+      o.tm = fmaxf(o.tm, t);
+      if (marks) o.dup |= mark<TAIL>(l.bits, a.K, i, lo, hi);
     }
     l.idx[k] = i;
-    l.p[k] = e.t;
+    l.p[k] = t;
     l.z[k] = z;
     o.z0 = fmaxf(o.z0, z);
   }
@@ -343,8 +351,8 @@ void distill_row_kernel(DistillArgs a) {
   const bool teacher_wave = wv == (SIDE ? NT / 64 : 0);
   const Row<T> r = row_of<T>(a, n);
   T* grad = static_cast<T*>(a.grad) + n * a.grad_stride;
-  Entry first = {-1, 0.0f};
-  if (teacher_wave) first = entry_at(a, n, tid & 63);
+  Entry first = {-1, 0};
+  if (R <= 12 && teacher_wave) first = entry_at(a, n, tid & 63);
   const float w = a.weight ? a.weight[n] : 1.0f;
   if (w == 0.0f) {
     const float zero[kVec<T>] = {};
@@ -352,7 +360,7 @@ void distill_row_kernel(DistillArgs a) {
     if (tid == 0) a.loss[n] = 0.0f;
     return;
   }
-  const uint32_t words = mark_words(TAIL, (int64_t)r.chunks * kVec<T>);
+  const uint32_t words = mark_words(TAIL, (int64_t)r.chunks * kVec<T>, a.K);
   const Lds l = lds_of(mem, a.K, words);
   Entries entries;
   auto sums = [&] {
@@ -362,6 +370,7 @@ void distill_row_kernel(DistillArgs a) {
   auto read_teacher = [&] {
     if (!teacher_wave) return;
     clear_marks(l.bits, words);
+    if (R > 12) first = entry_at(a, n, tid & 63);
     entries = read_entries<T, TAIL>(a, r, n, l, true, 0, r.chunks, first);
     if (!SIDE) sums();
   };
@@ -532,7 +541,7 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
   }
   const Row<T> r = row_of<T>(a, n);
   const Span s = span_of(a, r, split);
-  const uint32_t words = TAIL ? mark_words(true, (int64_t)(s.c1 - s.c0) * kVec<T>) : 0;
+  const uint32_t words = TAIL ? mark_words(true, (int64_t)(s.c1 - s.c0) * kVec<T>, a.K) : 0;
   const Lds l = lds_of(mem, a.K, words);
   Chunk<T> v[kBatch];
   Entries entries;
@@ -548,7 +557,7 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
       for (int k = tid & 63; k < a.K; k += 64) {
         const int i = a.tidx[n * a.K + k];
         if (i >= 0 && i < (int64_t)r.V)
-          mark<true>(l.bits, i, (int64_t)s.c0 * kVec<T> - r.mis, (int64_t)s.c1 * kVec<T> - r.mis);
+          mark<true>(l.bits, a.K, i, (int64_t)s.c0 * kVec<T> - r.mis, (int64_t)s.c1 * kVec<T> - r.mis);
       }
     }
   }
@@ -663,7 +672,7 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_grad_kernel(Distill
     for (uint32_t j = s.c0 + tid; j < s.c1; j += kPartThreads + 64) store_chunk(grad, r, j, zero);
     return;
   }
-  const uint32_t words = mark_words(false, (int64_t)(s.c1 - s.c0) * kVec<T>);
+  const uint32_t words = mark_words(false, (int64_t)(s.c1 - s.c0) * kVec<T>, a.K);
   const Lds l = lds_of(mem, a.K, words);
   Chunk<T> v[kBatch];
   if (row_wave) {
@@ -690,7 +699,7 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_grad_kernel(Distill
         l.idx[k] = i[u];
         l.p[k] = p[u];
         l.z[k] = z[u];
-        if (i[u] >= 0) dup |= mark<false>(l.bits, i[u], lo, hi);
+        if (i[u] >= 0) dup |= mark<false>(l.bits, a.K, i[u], lo, hi);
       }
     }
     const bool any = __any(dup);
@@ -817,13 +826,13 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
     dup = false;
     clear_marks(l.bits, words);
     for (int k = lane; k < a.K && !dead; k += 64) {
-      const Entry e = {a.tidx[n * a.K + k], saved[4 + k]};
-      const bool ok = e.i >= 0 && e.i < (int64_t)r.V;
-      l.idx[k] = ok ? e.i : -1;
-      l.p[k] = e.t;
+      const int i = a.tidx[n * a.K + k];
+      const bool ok = i >= 0 && i < (int64_t)r.V;
+      l.idx[k] = ok ? i : -1;
+      l.p[k] = saved[4 + k];
       if (ok) {
-        l.z[k] = (float)r.z[e.i];
-        dup |= mark<false>(l.bits, e.i, 0, (int64_t)r.V);
+        l.z[k] = (float)r.z[i];
+        dup |= mark<false>(l.bits, a.K, i, 0, (int64_t)r.V);
       }
     }
     dup = __any(dup);
@@ -884,7 +893,7 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
 }
 
 size_t lds_bytes(int K, bool tail, int64_t tokens) {
-  return (size_t)K * 12 + (size_t)mark_words(tail, tokens) * 4;
+  return (size_t)K * 12 + (size_t)mark_words(tail, tokens, K) * 4;
 }
 
 int elem_size(int type) { return type == 0 ? 4 : 2; }
@@ -915,7 +924,7 @@ bool by_waves(int64_t N, int64_t chunks, bool fused) {
 template <typename T, int PASS, bool TAIL>
 hipError_t wave_launch(const DistillArgs& a, hipStream_t s) {
   const int64_t chunks = (a.V + 2 * kVec<T> - 2) / kVec<T>;  // at most, for any alignment
-  const uint32_t words = mark_words(TAIL, chunks * kVec<T>);
+  const uint32_t words = mark_words(TAIL, chunks * kVec<T>, a.K);
   const size_t lds = (size_t)kWaveRows * 4 * (words + 3 * (size_t)((a.K + 3) / 4 * 4));
   const dim3 grid((uint32_t)((a.N + kWaveRows - 1) / kWaveRows));
   const dim3 block(64 * (PASS == kGradient ? kWaveRows : kWaveRows + teacher_waves(a.K)));
