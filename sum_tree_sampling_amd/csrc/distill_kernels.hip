@@ -333,8 +333,8 @@ __device__ __forceinline__ void add_chunk(const Chunk<T>& v, float m, float c, u
 // NT threads hold the row, R chunks each, so it is read once: the largest logit,
 // the sum and the gradient are three passes over registers.  512 threads of 17
 // chunks leave room for two rows to a CU, one loading while the other stores (8192
-// x 65536 bf16, fused: 409 us, 5.3 TB/s; with one row of 1024 threads to a CU 637
-// us).  With SIDE one more wave reads the teacher beside them (its chain of loads
+// x 65536 bf16, fused: 388-400 us, 5.4 TB/s; with one row of 1024 threads to a CU
+// 637 us).  With SIDE one more wave reads the teacher beside them (its chain of loads
 // and f64 exponentials is as long as the row's own), else the first wave does.
 // Gradients are stored past the caches: 64 MB 42.8 -> 34.6 us, and the products
 // that read them next take no longer (1 GB with both products of the head: 2915
@@ -352,7 +352,7 @@ void distill_row_kernel(DistillArgs a) {
   const Row<T> r = row_of<T>(a, n);
   T* grad = static_cast<T*>(a.grad) + n * a.grad_stride;
   Entry first = {-1, 0};
-  if (R <= 12 && teacher_wave) first = entry_at(a, n, tid & 63);
+  if (SIDE && teacher_wave) first = entry_at(a, n, tid & 63);
   const float w = a.weight ? a.weight[n] : 1.0f;
   if (w == 0.0f) {
     const float zero[kVec<T>] = {};
@@ -370,13 +370,15 @@ void distill_row_kernel(DistillArgs a) {
   auto read_teacher = [&] {
     if (!teacher_wave) return;
     clear_marks(l.bits, words);
-    if (R > 12) first = entry_at(a, n, tid & 63);
+    if (!SIDE) first = entry_at(a, n, tid & 63);
     entries = read_entries<T, TAIL>(a, r, n, l, true, 0, r.chunks, first);
     if (!SIDE) sums();
   };
-  // The row's loads come first, so that they are in flight meanwhile, unless
-  // they would take the registers the first wave needs for the teacher.
-  if (R > 12) read_teacher();
+  // With SIDE the row's loads go out first.  Without it they would take registers
+  // that the first wave's f64 exponentials need: with the teacher first, three rows
+  // of 9 chunks a thread are on a CU, and two the other way (4096 x 32768 bf16: 105
+  // and 128 us; four and three of 7 chunks, 4096 x 26000 with a rest: 91 and 100).
+  if (!SIDE) read_teacher();
   Chunk<T> v[R];
   if (row_wave) {
 #pragma unroll
@@ -390,7 +392,7 @@ void distill_row_kernel(DistillArgs a) {
       }
     }
   }
-  if (R <= 12) read_teacher();
+  if (SIDE) read_teacher();
   float m = kNegInf;
   if (row_wave) {
 #pragma unroll
@@ -952,11 +954,12 @@ hipError_t row_typed(DistillArgs a, hipStream_t s) {
   a.once = a.N * a.V * (int64_t)sizeof(T) >= (int64_t(1) << 27);
   // Few chunks to a thread and few threads leave room for more rows on a CU (4096 x
   // 10000 bf16: 512 x 9 64 us, 512 x 4 48, 256 x 6 43; 4096 x 20000: 512 x 9 93 us,
-  // 512 x 7 76), more threads are faster where each CU has two rows or fewer (512 x
+  // 512 x 7 75), more threads are faster where each CU has two rows or fewer (512 x
   // 10000 with a rest: 256 x 8 10.3 us, 512 x 4 9.5).  The teacher's extra wave pays
-  // in the small workgroups and where CUs have registers to spare (256 x 32000 with
-  // a rest: 12.3 us, 14.1 without; 512 x 20000 14.7 and 16.1), and otherwise takes
-  // the second row's place on the CU (4096 x 32768: 161 us, 128 without).
+  // in the small workgroups (512 x 11000 with a rest: 10.4 us, 11.8 without; 4096 x
+  // 11000 40 and 42) and where there are few rows (256 x 32000: 12.3 us, 14.1
+  // without); otherwise it takes the next row's place on the CU (1024 x 23000: 32.4
+  // us, 27.6 without).
   if (chunks <= 256 * 4) return row_launch<T, 256, 4, true>(a, s);
   if (chunks <= 256 * 6 && a.N > 512) return row_launch<T, 256, 6, true>(a, s);
   if (chunks <= 512 * 4) return row_launch<T, 512, 4, true>(a, s);
