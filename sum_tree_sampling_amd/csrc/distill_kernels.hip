@@ -385,6 +385,8 @@ void distill_row_kernel(DistillArgs a) {
     for (int q = 0; q < R; ++q) {
       const uint32_t j = tid + q * NT;
       if (j < r.chunks) {
+        // Never with SIDE, yet the branch helps there, too (8192 x 10000 bf16: 73 us,
+        // 78 without).
         v[q] = a.once ? load_chunk<T, true>(r, j) : load_chunk(r, j);
       } else {
 #pragma unroll
@@ -948,10 +950,6 @@ template <typename T>
 hipError_t row_typed(DistillArgs a, hipStream_t s) {
   const int64_t chunks = (a.V + 2 * kVec<T> - 2) / kVec<T>;
   if (by_waves(a.N, chunks, true)) return wave_typed<T, kFused>(a, s);
-  // Logits that fill half of the 256 MB Infinity Cache are loaded past it
-  // (128 MB of bf16 logits at 32768 tokens: 70.5 -> 68.6 us, 1 GB at 65536: 468
-  // -> 460 us; 64 MB the other way: 34.5 -> 37.9 us).
-  a.once = a.N * a.V * (int64_t)sizeof(T) >= (int64_t(1) << 27);
   // Few chunks to a thread and few threads leave room for more rows on a CU (4096 x
   // 10000 bf16: 512 x 9 64 us, 512 x 4 48, 256 x 6 43; 4096 x 20000: 512 x 9 93 us,
   // 512 x 7 75), more threads are faster where each CU has two rows or fewer (512 x
@@ -963,6 +961,10 @@ hipError_t row_typed(DistillArgs a, hipStream_t s) {
   if (chunks <= 256 * 4) return row_launch<T, 256, 4, true>(a, s);
   if (chunks <= 256 * 6 && a.N > 512) return row_launch<T, 256, 6, true>(a, s);
   if (chunks <= 512 * 4) return row_launch<T, 512, 4, true>(a, s);
+  // Long rows that fill half of the 256 MB Infinity Cache are loaded past it (2048 x
+  // 32768 bf16, 128 MB: 61 -> 56 us, 4096: 111 -> 101, 8192 x 65536 403 -> 399), not
+  // fewer (1024 x 32768: 29 -> 32) nor short ones (8192 x 10000: 73 -> 81).
+  a.once = a.N * a.V * (int64_t)sizeof(T) >= (int64_t(1) << 27);
   if (chunks <= 512 * 7)
     return a.N <= 512 ? row_launch<T, 512, 7, true>(a, s) : row_launch<T, 512, 7, false>(a, s);
   if (chunks <= 512 * 9)
