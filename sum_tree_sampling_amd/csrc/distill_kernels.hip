@@ -472,7 +472,7 @@ void distill_row_kernel(DistillArgs a) {
 // Rows longer than a workgroup's registers, few rows, and the two calls apart: 256
 // threads go over a part's chunks, one more wave takes the entries.  A row's parts
 // meet in a second launch of one wave per row (16 x 131071 bf16 with a rest: 5.8 +
-// 3.4 us, and 5.4 for the gradient; 4096 x 32768, forward and backward: 158 us, 5.1
+// 3.4 us, and 5.4 for the gradient; 4096 x 32768, forward and backward: 154 us, 5.2
 // TB/s over three readings and writings).
 constexpr int kPartThreads = 256;
 constexpr int kBatch = 2;  // chunks a thread loads at once
