@@ -333,7 +333,7 @@ __device__ __forceinline__ void add_chunk(const Chunk<T>& v, float m, float c, u
 // NT threads hold the row, R chunks each, so it is read once: the largest logit,
 // the sum and the gradient are three passes over registers.  512 threads of 17
 // chunks leave room for two rows to a CU, one loading while the other stores (8192
-// x 65536 bf16, fused: 388-400 us, 5.4 TB/s; with one row of 1024 threads to a CU
+// x 65536 bf16, fused: 388-412 us, 5.4 TB/s; with one row of 1024 threads to a CU
 // 637 us).  With SIDE one more wave reads the teacher beside them (its chain of loads
 // and f64 exponentials is as long as the row's own), else the first wave does.
 // Gradients are stored past the caches: 64 MB 42.8 -> 34.6 us, and the products
