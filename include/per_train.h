@@ -143,12 +143,13 @@ int per_scan_step(int64_t B, int64_t D, int32_t type, const void* d_x, int64_t x
  *     p_r = max(0, 1 - sum p_k) stands against the student's
  *     q_r = 1 - (the q of the distinct tokens present),
  *   loss_n = tau^2 [sum_k p_k (log p_k - log q_k) + p_r (log p_r - log q_r)],
- * where a term with p = 0 is 0, and so is the rest's when q_r = 0.  The
- * gradient by z_j, scaled by w_n, is tau w_n (q_j - p_j) with p_j the sum of
- * the entries for token j, or in place of p_j, for the tokens of the rest,
- * p_r q_j / q_r.  A row has loss 0 and gradient 0 when no entry is present
- * (without d_tlse) or every student logit is -Inf; NaN and +Inf logits give
- * NaN.
+ * where a term with p = 0 is 0, and so is the rest's when q_r = 0 (no token of
+ * the rest, or all of them at -Inf).  log q_r is taken from the rest's own largest
+ * logit, so it holds as well where q_r is too small for f32.  The gradient by z_j,
+ * scaled by w_n, is tau w_n (q_j - p_j) with p_j the sum of the entries for token
+ * j, or in place of p_j, for the tokens of the rest, p_r q_j / q_r.  A row has
+ * loss 0 and gradient 0 when no entry is present (without d_tlse) or every student
+ * logit is -Inf; NaN and +Inf logits give NaN.
  *
  * d_logits: [N x V] of `type`, stride >= V elements between rows; d_tidx:
  * dense [N x K] i32; d_tlogit: dense [N x K] of tlogit_type; 1 <= K <=
@@ -160,7 +161,9 @@ int per_scan_step(int64_t B, int64_t D, int32_t type, const void* d_x, int64_t x
  *   same stride).
  * per_distill_forward: the losses, and d_saved [N x (4 + K)] f32 (or NULL):
  *   largest logit m, S = sum of exp((z - m) / tau) (0 for a row without loss),
- *   the same over the rest, p_r, and the K probabilities p_k.
+ *   largest logit m_r of the rest, C = exp((m_r - m) / tau) / S - p_r / (sum of
+ *   exp((z - m_r) / tau) over the rest), and the K probabilities p_k.  Without
+ *   d_tlse, or where the rest has no mass, m_r = m and C = 1 / S or 0.
  * per_distill_backward: the gradient from d_saved, weighted by d_gloss [N]
  *   f32, the gradient by each row's loss; d_grad may be d_logits.
  * per_distill_workspace_bytes: device workspace of per_distill and

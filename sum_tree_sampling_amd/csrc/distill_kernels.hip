@@ -1,11 +1,15 @@
 // distill_kernels.hip -- distillation from a teacher's top logits: per-row loss
 // and its gradient by the student's logits.
 //
-// With m the row's largest logit, S = sum exp((z - m) / tau) over all tokens
-// and S_r the same over the tokens of the rest, the gradient by z_j is
-//   w tau (e_j / S - p_j)             at a token of the teacher's top,
-//   w tau e_j (1 / S - p_r / S_r)     at the others (p_r = 0 without a rest),
+// With m the row's largest logit and S = sum exp((z - m) / tau) over all tokens,
+// m_r and S_r the same over the tokens of the rest, the gradient by z_j is
+//   w tau (exp((z_j - m) / tau) / S - p_j)   at a token of the teacher's top,
+//   w tau C exp((z_j - m_r) / tau)           at the others,
+//   C = exp((m_r - m) / tau) / S - p_r / S_r,
 // so one coefficient serves the whole row and K places are put right after.
+// Without a rest m_r = m and C = 1 / S.  The rest has its own largest logit
+// because the row's may be a top token so far above it that every exp((z - m) /
+// tau) of the rest is 0 in f32, where log q_r is an ordinary number.
 //
 // A row is read in 16-byte chunks aligned in memory; chunk j holds the tokens
 // [j * kVec - mis, (j + 1) * kVec - mis).  The tokens of the top are marked in
@@ -195,6 +199,7 @@ __device__ __forceinline__ bool mark(uint32_t* bits, int K, int i, int64_t lo, i
 struct Entries {
   float tm, z0;  // largest teacher's and student's logits of the entries present
   bool any, dup;
+  uint32_t own;  // bit r: the entry of the lane's round r is the first of its token in the span
 };
 template <typename T, bool TAIL>
 __device__ __forceinline__ Entries read_entries(const DistillArgs& a, const Row<T>& r, int64_t n,
@@ -203,9 +208,10 @@ __device__ __forceinline__ Entries read_entries(const DistillArgs& a, const Row<
   const int first = threadIdx.x & ((1 << lg) - 1);
   const int64_t lo = (int64_t)c0 * kVec<T> - r.mis;
   const int64_t hi = (int64_t)c1 * kVec<T> - r.mis;
-  Entries o = {kNegInf, kNegInf, false, false};
+  Entries o = {kNegInf, kNegInf, false, false, 0};
   if (n >= a.N) return o;
-  for (int k = first; k < a.K; k += 1 << lg) {
+  uint32_t round = 1;
+  for (int k = first; k < a.K; k += 1 << lg, round <<= 1) {
     if (k != first) e = entry_at(a, n, k);
     const int i = e.i < 0 || e.i >= (int64_t)r.V ? -1 : e.i;
     const float z = i >= 0 ? (float)r.z[i] : kNegInf;
@@ -213,7 +219,11 @@ __device__ __forceinline__ Entries read_entries(const DistillArgs& a, const Row<
     if (i >= 0) {
       o.any = true;
       o.tm = fmaxf(o.tm, t);
-      if (marks) o.dup |= mark<TAIL>(l.bits, a.K, i, lo, hi);
+      if (marks) {
+        const bool again = mark<TAIL>(l.bits, a.K, i, lo, hi);
+        o.dup |= again;
+        if (!again && i >= lo && i < hi) o.own |= round;
+      }
     }
     l.idx[k] = i;
     l.p[k] = t;
@@ -272,17 +282,52 @@ __device__ __forceinline__ Teacher sum_entries(const DistillArgs& a, int64_t n, 
   return o;
 }
 
+// The student's side of a row: m and S, m_r and S_r (S_r = 0, m_r = m where no
+// token of the rest has mass, or without a rest).
+struct Student {
+  float m, S, mr, Sr;
+};
+
 // The row's loss from the teacher's sums and the student's statistics:
 //   sum p (log p - log q) = h - log norm + ps log S - sum p (z - m) / tau
 // (norm = 1 with a rest, ps = 1 without one), and the rest's term.
-__device__ __forceinline__ float row_loss(const DistillArgs& a, const Teacher& t, float m, float S,
-                                          float Sr, bool tail) {
-  const double logS = log((double)S / t.norm);
+__device__ __forceinline__ float row_loss(const DistillArgs& a, const Teacher& t, const Student& s,
+                                          bool tail) {
+  const double logS = log((double)s.S / t.norm);
   double v = t.h + t.ps * logS;
-  if (t.ps != 0.0) v -= (t.pz + t.ps * ((double)t.z0 - (double)m)) * a.inv_tau;
-  if (tail && t.rest > 0.0 && Sr != 0.0f) v += t.rest * log(t.rest * (double)S / (double)Sr);
+  if (t.ps != 0.0) v -= (t.pz + t.ps * ((double)t.z0 - (double)s.m)) * a.inv_tau;
+  if (tail && t.rest > 0.0 && s.Sr != 0.0f)
+    v += t.rest * (log(t.rest * (double)s.S / (double)s.Sr) -
+                   ((double)s.mr - (double)s.m) * a.inv_tau);
   return (float)(v * (double)a.tau * (double)a.tau);
 }
+
+// C.  With one maximum the two quotients are one rounded difference over the
+// product.
+template <bool TAIL>
+__device__ __forceinline__ float rest_coef(const DistillArgs& a, const Student& s, float p_rest) {
+  if (!TAIL) return 1.0f / s.S;
+  if (s.Sr == 0.0f) return 0.0f;
+  if (s.mr == s.m) return __builtin_fmaf(-p_rest, s.S, s.Sr) / (s.S * s.Sr);
+  return ex2((s.mr - s.m) * a.c) / s.S - p_rest / s.Sr;
+}
+
+// What a row's gradient needs from the forward pass: m, S (0: the row has no
+// loss), m_r, C, behind which its probabilities p_k stand.
+template <bool TAIL>
+__device__ __forceinline__ void save_row(const DistillArgs& a, int64_t n, bool dead,
+                                         const Student& s, float p_rest) {
+  float* to = a.saved + n * (4 + a.K);
+  to[0] = s.m;
+  to[1] = dead ? 0.0f : s.S;
+  to[2] = s.mr;
+  to[3] = dead ? 0.0f : rest_coef<TAIL>(a, s, p_rest);
+}
+
+// Where the rest's sum against the row's largest logit is below this, it is taken
+// again against its own: above, what its smallest terms lose to underflow is less
+// than 2^-42 of it (2^24 terms below 2^-126).
+constexpr float kFar = 0x1p-60f;
 
 // Puts right the gradient at the teacher's tokens within [lo, hi).
 template <typename T>
@@ -326,6 +371,24 @@ __device__ __forceinline__ void add_chunk(const Chunk<T>& v, float m, float c, u
       else rest += x;
     }
   }
+}
+
+// A chunk's largest logit and m, and its sum against m, without its marked tokens.
+template <typename T>
+__device__ __forceinline__ float rest_max(const Chunk<T>& v, uint32_t marks, float m) {
+  float z[kVec<T>];
+  unpack(v, z);
+#pragma unroll
+  for (int e = 0; e < kVec<T>; ++e) m = (marks >> e) & 1u ? m : fmaxf(m, z[e]);
+  return m;
+}
+template <typename T>
+__device__ __forceinline__ float rest_sum(const Chunk<T>& v, uint32_t marks, float m, float c) {
+  float z[kVec<T>], s = 0.0f;
+  unpack(v, z);
+#pragma unroll
+  for (int e = 0; e < kVec<T>; ++e) s += (marks >> e) & 1u ? 0.0f : ex2((z[e] - m) * c);
+  return s;
 }
 
 // ------------------------------------------------- one workgroup holds the row
@@ -438,14 +501,47 @@ void distill_row_kernel(DistillArgs a) {
     if (TAIL) top += red[2][q];
   }
   const float S = rest + top;
+  float mr = m;
+  if (TAIL && rest < kFar) {  // the same in every thread
+    if (row_wave) {
+      mr = kNegInf;
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const uint32_t j = tid + q * NT;
+        if (j < r.chunks) mr = rest_max<T>(v[q], chunk_bits<T>(l.bits, j), mr);
+        keep_packed<T>(v[q]);
+      }
+      mr = wave_max(mr);
+      if ((tid & 63) == 0) red[0][wv] = mr;
+    }
+    __syncthreads();
+    mr = red[0][0];
+#pragma unroll
+    for (int q = 1; q < NT / 64; ++q) mr = fmaxf(mr, red[0][q]);
+    rest = 0.0f;
+    if (mr == kNegInf) {
+      mr = m;
+    } else {
+      if (row_wave) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          const uint32_t j = tid + q * NT;
+          if (j < r.chunks) rest += rest_sum<T>(v[q], chunk_bits<T>(l.bits, j), mr, a.c);
+          keep_packed<T>(v[q]);
+        }
+        rest = wave_sum(rest);
+        if ((tid & 63) == 0) red[1][wv] = rest;
+      }
+      __syncthreads();
+      rest = 0.0f;
+#pragma unroll
+      for (int q = 0; q < NT / 64; ++q) rest += red[1][q];
+    }
+  }
+  const Student st = {m, S, mr, rest};
   const bool dead = S == 0.0f || (!TAIL && !t.any);
   const float scale = dead ? 0.0f : w * a.tau;
-  // 1 / S - p_r / S_r as one rounded difference over the product
-  float coef = 0.0f;
-  if (!dead)
-    coef = TAIL ? (rest == 0.0f ? 0.0f
-                                : scale * (__builtin_fmaf(-(float)t.rest, S, rest) / (S * rest)))
-                : scale / S;
+  const float coef = dead ? 0.0f : scale * rest_coef<TAIL>(a, st, (float)t.rest);
   if (row_wave) {
 #pragma unroll
     for (int q = 0; q < R; ++q) {
@@ -454,13 +550,13 @@ void distill_row_kernel(DistillArgs a) {
         float z[kVec<T>], g[kVec<T>];
         unpack(v[q], z);
 #pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) g[e] = dead ? 0.0f : coef * ex2((z[e] - m) * a.c);
+        for (int e = 0; e < kVec<T>; ++e) g[e] = dead ? 0.0f : coef * ex2((z[e] - mr) * a.c);
         store_chunk(grad, r, j, g);
       }
     }
   }
   if (teacher_wave) {
-    const float loss = dead ? 0.0f : row_loss(a, t, m, S, rest, TAIL);
+    const float loss = dead ? 0.0f : row_loss(a, t, st, TAIL);
     if ((tid & 63) == 0) a.loss[n] = loss;
   }
   __syncthreads();
@@ -505,25 +601,45 @@ __device__ __forceinline__ void load_batch(const Row<T>& r, uint32_t j0, uint32_
   }
 }
 
+// Statistics of a part: largest logit and sum of exp((z - largest) / tau) over the
+// tokens of the rest (of all tokens without one), and over the top's.
+struct Part {
+  float mr, rest, mt, top;
+};
+constexpr Part kNoPart = {kNegInf, 0.0f, kNegInf, 0.0f};
+
+// Factor that takes a sum against `from` to one against `to`, where `to` is not
+// smaller.  -Inf comes with a sum of 0, or NaN where nothing but NaN was seen.
+__device__ __forceinline__ float shift(float from, float to, float sum, float c) {
+  return from == kNegInf ? (sum == sum ? 0.0f : 1.0f) : ex2((from - to) * c);
+}
+
 // A row's loss and what its gradient needs, by one wave.
 template <bool TAIL>
 __device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t n, bool off,
-                                           const Teacher& t, float m, float rest, float top) {
-  if (m == kNegInf) m = 0.0f;
-  float S = rest + top;
-  const bool dead = off || S == 0.0f || (!TAIL && !t.any);
-  if (dead) S = rest = 0.0f;
-  const float loss = dead ? 0.0f : row_loss(a, t, m, S, rest, TAIL);
+                                           const Teacher& t, const Part& p) {
+  Student s;
+  s.m = TAIL ? fmaxf(p.mr, p.mt) : p.mr;
+  s.S = p.rest * shift(p.mr, s.m, p.rest, a.c);
+  if (TAIL) s.S += p.top * shift(p.mt, s.m, p.top, a.c);
+  if (s.m == kNegInf) s.m = 0.0f;
+  s.mr = p.mr == kNegInf ? s.m : p.mr;
+  s.Sr = p.rest;
+  const bool dead = off || s.S == 0.0f || (!TAIL && !t.any);
+  const float loss = dead ? 0.0f : row_loss(a, t, s, TAIL);
   if ((threadIdx.x & 63) == 0) {
     a.loss[n] = loss;
-    if (a.saved) {
-      float* s = a.saved + n * (4 + a.K);
-      s[0] = m;
-      s[1] = S;
-      s[2] = rest;
-      s[3] = (float)t.rest;
-    }
+    if (a.saved) save_row<TAIL>(a, n, dead, s, (float)t.rest);
   }
+}
+
+// Takes the marked tokens out of a chunk: -Inf has no mass.  Once per chunk here;
+// where a row stays in registers, the selects of rest_max and rest_sum take fewer.
+template <typename T>
+__device__ __forceinline__ void drop_top(Chunk<T>& v, uint32_t marks) {
+  if (marks == 0) return;
+#pragma unroll
+  for (int e = 0; e < kVec<T>; ++e) v.v[e] = (marks >> e) & 1u ? (T)kNegInf : v.v[e];
 }
 
 // Largest logit and sums of one part of a row; the first part's extra wave
@@ -531,16 +647,17 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t n, bool
 template <typename T, bool TAIL>
 __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(DistillArgs a) {
   extern __shared__ char mem[];
-  __shared__ float red[3][kPartThreads / 64];
+  __shared__ float red[2][kPartThreads / 64];
+  __shared__ float top_mt, top_sum;
   __shared__ Teacher whole;  // where the part is the row
   const int64_t n = blockIdx.x / (uint32_t)a.splits;
   const int split = (int)(blockIdx.x % (uint32_t)a.splits);
   const int tid = threadIdx.x, wv = tid >> 6;
   const bool row_wave = wv < kPartThreads / 64;
-  float* part = a.part + (int64_t)blockIdx.x * 4;
+  Part* part = reinterpret_cast<Part*>(a.part) + blockIdx.x;
   if (a.weight && a.weight[n] == 0.0f) {
-    if (tid == 0) part[0] = kNegInf, part[1] = part[2] = 0.0f;
-    if (a.splits == 1 && !row_wave) finish_row<TAIL>(a, n, true, Teacher{}, 0.0f, 0.0f, 0.0f);
+    if (tid == 0) *part = kNoPart;
+    if (a.splits == 1 && !row_wave) finish_row<TAIL>(a, n, true, Teacher{}, kNoPart);
     return;
   }
   const Row<T> r = row_of<T>(a, n);
@@ -557,11 +674,15 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
       clear_marks(l.bits, words);
       entries = read_entries<T, TAIL>(a, r, n, l, TAIL, s.c0, s.c1, first);
     } else if (TAIL) {
+      const int64_t lo = (int64_t)s.c0 * kVec<T> - r.mis, hi = (int64_t)s.c1 * kVec<T> - r.mis;
       clear_marks(l.bits, words);
-      for (int k = tid & 63; k < a.K; k += 64) {
+      entries.own = 0;
+      uint32_t round = 1;
+      for (int k = tid & 63; k < a.K; k += 64, round <<= 1) {
         const int i = a.tidx[n * a.K + k];
-        if (i >= 0 && i < (int64_t)r.V)
-          mark<true>(l.bits, a.K, i, (int64_t)s.c0 * kVec<T> - r.mis, (int64_t)s.c1 * kVec<T> - r.mis);
+        if (i < 0 || i >= (int64_t)r.V || i < lo || i >= hi) continue;
+        l.z[k] = (float)r.z[i];
+        if (!mark<true>(l.bits, a.K, i, lo, hi)) entries.own |= round;
       }
     }
   }
@@ -572,63 +693,58 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
     if (a.saved)
       for (int k = tid & 63; k < a.K; k += 64) a.saved[n * (4 + a.K) + 4 + k] = l.p[k];
   }
-  float m = kNegInf, rest = 0.0f, top = 0.0f;
+  if (TAIL && !row_wave) {  // the top's tokens of the part, each once
+    float mt = kNegInf, top = 0.0f;
+    uint32_t own = entries.own;
+    for (int k = tid & 63; k < a.K; k += 64, own >>= 1)
+      if (own & 1u) mt = fmaxf(mt, l.z[k]);
+    mt = wave_max(mt);
+    own = entries.own;
+    for (int k = tid & 63; k < a.K; k += 64, own >>= 1)
+      if (own & 1u) top += ex2((l.z[k] - (mt == kNegInf ? 0.0f : mt)) * a.c);
+    top = wave_sum(top);
+    if ((tid & 63) == 0) top_mt = mt, top_sum = top;
+  }
+  Part o = kNoPart;
   if (row_wave) {
     for (uint32_t j0 = s.c0 + tid; j0 < s.c1; j0 += kBatch * kPartThreads) {
-      float mb = m;
-#pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        float z[kVec<T>];
-        unpack(v[q], z);
-#pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) mb = fmaxf(mb, z[e]);
-      }
-      if (mb > m) {
-        const float k = m == kNegInf ? 0.0f : ex2((m - mb) * a.c);
-        rest *= k;
-        top *= k;
-        m = mb;
-      }
-      const float ms = m == kNegInf ? 0.0f : m;
+      float mb = o.mr;
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         const uint32_t j = j0 + q * kPartThreads;
-        if (j < s.c1)
-          add_chunk<T, TAIL>(v[q], ms, a.c, TAIL ? chunk_bits<T>(l.bits, j - s.c0) : 0u, rest, top);
+        if (TAIL && j < s.c1) drop_top<T>(v[q], chunk_bits<T>(l.bits, j - s.c0));
+        mb = rest_max<T>(v[q], 0, mb);
+      }
+      if (mb > o.mr) {
+        o.rest *= shift(o.mr, mb, o.rest, a.c);
+        o.mr = mb;
+      }
+      const float ms = o.mr == kNegInf ? 0.0f : o.mr;
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const uint32_t j = j0 + q * kPartThreads;
+        if (j < s.c1) o.rest += rest_sum<T>(v[q], 0, ms, a.c);
       }
       if (j0 + kBatch * kPartThreads < s.c1) load_batch(r, j0 + kBatch * kPartThreads, s.c1, v);
     }
-    const float mw = wave_max(m);
+    const float mw = wave_max(o.mr);
     if ((tid & 63) == 0) red[0][wv] = mw;
   }
   __syncthreads();
-  float mw = red[0][0];
+  Part all = kNoPart;
 #pragma unroll
-  for (int q = 1; q < kPartThreads / 64; ++q) mw = fmaxf(mw, red[0][q]);
+  for (int q = 0; q < kPartThreads / 64; ++q) all.mr = fmaxf(all.mr, red[0][q]);
+  if (TAIL) all.mt = top_mt, all.top = top_sum;
   if (row_wave) {
-    const float k = m == kNegInf ? (rest == rest ? 0.0f : 1.0f) : ex2((m - mw) * a.c);
-    rest = wave_sum(rest * k);
-    top = wave_sum(top * k);
-    if ((tid & 63) == 0) {
-      red[1][wv] = rest;
-      red[2][wv] = top;
-    }
+    const float rest = wave_sum(o.rest * shift(o.mr, all.mr, o.rest, a.c));
+    if ((tid & 63) == 0) red[1][wv] = rest;
   }
   __syncthreads();
   if (a.splits == 1 ? row_wave : tid != 0) return;
-  rest = top = 0.0f;
 #pragma unroll
-  for (int q = 0; q < kPartThreads / 64; ++q) {
-    rest += red[1][q];
-    top += red[2][q];
-  }
-  if (a.splits == 1) {
-    finish_row<TAIL>(a, n, false, whole, mw, rest, top);
-  } else {
-    part[0] = mw;
-    part[1] = rest;
-    part[2] = top;
-  }
+  for (int q = 0; q < kPartThreads / 64; ++q) all.rest += red[1][q];
+  if (a.splits == 1) finish_row<TAIL>(a, n, false, whole, all);
+  else *part = all;
 }
 
 // Joins a row's parts; one wave per row.
@@ -636,22 +752,25 @@ template <bool TAIL>
 __global__ __launch_bounds__(64) void distill_join_kernel(DistillArgs a) {
   const int64_t n = blockIdx.x;
   const int lane = threadIdx.x;
-  const float* part = a.part + n * a.splits * 4;
+  const Part* part = reinterpret_cast<const Part*>(a.part) + n * a.splits;
   const bool off = a.weight && a.weight[n] == 0.0f;
   Teacher t = {0.0, 0.0, 0.0, 0.0, 1.0, 0.0f, false, false};
   if (!off) t = a.teacher[n];
-  float m = kNegInf, rest = 0.0f, top = 0.0f;
-  for (int q = lane; q < a.splits; q += 64) m = fmaxf(m, part[4 * q]);
-  m = wave_max(m);
+  Part all = kNoPart;
   for (int q = lane; q < a.splits; q += 64) {
-    const float pm = part[4 * q], pr = part[4 * q + 1], pt = part[4 * q + 2];
-    const float k = pm == kNegInf ? (pr == pr ? 0.0f : 1.0f) : ex2((pm - m) * a.c);
-    rest += pr * k;
-    top += pt * k;
+    all.mr = fmaxf(all.mr, part[q].mr);
+    if (TAIL) all.mt = fmaxf(all.mt, part[q].mt);
   }
-  rest = wave_sum(rest);
-  top = wave_sum(top);
-  finish_row<TAIL>(a, n, off, t, m, rest, top);
+  all.mr = wave_max(all.mr);
+  if (TAIL) all.mt = wave_max(all.mt);
+  for (int q = lane; q < a.splits; q += 64) {
+    const Part p = part[q];
+    all.rest += p.rest * shift(p.mr, all.mr, p.rest, a.c);
+    if (TAIL) all.top += p.top * shift(p.mt, all.mt, p.top, a.c);
+  }
+  all.rest = wave_sum(all.rest);
+  if (TAIL) all.top = wave_sum(all.top);
+  finish_row<TAIL>(a, n, off, t, all);
 }
 
 constexpr int kAhead = 4;  // entries a lane loads at once
@@ -670,7 +789,7 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_grad_kernel(Distill
   T* grad = static_cast<T*>(a.grad) + n * a.grad_stride;
   const float* saved = a.saved + n * (4 + a.K);
   const float w = a.weight ? a.weight[n] : 1.0f;
-  const float m = saved[0], S = saved[1], rest = saved[2];
+  const float m = saved[0], S = saved[1], mr = saved[2];
   if (w == 0.0f || S == 0.0f) {
     const float zero[kVec<T>] = {};
     for (uint32_t j = s.c0 + tid; j < s.c1; j += kPartThreads + 64) store_chunk(grad, r, j, zero);
@@ -712,9 +831,7 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_grad_kernel(Distill
   __syncthreads();  // the top's logits are read before they may be overwritten
   const float scale = w * a.tau;
   if (row_wave) {
-    const float coef =
-        TAIL ? (rest == 0.0f ? 0.0f : scale * (__builtin_fmaf(-saved[3], S, rest) / (S * rest)))
-             : scale / S;
+    const float coef = scale * saved[3];
     for (uint32_t j0 = s.c0 + tid; j0 < s.c1; j0 += kBatch * kPartThreads) {
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
@@ -723,7 +840,7 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_grad_kernel(Distill
           float z[kVec<T>], g[kVec<T>];
           unpack(v[q], z);
 #pragma unroll
-          for (int e = 0; e < kVec<T>; ++e) g[e] = coef * ex2((z[e] - m) * a.c);
+          for (int e = 0; e < kVec<T>; ++e) g[e] = coef * ex2((z[e] - mr) * a.c);
           store_chunk(grad, r, j, g);
         }
       }
@@ -761,7 +878,7 @@ template <typename T, int R, bool TAIL, int PASS>
 __global__ __launch_bounds__(PASS == kGradient ? 64 * kWaveRows : 128 * kWaveRows)
 void distill_wave_kernel(DistillArgs a, uint32_t words) {
   extern __shared__ char mem[];
-  __shared__ float stat[kWaveRows][3];
+  __shared__ Student stat[kWaveRows];
   __shared__ Teacher teachers[kWaveRows];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -787,16 +904,10 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
     __syncthreads();
     if (q < kWaveRows && k0 == 0 && n < a.N) {
       const float w = PASS == kFused && a.weight ? a.weight[n] : 1.0f;
-      const float m = stat[q][0], S = stat[q][1], Sr = stat[q][2];
-      const bool dead = w == 0.0f || S == 0.0f || (!TAIL && !t.any);
-      a.loss[n] = dead ? 0.0f : row_loss(a, t, m, S, Sr, TAIL);
-      if (PASS == kLoss && a.saved) {
-        float* s = a.saved + n * (4 + a.K);
-        s[0] = m;
-        s[1] = dead ? 0.0f : S;
-        s[2] = Sr;
-        s[3] = (float)t.rest;
-      }
+      const Student s = stat[q];
+      const bool dead = w == 0.0f || s.S == 0.0f || (!TAIL && !t.any);
+      a.loss[n] = dead ? 0.0f : row_loss(a, t, s, TAIL);
+      if (PASS == kLoss && a.saved) save_row<TAIL>(a, n, dead, s, (float)t.rest);
     }
     return;
   }
@@ -818,15 +929,16 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
       for (int e = 0; e < kVec<T>; ++e) v[q].v[e] = (T)kNegInf;
     }
   }
-  float m, S, rest, p_rest = 0.0f;
+  Student s;
+  float p_rest = 0.0f, saved_coef = 0.0f;
   bool dead, dup;
   if (PASS == kGradient) {
     const float* saved = a.saved + (here ? n : 0) * (4 + a.K);
-    m = saved[0];
-    S = saved[1];
-    rest = saved[2];
-    p_rest = saved[3];
-    dead = w == 0.0f || S == 0.0f;
+    s.m = saved[0];
+    s.S = saved[1];
+    s.mr = saved[2];
+    saved_coef = saved[3];
+    dead = w == 0.0f || s.S == 0.0f;
     dup = false;
     clear_marks(l.bits, words);
     for (int k = lane; k < a.K && !dead; k += 64) {
@@ -841,7 +953,7 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
     }
     dup = __any(dup);
   } else {
-    m = kNegInf;
+    float m = kNegInf;
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       float z[kVec<T>];
@@ -852,8 +964,7 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
     m = wave_max(m);
     if (m == kNegInf) m = 0.0f;
     if (TAIL) __syncthreads();  // the marks
-    float top = 0.0f;
-    rest = 0.0f;
+    float rest = 0.0f, top = 0.0f;
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       const uint32_t j = lane + q * 64;
@@ -862,25 +973,38 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
     }
     rest = wave_sum(rest);
     if (TAIL) top = wave_sum(top);
-    S = rest + top;
-    if (lane == 0) {
-      stat[wv][0] = m;
-      stat[wv][1] = S;
-      stat[wv][2] = rest;
+    s = {m, rest + top, m, rest};
+    if (TAIL && w != 0.0f && rest < kFar) {  // the same in every lane
+      float mr = kNegInf;
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const uint32_t j = lane + q * 64;
+        if (j < r.chunks) mr = rest_max<T>(v[q], chunk_bits<T>(l.bits, j), mr);
+      }
+      mr = wave_max(mr);
+      rest = 0.0f;
+      if (mr != kNegInf) {
+        s.mr = mr;
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          const uint32_t j = lane + q * 64;
+          if (j < r.chunks) rest += rest_sum<T>(v[q], chunk_bits<T>(l.bits, j), mr, a.c);
+        }
+        rest = wave_sum(rest);
+      }
+      s.Sr = rest;
     }
+    if (lane == 0) stat[wv] = s;
     __syncthreads();  // the teachers, whose logits are read before they may be overwritten
     const Teacher t = teachers[wv];
-    dead = w == 0.0f || S == 0.0f || (!TAIL && !t.any);
+    dead = w == 0.0f || s.S == 0.0f || (!TAIL && !t.any);
     dup = t.dup;
     p_rest = (float)t.rest;
   }
   if (PASS != kLoss && here) {
     const float scale = dead ? 0.0f : w * a.tau;
-    float coef = 0.0f;
-    if (!dead)
-      coef = TAIL ? (rest == 0.0f ? 0.0f
-                                  : scale * (__builtin_fmaf(-p_rest, S, rest) / (S * rest)))
-                  : scale / S;
+    const float coef =
+        dead ? 0.0f : scale * (PASS == kGradient ? saved_coef : rest_coef<TAIL>(a, s, p_rest));
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       const uint32_t j = lane + q * 64;
@@ -888,11 +1012,11 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
         float z[kVec<T>], g[kVec<T>];
         unpack(v[q], z);
 #pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) g[e] = dead ? 0.0f : coef * ex2((z[e] - m) * a.c);
+        for (int e = 0; e < kVec<T>; ++e) g[e] = dead ? 0.0f : coef * ex2((z[e] - s.mr) * a.c);
         store_chunk(grad, r, j, g);
       }
     }
-    if (!dead) patch_top(a, l, grad, m, S, scale, dup, 0, (int64_t)r.V, lane, 64);
+    if (!dead) patch_top(a, l, grad, s.m, s.S, scale, dup, 0, (int64_t)r.V, lane, 64);
   }
 }
 
