@@ -153,7 +153,9 @@ int per_scan_step(int64_t B, int64_t D, int32_t type, const void* d_x, int64_t x
  *
  * d_logits: [N x V] of `type`, stride >= V elements between rows; d_tidx:
  * dense [N x K] i32; d_tlogit: dense [N x K] of tlogit_type; 1 <= K <=
- * PER_MAX_TOP; 2^-20 <= tau <= 2^20.
+ * PER_MAX_TOP; 2^-20 <= tau <= 2^6.  The loss is tau^2 times a difference of
+ * logarithms of sums, so its error grows as tau^2 whatever its own size: sums are
+ * f32 within a thread and f64 from there on, which leaves about 2^-31 tau^2.
  *
  * per_distill: loss and gradient in one call.  d_weight: [N] f32 or NULL (1);
  *   the losses are not weighted, the gradient is; a row of weight 0 is not

@@ -11,6 +11,11 @@
 // because the row's may be a top token so far above it that every exp((z - m) /
 // tau) of the rest is 0 in f32, where log q_r is an ordinary number.
 //
+// A thread's sums are f32, chunk by chunk; what threads join is f64.  The loss is
+// tau^2 times a difference of logarithms of S and S_r, in which the roundings of
+// joins in f32 stood out: of a student near its teacher (V = 120000, tau = 32) they
+// left an error of 8e-5 in a loss of 8e-7, and leave 3e-9 now.
+//
 // A row is read in 16-byte chunks aligned in memory; chunk j holds the tokens
 // [j * kVec - mis, (j + 1) * kVec - mis).  The tokens of the top are marked in
 // a bitmap in LDS, so sums over the rest leave them out instead of
@@ -285,7 +290,8 @@ __device__ __forceinline__ Teacher sum_entries(const DistillArgs& a, int64_t n, 
 // The student's side of a row: m and S, m_r and S_r (S_r = 0, m_r = m where no
 // token of the rest has mass, or without a rest).
 struct Student {
-  float m, S, mr, Sr;
+  float m, mr;
+  double S, Sr;
 };
 
 // The row's loss from the teacher's sums and the student's statistics:
@@ -293,35 +299,41 @@ struct Student {
 // (norm = 1 with a rest, ps = 1 without one), and the rest's term.
 __device__ __forceinline__ float row_loss(const DistillArgs& a, const Teacher& t, const Student& s,
                                           bool tail) {
-  const double logS = log((double)s.S / t.norm);
+  const double logS = log(s.S / t.norm);
   double v = t.h + t.ps * logS;
   if (t.ps != 0.0) v -= (t.pz + t.ps * ((double)t.z0 - (double)s.m)) * a.inv_tau;
-  if (tail && t.rest > 0.0 && s.Sr != 0.0f)
-    v += t.rest * (log(t.rest * (double)s.S / (double)s.Sr) -
-                   ((double)s.mr - (double)s.m) * a.inv_tau);
+  if (tail && t.rest > 0.0 && s.Sr != 0.0)
+    v += t.rest * (log(t.rest * s.S / s.Sr) - ((double)s.mr - (double)s.m) * a.inv_tau);
   return (float)(v * (double)a.tau * (double)a.tau);
 }
 
-// C.  With one maximum the two quotients are one rounded difference over the
-// product.
+// C in f32, by every thread.  With one maximum it is (S_r - p_r S) / (S S_r), the
+// difference taken as (1 - p_r) S_r - p_r S_t with S_t = S - S_r: S_r and p_r S agree
+// in most of their digits where the top holds little or tau is large.
 template <bool TAIL>
-__device__ __forceinline__ float rest_coef(const DistillArgs& a, const Student& s, float p_rest) {
-  if (!TAIL) return 1.0f / s.S;
-  if (s.Sr == 0.0f) return 0.0f;
-  if (s.mr == s.m) return __builtin_fmaf(-p_rest, s.S, s.Sr) / (s.S * s.Sr);
-  return ex2((s.mr - s.m) * a.c) / s.S - p_rest / s.Sr;
+__device__ __forceinline__ float rest_coef(const DistillArgs& a, float m, float S, float mr,
+                                           float Sr, float St, double p_rest) {
+  if (!TAIL) return 1.0f / S;
+  if (Sr == 0.0f) return 0.0f;
+  const float pr = (float)p_rest, pt = (float)(1.0 - p_rest);
+  if (mr == m) return (pt * Sr - pr * St) / (S * Sr);
+  return ex2((mr - m) * a.c) / S - pr / Sr;
 }
 
 // What a row's gradient needs from the forward pass: m, S (0: the row has no
 // loss), m_r, C, behind which its probabilities p_k stand.
 template <bool TAIL>
 __device__ __forceinline__ void save_row(const DistillArgs& a, int64_t n, bool dead,
-                                         const Student& s, float p_rest) {
+                                         const Student& s, double p_rest) {
+  const double C = !TAIL ? 1.0 / s.S
+                   : s.Sr == 0.0
+                       ? 0.0
+                       : exp(((double)s.mr - (double)s.m) * a.inv_tau) / s.S - p_rest / s.Sr;
   float* to = a.saved + n * (4 + a.K);
   to[0] = s.m;
-  to[1] = dead ? 0.0f : s.S;
+  to[1] = dead ? 0.0f : (float)s.S;
   to[2] = s.mr;
-  to[3] = dead ? 0.0f : rest_coef<TAIL>(a, s, p_rest);
+  to[3] = dead ? 0.0f : (float)C;
 }
 
 // Where the rest's sum against the row's largest logit is below this, it is taken
@@ -358,19 +370,20 @@ __device__ __forceinline__ uint32_t chunk_bits(const uint32_t* bits, uint32_t j)
 template <typename T, bool TAIL>
 __device__ __forceinline__ void add_chunk(const Chunk<T>& v, float m, float c, uint32_t marks,
                                           float& rest, float& top) {
-  float z[kVec<T>];
+  float z[kVec<T>], sum = 0.0f;
   unpack(v, z);
   if (!TAIL || marks == 0) {
 #pragma unroll
-    for (int e = 0; e < kVec<T>; ++e) rest += ex2((z[e] - m) * c);
+    for (int e = 0; e < kVec<T>; ++e) sum += ex2((z[e] - m) * c);
   } else {
 #pragma unroll
     for (int e = 0; e < kVec<T>; ++e) {
       const float x = ex2((z[e] - m) * c);
       if ((marks >> e) & 1u) top += x;
-      else rest += x;
+      else sum += x;
     }
   }
+  rest += sum;
 }
 
 // A chunk's largest logit and m, and its sum against m, without its marked tokens.
@@ -407,6 +420,7 @@ __global__ __launch_bounds__(SIDE ? NT + 64 : NT, NT < 512 ? 1 : 4)
 void distill_row_kernel(DistillArgs a) {
   extern __shared__ char mem[];
   __shared__ float red[3][NT / 64];
+  __shared__ double wide[2][NT / 64];  // the waves' sums over the rest and over all tokens
   __shared__ Teacher t;  // kept here, not in registers across the passes
   const int64_t n = blockIdx.x;
   const int tid = threadIdx.x, wv = tid >> 6;
@@ -486,11 +500,12 @@ void distill_row_kernel(DistillArgs a) {
         add_chunk<T, TAIL>(v[q], m, a.c, TAIL ? chunk_bits<T>(l.bits, j) : 0u, rest, top);
       keep_packed<T>(v[q]);
     }
-    rest = wave_sum(rest);
-    if (TAIL) top = wave_sum(top);
+    const double wr = wave_sum((double)rest), wt = TAIL ? wave_sum((double)top) : 0.0;
     if ((tid & 63) == 0) {
-      red[1][wv] = rest;
-      red[2][wv] = top;
+      red[1][wv] = (float)wr;
+      red[2][wv] = (float)wt;
+      wide[0][wv] = wr;
+      wide[1][wv] = wr + wt;
     }
   }
   __syncthreads();
@@ -529,8 +544,11 @@ void distill_row_kernel(DistillArgs a) {
           if (j < r.chunks) rest += rest_sum<T>(v[q], chunk_bits<T>(l.bits, j), mr, a.c);
           keep_packed<T>(v[q]);
         }
-        rest = wave_sum(rest);
-        if ((tid & 63) == 0) red[1][wv] = rest;
+        const double wr = wave_sum((double)rest);
+        if ((tid & 63) == 0) {
+          red[1][wv] = (float)wr;
+          wide[0][wv] = wr;
+        }
       }
       __syncthreads();
       rest = 0.0f;
@@ -538,10 +556,9 @@ void distill_row_kernel(DistillArgs a) {
       for (int q = 0; q < NT / 64; ++q) rest += red[1][q];
     }
   }
-  const Student st = {m, S, mr, rest};
   const bool dead = S == 0.0f || (!TAIL && !t.any);
   const float scale = dead ? 0.0f : w * a.tau;
-  const float coef = dead ? 0.0f : scale * rest_coef<TAIL>(a, st, (float)t.rest);
+  const float coef = dead ? 0.0f : scale * rest_coef<TAIL>(a, m, S, mr, rest, top, t.rest);
   if (row_wave) {
 #pragma unroll
     for (int q = 0; q < R; ++q) {
@@ -556,6 +573,11 @@ void distill_row_kernel(DistillArgs a) {
     }
   }
   if (teacher_wave) {
+    Student st = {m, mr, 0.0, 0.0};
+    for (int q = 0; q < NT / 64; ++q) {
+      st.S += wide[1][q];
+      st.Sr += rest == 0.0f ? 0.0 : wide[0][q];
+    }
     const float loss = dead ? 0.0f : row_loss(a, t, st, TAIL);
     if ((tid & 63) == 0) a.loss[n] = loss;
   }
@@ -604,14 +626,21 @@ __device__ __forceinline__ void load_batch(const Row<T>& r, uint32_t j0, uint32_
 // Statistics of a part: largest logit and sum of exp((z - largest) / tau) over the
 // tokens of the rest (of all tokens without one), and over the top's.
 struct Part {
-  float mr, rest, mt, top;
+  float mr, mt;
+  double rest, top;
 };
-constexpr Part kNoPart = {kNegInf, 0.0f, kNegInf, 0.0f};
+static_assert(sizeof(Part) == 24, "the workspace counts 24 bytes");
+constexpr Part kNoPart = {kNegInf, kNegInf, 0.0, 0.0};
 
 // Factor that takes a sum against `from` to one against `to`, where `to` is not
-// smaller.  -Inf comes with a sum of 0, or NaN where nothing but NaN was seen.
+// smaller.  -Inf comes with a sum of 0, or NaN where nothing but NaN was seen.  A
+// thread's sum is moved in f32, one of many whose errors average; a part's in f64.
 __device__ __forceinline__ float shift(float from, float to, float sum, float c) {
   return from == kNegInf ? (sum == sum ? 0.0f : 1.0f) : ex2((from - to) * c);
+}
+__device__ __forceinline__ double moved(float from, float to, double sum, double inv_tau) {
+  if (from == kNegInf) return sum == sum ? 0.0 : sum;
+  return from == to ? sum : sum * exp(((double)from - (double)to) * inv_tau);
 }
 
 // A row's loss and what its gradient needs, by one wave.
@@ -620,16 +649,16 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t n, bool
                                            const Teacher& t, const Part& p) {
   Student s;
   s.m = TAIL ? fmaxf(p.mr, p.mt) : p.mr;
-  s.S = p.rest * shift(p.mr, s.m, p.rest, a.c);
-  if (TAIL) s.S += p.top * shift(p.mt, s.m, p.top, a.c);
+  s.S = moved(p.mr, s.m, p.rest, a.inv_tau);
+  if (TAIL) s.S += moved(p.mt, s.m, p.top, a.inv_tau);
   if (s.m == kNegInf) s.m = 0.0f;
   s.mr = p.mr == kNegInf ? s.m : p.mr;
   s.Sr = p.rest;
-  const bool dead = off || s.S == 0.0f || (!TAIL && !t.any);
+  const bool dead = off || s.S == 0.0 || (!TAIL && !t.any);
   const float loss = dead ? 0.0f : row_loss(a, t, s, TAIL);
   if ((threadIdx.x & 63) == 0) {
     a.loss[n] = loss;
-    if (a.saved) save_row<TAIL>(a, n, dead, s, (float)t.rest);
+    if (a.saved) save_row<TAIL>(a, n, dead, s, t.rest);
   }
 }
 
@@ -647,14 +676,16 @@ __device__ __forceinline__ void drop_top(Chunk<T>& v, uint32_t marks) {
 template <typename T, bool TAIL>
 __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(DistillArgs a) {
   extern __shared__ char mem[];
-  __shared__ float red[2][kPartThreads / 64];
-  __shared__ float top_mt, top_sum;
+  __shared__ float red[kPartThreads / 64];
+  __shared__ double sums_of[kPartThreads / 64];
+  __shared__ float top_mt;
+  __shared__ double top_sum;
   __shared__ Teacher whole;  // where the part is the row
   const int64_t n = blockIdx.x / (uint32_t)a.splits;
   const int split = (int)(blockIdx.x % (uint32_t)a.splits);
   const int tid = threadIdx.x, wv = tid >> 6;
   const bool row_wave = wv < kPartThreads / 64;
-  Part* part = reinterpret_cast<Part*>(a.part) + blockIdx.x;
+  Part* part = static_cast<Part*>(a.part) + blockIdx.x;
   if (a.weight && a.weight[n] == 0.0f) {
     if (tid == 0) *part = kNoPart;
     if (a.splits == 1 && !row_wave) finish_row<TAIL>(a, n, true, Teacher{}, kNoPart);
@@ -702,47 +733,47 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
     own = entries.own;
     for (int k = tid & 63; k < a.K; k += 64, own >>= 1)
       if (own & 1u) top += ex2((l.z[k] - (mt == kNegInf ? 0.0f : mt)) * a.c);
-    top = wave_sum(top);
-    if ((tid & 63) == 0) top_mt = mt, top_sum = top;
+    const double sum = wave_sum((double)top);
+    if ((tid & 63) == 0) top_mt = mt, top_sum = sum;
   }
-  Part o = kNoPart;
+  float m = kNegInf, rest = 0.0f;
   if (row_wave) {
     for (uint32_t j0 = s.c0 + tid; j0 < s.c1; j0 += kBatch * kPartThreads) {
-      float mb = o.mr;
+      float mb = m;
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         const uint32_t j = j0 + q * kPartThreads;
         if (TAIL && j < s.c1) drop_top<T>(v[q], chunk_bits<T>(l.bits, j - s.c0));
         mb = rest_max<T>(v[q], 0, mb);
       }
-      if (mb > o.mr) {
-        o.rest *= shift(o.mr, mb, o.rest, a.c);
-        o.mr = mb;
+      if (mb > m) {
+        rest *= shift(m, mb, rest, a.c);
+        m = mb;
       }
-      const float ms = o.mr == kNegInf ? 0.0f : o.mr;
+      const float ms = m == kNegInf ? 0.0f : m;
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         const uint32_t j = j0 + q * kPartThreads;
-        if (j < s.c1) o.rest += rest_sum<T>(v[q], 0, ms, a.c);
+        if (j < s.c1) rest += rest_sum<T>(v[q], 0, ms, a.c);
       }
       if (j0 + kBatch * kPartThreads < s.c1) load_batch(r, j0 + kBatch * kPartThreads, s.c1, v);
     }
-    const float mw = wave_max(o.mr);
-    if ((tid & 63) == 0) red[0][wv] = mw;
+    const float mw = wave_max(m);
+    if ((tid & 63) == 0) red[wv] = mw;
   }
   __syncthreads();
   Part all = kNoPart;
 #pragma unroll
-  for (int q = 0; q < kPartThreads / 64; ++q) all.mr = fmaxf(all.mr, red[0][q]);
+  for (int q = 0; q < kPartThreads / 64; ++q) all.mr = fmaxf(all.mr, red[q]);
   if (TAIL) all.mt = top_mt, all.top = top_sum;
   if (row_wave) {
-    const float rest = wave_sum(o.rest * shift(o.mr, all.mr, o.rest, a.c));
-    if ((tid & 63) == 0) red[1][wv] = rest;
+    const double sum = wave_sum((double)rest * (double)shift(m, all.mr, rest, a.c));
+    if ((tid & 63) == 0) sums_of[wv] = sum;
   }
   __syncthreads();
   if (a.splits == 1 ? row_wave : tid != 0) return;
 #pragma unroll
-  for (int q = 0; q < kPartThreads / 64; ++q) all.rest += red[1][q];
+  for (int q = 0; q < kPartThreads / 64; ++q) all.rest += sums_of[q];
   if (a.splits == 1) finish_row<TAIL>(a, n, false, whole, all);
   else *part = all;
 }
@@ -752,7 +783,7 @@ template <bool TAIL>
 __global__ __launch_bounds__(64) void distill_join_kernel(DistillArgs a) {
   const int64_t n = blockIdx.x;
   const int lane = threadIdx.x;
-  const Part* part = reinterpret_cast<const Part*>(a.part) + n * a.splits;
+  const Part* part = static_cast<const Part*>(a.part) + n * a.splits;
   const bool off = a.weight && a.weight[n] == 0.0f;
   Teacher t = {0.0, 0.0, 0.0, 0.0, 1.0, 0.0f, false, false};
   if (!off) t = a.teacher[n];
@@ -765,8 +796,8 @@ __global__ __launch_bounds__(64) void distill_join_kernel(DistillArgs a) {
   if (TAIL) all.mt = wave_max(all.mt);
   for (int q = lane; q < a.splits; q += 64) {
     const Part p = part[q];
-    all.rest += p.rest * shift(p.mr, all.mr, p.rest, a.c);
-    if (TAIL) all.top += p.top * shift(p.mt, all.mt, p.top, a.c);
+    all.rest += moved(p.mr, all.mr, p.rest, a.inv_tau);
+    if (TAIL) all.top += moved(p.mt, all.mt, p.top, a.inv_tau);
   }
   all.rest = wave_sum(all.rest);
   if (TAIL) all.top = wave_sum(all.top);
@@ -875,7 +906,7 @@ int teacher_waves(int K) {
 }
 
 template <typename T, int R, bool TAIL, int PASS>
-__global__ __launch_bounds__(PASS == kGradient ? 64 * kWaveRows : 128 * kWaveRows)
+__global__ __launch_bounds__(PASS == kGradient ? 64 * kWaveRows : 128 * kWaveRows, R == 12 ? 4 : 1)
 void distill_wave_kernel(DistillArgs a, uint32_t words) {
   extern __shared__ char mem[];
   __shared__ Student stat[kWaveRows];
@@ -905,9 +936,9 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
     if (q < kWaveRows && k0 == 0 && n < a.N) {
       const float w = PASS == kFused && a.weight ? a.weight[n] : 1.0f;
       const Student s = stat[q];
-      const bool dead = w == 0.0f || s.S == 0.0f || (!TAIL && !t.any);
+      const bool dead = w == 0.0f || s.S == 0.0 || (!TAIL && !t.any);
       a.loss[n] = dead ? 0.0f : row_loss(a, t, s, TAIL);
-      if (PASS == kLoss && a.saved) save_row<TAIL>(a, n, dead, s, (float)t.rest);
+      if (PASS == kLoss && a.saved) save_row<TAIL>(a, n, dead, s, t.rest);
     }
     return;
   }
@@ -929,16 +960,15 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
       for (int e = 0; e < kVec<T>; ++e) v[q].v[e] = (T)kNegInf;
     }
   }
-  Student s;
-  float p_rest = 0.0f, saved_coef = 0.0f;
+  float m, S, mr, coef = 0.0f;
   bool dead, dup;
   if (PASS == kGradient) {
     const float* saved = a.saved + (here ? n : 0) * (4 + a.K);
-    s.m = saved[0];
-    s.S = saved[1];
-    s.mr = saved[2];
-    saved_coef = saved[3];
-    dead = w == 0.0f || s.S == 0.0f;
+    m = saved[0];
+    S = saved[1];
+    mr = saved[2];
+    coef = saved[3];
+    dead = w == 0.0f || S == 0.0f;
     dup = false;
     clear_marks(l.bits, words);
     for (int k = lane; k < a.K && !dead; k += 64) {
@@ -953,7 +983,7 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
     }
     dup = __any(dup);
   } else {
-    float m = kNegInf;
+    m = kNegInf;
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       float z[kVec<T>];
@@ -971,11 +1001,11 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
       if (w != 0.0f && j < r.chunks)
         add_chunk<T, TAIL>(v[q], m, a.c, TAIL ? chunk_bits<T>(l.bits, j) : 0u, rest, top);
     }
-    rest = wave_sum(rest);
-    if (TAIL) top = wave_sum(top);
-    s = {m, rest + top, m, rest};
-    if (TAIL && w != 0.0f && rest < kFar) {  // the same in every lane
-      float mr = kNegInf;
+    mr = m;
+    double wr = wave_sum((double)rest);
+    const double wt = TAIL ? wave_sum((double)top) : 0.0, ws = wr + wt;
+    if (TAIL && w != 0.0f && wr < kFar) {  // the same in every lane
+      mr = kNegInf;
 #pragma unroll
       for (int q = 0; q < R; ++q) {
         const uint32_t j = lane + q * 64;
@@ -983,28 +1013,28 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
       }
       mr = wave_max(mr);
       rest = 0.0f;
-      if (mr != kNegInf) {
-        s.mr = mr;
+      if (mr == kNegInf) {
+        mr = m;
+      } else {
 #pragma unroll
         for (int q = 0; q < R; ++q) {
           const uint32_t j = lane + q * 64;
           if (j < r.chunks) rest += rest_sum<T>(v[q], chunk_bits<T>(l.bits, j), mr, a.c);
         }
-        rest = wave_sum(rest);
       }
-      s.Sr = rest;
+      wr = wave_sum((double)rest);
     }
-    if (lane == 0) stat[wv] = s;
+    S = (float)ws;
+    if (lane == 0) stat[wv] = {m, mr, ws, wr};
     __syncthreads();  // the teachers, whose logits are read before they may be overwritten
     const Teacher t = teachers[wv];
-    dead = w == 0.0f || s.S == 0.0f || (!TAIL && !t.any);
+    dead = w == 0.0f || S == 0.0f || (!TAIL && !t.any);
     dup = t.dup;
-    p_rest = (float)t.rest;
+    if (PASS == kFused) coef = rest_coef<TAIL>(a, m, S, mr, (float)wr, (float)wt, t.rest);
   }
   if (PASS != kLoss && here) {
     const float scale = dead ? 0.0f : w * a.tau;
-    const float coef =
-        dead ? 0.0f : scale * (PASS == kGradient ? saved_coef : rest_coef<TAIL>(a, s, p_rest));
+    coef = dead ? 0.0f : scale * coef;
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       const uint32_t j = lane + q * 64;
@@ -1012,11 +1042,11 @@ void distill_wave_kernel(DistillArgs a, uint32_t words) {
         float z[kVec<T>], g[kVec<T>];
         unpack(v[q], z);
 #pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) g[e] = dead ? 0.0f : coef * ex2((z[e] - s.mr) * a.c);
+        for (int e = 0; e < kVec<T>; ++e) g[e] = dead ? 0.0f : coef * ex2((z[e] - mr) * a.c);
         store_chunk(grad, r, j, g);
       }
     }
-    if (!dead) patch_top(a, l, grad, s.m, s.S, scale, dup, 0, (int64_t)r.V, lane, 64);
+    if (!dead) patch_top(a, l, grad, m, S, scale, dup, 0, (int64_t)r.V, lane, 64);
   }
 }
 

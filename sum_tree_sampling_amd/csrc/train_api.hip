@@ -119,7 +119,7 @@ int check_distill(per::DistillArgs& a, int64_t N, int64_t V, int64_t K, int32_t 
   if (V < 1 || V > PER_MAX_VOCAB) return bad("V %lld outside [1, 2^24]", (long long)V);
   if (K < 1 || K > PER_MAX_TOP) return bad("K %lld outside [1, 1024]", (long long)K);
   if (!type_ok(type) || !type_ok(t_type)) return bad("type is none");
-  if (!(tau >= 0x1p-20 && tau <= 0x1p20)) return bad("temperature outside [2^-20, 2^20]");
+  if (!(tau >= 0x1p-20 && tau <= 0x1p6)) return bad("temperature outside [2^-20, 2^6]");
   if (stride < V || stride > kMaxStride) return bad("logits' stride %lld below V", (long long)stride);
   if (N == 0) return PER_OK;
   if (!z || !tidx || !t) return bad("logits, token indices and teacher logits are required");
@@ -153,7 +153,7 @@ DistillSpace distill_space(int64_t N, int64_t V, int64_t K, int32_t type) {
   DistillSpace s = {0, 0, 0};
   if (per::distill_small(N, V, type)) return s;
   s.part = (size_t)N * sizeof(per::Teacher);
-  s.saved = s.part + (size_t)N * per::distill_splits(N, V, type) * 16;
+  s.saved = s.part + (size_t)N * per::distill_splits(N, V, type) * 24;
   s.total = s.saved + (size_t)N * (size_t)(4 + K) * 4;
   return s;
 }
@@ -161,7 +161,7 @@ void set_space(per::DistillArgs& a, void* ws, int32_t type) {
   const DistillSpace s = distill_space(a.N, a.V, a.K, type);
   char* base = static_cast<char*>(ws);
   a.teacher = reinterpret_cast<per::Teacher*>(base);
-  a.part = reinterpret_cast<float*>(base + s.part);
+  a.part = base + s.part;
   a.saved = reinterpret_cast<float*>(base + s.saved);
 }
 

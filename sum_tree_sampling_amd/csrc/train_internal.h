@@ -95,7 +95,7 @@ struct DistillArgs {
   float* saved;           // [N x (4 + K)]
   void* grad;
   int64_t grad_stride;
-  float* part;            // [N x splits x 4]
+  void* part;             // [N x splits] statistics of 24 bytes
   Teacher* teacher;       // [N]
   int splits;
   bool once;              // logits are loaded past the caches

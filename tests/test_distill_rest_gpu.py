@@ -184,3 +184,27 @@ def test_rest_differences():
     # third derivative by one direction: at most about 8; the loss, below 100, is rounded to f32, and z + eps r to
     # steps of 2^-17 of logits near 100
     assert ((num - ana).abs() <= eps ** 2 * 8 + 64 * U * 128 / eps).all(), (num, ana)
+
+
+@pytest.mark.parametrize("tau", [8.0, 20.0, 32.0, 64.0])
+@pytest.mark.parametrize("V,K,N", [(4001, 30, 1100), (9001, 64, 64), (30000, 64, 200), (120000, 50, 16)])
+def test_loss_at_large_temperatures(V, K, N, tau):
+    """A student near its teacher, whose loss is far below tau^2.  An exponential is
+    off by at most 4 u and they are independent, so the mean of V of them is off by
+    less than 4 * 4 u / sqrt(V) (four standard deviations), S and S_r alike."""
+    import sum_tree_sampling_amd as p
+    teacher = torch.randn(N, V, generator=gen(V))
+    z = teacher + 0.06 * torch.randn(N, V, generator=gen(1))
+    t, at = teacher.topk(K, 1)
+    tlse = torch.logsumexp(teacher.double() / tau, 1).float()
+    logp = t.double() / tau - tlse.double()[:, None]
+    logq = torch.log_softmax(z.double() / tau, 1)
+    rest = 1 - logp.exp().sum(1)
+    log_rest = torch.logsumexp(logq.scatter(1, at, -math.inf), 1)
+    want = tau * tau * ((logp.exp() * (logp - logq.gather(1, at))).sum(1) + rest * (rest.log() - log_rest))
+    args = (z.cuda(), at.to(torch.int32).cuda(), t.cuda())
+    fused, _ = p.per_distill(*args, tlse=tlse.cuda(), temperature=tau)
+    apart, _ = p.per_distill_forward(*args, tlse=tlse.cuda(), temperature=tau)
+    tol = tau * tau * 32 * U / math.sqrt(V) + 2 * U * want.abs()
+    assert_close(fused, want, tol, "loss")
+    assert_close(apart, want, tol, "forward loss")
