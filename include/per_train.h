@@ -15,7 +15,9 @@
  * anything is enqueued, and PER_EINVAL / PER_ENOSPC / PER_EHIP come with a
  * text in per_last_error().  There is no handle: every call takes the arrays
  * it works on.  Calls that share no writable array may overlap on different
- * streams.  The tensors belong to the current device.
+ * streams.  The tensors belong to the current device.  A call whose largest
+ * launch would take 2^32 work-items or more (its rows times the threads that a
+ * row takes, at most 1024) is refused with PER_EINVAL; it can be made in pieces.
  *
  * Element types are PER_F32, PER_BF16 and PER_F16; strides count elements.
  * Sums, softmax statistics, scales and recurrent states are f32 or wider;

@@ -1067,8 +1067,8 @@ template <typename T, int NT, int R, bool SIDE>
 hipError_t row_launch(const DistillArgs& a, hipStream_t s) {
   const size_t lds = lds_bytes(a.K, a.tlse != nullptr, a.V + 2 * kVec<T>);
   const dim3 grid((uint32_t)a.N), block(SIDE ? NT + 64 : NT);
-  return a.tlse ? launch_kernel(distill_row_kernel<T, NT, R, true, SIDE>, grid, block, lds, s, a)
-                : launch_kernel(distill_row_kernel<T, NT, R, false, SIDE>, grid, block, lds, s, a);
+  return a.tlse ? enqueue(distill_row_kernel<T, NT, R, true, SIDE>, grid, block, lds, s, a)
+                : enqueue(distill_row_kernel<T, NT, R, false, SIDE>, grid, block, lds, s, a);
 }
 
 // Whether the wave kernel takes rows of so many chunks.  From 1024 rows on there are
@@ -1087,13 +1087,13 @@ hipError_t wave_launch(const DistillArgs& a, hipStream_t s) {
   const dim3 grid((uint32_t)((a.N + kWaveRows - 1) / kWaveRows));
   const dim3 block(64 * (PASS == kGradient ? kWaveRows : kWaveRows + teacher_waves(a.K)));
   if (chunks <= 64)
-    return launch_kernel(distill_wave_kernel<T, 1, TAIL, PASS>, grid, block, lds, s, a, words);
+    return enqueue(distill_wave_kernel<T, 1, TAIL, PASS>, grid, block, lds, s, a, words);
   if constexpr (PASS != kFused)
     if (chunks > 512)
-      return launch_kernel(distill_wave_kernel<T, 12, TAIL, PASS>, grid, block, lds, s, a, words);
+      return enqueue(distill_wave_kernel<T, 12, TAIL, PASS>, grid, block, lds, s, a, words);
   if (chunks > 256)
-    return launch_kernel(distill_wave_kernel<T, 8, TAIL, PASS>, grid, block, lds, s, a, words);
-  return launch_kernel(distill_wave_kernel<T, 4, TAIL, PASS>, grid, block, lds, s, a, words);
+    return enqueue(distill_wave_kernel<T, 8, TAIL, PASS>, grid, block, lds, s, a, words);
+  return enqueue(distill_wave_kernel<T, 4, TAIL, PASS>, grid, block, lds, s, a, words);
 }
 template <typename T, int PASS>
 hipError_t wave_typed(const DistillArgs& a, hipStream_t s) {
@@ -1132,15 +1132,15 @@ hipError_t stats_typed(const DistillArgs& a, int type, hipStream_t s) {
   if (distill_small(a.N, a.V, type)) return wave_typed<T, kLoss>(a, s);
   const dim3 grid((uint32_t)(a.N * a.splits)), block(kPartThreads + 64);
   if (a.tlse) {
-    const hipError_t e = launch_kernel(distill_part_kernel<T, true>, grid, block,
+    const hipError_t e = enqueue(distill_part_kernel<T, true>, grid, block,
                                        lds_bytes(a.K, true, part_tokens(a, type)), s, a);
     if (e != hipSuccess || a.splits == 1) return e;
-    return launch_kernel(distill_join_kernel<true>, dim3((uint32_t)a.N), dim3(64), 0, s, a);
+    return enqueue(distill_join_kernel<true>, dim3((uint32_t)a.N), dim3(64), 0, s, a);
   }
-  const hipError_t e = launch_kernel(distill_part_kernel<T, false>, grid, block,
+  const hipError_t e = enqueue(distill_part_kernel<T, false>, grid, block,
                                      lds_bytes(a.K, true, 0), s, a);
   if (e != hipSuccess || a.splits == 1) return e;
-  return launch_kernel(distill_join_kernel<false>, dim3((uint32_t)a.N), dim3(64), 0, s, a);
+  return enqueue(distill_join_kernel<false>, dim3((uint32_t)a.N), dim3(64), 0, s, a);
 }
 
 template <typename T>
@@ -1148,8 +1148,8 @@ hipError_t grad_typed(const DistillArgs& a, int type, hipStream_t s) {
   if (distill_small(a.N, a.V, type)) return wave_typed<T, kGradient>(a, s);
   const dim3 grid((uint32_t)(a.N * a.splits)), block(kPartThreads + 64);
   const size_t lds = lds_bytes(a.K, false, part_tokens(a, type));
-  return a.tlse ? launch_kernel(distill_grad_kernel<T, true>, grid, block, lds, s, a)
-                : launch_kernel(distill_grad_kernel<T, false>, grid, block, lds, s, a);
+  return a.tlse ? enqueue(distill_grad_kernel<T, true>, grid, block, lds, s, a)
+                : enqueue(distill_grad_kernel<T, false>, grid, block, lds, s, a);
 }
 
 }  // namespace

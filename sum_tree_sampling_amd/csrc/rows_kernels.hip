@@ -375,7 +375,7 @@ int ceil_log2(uint32_t v) {
 template <typename T, int FMT>
 hipError_t write_typed(const RowsArgs& a, hipStream_t s) {
   if (a.slots) {
-    const hipError_t e = launch_kernel(rows_claim_kernel, dim3((a.rows + kThreads - 1) / kThreads),
+    const hipError_t e = enqueue(rows_claim_kernel, dim3((a.rows + kThreads - 1) / kThreads),
                                        dim3(kThreads), 0, s, a);
     if (e != hipSuccess) return e;
   }
@@ -388,14 +388,14 @@ hipError_t write_typed(const RowsArgs& a, hipStream_t s) {
   if (row && per_lane > 4) {
     const dim3 grid(a.rows);
     if (units <= kThreads * 2)
-      return launch_kernel(rows_write_long_kernel<T, FMT, kThreads, 2, true>, grid, dim3(kThreads),
+      return enqueue(rows_write_long_kernel<T, FMT, kThreads, 2, true>, grid, dim3(kThreads),
                            0, s, a);
     if (units <= kThreads * 4)
-      return launch_kernel(rows_write_long_kernel<T, FMT, kThreads, 4, true>, grid, dim3(kThreads),
+      return enqueue(rows_write_long_kernel<T, FMT, kThreads, 4, true>, grid, dim3(kThreads),
                            0, s, a);
     if (units <= 1024 * 4)
-      return launch_kernel(rows_write_long_kernel<T, FMT, 1024, 4, true>, grid, dim3(1024), 0, s, a);
-    return launch_kernel(rows_write_long_kernel<T, FMT, 1024, 4, false>, grid, dim3(1024), 0, s, a);
+      return enqueue(rows_write_long_kernel<T, FMT, 1024, 4, true>, grid, dim3(1024), 0, s, a);
+    return enqueue(rows_write_long_kernel<T, FMT, 1024, 4, false>, grid, dim3(1024), 0, s, a);
   }
   const uint32_t rpb = kThreads >> lg;
   const int U = per_lane <= 1 ? 1 : per_lane <= 2 ? 2 : 4;
@@ -404,13 +404,13 @@ hipError_t write_typed(const RowsArgs& a, hipStream_t s) {
   const uint32_t steps = a.slots ? 1 : (per_lane + U - 1) / U;
   const dim3 grid((a.rows + rpb - 1) / rpb, steps);
   if (row) {
-    if (U == 1) return launch_kernel(rows_write_kernel<T, FMT, 1, true>, grid, dim3(kThreads), 0, s, a, lg);
-    if (U == 2) return launch_kernel(rows_write_kernel<T, FMT, 2, true>, grid, dim3(kThreads), 0, s, a, lg);
-    return launch_kernel(rows_write_kernel<T, FMT, 4, true>, grid, dim3(kThreads), 0, s, a, lg);
+    if (U == 1) return enqueue(rows_write_kernel<T, FMT, 1, true>, grid, dim3(kThreads), 0, s, a, lg);
+    if (U == 2) return enqueue(rows_write_kernel<T, FMT, 2, true>, grid, dim3(kThreads), 0, s, a, lg);
+    return enqueue(rows_write_kernel<T, FMT, 4, true>, grid, dim3(kThreads), 0, s, a, lg);
   }
-  if (U == 1) return launch_kernel(rows_write_kernel<T, FMT, 1, false>, grid, dim3(kThreads), 0, s, a, lg);
-  if (U == 2) return launch_kernel(rows_write_kernel<T, FMT, 2, false>, grid, dim3(kThreads), 0, s, a, lg);
-  return launch_kernel(rows_write_kernel<T, FMT, 4, false>, grid, dim3(kThreads), 0, s, a, lg);
+  if (U == 1) return enqueue(rows_write_kernel<T, FMT, 1, false>, grid, dim3(kThreads), 0, s, a, lg);
+  if (U == 2) return enqueue(rows_write_kernel<T, FMT, 2, false>, grid, dim3(kThreads), 0, s, a, lg);
+  return enqueue(rows_write_kernel<T, FMT, 4, false>, grid, dim3(kThreads), 0, s, a, lg);
 }
 
 template <typename T, int FMT>
@@ -422,10 +422,10 @@ hipError_t read_typed(const RowsArgs& a, hipStream_t s) {
   const uint32_t rpb = kThreads >> lg;
   const uint32_t nx = (a.rows + rpb - 1) / rpb;
   if (per_lane <= 1)
-    return launch_kernel(rows_read_kernel<T, FMT, 1>, dim3(nx), dim3(kThreads), 0, s, a, lg);
+    return enqueue(rows_read_kernel<T, FMT, 1>, dim3(nx), dim3(kThreads), 0, s, a, lg);
   if (per_lane <= 2)
-    return launch_kernel(rows_read_kernel<T, FMT, 2>, dim3(nx), dim3(kThreads), 0, s, a, lg);
-  return launch_kernel(rows_read_kernel<T, FMT, 4>, dim3(nx, (per_lane + 3) / 4), dim3(kThreads), 0,
+    return enqueue(rows_read_kernel<T, FMT, 2>, dim3(nx), dim3(kThreads), 0, s, a, lg);
+  return enqueue(rows_read_kernel<T, FMT, 4>, dim3(nx, (per_lane + 3) / 4), dim3(kThreads), 0,
                        s, a, lg);
 }
 

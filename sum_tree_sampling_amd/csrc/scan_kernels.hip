@@ -599,23 +599,23 @@ __global__ __launch_bounds__(256) void scan_step_kernel(StepArgs a, int lg) {
 template <typename T, int C, bool PACK = false>
 hipError_t forward_typed(ScanArgs a, uint32_t blocks, int waves, hipStream_t s) {
   if (a.nseg > 1) {
-    const hipError_t e = launch_kernel(scan_segment_kernel<T, C, PACK, false>, dim3(blocks),
+    const hipError_t e = enqueue(scan_segment_kernel<T, C, PACK, false>, dim3(blocks),
                                        dim3(kWaves * 64), 0, s, a);
     if (e != hipSuccess) return e;
     // The last segment's workgroup may write h_last = h0 before others start.
     if (a.h0) a.h0 = a.h0_copy;
   }
-  return launch_kernel(scan_forward_kernel<T, C, PACK>, dim3(blocks), dim3(64 * waves), 0, s, a);
+  return enqueue(scan_forward_kernel<T, C, PACK>, dim3(blocks), dim3(64 * waves), 0, s, a);
 }
 
 template <typename T, int C, bool PACK = false>
 hipError_t backward_typed(const ScanArgs& a, uint32_t blocks, int waves, hipStream_t s) {
   if (a.nseg > 1) {
-    const hipError_t e = launch_kernel(scan_segment_kernel<T, C, PACK, true>, dim3(blocks),
+    const hipError_t e = enqueue(scan_segment_kernel<T, C, PACK, true>, dim3(blocks),
                                        dim3(kWaves * 64), 0, s, a);
     if (e != hipSuccess) return e;
   }
-  return launch_kernel(scan_backward_kernel<T, C, PACK>, dim3(blocks), dim3(64 * waves), 0, s, a);
+  return enqueue(scan_backward_kernel<T, C, PACK>, dim3(blocks), dim3(64 * waves), 0, s, a);
 }
 
 // Waves of a workgroup: as many as the sequence has steps for, up to 8, or 16 where
@@ -743,7 +743,7 @@ static hipError_t step_launch(const StepArgs& a, hipStream_t s) {
   while (lg < 8 && (int64_t(1) << lg) < units) ++lg;
   const int64_t cols = (units + (1 << lg) - 1) >> lg;
   const int64_t rows = (a.B + (256 >> lg) - 1) / (256 >> lg);
-  return launch_kernel(scan_step_kernel<T, C>,
+  return enqueue(scan_step_kernel<T, C>,
                        dim3((uint32_t)rows, (uint32_t)(cols < 65535 ? cols : 65535)), dim3(256), 0,
                        s, a, lg);
 }

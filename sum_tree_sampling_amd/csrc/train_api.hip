@@ -20,7 +20,19 @@ __attribute__((format(printf, 1, 2))) int bad(const char* fmt, ...) {
   return per::api_fail(PER_EINVAL, buf);
 }
 
-int done(hipError_t e, const char* what) {
+thread_local per::Launches g_launches;
+
+// Runs a call's launches, once to count and then in earnest.
+template <typename F>
+int run(const char* what, F launch) {
+  g_launches.counting = true;
+  g_launches.items = 0;
+  hipError_t e = launch();
+  g_launches.counting = false;
+  if (e == hipSuccess && g_launches.items >> 32)
+    return bad("%s would take %llu work-items in one launch, 2^32 or more: call it in pieces", what,
+               (unsigned long long)g_launches.items);
+  if (e == hipSuccess) e = launch();
   if (e == hipSuccess) return per::api_ok();
   char buf[256];
   snprintf(buf, sizeof buf, "%s: %s", what, hipGetErrorString(e));
@@ -176,6 +188,8 @@ int check_grad(const void* grad, int64_t stride, int32_t type, int64_t V, const 
 
 }  // namespace
 
+per::Launches& per::launches() { return g_launches; }
+
 int per_rows_write(int64_t capacity, int64_t dim, int32_t format, int32_t group, uint8_t* d_codes,
                    int64_t codes_stride, float* d_scales, int64_t scales_stride, int64_t count,
                    int64_t first, const void* d_src, int32_t type, int64_t src_stride,
@@ -194,7 +208,7 @@ int per_rows_write(int64_t capacity, int64_t dim, int32_t format, int32_t group,
   a.src = d_src;
   a.first = first;
   a.rows = (uint32_t)count;
-  return done(per::launch_rows_write(a, type, format, stream), "per_rows_write");
+  return run("per_rows_write", [&] { return per::launch_rows_write(a, type, format, stream); });
 }
 
 int per_rows_write_at(int64_t capacity, int64_t dim, int32_t format, int32_t group,
@@ -215,7 +229,7 @@ int per_rows_write_at(int64_t capacity, int64_t dim, int32_t format, int32_t gro
   a.slots = d_slots;
   a.claims = d_claims;
   a.rows = (uint32_t)count;
-  return done(per::launch_rows_write(a, type, format, stream), "per_rows_write_at");
+  return run("per_rows_write_at", [&] { return per::launch_rows_write(a, type, format, stream); });
 }
 
 int per_rows_read(int64_t capacity, int64_t dim, int32_t format, int32_t group,
@@ -238,7 +252,7 @@ int per_rows_read(int64_t capacity, int64_t dim, int32_t format, int32_t group,
   a.out = d_out;
   a.window = (uint32_t)window;
   a.rows = (uint32_t)(B * window);
-  return done(per::launch_rows_read(a, type, format, stream), "per_rows_read");
+  return run("per_rows_read", [&] { return per::launch_rows_read(a, type, format, stream); });
 }
 
 int per_scan_workspace_bytes(int64_t B, int64_t T, int64_t D, size_t* out) {
@@ -285,7 +299,7 @@ int per_scan_forward(int64_t B, int64_t T, int64_t D, int32_t type, const void* 
   a.h_last = d_h_last;
   a.carries = d_carries;
   a.agg = static_cast<float*>(d_ws);
-  return done(per::launch_scan_forward(a, type, stream), "per_scan_forward");
+  return run("per_scan_forward", [&] { return per::launch_scan_forward(a, type, stream); });
 }
 
 int per_scan_backward(int64_t B, int64_t T, int64_t D, int32_t type, const void* d_x, int64_t x_sb,
@@ -335,7 +349,7 @@ int per_scan_backward(int64_t B, int64_t T, int64_t D, int32_t type, const void*
   a.dh_last = d_dh_last;
   a.dh0 = d_dh0;
   a.agg = static_cast<float*>(d_ws);
-  return done(per::launch_scan_backward(a, type, stream), "per_scan_backward");
+  return run("per_scan_backward", [&] { return per::launch_scan_backward(a, type, stream); });
 }
 
 int per_scan_step(int64_t B, int64_t D, int32_t type, const void* d_x, int64_t x_stride,
@@ -361,7 +375,7 @@ int per_scan_step(int64_t B, int64_t D, int32_t type, const void* d_x, int64_t x
   a.reset = d_reset;
   a.h = d_h;
   a.h_out = d_h_out;
-  return done(per::launch_scan_step(a, type, stream), "per_scan_step");
+  return run("per_scan_step", [&] { return per::launch_scan_step(a, type, stream); });
 }
 
 int per_distill_workspace_bytes(int64_t N, int64_t V, int64_t K, int32_t type, size_t* out) {
@@ -391,12 +405,13 @@ int per_distill(int64_t N, int64_t V, int64_t K, int32_t type, const void* d_log
   a.grad = d_grad;
   a.grad_stride = grad_stride;
   if (per::distill_resident(N, V, type))
-    return done(per::launch_distill_fused(a, type, stream), "per_distill");
+    return run("per_distill", [&] { return per::launch_distill_fused(a, type, stream); });
   if ((rc = check_ws(d_ws, ws_bytes, distill_space(N, V, K, type).total))) return rc;
   set_space(a, d_ws, type);
-  hipError_t e = per::launch_distill_forward(a, type, stream);
-  if (e == hipSuccess) e = per::launch_distill_backward(a, type, stream);
-  return done(e, "per_distill");
+  return run("per_distill", [&] {
+    const hipError_t e = per::launch_distill_forward(a, type, stream);
+    return e == hipSuccess ? per::launch_distill_backward(a, type, stream) : e;
+  });
 }
 
 int per_distill_forward(int64_t N, int64_t V, int64_t K, int32_t type, const void* d_logits,
@@ -415,7 +430,7 @@ int per_distill_forward(int64_t N, int64_t V, int64_t K, int32_t type, const voi
   set_space(a, d_ws, type);
   a.loss = d_loss;
   a.saved = d_saved;
-  return done(per::launch_distill_forward(a, type, stream), "per_distill_forward");
+  return run("per_distill_forward", [&] { return per::launch_distill_forward(a, type, stream); });
 }
 
 int per_distill_backward(int64_t N, int64_t V, int64_t K, int32_t type, const void* d_logits,
@@ -435,5 +450,5 @@ int per_distill_backward(int64_t N, int64_t V, int64_t K, int32_t type, const vo
   a.weight = d_gloss;
   a.grad = d_grad;
   a.grad_stride = grad_stride;
-  return done(per::launch_distill_backward(a, type, stream), "per_distill_backward");
+  return run("per_distill_backward", [&] { return per::launch_distill_backward(a, type, stream); });
 }

@@ -6,6 +6,28 @@
 
 namespace per {
 
+// Every launch of these operators goes through here.  An entry point runs its
+// launches twice: first `counting`, which only takes the work-items of the
+// largest (a dispatch holds fewer than 2^32), so that a call too large for one
+// of them is refused before any of them has run.
+struct Launches {
+  bool counting = false;
+  uint64_t items = 0;
+};
+Launches& launches();  // the calling thread's
+
+template <typename... KArgs, typename... Args>
+hipError_t enqueue(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t lds, hipStream_t s,
+                   Args... args) {
+  Launches& l = launches();
+  if (l.counting) {
+    const uint64_t n = (uint64_t)grid.x * block.x;
+    if (n > l.items) l.items = n;
+    return hipSuccess;
+  }
+  return launch_kernel(kern, grid, block, lds, s, args...);
+}
+
 // ------------------------------------------------------------ 8-bit row store
 struct RowsArgs {
   uint8_t* codes;
