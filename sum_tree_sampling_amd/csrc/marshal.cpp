@@ -12,6 +12,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/core/grad_mode.h>
+#include <c10/core/AutogradState.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -148,15 +149,6 @@ struct Where {
     return at::empty(shape, at::TensorOptions().dtype(dtype).device(at::kCUDA, device));
   }
 };
-
-// Nothing here is recorded for autograd: a call that would silently cut a graph is
-// refused (inside an autograd.Function, and under no_grad, recording is off).
-void unrecorded(const Args& a, int i) {
-  if (a.v[i] && at::GradMode::is_enabled() && a.tensor(i).requires_grad())
-    refuse(std::string(a.names[i]) +
-           " requires grad: call this under torch.no_grad() or from an autograd.Function; its "
-           "gradients come from explicit calls");
-}
 
 std::string text(at::IntArrayRef s) {
   std::string t = "(";
@@ -363,7 +355,6 @@ Sequences sequences(const Args& a, const Where& w) {
 // x, g, reset, length, h0, y, h_last, carries, stream
 PyObject* scan_forward(const Args& a) {
   const Where w(a.v[8], a.tensor(0), "x");
-  for (int i : {0, 1, 4}) unrecorded(a, i);
   const Sequences s = sequences(a, w);
   const int64_t all[] = {s.B, s.T, s.D}, state[] = {s.B, s.D}, carry[] = {s.B, s.chunks, s.D};
   const uint8_t* reset = flags(a, 2, {s.B, s.T}, w);
@@ -411,7 +402,6 @@ PyObject* scan_backward(const Args& a) {
 PyObject* scan_step(const Args& a) {
   const Tensor& x = a.tensor(0);
   const Where w(a.v[6], x, "x");
-  for (int i : {0, 1, 2}) unrecorded(a, i);
   if (x.dim() != 2) refuse("x must be [B x D]");
   const int type = type_of(x, "x");
   const auto dt = x.scalar_type();
@@ -425,6 +415,7 @@ PyObject* scan_step(const Args& a) {
   const Matrix my = matrix(y, "y", dt, shape, w);
   check(api.per_scan_step(shape[0], shape[1], type, mx.p, mx.stride, mg.p, mg.stride, reset, h, pho,
                           my.p, my.stride, w.stream));
+  if (!a.v[4] && !ho.is_inference()) ho.unsafeGetTensorImpl()->bump_version();
   return pair(y, ho);
 }
 
@@ -474,7 +465,6 @@ Top top(const Args& a, int lse, const Where& w) {
 // logits, tidx, tlogit, tlse, temperature, weight, loss, grad, stream
 PyObject* distill(const Args& a) {
   const Where w(a.v[8], a.tensor(0), "logits");
-  unrecorded(a, 0);
   const Top o = top(a, 3, w);
   const int64_t all[] = {o.N, o.V};
   const auto* weight = dense<const float>(a, 5, at::kFloat, {o.N}, w);
@@ -492,7 +482,6 @@ PyObject* distill(const Args& a) {
 // logits, tidx, tlogit, tlse, temperature, loss, saved, stream
 PyObject* distill_forward(const Args& a) {
   const Where w(a.v[7], a.tensor(0), "logits");
-  unrecorded(a, 0);
   const Top o = top(a, 3, w);
   const Tensor loss = output(a, 5, {o.N}, at::kFloat, w),
                saved = output(a, 6, {o.N, 4 + o.K}, at::kFloat, w);
@@ -531,57 +520,94 @@ struct Function {
   PyObject* (*run)(const Args&);
   int required;
   int n;
+  unsigned written;  // bit i: argument i is written where it is given
   const char* names[kMaxArgs];
   const char* doc;
   PyObject* interned[kMaxArgs];
 };
+constexpr unsigned bits() { return 0; }
+template <typename... I>
+constexpr unsigned bits(int i, I... more) {
+  return 1u << i | bits(more...);
+}
+
+// Nothing here is recorded for autograd: a call that would silently cut a graph, or
+// drop a tangent, is refused, whichever argument it is.  (Inside an
+// autograd.Function, and under no_grad, recording is off.)
+void unrecorded(const Function& f, const Args& a) {
+  const bool grad = at::GradMode::is_enabled();
+  const bool tangent = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+  if (!grad && !tangent) return;
+  for (int i = 0; i < f.n; ++i) {
+    if (!a.v[i] || !THPVariable_Check(a.v[i])) continue;
+    const Tensor& t = THPVariable_Unpack(a.v[i]);
+    if (!t.unsafeGetTensorImpl()->autograd_meta()) continue;
+    if (grad && t.requires_grad())
+      refuse(std::string(f.names[i]) +
+             " requires grad: call this under torch.no_grad() or from an autograd.Function; its "
+             "gradients come from explicit calls");
+    if (tangent && t._fw_grad(0).defined())
+      refuse(std::string(f.names[i]) +
+             " carries a forward-mode tangent, which this call would drop: pass its primal");
+  }
+}
+
+// The tensors a call wrote count as changed in place, so that autograd notices where
+// one of them had been saved.
+void wrote(const Function& f, const Args& a) {
+  for (int i = 0; i < f.n; ++i) {
+    if (!(f.written >> i & 1u) || !a.v[i]) continue;
+    const Tensor& t = THPVariable_Unpack(a.v[i]);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
+}
 
 Function functions[] = {
-    {"per_rows_write", rows_write, 3, 6, {"codes", "scales", "src", "first", "group", "stream"},
+    {"per_rows_write", rows_write, 3, 6, bits(0, 1), {"codes", "scales", "src", "first", "group", "stream"},
      "per_rows_write(codes, scales, src, first=0, group=128, stream=None)\n\n"
      "Quantise the rows of src into the ring's slots first, first + 1, ...", {}},
-    {"per_rows_write_at", rows_write_at, 5, 7,
+    {"per_rows_write_at", rows_write_at, 5, 7, bits(0, 1, 4),
      {"codes", "scales", "src", "slots", "claims", "group", "stream"},
      "per_rows_write_at(codes, scales, src, slots, claims, group=128, stream=None)\n\n"
      "Quantise row j of src into slot slots[j]; of a repeated slot the last position wins.\n"
      "claims: [capacity] int32 zeros, zero again afterwards.", {}},
-    {"per_rows_read", rows_read, 3, 8,
+    {"per_rows_read", rows_read, 3, 8, bits(5),
      {"codes", "scales", "idx", "window", "group", "out", "dtype", "stream"},
      "per_rows_read(codes, scales, idx, window=1, group=128, out=None, dtype=torch.float32, "
      "stream=None)\n\n[B x window x dim]: the rows of slots idx[b], idx[b] + 1, ... of the ring.",
      {}},
-    {"per_scan_workspace_bytes", scan_workspace, 3, 3, {"B", "T", "D"},
+    {"per_scan_workspace_bytes", scan_workspace, 3, 3, bits(), {"B", "T", "D"},
      "per_scan_workspace_bytes(B, T, D)", {}},
-    {"per_scan_forward", scan_forward, 2, 9,
+    {"per_scan_forward", scan_forward, 2, 9, bits(5, 6, 7),
      {"x", "g", "reset", "length", "h0", "y", "h_last", "carries", "stream"},
      "per_scan_forward(x, g, reset=None, length=None, h0=None, y=None, h_last=None, carries=None, "
      "stream=None)\n\nh_t = f h_{t-1} + (1 - f) x_t with f = sigmoid(g_t) along dim 1 of x, g\n"
      "[B x T x D].  Returns (y [B x T x D], h_last [B x D] f32, carries: the f32 states that\n"
      "per_scan_backward takes).", {}},
-    {"per_scan_backward", scan_backward, 4, 11,
+    {"per_scan_backward", scan_backward, 4, 11, bits(7, 8, 9),
      {"x", "g", "carries", "dy", "reset", "length", "dh_last", "dx", "dg", "dh0", "stream"},
      "per_scan_backward(x, g, carries, dy, reset=None, length=None, dh_last=None, dx=None, "
      "dg=None, dh0=None, stream=None)\n\n"
      "Gradients (dx, dg, dh0) of per_scan_forward from dy and dh_last.", {}},
-    {"per_scan_step", scan_step, 3, 7, {"x", "g", "h", "reset", "h_out", "y", "stream"},
+    {"per_scan_step", scan_step, 3, 7, bits(4, 5), {"x", "g", "h", "reset", "h_out", "y", "stream"},
      "per_scan_step(x, g, h, reset=None, h_out=None, y=None, stream=None)\n\n"
      "One step of B sequences: x, g [B x D], h [B x D] f32 (updated in place without h_out).\n"
      "Returns (y, h_out).", {}},
-    {"per_distill_workspace_bytes", distill_workspace, 4, 4, {"N", "V", "K", "type"},
+    {"per_distill_workspace_bytes", distill_workspace, 4, 4, bits(), {"N", "V", "K", "type"},
      "per_distill_workspace_bytes(N, V, K, type)", {}},
-    {"per_distill", distill, 3, 9,
+    {"per_distill", distill, 3, 9, bits(6, 7),
      {"logits", "tidx", "tlogit", "tlse", "temperature", "weight", "loss", "grad", "stream"},
      "per_distill(logits, tidx, tlogit, tlse=None, temperature=1.0, weight=None, loss=None, "
      "grad=None, stream=None)\n\n"
      "Per-row distillation loss [N] (not weighted) and its gradient by the logits [N x V]\n"
      "(weighted), against the teacher's logits tlogit [N x K] at tokens tidx [N x K] int32.\n"
      "grad may be logits.  Returns (loss, grad).", {}},
-    {"per_distill_forward", distill_forward, 3, 8,
+    {"per_distill_forward", distill_forward, 3, 8, bits(5, 6),
      {"logits", "tidx", "tlogit", "tlse", "temperature", "loss", "saved", "stream"},
      "per_distill_forward(logits, tidx, tlogit, tlse=None, temperature=1.0, loss=None, saved=None, "
      "stream=None)\n\n"
      "Per-row loss [N], and the row statistics per_distill_backward takes.", {}},
-    {"per_distill_backward", distill_backward, 5, 9,
+    {"per_distill_backward", distill_backward, 5, 9, bits(7),
      {"logits", "tidx", "tlogit", "saved", "gloss", "tlse", "temperature", "grad", "stream"},
      "per_distill_backward(logits, tidx, tlogit, saved, gloss, tlse=None, temperature=1.0, "
      "grad=None, stream=None)\n\n"
@@ -600,7 +626,11 @@ PyObject* call(Function& f, PyObject* const* args, Py_ssize_t nargs, PyObject* k
     }
   }
   try {
-    return f.run(Args(f.name, f.names, f.interned, f.n, f.required, args, nargs, kwnames));
+    const Args a(f.name, f.names, f.interned, f.n, f.required, args, nargs, kwnames);
+    unrecorded(f, a);
+    PyObject* out = f.run(a);
+    wrote(f, a);
+    return out;
   } catch (const Refused& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
   } catch (const Failed& e) {

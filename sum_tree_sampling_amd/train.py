@@ -8,8 +8,10 @@ not given are allocated on the stream the call runs on; with an explicit
 `stream` the usual rule of torch holds for tensors used on another stream than
 their own: the caller orders the streams and keeps the tensors alive
 (Tensor.record_stream).  Forward and backward passes are explicit calls;
-nothing is recorded for autograd, and an input that requires grad is refused
-while autograd records (not under no_grad, nor inside an autograd.Function).
+nothing is recorded for autograd.  Any argument that requires grad is refused
+while autograd records (not under no_grad, nor inside an autograd.Function), and
+any that carries a forward-mode tangent while those are taken.  Tensors that a
+call writes count as changed in place (Tensor._version).
 """
 from __future__ import annotations
 
