@@ -418,7 +418,7 @@ __device__ __forceinline__ float rest_sum(const Chunk<T>& v, uint32_t marks, flo
 template <typename T, int NT, int R, bool TAIL, bool SIDE>
 __global__ __launch_bounds__(SIDE ? NT + 64 : NT, NT < 512 ? 1 : 4)
 void distill_row_kernel(DistillArgs a) {
-  extern __shared__ char mem[];
+  extern __shared__ __attribute__((aligned(16))) char mem[];
   __shared__ float red[3][NT / 64];
   __shared__ double wide[2][NT / 64];  // the waves' sums over the rest and over all tokens
   __shared__ Teacher t;  // kept here, not in registers across the passes
@@ -675,7 +675,7 @@ __device__ __forceinline__ void drop_top(Chunk<T>& v, uint32_t marks) {
 // reads the teacher.
 template <typename T, bool TAIL>
 __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(DistillArgs a) {
-  extern __shared__ char mem[];
+  extern __shared__ __attribute__((aligned(16))) char mem[];
   __shared__ float red[kPartThreads / 64];
   __shared__ double sums_of[kPartThreads / 64];
   __shared__ float top_mt;
@@ -809,7 +809,7 @@ constexpr int kAhead = 4;  // entries a lane loads at once
 // Gradient of one part of a row from its saved statistics and probabilities.
 template <typename T, bool TAIL>
 __global__ __launch_bounds__(kPartThreads + 64) void distill_grad_kernel(DistillArgs a) {
-  extern __shared__ char mem[];
+  extern __shared__ __attribute__((aligned(16))) char mem[];
   __shared__ uint32_t sh_dup;
   const int64_t n = blockIdx.x / (uint32_t)a.splits;
   const int tid = threadIdx.x, wv = tid >> 6;
@@ -908,7 +908,7 @@ int teacher_waves(int K) {
 template <typename T, int R, bool TAIL, int PASS>
 __global__ __launch_bounds__(PASS == kGradient ? 64 * kWaveRows : 128 * kWaveRows, R == 12 ? 4 : 1)
 void distill_wave_kernel(DistillArgs a, uint32_t words) {
-  extern __shared__ char mem[];
+  extern __shared__ __attribute__((aligned(16))) char mem[];
   __shared__ Student stat[kWaveRows];
   __shared__ Teacher teachers[kWaveRows];
   const int lane = threadIdx.x & 63;
