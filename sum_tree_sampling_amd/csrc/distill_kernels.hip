@@ -325,15 +325,18 @@ __device__ __forceinline__ float rest_coef(const DistillArgs& a, float m, float 
 template <bool TAIL>
 __device__ __forceinline__ void save_row(const DistillArgs& a, int64_t n, bool dead,
                                          const Student& s, double p_rest) {
-  const double C = !TAIL ? 1.0 / s.S
-                   : s.Sr == 0.0
-                       ? 0.0
-                       : exp(((double)s.mr - (double)s.m) * a.inv_tau) / s.S - p_rest / s.Sr;
+  float C = 0.0f;
+  if (!TAIL) {
+    C = 1.0f / (float)s.S;
+  } else if (s.Sr != 0.0) {
+    const double e = s.mr == s.m ? 1.0 : exp(((double)s.mr - (double)s.m) * a.inv_tau);
+    C = (float)(e * s.Sr - p_rest * s.S) / (float)(s.S * s.Sr);
+  }
   float* to = a.saved + n * (4 + a.K);
   to[0] = s.m;
   to[1] = dead ? 0.0f : (float)s.S;
   to[2] = s.mr;
-  to[3] = dead ? 0.0f : (float)C;
+  to[3] = dead ? 0.0f : C;
 }
 
 // Where the rest's sum against the row's largest logit is below this, it is taken
