@@ -136,9 +136,11 @@ __device__ __forceinline__ void store_chunk(T* grad, const Row<T>& r, uint32_t j
 // marks the tokens of chunks [c0, c1) of the row; without one it only has to
 // find repeated entries, and marks them modulo its size.  Tokens that merely meet
 // there cost patch_top a second look, K^2 of LDS reads (10 us of a row with K = 239),
-// so the size grows with K: at most one row in four has such a pair up to K = 256.
+// so the size grows with K: at most one row in four has such a pair up to K = 256,
+// and past that no two tokens meet, 2^18 bits being a whole part's (1024 rows of 139000
+// with K = 1024: 180 us, 380 where 2^17 bits let one pair of each row meet).
 __host__ __device__ inline uint32_t hash_words(int K) {
-  return K <= 128 ? 1024 : K <= 181 ? 2048 : 4096;
+  return K <= 128 ? 1024 : K <= 181 ? 2048 : K <= 256 ? 4096 : 8192;
 }
 __host__ __device__ inline uint32_t mark_words(bool tail, int64_t tokens, int K) {
   const uint32_t w = (uint32_t)((tokens + 127) / 128 * 4), h = hash_words(K);
