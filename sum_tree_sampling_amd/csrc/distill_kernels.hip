@@ -756,11 +756,13 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_part_kernel(Distill
         m = mb;
       }
       const float ms = m == kNegInf ? 0.0f : m;
+      float sum = 0.0f;  // so a thread adds at most 128 of these, of a part's 2^18 tokens
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         const uint32_t j = j0 + q * kPartThreads;
-        if (j < s.c1) rest += rest_sum<T>(v[q], 0, ms, a.c);
+        if (j < s.c1) sum += rest_sum<T>(v[q], 0, ms, a.c);
       }
+      rest += sum;
       if (j0 + kBatch * kPartThreads < s.c1) load_batch(r, j0 + kBatch * kPartThreads, s.c1, v);
     }
     const float mw = wave_max(m);

@@ -208,3 +208,31 @@ def test_loss_at_large_temperatures(V, K, N, tau):
     tol = tau * tau * 32 * U / math.sqrt(V) + 2 * U * want.abs()
     assert_close(fused, want, tol, "loss")
     assert_close(apart, want, tol, "forward loss")
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype,V", [("f32", 262140), ("bf16", 200003), ("f32", 131073)])
+def test_long_rows_in_one_part(dtype, V, tail):
+    """From 641 rows on a row of up to 2^18 tokens is one workgroup's, whose threads
+    add up to 1024 exponentials each: 8 or 16 at a time, so that no sum is longer than 128
+    + 16 roundings.  One of the rows has nearly equal logits."""
+    import sum_tree_sampling_amd as p
+    from train_oracle import distill
+    N, K, tau = 1300, 40, 1.2
+    g = gen(V)
+    z = 3 * torch.randn(3, V, generator=g)
+    z[1] = 1e-3 * torch.randn(V, generator=g)
+    z = z.to(TYPES[dtype])
+    tidx = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(3)]).to(torch.int32)
+    t, w = (3 * torch.randn(3, K, generator=g)).to(TYPES[dtype]), torch.rand(3, generator=g)
+    tlse = (torch.logsumexp(t.double() / tau, 1) + 0.5).float() if tail else None
+    want = distill(z, tidx, t, tlse, tau, w, z.dtype)
+    plain = distill(z, tidx, t, tlse, tau, None, z.dtype)["loss"]
+    at = torch.arange(N) % 3
+    gz, gi, gt, gw = (a.cuda()[at.cuda()] for a in (z, tidx, t, w))
+    gl = None if tlse is None else tlse[at].cuda()
+    loss, saved = p.per_distill_forward(gz, gi, gt, tlse=gl, temperature=tau)
+    grad = p.per_distill_backward(gz, gi, gt, saved, gw, tlse=gl, temperature=tau)
+    for lo in (0, N // 3 * 3 - 3):
+        assert_close(loss[lo:lo + 3], *plain, "loss")
+        assert_close(grad[lo:lo + 3], *want["grad"], "grad")
