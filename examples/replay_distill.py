@@ -53,6 +53,13 @@ class Replay:
         self.begins[self.tree.cursor] = True  # what lies behind the newest row does not follow it
 
 
+def slots_ahead(idx, ahead, cursor):
+    """The slots `ahead` of idx; -1, which is no slot, where the newest row comes
+    before them: what lies there is of an older episode, or not yet written."""
+    newer = (cursor - 1 - idx) % CAPACITY
+    return torch.where(ahead <= newer, (idx + ahead) % CAPACITY, -1)
+
+
 class Student:
     """rows -> (values, gates) -> gated linear recurrence -> logits."""
 
@@ -104,7 +111,8 @@ class Student:
         replay.tree.update(idx, (0.9 * seq.amax(1) + 0.1 * seq.mean(1)).contiguous())
         # the state before the slot half a window on, with the weights that made it
         half = WINDOW // 2
-        per.per_rows_write_at(*replay.states, y[:, half - 1], (idx + half) % CAPACITY, replay.claims, group=64)
+        per.per_rows_write_at(*replay.states, y[:, half - 1], slots_ahead(idx, half, replay.tree.cursor),
+                              replay.claims, group=64)
         return loss.mean()
 
 
