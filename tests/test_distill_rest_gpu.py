@@ -236,3 +236,28 @@ def test_long_rows_in_one_part(dtype, V, tail):
     for lo in (0, N // 3 * 3 - 3):
         assert_close(loss[lo:lo + 3], *plain, "loss")
         assert_close(grad[lo:lo + 3], *want["grad"], "grad")
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V,N", [(300, 5), (4000, 1100), (11000, 520), (40000, 130), (150001, 3)])
+def test_rows_of_weight_0(V, N, tail):
+    """Loss 0 and gradient 0, whatever the row's logits, entries and normaliser hold."""
+    import sum_tree_sampling_amd as p
+    K = 5
+    z = torch.randn(N, V, device="cuda")
+    tidx = torch.randint(0, V, (N, K), device="cuda", dtype=torch.int32)
+    t, w = torch.randn(N, K, device="cuda"), torch.rand(N, device="cuda") + 0.1
+    tlse = torch.logsumexp(t, 1) + 0.5 if tail else None
+    clean = p.per_distill(z, tidx, t, tlse=tlse, weight=w)
+    off = torch.arange(N, device="cuda") % 3 == 1
+    w[off] = 0.0
+    z[off] = math.nan
+    t[off] = math.inf
+    tidx[off] = -7
+    if tail:
+        tlse[off] = math.nan
+    loss, grad = p.per_distill(z, tidx, t, tlse=tlse, weight=w)
+    _, saved = p.per_distill_forward(z, tidx, t, tlse=tlse)
+    g2 = p.per_distill_backward(z, tidx, t, saved, w, tlse=tlse)
+    assert not loss[off].any() and not grad[off].any() and not g2[off].any()
+    assert torch.equal(loss[~off], clean[0][~off]) and torch.equal(grad[~off], clean[1][~off])
