@@ -156,6 +156,11 @@ __device__ __forceinline__ bool whole(int n, uint32_t mask) {
 }
 
 __device__ __forceinline__ bool ignores(float A) { return __float_as_uint(A) == 0x80000000u; }
+// A product of gates that has come out as 0 stands for one that is not: an infinite
+// state stays infinite through it (0 would make it NaN), a finite one vanishes.
+__device__ __forceinline__ float gates(float A) {
+  return __float_as_uint(A) == 0 ? 0x1p-149f : A;
+}
 // The map (A, B) on a state.
 __device__ __forceinline__ float apply(float A, float B, float h) {
   return ignores(A) ? B : __builtin_fmaf(A, h, B);
@@ -213,7 +218,7 @@ __global__ __launch_bounds__(kMaxWaves * 64, 4) void scan_forward_kernel(ScanArg
       for (int c = 0; c < C; ++c) {
         const float sa = in ? m[c] : 0.0f, sb = in ? m[a.D + c] : 0.0f;
         B[c] = apply(sa, sb, B[c]);
-        A[c] = ignores(sa) ? sa : A[c] * sa;
+        A[c] = ignores(sa) ? sa : gates(A[c] * sa);
       }
     }
 #pragma unroll
@@ -262,7 +267,7 @@ __global__ __launch_bounds__(kMaxWaves * 64, 4) void scan_forward_kernel(ScanArg
     if ((PACK || in) && full) reduce(std::true_type{});
     else if (PACK ? __any(n > 0) : in && n > 0) reduce(std::false_type{});
 #pragma unroll
-    for (int c = 0; c < C; ++c) sA[buf][wv][c][lane] = A[c], sB[buf][wv][c][lane] = B[c];
+    for (int c = 0; c < C; ++c) sA[buf][wv][c][lane] = gates(A[c]), sB[buf][wv][c][lane] = B[c];
     __syncthreads();
     float hs[C];
 #pragma unroll
@@ -367,7 +372,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void scan_segment_kernel(ScanArgs a
     else reduce(std::false_type{});
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c) sA[wv][c][lane] = A[c], sB[wv][c][lane] = B[c];
+  for (int c = 0; c < C; ++c) sA[wv][c][lane] = gates(A[c]), sB[wv][c][lane] = B[c];
   __syncthreads();
   if (wv != 0) return;
 #pragma unroll
@@ -379,7 +384,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void scan_segment_kernel(ScanArgs a
     for (int c = 0; c < C; ++c) {
       const float wa = sA[w][c][lane];
       B[c] = apply(wa, sB[w][c][lane], B[c]);
-      A[c] = ignores(wa) ? wa : A[c] * wa;
+      A[c] = ignores(wa) ? wa : gates(A[c] * wa);
     }
   }
   if (in) {
@@ -432,7 +437,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void scan_backward_kernel(ScanAr
       for (int c = 0; c < C; ++c) {
         const float sa = in ? m[c] : 0.0f, sb = in ? m[a.D + c] : 0.0f;
         B[c] = apply(sa, sb, B[c]);
-        A[c] = ignores(sa) ? sa : A[c] * sa;
+        A[c] = ignores(sa) ? sa : gates(A[c] * sa);
       }
     }
 #pragma unroll
@@ -505,7 +510,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void scan_backward_kernel(ScanAr
     else if (PACK ? __any(n > 0) : in && n > 0) reduce(std::false_type{});
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      sA[buf][wv][c][lane] = A[c];
+      sA[buf][wv][c][lane] = gates(A[c]);
       sB[buf][wv][c][lane] = B[c];
       sQ[buf][wv][c][lane] = Q[c];
     }
