@@ -601,6 +601,7 @@ Function functions[] = {
      "grad=None, stream=None)\n\n"
      "Per-row distillation loss [N] (not weighted) and its gradient by the logits [N x V]\n"
      "(weighted), against the teacher's logits tlogit [N x K] at tokens tidx [N x K] int32.\n"
+     "Temperatures lie in [2^-20, 64].\n"
      "grad may be logits.  Returns (loss, grad).", {}},
     {"per_distill_forward", distill_forward, 3, 8, bits(5, 6),
      {"logits", "tidx", "tlogit", "tlse", "temperature", "loss", "saved", "stream"},
