@@ -1,0 +1,156 @@
+/*
+ * per_block.h -- C ABI of the layers of a student that reads tokens, next to the
+ * operators of per_train.h (libper.so, MI355X gfx950):
+ *
+ *   - the embedding of tokens, with its gradient summed in the tokens' order;
+ *   - layer norm, forward and backward, with the gradients of weight and bias;
+ *   - the gated delta rule, a recurrence whose state is a matrix: forward,
+ *     backward, and one step for an actor.
+ *
+ * Conventions are those of per_train.h: d_ pointers are device pointers owned by
+ * the caller, work is enqueued on the caller's stream without waiting, nothing is
+ * allocated, all checks happen on the host before anything is enqueued, there is
+ * no handle, and calls that share no writable array may overlap on different
+ * streams.  Types are PER_F32, PER_BF16 and PER_F16; strides count elements.
+ * Sums, statistics and states are f32 or wider; what is returned in 16 bits is
+ * rounded once, to nearest even.  Results do not depend on the order in which
+ * workgroups run.
+ */
+#ifndef PER_BLOCK_H
+#define PER_BLOCK_H
+
+#include "per_train.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * The embedding.  Token n is d_tokens[n], an int32 (token_bytes 4) or an int64
+ * (token_bytes 8); tokens outside [0, V) are absent (padding).
+ *
+ * per_embed_forward: out[n] = scale * table[token n] (the product in f32, rounded
+ *   to out_type), zeros where the token is absent.  d_table [V x D] of
+ *   table_type, d_out [N x D] of out_type, both with rows stride elements apart.
+ * per_embed_backward: grad[v] = scale * sum of d_dout[n] over the n whose token is
+ *   v, zeros for tokens that do not occur; with accumulate the sum is added to
+ *   what d_grad holds, and rows of tokens that do not occur are left alone.  Rows
+ *   are added in f32 in an order that depends on N, V and D alone, so the same
+ *   call gives the same bits.  d_dout [N x D] of dout_type, d_grad [V x D] of
+ *   grad_type.  The two must not overlap.
+ * per_embed_workspace_bytes: device workspace of per_embed_backward, 16-byte
+ *   aligned, scratch of one call.
+ * N in [0, 2^28], V in [1, 2^24], D in [1, 2^20].
+ */
+#define PER_MAX_TOKENS (1LL << 28)
+
+int per_embed_forward(int64_t N, int64_t V, int64_t D, const void* d_tokens, int32_t token_bytes,
+                      const void* d_table, int32_t table_type, int64_t table_stride, double scale,
+                      void* d_out, int32_t out_type, int64_t out_stride, hipStream_t stream);
+int per_embed_workspace_bytes(int64_t N, int64_t V, int64_t D, size_t* out);
+int per_embed_backward(int64_t N, int64_t V, int64_t D, const void* d_tokens, int32_t token_bytes,
+                       const void* d_dout, int32_t dout_type, int64_t dout_stride, double scale,
+                       int32_t accumulate, void* d_grad, int32_t grad_type, int64_t grad_stride,
+                       void* d_ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Layer norm over the D columns of each of N rows:
+ *     m = mean(x), r = 1 / sqrt(mean((x - m)^2) + eps), xhat = (x - m) r,
+ *     y = xhat * weight + bias
+ * d_weight, d_bias: [D] of affine_type (PER_F32, or the type of x), each may be
+ * NULL (1 and 0).
+ *
+ * per_norm_forward: d_stats (or NULL) [N x 2] f32 gets m and r of each row, for the
+ *   backward pass.  d_y may be d_x (with the same stride).
+ * per_norm_backward: with e = dy * weight,
+ *     dx = r (e - mean(e) - xhat mean(e xhat)),
+ *     dweight = sum over rows of dy xhat, dbias = sum over rows of dy,
+ *   both [D] f32, either may be NULL.  Rows are added in an order that depends on N
+ *   and D alone.  d_dx may be d_dy (with the same stride).  With N = 0, dweight and
+ *   dbias are zeros.
+ * per_norm_workspace_bytes: device workspace of per_norm_backward, 16-byte
+ *   aligned, scratch of one call.
+ * N in [0, 2^31), D in [1, 2^20], 0 <= eps < infinity; a row whose values are all
+ * equal has r = 1 / sqrt(eps), infinite for eps = 0.
+ */
+int per_norm_forward(int64_t N, int64_t D, int32_t type, const void* d_x, int64_t x_stride,
+                     const void* d_weight, const void* d_bias, int32_t affine_type, double eps,
+                     void* d_y, int64_t y_stride, float* d_stats, hipStream_t stream);
+int per_norm_workspace_bytes(int64_t N, int64_t D, int32_t type, size_t* out);
+int per_norm_backward(int64_t N, int64_t D, int32_t type, const void* d_x, int64_t x_stride,
+                      const float* d_stats, const void* d_dy, int64_t dy_stride,
+                      const void* d_weight, int32_t affine_type, void* d_dx, int64_t dx_stride,
+                      float* d_dweight, float* d_dbias, void* d_ws, size_t ws_bytes,
+                      hipStream_t stream);
+
+/*
+ * The gated delta rule.  Sequence b and value head h carry a state S [DK x DV] f32.
+ * With f = 1 / (1 + exp(-g)), w = 1 / (1 + exp(-b)) and the head's query q, key k
+ * and value v of step t:
+ *     S' = f S                     (S' = 0 where d_reset[b, t] is not 0)
+ *     u  = w (v - S'^T k)          what the state takes up at k
+ *     S  = S' + k u^T
+ *     o  = scale S^T q
+ * H value heads share HK heads of queries and keys, HK a divisor of H: value head h
+ * reads head h / (H / HK).  A sequence ends after d_length[b] steps (T when NULL;
+ * values outside [0, T] are clamped): outputs and gradients past its end are 0, and
+ * what the inputs hold there is not used.
+ *
+ * q, k: [B x T x HK x DK], v, o: [B x T x H x DV], g, b: [B x T x H], all of `type`
+ * with unit stride along DK and DV and their own strides between sequences (sb),
+ * steps (st) and heads (sh).  d_reset: [B x T] u8, dense.  States (s0, s_last, s,
+ * ds_last, ds0) are dense [B x H x DK x DV] f32; NULL where read means 0, and where
+ * written that it is not wanted.
+ *
+ * per_delta_forward writes o, s_last and d_carries (or NULL), for the backward
+ *   pass: dense [B x ceil(T / PER_DELTA_CHUNK) x H x (DK + PER_DELTA_CHUNK) x DV]
+ *   f32, the state before each chunk of steps and behind it the u of its steps
+ *   (not written for chunks past a sequence's end).  d_s_last may be d_s0.
+ * per_delta_backward takes those carries, do, and ds_last, the gradient of s_last,
+ *   and writes the gradients of q, k, v, g, b and s0 (dq and dk summed over the
+ *   value heads that share a head).
+ * per_delta_workspace_bytes: device workspace of per_delta_forward, or of
+ *   per_delta_backward where `backward` is not 0; 16-byte aligned, scratch of one
+ *   call.
+ * per_delta_step: one step of B sequences: q, k [B x HK x DK], v, o [B x H x DV],
+ *   g, b [B x H], strides between sequences (sb) and heads (sh); d_s_out may be d_s.
+ *
+ * DK in [1, 128], DV in [1, 256].  Steps are taken 64 at a time, as products of
+ * matrices whose factors are held to 24 bits, so results are those of f32
+ * arithmetic for keys up to length 1, for which the rule is meant; longer keys
+ * (w |k|^2 > 2) make the recurrence itself grow.  A state that is
+ * not finite does not pass a reset, nor does the gradient of one; q, k, v, g, b and do
+ * that are not finite leave what is computed of their own sequence and head undefined
+ * from their chunk of steps on (before it, for do), up to a reset in another chunk.
+ */
+#define PER_DELTA_CHUNK 64
+#define PER_DELTA_MAX_DK 128
+#define PER_DELTA_MAX_DV 256
+
+/* An array of sequences: data, and strides between sequences, steps and heads. */
+typedef struct per_seq {
+  void* p;
+  int64_t sb, st, sh;
+} per_seq;
+
+int per_delta_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t DK, int64_t DV,
+                              int32_t type, int32_t backward, size_t* out);
+int per_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t DK, int64_t DV,
+                      int32_t type, per_seq q, per_seq k, per_seq v, per_seq g, per_seq b,
+                      const uint8_t* d_reset, const int64_t* d_length, const float* d_s0,
+                      double scale, per_seq o, float* d_s_last, float* d_carries, void* d_ws,
+                      size_t ws_bytes, hipStream_t stream);
+int per_delta_backward(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t DK, int64_t DV,
+                       int32_t type, per_seq q, per_seq k, per_seq v, per_seq g, per_seq b,
+                       const uint8_t* d_reset, const int64_t* d_length, const float* d_carries,
+                       per_seq d_o, const float* d_ds_last, double scale, per_seq dq, per_seq dk,
+                       per_seq dv, per_seq dg, per_seq db, float* d_ds0, void* d_ws,
+                       size_t ws_bytes, hipStream_t stream);
+int per_delta_step(int64_t B, int64_t H, int64_t HK, int64_t DK, int64_t DV, int32_t type,
+                   per_seq q, per_seq k, per_seq v, per_seq g, per_seq b, const uint8_t* d_reset,
+                   const float* d_s, double scale, float* d_s_out, per_seq o, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* PER_BLOCK_H */

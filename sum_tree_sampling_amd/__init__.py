@@ -1,6 +1,6 @@
 """MI355X (gfx950) prioritized-replay sum tree: HIP kernels behind a C ABI.
 
-The public ABI is include/per.h and include/per_train.h (libper.so); per.py and
+The public ABI is include/per.h, include/per_train.h and include/per_block.h (libper.so); per.py and
 train.py are its Python bindings.
 """
 from .per import (PerBuffer, PerError, load, per_add, per_capacity, per_create, per_cursor,
@@ -11,8 +11,11 @@ from .per import (PerBuffer, PerError, load, per_add, per_capacity, per_create, 
                   per_set_sample_lanes, per_size,
                   per_state_dim, per_time_next, per_total, per_tree_ptrs, per_update, per_update_add,
                   per_update_static, per_workspace_bytes)
-from .train import (per_distill, per_distill_backward, per_distill_forward,
-                    per_distill_workspace_bytes, per_rows_read, per_rows_write, per_rows_write_at,
+from .train import (per_delta_backward, per_delta_forward, per_delta_step,
+                    per_delta_workspace_bytes, per_distill, per_distill_backward, per_distill_forward,
+                    per_distill_workspace_bytes, per_embed_backward, per_embed_forward,
+                    per_embed_workspace_bytes, per_norm_backward, per_norm_forward,
+                    per_norm_workspace_bytes, per_rows_read, per_rows_write, per_rows_write_at,
                     per_scan_backward, per_scan_forward, per_scan_step, per_scan_workspace_bytes,
                     rows_alloc)
 
@@ -26,4 +29,7 @@ __all__ = ["PerBuffer", "PerError", "load", "per_add", "per_capacity", "per_crea
            "per_distill", "per_distill_backward", "per_distill_forward",
            "per_distill_workspace_bytes", "per_rows_read", "per_rows_write", "per_rows_write_at",
            "per_scan_backward", "per_scan_forward", "per_scan_step", "per_scan_workspace_bytes",
-           "rows_alloc"]
+           "rows_alloc",
+           "per_delta_backward", "per_delta_forward", "per_delta_step", "per_delta_workspace_bytes",
+           "per_embed_backward", "per_embed_forward", "per_embed_workspace_bytes",
+           "per_norm_backward", "per_norm_forward", "per_norm_workspace_bytes"]

@@ -1,7 +1,7 @@
 """Compile the HIP library (libper.so), the latency probe (libper_probe.so)
 and the library's phase-stamped measurement build (libper_stamps.so) for
 gfx950, in-tree, with hipcc, and the Python binding of include/per_train.h
-(_marshal.so) with the host compiler."""
+and include/per_block.h (_marshal.so) with the host compiler."""
 from __future__ import annotations
 
 import os
@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libper.so")
 SOURCES = ["per_api.hip", "tree_kernels.hip", "sample_kernels.hip", "rank_kernels.hip",
-           "train_api.hip", "rows_kernels.hip", "scan_kernels.hip", "distill_kernels.hip"]
+           "train_api.hip", "rows_kernels.hip", "scan_kernels.hip", "distill_kernels.hip",
+           "block_api.hip", "embed_kernels.hip", "norm_kernels.hip", "delta_kernels.hip"]
 PROBE_SRC = os.path.join(HERE, "probe", "latency_probe.hip")
 PROBE_LIB = os.path.join(HERE, "libper_probe.so")
 STAMPS_LIB = os.path.join(HERE, "libper_stamps.so")

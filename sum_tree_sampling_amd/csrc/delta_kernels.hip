@@ -1,0 +1,1299 @@
+// delta_kernels.hip -- the gated delta rule: forward, backward and one step.
+//
+// A chunk of 64 steps at a time.  With D_ij the product of the gates of steps j + 1 to i
+// (0 across a reset), gamma_i that of the steps up to i, d_j that of the steps behind j,
+// and A_ij = w_i D_ij k_i.k_j below the diagonal, what the state takes up is
+//     U = (I + A)^-1 w (V - gamma K S),
+// the outputs are scale (gamma Q S + (Q K^T . D) U), and the state goes on as
+// gamma_63 S + (d K)^T U.  Backward, with P = scale (Q K^T . D) and dS the gradient of
+// the state behind the chunk,
+//     E = (I + A)^-T (P^T dO + d K dS),   G = w E = dV,
+//     dS' = gamma_63 dS + scale (gamma Q)^T dO - (gamma K)^T G,
+//     dQ = scale gamma dO S^T + (scale dO U^T . D) K,
+//     dK = d U dS^T + (scale dO U^T . D)^T Q - gamma G S^T - (M + M^T) K,  M = G U^T . D,
+//     the gradient by the logit of w is (1 - w) E.U, and that by log f_i the sum of
+//     q_j.dq_j - v_j.dv_j over the steps j >= i of the chunk and dS.S behind it
+// (all by rows; D is scale-free, a reset ends each sum).
+//
+// What does not depend on the state ((I + A)^-1, Q K^T . D, the decays) is prepared for
+// all chunks at once; one pass then walks over the chunks of a sequence with a slice of
+// the state's columns in each wave's registers (the columns are independent), forward
+// in time, or backward for dS; and the rest of the backward pass takes all chunks at
+// once again.
+//
+// Products run on the bf16 matrix units, f32 factors as sums of three bf16 values (24
+// bits; products below 2^-24 of the largest are left out), 16-bit inputs as one or two:
+// 16 times the f32 units' rate, for 3 to 6 products.  Where only an output in 16 bits
+// depends on it, two values (16 bits) do.
+//
+// The layout of a 16 x 16 result (lane 16 g + n has rows 4 g .. 4 g + 3 of column n) is
+// that of half an operand of the next product, if the 32 terms of a sum are taken in the
+// order rows 4 g + e of the first 16, then of the second: results feed products without
+// a move.  Operands are kept in that order as blocks of 16 bytes for each lane.
+#include <algorithm>
+
+#include "block_internal.h"
+#include "elem.h"
+#include "lanes.h"
+
+namespace per {
+namespace {
+
+constexpr int kC = PER_DELTA_CHUNK;
+typedef bf16_t bf8 __attribute__((ext_vector_type(8)));
+typedef bf16_t bf4 __attribute__((ext_vector_type(4)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Tag {
+  using type = T;
+};
+
+// bf16 values that hold one of the type, and the weakest products that are taken of
+// those behind an output of it: parts i and j where i + j <= kWeak.
+template <typename T>
+constexpr int kParts = 3;
+template <>
+constexpr int kParts<bf16_t> = 1;
+template <>
+constexpr int kParts<f16_t> = 2;
+template <typename T>
+constexpr int kOutParts = sizeof(T) == 4 ? 3 : 2;
+template <typename T>
+constexpr int kWeak = kOutParts<T> - 1;
+
+// 8 values as N bf16 parts, each the rounding of what the ones before leave.
+template <int N>
+__device__ __forceinline__ void split(const f4& lo, const f4& hi, bf8 (&p)[N]) {
+  typedef float f8 __attribute__((ext_vector_type(8)));
+  f8 x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    p[i] = __builtin_convertvector(x, bf8);
+    if (i + 1 < N) x = x - __builtin_convertvector(p[i], f8);
+  }
+}
+template <int N>
+__device__ __forceinline__ void split4(f4 x, bf4 (&p)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    p[i] = __builtin_convertvector(x, bf4);
+    if (i + 1 < N) x = x - __builtin_convertvector(p[i], f4);
+  }
+}
+
+// c + a b over 32 terms, from the parts of a and b, the weakest products first.
+template <int WEAK, int NA, int NB>
+__device__ __forceinline__ f4 mul(const bf8 (&a)[NA], const bf8 (&b)[NB], f4 c) {
+#pragma unroll
+  for (int s = WEAK; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[s - i], c, 0, 0, 0);
+  return c;
+}
+
+// Operand blocks in LDS or memory: block n of N parts, 64 lanes of 16 bytes each.
+template <int N>
+__device__ __forceinline__ void load_block(const char* blocks, int n, bf8 (&p)[N],
+                                           int lane = threadIdx.x & 63) {
+  const char* at = blocks + n * N * 1024 + lane * 16;
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[i] = *reinterpret_cast<const bf8*>(at + i * 1024);
+}
+// Half of a block from a 16 x 16 result: its rows are the terms of the sum.
+template <int N>
+__device__ __forceinline__ void store_half(char* blocks, int n, int half, const f4& v,
+                                           int lane = threadIdx.x & 63) {
+  bf4 p[N];
+  split4<N>(v, p);
+  char* at = blocks + n * N * 1024 + lane * 16 + half * 8;
+#pragma unroll
+  for (int i = 0; i < N; ++i) *reinterpret_cast<bf4*>(at + i * 1024) = p[i];
+}
+
+// 6 of the 8 blocks of 16 rows x 32 terms of a triangular 64 x 64 matrix: rows 16 it of
+// a lower one meet terms 32 kt with kt <= it / 2, those of an upper one kt >= it / 2.
+__device__ __forceinline__ constexpr int lower_block(int it, int kt) {
+  return it < 2 ? it : 2 * (it - 1) + kt;
+}
+__device__ __forceinline__ constexpr int upper_block(int it, int kt) {
+  return it < 2 ? 2 * it + kt : it + 2;
+}
+
+// A thread's 4 x 8 piece of a [64 x 32 KT] matrix: rows 4 a + r, columns 8 m + c.  As
+// rows: blocks it * KT + kt, the columns being the terms.  As columns: blocks dt * 2 +
+// jt, the rows being the terms.
+template <int N, int KT>
+__device__ __forceinline__ void store_piece(const float (&v)[4][8], int a, int m, char* rows,
+                                            char* cols) {
+  if (rows) {
+    const int half = m % 4 / 2, g = m % 2 * 2;
+    char* at = rows + (a / 4 * KT + m / 4) * N * 1024 + half * 8;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = a % 4 * 4 + r;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const f4 x = {v[r][4 * k], v[r][4 * k + 1], v[r][4 * k + 2], v[r][4 * k + 3]};
+        bf4 p[N];
+        split4<N>(x, p);
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          *reinterpret_cast<bf4*>(at + q * 1024 + (16 * (g + k) + i) * 16) = p[q];
+      }
+    }
+  }
+  if (cols) {
+    char* at = cols + (m / 2 * 2 + a / 8) * N * 1024 + a % 8 / 4 * 8;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const f4 x = {v[0][c], v[1][c], v[2][c], v[3][c]};
+      bf4 p[N];
+      split4<N>(x, p);
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+        *reinterpret_cast<bf4*>(at + q * 1024 + (16 * (a % 4) + m % 2 * 8 + c) * 16) = p[q];
+    }
+  }
+}
+// The piece's values, 0 from row `rows` and from column `width` on.
+template <typename T>
+__device__ __forceinline__ void load_piece(const T* base, int64_t stride, int rows, int width,
+                                           int a, int m, float (&v)[4][8]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const T* at = base + (4 * a + r) * stride + 8 * m;
+    if (4 * a + r < rows && 8 * m + 8 <= width) {
+      unpack<T, 8>(load_pack<T, 8>(at), v[r]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        v[r][c] = 4 * a + r < rows && 8 * m + c < width ? (float)at[c] : 0.0f;
+    }
+  }
+}
+// A chunk's rows as operand blocks, by all of a workgroup's threads.
+template <typename T, int KT>
+__device__ __forceinline__ void stage(const T* base, int64_t stride, int rows, int width, char* as_rows,
+                                      char* as_cols) {
+  for (int id = threadIdx.x; id < 64 * KT; id += blockDim.x) {
+    float v[4][8];
+    load_piece<T>(base, stride, rows, width, id / (4 * KT), id % (4 * KT), v);
+    store_piece<kParts<T>, KT>(v, id / (4 * KT), id % (4 * KT), as_rows, as_cols);
+  }
+}
+
+// What is prepared for each (sequence, chunk, head): the decays and writing strengths,
+// then operand blocks: (I + A)^-1 and Q K^T . D (forward), or the transposes of both.
+struct Decays {
+  double log[kC];   // of the gates up to a step
+  float first[kC];  // gamma; -1 behind a reset
+  float last[kC];   // d
+  float w[kC];
+  int resets[kC];   // up to a step
+};
+constexpr int kInvParts = 3;
+template <typename T>
+constexpr int kScoreParts(bool backward) {
+  return backward ? 3 : kOutParts<T>;
+}
+constexpr size_t prep_bytes(int score_parts) {
+  return sizeof(Decays) + (size_t)6 * (kInvParts + score_parts) * 1024;
+}
+size_t prep_bytes_of(int type, bool backward) {
+  return prep_bytes(backward || type == PER_F32 ? 3 : 2);
+}
+
+__device__ __forceinline__ int steps_of(const DeltaArgs& a, int64_t b) {
+  return (int)(a.length ? min(max(a.length[b], (int64_t)0), a.T) : a.T);
+}
+template <typename T>
+__device__ __forceinline__ const T* at(const Seq& s, int64_t b, int64_t t, int64_t h) {
+  return static_cast<const T*>(s.p) + b * s.sb + t * s.st + h * s.sh;
+}
+
+__device__ __forceinline__ float decay(const Decays& d, int i, int j) {
+  return d.resets[i] == d.resets[j] ? expf((float)(d.log[i] - d.log[j])) : 0.0f;
+}
+
+// One workgroup of 4 waves for each (sequence, chunk, head).
+template <typename T, int KT, bool BACKWARD>
+__global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
+  constexpr int N = kParts<T>, NS = kScoreParts<T>(BACKWARD), kPad = 68;
+  __shared__ __attribute__((aligned(16))) char ks[4 * KT * N * 1024];
+  __shared__ __attribute__((aligned(16))) char qs[4 * KT * N * 1024];
+  __shared__ __attribute__((aligned(16))) float lower[kC][kPad];
+  __shared__ __attribute__((aligned(16))) float inv[kC][kPad];
+  __shared__ Decays dec;
+  const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int h = (int)(blockIdx.x % a.H);
+  const int64_t c = blockIdx.x / a.H % a.chunks, b = blockIdx.x / a.H / a.chunks;
+  const int64_t t0 = c * kC;
+  const int rows = min(kC, steps_of(a, b) - (int)t0);
+  if (rows <= 0) return;
+  char* out = static_cast<char*>(a.prep) + (int64_t)blockIdx.x * prep_bytes(NS);
+  const int hk = h / (a.H / a.HK);
+  stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, ks, nullptr);
+  stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, qs, nullptr);
+  if (wave == 3) {
+    const bool on = lane < rows;
+    const float gate = on ? (float)*at<T>(a.g, b, t0 + lane, h) : 0.0f;
+    const float wt = on ? (float)*at<T>(a.b, b, t0 + lane, h) : 0.0f;
+    const bool reset = on && a.reset && a.reset[b * a.T + t0 + lane];
+    // log f; a gate below 2^-200 is 0 in f32 whatever it is
+    const float lf = fminf(gate, 0.0f) - log1pf(expf(-fabsf(gate)));
+    double log = on && !reset ? (double)(lf < -200.0f ? -200.0f : lf) : 0.0;
+    int resets = reset;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const double l = __shfl_up(log, d);
+      const int r = __shfl_up(resets, d);
+      log += lane >= d ? l : 0.0;
+      resets += lane >= d ? r : 0;
+    }
+    const double end = __shfl(log, 63);
+    const int all = __shfl(resets, 63);
+    dec.log[lane] = log;
+    dec.resets[lane] = resets;
+    dec.first[lane] = resets == 0 ? expf((float)log) : -1.0f;
+    dec.last[lane] = resets == all ? expf((float)(end - log)) : 0.0f;
+    dec.w[lane] = on ? 1.0f / (1.0f + expf(-wt)) : 0.0f;
+  }
+  for (int i = threadIdx.x; i < kC * kPad; i += 256) (&inv[0][0])[i] = 0.0f;
+  __syncthreads();
+  for (int i = threadIdx.x; i < (int)sizeof(Decays) / 16; i += 256)
+    reinterpret_cast<f4*>(out)[i] = reinterpret_cast<const f4*>(&dec)[i];
+
+  // 12 pairs of 16 rows and 16 columns, 10 of them on or below the diagonal: A for the
+  // inverse, and scores as halves of blocks, zeros above the diagonal
+  char* scores = out + sizeof(Decays) + 6 * kInvParts * 1024;
+  for (int id = wave; id < 12; id += 4) {
+    const int it = id < 4 ? id / 2 : 2 + (id - 4) / 4, jt = id < 4 ? id % 2 : (id - 4) % 4;
+    f4 kk = {}, qk = {};
+    if (jt <= it) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        bf8 ki[N], kj[N], qi[N];
+        load_block<N>(ks, it * KT + kt, ki);
+        load_block<N>(ks, jt * KT + kt, kj);
+        load_block<N>(qs, it * KT + kt, qi);
+        kk = mul<2>(ki, kj, kk);  // rows of it, columns of jt
+        qk = BACKWARD ? mul<2>(qi, kj, qk) : mul<2>(kj, qi, qk);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * it + 4 * g + r, j = 16 * jt + n;
+        lower[i][j] = j < i ? dec.w[i] * decay(dec, i, j) * kk[r] : 0.0f;
+        const int si = BACKWARD ? i : 16 * it + n, sj = BACKWARD ? j : 16 * jt + 4 * g + r;
+        qk[r] = sj <= si ? decay(dec, si, sj) * qk[r] : 0.0f;
+      }
+    }
+    if (BACKWARD) {  // rows of it are the terms of a row of jt
+      if (it / 2 >= jt / 2 && jt < 4) store_half<NS>(scores, upper_block(jt, it / 2), it % 2, qk);
+    } else {
+      store_half<NS>(scores, lower_block(it, jt / 2), jt % 2, qk);
+    }
+  }
+  __syncthreads();
+
+  // (I + A)^-1: the blocks of 16 on the diagonal by substitution, a column to a lane
+  if (lane < 16) {
+    const int o = 16 * wave;
+    float x[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float s = r == lane ? 1.0f : 0.0f;
+#pragma unroll
+      for (int k = 0; k < r; ++k) s -= lower[o + r][o + k] * x[k];
+      x[r] = s;
+      inv[o + r][o + lane] = s;
+    }
+  }
+  __syncthreads();
+  // and below it X_ij = -X_ii sum_k A_ik X_kj, a column of blocks to a wave
+  {
+    const int j = wave;
+    f4 x[3];
+#pragma unroll
+    for (int step = 0; step < 3; ++step) {
+      const int i = j + 1 + step;
+      if (i < 4) {
+        f4 z = {};
+#pragma unroll
+        for (int s = 0; s <= step; ++s) {
+          const int k = j + s;
+          const f4 p = *reinterpret_cast<const f4*>(&lower[16 * i + n][16 * k + 4 * g]);
+          f4 q;
+          if (s == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) q[r] = inv[16 * j + 4 * g + r][16 * j + n];
+          } else {
+            q = x[s - 1];
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            z = __builtin_amdgcn_mfma_f32_16x16x4f32(p[r], q[r], z, 0, 0, 0);
+        }
+        const f4 p = *reinterpret_cast<const f4*>(&inv[16 * i + n][16 * i + 4 * g]);
+        f4 y = {};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          y = __builtin_amdgcn_mfma_f32_16x16x4f32(p[r], z[r], y, 0, 0, 0);
+        x[step] = -y;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) inv[16 * i + 4 * g + r][16 * j + n] = -y[r];
+      }
+    }
+  }
+  __syncthreads();
+  char* blocks = out + sizeof(Decays);
+  for (int id = wave; id < 6; id += 4) {
+    f4 lo, hi;
+    if (BACKWARD) {
+      const int jt = id < 4 ? id / 2 : id - 2, kt = id < 4 ? id % 2 : 1;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        lo[r] = inv[32 * kt + 4 * g + r][16 * jt + n];
+        hi[r] = inv[32 * kt + 16 + 4 * g + r][16 * jt + n];
+      }
+    } else {
+      const int it = id < 2 ? id : id / 2 + 1, kt = id < 2 ? 0 : id % 2;
+      lo = *reinterpret_cast<const f4*>(&inv[16 * it + n][32 * kt + 4 * g]);
+      hi = *reinterpret_cast<const f4*>(&inv[16 * it + n][32 * kt + 16 + 4 * g]);
+    }
+    bf8 p[kInvParts];
+    split<kInvParts>(lo, hi, p);
+#pragma unroll
+    for (int q = 0; q < kInvParts; ++q)
+      *reinterpret_cast<bf8*>(blocks + (id * kInvParts + q) * 1024 + lane * 16) = p[q];
+  }
+}
+
+// Copies whole 16 bytes from memory to LDS by a workgroup.
+__device__ __forceinline__ void copy16(char* to, const char* from, int bytes) {
+  for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
+    *reinterpret_cast<f4*>(to + i) = *reinterpret_cast<const f4*>(from + i);
+}
+
+// NT neighbouring values of a row, 0 past `width`.
+template <typename T, int NT>
+__device__ __forceinline__ void load_few(const T* row, int col, int width, float (&v)[NT]) {
+  if (col + NT <= width) {
+    unpack<T, NT>(load_pack<T, NT>(row + col), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) v[i] = col + i < width ? (float)row[col + i] : 0.0f;
+  }
+}
+template <typename T, int NT>
+__device__ __forceinline__ void store_few(T* row, int col, int width, const float (&v)[NT]) {
+  if (col + NT <= width) {
+    store_vals<T, NT>(row + col, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      if (col + i < width) row[col + i] = (T)v[i];
+  }
+}
+// A wave's columns of a state [DK x DV], rows 16 dt + 4 g + r.
+template <int KT, int NT>
+__device__ __forceinline__ void load_state(const float* s, int DK, int DV, int col,
+                                           f4 (&v)[2 * KT][NT]) {
+  const int g = (threadIdx.x & 63) / 16;
+#pragma unroll
+  for (int dt = 0; dt < 2 * KT; ++dt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * dt + 4 * g + r;
+      float x[NT] = {};
+      if (s && row < DK) load_few<float, NT>(s + (int64_t)row * DV, col, DV, x);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) v[dt][nt][r] = x[nt];
+    }
+}
+template <int KT, int NT>
+__device__ __forceinline__ void store_state(float* s, int DK, int DV, int col,
+                                            const f4 (&v)[2 * KT][NT]) {
+  const int g = (threadIdx.x & 63) / 16;
+#pragma unroll
+  for (int dt = 0; dt < 2 * KT; ++dt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * dt + 4 * g + r;
+      float x[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[nt] = v[dt][nt][r];
+      if (row < DK) store_few<float, NT>(s + (int64_t)row * DV, col, DV, x);
+    }
+}
+// The chunk's rows of a wave's columns.
+template <int NT>
+__device__ __forceinline__ void store_rows(float* s, int DV, int col, const f4 (&v)[4][NT]) {
+  const int g = (threadIdx.x & 63) / 16;
+#pragma unroll
+  for (int it = 0; it < 4; ++it)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float x[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[nt] = v[it][nt][r];
+      store_few<float, NT>(s + (int64_t)(16 * it + 4 * g + r) * DV, col, DV, x);
+    }
+}
+
+// A state that is not finite stays on its side of a reset: the rows of the chunk on
+// that side (`with`) give 0 to the other rows' sums, where 0 times them would not be 0.
+// Called where the chunk has a reset.
+template <int NT, typename F>
+__device__ __forceinline__ void keep_apart(f4 (&x)[4][NT], F with) {
+  const int g = (threadIdx.x & 63) / 16;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float bad = 0.0f;
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (with(16 * it + 4 * g + r) && !__builtin_isfinite(x[it][nt][r])) bad = 1.0f;
+    bad = fmaxf(bad, xor_lanes(bad, 4));
+    bad = fmaxf(bad, xor_lanes(bad, 5));
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (bad != 0.0f && with(16 * it + 4 * g + r)) x[it][nt][r] = 0.0f;
+  }
+}
+
+constexpr int64_t carry_size(int DK, int DV) { return (int64_t)(DK + kC) * DV; }
+
+// A workgroup has a head of a sequence and 4 * 16 NT columns of its state, 16 NT to a
+// wave: lane 16 g + n the columns NT n .. NT n + NT - 1 of them.
+template <typename T, int KT, int NT>
+__global__ __launch_bounds__(256) void delta_forward_kernel(DeltaArgs a, int slices) {
+  constexpr int N = kParts<T>, NO = kOutParts<T>, WEAK = kWeak<T>;
+  constexpr int kTile = 4 * KT * N * 1024;
+  constexpr bool kApart = N == 1;  // queries have a place of their own in LDS
+  __shared__ __attribute__((aligned(16))) char krows[kTile], kcols[kTile];
+  __shared__ __attribute__((aligned(16))) char qrows_[kApart ? kTile : 16];
+  __shared__ __attribute__((aligned(16))) char prep[prep_bytes(NO)];
+  char* qrows = kApart ? qrows_ : krows;
+  const Decays& dec = *reinterpret_cast<const Decays*>(prep);
+  const char* invs = prep + sizeof(Decays);
+  const char* scores = invs + 6 * kInvParts * 1024;
+
+  const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int slice = (int)(blockIdx.x % slices);
+  const int64_t bh = blockIdx.x / slices, b = bh / a.H;
+  const int h = (int)(bh % a.H), hk = h / (a.H / a.HK);
+  const int col = ((slice * 4 + wave) * 16 + n) * NT;
+  const int steps = steps_of(a, b);
+
+  f4 s[2 * KT][NT];
+  load_state<KT, NT>(a.s0 ? a.s0 + bh * a.DK * a.DV : nullptr, a.DK, a.DV, col, s);
+  for (int t0 = 0; t0 < steps; t0 += kC) {
+    const int rows = min(kC, steps - t0);
+    const int64_t unit = (b * a.chunks + t0 / kC) * a.H + h;
+    __syncthreads();
+    stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, krows, kcols);
+    if (kApart) stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, qrows, nullptr);
+    copy16(prep, static_cast<const char*>(a.prep) + unit * prep_bytes(NO), prep_bytes(NO));
+    float v[4][4][NT];
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * it + 4 * g + r;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) v[it][r][nt] = 0.0f;
+        if (i < rows) load_few<T, NT>(at<T>(a.v, b, t0 + i, h), col, a.DV, v[it][r]);
+      }
+    float* carry = a.carries ? a.carries + unit * carry_size(a.DK, a.DV) : nullptr;
+    if (carry) store_state<KT, NT>(carry, a.DK, a.DV, col, s);
+    __syncthreads();
+
+    // K S and Q S
+    f4 x[4][NT] = {}, y[4][NT] = {};
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      bf8 sp[NT][3];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) split<3>(s[2 * kt][nt], s[2 * kt + 1][nt], sp[nt]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        bf8 p[N];
+        load_block<N>(krows, it * KT + kt, p);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) x[it][nt] = mul<2>(p, sp[nt], x[it][nt]);
+        if (kApart) {
+          load_block<N>(qrows, it * KT + kt, p);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) y[it][nt] = mul<WEAK>(p, sp[nt], y[it][nt]);
+        }
+      }
+    }
+    if (!kApart) {
+      __syncthreads();
+      stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, qrows, nullptr);
+      __syncthreads();
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        bf8 sp[NT][NO];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) split<NO>(s[2 * kt][nt], s[2 * kt + 1][nt], sp[nt]);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          bf8 p[N];
+          load_block<N>(qrows, it * KT + kt, p);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) y[it][nt] = mul<WEAK>(p, sp[nt], y[it][nt]);
+        }
+      }
+    }
+    // w (V - gamma K S)
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * it + 4 * g + r;
+        const float first = dec.first[i], w = dec.w[i];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float past = first < 0.0f ? 0.0f : first * x[it][nt][r];
+          x[it][nt][r] = w * (v[it][r][nt] - past);
+          y[it][nt][r] = first < 0.0f ? 0.0f : first * y[it][nt][r];
+        }
+      }
+    if (dec.resets[kC - 1] > 0)
+      keep_apart<NT>(x, [&](int i) { return dec.first[i] >= 0.0f; });
+    // U
+    f4 u[4][NT] = {};
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      bf8 xp[NT][3];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) split<3>(x[2 * kt][nt], x[2 * kt + 1][nt], xp[nt]);
+#pragma unroll
+      for (int it = 2 * kt; it < 4; ++it) {
+        bf8 p[kInvParts];
+        load_block<kInvParts>(invs, lower_block(it, kt), p);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) u[it][nt] = mul<2>(p, xp[nt], u[it][nt]);
+      }
+    }
+    if (carry) store_rows<NT>(carry + (int64_t)a.DK * a.DV, a.DV, col, u);
+    // the outputs
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      bf8 up[NT][NO];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) split<NO>(u[2 * kt][nt], u[2 * kt + 1][nt], up[nt]);
+#pragma unroll
+      for (int it = 2 * kt; it < 4; ++it) {
+        bf8 p[NO];
+        load_block<NO>(scores, lower_block(it, kt), p);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) y[it][nt] = mul<WEAK>(p, up[nt], y[it][nt]);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * it + 4 * g + r;
+        float o[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          o[nt] = a.scale * y[it][nt][r];
+          u[it][nt][r] *= dec.last[i];
+        }
+        if (i < rows) store_few<T, NT>(const_cast<T*>(at<T>(a.o, b, t0 + i, h)), col, a.DV, o);
+      }
+    // the state behind the chunk
+    const float kept = dec.first[kC - 1];
+#pragma unroll
+    for (int dt = 0; dt < 2 * KT; ++dt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[dt][nt][r] = kept < 0.0f ? 0.0f : kept * s[dt][nt][r];
+#pragma unroll
+    for (int jt = 0; jt < 2; ++jt) {
+      bf8 up[NT][3];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) split<3>(u[2 * jt][nt], u[2 * jt + 1][nt], up[nt]);
+#pragma unroll
+      for (int dt = 0; dt < 2 * KT; ++dt) {
+        bf8 p[N];
+        load_block<N>(kcols, dt * 2 + jt, p);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[dt][nt] = mul<2>(p, up[nt], s[dt][nt]);
+      }
+    }
+  }
+  if (a.s_last) store_state<KT, NT>(a.s_last + bh * a.DK * a.DV, a.DK, a.DV, col, s);
+  const float zero[NT] = {};
+  for (int64_t t = steps + wave * 0 + g; t < a.T; t += 4)
+    store_few<T, NT>(const_cast<T*>(at<T>(a.o, b, t, h)), col, a.DV, zero);
+}
+
+// Backward in time: dS behind each chunk, E, and dV.
+template <typename T, int KT, int NT>
+__global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int slices) {
+  constexpr int N = kParts<T>;
+  constexpr int kTile = 4 * KT * N * 1024;
+  __shared__ __attribute__((aligned(16))) char krows[kTile], kcols[kTile];
+  __shared__ __attribute__((aligned(16))) char prep[prep_bytes(3)];
+  char* qcols = krows;
+  const Decays& dec = *reinterpret_cast<const Decays*>(prep);
+  const char* invs = prep + sizeof(Decays);
+  const char* scores = invs + 6 * kInvParts * 1024;
+
+  const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int slice = (int)(blockIdx.x % slices);
+  const int64_t bh = blockIdx.x / slices, b = bh / a.H;
+  const int h = (int)(bh % a.H), hk = h / (a.H / a.HK);
+  const int col = ((slice * 4 + wave) * 16 + n) * NT;
+  const int steps = steps_of(a, b);
+
+  f4 s[2 * KT][NT];
+  load_state<KT, NT>(a.s0 ? a.s0 + bh * a.DK * a.DV : nullptr, a.DK, a.DV, col, s);
+  for (int t0 = (steps - 1) / kC * kC; steps > 0 && t0 >= 0; t0 -= kC) {
+    const int rows = min(kC, steps - t0);
+    const int64_t unit = (b * a.chunks + t0 / kC) * a.H + h;
+    __syncthreads();
+    stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, krows, kcols);
+    copy16(prep, static_cast<const char*>(a.prep) + unit * prep_bytes(3), prep_bytes(3));
+    float d[4][4][NT];  // dO
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * it + 4 * g + r;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) d[it][r][nt] = 0.0f;
+        if (i < rows) load_few<T, NT>(at<T>(a.o, b, t0 + i, h), col, a.DV, d[it][r]);
+      }
+    store_state<KT, NT>(a.dstate + unit * a.DK * a.DV, a.DK, a.DV, col, s);
+    __syncthreads();
+
+    // d K dS + scale P^T dO
+    f4 x[4][NT] = {}, y[4][NT] = {};
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      bf8 sp[NT][3];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) split<3>(s[2 * kt][nt], s[2 * kt + 1][nt], sp[nt]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        bf8 p[N];
+        load_block<N>(krows, it * KT + kt, p);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) x[it][nt] = mul<2>(p, sp[nt], x[it][nt]);
+      }
+    }
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      bf8 dp[NT][N];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f4 lo, hi;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) lo[r] = d[2 * kt][r][nt], hi[r] = d[2 * kt + 1][r][nt];
+        split<N>(lo, hi, dp[nt]);
+      }
+#pragma unroll
+      for (int jt = 0; jt < 2 * kt + 2; ++jt) {
+        bf8 p[3];
+        load_block<3>(scores, upper_block(jt, kt), p);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) y[jt][nt] = mul<2>(p, dp[nt], y[jt][nt]);
+      }
+    }
+    __syncthreads();  // the keys' rows make room for the queries
+    stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, nullptr, qcols);
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float last = dec.last[16 * it + 4 * g + r];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          x[it][nt][r] = (last != 0.0f ? last * x[it][nt][r] : 0.0f) + a.scale * y[it][nt][r];
+      }
+    if (dec.resets[kC - 1] > 0)
+      keep_apart<NT>(x, [&](int i) { return dec.resets[i] == dec.resets[kC - 1]; });
+    // E
+    f4 e[4][NT] = {};
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      bf8 xp[NT][3];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) split<3>(x[2 * kt][nt], x[2 * kt + 1][nt], xp[nt]);
+#pragma unroll
+      for (int jt = 0; jt < 2 * kt + 2; ++jt) {
+        bf8 p[kInvParts];
+        load_block<kInvParts>(invs, upper_block(jt, kt), p);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) e[jt][nt] = mul<2>(p, xp[nt], e[jt][nt]);
+      }
+    }
+    store_rows<NT>(a.e + unit * kC * a.DV, a.DV, col, e);
+    // dV, then what goes back to the state before the chunk
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * it + 4 * g + r;
+        const float first = dec.first[i], w = dec.w[i];
+        float o[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          o[nt] = w * e[it][nt][r];
+          e[it][nt][r] = first < 0.0f ? 0.0f : -first * o[nt];
+          d[it][r][nt] = first < 0.0f ? 0.0f : a.scale * first * d[it][r][nt];
+        }
+        if (i < rows) store_few<T, NT>(const_cast<T*>(at<T>(a.dv, b, t0 + i, h)), col, a.DV, o);
+      }
+    __syncthreads();
+    const float kept = dec.first[kC - 1];
+#pragma unroll
+    for (int dt = 0; dt < 2 * KT; ++dt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[dt][nt][r] = kept < 0.0f ? 0.0f : kept * s[dt][nt][r];
+#pragma unroll
+    for (int jt = 0; jt < 2; ++jt) {
+      bf8 ep[NT][3], dp[NT][3];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        split<3>(e[2 * jt][nt], e[2 * jt + 1][nt], ep[nt]);
+        f4 lo, hi;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) lo[r] = d[2 * jt][r][nt], hi[r] = d[2 * jt + 1][r][nt];
+        split<3>(lo, hi, dp[nt]);
+      }
+#pragma unroll
+      for (int dt = 0; dt < 2 * KT; ++dt) {
+        bf8 p[N];
+        load_block<N>(kcols, dt * 2 + jt, p);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[dt][nt] = mul<2>(p, ep[nt], s[dt][nt]);
+        load_block<N>(qcols, dt * 2 + jt, p);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[dt][nt] = mul<2>(p, dp[nt], s[dt][nt]);
+      }
+    }
+  }
+  if (a.s_last) store_state<KT, NT>(a.s_last + bh * a.DK * a.DV, a.DK, a.DV, col, s);
+  const float zero[NT] = {};
+  for (int64_t t = steps + g; t < a.T; t += 4)
+    store_few<T, NT>(const_cast<T*>(at<T>(a.dv, b, t, h)), col, a.DV, zero);
+}
+
+// dQ, dK and the gradients of gates and strengths, for each (sequence, chunk, head of
+// keys): 8 waves.  What sums over the state's columns takes 64 of them at a time; a wave
+// has 16 columns of dQ and dK (dt) and NI of the chunk's 4 groups of rows.
+template <typename T, int KT>
+__global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
+  constexpr int N = kParts<T>, NO = kOutParts<T>, WEAK = kWeak<T>;
+  constexpr int kDt = 2 * KT, NI = kDt / 2;
+  constexpr int kTile = 4 * KT * N * 1024;
+  constexpr int kStage = (8 * N + 16 * NO) * 1024, kPairs = 20 * NO * 1024;
+  constexpr bool kApart = N < 3;
+  __shared__ __attribute__((aligned(16))) char space[kStage > kPairs ? kStage : kPairs];
+  __shared__ __attribute__((aligned(16))) char kcols_[kTile], qcols_[kApart ? kTile : 16];
+  __shared__ __attribute__((aligned(16))) Decays dec;
+  __shared__ float eu[kC], gv[kC], qd[kDt][kC], ends[8][2];
+  char *dos = space, *us = dos + 8 * N * 1024, *gs = us + 8 * NO * 1024;
+  char *da = space, *dt_ = da + 6 * NO * 1024, *mm = dt_ + 6 * NO * 1024;
+  char *kcols = kcols_, *qcols = kApart ? qcols_ : kcols_;
+
+  const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int hk = (int)(blockIdx.x % a.HK), shared = a.H / a.HK;
+  const int64_t c = blockIdx.x / a.HK % a.chunks, b = blockIdx.x / a.HK / a.chunks;
+  const int64_t t0 = c * kC;
+  const int steps = steps_of(a, b), rows = min(kC, steps - (int)t0);
+  const int here = (int)min((int64_t)kC, a.T - t0);  // rows that are written
+  const int dt = wave % kDt, i0 = wave / kDt * NI;
+  const int dcol = 16 * dt + n;
+  f4 dq[NI] = {}, dk[NI] = {};
+
+  if (rows > 0) {
+    for (int gi = 0; gi < shared; ++gi) {
+      // else every place in LDS is computed before this loop, and registers run out
+      int lane = threadIdx.x & 63;
+      asm volatile("" : "+v"(lane));
+      const int g = lane / 16, n = lane % 16, dcol = 16 * dt + n;
+      const int h = hk * shared + gi;
+      const int64_t unit = (b * a.chunks + c) * a.H + h;
+      const float* s0 = a.carries + unit * carry_size(a.DK, a.DV);
+      const float* u = s0 + (int64_t)a.DK * a.DV;
+      const float* ds = a.dstate + unit * a.DK * a.DV;
+      const float* e = a.e + unit * kC * a.DV;
+      f4 qs[NI] = {}, k1[NI] = {}, k2[NI] = {}, pair[5] = {};
+      float ss = 0.0f;
+      __syncthreads();
+      copy16(reinterpret_cast<char*>(&dec), static_cast<const char*>(a.prep) + unit * prep_bytes(3),
+             sizeof(Decays));
+      if (threadIdx.x < kC) eu[threadIdx.x] = gv[threadIdx.x] = 0.0f;
+      if (kApart && gi == 0) {
+        stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, nullptr, kcols);
+        stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, nullptr, qcols);
+      }
+      for (int v0 = 0; v0 < a.DV; v0 += 64) {
+        __syncthreads();
+        const int width = a.DV - v0;
+        {
+          // 128 threads each: U; dO; G and the sums E.U; the sums G.V
+          const int pa = wave % 2 * 8 + lane / 8, pm = lane % 8, job = wave / 2;
+          float x[4][8], y[4][8];
+          if (job == 0) {
+            load_piece<float>(u + v0, a.DV, kC, width, pa, pm, x);
+            store_piece<NO, 2>(x, pa, pm, us, nullptr);
+          } else if (job == 1) {
+            load_piece<T>(at<T>(a.o, b, t0, h) + v0, a.o.st, rows, width, pa, pm, x);
+            store_piece<N, 2>(x, pa, pm, dos, nullptr);
+          } else {
+            load_piece<float>(e + v0, a.DV, kC, width, pa, pm, x);
+            if (job == 2) {
+              load_piece<float>(u + v0, a.DV, kC, width, pa, pm, y);
+            } else {
+              load_piece<T>(at<T>(a.v, b, t0, h) + v0, a.v.st, rows, width, pa, pm, y);
+            }
+            float sum[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float w = dec.w[4 * pa + r];
+              sum[r] = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                sum[r] += x[r][k] * y[r][k];
+                x[r][k] *= w;
+              }
+              if (job == 3) sum[r] *= w;
+#pragma unroll
+              for (int q = 0; q < 3; ++q) sum[r] += xor_lanes(sum[r], q);
+              if (pm == 0) (job == 2 ? eu : gv)[4 * pa + r] += sum[r];
+            }
+            if (job == 2) store_piece<NO, 2>(x, pa, pm, gs, nullptr);
+          }
+        }
+        __syncthreads();
+        // 64 x 64 products: waves 0 to 3 G U^T, twice for the 16 x 16 on the diagonal (once
+        // for each side of it), waves 4 to 7 dO U^T and its transpose
+#pragma unroll 1
+        for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+          for (int p = 0; p < 5; ++p) {
+            __builtin_amdgcn_sched_barrier(0);  // else all loads come first, and registers run out
+            if (wave < 4) {
+              // rows j, columns i: U_j G_i above the diagonal of this result, G_j U_i below
+              const int it = wave, jt = p < 2 ? wave : (wave + p - 1) & 3;
+              const bool up = p < 2 ? p == 0 : jt < it;
+              bf8 x[NO], y[NO];
+              load_block<NO>(up ? us : gs, jt * 2 + kt, x, lane);
+              load_block<NO>(up ? gs : us, it * 2 + kt, y, lane);
+              pair[p] = mul<WEAK>(x, y, pair[p]);
+            } else {
+              const int id = (wave - 4) * 5 + p, k = id % 10;
+              const int it = k < 1 ? 0 : k < 3 ? 1 : k < 6 ? 2 : 3, jt = k - it * (it + 1) / 2;
+              bf8 x[NO], y[N];
+              load_block<NO>(us, jt * 2 + kt, x, lane);
+              load_block<N>(dos, it * 2 + kt, y, lane);
+              pair[p] = id < 10 ? mul<WEAK>(x, y, pair[p]) : mul<WEAK>(y, x, pair[p]);
+            }
+          }
+        }
+        // dO S^T, U dS^T, G S^T
+#pragma unroll 1
+        for (int kt = 0; kt < 2; ++kt) {
+          const int v = v0 + 32 * kt + 4 * g;
+          f4 x[2], y[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float p[4] = {}, q[4] = {};
+            if (dcol < a.DK) {
+              load_few<float, 4>(s0 + (int64_t)dcol * a.DV, v + 16 * k, a.DV, p);
+              load_few<float, 4>(ds + (int64_t)dcol * a.DV, v + 16 * k, a.DV, q);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              x[k][r] = p[r];
+              y[k][r] = q[r];
+              ss += p[r] * q[r];
+            }
+          }
+          bf8 xp[NO], yp[NO];
+          split<NO>(x[0], x[1], xp);
+          split<NO>(y[0], y[1], yp);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            bf8 od[N], ou[NO], og[NO];
+            load_block<N>(dos, (i0 + i) * 2 + kt, od, lane);
+            load_block<NO>(us, (i0 + i) * 2 + kt, ou, lane);
+            load_block<NO>(gs, (i0 + i) * 2 + kt, og, lane);
+            qs[i] = mul<WEAK>(od, xp, qs[i]);
+            k1[i] = mul<WEAK>(ou, yp, k1[i]);
+            k2[i] = mul<WEAK>(og, xp, k2[i]);
+          }
+        }
+      }
+      __syncthreads();
+      // the 64 x 64 matrices with their decays, as operands
+      if (wave < 4) {
+        const int it = wave;
+#pragma unroll
+        for (int p = 0; p < 5; ++p) {
+          if (p == 1) continue;
+          __builtin_amdgcn_sched_barrier(0);
+          const int jt = p < 2 ? wave : (wave + p - 1) & 3;
+          f4 v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 16 * it + n, j = 16 * jt + 4 * g + r;
+            const float x = p == 0 && j > i ? pair[1][r] : pair[p][r];
+            v[r] = i == j ? 0.0f : -x * decay(dec, max(i, j), min(i, j));
+          }
+          store_half<NO>(mm, it * 2 + jt / 2, jt % 2, v, lane);
+        }
+        const f4 zero = {};
+        if (wave == 0) store_half<NO>(da, lower_block(0, 0), 1, zero, lane);
+        if (wave == 1) store_half<NO>(da, lower_block(2, 1), 1, zero, lane);
+        if (wave == 2) store_half<NO>(dt_, upper_block(1, 0), 0, zero, lane);
+        if (wave == 3) store_half<NO>(dt_, upper_block(3, 1), 0, zero, lane);
+      } else {
+#pragma unroll
+        for (int p = 0; p < 5; ++p) {
+          const int id = (wave - 4) * 5 + p, k = id % 10;
+          const int it = k < 1 ? 0 : k < 3 ? 1 : k < 6 ? 2 : 3, jt = k - it * (it + 1) / 2;
+          __builtin_amdgcn_sched_barrier(0);
+          f4 v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 16 * it + (id < 10 ? n : 4 * g + r);
+            const int j = 16 * jt + (id < 10 ? 4 * g + r : n);
+            v[r] = j <= i ? a.scale * pair[p][r] * decay(dec, i, j) : 0.0f;
+          }
+          if (id < 10) {
+            store_half<NO>(da, lower_block(it, jt / 2), jt % 2, v, lane);
+          } else {
+            store_half<NO>(dt_, upper_block(jt, it / 2), it % 2, v, lane);
+          }
+        }
+      }
+      if (!kApart) stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, nullptr, kcols);
+      __syncthreads();
+      float end = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        const int it = i0 + i;
+        bf4 kp[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          kp[q] = *reinterpret_cast<const bf4*>(kcols + ((dt * 2 + it / 2) * N + q) * 1024 +
+                                                lane * 16 + it % 2 * 8);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * it + 4 * g + r;
+          const float first = dec.first[row], last = dec.last[row];
+          float kx = 0.0f;
+#pragma unroll
+          for (int q = N - 1; q >= 0; --q) kx += (float)kp[q][r];
+          qs[i][r] = first >= 0.0f ? qs[i][r] * (a.scale * first) : 0.0f;
+          k1[i][r] = last != 0.0f ? k1[i][r] * last : 0.0f;
+          end += kx * k1[i][r];
+          if (first >= 0.0f) k1[i][r] -= first * k2[i][r];
+        }
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          bf8 y[N], x[NO];
+          load_block<N>(kcols, dt * 2 + kt, y, lane);
+          if (kt <= it / 2) {
+            load_block<NO>(da, lower_block(it, kt), x, lane);
+            qs[i] = mul<WEAK>(x, y, qs[i]);
+          }
+          load_block<NO>(mm, it * 2 + kt, x, lane);
+          k1[i] = mul<WEAK>(x, y, k1[i]);
+        }
+      }
+      if (!kApart) {
+        __syncthreads();
+        stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, nullptr, qcols);
+        __syncthreads();
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        const int it = i0 + i;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          if (kt < it / 2) continue;
+          bf8 y[N], x[NO];
+          load_block<N>(qcols, dt * 2 + kt, y, lane);
+          load_block<NO>(dt_, upper_block(it, kt), x, lane);
+          k1[i] = mul<WEAK>(x, y, k1[i]);
+        }
+        bf4 qp[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          qp[q] = *reinterpret_cast<const bf4*>(qcols + ((dt * 2 + it / 2) * N + q) * 1024 +
+                                                lane * 16 + it % 2 * 8);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float x = 0.0f;
+#pragma unroll
+          for (int q = N - 1; q >= 0; --q) x += (float)qp[q][r];
+          x *= qs[i][r];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x += xor_lanes(x, q);
+          if (n == 0) qd[dt][16 * it + 4 * g + r] = x;
+        }
+        dq[i] += qs[i];
+        dk[i] += k1[i];
+      }
+      // dS . S behind the chunk
+      if (i0 > 0) ss = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 6; ++q) {
+        end += xor_lanes(end, q);
+        ss += xor_lanes(ss, q);
+      }
+      if (lane == 0) {
+        ends[wave][0] = end;
+        ends[wave][1] = ss;
+      }
+      __syncthreads();
+      if (wave == 0) {
+        double z = 0.0, last = 0.0, across = 0.0;
+#pragma unroll
+        for (int k = 0; k < kDt; ++k) z += qd[k][lane];
+        z -= gv[lane];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          last += ends[k][0];
+          across += ends[k][1];
+        }
+        const float kept = dec.first[kC - 1];
+        if (kept >= 0.0f) last += (double)kept * across;
+        if (lane == kC - 1) z += last;
+        const int mine = dec.resets[lane];
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+          const double o = __shfl_down(z, d);
+          const int theirs = __shfl_down(mine, d);
+          if (lane + d < 64 && theirs == mine) z += o;
+        }
+        const int before = __shfl_up(mine, 1);
+        const bool reset = lane == 0 ? mine != 0 : mine != before;
+        if (lane < here) {
+          const bool on = lane < rows;
+          const float gate = on ? (float)*at<T>(a.g, b, t0 + lane, h) : 0.0f;
+          const float wt = on ? (float)*at<T>(a.b, b, t0 + lane, h) : 0.0f;
+          *const_cast<T*>(at<T>(a.dg, b, t0 + lane, h)) =
+              (T)(on && !reset ? (float)z / (1.0f + expf(gate)) : 0.0f);
+          *const_cast<T*>(at<T>(a.db, b, t0 + lane, h)) =
+              (T)(on ? eu[lane] / (1.0f + expf(wt)) : 0.0f);
+        }
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < here * shared; i += 512) {
+      const int64_t t = t0 + i / shared;
+      const int h = hk * shared + i % shared;
+      *const_cast<T*>(at<T>(a.dg, b, t, h)) = (T)0.0f;
+      *const_cast<T*>(at<T>(a.db, b, t, h)) = (T)0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * (i0 + i) + 4 * g + r;
+      if (row < here && dcol < a.DK) {
+        const_cast<T*>(at<T>(a.dq, b, t0 + row, hk))[dcol] = (T)(row < rows ? dq[i][r] : 0.0f);
+        const_cast<T*>(at<T>(a.dk, b, t0 + row, hk))[dcol] = (T)(row < rows ? dk[i][r] : 0.0f);
+      }
+    }
+}
+
+// One step: a workgroup has a head's state, 32 groups of 4 columns by 8 groups of 16
+// rows, so all of it is asked for at once.  The state is read and written once.
+__global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, int type, int slices) {
+  __shared__ float sum[2][8][128];
+  __shared__ float ks[PER_DELTA_MAX_DK], qs[PER_DELTA_MAX_DK];
+  const int slice = (int)(blockIdx.x % slices);
+  const int64_t bh = blockIdx.x / slices, b = bh / a.H;
+  const int h = (int)(bh % a.H), hk = h / (a.H / a.HK);
+  const int part = threadIdx.x / 32, cl = threadIdx.x % 32 * 4, col = slice * 128 + cl;
+  auto value = [&](const Seq& s, int64_t head, int i) {
+    const int64_t off = b * s.sb + head * s.sh + i;
+    return type == PER_F32    ? static_cast<const float*>(s.p)[off]
+           : type == PER_BF16 ? (float)static_cast<const bf16_t*>(s.p)[off]
+                              : (float)static_cast<const f16_t*>(s.p)[off];
+  };
+  const float* s = a.s0 + bh * a.DK * a.DV;
+  float v[16][4];
+  const bool reset = a.reset && a.reset[b];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int row = part * 16 + r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[r][i] = 0.0f;
+    if (row < a.DK && !reset) load_few<float, 4>(s + (int64_t)row * a.DV, col, a.DV, v[r]);
+  }
+  if (threadIdx.x < 128) {
+    ks[threadIdx.x] = (int)threadIdx.x < a.DK ? value(a.k, hk, threadIdx.x) : 0.0f;
+  } else {
+    const int i = threadIdx.x - 128;
+    qs[i] = i < a.DK ? value(a.q, hk, i) : 0.0f;
+  }
+  const float gate = value(a.g, h, 0), wt = value(a.b, h, 0);
+  const float f = 1.0f / (1.0f + expf(-gate)), w = 1.0f / (1.0f + expf(-wt));
+  __syncthreads();
+  float k[4] = {}, q[4] = {};
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const float kr = ks[part * 16 + r];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[r][i] *= f;
+      k[i] += kr * v[r][i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[0][part][cl + i] = k[i];
+  __syncthreads();
+  float u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) x += sum[0][p][cl + i];
+    u[i] = col + i < a.DV ? w * (value(a.v, h, col + i) - x) : 0.0f;
+  }
+  float* to = a.s_last + bh * a.DK * a.DV;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int row = part * 16 + r;
+    const float kr = ks[row], qr = qs[row];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[r][i] += kr * u[i];
+      q[i] += qr * v[r][i];
+    }
+    if (row < a.DK) store_few<float, 4>(to + (int64_t)row * a.DV, col, a.DV, v[r]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[1][part][cl + i] = q[i];
+  __syncthreads();
+  const int c = slice * 128 + threadIdx.x;
+  if (threadIdx.x < 128 && c < a.DV) {
+    float x = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) x += sum[1][p][threadIdx.x];
+    x *= a.scale;
+    const int64_t off = b * a.o.sb + h * a.o.sh + c;
+    if (type == PER_F32) {
+      static_cast<float*>(a.o.p)[off] = x;
+    } else if (type == PER_BF16) {
+      static_cast<bf16_t*>(a.o.p)[off] = (bf16_t)x;
+    } else {
+      static_cast<f16_t*>(a.o.p)[off] = (f16_t)x;
+    }
+  }
+}
+
+template <typename F>
+hipError_t by_type(int type, F f) {
+  switch (type) {
+    case PER_F32: return f(Tag<float>{});
+    case PER_BF16: return f(Tag<bf16_t>{});
+    default: return f(Tag<f16_t>{});
+  }
+}
+template <int K>
+struct Size {
+  static constexpr int value = K;
+};
+template <typename F>
+hipError_t by_keys(int DK, F f) {
+  if (DK <= 32) return f(Size<1>{});
+  if (DK <= 64) return f(Size<2>{});
+  return f(Size<4>{});
+}
+
+hipError_t launch_prepare(const DeltaArgs& a, int type, bool backward, hipStream_t s) {
+  return by_type(type, [&](auto tag) {
+    return by_keys(a.DK, [&](auto keys) {
+      using T = typename decltype(tag)::type;
+      constexpr int KT = decltype(keys)::value;
+      return enqueue(backward ? delta_prepare_kernel<T, KT, true> : delta_prepare_kernel<T, KT, false>,
+                     dim3((uint32_t)(a.B * a.chunks * a.H)), dim3(256), 0, s, a);
+    });
+  });
+}
+
+}  // namespace
+
+size_t delta_workspace(int64_t B, int64_t T, int64_t H, int64_t DK, int64_t DV, int type,
+                       bool backward, DeltaArgs* a, void* ws) {
+  const int64_t units = B * ((T + kC - 1) / kC) * H;
+  const size_t prep = (size_t)units * prep_bytes_of(type, backward);
+  const size_t state = backward ? ((size_t)(units * DK * DV) * 4 + 15) / 16 * 16 : 0;
+  const size_t rows = backward ? (size_t)(units * kC * DV) * 4 : 0;
+  if (a) {
+    char* p = static_cast<char*>(ws);
+    a->prep = p;
+    a->dstate = reinterpret_cast<float*>(p + prep);
+    a->e = reinterpret_cast<float*>(p + prep + state);
+  }
+  return prep + state + rows;
+}
+
+hipError_t launch_delta_forward(const DeltaArgs& a, int type, hipStream_t s) {
+  hipError_t e = a.chunks > 0 ? launch_prepare(a, type, false, s) : hipSuccess;
+  if (e != hipSuccess) return e;
+  return by_type(type, [&](auto tag) {
+    return by_keys(a.DK, [&](auto keys) {
+      using T = typename decltype(tag)::type;
+      constexpr int KT = decltype(keys)::value;
+      const int slices = (a.DV + 63) / 64;
+      return enqueue(delta_forward_kernel<T, KT, 1>, dim3((uint32_t)(a.B * a.H * slices)), dim3(256),
+                     0, s, a, slices);
+    });
+  });
+}
+
+hipError_t launch_delta_backward(const DeltaArgs& a, int type, hipStream_t s) {
+  hipError_t e = a.chunks > 0 ? launch_prepare(a, type, true, s) : hipSuccess;
+  if (e != hipSuccess) return e;
+  return by_type(type, [&](auto tag) {
+    return by_keys(a.DK, [&](auto keys) {
+      using T = typename decltype(tag)::type;
+      constexpr int KT = decltype(keys)::value;
+      const int slices = (a.DV + 63) / 64;
+      const hipError_t e = enqueue(delta_reverse_kernel<T, KT, 1>,
+                                   dim3((uint32_t)(a.B * a.H * slices)), dim3(256), 0, s, a, slices);
+      if (e != hipSuccess || a.chunks == 0) return e;
+      return enqueue(delta_gradient_kernel<T, KT>, dim3((uint32_t)(a.B * a.chunks * a.HK)), dim3(512),
+                     0, s, a);
+    });
+  });
+}
+
+hipError_t launch_delta_step(const DeltaArgs& a, int type, hipStream_t s) {
+  const int slices = (a.DV + 127) / 128;
+  return enqueue(delta_step_kernel, dim3((uint32_t)(a.B * a.H * slices)), dim3(256), 0, s, a, type,
+                 slices);
+}
+
+}  // namespace per

@@ -1,4 +1,4 @@
-// marshal.cpp -- Python binding of include/per_train.h: takes tensors, checks
+// marshal.cpp -- Python binding of include/per_train.h and include/per_block.h: takes tensors, checks
 // them, and passes pointers, sizes and strides to the C entry points.
 //
 // The smallest of these calls take 3 us on the device; the same checks written
@@ -21,8 +21,9 @@
 
 #include <stdexcept>
 #include <string>
+#include <vector>
 
-#include "../../include/per_train.h"
+#include "../../include/per_block.h"
 
 namespace {
 
@@ -31,7 +32,10 @@ using at::Tensor;
 #define ENTRY_POINTS(X)                                                                     \
   X(per_rows_write) X(per_rows_write_at) X(per_rows_read) X(per_scan_workspace_bytes)       \
   X(per_scan_forward) X(per_scan_backward) X(per_scan_step) X(per_distill_workspace_bytes)  \
-  X(per_distill) X(per_distill_forward) X(per_distill_backward) X(per_last_error)
+  X(per_distill) X(per_distill_forward) X(per_distill_backward) X(per_embed_forward)        \
+  X(per_embed_workspace_bytes) X(per_embed_backward) X(per_norm_forward)                    \
+  X(per_norm_workspace_bytes) X(per_norm_backward) X(per_delta_workspace_bytes)             \
+  X(per_delta_forward) X(per_delta_backward) X(per_delta_step) X(per_last_error)
 
 struct Api {
 #define MEMBER(name) decltype(&::name) name = nullptr;
@@ -55,7 +59,7 @@ void check(int rc) {
 
 // ------------------------------------------------------------------ arguments
 
-constexpr int kMaxArgs = 16;
+constexpr int kMaxArgs = 18;
 
 // Arguments of one call by position in `names`; NULL where not given or None.
 struct Args {
@@ -513,6 +517,312 @@ PyObject* distill_workspace(const Args& a) {
       distill_bytes(a.integer(0, 0), a.integer(1, 0), a.integer(2, 0), (int)a.integer(3, 0)));
 }
 
+// -------------------------------------------------------------------- embedding
+
+// A dense array of int32 or int64 tokens.
+struct Tokens {
+  const void* p;
+  int64_t N;
+  int bytes;
+};
+Tokens tokens_of(const Tensor& t, const Where& w) {
+  const bool wide = t.scalar_type() == at::kLong;
+  if (t.dim() != 1 || (!wide && t.scalar_type() != at::kInt))
+    refuse("tokens must be [N], int32 or int64");
+  return {dense<const void>(t, "tokens", t.scalar_type(), t.sizes(), w), t.size(0), wide ? 8 : 4};
+}
+bool flag(const Args& a, int i, bool otherwise) {
+  if (!a.v[i]) return otherwise;
+  const int on = PyObject_IsTrue(a.v[i]);
+  if (on < 0) {
+    PyErr_Clear();
+    refuse(std::string(a.names[i]) + " must be a truth value");
+  }
+  return on != 0;
+}
+at::ScalarType dtype_of(const Args& a, int i, at::ScalarType otherwise) {
+  if (!a.v[i]) return otherwise;
+  if (!THPDtype_Check(a.v[i])) refuse("dtype must be a torch.dtype");
+  const at::ScalarType t = reinterpret_cast<THPDtype*>(a.v[i])->scalar_type;
+  if (t != at::kFloat && t != at::kBFloat16 && t != at::kHalf)
+    refuse("dtype must be float32, bfloat16 or float16");
+  return t;
+}
+Tensor scratch(int64_t bytes, const Where& w) {
+  return bytes ? w.empty({bytes}, at::kByte) : Tensor();
+}
+void* data(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// tokens, table, scale = 1, out, dtype, stream
+PyObject* embed_forward(const Args& a) {
+  const Tensor& table = a.tensor(1);
+  const Where w(a.v[5], table, "table");
+  if (table.dim() != 2) refuse("table must be [V x D]");
+  const int from = type_of(table, "table");
+  const Matrix mt = matrix(table, "table", table.scalar_type(), table.sizes(), w);
+  const Tokens t = tokens_of(a.tensor(0), w);
+  const int64_t shape[] = {t.N, table.size(1)};
+  const Tensor out = output(a, 3, shape, dtype_of(a, 4, table.scalar_type()), w);
+  const int to = type_of(out, "out");
+  if (a.v[3] && a.v[4] && out.scalar_type() != dtype_of(a, 4, at::kFloat))
+    refuse("out is not of the dtype given");
+  const Matrix mo = matrix(out, "out", out.scalar_type(), shape, w);
+  check(api.per_embed_forward(t.N, table.size(0), shape[1], t.p, t.bytes, mt.p, from, mt.stride,
+                              a.real(2, 1.0), mo.p, to, mo.stride, w.stream));
+  return THPVariable_Wrap(out);
+}
+
+int64_t embed_bytes(int64_t N, int64_t V, int64_t D) {
+  size_t n = 0;
+  check(api.per_embed_workspace_bytes(N, V, D, &n));
+  return (int64_t)n;
+}
+
+// tokens, dout, vocab, scale = 1, grad, accumulate = False, stream
+PyObject* embed_backward(const Args& a) {
+  const Tensor& dout = a.tensor(1);
+  const Where w(a.v[6], dout, "dout");
+  const Tokens t = tokens_of(a.tensor(0), w);
+  if (dout.dim() != 2) refuse("dout must be [N x D]");
+  const int from = type_of(dout, "dout");
+  const int64_t rows[] = {t.N, dout.size(1)}, V = a.integer(2, 0);
+  const Matrix md = matrix(dout, "dout", dout.scalar_type(), rows, w);
+  const bool add = flag(a, 5, false);
+  if (add && !a.v[4]) refuse("accumulate needs the grad to add to");
+  const int64_t bytes = embed_bytes(t.N, V, rows[1]);
+  const int64_t shape[] = {V, rows[1]};
+  const Tensor grad = output(a, 4, shape, at::kFloat, w);
+  const int to = type_of(grad, "grad");
+  const Matrix mg = matrix(grad, "grad", grad.scalar_type(), shape, w);
+  const Tensor ws = scratch(bytes, w);
+  check(api.per_embed_backward(t.N, V, rows[1], t.p, t.bytes, md.p, from, md.stride, a.real(3, 1.0),
+                               add, mg.p, to, mg.stride, data(ws), (size_t)bytes, w.stream));
+  return THPVariable_Wrap(grad);
+}
+
+PyObject* embed_workspace(const Args& a) {
+  return PyLong_FromLongLong(embed_bytes(a.integer(0, 0), a.integer(1, 0), a.integer(2, 0)));
+}
+
+// ------------------------------------------------------------------- layer norm
+
+// Weight and bias [D], both f32 or both of the rows' type.
+struct Affine {
+  const void* weight = nullptr;
+  const void* bias = nullptr;
+  int type = PER_F32;
+};
+Affine affine(const Args& a, int weight, int bias, int64_t D, at::ScalarType rows, const Where& w) {
+  Affine f;
+  bool known = false;
+  for (int i : {weight, bias}) {
+    if (i < 0 || !a.v[i]) continue;
+    const Tensor& t = a.tensor(i);
+    if (t.scalar_type() != at::kFloat && t.scalar_type() != rows)
+      refuse(std::string(a.names[i]) + " must be float32 or of the type of x");
+    const int type = type_of(t, a.names[i]);
+    if (known && type != f.type) refuse("weight and bias must have one type");
+    f.type = type;
+    known = true;
+    (i == weight ? f.weight : f.bias) = dense<const void>(t, a.names[i], t.scalar_type(), {D}, w);
+  }
+  return f;
+}
+
+// x, weight, bias, eps = 1e-5, y, stats, stream
+PyObject* norm_forward(const Args& a) {
+  const Tensor& x = a.tensor(0);
+  const Where w(a.v[6], x, "x");
+  if (x.dim() != 2) refuse("x must be [N x D]");
+  const int type = type_of(x, "x");
+  const int64_t N = x.size(0), D = x.size(1);
+  const Matrix mx = matrix(x, "x", x.scalar_type(), x.sizes(), w);
+  const Affine f = affine(a, 1, 2, D, x.scalar_type(), w);
+  const Tensor y = output(a, 4, x.sizes(), x.scalar_type(), w),
+               stats = output(a, 5, {N, 2}, at::kFloat, w);
+  const Matrix my = matrix(y, "y", x.scalar_type(), x.sizes(), w);
+  float* ps = dense<float>(stats, "stats", at::kFloat, {N, 2}, w);
+  check(api.per_norm_forward(N, D, type, mx.p, mx.stride, f.weight, f.bias, f.type,
+                             a.real(3, 1e-5), my.p, my.stride, ps, w.stream));
+  return pair(y, stats);
+}
+
+int64_t norm_bytes(int64_t N, int64_t D, int type) {
+  size_t n = 0;
+  check(api.per_norm_workspace_bytes(N, D, type, &n));
+  return (int64_t)n;
+}
+
+// x, stats, dy, weight, dx, dweight, dbias, sums = True, stream
+PyObject* norm_backward(const Args& a) {
+  const Tensor& x = a.tensor(0);
+  const Where w(a.v[8], x, "x");
+  if (x.dim() != 2) refuse("x must be [N x D]");
+  const int type = type_of(x, "x");
+  const auto dt = x.scalar_type();
+  const int64_t N = x.size(0), D = x.size(1);
+  const Matrix mx = matrix(x, "x", dt, x.sizes(), w),
+               md = matrix(a.tensor(2), "dy", dt, x.sizes(), w);
+  const auto* stats = dense<const float>(a, 1, at::kFloat, {N, 2}, w);
+  const Affine f = affine(a, 3, -1, D, dt, w);
+  const bool sums = flag(a, 7, true);
+  if (!sums && (a.v[5] || a.v[6])) refuse("dweight and dbias are given, and sums is false");
+  const Tensor dx = output(a, 4, x.sizes(), dt, w);
+  const Matrix mo = matrix(dx, "dx", dt, x.sizes(), w);
+  Tensor dw, db;
+  float *pw = nullptr, *pb = nullptr;
+  if (sums) {
+    dw = output(a, 5, {D}, at::kFloat, w);
+    db = output(a, 6, {D}, at::kFloat, w);
+    pw = dense<float>(dw, "dweight", at::kFloat, {D}, w);
+    pb = dense<float>(db, "dbias", at::kFloat, {D}, w);
+  }
+  const int64_t bytes = norm_bytes(N, D, type);
+  const Tensor ws = scratch(bytes, w);
+  check(api.per_norm_backward(N, D, type, mx.p, mx.stride, stats, md.p, md.stride, f.weight, f.type,
+                              mo.p, mo.stride, pw, pb, data(ws), (size_t)bytes, w.stream));
+  return triple(dx, dw, db);  // an undefined tensor is None
+}
+
+PyObject* norm_workspace(const Args& a) {
+  return PyLong_FromLongLong(norm_bytes(a.integer(0, 0), a.integer(1, 0), (int)a.integer(2, 0)));
+}
+
+// ------------------------------------------------------------- gated delta rule
+
+// [B x T x H x D], or without T; unit stride along D.
+per_seq seq(const Tensor& t, const char* name, at::ScalarType dtype, at::IntArrayRef shape,
+            bool steps, const Where& w) {
+  expect(t, name, dtype, shape, w);
+  const int n = steps ? 3 : 2;  // dimensions before D
+  if ((int)shape.size() > n && shape[n] > 1 && t.stride(n) != 1)
+    refuse(std::string(name) + " must have unit stride in its last dimension");
+  return {t.data_ptr(), t.stride(0), steps ? t.stride(1) : 0, t.stride(n - 1)};
+}
+struct Delta {
+  int64_t B, T, H, HK, DK, DV;
+  int type;
+  at::ScalarType dtype;
+  std::vector<int64_t> qk, vo, gate, state;  // shapes
+  per_seq q, k, v, g, b;
+};
+// Arguments 0 to 4: q, k, v, g, b.
+Delta delta(const Args& a, bool steps, const Where& w) {
+  const Tensor &q = a.tensor(0), &v = a.tensor(2);
+  const int n = steps ? 4 : 3;
+  if (q.dim() != n || v.dim() != n)
+    refuse(steps ? "q must be [B x T x HK x DK], v [B x T x H x DV]"
+                 : "q must be [B x HK x DK], v [B x H x DV]");
+  Delta d;
+  d.type = type_of(q, "q");
+  d.dtype = q.scalar_type();
+  d.B = v.size(0);
+  d.T = steps ? v.size(1) : 1;
+  d.H = v.size(n - 2);
+  d.DV = v.size(n - 1);
+  d.HK = q.size(n - 2);
+  d.DK = q.size(n - 1);
+  d.vo = v.sizes().vec();
+  d.qk = d.vo;
+  d.qk[n - 2] = d.HK;
+  d.qk[n - 1] = d.DK;
+  d.gate = d.vo;
+  d.gate.pop_back();
+  d.state = {d.B, d.H, d.DK, d.DV};
+  d.q = seq(q, "q", d.dtype, d.qk, steps, w);
+  d.k = seq(a.tensor(1), "k", d.dtype, d.qk, steps, w);
+  d.v = seq(v, "v", d.dtype, d.vo, steps, w);
+  d.g = seq(a.tensor(3), "g", d.dtype, d.gate, steps, w);
+  d.b = seq(a.tensor(4), "b", d.dtype, d.gate, steps, w);
+  return d;
+}
+#define DELTA(d) d.H, d.HK, d.DK, d.DV, d.type, d.q, d.k, d.v, d.g, d.b
+
+int64_t delta_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t DK, int64_t DV, int type,
+                    bool backward) {
+  size_t n = 0;
+  check(api.per_delta_workspace_bytes(B, T, H, HK, DK, DV, type, backward, &n));
+  return (int64_t)n;
+}
+std::vector<int64_t> carry_shape(const Delta& d) {
+  return {d.B, (d.T + PER_DELTA_CHUNK - 1) / PER_DELTA_CHUNK, d.H, d.DK + PER_DELTA_CHUNK, d.DV};
+}
+
+// q, k, v, g, b, reset, length, s0, scale = 1, save = True, out, s_last, carries, stream
+PyObject* delta_forward(const Args& a) {
+  const Where w(a.v[13], a.tensor(0), "q");
+  const Delta d = delta(a, true, w);
+  const uint8_t* reset = flags(a, 5, {d.B, d.T}, w);
+  const auto* length = dense<const int64_t>(a, 6, at::kLong, {d.B}, w);
+  const auto* s0 = dense<const float>(a, 7, at::kFloat, d.state, w);
+  const bool save = flag(a, 9, true);
+  if (!save && a.v[12]) refuse("carries are given, and save is false");
+  const int64_t bytes = delta_bytes(d.B, d.T, d.H, d.HK, d.DK, d.DV, d.type, false);
+  const Tensor o = output(a, 10, d.vo, d.dtype, w), s = output(a, 11, d.state, at::kFloat, w);
+  const per_seq vo = seq(o, "out", d.dtype, d.vo, true, w);
+  float* ps = dense<float>(s, "s_last", at::kFloat, d.state, w);
+  Tensor c;
+  float* pc = nullptr;
+  if (save) {
+    c = output(a, 12, carry_shape(d), at::kFloat, w);
+    pc = dense<float>(c, "carries", at::kFloat, carry_shape(d), w);
+  }
+  const Tensor ws = scratch(bytes, w);
+  check(api.per_delta_forward(d.B, d.T, DELTA(d), reset, length, s0, a.real(8, 1.0), vo, ps, pc,
+                              data(ws), (size_t)bytes, w.stream));
+  return triple(o, s, c);
+}
+
+// q, k, v, g, b, carries, do, reset, length, ds_last, scale = 1, dq, dk, dv, dg, db, ds0, stream
+PyObject* delta_backward(const Args& a) {
+  const Where w(a.v[17], a.tensor(0), "q");
+  const Delta d = delta(a, true, w);
+  const auto* pc = dense<const float>(a, 5, at::kFloat, carry_shape(d), w);
+  const per_seq d_o = seq(a.tensor(6), "do", d.dtype, d.vo, true, w);
+  const uint8_t* reset = flags(a, 7, {d.B, d.T}, w);
+  const auto* length = dense<const int64_t>(a, 8, at::kLong, {d.B}, w);
+  const auto* dl = dense<const float>(a, 9, at::kFloat, d.state, w);
+  const int64_t bytes = delta_bytes(d.B, d.T, d.H, d.HK, d.DK, d.DV, d.type, true);
+  const std::vector<int64_t>* shapes[] = {&d.qk, &d.qk, &d.vo, &d.gate, &d.gate};
+  Tensor out[6];
+  per_seq views[5];
+  for (int i = 0; i < 5; ++i) {
+    out[i] = output(a, 11 + i, *shapes[i], d.dtype, w);
+    views[i] = seq(out[i], a.names[11 + i], d.dtype, *shapes[i], true, w);
+  }
+  out[5] = output(a, 16, d.state, at::kFloat, w);
+  float* p0 = dense<float>(out[5], "ds0", at::kFloat, d.state, w);
+  const Tensor ws = scratch(bytes, w);
+  check(api.per_delta_backward(d.B, d.T, DELTA(d), reset, length, pc, d_o, dl, a.real(10, 1.0),
+                               views[0], views[1], views[2], views[3], views[4], p0, data(ws),
+                               (size_t)bytes, w.stream));
+  PyObject* t = PyTuple_New(6);
+  if (!t) return nullptr;
+  for (int i = 0; i < 6; ++i) PyTuple_SET_ITEM(t, i, THPVariable_Wrap(out[i]));
+  return t;
+}
+
+// q, k, v, g, b, s, reset, scale = 1, s_out, out, stream
+PyObject* delta_step(const Args& a) {
+  const Where w(a.v[10], a.tensor(0), "q");
+  const Delta d = delta(a, false, w);
+  const auto* s = dense<const float>(a, 5, at::kFloat, d.state, w);
+  const uint8_t* reset = flags(a, 6, {d.B}, w);
+  const Tensor so = a.v[8] ? a.tensor(8) : a.tensor(5);
+  float* ps = dense<float>(so, "s_out", at::kFloat, d.state, w);
+  const Tensor o = output(a, 9, d.vo, d.dtype, w);
+  const per_seq vo = seq(o, "out", d.dtype, d.vo, false, w);
+  check(api.per_delta_step(d.B, DELTA(d), reset, s, a.real(7, 1.0), ps, vo, w.stream));
+  if (!a.v[8] && !so.is_inference()) so.unsafeGetTensorImpl()->bump_version();
+  return pair(o, so);
+}
+
+PyObject* delta_workspace(const Args& a) {
+  return PyLong_FromLongLong(delta_bytes(a.integer(0, 0), a.integer(1, 0), a.integer(2, 0),
+                                         a.integer(3, 0), a.integer(4, 0), a.integer(5, 0),
+                                         (int)a.integer(6, 0), flag(a, 7, false)));
+}
+
 // ----------------------------------------------------------------- the module
 
 struct Function {
@@ -613,6 +923,53 @@ Function functions[] = {
      "per_distill_backward(logits, tidx, tlogit, saved, gloss, tlse=None, temperature=1.0, "
      "grad=None, stream=None)\n\n"
      "Gradient by the logits from the gradient by each row's loss.", {}},
+    {"per_embed_forward", embed_forward, 2, 6, bits(3),
+     {"tokens", "table", "scale", "out", "dtype", "stream"},
+     "per_embed_forward(tokens, table, scale=1.0, out=None, dtype=None, stream=None)\n\n"
+     "[N x D]: scale times the rows of table [V x D] that tokens [N] (int32 or int64) name, zeros\n"
+     "for tokens outside [0, V); of dtype (the table's by default).", {}},
+    {"per_embed_workspace_bytes", embed_workspace, 3, 3, bits(), {"N", "V", "D"},
+     "per_embed_workspace_bytes(N, V, D)", {}},
+    {"per_embed_backward", embed_backward, 3, 7, bits(4),
+     {"tokens", "dout", "vocab", "scale", "grad", "accumulate", "stream"},
+     "per_embed_backward(tokens, dout, vocab, scale=1.0, grad=None, accumulate=False, stream=None)"
+     "\n\nGradient by the table [vocab x D] (float32 without grad): scale times the sum of each\n"
+     "token's rows of dout, zeros for tokens that do not occur, or added to what grad holds.", {}},
+    {"per_norm_forward", norm_forward, 1, 7, bits(4, 5),
+     {"x", "weight", "bias", "eps", "y", "stats", "stream"},
+     "per_norm_forward(x, weight=None, bias=None, eps=1e-5, y=None, stats=None, stream=None)\n\n"
+     "Layer norm of the rows of x [N x D].  Returns (y, stats [N x 2] f32: mean and reciprocal\n"
+     "deviation, which per_norm_backward takes).  y may be x.", {}},
+    {"per_norm_workspace_bytes", norm_workspace, 3, 3, bits(), {"N", "D", "type"},
+     "per_norm_workspace_bytes(N, D, type)", {}},
+    {"per_norm_backward", norm_backward, 3, 9, bits(4, 5, 6),
+     {"x", "stats", "dy", "weight", "dx", "dweight", "dbias", "sums", "stream"},
+     "per_norm_backward(x, stats, dy, weight=None, dx=None, dweight=None, dbias=None, sums=True, "
+     "stream=None)\n\n"
+     "Gradients (dx, dweight [D] f32, dbias [D] f32) of per_norm_forward; without sums dx alone,\n"
+     "and None for the others.  dx may be dy.", {}},
+    {"per_delta_workspace_bytes", delta_workspace, 7, 8, bits(),
+     {"B", "T", "H", "HK", "DK", "DV", "type", "backward"},
+     "per_delta_workspace_bytes(B, T, H, HK, DK, DV, type, backward=False)", {}},
+    {"per_delta_forward", delta_forward, 5, 14, bits(10, 11, 12),
+     {"q", "k", "v", "g", "b", "reset", "length", "s0", "scale", "save", "out", "s_last", "carries",
+      "stream"},
+     "per_delta_forward(q, k, v, g, b, reset=None, length=None, s0=None, scale=1.0, save=True, "
+     "out=None, s_last=None, carries=None, stream=None)\n\n"
+     "The gated delta rule along dim 1 of q, k [B x T x HK x DK], v [B x T x H x DV] and the logits\n"
+     "g, b [B x T x H] of gates and writing strengths.  Returns (out [B x T x H x DV], s_last\n"
+     "[B x H x DK x DV] f32, carries: what per_delta_backward takes, None without save).", {}},
+    {"per_delta_backward", delta_backward, 7, 18, bits(11, 12, 13, 14, 15, 16),
+     {"q", "k", "v", "g", "b", "carries", "do", "reset", "length", "ds_last", "scale", "dq", "dk",
+      "dv", "dg", "db", "ds0", "stream"},
+     "per_delta_backward(q, k, v, g, b, carries, do, reset=None, length=None, ds_last=None, "
+     "scale=1.0, dq=None, dk=None, dv=None, dg=None, db=None, ds0=None, stream=None)\n\n"
+     "Gradients (dq, dk, dv, dg, db, ds0) of per_delta_forward from do and ds_last.", {}},
+    {"per_delta_step", delta_step, 6, 11, bits(8, 9),
+     {"q", "k", "v", "g", "b", "s", "reset", "scale", "s_out", "out", "stream"},
+     "per_delta_step(q, k, v, g, b, s, reset=None, scale=1.0, s_out=None, out=None, stream=None)\n\n"
+     "One step of B sequences: q, k [B x HK x DK], v [B x H x DV], g, b [B x H], s [B x H x DK x DV]\n"
+     "f32 (updated in place without s_out).  Returns (out, s_out).", {}},
 };
 constexpr int kFunctions = sizeof functions / sizeof functions[0];
 
@@ -701,7 +1058,7 @@ void fill(std::integer_sequence<int, I...>) {
    ...);
 }
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "Binding of include/per_train.h.", -1,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "Binding of include/per_train.h and include/per_block.h.", -1,
                       methods,               nullptr,    nullptr, nullptr, nullptr};
 
 }  // namespace

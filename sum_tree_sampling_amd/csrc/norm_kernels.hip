@@ -1,0 +1,472 @@
+// norm_kernels.hip -- layer norm, forward and backward.
+//
+// A row is held in the registers of a group of lanes (16 lanes to 1024 threads)
+// between its statistics and its result, so each tensor is read and written once.
+// The mean is taken first and the squares of the distances from it after; the sum of
+// the distances, which is what rounding left in the mean, corrects both.
+//
+// Backward, a group of lanes walks over rows and keeps its columns' sums for the
+// weight and the bias in registers; a block's sums go to memory once, and a second
+// launch adds the blocks in order.
+#include <algorithm>
+
+#include "block_internal.h"
+#include "elem.h"
+#include "lanes.h"
+
+namespace per {
+namespace {
+
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);  // columns of a chunk
+
+template <typename T>
+struct Tag {
+  using type = T;
+};
+
+// The values of columns [col, col + W), 0 past D.
+template <typename T, int W>
+__device__ __forceinline__ void load_cols(const T* p, uint32_t col, uint32_t D, float (&v)[W]) {
+  if (col + W <= D) {
+    unpack<T, W>(load_pack<T, W>(p + col), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = col + i < D ? (float)p[col + i] : 0.0f;
+  }
+}
+template <typename T, int W, bool ONCE>
+__device__ __forceinline__ void store_cols(T* p, uint32_t col, uint32_t D, const float (&v)[W]) {
+  if (col + W <= D) {
+    if constexpr (ONCE) {
+      store_once<T, W>(p + col, v);
+    } else {
+      store_vals<T, W>(p + col, v);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (col + i < D) p[col + i] = (T)v[i];
+  }
+}
+// Columns of weight or bias: f32 or the rows' type.
+template <typename T, int W>
+__device__ __forceinline__ void load_affine(const void* p, bool f32, uint32_t col, uint32_t D,
+                                            float (&v)[W]) {
+  if (f32) {
+    load_cols<float, W>(static_cast<const float*>(p), col, D, v);
+  } else {
+    load_cols<T, W>(static_cast<const T*>(p), col, D, v);
+  }
+}
+
+// Sums of two values over a group of GROUP threads, the same in all of them.  Groups
+// of a wave or less exchange lanes; larger ones are whole workgroups, and call this
+// together.  `space` of 64 floats is used alternately.
+template <int GROUP>
+__device__ __forceinline__ void group_sum(float& a, float& b, float* space) {
+  constexpr int kLg = GROUP >= 64 ? 6 : GROUP == 32 ? 5 : 4;
+#pragma unroll
+  for (int s = 0; s < kLg; ++s) {
+    a += xor_lanes(a, s);
+    b += xor_lanes(b, s);
+  }
+  if constexpr (GROUP > 64) {
+    constexpr int kWaves = GROUP / 64;
+    const int wave = threadIdx.x / 64;
+    if (threadIdx.x % 64 == 0) {
+      space[2 * wave] = a;
+      space[2 * wave + 1] = b;
+    }
+    __syncthreads();
+    a = b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      a += space[2 * w];
+      b += space[2 * w + 1];
+    }
+  }
+}
+
+template <typename T, int GROUP, int CH>
+__global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void norm_forward_kernel(NormArgs a) {
+  constexpr int W = kVec<T>;
+  __shared__ float space[2][64];
+  const int lane = threadIdx.x % GROUP;
+  const int64_t at = (int64_t)blockIdx.x * (blockDim.x / GROUP) + threadIdx.x / GROUP;
+  const int64_t row = min(at, a.N - 1);  // all lanes take part in the exchanges
+  const T* x = static_cast<const T*>(a.x) + row * a.xs;
+  float v[CH][W];
+  float s = 0.0f, none = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    load_cols<T, W>(x, (uint32_t)(c * GROUP + lane) * W, a.D, v[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int i = 0; i < W; ++i) s += v[c][i];
+  group_sum<GROUP>(s, none, space[0]);
+  const float inv = 1.0f / (float)a.D;
+  float mean = s * inv;
+  float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const bool on = (uint32_t)(c * GROUP + lane) * W + i < a.D;
+      v[c][i] = on ? v[c][i] - mean : 0.0f;
+      s1 += v[c][i];
+      s2 += v[c][i] * v[c][i];
+    }
+  group_sum<GROUP>(s1, s2, space[1]);
+  const float off = s1 * inv;
+  const float rstd = 1.0f / sqrtf(fmaxf(s2 * inv - off * off, 0.0f) + a.eps);
+  if (at >= a.N) return;
+  if (a.stats && lane == 0) {
+    a.stats[2 * row] = mean + off;
+    a.stats[2 * row + 1] = rstd;
+  }
+  T* y = static_cast<T*>(a.y) + row * a.ys;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const uint32_t col = (uint32_t)(c * GROUP + lane) * W;
+    if (col >= a.D) break;
+    float out[W], t[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) out[i] = (v[c][i] - off) * rstd;
+    if (a.weight) {
+      load_affine<T, W>(a.weight, a.affine_f32, col, a.D, t);
+#pragma unroll
+      for (int i = 0; i < W; ++i) out[i] *= t[i];
+    }
+    if (a.bias) {
+      load_affine<T, W>(a.bias, a.affine_f32, col, a.D, t);
+#pragma unroll
+      for (int i = 0; i < W; ++i) out[i] += t[i];
+    }
+    store_cols<T, W, false>(y, col, a.D, out);
+  }
+}
+
+// Rows too long for registers: a workgroup of 1024 walks over its row three times.
+template <typename T>
+__global__ __launch_bounds__(1024) void norm_forward_long_kernel(NormArgs a) {
+  constexpr int W = kVec<T>;
+  __shared__ float space[2][64];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.xs;
+  float v[W], s = 0.0f, none = 0.0f;
+  for (uint32_t col = threadIdx.x * W; col < a.D; col += 1024 * W) {
+    load_cols<T, W>(x, col, a.D, v);
+#pragma unroll
+    for (int i = 0; i < W; ++i) s += v[i];
+  }
+  group_sum<1024>(s, none, space[0]);
+  const float inv = 1.0f / (float)a.D;
+  const float mean = s * inv;
+  float s1 = 0.0f, s2 = 0.0f;
+  for (uint32_t col = threadIdx.x * W; col < a.D; col += 1024 * W) {
+    load_cols<T, W>(x, col, a.D, v);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float d = col + i < a.D ? v[i] - mean : 0.0f;
+      s1 += d;
+      s2 += d * d;
+    }
+  }
+  group_sum<1024>(s1, s2, space[1]);
+  const float off = s1 * inv;
+  const float rstd = 1.0f / sqrtf(fmaxf(s2 * inv - off * off, 0.0f) + a.eps);
+  if (a.stats && threadIdx.x == 0) {
+    a.stats[2 * row] = mean + off;
+    a.stats[2 * row + 1] = rstd;
+  }
+  T* y = static_cast<T*>(a.y) + row * a.ys;
+  for (uint32_t col = threadIdx.x * W; col < a.D; col += 1024 * W) {
+    float t[W];
+    load_cols<T, W>(x, col, a.D, v);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = (v[i] - mean - off) * rstd;
+    if (a.weight) {
+      load_affine<T, W>(a.weight, a.affine_f32, col, a.D, t);
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] *= t[i];
+    }
+    if (a.bias) {
+      load_affine<T, W>(a.bias, a.affine_f32, col, a.D, t);
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] += t[i];
+    }
+    store_cols<T, W, false>(y, col, a.D, v);
+  }
+}
+
+// SUMS: the gradients of weight and bias are wanted.
+template <typename T, int GROUP, int CH, bool SUMS>
+__global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void norm_backward_kernel(NormArgs a) {
+  constexpr int W = kVec<T>;
+  constexpr int kGroups = GROUP >= 256 ? 1 : 256 / GROUP;
+  __shared__ float space[2][64];
+  const int lane = threadIdx.x % GROUP, group = threadIdx.x / GROUP;
+  const float inv = 1.0f / (float)a.D;
+  float wt[CH][W], aw[CH][W], ab[CH][W];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const uint32_t col = (uint32_t)(c * GROUP + lane) * W;
+#pragma unroll
+    for (int i = 0; i < W; ++i) aw[c][i] = ab[c][i] = 0.0f, wt[c][i] = 1.0f;
+    if (a.weight && col < a.D) load_affine<T, W>(a.weight, a.affine_f32, col, a.D, wt[c]);
+  }
+  int flip = 0;
+  const int64_t step = (int64_t)gridDim.x * kGroups;
+  for (int64_t first = (int64_t)blockIdx.x * kGroups; first < a.N; first += step) {
+    const bool on = first + group < a.N;
+    const int64_t row = on ? first + group : a.N - 1;
+    const T* x = static_cast<const T*>(a.x) + row * a.xs;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.dys;
+    float xh[CH][W], d[CH][W];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint32_t col = (uint32_t)(c * GROUP + lane) * W;
+      load_cols<T, W>(x, col, a.D, xh[c]);
+      load_cols<T, W>(dy, col, a.D, d[c]);
+    }
+    const float mean = a.stats[2 * row], rstd = a.stats[2 * row + 1];
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const bool in = (uint32_t)(c * GROUP + lane) * W + i < a.D;
+        xh[c][i] = in ? (xh[c][i] - mean) * rstd : 0.0f;
+        if (SUMS && on) {
+          aw[c][i] += d[c][i] * xh[c][i];
+          ab[c][i] += d[c][i];
+        }
+        d[c][i] *= wt[c][i];
+        s1 += d[c][i];
+        s2 += d[c][i] * xh[c][i];
+      }
+    group_sum<GROUP>(s1, s2, space[flip]);
+    flip ^= 1;
+    s1 *= inv;
+    s2 *= inv;
+    if (on) {
+      T* dx = static_cast<T*>(a.y) + row * a.ys;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const uint32_t col = (uint32_t)(c * GROUP + lane) * W;
+        if (col >= a.D) break;
+        float out[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) out[i] = rstd * (d[c][i] - s1 - xh[c][i] * s2);
+        store_cols<T, W, true>(dx, col, a.D, out);
+      }
+    }
+  }
+  if constexpr (SUMS) {
+    float* part = a.part + (int64_t)blockIdx.x * 2 * a.D;
+    if constexpr (kGroups == 1) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const uint32_t col = (uint32_t)(c * GROUP + lane) * W;
+        if (col >= a.D) break;
+        store_cols<float, W, false>(part, col, a.D, aw[c]);
+        store_cols<float, W, false>(part + a.D, col, a.D, ab[c]);
+      }
+    } else {
+      // the groups of a block, one after the other
+      constexpr int kCols = GROUP * CH * W;
+      __shared__ float sum[2][kCols];
+#pragma unroll 1
+      for (int g = 0; g < kGroups; ++g) {
+        if (group == g) {
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+              const int at = (c * GROUP + lane) * W + i;
+              sum[0][at] = g == 0 ? aw[c][i] : sum[0][at] + aw[c][i];
+              sum[1][at] = g == 0 ? ab[c][i] : sum[1][at] + ab[c][i];
+            }
+        }
+        __syncthreads();
+      }
+      for (uint32_t col = threadIdx.x; col < a.D; col += blockDim.x) {
+        part[col] = sum[0][col];
+        part[a.D + col] = sum[1][col];
+      }
+    }
+  }
+}
+
+// Rows too long for registers: their two means first, then columns apart.
+template <typename T>
+__global__ __launch_bounds__(1024) void norm_means_kernel(NormArgs a) {
+  constexpr int W = kVec<T>;
+  __shared__ float space[64];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.xs;
+  const T* dy = static_cast<const T*>(a.dy) + row * a.dys;
+  const float mean = a.stats[2 * row], rstd = a.stats[2 * row + 1];
+  float s1 = 0.0f, s2 = 0.0f;
+  for (uint32_t col = threadIdx.x * W; col < a.D; col += 1024 * W) {
+    float v[W], d[W], w[W];
+    load_cols<T, W>(x, col, a.D, v);
+    load_cols<T, W>(dy, col, a.D, d);
+    if (a.weight) load_affine<T, W>(a.weight, a.affine_f32, col, a.D, w);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float e = col + i < a.D ? (a.weight ? d[i] * w[i] : d[i]) : 0.0f;
+      s1 += e;
+      s2 += col + i < a.D ? e * ((v[i] - mean) * rstd) : 0.0f;
+    }
+  }
+  group_sum<1024>(s1, s2, space);
+  if (threadIdx.x == 0) {
+    a.means[2 * row] = s1 / (float)a.D;
+    a.means[2 * row + 1] = s2 / (float)a.D;
+  }
+}
+template <typename T>
+__global__ __launch_bounds__(256) void norm_columns_kernel(NormArgs a, uint32_t strips) {
+  constexpr int W = kVec<T>;
+  const uint32_t strip = blockIdx.x % strips, block = blockIdx.x / strips;
+  const uint32_t col = (strip * 256 + threadIdx.x) * W;
+  if (col >= a.D) return;
+  float wt[W], aw[W], ab[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) aw[i] = ab[i] = 0.0f, wt[i] = 1.0f;
+  if (a.weight) load_affine<T, W>(a.weight, a.affine_f32, col, a.D, wt);
+  for (int64_t row = block; row < a.N; row += a.blocks) {
+    const float mean = a.stats[2 * row], rstd = a.stats[2 * row + 1];
+    const float s1 = a.means[2 * row], s2 = a.means[2 * row + 1];
+    float v[W], d[W], out[W];
+    load_cols<T, W>(static_cast<const T*>(a.x) + row * a.xs, col, a.D, v);
+    load_cols<T, W>(static_cast<const T*>(a.dy) + row * a.dys, col, a.D, d);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float h = col + i < a.D ? (v[i] - mean) * rstd : 0.0f;
+      aw[i] += d[i] * h;
+      ab[i] += d[i];
+      out[i] = rstd * (d[i] * wt[i] - s1 - h * s2);
+    }
+    store_cols<T, W, true>(static_cast<T*>(a.y) + row * a.ys, col, a.D, out);
+  }
+  float* part = a.part + (int64_t)block * 2 * a.D;
+  store_cols<float, W, false>(part, col, a.D, aw);
+  store_cols<float, W, false>(part + a.D, col, a.D, ab);
+}
+
+// Adds the blocks' sums: 64 columns to a workgroup, 16 threads to a column.
+__global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
+  __shared__ float sum[16][64];
+  const uint32_t col = blockIdx.x * 64 + threadIdx.x % 64, part = threadIdx.x / 64;
+  float s = 0.0f;
+  if (col < 2 * a.D) {
+    int b = (int)part;
+    for (; b + 48 < a.blocks; b += 64) {
+      const float* p = a.part + (int64_t)b * 2 * a.D + col;
+      const int64_t step = (int64_t)32 * a.D;
+      const float v0 = p[0], v1 = p[step], v2 = p[2 * step], v3 = p[3 * step];
+      s += v0;
+      s += v1;
+      s += v2;
+      s += v3;
+    }
+    for (; b < a.blocks; b += 16) s += a.part[(int64_t)b * 2 * a.D + col];
+  }
+  sum[part][threadIdx.x % 64] = s;
+  __syncthreads();
+  if (part == 0 && col < 2 * a.D) {
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s += sum[k][threadIdx.x];
+    float* to = col < a.D ? a.dweight : a.dbias;
+    if (to) to[col < a.D ? col : col - a.D] = s;
+  }
+}
+
+template <typename F>
+hipError_t by_type(int type, F f) {
+  switch (type) {
+    case PER_F32: return f(Tag<float>{});
+    case PER_BF16: return f(Tag<bf16_t>{});
+    default: return f(Tag<f16_t>{});
+  }
+}
+
+// Columns that the widest group of registers holds in the backward pass.
+constexpr uint32_t longest(int type) { return 2u * 1024 * (type == PER_F32 ? 4 : 8); }
+
+}  // namespace
+
+// Blocks of the backward pass: enough to fill the chip, few enough that their sums
+// are little next to the rows.
+size_t norm_workspace(int64_t N, int64_t D, int type, NormArgs* a, void* ws) {
+  const uint32_t vec = type == PER_F32 ? 4 : 8;
+  const int64_t rows = D <= 256 * vec ? 4 : 1;  // rows that a block has at once
+  const int64_t most = D <= 1024 * vec ? 512 : 256;
+  const int64_t blocks = N == 0 ? 0 : std::min(most, (N + rows - 1) / rows);
+  const size_t part = (size_t)blocks * 2 * (size_t)D * 4;
+  if (a) {
+    a->blocks = (int)blocks;
+    a->part = static_cast<float*>(ws);
+    a->means = reinterpret_cast<float*>(static_cast<char*>(ws) + part);
+  }
+  return part + (D > longest(type) ? (size_t)N * 8 : 0);
+}
+
+hipError_t launch_norm_forward(const NormArgs& a, int type, hipStream_t s) {
+  return by_type(type, [&](auto tag) {
+    using T = typename decltype(tag)::type;
+    const uint32_t chunks = (a.D + kVec<T> - 1) / kVec<T>;
+    auto go = [&](auto kern, int group) {
+      const int threads = group > 256 ? group : 256;
+      const int64_t rows = threads / group;
+      return enqueue(kern, dim3((uint32_t)((a.N + rows - 1) / rows)), dim3(threads), 0, s, a);
+    };
+    if (chunks <= 16) return go(norm_forward_kernel<T, 16, 1>, 16);
+    if (chunks <= 64) return go(norm_forward_kernel<T, 64, 1>, 64);
+    if (chunks <= 128) return go(norm_forward_kernel<T, 64, 2>, 64);
+    if (chunks <= 256) return go(norm_forward_kernel<T, 64, 4>, 64);
+    if (chunks <= 512) return go(norm_forward_kernel<T, 256, 2>, 256);
+    if (chunks <= 1024) return go(norm_forward_kernel<T, 256, 4>, 256);
+    if (chunks <= 2048) return go(norm_forward_kernel<T, 1024, 2>, 1024);
+    if (chunks <= 4096) return go(norm_forward_kernel<T, 1024, 4>, 1024);
+    return enqueue(norm_forward_long_kernel<T>, dim3((uint32_t)a.N), dim3(1024), 0, s, a);
+  });
+}
+
+hipError_t launch_norm_backward(const NormArgs& a, int type, hipStream_t s) {
+  const bool sums = a.dweight || a.dbias;
+  hipError_t e = hipSuccess;
+  if (a.N > 0)
+    e = by_type(type, [&](auto tag) {
+      using T = typename decltype(tag)::type;
+      const uint32_t chunks = (a.D + kVec<T> - 1) / kVec<T>;
+      auto go = [&](auto with, auto without, int group) {
+        return enqueue(sums ? with : without, dim3(a.blocks), dim3(group > 256 ? group : 256), 0, s,
+                       a);
+      };
+#define GO(G, C) go(norm_backward_kernel<T, G, C, true>, norm_backward_kernel<T, G, C, false>, G)
+      if (chunks <= 16) return GO(16, 1);
+      if (chunks <= 64) return GO(64, 1);
+      if (chunks <= 128) return GO(64, 2);
+      if (chunks <= 256) return GO(64, 4);
+      if (chunks <= 512) return GO(256, 2);
+      if (chunks <= 1024) return GO(256, 4);
+      if (chunks <= 2048) return GO(1024, 2);
+#undef GO
+      const hipError_t e =
+          enqueue(norm_means_kernel<T>, dim3((uint32_t)a.N), dim3(1024), 0, s, a);
+      if (e != hipSuccess) return e;
+      const uint32_t strips = (chunks + 255) / 256;
+      return enqueue(norm_columns_kernel<T>, dim3(strips * (uint32_t)a.blocks), dim3(256), 0, s, a,
+                     strips);
+    });
+  if (e != hipSuccess || !sums) return e;
+  return enqueue(norm_join_kernel, dim3((2 * a.D + 63) / 64), dim3(1024), 0, s, a);
+}
+
+}  // namespace per

@@ -1,5 +1,6 @@
-"""Thin Python binding of the C ABI in include/per_train.h: the operators a
-learner that replays sequences runs next to the sum tree.
+"""Thin Python binding of the C ABI in include/per_train.h and include/per_block.h:
+the operators a learner that replays sequences runs next to the sum tree, and the
+layers of a student that reads tokens.
 
 Functions carry the C names; sizes, types and strides come from the tensors
 (csrc/marshal.cpp checks them and raises ValueError, or PerError with the
@@ -28,13 +29,18 @@ PER_SCAN_CHUNK = 64
 NAMES = ("per_rows_write", "per_rows_write_at", "per_rows_read", "per_scan_workspace_bytes",
          "per_scan_forward", "per_scan_backward", "per_scan_step", "per_distill_workspace_bytes",
          "per_distill", "per_distill_forward", "per_distill_backward")
+BLOCK_NAMES = ("per_embed_forward", "per_embed_workspace_bytes", "per_embed_backward",
+               "per_norm_forward", "per_norm_workspace_bytes", "per_norm_backward",
+               "per_delta_workspace_bytes", "per_delta_forward", "per_delta_backward",
+               "per_delta_step")
+PER_DELTA_CHUNK = 64
 
 
 def _bind():
     """Hand the library's entry points to the binding (at its first call)."""
     lib = load()
     _marshal.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
-                   for n in NAMES + ("per_last_error",)}, PerError)
+                   for n in NAMES + BLOCK_NAMES + ("per_last_error",)}, PerError)
 
 
 def _missing(name):
@@ -48,10 +54,10 @@ def _missing(name):
 try:
     from . import _marshal
     _marshal.set_loader(_bind)
-    globals().update({n: getattr(_marshal, n) for n in NAMES})
-except ImportError as e:  # before the first build; the calls say so
+    globals().update({n: getattr(_marshal, n) for n in NAMES + BLOCK_NAMES})
+except (ImportError, AttributeError) as e:  # before the first build, or an older one; the calls say so
     _why = e
-    globals().update({n: _missing(n) for n in NAMES})
+    globals().update({n: _missing(n) for n in NAMES + BLOCK_NAMES})
 
 
 def rows_alloc(capacity, dim, dtype=torch.float8_e4m3fn, group=128, device="cuda"):
