@@ -98,7 +98,7 @@ int per_norm_backward(int64_t N, int64_t D, int32_t type, const void* d_x, int64
  *
  * q, k: [B x T x HK x DK], v, o: [B x T x H x DV], g, b: [B x T x H], all of `type`
  * with unit stride along DK and DV and their own strides between sequences (sb),
- * steps (st) and heads (sh).  d_reset: [B x T] u8, dense.  States (s0, s_last, s,
+ * steps (st, at most 2^23) and heads (sh).  d_reset: [B x T] u8, dense.  States (s0, s_last, s,
  * ds_last, ds0) are dense [B x H x DK x DV] f32; NULL where read means 0, and where
  * written that it is not wanted.
  *

@@ -75,6 +75,9 @@ int check_delta(DeltaArgs& a, int64_t B, int64_t T, int64_t H, int64_t HK, int64
   a.chunks = chunks;
   return PER_OK;
 }
+// A chunk's rows lie within 2^31 bytes, so that places in them are 32-bit offsets.
+constexpr int64_t kMaxStep = 1 << 23;
+
 // An array of sequences [B x T x H] of rows of D values.  An output's rows must not
 // overlap: by rising stride, each dimension steps past the extent of those before.
 int check_seq(Seq& to, const per_seq& s, int32_t type, int64_t B, int64_t T, int64_t H, int64_t D,
@@ -84,6 +87,8 @@ int check_seq(Seq& to, const per_seq& s, int32_t type, int64_t B, int64_t T, int
   if (s.sb < 0 || s.st < 0 || s.sh < 0 || s.sb > kMaxStride || s.st > kMaxStride ||
       s.sh > kMaxStride)
     return bad("%s has a stride that is negative or too large", what);
+  if (T > 1 && s.st > kMaxStep)
+    return bad("%s has steps %lld elements apart, more than 2^23", what, (long long)s.st);
   if (output) {
     std::pair<int64_t, int64_t> dims[3] = {{s.sb, B}, {s.st, T}, {s.sh, H}};
     std::sort(dims, dims + 3);
@@ -95,7 +100,7 @@ int check_seq(Seq& to, const per_seq& s, int32_t type, int64_t B, int64_t T, int
       extent += (d.second - 1) * d.first;
     }
   }
-  to = Seq{s.p, s.sb, s.st, s.sh};
+  to = Seq{s.p, s.sb, T > 1 ? s.st : 0, s.sh};
   return PER_OK;
 }
 

@@ -122,66 +122,104 @@ __device__ __forceinline__ constexpr int upper_block(int it, int kt) {
   return it < 2 ? 2 * it + kt : it + 2;
 }
 
-// A thread's 4 x 8 piece of a [64 x 32 KT] matrix: rows 4 a + r, columns 8 m + c.  As
-// rows: blocks it * KT + kt, the columns being the terms.  As columns: blocks dt * 2 +
+// A thread's 4 x 8 piece of a [64 x 32 KT] matrix, as it lies in memory: rows 4 a + r,
+// columns 8 m + c; 0 from row `rows` and from column `width` on.
+template <typename T>
+struct Piece {
+  typedef T row __attribute__((ext_vector_type(8)));
+  row v[4];
+};
+template <typename T>
+__device__ __forceinline__ void load_piece(const T* base, int64_t stride, int rows, int width,
+                                           int a, int m, Piece<T>& v) {
+  // a chunk's rows lie within 2^31 bytes
+  const uint32_t at = (uint32_t)(4 * a) * (uint32_t)stride + 8 * m;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    typename Piece<T>::row x = {};
+    const T* row = base + r * stride;
+    if (4 * a + r < rows) {
+      if (8 * m + 8 <= width) {
+        x = load_pack<T, 8>(row + at).v;
+      } else if (8 * m < width) {
+        const int last = width - 1 - 8 * m;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const T e = row[at + min(c, last)];
+          x[c] = c <= last ? e : (T)0.0f;
+        }
+      }
+    }
+    v.v[r] = x;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void unpack_piece(const Piece<T>& v, float (&x)[4][8]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[r][c] = (float)v.v[r][c];
+}
+// Four of its values as N parts.
+template <int N, typename V>
+__device__ __forceinline__ void split_four(V x, bf4 (&p)[N]) {
+  if constexpr (N == 1) {
+    p[0] = __builtin_convertvector(x, bf4);
+  } else {
+    split4<N>(__builtin_convertvector(x, f4), p);
+  }
+}
+// As rows: blocks it * KT + kt, the columns being the terms.  As columns: blocks dt * 2 +
 // jt, the rows being the terms.
-template <int N, int KT>
-__device__ __forceinline__ void store_piece(const float (&v)[4][8], int a, int m, char* rows,
-                                            char* cols) {
+template <int N, int KT, typename T>
+__device__ __forceinline__ void store_piece(const Piece<T>& v, int a, int m, char* rows, char* cols) {
+  typedef T t4 __attribute__((ext_vector_type(4)));
   if (rows) {
     const int half = m % 4 / 2, g = m % 2 * 2;
-    char* at = rows + (a / 4 * KT + m / 4) * N * 1024 + half * 8;
+    char* at = rows + (a / 4 * KT + m / 4) * N * 1024 + half * 8 + (16 * g + a % 4 * 4) * 16;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int i = a % 4 * 4 + r;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const f4 x = {v[r][4 * k], v[r][4 * k + 1], v[r][4 * k + 2], v[r][4 * k + 3]};
+        const t4 x = {v.v[r][4 * k], v.v[r][4 * k + 1], v.v[r][4 * k + 2], v.v[r][4 * k + 3]};
         bf4 p[N];
-        split4<N>(x, p);
+        split_four<N>(x, p);
 #pragma unroll
         for (int q = 0; q < N; ++q)
-          *reinterpret_cast<bf4*>(at + q * 1024 + (16 * (g + k) + i) * 16) = p[q];
+          *reinterpret_cast<bf4*>(at + q * 1024 + (16 * k + r) * 16) = p[q];
       }
     }
   }
   if (cols) {
-    char* at = cols + (m / 2 * 2 + a / 8) * N * 1024 + a % 8 / 4 * 8;
+    char* at = cols + (m / 2 * 2 + a / 8) * N * 1024 + a % 8 / 4 * 8 + (16 * (a % 4) + m % 2 * 8) * 16;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const f4 x = {v[0][c], v[1][c], v[2][c], v[3][c]};
+      const t4 x = {v.v[0][c], v.v[1][c], v.v[2][c], v.v[3][c]};
       bf4 p[N];
-      split4<N>(x, p);
+      split_four<N>(x, p);
 #pragma unroll
-      for (int q = 0; q < N; ++q)
-        *reinterpret_cast<bf4*>(at + q * 1024 + (16 * (a % 4) + m % 2 * 8 + c) * 16) = p[q];
+      for (int q = 0; q < N; ++q) *reinterpret_cast<bf4*>(at + q * 1024 + c * 16) = p[q];
     }
   }
 }
-// The piece's values, 0 from row `rows` and from column `width` on.
-template <typename T>
-__device__ __forceinline__ void load_piece(const T* base, int64_t stride, int rows, int width,
-                                           int a, int m, float (&v)[4][8]) {
+// The same of f32 values.
+template <int N, int KT>
+__device__ __forceinline__ void store_piece(const float (&x)[4][8], int a, int m, char* rows) {
+  Piece<float> v;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const T* at = base + (4 * a + r) * stride + 8 * m;
-    if (4 * a + r < rows && 8 * m + 8 <= width) {
-      unpack<T, 8>(load_pack<T, 8>(at), v[r]);
-    } else {
+  for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        v[r][c] = 4 * a + r < rows && 8 * m + c < width ? (float)at[c] : 0.0f;
-    }
-  }
+    for (int c = 0; c < 8; ++c) v.v[r][c] = x[r][c];
+  store_piece<N, KT, float>(v, a, m, rows, nullptr);
 }
 // A chunk's rows as operand blocks, by all of a workgroup's threads.
 template <typename T, int KT>
 __device__ __forceinline__ void stage(const T* base, int64_t stride, int rows, int width, char* as_rows,
                                       char* as_cols) {
   for (int id = threadIdx.x; id < 64 * KT; id += blockDim.x) {
-    float v[4][8];
+    Piece<T> v;
     load_piece<T>(base, stride, rows, width, id / (4 * KT), id % (4 * KT), v);
-    store_piece<kParts<T>, KT>(v, id / (4 * KT), id % (4 * KT), as_rows, as_cols);
+    store_piece<kParts<T>, KT, T>(v, id / (4 * KT), id % (4 * KT), as_rows, as_cols);
   }
 }
 
@@ -207,11 +245,18 @@ size_t prep_bytes_of(int type, bool backward) {
 }
 
 __device__ __forceinline__ int steps_of(const DeltaArgs& a, int64_t b) {
-  return (int)(a.length ? min(max(a.length[b], (int64_t)0), a.T) : a.T);
+  return __builtin_amdgcn_readfirstlane(
+      (int)(a.length ? min(max(a.length[b], (int64_t)0), a.T) : a.T));
 }
 template <typename T>
 __device__ __forceinline__ const T* at(const Seq& s, int64_t b, int64_t t, int64_t h) {
   return static_cast<const T*>(s.p) + b * s.sb + t * s.st + h * s.sh;
+}
+
+// Quotient and rest of a workgroup's number, in scalar registers.
+__device__ __forceinline__ void divide(uint32_t x, uint32_t by, int& quotient, int& rest) {
+  quotient = __builtin_amdgcn_readfirstlane((int)(x / by));
+  rest = (int)(x - (uint32_t)quotient * by);
 }
 
 __device__ __forceinline__ float decay(const Decays& d, int i, int j) {
@@ -229,9 +274,10 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
   __shared__ Decays dec;
   const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int h = (int)(blockIdx.x % a.H);
-  const int64_t c = blockIdx.x / a.H % a.chunks, b = blockIdx.x / a.H / a.chunks;
-  const int64_t t0 = c * kC;
+  int b, c, h;
+  divide(blockIdx.x, (uint32_t)a.H, b, h);
+  divide((uint32_t)b, (uint32_t)a.chunks, b, c);
+  const int64_t t0 = (int64_t)c * kC;
   const int rows = min(kC, steps_of(a, b) - (int)t0);
   if (rows <= 0) return;
   char* out = static_cast<char*>(a.prep) + (int64_t)blockIdx.x * prep_bytes(NS);
@@ -378,423 +424,486 @@ __device__ __forceinline__ void copy16(char* to, const char* from, int bytes) {
     *reinterpret_cast<f4*>(to + i) = *reinterpret_cast<const f4*>(from + i);
 }
 
-// NT neighbouring values of a row, 0 past `width`.
-template <typename T, int NT>
-__device__ __forceinline__ void load_few(const T* row, int col, int width, float (&v)[NT]) {
-  if (col + NT <= width) {
-    unpack<T, NT>(load_pack<T, NT>(row + col), v);
+// W neighbouring values of a row, 0 past `width`.
+template <typename T, int W>
+__device__ __forceinline__ void load_few(const T* row, int col, int width, float (&v)[W]) {
+  if (col + W <= width) {
+    unpack<T, W>(load_pack<T, W>(row + col), v);
   } else {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) v[i] = col + i < width ? (float)row[col + i] : 0.0f;
+    for (int i = 0; i < W; ++i) v[i] = col + i < width ? (float)row[col + i] : 0.0f;
   }
 }
-template <typename T, int NT>
-__device__ __forceinline__ void store_few(T* row, int col, int width, const float (&v)[NT]) {
-  if (col + NT <= width) {
-    store_vals<T, NT>(row + col, v);
+template <typename T, int W>
+__device__ __forceinline__ void store_few(T* row, int col, int width, const float (&v)[W]) {
+  if (col + W <= width) {
+    store_vals<T, W>(row + col, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < W; ++i)
       if (col + i < width) row[col + i] = (T)v[i];
   }
 }
-// A wave's columns of a state [DK x DV], rows 16 dt + 4 g + r.
-template <int KT, int NT>
-__device__ __forceinline__ void load_state(const float* s, int DK, int DV, int col,
-                                           f4 (&v)[2 * KT][NT]) {
+
+// A wave's column of a matrix [. x width] for each lane n, as 16 x 16 results: rows 16 t +
+// 4 g + r of column col, from `rows` rows.  The rows' places are the same for the whole
+// wave but for 4 g, so they stay in scalar registers.
+template <typename T, int TILES>
+__device__ __forceinline__ void load_column(const T* base, int64_t stride, int rows, int col, int width,
+                                            T (&v)[TILES][4]) {
   const int g = (threadIdx.x & 63) / 16;
+  const uint32_t at = (uint32_t)(4 * g) * (uint32_t)stride + col;
+  const bool in = col < width;
+  // else the places of all rows are kept from chunk to chunk, and registers run out
+  asm volatile("" : "+s"(rows), "+s"(stride));
 #pragma unroll
-  for (int dt = 0; dt < 2 * KT; ++dt)
+  for (int t = 0; t < TILES; ++t)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * dt + 4 * g + r;
-      float x[NT] = {};
-      if (s && row < DK) load_few<float, NT>(s + (int64_t)row * DV, col, DV, x);
+    for (int r = 0; r < 4; ++r) v[t][r] = (T)0.0f;
+  if (rows >= 16 * TILES) {
+    if (in) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) v[dt][nt][r] = x[nt];
+      for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[t][r] = (base + (16 * t + r) * stride)[at];
     }
+  } else {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (in && 16 * t + 4 * g + r < rows) v[t][r] = (base + (16 * t + r) * stride)[at];
+  }
 }
-template <int KT, int NT>
-__device__ __forceinline__ void store_state(float* s, int DK, int DV, int col,
-                                            const f4 (&v)[2 * KT][NT]) {
+template <typename T, int TILES>
+__device__ __forceinline__ void store_column(T* base, int64_t stride, int rows, int col, int width,
+                                             const f4 (&v)[TILES]) {
   const int g = (threadIdx.x & 63) / 16;
+  const uint32_t at = (uint32_t)(4 * g) * (uint32_t)stride + col;
+  const bool in = col < width;
+  asm volatile("" : "+s"(rows), "+s"(stride));
+  if (rows >= 16 * TILES) {
+    if (in) {
 #pragma unroll
-  for (int dt = 0; dt < 2 * KT; ++dt)
+      for (int t = 0; t < TILES; ++t)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * dt + 4 * g + r;
-      float x[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt] = v[dt][nt][r];
-      if (row < DK) store_few<float, NT>(s + (int64_t)row * DV, col, DV, x);
+        for (int r = 0; r < 4; ++r) (base + (16 * t + r) * stride)[at] = (T)v[t][r];
     }
+  } else {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (in && 16 * t + 4 * g + r < rows) (base + (16 * t + r) * stride)[at] = (T)v[t][r];
+  }
 }
-// The chunk's rows of a wave's columns.
-template <int NT>
-__device__ __forceinline__ void store_rows(float* s, int DV, int col, const f4 (&v)[4][NT]) {
-  const int g = (threadIdx.x & 63) / 16;
+template <int TILES>
+__device__ __forceinline__ void load_state(const float* s, int DK, int DV, int col, f4 (&v)[TILES]) {
+  float x[TILES][4] = {};
+  if (s) load_column<float, TILES>(s, DV, DK, col, DV, x);
 #pragma unroll
-  for (int it = 0; it < 4; ++it)
+  for (int t = 0; t < TILES; ++t)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float x[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt] = v[it][nt][r];
-      store_few<float, NT>(s + (int64_t)(16 * it + 4 * g + r) * DV, col, DV, x);
-    }
+    for (int r = 0; r < 4; ++r) v[t][r] = x[t][r];
+}
+// The rows' values of a chunk, 4 neighbouring ones of each 16.
+__device__ __forceinline__ f4 rows_of(const float (&v)[kC], int it) {
+  return *reinterpret_cast<const f4*>(&v[16 * it + 4 * ((threadIdx.x & 63) / 16)]);
 }
 
 // A state that is not finite stays on its side of a reset: the rows of the chunk on
 // that side (`with`) give 0 to the other rows' sums, where 0 times them would not be 0.
 // Called where the chunk has a reset.
-template <int NT, typename F>
-__device__ __forceinline__ void keep_apart(f4 (&x)[4][NT], F with) {
+template <typename F>
+__device__ __forceinline__ void keep_apart(f4 (&x)[4], F with) {
   const int g = (threadIdx.x & 63) / 16;
+  float bad = 0.0f;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float bad = 0.0f;
+  for (int it = 0; it < 4; ++it)
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
+    for (int r = 0; r < 4; ++r)
+      if (with(16 * it + 4 * g + r) && !__builtin_isfinite(x[it][r])) bad = 1.0f;
+  bad = fmaxf(bad, xor_lanes(bad, 4));
+  bad = fmaxf(bad, xor_lanes(bad, 5));
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (with(16 * it + 4 * g + r) && !__builtin_isfinite(x[it][nt][r])) bad = 1.0f;
-    bad = fmaxf(bad, xor_lanes(bad, 4));
-    bad = fmaxf(bad, xor_lanes(bad, 5));
+  for (int it = 0; it < 4; ++it)
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (bad != 0.0f && with(16 * it + 4 * g + r)) x[it][nt][r] = 0.0f;
-  }
+    for (int r = 0; r < 4; ++r)
+      if (bad != 0.0f && with(16 * it + 4 * g + r)) x[it][r] = 0.0f;
 }
 
 constexpr int64_t carry_size(int DK, int DV) { return (int64_t)(DK + kC) * DV; }
 
-// A workgroup has a head of a sequence and 4 * 16 NT columns of its state, 16 NT to a
-// wave: lane 16 g + n the columns NT n .. NT n + NT - 1 of them.
-template <typename T, int KT, int NT>
-__global__ __launch_bounds__(256) void delta_forward_kernel(DeltaArgs a, int slices) {
+// What a workgroup of THREADS takes from memory for a chunk, held in registers while
+// the chunk before is computed: pieces of the keys and queries, and what is prepared.
+template <typename T, int KT, int THREADS, int BYTES>
+struct Ahead {
+  static constexpr int kPieces = (128 * KT + THREADS - 1) / THREADS;
+  static constexpr int kCopies = (BYTES / 16 + THREADS - 1) / THREADS;
+  Piece<T> piece[kPieces];
+  f4 copy[kCopies];
+
+  __device__ __forceinline__ void load(const DeltaArgs& a, int64_t b, int64_t t0, int hk, int rows,
+                                       const char* prep) {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      const int id = threadIdx.x + p * THREADS, at = id % (64 * KT);
+      const bool query = __builtin_amdgcn_readfirstlane(id / (64 * KT)) != 0;
+      const Seq& s = query ? a.q : a.k;
+      if (id < 128 * KT)
+        load_piece<T>(static_cast<const T*>(s.p) + b * s.sb + t0 * s.st + hk * s.sh, s.st, rows, a.DK,
+                      at / (4 * KT), at % (4 * KT), piece[p]);
+    }
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      const uint32_t at = (threadIdx.x + c * THREADS) * 16;
+      if (at < BYTES) copy[c] = *reinterpret_cast<const f4*>(prep + at);
+    }
+  }
+  // which: 1 keys, 2 queries, 3 both
+  __device__ __forceinline__ void store(char* krows, char* kcols, char* qrows, char* qcols, char* prep,
+                                        int which = 3) const {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      const int id = threadIdx.x + p * THREADS, at = id % (64 * KT);
+      const int query = __builtin_amdgcn_readfirstlane(id / (64 * KT));
+      if (query == 0) {
+        if (which & 1)
+          store_piece<kParts<T>, KT, T>(piece[p], at / (4 * KT), at % (4 * KT), krows, kcols);
+      } else if (query == 1 && (which & 2)) {
+        store_piece<kParts<T>, KT, T>(piece[p], at / (4 * KT), at % (4 * KT), qrows, qcols);
+      }
+    }
+    if (which & 1) {
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) {
+        const uint32_t at = (threadIdx.x + c * THREADS) * 16;
+        if (at < BYTES) *reinterpret_cast<f4*>(prep + at) = copy[c];
+      }
+    }
+  }
+};
+
+// A workgroup has a head of a sequence and 16 columns of its state for each of its waves.
+// While a chunk is computed the next one's operands are on their way in registers; they
+// go to a second place in LDS where there is room for one, so a chunk needs one barrier.
+template <typename T, int KT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void delta_forward_kernel(DeltaArgs a, int slices) {
   constexpr int N = kParts<T>, NO = kOutParts<T>, WEAK = kWeak<T>;
-  constexpr int kTile = 4 * KT * N * 1024;
-  constexpr bool kApart = N == 1;  // queries have a place of their own in LDS
-  __shared__ __attribute__((aligned(16))) char krows[kTile], kcols[kTile];
-  __shared__ __attribute__((aligned(16))) char qrows_[kApart ? kTile : 16];
-  __shared__ __attribute__((aligned(16))) char prep[prep_bytes(NO)];
-  char* qrows = kApart ? qrows_ : krows;
-  const Decays& dec = *reinterpret_cast<const Decays*>(prep);
-  const char* invs = prep + sizeof(Decays);
-  const char* scores = invs + 6 * kInvParts * 1024;
+  constexpr int kTile = 4 * KT * N * 1024, kPrep = (int)prep_bytes(NO);
+  constexpr bool kApart = N < 3;  // queries have a place of their own in LDS
+  constexpr int kRoom = (kApart ? 3 : 2) * kTile + kPrep;
+  constexpr bool kTwice = 2 * kRoom <= 160 * 1024;
+  __shared__ __attribute__((aligned(16))) char room[kTwice ? 2 : 1][kRoom];
 
   const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int slice = (int)(blockIdx.x % slices);
-  const int64_t bh = blockIdx.x / slices, b = bh / a.H;
-  const int h = (int)(bh % a.H), hk = h / (a.H / a.HK);
-  const int col = ((slice * 4 + wave) * 16 + n) * NT;
+  int bh, b, h, hk, slice, rest;
+  divide(blockIdx.x, (uint32_t)slices, bh, slice);
+  divide((uint32_t)bh, (uint32_t)a.H, b, h);
+  divide((uint32_t)h, (uint32_t)(a.H / a.HK), hk, rest);
+  const int col = (slice * WAVES + wave) * 16 + n;
   const int steps = steps_of(a, b);
+  const int64_t unit0 = (int64_t)b * a.chunks * a.H + h;  // the head's first chunk; others lie H apart
+  const T* vs = at<T>(a.v, b, 0, h);
+  T* os = const_cast<T*>(at<T>(a.o, b, 0, h));
 
-  f4 s[2 * KT][NT];
-  load_state<KT, NT>(a.s0 ? a.s0 + bh * a.DK * a.DV : nullptr, a.DK, a.DV, col, s);
-  for (int t0 = 0; t0 < steps; t0 += kC) {
-    const int rows = min(kC, steps - t0);
-    const int64_t unit = (b * a.chunks + t0 / kC) * a.H + h;
-    __syncthreads();
-    stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, krows, kcols);
-    if (kApart) stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, qrows, nullptr);
-    copy16(prep, static_cast<const char*>(a.prep) + unit * prep_bytes(NO), prep_bytes(NO));
-    float v[4][4][NT];
+  f4 s[2 * KT];
+  load_state<2 * KT>(a.s0 ? a.s0 + (int64_t)bh * a.DK * a.DV : nullptr, a.DK, a.DV, col, s);
+  Ahead<T, KT, 64 * WAVES, kPrep> ahead;
+  T v[4][4];
+  if (steps > 0) {
+    ahead.load(a, b, 0, hk, min(kC, steps), static_cast<const char*>(a.prep) + unit0 * kPrep);
+    load_column<T, 4>(vs, a.v.st, min(kC, steps), col, a.DV, v);
+    ahead.store(room[0], room[0] + kTile, room[0] + 2 * kTile, nullptr, room[0] + kRoom - kPrep,
+                kApart ? 3 : 1);
+  }
+  __syncthreads();
+  for (int t0 = 0, flip = 0; t0 < steps; t0 += kC) {
+    const int rows = min(kC, steps - t0), more = min(kC, steps - t0 - kC);
+    const int64_t unit = unit0 + t0 / kC * a.H;
+    char *krows = room[kTwice ? flip : 0], *kcols = krows + kTile;
+    char* qrows = kApart ? krows + 2 * kTile : krows;
+    const char* prep = krows + kRoom - kPrep;
+    const Decays& dec = *reinterpret_cast<const Decays*>(prep);
+    const char *invs = prep + sizeof(Decays), *scores = invs + 6 * kInvParts * 1024;
+    f4 r[4];  // V
 #pragma unroll
     for (int it = 0; it < 4; ++it)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * it + 4 * g + r;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) v[it][r][nt] = 0.0f;
-        if (i < rows) load_few<T, NT>(at<T>(a.v, b, t0 + i, h), col, a.DV, v[it][r]);
-      }
+      for (int i = 0; i < 4; ++i) r[it][i] = (float)v[it][i];
+    Ahead<T, KT, 64 * WAVES, kPrep> queries;
+    if constexpr (!kApart) queries = ahead;
+    if (more > 0) {
+      ahead.load(a, b, t0 + kC, hk, more, static_cast<const char*>(a.prep) + (unit + a.H) * kPrep);
+      load_column<T, 4>(vs + (int64_t)(t0 + kC) * a.v.st, a.v.st, more, col, a.DV, v);
+    }
     float* carry = a.carries ? a.carries + unit * carry_size(a.DK, a.DV) : nullptr;
-    if (carry) store_state<KT, NT>(carry, a.DK, a.DV, col, s);
-    __syncthreads();
+    if (carry) store_column<float, 2 * KT>(carry, a.DV, a.DK, col, a.DV, s);
 
     // K S and Q S
-    f4 x[4][NT] = {}, y[4][NT] = {};
+    f4 x[4] = {}, y[4] = {};
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
-      bf8 sp[NT][3];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) split<3>(s[2 * kt][nt], s[2 * kt + 1][nt], sp[nt]);
+      bf8 sp[3];
+      split<3>(s[2 * kt], s[2 * kt + 1], sp);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         bf8 p[N];
         load_block<N>(krows, it * KT + kt, p);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[it][nt] = mul<2>(p, sp[nt], x[it][nt]);
-        if (kApart) {
+        x[it] = mul<2>(p, sp, x[it]);
+        if constexpr (kApart) {
           load_block<N>(qrows, it * KT + kt, p);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) y[it][nt] = mul<WEAK>(p, sp[nt], y[it][nt]);
+          y[it] = mul<WEAK>(p, sp, y[it]);
         }
       }
     }
-    if (!kApart) {
+    if constexpr (!kApart) {
       __syncthreads();
-      stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, qrows, nullptr);
+      queries.store(nullptr, nullptr, qrows, nullptr, nullptr, 2);
       __syncthreads();
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        bf8 sp[NT][NO];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) split<NO>(s[2 * kt][nt], s[2 * kt + 1][nt], sp[nt]);
+        bf8 sp[3];
+        split<3>(s[2 * kt], s[2 * kt + 1], sp);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
           bf8 p[N];
           load_block<N>(qrows, it * KT + kt, p);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) y[it][nt] = mul<WEAK>(p, sp[nt], y[it][nt]);
+          y[it] = mul<WEAK>(p, sp, y[it]);
         }
       }
     }
     // w (V - gamma K S)
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
+    for (int it = 0; it < 4; ++it) {
+      const f4 first = rows_of(dec.first, it), w = rows_of(dec.w, it);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * it + 4 * g + r;
-        const float first = dec.first[i], w = dec.w[i];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float past = first < 0.0f ? 0.0f : first * x[it][nt][r];
-          x[it][nt][r] = w * (v[it][r][nt] - past);
-          y[it][nt][r] = first < 0.0f ? 0.0f : first * y[it][nt][r];
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float past = first[i] < 0.0f ? 0.0f : first[i] * x[it][i];
+        x[it][i] = w[i] * (r[it][i] - past);
+        y[it][i] = first[i] < 0.0f ? 0.0f : first[i] * y[it][i];
       }
-    if (dec.resets[kC - 1] > 0)
-      keep_apart<NT>(x, [&](int i) { return dec.first[i] >= 0.0f; });
+    }
+    if (dec.resets[kC - 1] > 0) keep_apart(x, [&](int i) { return dec.first[i] >= 0.0f; });
     // U
-    f4 u[4][NT] = {};
+    f4 u[4] = {};
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
-      bf8 xp[NT][3];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) split<3>(x[2 * kt][nt], x[2 * kt + 1][nt], xp[nt]);
+      bf8 xp[3];
+      split<3>(x[2 * kt], x[2 * kt + 1], xp);
 #pragma unroll
       for (int it = 2 * kt; it < 4; ++it) {
         bf8 p[kInvParts];
         load_block<kInvParts>(invs, lower_block(it, kt), p);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) u[it][nt] = mul<2>(p, xp[nt], u[it][nt]);
+        u[it] = mul<2>(p, xp, u[it]);
       }
     }
-    if (carry) store_rows<NT>(carry + (int64_t)a.DK * a.DV, a.DV, col, u);
+    if (carry) store_column<float, 4>(carry + (int64_t)a.DK * a.DV, a.DV, kC, col, a.DV, u);
     // the outputs
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
-      bf8 up[NT][NO];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) split<NO>(u[2 * kt][nt], u[2 * kt + 1][nt], up[nt]);
+      bf8 up[NO];
+      split<NO>(u[2 * kt], u[2 * kt + 1], up);
 #pragma unroll
       for (int it = 2 * kt; it < 4; ++it) {
         bf8 p[NO];
         load_block<NO>(scores, lower_block(it, kt), p);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) y[it][nt] = mul<WEAK>(p, up[nt], y[it][nt]);
+        y[it] = mul<WEAK>(p, up, y[it]);
       }
     }
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * it + 4 * g + r;
-        float o[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          o[nt] = a.scale * y[it][nt][r];
-          u[it][nt][r] *= dec.last[i];
-        }
-        if (i < rows) store_few<T, NT>(const_cast<T*>(at<T>(a.o, b, t0 + i, h)), col, a.DV, o);
-      }
+    for (int it = 0; it < 4; ++it) {
+      y[it] = y[it] * a.scale;
+      u[it] = u[it] * rows_of(dec.last, it);
+    }
+    store_column<T, 4>(os + (int64_t)t0 * a.o.st, a.o.st, rows, col, a.DV, y);
     // the state behind the chunk
     const float kept = dec.first[kC - 1];
 #pragma unroll
     for (int dt = 0; dt < 2 * KT; ++dt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s[dt][nt][r] = kept < 0.0f ? 0.0f : kept * s[dt][nt][r];
+      for (int i = 0; i < 4; ++i) s[dt][i] = kept < 0.0f ? 0.0f : kept * s[dt][i];
 #pragma unroll
     for (int jt = 0; jt < 2; ++jt) {
-      bf8 up[NT][3];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) split<3>(u[2 * jt][nt], u[2 * jt + 1][nt], up[nt]);
+      bf8 up[3];
+      split<3>(u[2 * jt], u[2 * jt + 1], up);
 #pragma unroll
       for (int dt = 0; dt < 2 * KT; ++dt) {
         bf8 p[N];
         load_block<N>(kcols, dt * 2 + jt, p);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[dt][nt] = mul<2>(p, up[nt], s[dt][nt]);
+        s[dt] = mul<2>(p, up, s[dt]);
       }
     }
+    if (more > 0) {
+      if (kTwice) {
+        flip ^= 1;
+      } else {
+        __syncthreads();
+      }
+      char* next = room[kTwice ? flip : 0];
+      ahead.store(next, next + kTile, next + 2 * kTile, nullptr, next + kRoom - kPrep, kApart ? 3 : 1);
+    }
+    __syncthreads();
   }
-  if (a.s_last) store_state<KT, NT>(a.s_last + bh * a.DK * a.DV, a.DK, a.DV, col, s);
-  const float zero[NT] = {};
-  for (int64_t t = steps + wave * 0 + g; t < a.T; t += 4)
-    store_few<T, NT>(const_cast<T*>(at<T>(a.o, b, t, h)), col, a.DV, zero);
+  if (a.s_last) store_column<float, 2 * KT>(a.s_last + (int64_t)bh * a.DK * a.DV, a.DV, a.DK, col, a.DV, s);
+  for (int64_t t = steps + g; t < a.T; t += 4)
+    if (col < a.DV) os[t * a.o.st + col] = (T)0.0f;
 }
 
 // Backward in time: dS behind each chunk, E, and dV.
-template <typename T, int KT, int NT>
-__global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int slices) {
+template <typename T, int KT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void delta_reverse_kernel(DeltaArgs a, int slices) {
   constexpr int N = kParts<T>;
-  constexpr int kTile = 4 * KT * N * 1024;
-  __shared__ __attribute__((aligned(16))) char krows[kTile], kcols[kTile];
-  __shared__ __attribute__((aligned(16))) char prep[prep_bytes(3)];
-  char* qcols = krows;
-  const Decays& dec = *reinterpret_cast<const Decays*>(prep);
-  const char* invs = prep + sizeof(Decays);
-  const char* scores = invs + 6 * kInvParts * 1024;
+  constexpr int kTile = 4 * KT * N * 1024, kPrep = (int)prep_bytes(3);
+  constexpr bool kApart = N < 3;
+  constexpr int kRoom = (kApart ? 3 : 2) * kTile + kPrep;
+  constexpr bool kTwice = 2 * kRoom <= 160 * 1024;
+  __shared__ __attribute__((aligned(16))) char room[kTwice ? 2 : 1][kRoom];
 
   const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int slice = (int)(blockIdx.x % slices);
-  const int64_t bh = blockIdx.x / slices, b = bh / a.H;
-  const int h = (int)(bh % a.H), hk = h / (a.H / a.HK);
-  const int col = ((slice * 4 + wave) * 16 + n) * NT;
+  int bh, b, h, hk, slice, rest;
+  divide(blockIdx.x, (uint32_t)slices, bh, slice);
+  divide((uint32_t)bh, (uint32_t)a.H, b, h);
+  divide((uint32_t)h, (uint32_t)(a.H / a.HK), hk, rest);
+  const int col = (slice * WAVES + wave) * 16 + n;
   const int steps = steps_of(a, b);
+  const int64_t unit0 = (int64_t)b * a.chunks * a.H + h;
+  const T* os = at<T>(a.o, b, 0, h);
+  T* dvs = const_cast<T*>(at<T>(a.dv, b, 0, h));
 
-  f4 s[2 * KT][NT];
-  load_state<KT, NT>(a.s0 ? a.s0 + bh * a.DK * a.DV : nullptr, a.DK, a.DV, col, s);
-  for (int t0 = (steps - 1) / kC * kC; steps > 0 && t0 >= 0; t0 -= kC) {
+  f4 s[2 * KT];
+  load_state<2 * KT>(a.s0 ? a.s0 + (int64_t)bh * a.DK * a.DV : nullptr, a.DK, a.DV, col, s);
+  Ahead<T, KT, 64 * WAVES, kPrep> ahead;
+  T d[4][4];  // dO
+  const int tail = steps > 0 ? (steps - 1) / kC * kC : -kC;  // the last chunk
+  if (steps > 0) {
+    ahead.load(a, b, tail, hk, steps - tail, static_cast<const char*>(a.prep) + (unit0 + tail / kC * a.H) * kPrep);
+    load_column<T, 4>(os + (int64_t)tail * a.o.st, a.o.st, steps - tail, col, a.DV, d);
+    ahead.store(room[0], room[0] + kTile, nullptr, room[0] + 2 * kTile, room[0] + kRoom - kPrep,
+                kApart ? 3 : 1);
+  }
+  __syncthreads();
+  for (int t0 = tail, flip = 0; t0 >= 0; t0 -= kC) {
     const int rows = min(kC, steps - t0);
-    const int64_t unit = (b * a.chunks + t0 / kC) * a.H + h;
-    __syncthreads();
-    stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, krows, kcols);
-    copy16(prep, static_cast<const char*>(a.prep) + unit * prep_bytes(3), prep_bytes(3));
-    float d[4][4][NT];  // dO
+    const int64_t unit = unit0 + t0 / kC * a.H;
+    char *krows = room[kTwice ? flip : 0], *kcols = krows + kTile;
+    char* qcols = kApart ? krows + 2 * kTile : krows;
+    const char* prep = krows + kRoom - kPrep;
+    const Decays& dec = *reinterpret_cast<const Decays*>(prep);
+    const char *invs = prep + sizeof(Decays), *scores = invs + 6 * kInvParts * 1024;
+    f4 o[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * it + 4 * g + r;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) d[it][r][nt] = 0.0f;
-        if (i < rows) load_few<T, NT>(at<T>(a.o, b, t0 + i, h), col, a.DV, d[it][r]);
-      }
-    store_state<KT, NT>(a.dstate + unit * a.DK * a.DV, a.DK, a.DV, col, s);
-    __syncthreads();
+      for (int i = 0; i < 4; ++i) o[it][i] = (float)d[it][i];
+    Ahead<T, KT, 64 * WAVES, kPrep> queries;
+    if constexpr (!kApart) queries = ahead;
+    if (t0 > 0) {
+      ahead.load(a, b, t0 - kC, hk, kC, static_cast<const char*>(a.prep) + (unit - a.H) * kPrep);
+      load_column<T, 4>(os + (int64_t)(t0 - kC) * a.o.st, a.o.st, kC, col, a.DV, d);
+    }
+    store_column<float, 2 * KT>(a.dstate + unit * a.DK * a.DV, a.DV, a.DK, col, a.DV, s);
 
     // d K dS + scale P^T dO
-    f4 x[4][NT] = {}, y[4][NT] = {};
+    f4 x[4] = {}, y[4] = {};
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
-      bf8 sp[NT][3];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) split<3>(s[2 * kt][nt], s[2 * kt + 1][nt], sp[nt]);
+      bf8 sp[3];
+      split<3>(s[2 * kt], s[2 * kt + 1], sp);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         bf8 p[N];
         load_block<N>(krows, it * KT + kt, p);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[it][nt] = mul<2>(p, sp[nt], x[it][nt]);
+        x[it] = mul<2>(p, sp, x[it]);
       }
     }
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
-      bf8 dp[NT][N];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        f4 lo, hi;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) lo[r] = d[2 * kt][r][nt], hi[r] = d[2 * kt + 1][r][nt];
-        split<N>(lo, hi, dp[nt]);
-      }
+      bf8 op[N];
+      split<N>(o[2 * kt], o[2 * kt + 1], op);
 #pragma unroll
       for (int jt = 0; jt < 2 * kt + 2; ++jt) {
         bf8 p[3];
         load_block<3>(scores, upper_block(jt, kt), p);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) y[jt][nt] = mul<2>(p, dp[nt], y[jt][nt]);
+        y[jt] = mul<2>(p, op, y[jt]);
       }
     }
-    __syncthreads();  // the keys' rows make room for the queries
-    stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, nullptr, qcols);
+    if constexpr (!kApart) {
+      __syncthreads();  // the keys' rows make room for the queries
+      queries.store(nullptr, nullptr, nullptr, qcols, nullptr, 2);
+    }
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
+    for (int it = 0; it < 4; ++it) {
+      const f4 last = rows_of(dec.last, it);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float last = dec.last[16 * it + 4 * g + r];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          x[it][nt][r] = (last != 0.0f ? last * x[it][nt][r] : 0.0f) + a.scale * y[it][nt][r];
-      }
+      for (int i = 0; i < 4; ++i)
+        x[it][i] = (last[i] != 0.0f ? last[i] * x[it][i] : 0.0f) + a.scale * y[it][i];
+    }
     if (dec.resets[kC - 1] > 0)
-      keep_apart<NT>(x, [&](int i) { return dec.resets[i] == dec.resets[kC - 1]; });
+      keep_apart(x, [&](int i) { return dec.resets[i] == dec.resets[kC - 1]; });
     // E
-    f4 e[4][NT] = {};
+    f4 e[4] = {};
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
-      bf8 xp[NT][3];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) split<3>(x[2 * kt][nt], x[2 * kt + 1][nt], xp[nt]);
+      bf8 xp[3];
+      split<3>(x[2 * kt], x[2 * kt + 1], xp);
 #pragma unroll
       for (int jt = 0; jt < 2 * kt + 2; ++jt) {
         bf8 p[kInvParts];
         load_block<kInvParts>(invs, upper_block(jt, kt), p);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) e[jt][nt] = mul<2>(p, xp[nt], e[jt][nt]);
+        e[jt] = mul<2>(p, xp, e[jt]);
       }
     }
-    store_rows<NT>(a.e + unit * kC * a.DV, a.DV, col, e);
+    store_column<float, 4>(a.e + unit * kC * a.DV, a.DV, kC, col, a.DV, e);
     // dV, then what goes back to the state before the chunk
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
+    for (int it = 0; it < 4; ++it) {
+      const f4 first = rows_of(dec.first, it);
+      e[it] = e[it] * rows_of(dec.w, it);
+      y[it] = e[it];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * it + 4 * g + r;
-        const float first = dec.first[i], w = dec.w[i];
-        float o[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          o[nt] = w * e[it][nt][r];
-          e[it][nt][r] = first < 0.0f ? 0.0f : -first * o[nt];
-          d[it][r][nt] = first < 0.0f ? 0.0f : a.scale * first * d[it][r][nt];
-        }
-        if (i < rows) store_few<T, NT>(const_cast<T*>(at<T>(a.dv, b, t0 + i, h)), col, a.DV, o);
+      for (int i = 0; i < 4; ++i) {
+        e[it][i] = first[i] < 0.0f ? 0.0f : -first[i] * e[it][i];
+        o[it][i] = first[i] < 0.0f ? 0.0f : a.scale * first[i] * o[it][i];
       }
-    __syncthreads();
+    }
+    store_column<T, 4>(dvs + (int64_t)t0 * a.dv.st, a.dv.st, rows, col, a.DV, y);
+    if constexpr (!kApart) __syncthreads();
     const float kept = dec.first[kC - 1];
 #pragma unroll
     for (int dt = 0; dt < 2 * KT; ++dt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s[dt][nt][r] = kept < 0.0f ? 0.0f : kept * s[dt][nt][r];
+      for (int i = 0; i < 4; ++i) s[dt][i] = kept < 0.0f ? 0.0f : kept * s[dt][i];
 #pragma unroll
     for (int jt = 0; jt < 2; ++jt) {
-      bf8 ep[NT][3], dp[NT][3];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        split<3>(e[2 * jt][nt], e[2 * jt + 1][nt], ep[nt]);
-        f4 lo, hi;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) lo[r] = d[2 * jt][r][nt], hi[r] = d[2 * jt + 1][r][nt];
-        split<3>(lo, hi, dp[nt]);
-      }
+      bf8 ep[3], op[3];
+      split<3>(e[2 * jt], e[2 * jt + 1], ep);
+      split<3>(o[2 * jt], o[2 * jt + 1], op);
 #pragma unroll
       for (int dt = 0; dt < 2 * KT; ++dt) {
         bf8 p[N];
         load_block<N>(kcols, dt * 2 + jt, p);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[dt][nt] = mul<2>(p, ep[nt], s[dt][nt]);
+        s[dt] = mul<2>(p, ep, s[dt]);
         load_block<N>(qcols, dt * 2 + jt, p);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[dt][nt] = mul<2>(p, dp[nt], s[dt][nt]);
+        s[dt] = mul<2>(p, op, s[dt]);
       }
     }
+    if (t0 > 0) {
+      if (kTwice) {
+        flip ^= 1;
+      } else {
+        __syncthreads();
+      }
+      char* next = room[kTwice ? flip : 0];
+      ahead.store(next, next + kTile, nullptr, next + 2 * kTile, next + kRoom - kPrep, kApart ? 3 : 1);
+    }
+    __syncthreads();
   }
-  if (a.s_last) store_state<KT, NT>(a.s_last + bh * a.DK * a.DV, a.DK, a.DV, col, s);
-  const float zero[NT] = {};
+  if (a.s_last) store_column<float, 2 * KT>(a.s_last + (int64_t)bh * a.DK * a.DV, a.DV, a.DK, col, a.DV, s);
   for (int64_t t = steps + g; t < a.T; t += 4)
-    store_few<T, NT>(const_cast<T*>(at<T>(a.dv, b, t, h)), col, a.DV, zero);
+    if (col < a.DV) dvs[t * a.dv.st + col] = (T)0.0f;
 }
 
 // dQ, dK and the gradients of gates and strengths, for each (sequence, chunk, head of
@@ -815,15 +924,15 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
   char *da = space, *dt_ = da + 6 * NO * 1024, *mm = dt_ + 6 * NO * 1024;
   char *kcols = kcols_, *qcols = kApart ? qcols_ : kcols_;
 
-  const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int hk = (int)(blockIdx.x % a.HK), shared = a.H / a.HK;
-  const int64_t c = blockIdx.x / a.HK % a.chunks, b = blockIdx.x / a.HK / a.chunks;
-  const int64_t t0 = c * kC;
+  int b, c, hk;
+  divide(blockIdx.x, (uint32_t)a.HK, b, hk);
+  divide((uint32_t)b, (uint32_t)a.chunks, b, c);
+  const int shared = a.H / a.HK;
+  const int64_t t0 = (int64_t)c * kC;
   const int steps = steps_of(a, b), rows = min(kC, steps - (int)t0);
   const int here = (int)min((int64_t)kC, a.T - t0);  // rows that are written
   const int dt = wave % kDt, i0 = wave / kDt * NI;
-  const int dcol = 16 * dt + n;
   f4 dq[NI] = {}, dk[NI] = {};
 
   if (rows > 0) {
@@ -833,7 +942,7 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
       asm volatile("" : "+v"(lane));
       const int g = lane / 16, n = lane % 16, dcol = 16 * dt + n;
       const int h = hk * shared + gi;
-      const int64_t unit = (b * a.chunks + c) * a.H + h;
+      const int64_t unit = ((int64_t)b * a.chunks + c) * a.H + h;
       const float* s0 = a.carries + unit * carry_size(a.DK, a.DV);
       const float* u = s0 + (int64_t)a.DK * a.DV;
       const float* ds = a.dstate + unit * a.DK * a.DV;
@@ -854,19 +963,26 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
         {
           // 128 threads each: U; dO; G and the sums E.U; the sums G.V
           const int pa = wave % 2 * 8 + lane / 8, pm = lane % 8, job = wave / 2;
-          float x[4][8], y[4][8];
           if (job == 0) {
+            Piece<float> x;
             load_piece<float>(u + v0, a.DV, kC, width, pa, pm, x);
-            store_piece<NO, 2>(x, pa, pm, us, nullptr);
+            store_piece<NO, 2, float>(x, pa, pm, us, nullptr);
           } else if (job == 1) {
+            Piece<T> x;
             load_piece<T>(at<T>(a.o, b, t0, h) + v0, a.o.st, rows, width, pa, pm, x);
-            store_piece<N, 2>(x, pa, pm, dos, nullptr);
+            store_piece<N, 2, T>(x, pa, pm, dos, nullptr);
           } else {
-            load_piece<float>(e + v0, a.DV, kC, width, pa, pm, x);
+            Piece<float> p;
+            float x[4][8], y[4][8];
+            load_piece<float>(e + v0, a.DV, kC, width, pa, pm, p);
+            unpack_piece<float>(p, x);
             if (job == 2) {
-              load_piece<float>(u + v0, a.DV, kC, width, pa, pm, y);
+              load_piece<float>(u + v0, a.DV, kC, width, pa, pm, p);
+              unpack_piece<float>(p, y);
             } else {
-              load_piece<T>(at<T>(a.v, b, t0, h) + v0, a.v.st, rows, width, pa, pm, y);
+              Piece<T> q;
+              load_piece<T>(at<T>(a.v, b, t0, h) + v0, a.v.st, rows, width, pa, pm, q);
+              unpack_piece<T>(q, y);
             }
             float sum[4];
 #pragma unroll
@@ -883,7 +999,7 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
               for (int q = 0; q < 3; ++q) sum[r] += xor_lanes(sum[r], q);
               if (pm == 0) (job == 2 ? eu : gv)[4 * pa + r] += sum[r];
             }
-            if (job == 2) store_piece<NO, 2>(x, pa, pm, gs, nullptr);
+            if (job == 2) store_piece<NO, 2>(x, pa, pm, gs);
           }
         }
         __syncthreads();
@@ -936,6 +1052,7 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
           split<NO>(y[0], y[1], yp);
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
             bf8 od[N], ou[NO], og[NO];
             load_block<N>(dos, (i0 + i) * 2 + kt, od, lane);
             load_block<NO>(us, (i0 + i) * 2 + kt, ou, lane);
@@ -1113,6 +1230,9 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
       *const_cast<T*>(at<T>(a.db, b, t, h)) = (T)0.0f;
     }
   }
+  int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // the places of dQ and dK are computed here, not before the loop
+  const int g = lane / 16, dcol = 16 * dt + lane % 16;
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -1130,9 +1250,10 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
 __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, int type, int slices) {
   __shared__ float sum[2][8][128];
   __shared__ float ks[PER_DELTA_MAX_DK], qs[PER_DELTA_MAX_DK];
-  const int slice = (int)(blockIdx.x % slices);
-  const int64_t bh = blockIdx.x / slices, b = bh / a.H;
-  const int h = (int)(bh % a.H), hk = h / (a.H / a.HK);
+  int bh, b, h, hk, slice, rest;
+  divide(blockIdx.x, (uint32_t)slices, bh, slice);
+  divide((uint32_t)bh, (uint32_t)a.H, b, h);
+  divide((uint32_t)h, (uint32_t)(a.H / a.HK), hk, rest);
   const int part = threadIdx.x / 32, cl = threadIdx.x % 32 * 4, col = slice * 128 + cl;
   auto value = [&](const Seq& s, int64_t head, int i) {
     const int64_t off = b * s.sb + head * s.sh + i;
@@ -1140,7 +1261,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, int type, 
            : type == PER_BF16 ? (float)static_cast<const bf16_t*>(s.p)[off]
                               : (float)static_cast<const f16_t*>(s.p)[off];
   };
-  const float* s = a.s0 + bh * a.DK * a.DV;
+  const float* s = a.s0 + (int64_t)bh * a.DK * a.DV;
   float v[16][4];
   const bool reset = a.reset && a.reset[b];
 #pragma unroll
@@ -1180,7 +1301,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, int type, 
     for (int p = 0; p < 8; ++p) x += sum[0][p][cl + i];
     u[i] = col + i < a.DV ? w * (value(a.v, h, col + i) - x) : 0.0f;
   }
-  float* to = a.s_last + bh * a.DK * a.DV;
+  float* to = a.s_last + (int64_t)bh * a.DK * a.DV;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     const int row = part * 16 + r;
@@ -1259,16 +1380,31 @@ size_t delta_workspace(int64_t B, int64_t T, int64_t H, int64_t DK, int64_t DV, 
   return prep + state + rows;
 }
 
+// Waves of a workgroup, 16 columns of the state each: up to 128 columns, or 64 where the
+// states are few and twice as many workgroups find a place, or where 8 waves' registers
+// do not hold what a chunk takes (128 keys of more than one part).
+static int column_waves(const DeltaArgs& a, int type) {
+  if (type != PER_BF16 && a.DK > 64) return 4;
+  return a.DV <= 64 || a.B * a.H * ((a.DV + 127) / 128) <= 128 ? 4 : 8;
+}
+template <typename T, int KT>
+struct Columns {
+  static constexpr int most = kParts<T> > 1 && KT == 4 ? 4 : 8;
+  static constexpr auto forward4 = delta_forward_kernel<T, KT, 4>;
+  static constexpr auto forward8 = delta_forward_kernel<T, KT, most>;
+  static constexpr auto reverse4 = delta_reverse_kernel<T, KT, 4>;
+  static constexpr auto reverse8 = delta_reverse_kernel<T, KT, most>;
+};
+
 hipError_t launch_delta_forward(const DeltaArgs& a, int type, hipStream_t s) {
   hipError_t e = a.chunks > 0 ? launch_prepare(a, type, false, s) : hipSuccess;
   if (e != hipSuccess) return e;
+  const int waves = column_waves(a, type), slices = (a.DV + 16 * waves - 1) / (16 * waves);
   return by_type(type, [&](auto tag) {
     return by_keys(a.DK, [&](auto keys) {
-      using T = typename decltype(tag)::type;
-      constexpr int KT = decltype(keys)::value;
-      const int slices = (a.DV + 63) / 64;
-      return enqueue(delta_forward_kernel<T, KT, 1>, dim3((uint32_t)(a.B * a.H * slices)), dim3(256),
-                     0, s, a, slices);
+      using K = Columns<typename decltype(tag)::type, decltype(keys)::value>;
+      return enqueue(waves == 4 ? K::forward4 : K::forward8, dim3((uint32_t)(a.B * a.H * slices)),
+                     dim3(64 * waves), 0, s, a, slices);
     });
   });
 }
@@ -1276,13 +1412,15 @@ hipError_t launch_delta_forward(const DeltaArgs& a, int type, hipStream_t s) {
 hipError_t launch_delta_backward(const DeltaArgs& a, int type, hipStream_t s) {
   hipError_t e = a.chunks > 0 ? launch_prepare(a, type, true, s) : hipSuccess;
   if (e != hipSuccess) return e;
+  const int waves = column_waves(a, type), slices = (a.DV + 16 * waves - 1) / (16 * waves);
   return by_type(type, [&](auto tag) {
     return by_keys(a.DK, [&](auto keys) {
       using T = typename decltype(tag)::type;
       constexpr int KT = decltype(keys)::value;
-      const int slices = (a.DV + 63) / 64;
-      const hipError_t e = enqueue(delta_reverse_kernel<T, KT, 1>,
-                                   dim3((uint32_t)(a.B * a.H * slices)), dim3(256), 0, s, a, slices);
+      using K = Columns<T, KT>;
+      const hipError_t e = enqueue(waves == 4 ? K::reverse4 : K::reverse8,
+                                   dim3((uint32_t)(a.B * a.H * slices)), dim3(64 * waves), 0, s, a,
+                                   slices);
       if (e != hipSuccess || a.chunks == 0) return e;
       return enqueue(delta_gradient_kernel<T, KT>, dim3((uint32_t)(a.B * a.chunks * a.HK)), dim3(512),
                      0, s, a);
