@@ -94,6 +94,19 @@ __device__ __forceinline__ f4 mul(const bf8 (&a)[NA], const bf8 (&b)[NB], f4 c) 
   return c;
 }
 
+// The same for several a: the products of one sum lie COUNT instructions apart.
+template <int WEAK, int COUNT, int NA, int NB>
+__device__ __forceinline__ void mul_each(const bf8 (&a)[COUNT][NA], const bf8 (&b)[NB], f4* c) {
+#pragma unroll
+  for (int s = WEAK; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k)
+          c[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[k][i], b[s - i], c[k], 0, 0, 0);
+}
+
 // Operand blocks in LDS or memory: block n of N parts, 64 lanes of 16 bytes each.
 template <int N>
 __device__ __forceinline__ void load_block(const char* blocks, int n, bf8 (&p)[N],
@@ -226,7 +239,7 @@ __device__ __forceinline__ void stage(const T* base, int64_t stride, int rows, i
 // What is prepared for each (sequence, chunk, head): the decays and writing strengths,
 // then operand blocks: (I + A)^-1 and Q K^T . D (forward), or the transposes of both.
 struct Decays {
-  double log[kC];   // of the gates up to a step
+  double log[kC];   // base 2, of the gates up to a step; 2^12 less behind each reset
   float first[kC];  // gamma; -1 behind a reset
   float last[kC];   // d
   float w[kC];
@@ -259,8 +272,9 @@ __device__ __forceinline__ void divide(uint32_t x, uint32_t by, int& quotient, i
   rest = (int)(x - (uint32_t)quotient * by);
 }
 
+// Of the gates of steps j + 1 to i, 0 across a reset.
 __device__ __forceinline__ float decay(const Decays& d, int i, int j) {
-  return d.resets[i] == d.resets[j] ? expf((float)(d.log[i] - d.log[j])) : 0.0f;
+  return __builtin_amdgcn_exp2f((float)(d.log[i] - d.log[j]));
 }
 
 // One workgroup of 4 waves for each (sequence, chunk, head).
@@ -289,9 +303,10 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     const float gate = on ? (float)*at<T>(a.g, b, t0 + lane, h) : 0.0f;
     const float wt = on ? (float)*at<T>(a.b, b, t0 + lane, h) : 0.0f;
     const bool reset = on && a.reset && a.reset[b * a.T + t0 + lane];
-    // log f; a gate below 2^-200 is 0 in f32 whatever it is
+    // log f; a gate below 2^-256 is 0 in f32 whatever it is
     const float lf = fminf(gate, 0.0f) - log1pf(expf(-fabsf(gate)));
-    double log = on && !reset ? (double)(lf < -200.0f ? -200.0f : lf) : 0.0;
+    double log = reset ? -4096.0 : on ? fmax((double)lf * 1.4426950408889634074, -256.0) : 0.0;
+    if (lf != lf && !reset) log = (double)lf;
     int resets = reset;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -301,11 +316,10 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
       resets += lane >= d ? r : 0;
     }
     const double end = __shfl(log, 63);
-    const int all = __shfl(resets, 63);
     dec.log[lane] = log;
     dec.resets[lane] = resets;
-    dec.first[lane] = resets == 0 ? expf((float)log) : -1.0f;
-    dec.last[lane] = resets == all ? expf((float)(end - log)) : 0.0f;
+    dec.first[lane] = resets == 0 ? __builtin_amdgcn_exp2f((float)log) : -1.0f;
+    dec.last[lane] = __builtin_amdgcn_exp2f((float)(end - log));
     dec.w[lane] = on ? 1.0f / (1.0f + expf(-wt)) : 0.0f;
   }
   for (int i = threadIdx.x; i < kC * kPad; i += 256) (&inv[0][0])[i] = 0.0f;
@@ -326,15 +340,20 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
         load_block<N>(ks, it * KT + kt, ki);
         load_block<N>(ks, jt * KT + kt, kj);
         load_block<N>(qs, it * KT + kt, qi);
-        kk = mul<2>(ki, kj, kk);  // rows of it, columns of jt
-        qk = BACKWARD ? mul<2>(qi, kj, qk) : mul<2>(kj, qi, qk);
+        if (BACKWARD) {  // rows of it, columns of jt
+          kk = mul<2>(ki, kj, kk);
+          qk = mul<2>(qi, kj, qk);
+        } else {
+          kk = mul<2>(kj, ki, kk);
+          qk = mul<2>(kj, qi, qk);
+        }
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * it + 4 * g + r, j = 16 * jt + n;
-        lower[i][j] = j < i ? dec.w[i] * decay(dec, i, j) * kk[r] : 0.0f;
-        const int si = BACKWARD ? i : 16 * it + n, sj = BACKWARD ? j : 16 * jt + 4 * g + r;
-        qk[r] = sj <= si ? decay(dec, si, sj) * qk[r] : 0.0f;
+        const int i = 16 * it + (BACKWARD ? 4 * g + r : n), j = 16 * jt + (BACKWARD ? n : 4 * g + r);
+        const float d = decay(dec, i, j);
+        lower[i][j] = j < i ? dec.w[i] * d * kk[r] : 0.0f;
+        qk[r] = j <= i ? d * qk[r] : 0.0f;
       }
     }
     if (BACKWARD) {  // rows of it are the terms of a row of jt
@@ -588,11 +607,13 @@ struct Ahead {
 // While a chunk is computed the next one's operands are on their way in registers; they
 // go to a second place in LDS where there is room for one, so a chunk needs one barrier.
 template <typename T, int KT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void delta_forward_kernel(DeltaArgs a, int slices) {
+__global__ __launch_bounds__(64 * WAVES)
+__attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_forward_kernel(DeltaArgs a, int slices) {
   constexpr int N = kParts<T>, NO = kOutParts<T>, WEAK = kWeak<T>;
   constexpr int kTile = 4 * KT * N * 1024, kPrep = (int)prep_bytes(NO);
   constexpr bool kApart = N < 3;  // queries have a place of their own in LDS
   constexpr int kRoom = (kApart ? 3 : 2) * kTile + kPrep;
+  constexpr int kSome = WAVES == 8 || KT == 1 ? 2 : 4;  // blocks that are held at a time
   constexpr bool kTwice = 2 * kRoom <= 160 * 1024;
   __shared__ __attribute__((aligned(16))) char room[kTwice ? 2 : 1][kRoom];
 
@@ -645,18 +666,15 @@ __global__ __launch_bounds__(64 * WAVES) void delta_forward_kernel(DeltaArgs a, 
     f4 x[4] = {}, y[4] = {};
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
-      bf8 sp[3];
-      split<3>(s[2 * kt], s[2 * kt + 1], sp);
+      bf8 sp[3], kp[4][N], qp[4][N];
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        bf8 p[N];
-        load_block<N>(krows, it * KT + kt, p);
-        x[it] = mul<2>(p, sp, x[it]);
-        if constexpr (kApart) {
-          load_block<N>(qrows, it * KT + kt, p);
-          y[it] = mul<WEAK>(p, sp, y[it]);
-        }
+        load_block<N>(krows, it * KT + kt, kp[it]);
+        if constexpr (kApart) load_block<N>(qrows, it * KT + kt, qp[it]);
       }
+      split<3>(s[2 * kt], s[2 * kt + 1], sp);
+      mul_each<2>(kp, sp, x);
+      if constexpr (kApart) mul_each<WEAK>(qp, sp, y);
     }
     if constexpr (!kApart) {
       __syncthreads();
@@ -664,14 +682,11 @@ __global__ __launch_bounds__(64 * WAVES) void delta_forward_kernel(DeltaArgs a, 
       __syncthreads();
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        bf8 sp[3];
-        split<3>(s[2 * kt], s[2 * kt + 1], sp);
+        bf8 sp[3], qp[4][N];
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          bf8 p[N];
-          load_block<N>(qrows, it * KT + kt, p);
-          y[it] = mul<WEAK>(p, sp, y[it]);
-        }
+        for (int it = 0; it < 4; ++it) load_block<N>(qrows, it * KT + kt, qp[it]);
+        split<3>(s[2 * kt], s[2 * kt + 1], sp);
+        mul_each<WEAK>(qp, sp, y);
       }
     }
     // w (V - gamma K S)
@@ -688,29 +703,33 @@ __global__ __launch_bounds__(64 * WAVES) void delta_forward_kernel(DeltaArgs a, 
     if (dec.resets[kC - 1] > 0) keep_apart(x, [&](int i) { return dec.first[i] >= 0.0f; });
     // U
     f4 u[4] = {};
+    {
+      bf8 xp[3], p[kSome][kInvParts], q[2][kInvParts];
+      split<3>(x[0], x[1], xp);
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      bf8 xp[3];
-      split<3>(x[2 * kt], x[2 * kt + 1], xp);
+      for (int i0 = 0; i0 < 4; i0 += kSome) {
 #pragma unroll
-      for (int it = 2 * kt; it < 4; ++it) {
-        bf8 p[kInvParts];
-        load_block<kInvParts>(invs, lower_block(it, kt), p);
-        u[it] = mul<2>(p, xp, u[it]);
+        for (int i = 0; i < kSome; ++i) load_block<kInvParts>(invs, lower_block(i0 + i, 0), p[i]);
+        mul_each<2>(p, xp, u + i0);
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) load_block<kInvParts>(invs, lower_block(i + 2, 1), q[i]);
+      split<3>(x[2], x[3], xp);
+      mul_each<2>(q, xp, u + 2);
     }
     if (carry) store_column<float, 4>(carry + (int64_t)a.DK * a.DV, a.DV, kC, col, a.DV, u);
     // the outputs
+    {
+      bf8 p[4][NO], up[NO];
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      bf8 up[NO];
-      split<NO>(u[2 * kt], u[2 * kt + 1], up);
+      for (int it = 0; it < 4; ++it) load_block<NO>(scores, lower_block(it, 0), p[it]);
+      split<NO>(u[0], u[1], up);
+      mul_each<WEAK>(p, up, y);
+      bf8 q[2][NO];
 #pragma unroll
-      for (int it = 2 * kt; it < 4; ++it) {
-        bf8 p[NO];
-        load_block<NO>(scores, lower_block(it, kt), p);
-        y[it] = mul<WEAK>(p, up, y[it]);
-      }
+      for (int it = 0; it < 2; ++it) load_block<NO>(scores, lower_block(it + 2, 1), q[it]);
+      split<NO>(u[2], u[3], up);
+      mul_each<WEAK>(q, up, y + 2);
     }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
@@ -729,10 +748,11 @@ __global__ __launch_bounds__(64 * WAVES) void delta_forward_kernel(DeltaArgs a, 
       bf8 up[3];
       split<3>(u[2 * jt], u[2 * jt + 1], up);
 #pragma unroll
-      for (int dt = 0; dt < 2 * KT; ++dt) {
-        bf8 p[N];
-        load_block<N>(kcols, dt * 2 + jt, p);
-        s[dt] = mul<2>(p, up, s[dt]);
+      for (int d0 = 0; d0 < 2 * KT; d0 += kSome) {
+        bf8 p[kSome][N];
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) load_block<N>(kcols, (d0 + i) * 2 + jt, p[i]);
+        mul_each<2>(p, up, s + d0);
       }
     }
     if (more > 0) {
@@ -753,11 +773,13 @@ __global__ __launch_bounds__(64 * WAVES) void delta_forward_kernel(DeltaArgs a, 
 
 // Backward in time: dS behind each chunk, E, and dV.
 template <typename T, int KT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void delta_reverse_kernel(DeltaArgs a, int slices) {
+__global__ __launch_bounds__(64 * WAVES)
+__attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_reverse_kernel(DeltaArgs a, int slices) {
   constexpr int N = kParts<T>;
   constexpr int kTile = 4 * KT * N * 1024, kPrep = (int)prep_bytes(3);
   constexpr bool kApart = N < 3;
   constexpr int kRoom = (kApart ? 3 : 2) * kTile + kPrep;
+  constexpr int kSome = WAVES == 8 || KT == 1 ? 2 : 4;  // blocks that are held at a time
   constexpr bool kTwice = 2 * kRoom <= 160 * 1024;
   __shared__ __attribute__((aligned(16))) char room[kTwice ? 2 : 1][kRoom];
 
@@ -810,24 +832,24 @@ __global__ __launch_bounds__(64 * WAVES) void delta_reverse_kernel(DeltaArgs a, 
     f4 x[4] = {}, y[4] = {};
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
-      bf8 sp[3];
+      bf8 sp[3], kp[4][N];
+#pragma unroll
+      for (int it = 0; it < 4; ++it) load_block<N>(krows, it * KT + kt, kp[it]);
       split<3>(s[2 * kt], s[2 * kt + 1], sp);
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        bf8 p[N];
-        load_block<N>(krows, it * KT + kt, p);
-        x[it] = mul<2>(p, sp, x[it]);
-      }
+      mul_each<2>(kp, sp, x);
     }
+    {
+      bf8 p[2][3], q[kSome][3], op[N];
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      bf8 op[N];
-      split<N>(o[2 * kt], o[2 * kt + 1], op);
+      for (int jt = 0; jt < 2; ++jt) load_block<3>(scores, upper_block(jt, 0), p[jt]);
+      split<N>(o[0], o[1], op);
+      mul_each<2>(p, op, y);
+      split<N>(o[2], o[3], op);
 #pragma unroll
-      for (int jt = 0; jt < 2 * kt + 2; ++jt) {
-        bf8 p[3];
-        load_block<3>(scores, upper_block(jt, kt), p);
-        y[jt] = mul<2>(p, op, y[jt]);
+      for (int j0 = 0; j0 < 4; j0 += kSome) {
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) load_block<3>(scores, upper_block(j0 + i, 1), q[i]);
+        mul_each<2>(q, op, y + j0);
       }
     }
     if constexpr (!kApart) {
@@ -845,15 +867,18 @@ __global__ __launch_bounds__(64 * WAVES) void delta_reverse_kernel(DeltaArgs a, 
       keep_apart(x, [&](int i) { return dec.resets[i] == dec.resets[kC - 1]; });
     // E
     f4 e[4] = {};
+    {
+      bf8 p[2][kInvParts], q[kSome][kInvParts], xp[3];
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      bf8 xp[3];
-      split<3>(x[2 * kt], x[2 * kt + 1], xp);
+      for (int jt = 0; jt < 2; ++jt) load_block<kInvParts>(invs, upper_block(jt, 0), p[jt]);
+      split<3>(x[0], x[1], xp);
+      mul_each<2>(p, xp, e);
+      split<3>(x[2], x[3], xp);
 #pragma unroll
-      for (int jt = 0; jt < 2 * kt + 2; ++jt) {
-        bf8 p[kInvParts];
-        load_block<kInvParts>(invs, upper_block(jt, kt), p);
-        e[jt] = mul<2>(p, xp, e[jt]);
+      for (int j0 = 0; j0 < 4; j0 += kSome) {
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) load_block<kInvParts>(invs, upper_block(j0 + i, 1), q[i]);
+        mul_each<2>(q, xp, e + j0);
       }
     }
     store_column<float, 4>(a.e + unit * kC * a.DV, a.DV, kC, col, a.DV, e);
@@ -882,12 +907,15 @@ __global__ __launch_bounds__(64 * WAVES) void delta_reverse_kernel(DeltaArgs a, 
       split<3>(e[2 * jt], e[2 * jt + 1], ep);
       split<3>(o[2 * jt], o[2 * jt + 1], op);
 #pragma unroll
-      for (int dt = 0; dt < 2 * KT; ++dt) {
-        bf8 p[N];
-        load_block<N>(kcols, dt * 2 + jt, p);
-        s[dt] = mul<2>(p, ep, s[dt]);
-        load_block<N>(qcols, dt * 2 + jt, p);
-        s[dt] = mul<2>(p, op, s[dt]);
+      for (int d0 = 0; d0 < 2 * KT; d0 += kSome) {
+        bf8 p[kSome][N], q[kSome][N];
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) {
+          load_block<N>(kcols, (d0 + i) * 2 + jt, p[i]);
+          load_block<N>(qcols, (d0 + i) * 2 + jt, q[i]);
+        }
+        mul_each<2>(p, ep, s + d0);
+        mul_each<2>(q, op, s + d0);
       }
     }
     if (t0 > 0) {
@@ -1245,22 +1273,17 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
     }
 }
 
-// One step: a workgroup has a head's state, 32 groups of 4 columns by 8 groups of 16
+// One step: a workgroup has a head's state, 32 groups of 4 columns by PARTS groups of 16
 // rows, so all of it is asked for at once.  The state is read and written once.
-__global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, int type, int slices) {
-  __shared__ float sum[2][8][128];
-  __shared__ float ks[PER_DELTA_MAX_DK], qs[PER_DELTA_MAX_DK];
+template <typename T, int PARTS>
+__global__ __launch_bounds__(32 * PARTS) void delta_step_kernel(DeltaArgs a, int slices) {
+  __shared__ float sum[2][PARTS][128];
+  __shared__ float ks[16 * PARTS], qs[16 * PARTS];
   int bh, b, h, hk, slice, rest;
   divide(blockIdx.x, (uint32_t)slices, bh, slice);
   divide((uint32_t)bh, (uint32_t)a.H, b, h);
   divide((uint32_t)h, (uint32_t)(a.H / a.HK), hk, rest);
   const int part = threadIdx.x / 32, cl = threadIdx.x % 32 * 4, col = slice * 128 + cl;
-  auto value = [&](const Seq& s, int64_t head, int i) {
-    const int64_t off = b * s.sb + head * s.sh + i;
-    return type == PER_F32    ? static_cast<const float*>(s.p)[off]
-           : type == PER_BF16 ? (float)static_cast<const bf16_t*>(s.p)[off]
-                              : (float)static_cast<const f16_t*>(s.p)[off];
-  };
   const float* s = a.s0 + (int64_t)bh * a.DK * a.DV;
   float v[16][4];
   const bool reset = a.reset && a.reset[b];
@@ -1271,13 +1294,15 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, int type, 
     for (int i = 0; i < 4; ++i) v[r][i] = 0.0f;
     if (row < a.DK && !reset) load_few<float, 4>(s + (int64_t)row * a.DV, col, a.DV, v[r]);
   }
-  if (threadIdx.x < 128) {
-    ks[threadIdx.x] = (int)threadIdx.x < a.DK ? value(a.k, hk, threadIdx.x) : 0.0f;
-  } else {
-    const int i = threadIdx.x - 128;
-    qs[i] = i < a.DK ? value(a.q, hk, i) : 0.0f;
+  {
+    const int i = threadIdx.x;
+    const int c = i % (16 * PARTS);
+    const T* from = i < 16 * PARTS ? at<T>(a.k, b, 0, hk) : at<T>(a.q, b, 0, hk);
+    (i < 16 * PARTS ? ks : qs)[c] = c < a.DK ? (float)from[c] : 0.0f;
   }
-  const float gate = value(a.g, h, 0), wt = value(a.b, h, 0);
+  float vs[4];
+  load_few<T, 4>(at<T>(a.v, b, 0, h), col, a.DV, vs);
+  const float gate = (float)*at<T>(a.g, b, 0, h), wt = (float)*at<T>(a.b, b, 0, h);
   const float f = 1.0f / (1.0f + expf(-gate)), w = 1.0f / (1.0f + expf(-wt));
   __syncthreads();
   float k[4] = {}, q[4] = {};
@@ -1298,8 +1323,8 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, int type, 
   for (int i = 0; i < 4; ++i) {
     float x = 0.0f;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) x += sum[0][p][cl + i];
-    u[i] = col + i < a.DV ? w * (value(a.v, h, col + i) - x) : 0.0f;
+    for (int p = 0; p < PARTS; ++p) x += sum[0][p][cl + i];
+    u[i] = col + i < a.DV ? w * (vs[i] - x) : 0.0f;
   }
   float* to = a.s_last + (int64_t)bh * a.DK * a.DV;
 #pragma unroll
@@ -1316,20 +1341,13 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, int type, 
 #pragma unroll
   for (int i = 0; i < 4; ++i) sum[1][part][cl + i] = q[i];
   __syncthreads();
-  const int c = slice * 128 + threadIdx.x;
-  if (threadIdx.x < 128 && c < a.DV) {
+  for (int i = threadIdx.x; i < 128; i += 32 * PARTS) {
+    const int c = slice * 128 + i;
+    if (c >= a.DV) break;
     float x = 0.0f;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) x += sum[1][p][threadIdx.x];
-    x *= a.scale;
-    const int64_t off = b * a.o.sb + h * a.o.sh + c;
-    if (type == PER_F32) {
-      static_cast<float*>(a.o.p)[off] = x;
-    } else if (type == PER_BF16) {
-      static_cast<bf16_t*>(a.o.p)[off] = (bf16_t)x;
-    } else {
-      static_cast<f16_t*>(a.o.p)[off] = (f16_t)x;
-    }
+    for (int p = 0; p < PARTS; ++p) x += sum[1][p][i];
+    const_cast<T*>(at<T>(a.o, b, 0, h))[c] = (T)(a.scale * x);
   }
 }
 
@@ -1382,14 +1400,14 @@ size_t delta_workspace(int64_t B, int64_t T, int64_t H, int64_t DK, int64_t DV, 
 
 // Waves of a workgroup, 16 columns of the state each: up to 128 columns, or 64 where the
 // states are few and twice as many workgroups find a place, or where 8 waves' registers
-// do not hold what a chunk takes (128 keys of more than one part).
+// do not hold what a chunk takes (f32, and 128 keys of f16).
 static int column_waves(const DeltaArgs& a, int type) {
-  if (type != PER_BF16 && a.DK > 64) return 4;
+  if (type == PER_F32 || (type == PER_F16 && a.DK > 64)) return 4;
   return a.DV <= 64 || a.B * a.H * ((a.DV + 127) / 128) <= 128 ? 4 : 8;
 }
 template <typename T, int KT>
 struct Columns {
-  static constexpr int most = kParts<T> > 1 && KT == 4 ? 4 : 8;
+  static constexpr int most = kParts<T> == 3 || (kParts<T> == 2 && KT == 4) ? 4 : 8;
   static constexpr auto forward4 = delta_forward_kernel<T, KT, 4>;
   static constexpr auto forward8 = delta_forward_kernel<T, KT, most>;
   static constexpr auto reverse4 = delta_reverse_kernel<T, KT, 4>;
@@ -1430,8 +1448,13 @@ hipError_t launch_delta_backward(const DeltaArgs& a, int type, hipStream_t s) {
 
 hipError_t launch_delta_step(const DeltaArgs& a, int type, hipStream_t s) {
   const int slices = (a.DV + 127) / 128;
-  return enqueue(delta_step_kernel, dim3((uint32_t)(a.B * a.H * slices)), dim3(256), 0, s, a, type,
-                 slices);
+  return by_type(type, [&](auto tag) {
+    return by_keys(a.DK, [&](auto keys) {
+      constexpr int parts = 2 * decltype(keys)::value;
+      return enqueue(delta_step_kernel<typename decltype(tag)::type, parts>,
+                     dim3((uint32_t)(a.B * a.H * slices)), dim3(32 * parts), 0, s, a, slices);
+    });
+  });
 }
 
 }  // namespace per

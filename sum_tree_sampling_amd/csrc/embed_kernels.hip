@@ -167,7 +167,7 @@ __global__ __launch_bounds__(1024) void embed_sort_small_kernel(EmbedArgs a, int
 
 // More of them: a block has `per` consecutive items, and each pass is two launches, the
 // digits' counts of each block and the scatter.
-constexpr int kSortThreads = 256, kSortTile = 1024;  // a wave has 4 * 64 items of a tile
+constexpr int kSortThreads = 1024, kSortTile = 1024;  // a wave has 64 items of a tile
 
 __device__ __forceinline__ uint32_t sort_key(const EmbedArgs& a, const uint32_t* keys, int64_t n) {
   return keys ? keys[n] : token_at(a, n);
@@ -197,21 +197,43 @@ __global__ __launch_bounds__(kSortThreads) void embed_scatter_kernel(
   __shared__ uint32_t space[kWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
   const uint32_t mask = (1u << bits) - 1;
-  // where this block's items of each digit begin: two neighbouring digits to a thread
+  // where this block's items of each digit begin: the blocks' counts are added by 8
+  // groups of threads, 4 neighbouring digits to a thread
   {
-    uint32_t before[2] = {0, 0}, total[2] = {0, 0};
-    const uint2* counts = reinterpret_cast<const uint2*>(a.counts) + threadIdx.x;
+    static_assert(kSortThreads == 8 * kBins / 4 && 2 * 8 * kBins <= kWaves * kBins, "groups");
+    uint32_t before[4] = {0, 0, 0, 0}, total[4] = {0, 0, 0, 0};
+    const uint32_t group = threadIdx.x / (kBins / 4), at = threadIdx.x % (kBins / 4);
+    const uint4* counts = reinterpret_cast<const uint4*>(a.counts) + at;
 #pragma unroll 8
-    for (uint32_t b = 0; b < gridDim.x; ++b) {
-      const uint2 c = counts[(int64_t)b * (kBins / 2)];
+    for (uint32_t b = group; b < gridDim.x; b += 8) {
+      const uint4 c = counts[(int64_t)b * (kBins / 4)];
+      const bool mine = b < blockIdx.x;
       total[0] += c.x;
       total[1] += c.y;
-      before[0] += b < blockIdx.x ? c.x : 0;
-      before[1] += b < blockIdx.x ? c.y : 0;
+      total[2] += c.z;
+      total[3] += c.w;
+      before[0] += mine ? c.x : 0;
+      before[1] += mine ? c.y : 0;
+      before[2] += mine ? c.z : 0;
+      before[3] += mine ? c.w : 0;
     }
-    const uint32_t at = block_exclusive<kWaves>(total[0] + total[1], space);
-    base[2 * threadIdx.x] = at + before[0];
-    base[2 * threadIdx.x + 1] = at + total[0] + before[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cnt[group][4 * at + i] = total[i];
+      cnt[8 + group][4 * at + i] = before[i];
+    }
+    __syncthreads();
+    uint32_t all = 0, mine = 0;
+    if (threadIdx.x < kBins) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        all += cnt[k][threadIdx.x];
+        mine += cnt[8 + k][threadIdx.x];
+      }
+    }
+    const uint32_t begin = block_exclusive<kWaves>(all, space);
+    if (threadIdx.x < kBins) base[threadIdx.x] = begin + mine;
+    __syncthreads();
   }
   const int64_t lo = blockIdx.x * per, hi = min(a.N, lo + per);
   for (int64_t tile = lo; tile < hi; tile += kSortTile) {
@@ -400,74 +422,65 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, uint32_t sl
   }
 }
 
-// Tokens that chunks share: a workgroup looks over 16 chunks for tokens that begin in
-// one of them and go on, and adds their parts in the chunks' order, a quarter of them
-// to each wave.
-constexpr int kJoinChunks = 16;
+// A token that begins in a chunk and goes on in others: a workgroup adds its parts in the
+// chunks' order, a run of them to each of its waves.  Most find nothing to do.
+constexpr int kJoinWaves = 8;
 template <typename G>
-__global__ __launch_bounds__(256) void embed_join_kernel(EmbedArgs a, uint32_t slices,
-                                                         int64_t chunks) {
+__global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs a, uint32_t slices,
+                                                                    int64_t chunks) {
   constexpr int W = 4;
-  __shared__ float sum[3][64][W];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-  const int64_t group = blockIdx.x / slices;
+  __shared__ float sum[kJoinWaves][64][W];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t first = blockIdx.x / slices;
   const uint32_t col = ((uint32_t)(blockIdx.x % slices) * 64 + lane) * W;
   const uint32_t D = (uint32_t)a.D;
-  const int64_t mine = group * kJoinChunks + lane;
-  bool starts = false;
-  if (lane < kJoinChunks && mine + 1 < chunks) {
-    const int64_t i0 = mine << a.lg_rows, i1 = (mine + 1) << a.lg_rows;
-    const uint32_t key = a.keys[i1];
-    starts = key < (uint32_t)a.V && a.keys[i1 - 1] == key &&
-             !(a.keys[i0] == key && mine > 0 && a.keys[i0 - 1] == key);
+  const int64_t i0 = first << a.lg_rows, i1 = (first + 1) << a.lg_rows;
+  const uint32_t key = a.keys[i1], last = a.keys[i1 - 1], head = a.keys[i0];
+  const uint32_t past = first > 0 ? a.keys[i0 - 1] : 0xFFFFFFFFu;
+  if (key >= (uint32_t)a.V || last != key || (head == key && past == key)) return;
+  // chunks behind the first that begin with the token
+  int64_t more = 1;
+  for (;;) {
+    const int64_t c = first + 1 + more + lane;
+    const uint64_t on = __ballot(c < chunks && a.keys[min(c, chunks - 1) << a.lg_rows] == key);
+    const int n = on == ~0ull ? 64 : __builtin_ctzll(~on);
+    more += n;
+    if (n < 64) break;
   }
-  uint32_t todo = (uint32_t)__ballot(starts);
-  while (todo) {
-    const int64_t first = group * kJoinChunks + __builtin_ctz(todo);
-    todo &= todo - 1;
-    const uint32_t key = a.keys[(first + 1) << a.lg_rows];
-    // chunks behind the first that begin with the token
-    int64_t more = 1;
-    for (;;) {
-      const int64_t c = first + 1 + more + lane;
-      const uint64_t on = __ballot(c < chunks && a.keys[min(c, chunks - 1) << a.lg_rows] == key);
-      const int n = on == ~0ull ? 64 : __builtin_ctzll(~on);
-      more += n;
-      if (n < 64) break;
-    }
-    // parts first * 2 + 1, then (first + 1 + j) * 2
-    const int64_t per = (more + 4) / 4;  // of more + 1 parts
-    const int64_t lo = wave * per, hi = min(more + 1, lo + per);
-    float acc[W] = {};
-    if (col < D) {
-      const float* part = a.part + col;
-#pragma unroll 8
-      for (int64_t j = lo; j < hi; ++j) {
-        const float* p = part + (j == 0 ? first * 2 + 1 : (first + j) * 2) * a.D;
-        float v[W];
-        if (col + W <= D) {
-          unpack<float, W>(load_pack<float, W>(p), v);
-        } else {
+  // part 1 of the first chunk, then part 0 of the others
+  const int64_t per = (more + kJoinWaves) / kJoinWaves;  // of more + 1 parts
+  const int64_t lo = wave * per, hi = min(more + 1, lo + per);
+  float acc[W] = {};
+  if (col < D) {
+    const float* part = a.part + first * 2 * a.D + col;
+    auto add = [&](const float* p) {
+      float v[W];
+      if (col + W <= D) {
+        unpack<float, W>(load_pack<float, W>(p), v);
+      } else {
 #pragma unroll
-          for (int i = 0; i < W; ++i) v[i] = col + i < D ? p[i] : 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < W; ++i) acc[i] += v[i];
+        for (int i = 0; i < W; ++i) v[i] = col + i < D ? p[i] : 0.0f;
       }
-    }
-    if (wave > 0) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) sum[wave - 1][lane][i] = acc[i];
+      for (int i = 0; i < W; ++i) acc[i] += v[i];
+    };
+    int64_t j = lo;
+    if (j == 0) {
+      add(part + a.D);
+      j = 1;
     }
-    __syncthreads();
-    if (wave == 0 && col < D) {
+#pragma unroll 8
+    for (; j < hi; ++j) add(part + j * 2 * a.D);
+  }
 #pragma unroll
-      for (int w = 0; w < 3; ++w)
+  for (int i = 0; i < W; ++i) sum[wave][lane][i] = acc[i];
+  __syncthreads();
+  if (wave == 0 && col < D) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) acc[i] += sum[w][lane][i];
-      write_sum<G, W>(a, key, col, acc);
-    }
-    __syncthreads();
+    for (int w = 1; w < kJoinWaves; ++w)
+#pragma unroll
+      for (int i = 0; i < W; ++i) acc[i] += sum[w][lane][i];
+    write_sum<G, W>(a, key, col, acc);
   }
 }
 
@@ -485,11 +498,11 @@ constexpr int64_t kSmall = 8192;  // tokens that one workgroup sorts
 // Blocks of a sorting pass.
 int64_t sort_blocks(int64_t N) { return std::min<int64_t>(256, (N + kSortTile - 1) / kSortTile); }
 
-// Rows of a chunk: at least 2048 waves where the rows allow it, 8 to 64 rows each.
+// Rows of a chunk: at least 1024 waves where the rows allow it, 8 to 64 rows each.
 int chunk_rows(int64_t N, int64_t D) {
   const int64_t slices = (D + 511) / 512;
   int lg = 3;
-  while (lg < 6 && (N * slices >> (lg + 1)) >= 2048) ++lg;
+  while (lg < 6 && (N * slices >> (lg + 1)) >= 1024) ++lg;
   return lg;
 }
 
@@ -574,9 +587,8 @@ hipError_t launch_embed_backward(EmbedArgs a, int dout_type, int grad_type, hipS
     });
     if (e != hipSuccess || chunks < 2) return e;
     const uint32_t slices = (uint32_t)((a.D + 255) / 256);
-    const int64_t groups = (chunks + kJoinChunks - 1) / kJoinChunks;
-    return enqueue(embed_join_kernel<G>, dim3((uint32_t)(groups * slices)), dim3(256), 0, s, a,
-                   slices, chunks);
+    return enqueue(embed_join_kernel<G>, dim3((uint32_t)((chunks - 1) * slices)),
+                   dim3(64 * kJoinWaves), 0, s, a, slices, chunks);
   });
 }
 

@@ -365,17 +365,9 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
   const uint32_t col = blockIdx.x * 64 + threadIdx.x % 64, part = threadIdx.x / 64;
   float s = 0.0f;
   if (col < 2 * a.D) {
-    int b = (int)part;
-    for (; b + 48 < a.blocks; b += 64) {
-      const float* p = a.part + (int64_t)b * 2 * a.D + col;
-      const int64_t step = (int64_t)32 * a.D;
-      const float v0 = p[0], v1 = p[step], v2 = p[2 * step], v3 = p[3 * step];
-      s += v0;
-      s += v1;
-      s += v2;
-      s += v3;
-    }
-    for (; b < a.blocks; b += 16) s += a.part[(int64_t)b * 2 * a.D + col];
+    const float* p = a.part + col;
+#pragma unroll 16
+    for (int b = (int)part; b < a.blocks; b += 16) s += p[(int64_t)b * 2 * a.D];
   }
   sum[part][threadIdx.x % 64] = s;
   __syncthreads();
@@ -405,8 +397,8 @@ constexpr uint32_t longest(int type) { return 2u * 1024 * (type == PER_F32 ? 4 :
 // are little next to the rows.
 size_t norm_workspace(int64_t N, int64_t D, int type, NormArgs* a, void* ws) {
   const uint32_t vec = type == PER_F32 ? 4 : 8;
-  const int64_t rows = D <= 256 * vec ? 4 : 1;  // rows that a block has at once
-  const int64_t most = D <= 1024 * vec ? 512 : 256;
+  const int64_t rows = D <= 128 * vec ? 4 : 1;  // rows that a block has at once
+  const int64_t most = D <= 128 * vec ? 512 : D <= 256 * vec ? 1536 : D <= 1024 * vec ? 512 : 256;
   const int64_t blocks = N == 0 ? 0 : std::min(most, (N + rows - 1) / rows);
   const size_t part = (size_t)blocks * 2 * (size_t)D * 4;
   if (a) {
@@ -453,7 +445,7 @@ hipError_t launch_norm_backward(const NormArgs& a, int type, hipStream_t s) {
       if (chunks <= 16) return GO(16, 1);
       if (chunks <= 64) return GO(64, 1);
       if (chunks <= 128) return GO(64, 2);
-      if (chunks <= 256) return GO(64, 4);
+      if (chunks <= 256) return GO(256, 1);
       if (chunks <= 512) return GO(256, 2);
       if (chunks <= 1024) return GO(256, 4);
       if (chunks <= 2048) return GO(1024, 2);
