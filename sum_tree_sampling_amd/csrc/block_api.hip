@@ -100,7 +100,7 @@ int check_seq(Seq& to, const per_seq& s, int32_t type, int64_t B, int64_t T, int
       extent += (d.second - 1) * d.first;
     }
   }
-  to = Seq{s.p, s.sb, T > 1 ? s.st : 0, s.sh};
+  to = Seq{s.p, s.sb, T > 1 ? s.st : D, s.sh};
   return PER_OK;
 }
 

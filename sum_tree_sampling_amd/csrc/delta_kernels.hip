@@ -107,18 +107,45 @@ __device__ __forceinline__ void mul_each(const bf8 (&a)[COUNT][NA], const bf8 (&
           c[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[k][i], b[s - i], c[k], 0, 0, 0);
 }
 
-// Operand blocks in LDS or memory: block n of N parts, 64 lanes of 16 bytes each.
+// Operand blocks: N parts of 64 lanes of 16 bytes each.  As they are copied (what is
+// prepared, in memory and LDS) lane l's lie at 16 l; where pieces of rows are put together
+// in LDS at 16 (l ^ turn), with a turn for each block, or the pieces that a wave writes at
+// once would meet in few of the banks.
 template <int N>
-__device__ __forceinline__ void load_block(const char* blocks, int n, bf8 (&p)[N],
-                                           int lane = threadIdx.x & 63) {
-  const char* at = blocks + n * N * 1024 + lane * 16;
+__device__ __forceinline__ void load_block(const char* block, bf8 (&p)[N], uint32_t lane) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) p[i] = *reinterpret_cast<const bf8*>(at + i * 1024);
+  for (int i = 0; i < N; ++i)
+    p[i] = *reinterpret_cast<const bf8*>(block + i * 1024 + lane * 16);
+}
+// Rows 16 it.. of 32 KT terms; the 32 rows 32 jt.. as the terms of columns 16 dt..
+__device__ __forceinline__ constexpr int row_turn(int kt) { return kt & 3; }
+__device__ __forceinline__ constexpr int col_turn(int dt) { return dt & 7; }
+template <int N, int KT>
+__device__ __forceinline__ void load_rows(const char* rows, int it, int kt, bf8 (&p)[N], uint32_t lane) {
+  load_block<N>(rows + (it * KT + kt) * N * 1024, p, lane ^ row_turn(kt));
+}
+template <int N>
+__device__ __forceinline__ void load_cols(const char* cols, int dt, int jt, bf8 (&p)[N], uint32_t lane) {
+  load_block<N>(cols + (dt * 2 + jt) * N * 1024, p, lane ^ col_turn(dt));
+}
+// The same at a constant place of an array, by the offset 16 lane of a buffer in it.
+template <int N>
+__device__ __forceinline__ void lds_block(const char* room, int place, int n, bf8 (&p)[N], uint32_t me) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    p[i] = *reinterpret_cast<const bf8*>(room + me + (place + (n * N + i) * 1024));
+}
+template <int N, int KT>
+__device__ __forceinline__ void lds_rows(const char* room, int place, int it, int kt, bf8 (&p)[N], uint32_t me) {
+  lds_block<N>(room, place, it * KT + kt, p, me ^ (row_turn(kt) * 16));
+}
+template <int N>
+__device__ __forceinline__ void lds_cols(const char* room, int place, int dt, int jt, bf8 (&p)[N], uint32_t me) {
+  lds_block<N>(room, place, dt * 2 + jt, p, me ^ (col_turn(dt) * 16));
 }
 // Half of a block from a 16 x 16 result: its rows are the terms of the sum.
 template <int N>
-__device__ __forceinline__ void store_half(char* blocks, int n, int half, const f4& v,
-                                           int lane = threadIdx.x & 63) {
+__device__ __forceinline__ void store_half(char* blocks, int n, int half, const f4& v, uint32_t lane) {
   bf4 p[N];
   split4<N>(v, p);
   char* at = blocks + n * N * 1024 + lane * 16 + half * 8;
@@ -190,6 +217,7 @@ __device__ __forceinline__ void store_piece(const Piece<T>& v, int a, int m, cha
   if (rows) {
     const int half = m % 4 / 2, g = m % 2 * 2;
     char* at = rows + (a / 4 * KT + m / 4) * N * 1024 + half * 8 + (16 * g + a % 4 * 4) * 16;
+    const int turn = row_turn(m / 4);  // below 4, as r
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
 #pragma unroll
@@ -199,19 +227,21 @@ __device__ __forceinline__ void store_piece(const Piece<T>& v, int a, int m, cha
         split_four<N>(x, p);
 #pragma unroll
         for (int q = 0; q < N; ++q)
-          *reinterpret_cast<bf4*>(at + q * 1024 + (16 * k + r) * 16) = p[q];
+          *reinterpret_cast<bf4*>(at + q * 1024 + (16 * k + (r ^ turn)) * 16) = p[q];
       }
     }
   }
   if (cols) {
     char* at = cols + (m / 2 * 2 + a / 8) * N * 1024 + a % 8 / 4 * 8 + (16 * (a % 4) + m % 2 * 8) * 16;
+    const int turn = col_turn(m / 2);  // below 8, as c
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       const t4 x = {v.v[0][c], v.v[1][c], v.v[2][c], v.v[3][c]};
       bf4 p[N];
       split_four<N>(x, p);
 #pragma unroll
-      for (int q = 0; q < N; ++q) *reinterpret_cast<bf4*>(at + q * 1024 + c * 16) = p[q];
+      for (int q = 0; q < N; ++q)
+        *reinterpret_cast<bf4*>(at + q * 1024 + (c ^ turn) * 16) = p[q];
     }
   }
 }
@@ -337,9 +367,9 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         bf8 ki[N], kj[N], qi[N];
-        load_block<N>(ks, it * KT + kt, ki);
-        load_block<N>(ks, jt * KT + kt, kj);
-        load_block<N>(qs, it * KT + kt, qi);
+        load_rows<N, KT>(ks, it, kt, ki, lane);
+        load_rows<N, KT>(ks, jt, kt, kj, lane);
+        load_rows<N, KT>(qs, it, kt, qi, lane);
         if (BACKWARD) {  // rows of it, columns of jt
           kk = mul<2>(ki, kj, kk);
           qk = mul<2>(qi, kj, qk);
@@ -357,9 +387,9 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
       }
     }
     if (BACKWARD) {  // rows of it are the terms of a row of jt
-      if (it / 2 >= jt / 2 && jt < 4) store_half<NS>(scores, upper_block(jt, it / 2), it % 2, qk);
+      if (it / 2 >= jt / 2 && jt < 4) store_half<NS>(scores, upper_block(jt, it / 2), it % 2, qk, lane);
     } else {
-      store_half<NS>(scores, lower_block(it, jt / 2), jt % 2, qk);
+      store_half<NS>(scores, lower_block(it, jt / 2), jt % 2, qk, lane);
     }
   }
   __syncthreads();
@@ -464,57 +494,74 @@ __device__ __forceinline__ void store_few(T* row, int col, int width, const floa
   }
 }
 
-// A wave's column of a matrix [. x width] for each lane n, as 16 x 16 results: rows 16 t +
-// 4 g + r of column col, from `rows` rows.  The rows' places are the same for the whole
-// wave but for 4 g, so they stay in scalar registers.
+// A wave's column of a matrix [rows x width] for each lane n, as 16 x 16 results: rows 16 t
+// + 4 g + r of column col.  Through a buffer descriptor that ends with the last row: the
+// unit checks every access against it, so rows past the end read 0 and write nothing
+// without a branch, a row's place is one scalar for the whole wave, and a lane's part of it
+// (its column, past all rows where it has none) one register for all rows.
 template <typename T, int TILES>
-__device__ __forceinline__ void load_column(const T* base, int64_t stride, int rows, int col, int width,
-                                            T (&v)[TILES][4]) {
-  const int g = (threadIdx.x & 63) / 16;
-  const uint32_t at = (uint32_t)(4 * g) * (uint32_t)stride + col;
-  const bool in = col < width;
-  // else the places of all rows are kept from chunk to chunk, and registers run out
-  asm volatile("" : "+s"(rows), "+s"(stride));
-#pragma unroll
-  for (int t = 0; t < TILES; ++t)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v[t][r] = (T)0.0f;
-  if (rows >= 16 * TILES) {
-    if (in) {
-#pragma unroll
-      for (int t = 0; t < TILES; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[t][r] = (base + (16 * t + r) * stride)[at];
-    }
-  } else {
+struct Column {
+  __amdgpu_buffer_rsrc_t buffer;
+  uint32_t lane;  // the lane's part
+  int step;       // bytes between rows
+  __device__ __forceinline__ Column(const T* base, int64_t stride, int rows, int col, int width) {
+    step = (int)stride * (int)sizeof(T);
+    asm volatile("" : "+s"(step));  // else the places of all rows are kept from chunk to chunk
+    const int bytes = (rows - 1) * step + width * (int)sizeof(T);
+    buffer = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, rows > 0 ? bytes : 0, 0x00020000);
+    lane = col < width ? (threadIdx.x & 63) / 16 * 4 * (uint32_t)step + (uint32_t)col * (uint32_t)sizeof(T)
+                       : 0xFFFFFFFFu;
+  }
+  __device__ __forceinline__ void load(T (&v)[TILES][4]) const {
 #pragma unroll
     for (int t = 0; t < TILES; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (in && 16 * t + 4 * g + r < rows) v[t][r] = (base + (16 * t + r) * stride)[at];
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (sizeof(T) == 4) {
+          v[t][r] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(buffer, lane, (16 * t + r) * step, 0));
+        } else {
+          v[t][r] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(buffer, lane, (16 * t + r) * step, 0));
+        }
+      }
   }
+  __device__ __forceinline__ void store(const f4 (&v)[TILES]) const {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (sizeof(T) == 4) {
+          __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (T)v[t][r]), buffer, lane,
+                                                (16 * t + r) * step, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)v[t][r]), buffer, lane,
+                                                (16 * t + r) * step, 0);
+        }
+      }
+  }
+};
+template <typename T, int TILES>
+__device__ __forceinline__ void load_column(const T* base, int64_t stride, int rows, int col, int width,
+                                            T (&v)[TILES][4]) {
+  if (stride >= width) {
+    Column<T, TILES>(base, stride, rows, col, width).load(v);
+    return;
+  }
+  // rows that overlap (an expanded array) do not end with the last
+  asm volatile("" : "+s"(stride), "+s"(rows));
+  const int g = (threadIdx.x & 63) / 16;
+#pragma unroll
+  for (int t = 0; t < TILES; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * t + 4 * g + r;
+      v[t][r] = (T)0.0f;
+      if (row < rows && col < width) v[t][r] = base[row * stride + col];
+    }
 }
 template <typename T, int TILES>
 __device__ __forceinline__ void store_column(T* base, int64_t stride, int rows, int col, int width,
                                              const f4 (&v)[TILES]) {
-  const int g = (threadIdx.x & 63) / 16;
-  const uint32_t at = (uint32_t)(4 * g) * (uint32_t)stride + col;
-  const bool in = col < width;
-  asm volatile("" : "+s"(rows), "+s"(stride));
-  if (rows >= 16 * TILES) {
-    if (in) {
-#pragma unroll
-      for (int t = 0; t < TILES; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) (base + (16 * t + r) * stride)[at] = (T)v[t][r];
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < TILES; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (in && 16 * t + 4 * g + r < rows) (base + (16 * t + r) * stride)[at] = (T)v[t][r];
-  }
+  Column<T, TILES>(base, stride, rows, col, width).store(v);
 }
 template <int TILES>
 __device__ __forceinline__ void load_state(const float* s, int DK, int DV, int col, f4 (&v)[TILES]) {
@@ -562,16 +609,40 @@ struct Ahead {
   Piece<T> piece[kPieces];
   f4 copy[kCopies];
 
-  __device__ __forceinline__ void load(const DeltaArgs& a, int64_t b, int64_t t0, int hk, int rows,
-                                       const char* prep) {
+  // even: rows begin at whole 4 bytes, and hold whole pieces
+  __device__ __forceinline__ void load(const T* ks, int64_t kst, const T* qs, int64_t qst, bool even, int DK,
+                                       int rows, const char* prep) {
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
-      const int id = threadIdx.x + p * THREADS, at = id % (64 * KT);
-      const bool query = __builtin_amdgcn_readfirstlane(id / (64 * KT)) != 0;
-      const Seq& s = query ? a.q : a.k;
-      if (id < 128 * KT)
-        load_piece<T>(static_cast<const T*>(s.p) + b * s.sb + t0 * s.st + hk * s.sh, s.st, rows, a.DK,
-                      at / (4 * KT), at % (4 * KT), piece[p]);
+      const int id = threadIdx.x + p * THREADS, at = id % (64 * KT), a = at / (4 * KT), m = at % (4 * KT);
+      const int query = __builtin_amdgcn_readfirstlane(id / (64 * KT));
+      if (query > 1) continue;
+      const T* base = query ? qs : ks;
+      const int64_t stride = query ? qst : kst;
+      if (even) {
+        int step = (int)stride * (int)sizeof(T);
+        const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<T*>(base), 0, (rows - 1) * step + DK * (int)sizeof(T), 0x00020000);
+        const uint32_t lane = 8 * m < DK ? 4 * a * (uint32_t)step + 8 * m * (uint32_t)sizeof(T) : 0xFFFFFFFFu;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (sizeof(T) == 2) {
+            piece[p].v[r] = __builtin_bit_cast(typename Piece<T>::row,
+                                               __builtin_amdgcn_raw_buffer_load_b128(buffer, lane, r * step, 0));
+          } else {
+            typedef T t4 __attribute__((ext_vector_type(4)));
+            const t4 lo = __builtin_bit_cast(t4, __builtin_amdgcn_raw_buffer_load_b128(buffer, lane, r * step, 0));
+            const t4 hi = __builtin_bit_cast(
+                t4, __builtin_amdgcn_raw_buffer_load_b128(buffer, lane, r * step + 16, 0));
+            piece[p].v[r] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          }
+        }
+      } else {
+        int64_t step = stride;
+        int width = DK;
+        asm volatile("" : "+s"(step), "+s"(width));
+        load_piece<T>(base, step, rows, width, a, m, piece[p]);
+      }
     }
 #pragma unroll
     for (int c = 0; c < kCopies; ++c) {
@@ -602,6 +673,11 @@ struct Ahead {
     }
   }
 };
+// Whether rows of an array begin at whole 4 bytes, are whole pieces, and do not overlap.
+template <typename T>
+__device__ __forceinline__ bool even_rows(const T* p, int64_t stride, int D) {
+  return D % 8 == 0 && stride >= D && (((uint32_t)(uintptr_t)p | (uint32_t)stride * (uint32_t)sizeof(T)) & 3) == 0;
+}
 
 // A workgroup has a head of a sequence and 16 columns of its state for each of its waves.
 // While a chunk is computed the next one's operands are on their way in registers; they
@@ -613,9 +689,11 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
   constexpr int kTile = 4 * KT * N * 1024, kPrep = (int)prep_bytes(NO);
   constexpr bool kApart = N < 3;  // queries have a place of their own in LDS
   constexpr int kRoom = (kApart ? 3 : 2) * kTile + kPrep;
-  constexpr int kSome = WAVES == 8 || KT == 1 ? 2 : 4;  // blocks that are held at a time
+  constexpr int kSome = 2;  // blocks that are held at a time
   constexpr bool kTwice = 2 * kRoom <= 160 * 1024;
-  __shared__ __attribute__((aligned(16))) char room[kTwice ? 2 : 1][kRoom];
+  __shared__ __attribute__((aligned(16))) char room[(kTwice ? 2 : 1) * kRoom];
+  constexpr int kCols = kTile, kQueries = kApart ? 2 * kTile : 0, kReady = kRoom - kPrep;
+  constexpr int kInvs = kReady + (int)sizeof(Decays), kScores = kInvs + 6 * kInvParts * 1024;
 
   const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -626,7 +704,8 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
   const int col = (slice * WAVES + wave) * 16 + n;
   const int steps = steps_of(a, b);
   const int64_t unit0 = (int64_t)b * a.chunks * a.H + h;  // the head's first chunk; others lie H apart
-  const T* vs = at<T>(a.v, b, 0, h);
+  const T *ks = at<T>(a.k, b, 0, hk), *qs = at<T>(a.q, b, 0, hk), *vs = at<T>(a.v, b, 0, h);
+  const bool even = even_rows(ks, a.k.st, a.DK) && even_rows(qs, a.q.st, a.DK);
   T* os = const_cast<T*>(at<T>(a.o, b, 0, h));
 
   f4 s[2 * KT];
@@ -634,20 +713,21 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
   Ahead<T, KT, 64 * WAVES, kPrep> ahead;
   T v[4][4];
   if (steps > 0) {
-    ahead.load(a, b, 0, hk, min(kC, steps), static_cast<const char*>(a.prep) + unit0 * kPrep);
+    ahead.load(ks, a.k.st, qs, a.q.st, even, a.DK, min(kC, steps),
+               static_cast<const char*>(a.prep) + unit0 * kPrep);
     load_column<T, 4>(vs, a.v.st, min(kC, steps), col, a.DV, v);
-    ahead.store(room[0], room[0] + kTile, room[0] + 2 * kTile, nullptr, room[0] + kRoom - kPrep,
-                kApart ? 3 : 1);
+    ahead.store(room, room + kCols, room + kQueries, nullptr, room + kReady, kApart ? 3 : 1);
   }
   __syncthreads();
   for (int t0 = 0, flip = 0; t0 < steps; t0 += kC) {
     const int rows = min(kC, steps - t0), more = min(kC, steps - t0 - kC);
     const int64_t unit = unit0 + t0 / kC * a.H;
-    char *krows = room[kTwice ? flip : 0], *kcols = krows + kTile;
-    char* qrows = kApart ? krows + 2 * kTile : krows;
-    const char* prep = krows + kRoom - kPrep;
-    const Decays& dec = *reinterpret_cast<const Decays*>(prep);
-    const char *invs = prep + sizeof(Decays), *scores = invs + 6 * kInvParts * 1024;
+    char* now = room + (kTwice ? flip * kRoom : 0);
+    const Decays& dec = *reinterpret_cast<const Decays*>(now + kReady);
+    const bool resets = __builtin_amdgcn_readfirstlane(dec.resets[kC - 1]) != 0;
+    // one register for all places in LDS
+    uint32_t me = (uint32_t)(now - room) + (uint32_t)lane * 16;
+    asm volatile("" : "+v"(me));
     f4 r[4];  // V
 #pragma unroll
     for (int it = 0; it < 4; ++it)
@@ -656,7 +736,8 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
     Ahead<T, KT, 64 * WAVES, kPrep> queries;
     if constexpr (!kApart) queries = ahead;
     if (more > 0) {
-      ahead.load(a, b, t0 + kC, hk, more, static_cast<const char*>(a.prep) + (unit + a.H) * kPrep);
+      ahead.load(ks + (int64_t)(t0 + kC) * a.k.st, a.k.st, qs + (int64_t)(t0 + kC) * a.q.st, a.q.st, even,
+                 a.DK, more, static_cast<const char*>(a.prep) + (unit + a.H) * kPrep);
       load_column<T, 4>(vs + (int64_t)(t0 + kC) * a.v.st, a.v.st, more, col, a.DV, v);
     }
     float* carry = a.carries ? a.carries + unit * carry_size(a.DK, a.DV) : nullptr;
@@ -669,8 +750,8 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
       bf8 sp[3], kp[4][N], qp[4][N];
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        load_block<N>(krows, it * KT + kt, kp[it]);
-        if constexpr (kApart) load_block<N>(qrows, it * KT + kt, qp[it]);
+        lds_rows<N, KT>(room, 0, it, kt, kp[it], me);
+        if constexpr (kApart) lds_rows<N, KT>(room, kQueries, it, kt, qp[it], me);
       }
       split<3>(s[2 * kt], s[2 * kt + 1], sp);
       mul_each<2>(kp, sp, x);
@@ -678,13 +759,13 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
     }
     if constexpr (!kApart) {
       __syncthreads();
-      queries.store(nullptr, nullptr, qrows, nullptr, nullptr, 2);
+      queries.store(nullptr, nullptr, now + kQueries, nullptr, nullptr, 2);
       __syncthreads();
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         bf8 sp[3], qp[4][N];
 #pragma unroll
-        for (int it = 0; it < 4; ++it) load_block<N>(qrows, it * KT + kt, qp[it]);
+        for (int it = 0; it < 4; ++it) lds_rows<N, KT>(room, kQueries, it, kt, qp[it], me);
         split<3>(s[2 * kt], s[2 * kt + 1], sp);
         mul_each<WEAK>(qp, sp, y);
       }
@@ -695,12 +776,13 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
       const f4 first = rows_of(dec.first, it), w = rows_of(dec.w, it);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float past = first[i] < 0.0f ? 0.0f : first[i] * x[it][i];
-        x[it][i] = w[i] * (r[it][i] - past);
-        y[it][i] = first[i] < 0.0f ? 0.0f : first[i] * y[it][i];
+        x[it][i] *= first[i];
+        y[it][i] *= first[i];
+        if (resets && first[i] < 0.0f) x[it][i] = y[it][i] = 0.0f;
+        x[it][i] = w[i] * (r[it][i] - x[it][i]);
       }
     }
-    if (dec.resets[kC - 1] > 0) keep_apart(x, [&](int i) { return dec.first[i] >= 0.0f; });
+    if (resets) keep_apart(x, [&](int i) { return dec.first[i] >= 0.0f; });
     // U
     f4 u[4] = {};
     {
@@ -709,11 +791,11 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
 #pragma unroll
       for (int i0 = 0; i0 < 4; i0 += kSome) {
 #pragma unroll
-        for (int i = 0; i < kSome; ++i) load_block<kInvParts>(invs, lower_block(i0 + i, 0), p[i]);
+        for (int i = 0; i < kSome; ++i) lds_block<kInvParts>(room, kInvs, lower_block(i0 + i, 0), p[i], me);
         mul_each<2>(p, xp, u + i0);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) load_block<kInvParts>(invs, lower_block(i + 2, 1), q[i]);
+      for (int i = 0; i < 2; ++i) lds_block<kInvParts>(room, kInvs, lower_block(i + 2, 1), q[i], me);
       split<3>(x[2], x[3], xp);
       mul_each<2>(q, xp, u + 2);
     }
@@ -722,12 +804,12 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
     {
       bf8 p[4][NO], up[NO];
 #pragma unroll
-      for (int it = 0; it < 4; ++it) load_block<NO>(scores, lower_block(it, 0), p[it]);
+      for (int it = 0; it < 4; ++it) lds_block<NO>(room, kScores, lower_block(it, 0), p[it], me);
       split<NO>(u[0], u[1], up);
       mul_each<WEAK>(p, up, y);
       bf8 q[2][NO];
 #pragma unroll
-      for (int it = 0; it < 2; ++it) load_block<NO>(scores, lower_block(it + 2, 1), q[it]);
+      for (int it = 0; it < 2; ++it) lds_block<NO>(room, kScores, lower_block(it + 2, 1), q[it], me);
       split<NO>(u[2], u[3], up);
       mul_each<WEAK>(q, up, y + 2);
     }
@@ -740,9 +822,7 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
     // the state behind the chunk
     const float kept = dec.first[kC - 1];
 #pragma unroll
-    for (int dt = 0; dt < 2 * KT; ++dt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[dt][i] = kept < 0.0f ? 0.0f : kept * s[dt][i];
+    for (int dt = 0; dt < 2 * KT; ++dt) s[dt] = resets ? f4{} : s[dt] * kept;
 #pragma unroll
     for (int jt = 0; jt < 2; ++jt) {
       bf8 up[3];
@@ -751,7 +831,7 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
       for (int d0 = 0; d0 < 2 * KT; d0 += kSome) {
         bf8 p[kSome][N];
 #pragma unroll
-        for (int i = 0; i < kSome; ++i) load_block<N>(kcols, (d0 + i) * 2 + jt, p[i]);
+        for (int i = 0; i < kSome; ++i) lds_cols<N>(room, kCols, d0 + i, jt, p[i], me);
         mul_each<2>(p, up, s + d0);
       }
     }
@@ -761,8 +841,8 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_f
       } else {
         __syncthreads();
       }
-      char* next = room[kTwice ? flip : 0];
-      ahead.store(next, next + kTile, next + 2 * kTile, nullptr, next + kRoom - kPrep, kApart ? 3 : 1);
+      char* next = room + (kTwice ? flip * kRoom : 0);
+      ahead.store(next, next + kCols, next + kQueries, nullptr, next + kReady, kApart ? 3 : 1);
     }
     __syncthreads();
   }
@@ -779,9 +859,11 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_r
   constexpr int kTile = 4 * KT * N * 1024, kPrep = (int)prep_bytes(3);
   constexpr bool kApart = N < 3;
   constexpr int kRoom = (kApart ? 3 : 2) * kTile + kPrep;
-  constexpr int kSome = WAVES == 8 || KT == 1 ? 2 : 4;  // blocks that are held at a time
+  constexpr int kSome = 2;  // blocks that are held at a time
   constexpr bool kTwice = 2 * kRoom <= 160 * 1024;
-  __shared__ __attribute__((aligned(16))) char room[kTwice ? 2 : 1][kRoom];
+  __shared__ __attribute__((aligned(16))) char room[(kTwice ? 2 : 1) * kRoom];
+  constexpr int kCols = kTile, kQueries = kApart ? 2 * kTile : 0, kReady = kRoom - kPrep;
+  constexpr int kInvs = kReady + (int)sizeof(Decays), kScores = kInvs + 6 * kInvParts * 1024;
 
   const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -792,7 +874,8 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_r
   const int col = (slice * WAVES + wave) * 16 + n;
   const int steps = steps_of(a, b);
   const int64_t unit0 = (int64_t)b * a.chunks * a.H + h;
-  const T* os = at<T>(a.o, b, 0, h);
+  const T *ks = at<T>(a.k, b, 0, hk), *qs = at<T>(a.q, b, 0, hk), *os = at<T>(a.o, b, 0, h);
+  const bool even = even_rows(ks, a.k.st, a.DK) && even_rows(qs, a.q.st, a.DK);
   T* dvs = const_cast<T*>(at<T>(a.dv, b, 0, h));
 
   f4 s[2 * KT];
@@ -801,20 +884,20 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_r
   T d[4][4];  // dO
   const int tail = steps > 0 ? (steps - 1) / kC * kC : -kC;  // the last chunk
   if (steps > 0) {
-    ahead.load(a, b, tail, hk, steps - tail, static_cast<const char*>(a.prep) + (unit0 + tail / kC * a.H) * kPrep);
+    ahead.load(ks + (int64_t)tail * a.k.st, a.k.st, qs + (int64_t)tail * a.q.st, a.q.st, even, a.DK,
+               steps - tail, static_cast<const char*>(a.prep) + (unit0 + tail / kC * a.H) * kPrep);
     load_column<T, 4>(os + (int64_t)tail * a.o.st, a.o.st, steps - tail, col, a.DV, d);
-    ahead.store(room[0], room[0] + kTile, nullptr, room[0] + 2 * kTile, room[0] + kRoom - kPrep,
-                kApart ? 3 : 1);
+    ahead.store(room, room + kCols, nullptr, room + kQueries, room + kReady, kApart ? 3 : 1);
   }
   __syncthreads();
   for (int t0 = tail, flip = 0; t0 >= 0; t0 -= kC) {
     const int rows = min(kC, steps - t0);
     const int64_t unit = unit0 + t0 / kC * a.H;
-    char *krows = room[kTwice ? flip : 0], *kcols = krows + kTile;
-    char* qcols = kApart ? krows + 2 * kTile : krows;
-    const char* prep = krows + kRoom - kPrep;
-    const Decays& dec = *reinterpret_cast<const Decays*>(prep);
-    const char *invs = prep + sizeof(Decays), *scores = invs + 6 * kInvParts * 1024;
+    char* now = room + (kTwice ? flip * kRoom : 0);
+    const Decays& dec = *reinterpret_cast<const Decays*>(now + kReady);
+    const bool resets = __builtin_amdgcn_readfirstlane(dec.resets[kC - 1]) != 0;
+    uint32_t me = (uint32_t)(now - room) + (uint32_t)lane * 16;
+    asm volatile("" : "+v"(me));
     f4 o[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it)
@@ -823,7 +906,8 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_r
     Ahead<T, KT, 64 * WAVES, kPrep> queries;
     if constexpr (!kApart) queries = ahead;
     if (t0 > 0) {
-      ahead.load(a, b, t0 - kC, hk, kC, static_cast<const char*>(a.prep) + (unit - a.H) * kPrep);
+      ahead.load(ks + (int64_t)(t0 - kC) * a.k.st, a.k.st, qs + (int64_t)(t0 - kC) * a.q.st, a.q.st, even,
+                 a.DK, kC, static_cast<const char*>(a.prep) + (unit - a.H) * kPrep);
       load_column<T, 4>(os + (int64_t)(t0 - kC) * a.o.st, a.o.st, kC, col, a.DV, d);
     }
     store_column<float, 2 * KT>(a.dstate + unit * a.DK * a.DV, a.DV, a.DK, col, a.DV, s);
@@ -834,50 +918,50 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_r
     for (int kt = 0; kt < KT; ++kt) {
       bf8 sp[3], kp[4][N];
 #pragma unroll
-      for (int it = 0; it < 4; ++it) load_block<N>(krows, it * KT + kt, kp[it]);
+      for (int it = 0; it < 4; ++it) lds_rows<N, KT>(room, 0, it, kt, kp[it], me);
       split<3>(s[2 * kt], s[2 * kt + 1], sp);
       mul_each<2>(kp, sp, x);
     }
     {
       bf8 p[2][3], q[kSome][3], op[N];
 #pragma unroll
-      for (int jt = 0; jt < 2; ++jt) load_block<3>(scores, upper_block(jt, 0), p[jt]);
+      for (int jt = 0; jt < 2; ++jt) lds_block<3>(room, kScores, upper_block(jt, 0), p[jt], me);
       split<N>(o[0], o[1], op);
       mul_each<2>(p, op, y);
       split<N>(o[2], o[3], op);
 #pragma unroll
       for (int j0 = 0; j0 < 4; j0 += kSome) {
 #pragma unroll
-        for (int i = 0; i < kSome; ++i) load_block<3>(scores, upper_block(j0 + i, 1), q[i]);
+        for (int i = 0; i < kSome; ++i) lds_block<3>(room, kScores, upper_block(j0 + i, 1), q[i], me);
         mul_each<2>(q, op, y + j0);
       }
     }
     if constexpr (!kApart) {
       __syncthreads();  // the keys' rows make room for the queries
-      queries.store(nullptr, nullptr, nullptr, qcols, nullptr, 2);
+      queries.store(nullptr, nullptr, nullptr, now + kQueries, nullptr, 2);
     }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const f4 last = rows_of(dec.last, it);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        x[it][i] = (last[i] != 0.0f ? last[i] * x[it][i] : 0.0f) + a.scale * y[it][i];
+        x[it][i] = (resets && last[i] == 0.0f ? 0.0f : last[i] * x[it][i]) + a.scale * y[it][i];
     }
-    if (dec.resets[kC - 1] > 0)
+    if (resets)
       keep_apart(x, [&](int i) { return dec.resets[i] == dec.resets[kC - 1]; });
     // E
     f4 e[4] = {};
     {
       bf8 p[2][kInvParts], q[kSome][kInvParts], xp[3];
 #pragma unroll
-      for (int jt = 0; jt < 2; ++jt) load_block<kInvParts>(invs, upper_block(jt, 0), p[jt]);
+      for (int jt = 0; jt < 2; ++jt) lds_block<kInvParts>(room, kInvs, upper_block(jt, 0), p[jt], me);
       split<3>(x[0], x[1], xp);
       mul_each<2>(p, xp, e);
       split<3>(x[2], x[3], xp);
 #pragma unroll
       for (int j0 = 0; j0 < 4; j0 += kSome) {
 #pragma unroll
-        for (int i = 0; i < kSome; ++i) load_block<kInvParts>(invs, upper_block(j0 + i, 1), q[i]);
+        for (int i = 0; i < kSome; ++i) lds_block<kInvParts>(room, kInvs, upper_block(j0 + i, 1), q[i], me);
         mul_each<2>(q, xp, e + j0);
       }
     }
@@ -890,17 +974,16 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_r
       y[it] = e[it];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        e[it][i] = first[i] < 0.0f ? 0.0f : -first[i] * e[it][i];
-        o[it][i] = first[i] < 0.0f ? 0.0f : a.scale * first[i] * o[it][i];
+        e[it][i] *= -first[i];
+        o[it][i] *= a.scale * first[i];
+        if (resets && first[i] < 0.0f) e[it][i] = o[it][i] = 0.0f;
       }
     }
     store_column<T, 4>(dvs + (int64_t)t0 * a.dv.st, a.dv.st, rows, col, a.DV, y);
     if constexpr (!kApart) __syncthreads();
     const float kept = dec.first[kC - 1];
 #pragma unroll
-    for (int dt = 0; dt < 2 * KT; ++dt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[dt][i] = kept < 0.0f ? 0.0f : kept * s[dt][i];
+    for (int dt = 0; dt < 2 * KT; ++dt) s[dt] = resets ? f4{} : s[dt] * kept;
 #pragma unroll
     for (int jt = 0; jt < 2; ++jt) {
       bf8 ep[3], op[3];
@@ -911,8 +994,8 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_r
         bf8 p[kSome][N], q[kSome][N];
 #pragma unroll
         for (int i = 0; i < kSome; ++i) {
-          load_block<N>(kcols, (d0 + i) * 2 + jt, p[i]);
-          load_block<N>(qcols, (d0 + i) * 2 + jt, q[i]);
+          lds_cols<N>(room, kCols, d0 + i, jt, p[i], me);
+          lds_cols<N>(room, kQueries, d0 + i, jt, q[i], me);
         }
         mul_each<2>(p, ep, s + d0);
         mul_each<2>(q, op, s + d0);
@@ -924,8 +1007,8 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 ? 1 : 4))) void delta_r
       } else {
         __syncthreads();
       }
-      char* next = room[kTwice ? flip : 0];
-      ahead.store(next, next + kTile, nullptr, next + 2 * kTile, next + kRoom - kPrep, kApart ? 3 : 1);
+      char* next = room + (kTwice ? flip * kRoom : 0);
+      ahead.store(next, next + kCols, nullptr, next + kQueries, next + kReady, kApart ? 3 : 1);
     }
     __syncthreads();
   }
@@ -1043,15 +1126,15 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
               const int it = wave, jt = p < 2 ? wave : (wave + p - 1) & 3;
               const bool up = p < 2 ? p == 0 : jt < it;
               bf8 x[NO], y[NO];
-              load_block<NO>(up ? us : gs, jt * 2 + kt, x, lane);
-              load_block<NO>(up ? gs : us, it * 2 + kt, y, lane);
+              load_rows<NO, 2>(up ? us : gs, jt, kt, x, lane);
+              load_rows<NO, 2>(up ? gs : us, it, kt, y, lane);
               pair[p] = mul<WEAK>(x, y, pair[p]);
             } else {
               const int id = (wave - 4) * 5 + p, k = id % 10;
               const int it = k < 1 ? 0 : k < 3 ? 1 : k < 6 ? 2 : 3, jt = k - it * (it + 1) / 2;
               bf8 x[NO], y[N];
-              load_block<NO>(us, jt * 2 + kt, x, lane);
-              load_block<N>(dos, it * 2 + kt, y, lane);
+              load_rows<NO, 2>(us, jt, kt, x, lane);
+              load_rows<N, 2>(dos, it, kt, y, lane);
               pair[p] = id < 10 ? mul<WEAK>(x, y, pair[p]) : mul<WEAK>(y, x, pair[p]);
             }
           }
@@ -1082,9 +1165,9 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
           for (int i = 0; i < NI; ++i) {
             __builtin_amdgcn_sched_barrier(0);
             bf8 od[N], ou[NO], og[NO];
-            load_block<N>(dos, (i0 + i) * 2 + kt, od, lane);
-            load_block<NO>(us, (i0 + i) * 2 + kt, ou, lane);
-            load_block<NO>(gs, (i0 + i) * 2 + kt, og, lane);
+            load_rows<N, 2>(dos, i0 + i, kt, od, lane);
+            load_rows<NO, 2>(us, i0 + i, kt, ou, lane);
+            load_rows<NO, 2>(gs, i0 + i, kt, og, lane);
             qs[i] = mul<WEAK>(od, xp, qs[i]);
             k1[i] = mul<WEAK>(ou, yp, k1[i]);
             k2[i] = mul<WEAK>(og, xp, k2[i]);
@@ -1145,7 +1228,7 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
 #pragma unroll
         for (int q = 0; q < N; ++q)
           kp[q] = *reinterpret_cast<const bf4*>(kcols + ((dt * 2 + it / 2) * N + q) * 1024 +
-                                                lane * 16 + it % 2 * 8);
+                                                (lane ^ col_turn(dt)) * 16 + it % 2 * 8);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int row = 16 * it + 4 * g + r;
@@ -1161,12 +1244,12 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
           bf8 y[N], x[NO];
-          load_block<N>(kcols, dt * 2 + kt, y, lane);
+          load_cols<N>(kcols, dt, kt, y, lane);
           if (kt <= it / 2) {
-            load_block<NO>(da, lower_block(it, kt), x, lane);
+            load_block<NO>(da + lower_block(it, kt) * NO * 1024, x, lane);
             qs[i] = mul<WEAK>(x, y, qs[i]);
           }
-          load_block<NO>(mm, it * 2 + kt, x, lane);
+          load_block<NO>(mm + (it * 2 + kt) * NO * 1024, x, lane);
           k1[i] = mul<WEAK>(x, y, k1[i]);
         }
       }
@@ -1183,15 +1266,15 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
         for (int kt = 0; kt < 2; ++kt) {
           if (kt < it / 2) continue;
           bf8 y[N], x[NO];
-          load_block<N>(qcols, dt * 2 + kt, y, lane);
-          load_block<NO>(dt_, upper_block(it, kt), x, lane);
+          load_cols<N>(qcols, dt, kt, y, lane);
+          load_block<NO>(dt_ + upper_block(it, kt) * NO * 1024, x, lane);
           k1[i] = mul<WEAK>(x, y, k1[i]);
         }
         bf4 qp[N];
 #pragma unroll
         for (int q = 0; q < N; ++q)
           qp[q] = *reinterpret_cast<const bf4*>(qcols + ((dt * 2 + it / 2) * N + q) * 1024 +
-                                                lane * 16 + it % 2 * 8);
+                                                (lane ^ col_turn(dt)) * 16 + it % 2 * 8);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           float x = 0.0f;

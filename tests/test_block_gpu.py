@@ -402,6 +402,21 @@ def test_delta_views():
     assert all(same(x, y) for x, y in zip(got, want))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_delta_expanded_inputs(dtype):
+    """Steps, heads and sequences that share their rows."""
+    p = per()
+    host, dev = delta_case(2, 90, 2, 2, 32, 40, dtype, 7, wide=False)
+    for a in (host, dev):
+        a["length"] = torch.tensor([70, 90]).to(a["q"].device)
+        a["q"] = a["q"][:, :1].expand(-1, 90, -1, -1)
+        a["k"] = a["k"][:, :, :1].expand(-1, -1, 2, -1)
+        a["v"] = a["v"][:, :1].expand(-1, 90, -1, -1)
+        a["do"] = a["do"][:1, :1].expand(2, 90, -1, -1)
+        a["g"] = a["g"][:, :1].expand(-1, 90, -1)
+    check_delta(dev, {k: v.contiguous() if torch.is_tensor(v) else v for k, v in host.items()}, dtype)
+
+
 @pytest.mark.parametrize("B,H,HK,DK,DV", [(1, 1, 1, 1, 1), (3, 2, 1, 64, 64), (5, 4, 2, 33, 65), (2, 2, 2, 128, 128),
                                           (2, 1, 1, 100, 256), (70, 3, 3, 17, 129)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
