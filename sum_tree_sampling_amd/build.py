@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libper.so")
 SOURCES = ["per_api.hip", "tree_kernels.hip", "sample_kernels.hip", "rank_kernels.hip",
            "train_api.hip", "rows_kernels.hip", "scan_kernels.hip", "distill_kernels.hip",
-           "block_api.hip", "embed_kernels.hip", "norm_kernels.hip", "delta_kernels.hip"]
+           "block_api.hip", "embed_kernels.hip", "norm_kernels.hip", "delta_forward.hip",
+           "delta_backward.hip"]
 PROBE_SRC = os.path.join(HERE, "probe", "latency_probe.hip")
 PROBE_LIB = os.path.join(HERE, "libper_probe.so")
 STAMPS_LIB = os.path.join(HERE, "libper_stamps.so")

@@ -70,6 +70,11 @@ struct DeltaArgs {
   void* prep;             // per (sequence, chunk, head): what prepare_kernel leaves
   float* dstate;          // backward: gradient of the state behind each chunk
   float* e;               // backward: [B x chunks x H x 64 x DV] E
+  int segments;           // of the time axis, 1: not cut
+  int segment_chunks;
+  float* states;          // [B x H x segments x DK x DV] that segments begin with
+  float* locals;          // [..] what a segment makes of a state of 0
+  float* maps;            // [B x H x segments x DK x DK] what it makes of the unit columns
 };
 size_t delta_workspace(int64_t B, int64_t T, int64_t H, int64_t DK, int64_t DV, int type,
                        bool backward, DeltaArgs* a, void* ws);

@@ -1,0 +1,571 @@
+// delta_backward.hip -- the gated delta rule: the backward pass.
+#include "delta_common.h"
+
+namespace per {
+namespace {
+
+// Backward in time: dS behind each chunk, E, and dV.
+template <typename T, int KT, int WAVES, bool LOCAL>
+__global__ __launch_bounds__(64 * WAVES)
+__attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 && !LOCAL ? 1 : 4))) void delta_reverse_kernel(
+    DeltaArgs a, int slices) {
+  constexpr int N = kParts<T>;
+  constexpr int kTile = 4 * KT * N * 1024, kPrep = (int)prep_bytes(3);
+  constexpr bool kApart = N < 3;
+  constexpr int kRoom = (kApart ? 3 : 2) * kTile + kPrep;
+  constexpr int kSome = 2;  // blocks that are held at a time
+  constexpr bool kTwice = !LOCAL && 2 * kRoom <= 160 * 1024;
+  __shared__ __attribute__((aligned(16))) char room[(kTwice ? 2 : 1) * kRoom];
+  constexpr int kCols = kTile, kQueries = kApart ? 2 * kTile : 0, kReady = kRoom - kPrep;
+  constexpr int kInvs = kReady + (int)sizeof(Decays), kScores = kInvs + 6 * kInvParts * 1024;
+
+  const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  int bh, b, h, hk, slice, rest;
+  divide(blockIdx.x % (uint32_t)(a.B * a.H * slices), (uint32_t)slices, bh, slice);
+  divide((uint32_t)bh, (uint32_t)a.H, b, h);
+  divide((uint32_t)h, (uint32_t)(a.H / a.HK), hk, rest);
+  int seg = 0;
+  if (a.segments > 1) divide((uint32_t)blockIdx.x, (uint32_t)(a.B * a.H * slices), seg, rest);
+  const int64_t place = (int64_t)bh * a.segments + seg;
+  const int behind = LOCAL ? (a.DV + 16 * WAVES - 1) / (16 * WAVES) : slices;
+  const bool unit_columns = LOCAL && slice >= behind;
+  const int col = ((unit_columns ? slice - behind : slice) * WAVES + wave) * 16 + n;
+  const int steps = steps_of(a, b);
+  const int from = seg * a.segment_chunks * kC;
+  const int end = a.segments > 1 ? min(steps, from + a.segment_chunks * kC) : steps;
+  const int64_t unit0 = (int64_t)b * a.chunks * a.H + h;
+  const T *ks = at<T>(a.k, b, 0, hk), *qs = at<T>(a.q, b, 0, hk), *os = at<T>(a.o, b, 0, h);
+  const bool even = even_rows(ks, a.k.st, a.DK) && even_rows(qs, a.q.st, a.DK);
+  T* dvs = const_cast<T*>(at<T>(a.dv, b, 0, h));
+
+  f4 s[2 * KT];
+  if constexpr (LOCAL) {
+    unit_state<2 * KT>(unit_columns ? col : -1, s);
+  } else if (a.segments > 1) {
+    load_state<2 * KT>(a.states + place * a.DK * a.DV, a.DK, a.DV, col, s);
+  } else {
+    load_state<2 * KT>(a.s0 ? a.s0 + (int64_t)bh * a.DK * a.DV : nullptr, a.DK, a.DV, col, s);
+  }
+  const int width = unit_columns ? 0 : a.DV;  // no outputs' gradient
+  Ahead<T, KT, 64 * WAVES, kPrep, true> ahead;
+  T d[4][4];  // dO
+  const int tail = end > from ? (end - 1) / kC * kC : from - kC;  // the last chunk
+  if (end > from) {
+    ahead.load(ks + (int64_t)tail * a.k.st, a.k.st, qs + (int64_t)tail * a.q.st, a.q.st, even, a.DK,
+               end - tail, static_cast<const char*>(a.prep) + (unit0 + tail / kC * a.H) * kPrep);
+    load_column<T, 4>(os + (int64_t)tail * a.o.st, a.o.st, end - tail, col, width, d);
+    ahead.store(room, room + kCols, nullptr, room + kQueries, room + kReady, kApart ? 3 : 1);
+  }
+  __syncthreads();
+  for (int t0 = tail, flip = 0; t0 >= from; t0 -= kC) {
+    const int rows = min(kC, end - t0);
+    const int64_t unit = unit0 + t0 / kC * a.H;
+    char* now = room + (kTwice ? flip * kRoom : 0);
+    const Decays& dec = *reinterpret_cast<const Decays*>(now + kReady);
+    const bool resets = __builtin_amdgcn_readfirstlane(dec.resets[kC - 1]) != 0;
+    uint32_t me = (uint32_t)(now - room) + (uint32_t)lane * 16;
+    asm volatile("" : "+v"(me));
+    f4 o[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[it][i] = (float)d[it][i];
+    Ahead<T, KT, 64 * WAVES, kPrep, true> queries;
+    if constexpr (!kApart) queries = ahead;
+    if (t0 > from) {
+      ahead.load(ks + (int64_t)(t0 - kC) * a.k.st, a.k.st, qs + (int64_t)(t0 - kC) * a.q.st, a.q.st, even,
+                 a.DK, kC, static_cast<const char*>(a.prep) + (unit - a.H) * kPrep);
+      load_column<T, 4>(os + (int64_t)(t0 - kC) * a.o.st, a.o.st, kC, col, width, d);
+    }
+    if constexpr (!LOCAL)
+      store_column<float, 2 * KT>(a.dstate + unit * a.DK * a.DV, a.DV, a.DK, col, a.DV, s);
+
+    // d K dS + scale P^T dO
+    f4 x[4] = {}, y[4] = {};
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      bf8 sp[3], kp[4][N];
+#pragma unroll
+      for (int it = 0; it < 4; ++it) lds_rows<N, KT>(room, 0, it, kt, kp[it], me);
+      split<3>(s[2 * kt], s[2 * kt + 1], sp);
+      mul_each<2>(kp, sp, x);
+    }
+    {
+      bf8 p[2][3], q[kSome][3], op[N];
+#pragma unroll
+      for (int jt = 0; jt < 2; ++jt) lds_block<3>(room, kScores, upper_block(jt, 0), p[jt], me);
+      split<N>(o[0], o[1], op);
+      mul_each<2>(p, op, y);
+      split<N>(o[2], o[3], op);
+#pragma unroll
+      for (int j0 = 0; j0 < 4; j0 += kSome) {
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) lds_block<3>(room, kScores, upper_block(j0 + i, 1), q[i], me);
+        mul_each<2>(q, op, y + j0);
+      }
+    }
+    if constexpr (!kApart) {
+      __syncthreads();  // the keys' rows make room for the queries
+      queries.store(nullptr, nullptr, nullptr, now + kQueries, nullptr, 2);
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const f4 last = rows_of(dec.last, it);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[it][i] = (resets && last[i] == 0.0f ? 0.0f : last[i] * x[it][i]) + a.scale * y[it][i];
+    }
+    if (resets)
+      keep_apart(x, [&](int i) { return dec.resets[i] == dec.resets[kC - 1]; });
+    // E
+    f4 e[4] = {};
+    {
+      bf8 p[2][kInvParts], q[kSome][kInvParts], xp[3];
+#pragma unroll
+      for (int jt = 0; jt < 2; ++jt) lds_block<kInvParts>(room, kInvs, upper_block(jt, 0), p[jt], me);
+      split<3>(x[0], x[1], xp);
+      mul_each<2>(p, xp, e);
+      split<3>(x[2], x[3], xp);
+#pragma unroll
+      for (int j0 = 0; j0 < 4; j0 += kSome) {
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) lds_block<kInvParts>(room, kInvs, upper_block(j0 + i, 1), q[i], me);
+        mul_each<2>(q, xp, e + j0);
+      }
+    }
+    if constexpr (!LOCAL) store_column<float, 4>(a.e + unit * kC * a.DV, a.DV, kC, col, a.DV, e);
+    // dV, then what goes back to the state before the chunk
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const f4 first = rows_of(dec.first, it);
+      e[it] = e[it] * rows_of(dec.w, it);
+      y[it] = e[it];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        e[it][i] *= -first[i];
+        o[it][i] *= a.scale * first[i];
+        if (resets && first[i] < 0.0f) e[it][i] = o[it][i] = 0.0f;
+      }
+    }
+    if constexpr (!LOCAL) store_column<T, 4>(dvs + (int64_t)t0 * a.dv.st, a.dv.st, rows, col, a.DV, y);
+    if constexpr (!kApart) __syncthreads();
+    const float kept = dec.first[kC - 1];
+#pragma unroll
+    for (int dt = 0; dt < 2 * KT; ++dt) s[dt] = resets ? f4{} : s[dt] * kept;
+#pragma unroll
+    for (int jt = 0; jt < 2; ++jt) {
+      bf8 ep[3], op[3];
+      split<3>(e[2 * jt], e[2 * jt + 1], ep);
+      split<3>(o[2 * jt], o[2 * jt + 1], op);
+#pragma unroll
+      for (int d0 = 0; d0 < 2 * KT; d0 += kSome) {
+        bf8 p[kSome][N], q[kSome][N];
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) {
+          lds_cols<N>(room, kCols, d0 + i, jt, p[i], me);
+          lds_cols<N>(room, kQueries, d0 + i, jt, q[i], me);
+        }
+        mul_each<2>(p, ep, s + d0);
+        mul_each<2>(q, op, s + d0);
+      }
+    }
+    if (t0 > from) {
+      if (kTwice) {
+        flip ^= 1;
+      } else {
+        __syncthreads();
+      }
+      char* next = room + (kTwice ? flip * kRoom : 0);
+      ahead.store(next, next + kCols, nullptr, next + kQueries, next + kReady, kApart ? 3 : 1);
+    }
+    __syncthreads();
+  }
+  if constexpr (LOCAL) {
+    float* to = unit_columns ? a.maps + place * a.DK * a.DK : a.locals + place * a.DK * a.DV;
+    const int wide = unit_columns ? a.DK : a.DV;
+    store_column<float, 2 * KT>(to, wide, a.DK, col, wide, s);
+  } else {
+    if (a.s_last && seg == 0)
+      store_column<float, 2 * KT>(a.s_last + (int64_t)bh * a.DK * a.DV, a.DV, a.DK, col, a.DV, s);
+    const int64_t stop = a.segments > 1 ? min(a.T, (int64_t)from + a.segment_chunks * kC) : a.T;
+    for (int64_t t = max(from, steps) + g; t < stop; t += 4)
+      if (col < a.DV) dvs[t * a.dv.st + col] = (T)0.0f;
+  }
+}
+
+// dQ, dK and the gradients of gates and strengths, for each (sequence, chunk, head of
+// keys): 8 waves.  What sums over the state's columns takes 64 of them at a time; a wave
+// has 16 columns of dQ and dK (dt) and NI of the chunk's 4 groups of rows.
+template <typename T, int KT>
+__global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
+  constexpr int N = kParts<T>, NO = kOutParts<T>, WEAK = kWeak<T>;
+  constexpr int kDt = 2 * KT, NI = kDt / 2;
+  constexpr int kTile = 4 * KT * N * 1024;
+  constexpr int kStage = (8 * N + 16 * NO) * 1024, kPairs = 20 * NO * 1024;
+  constexpr bool kApart = N < 3;
+  __shared__ __attribute__((aligned(16))) char space[kStage > kPairs ? kStage : kPairs];
+  __shared__ __attribute__((aligned(16))) char kcols_[kTile], qcols_[kApart ? kTile : 16];
+  __shared__ __attribute__((aligned(16))) Decays dec;
+  __shared__ float eu[kC], gv[kC], qd[kDt][kC], ends[8][2];
+  char *dos = space, *us = dos + 8 * N * 1024, *gs = us + 8 * NO * 1024;
+  char *da = space, *dt_ = da + 6 * NO * 1024, *mm = dt_ + 6 * NO * 1024;
+  char *kcols = kcols_, *qcols = kApart ? qcols_ : kcols_;
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  int b, c, hk;
+  divide(blockIdx.x, (uint32_t)a.HK, b, hk);
+  divide((uint32_t)b, (uint32_t)a.chunks, b, c);
+  const int shared = a.H / a.HK;
+  const int64_t t0 = (int64_t)c * kC;
+  const int steps = steps_of(a, b), rows = min(kC, steps - (int)t0);
+  const int here = (int)min((int64_t)kC, a.T - t0);  // rows that are written
+  const int dt = wave % kDt, i0 = wave / kDt * NI;
+  f4 dq[NI] = {}, dk[NI] = {};
+
+  if (rows > 0) {
+    for (int gi = 0; gi < shared; ++gi) {
+      // else every place in LDS is computed before this loop, and registers run out
+      int lane = threadIdx.x & 63;
+      asm volatile("" : "+v"(lane));
+      const int g = lane / 16, n = lane % 16, dcol = 16 * dt + n;
+      const int h = hk * shared + gi;
+      const int64_t unit = ((int64_t)b * a.chunks + c) * a.H + h;
+      const float* s0 = a.carries + unit * carry_size(a.DK, a.DV);
+      const float* u = s0 + (int64_t)a.DK * a.DV;
+      const float* ds = a.dstate + unit * a.DK * a.DV;
+      const float* e = a.e + unit * kC * a.DV;
+      f4 qs[NI] = {}, k1[NI] = {}, k2[NI] = {}, pair[5] = {};
+      float ss = 0.0f;
+      __syncthreads();
+      copy16(reinterpret_cast<char*>(&dec), static_cast<const char*>(a.prep) + unit * prep_bytes(3),
+             sizeof(Decays));
+      if (threadIdx.x < kC) eu[threadIdx.x] = gv[threadIdx.x] = 0.0f;
+      if (kApart && gi == 0) {
+        stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, nullptr, kcols);
+        stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, nullptr, qcols);
+      }
+      for (int v0 = 0; v0 < a.DV; v0 += 64) {
+        __syncthreads();
+        const int width = a.DV - v0;
+        {
+          // 128 threads each: U; dO; G and the sums E.U; the sums G.V
+          const int pa = wave % 2 * 8 + lane / 8, pm = lane % 8, job = wave / 2;
+          if (job == 0) {
+            Piece<float> x;
+            load_piece<float>(u + v0, a.DV, kC, width, pa, pm, x);
+            store_piece<NO, 2, float>(x, pa, pm, us, nullptr);
+          } else if (job == 1) {
+            Piece<T> x;
+            load_piece<T>(at<T>(a.o, b, t0, h) + v0, a.o.st, rows, width, pa, pm, x);
+            store_piece<N, 2, T>(x, pa, pm, dos, nullptr);
+          } else {
+            Piece<float> p;
+            float x[4][8], y[4][8];
+            load_piece<float>(e + v0, a.DV, kC, width, pa, pm, p);
+            unpack_piece<float>(p, x);
+            if (job == 2) {
+              load_piece<float>(u + v0, a.DV, kC, width, pa, pm, p);
+              unpack_piece<float>(p, y);
+            } else {
+              Piece<T> q;
+              load_piece<T>(at<T>(a.v, b, t0, h) + v0, a.v.st, rows, width, pa, pm, q);
+              unpack_piece<T>(q, y);
+            }
+            float sum[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float w = dec.w[4 * pa + r];
+              sum[r] = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                sum[r] += x[r][k] * y[r][k];
+                x[r][k] *= w;
+              }
+              if (job == 3) sum[r] *= w;
+#pragma unroll
+              for (int q = 0; q < 3; ++q) sum[r] += xor_lanes(sum[r], q);
+              if (pm == 0) (job == 2 ? eu : gv)[4 * pa + r] += sum[r];
+            }
+            if (job == 2) store_piece<NO, 2>(x, pa, pm, gs);
+          }
+        }
+        __syncthreads();
+        // 64 x 64 products: waves 0 to 3 G U^T, twice for the 16 x 16 on the diagonal (once
+        // for each side of it), waves 4 to 7 dO U^T and its transpose
+#pragma unroll 1
+        for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+          for (int p = 0; p < 5; ++p) {
+            __builtin_amdgcn_sched_barrier(0);  // else all loads come first, and registers run out
+            if (wave < 4) {
+              // rows j, columns i: U_j G_i above the diagonal of this result, G_j U_i below
+              const int it = wave, jt = p < 2 ? wave : (wave + p - 1) & 3;
+              const bool up = p < 2 ? p == 0 : jt < it;
+              bf8 x[NO], y[NO];
+              load_rows<NO, 2>(up ? us : gs, jt, kt, x, lane);
+              load_rows<NO, 2>(up ? gs : us, it, kt, y, lane);
+              pair[p] = mul<WEAK>(x, y, pair[p]);
+            } else {
+              const int id = (wave - 4) * 5 + p, k = id % 10;
+              const int it = k < 1 ? 0 : k < 3 ? 1 : k < 6 ? 2 : 3, jt = k - it * (it + 1) / 2;
+              bf8 x[NO], y[N];
+              load_rows<NO, 2>(us, jt, kt, x, lane);
+              load_rows<N, 2>(dos, it, kt, y, lane);
+              pair[p] = id < 10 ? mul<WEAK>(x, y, pair[p]) : mul<WEAK>(y, x, pair[p]);
+            }
+          }
+        }
+        // dO S^T, U dS^T, G S^T
+#pragma unroll 1
+        for (int kt = 0; kt < 2; ++kt) {
+          const int v = v0 + 32 * kt + 4 * g;
+          f4 x[2], y[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float p[4] = {}, q[4] = {};
+            if (dcol < a.DK) {
+              load_few<float, 4>(s0 + (int64_t)dcol * a.DV, v + 16 * k, a.DV, p);
+              load_few<float, 4>(ds + (int64_t)dcol * a.DV, v + 16 * k, a.DV, q);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              x[k][r] = p[r];
+              y[k][r] = q[r];
+              ss += p[r] * q[r];
+            }
+          }
+          bf8 xp[NO], yp[NO];
+          split<NO>(x[0], x[1], xp);
+          split<NO>(y[0], y[1], yp);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            bf8 od[N], ou[NO], og[NO];
+            load_rows<N, 2>(dos, i0 + i, kt, od, lane);
+            load_rows<NO, 2>(us, i0 + i, kt, ou, lane);
+            load_rows<NO, 2>(gs, i0 + i, kt, og, lane);
+            qs[i] = mul<WEAK>(od, xp, qs[i]);
+            k1[i] = mul<WEAK>(ou, yp, k1[i]);
+            k2[i] = mul<WEAK>(og, xp, k2[i]);
+          }
+        }
+      }
+      __syncthreads();
+      // the 64 x 64 matrices with their decays, as operands
+      if (wave < 4) {
+        const int it = wave;
+#pragma unroll
+        for (int p = 0; p < 5; ++p) {
+          if (p == 1) continue;
+          __builtin_amdgcn_sched_barrier(0);
+          const int jt = p < 2 ? wave : (wave + p - 1) & 3;
+          f4 v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 16 * it + n, j = 16 * jt + 4 * g + r;
+            const float x = p == 0 && j > i ? pair[1][r] : pair[p][r];
+            v[r] = i == j ? 0.0f : -x * decay(dec, max(i, j), min(i, j));
+          }
+          store_half<NO>(mm, it * 2 + jt / 2, jt % 2, v, lane);
+        }
+        const f4 zero = {};
+        if (wave == 0) store_half<NO>(da, lower_block(0, 0), 1, zero, lane);
+        if (wave == 1) store_half<NO>(da, lower_block(2, 1), 1, zero, lane);
+        if (wave == 2) store_half<NO>(dt_, upper_block(1, 0), 0, zero, lane);
+        if (wave == 3) store_half<NO>(dt_, upper_block(3, 1), 0, zero, lane);
+      } else {
+#pragma unroll
+        for (int p = 0; p < 5; ++p) {
+          const int id = (wave - 4) * 5 + p, k = id % 10;
+          const int it = k < 1 ? 0 : k < 3 ? 1 : k < 6 ? 2 : 3, jt = k - it * (it + 1) / 2;
+          __builtin_amdgcn_sched_barrier(0);
+          f4 v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 16 * it + (id < 10 ? n : 4 * g + r);
+            const int j = 16 * jt + (id < 10 ? 4 * g + r : n);
+            v[r] = j <= i ? a.scale * pair[p][r] * decay(dec, i, j) : 0.0f;
+          }
+          if (id < 10) {
+            store_half<NO>(da, lower_block(it, jt / 2), jt % 2, v, lane);
+          } else {
+            store_half<NO>(dt_, upper_block(jt, it / 2), it % 2, v, lane);
+          }
+        }
+      }
+      if (!kApart) stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, nullptr, kcols);
+      __syncthreads();
+      float end = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        const int it = i0 + i;
+        bf4 kp[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          kp[q] = *reinterpret_cast<const bf4*>(kcols + ((dt * 2 + it / 2) * N + q) * 1024 +
+                                                (lane ^ col_turn(dt)) * 16 + it % 2 * 8);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * it + 4 * g + r;
+          const float first = dec.first[row], last = dec.last[row];
+          float kx = 0.0f;
+#pragma unroll
+          for (int q = N - 1; q >= 0; --q) kx += (float)kp[q][r];
+          qs[i][r] = first >= 0.0f ? qs[i][r] * (a.scale * first) : 0.0f;
+          k1[i][r] = last != 0.0f ? k1[i][r] * last : 0.0f;
+          end += kx * k1[i][r];
+          if (first >= 0.0f) k1[i][r] -= first * k2[i][r];
+        }
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          bf8 y[N], x[NO];
+          load_cols<N>(kcols, dt, kt, y, lane);
+          if (kt <= it / 2) {
+            load_block<NO>(da + lower_block(it, kt) * NO * 1024, x, lane);
+            qs[i] = mul<WEAK>(x, y, qs[i]);
+          }
+          load_block<NO>(mm + (it * 2 + kt) * NO * 1024, x, lane);
+          k1[i] = mul<WEAK>(x, y, k1[i]);
+        }
+      }
+      if (!kApart) {
+        __syncthreads();
+        stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, nullptr, qcols);
+        __syncthreads();
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        const int it = i0 + i;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          if (kt < it / 2) continue;
+          bf8 y[N], x[NO];
+          load_cols<N>(qcols, dt, kt, y, lane);
+          load_block<NO>(dt_ + upper_block(it, kt) * NO * 1024, x, lane);
+          k1[i] = mul<WEAK>(x, y, k1[i]);
+        }
+        bf4 qp[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          qp[q] = *reinterpret_cast<const bf4*>(qcols + ((dt * 2 + it / 2) * N + q) * 1024 +
+                                                (lane ^ col_turn(dt)) * 16 + it % 2 * 8);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float x = 0.0f;
+#pragma unroll
+          for (int q = N - 1; q >= 0; --q) x += (float)qp[q][r];
+          x *= qs[i][r];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x += xor_lanes(x, q);
+          if (n == 0) qd[dt][16 * it + 4 * g + r] = x;
+        }
+        dq[i] += qs[i];
+        dk[i] += k1[i];
+      }
+      // dS . S behind the chunk
+      if (i0 > 0) ss = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 6; ++q) {
+        end += xor_lanes(end, q);
+        ss += xor_lanes(ss, q);
+      }
+      if (lane == 0) {
+        ends[wave][0] = end;
+        ends[wave][1] = ss;
+      }
+      __syncthreads();
+      if (wave == 0) {
+        double z = 0.0, last = 0.0, across = 0.0;
+#pragma unroll
+        for (int k = 0; k < kDt; ++k) z += qd[k][lane];
+        z -= gv[lane];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          last += ends[k][0];
+          across += ends[k][1];
+        }
+        const float kept = dec.first[kC - 1];
+        if (kept >= 0.0f) last += (double)kept * across;
+        if (lane == kC - 1) z += last;
+        const int mine = dec.resets[lane];
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+          const double o = __shfl_down(z, d);
+          const int theirs = __shfl_down(mine, d);
+          if (lane + d < 64 && theirs == mine) z += o;
+        }
+        const int before = __shfl_up(mine, 1);
+        const bool reset = lane == 0 ? mine != 0 : mine != before;
+        if (lane < here) {
+          const bool on = lane < rows;
+          const float gate = on ? (float)*at<T>(a.g, b, t0 + lane, h) : 0.0f;
+          const float wt = on ? (float)*at<T>(a.b, b, t0 + lane, h) : 0.0f;
+          *const_cast<T*>(at<T>(a.dg, b, t0 + lane, h)) =
+              (T)(on && !reset ? (float)z / (1.0f + expf(gate)) : 0.0f);
+          *const_cast<T*>(at<T>(a.db, b, t0 + lane, h)) =
+              (T)(on ? eu[lane] / (1.0f + expf(wt)) : 0.0f);
+        }
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < here * shared; i += 512) {
+      const int64_t t = t0 + i / shared;
+      const int h = hk * shared + i % shared;
+      *const_cast<T*>(at<T>(a.dg, b, t, h)) = (T)0.0f;
+      *const_cast<T*>(at<T>(a.db, b, t, h)) = (T)0.0f;
+    }
+  }
+  int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // the places of dQ and dK are computed here, not before the loop
+  const int g = lane / 16, dcol = 16 * dt + lane % 16;
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * (i0 + i) + 4 * g + r;
+      if (row < here && dcol < a.DK) {
+        const_cast<T*>(at<T>(a.dq, b, t0 + row, hk))[dcol] = (T)(row < rows ? dq[i][r] : 0.0f);
+        const_cast<T*>(at<T>(a.dk, b, t0 + row, hk))[dcol] = (T)(row < rows ? dk[i][r] : 0.0f);
+      }
+    }
+}
+
+template <typename T, int KT>
+struct Columns {
+  static constexpr int most = kParts<T> == 3 || (kParts<T> == 2 && KT == 4) ? 4 : 8;
+  static constexpr auto four = delta_reverse_kernel<T, KT, 4, false>;
+  static constexpr auto eight = delta_reverse_kernel<T, KT, most, false>;
+};
+
+}  // namespace
+
+hipError_t launch_delta_backward(const DeltaArgs& a, int type, hipStream_t s) {
+  hipError_t e = a.chunks > 0 ? launch_prepare<true>(a, type, s) : hipSuccess;
+  if (e != hipSuccess) return e;
+  return by_type(type, [&](auto tag) {
+    return by_keys(a.DK, [&](auto keys) {
+      using T = typename decltype(tag)::type;
+      constexpr int KT = decltype(keys)::value;
+      using K = Columns<T, KT>;
+      const uint32_t heads = (uint32_t)(a.B * a.H);
+      hipError_t e = hipSuccess;
+      if (a.segments > 1) {
+        const int slices = (a.DV + 63) / 64 + (a.DK + 63) / 64;
+        e = enqueue(delta_reverse_kernel<T, KT, 4, true>, dim3(heads * slices * a.segments), dim3(256), 0, s, a,
+                    slices);
+        if (e == hipSuccess) e = launch_join<true>(a, s);
+        if (e != hipSuccess) return e;
+      }
+      const int waves = column_waves(a, type), slices = (a.DV + 16 * waves - 1) / (16 * waves);
+      e = enqueue(waves == 4 ? K::four : K::eight, dim3(heads * slices * a.segments), dim3(64 * waves), 0, s, a,
+                  slices);
+      if (e != hipSuccess || a.chunks == 0) return e;
+      return enqueue(delta_gradient_kernel<T, KT>, dim3((uint32_t)(a.B * a.chunks * a.HK)), dim3(512), 0, s, a);
+    });
+  });
+}
+
+}  // namespace per

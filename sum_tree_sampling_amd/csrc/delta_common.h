@@ -1,0 +1,800 @@
+// delta_common.h -- the gated delta rule: what its passes have in common.
+//
+// A chunk of 64 steps at a time.  With D_ij the product of the gates of steps j + 1 to i
+// (0 across a reset), gamma_i that of the steps up to i, d_j that of the steps behind j,
+// and A_ij = w_i D_ij k_i.k_j below the diagonal, what the state takes up is
+//     U = (I + A)^-1 w (V - gamma K S),
+// the outputs are scale (gamma Q S + (Q K^T . D) U), and the state goes on as
+// gamma_63 S + (d K)^T U.  Backward, with P = scale (Q K^T . D) and dS the gradient of
+// the state behind the chunk,
+//     E = (I + A)^-T (P^T dO + d K dS),   G = w E = dV,
+//     dS' = gamma_63 dS + scale (gamma Q)^T dO - (gamma K)^T G,
+//     dQ = scale gamma dO S^T + (scale dO U^T . D) K,
+//     dK = d U dS^T + (scale dO U^T . D)^T Q - gamma G S^T - (M + M^T) K,  M = G U^T . D,
+//     the gradient by the logit of w is (1 - w) E.U, and that by log f_i the sum of
+//     q_j.dq_j - v_j.dv_j over the steps j >= i of the chunk and dS.S behind it
+// (all by rows; D is scale-free, a reset ends each sum).
+//
+// What does not depend on the state ((I + A)^-1, Q K^T . D, the decays) is prepared for
+// all chunks at once; one pass then walks over the chunks of a sequence with a slice of
+// the state's columns in each wave's registers (the columns are independent), forward
+// in time, or backward for dS; and the rest of the backward pass takes all chunks at
+// once again.
+//
+// Products run on the bf16 matrix units, f32 factors as sums of three bf16 values (24
+// bits; products below 2^-24 of the largest are left out), 16-bit inputs as one or two:
+// 16 times the f32 units' rate, for 3 to 6 products.  Where only an output in 16 bits
+// depends on it, two values (16 bits) do.
+//
+// The layout of a 16 x 16 result (lane 16 g + n has rows 4 g .. 4 g + 3 of column n) is
+// that of half an operand of the next product, if the 32 terms of a sum are taken in the
+// order rows 4 g + e of the first 16, then of the second: results feed products without
+// a move.  Operands are kept in that order as blocks of 16 bytes for each lane.
+#pragma once
+
+#include <algorithm>
+
+#include "block_internal.h"
+#include "elem.h"
+#include "lanes.h"
+
+namespace per {
+namespace {
+
+constexpr int kC = PER_DELTA_CHUNK;
+typedef bf16_t bf8 __attribute__((ext_vector_type(8)));
+typedef bf16_t bf4 __attribute__((ext_vector_type(4)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Tag {
+  using type = T;
+};
+
+// bf16 values that hold one of the type, and the weakest products that are taken of
+// those behind an output of it: parts i and j where i + j <= kWeak.
+template <typename T>
+constexpr int kParts = 3;
+template <>
+constexpr int kParts<bf16_t> = 1;
+template <>
+constexpr int kParts<f16_t> = 2;
+template <typename T>
+constexpr int kOutParts = sizeof(T) == 4 ? 3 : 2;
+template <typename T>
+constexpr int kWeak = kOutParts<T> - 1;
+
+// 8 values as N bf16 parts, each the rounding of what the ones before leave.
+template <int N>
+__device__ __forceinline__ void split(const f4& lo, const f4& hi, bf8 (&p)[N]) {
+  typedef float f8 __attribute__((ext_vector_type(8)));
+  f8 x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    p[i] = __builtin_convertvector(x, bf8);
+    if (i + 1 < N) x = x - __builtin_convertvector(p[i], f8);
+  }
+}
+template <int N>
+__device__ __forceinline__ void split4(f4 x, bf4 (&p)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    p[i] = __builtin_convertvector(x, bf4);
+    if (i + 1 < N) x = x - __builtin_convertvector(p[i], f4);
+  }
+}
+
+// c + a b over 32 terms, from the parts of a and b, the weakest products first.
+template <int WEAK, int NA, int NB>
+__device__ __forceinline__ f4 mul(const bf8 (&a)[NA], const bf8 (&b)[NB], f4 c) {
+#pragma unroll
+  for (int s = WEAK; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[s - i], c, 0, 0, 0);
+  return c;
+}
+
+// The same for several a: the products of one sum lie COUNT instructions apart.
+template <int WEAK, int COUNT, int NA, int NB>
+__device__ __forceinline__ void mul_each(const bf8 (&a)[COUNT][NA], const bf8 (&b)[NB], f4* c) {
+#pragma unroll
+  for (int s = WEAK; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k)
+          c[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[k][i], b[s - i], c[k], 0, 0, 0);
+}
+
+// Operand blocks: N parts of 64 lanes of 16 bytes each.  As they are copied (what is
+// prepared, in memory and LDS) lane l's lie at 16 l; where pieces of rows are put together
+// in LDS at 16 (l ^ turn), with a turn for each block, or the pieces that a wave writes at
+// once would meet in few of the banks.
+template <int N>
+__device__ __forceinline__ void load_block(const char* block, bf8 (&p)[N], uint32_t lane) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    p[i] = *reinterpret_cast<const bf8*>(block + i * 1024 + lane * 16);
+}
+// Rows 16 it.. of 32 KT terms; the 32 rows 32 jt.. as the terms of columns 16 dt..
+__device__ __forceinline__ constexpr int row_turn(int kt) { return kt & 3; }
+__device__ __forceinline__ constexpr int col_turn(int dt) { return dt & 7; }
+template <int N, int KT>
+__device__ __forceinline__ void load_rows(const char* rows, int it, int kt, bf8 (&p)[N], uint32_t lane) {
+  load_block<N>(rows + (it * KT + kt) * N * 1024, p, lane ^ row_turn(kt));
+}
+template <int N>
+__device__ __forceinline__ void load_cols(const char* cols, int dt, int jt, bf8 (&p)[N], uint32_t lane) {
+  load_block<N>(cols + (dt * 2 + jt) * N * 1024, p, lane ^ col_turn(dt));
+}
+// The same at a constant place of an array, by the offset 16 lane of a buffer in it.
+template <int N>
+__device__ __forceinline__ void lds_block(const char* room, int place, int n, bf8 (&p)[N], uint32_t me) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    p[i] = *reinterpret_cast<const bf8*>(room + me + (place + (n * N + i) * 1024));
+}
+template <int N, int KT>
+__device__ __forceinline__ void lds_rows(const char* room, int place, int it, int kt, bf8 (&p)[N], uint32_t me) {
+  lds_block<N>(room, place, it * KT + kt, p, me ^ (row_turn(kt) * 16));
+}
+template <int N>
+__device__ __forceinline__ void lds_cols(const char* room, int place, int dt, int jt, bf8 (&p)[N], uint32_t me) {
+  lds_block<N>(room, place, dt * 2 + jt, p, me ^ (col_turn(dt) * 16));
+}
+// Half of a block from a 16 x 16 result: its rows are the terms of the sum.
+template <int N>
+__device__ __forceinline__ void store_half(char* blocks, int n, int half, const f4& v, uint32_t lane) {
+  bf4 p[N];
+  split4<N>(v, p);
+  char* at = blocks + n * N * 1024 + lane * 16 + half * 8;
+#pragma unroll
+  for (int i = 0; i < N; ++i) *reinterpret_cast<bf4*>(at + i * 1024) = p[i];
+}
+
+// 6 of the 8 blocks of 16 rows x 32 terms of a triangular 64 x 64 matrix: rows 16 it of
+// a lower one meet terms 32 kt with kt <= it / 2, those of an upper one kt >= it / 2.
+__device__ __forceinline__ constexpr int lower_block(int it, int kt) {
+  return it < 2 ? it : 2 * (it - 1) + kt;
+}
+__device__ __forceinline__ constexpr int upper_block(int it, int kt) {
+  return it < 2 ? 2 * it + kt : it + 2;
+}
+
+// A thread's 4 x 8 piece of a [64 x 32 KT] matrix, as it lies in memory: rows 4 a + r,
+// columns 8 m + c; 0 from row `rows` and from column `width` on.
+template <typename T>
+struct Piece {
+  typedef T row __attribute__((ext_vector_type(8)));
+  row v[4];
+};
+template <typename T>
+__device__ __forceinline__ void load_piece(const T* base, int64_t stride, int rows, int width,
+                                           int a, int m, Piece<T>& v) {
+  // a chunk's rows lie within 2^31 bytes
+  const uint32_t at = (uint32_t)(4 * a) * (uint32_t)stride + 8 * m;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    typename Piece<T>::row x = {};
+    const T* row = base + r * stride;
+    if (4 * a + r < rows) {
+      if (8 * m + 8 <= width) {
+        x = load_pack<T, 8>(row + at).v;
+      } else if (8 * m < width) {
+        const int last = width - 1 - 8 * m;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const T e = row[at + min(c, last)];
+          x[c] = c <= last ? e : (T)0.0f;
+        }
+      }
+    }
+    v.v[r] = x;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void unpack_piece(const Piece<T>& v, float (&x)[4][8]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[r][c] = (float)v.v[r][c];
+}
+// Four of its values as N parts.
+template <int N, typename V>
+__device__ __forceinline__ void split_four(V x, bf4 (&p)[N]) {
+  if constexpr (N == 1) {
+    p[0] = __builtin_convertvector(x, bf4);
+  } else {
+    split4<N>(__builtin_convertvector(x, f4), p);
+  }
+}
+// As rows: blocks it * KT + kt, the columns being the terms.  As columns: blocks dt * 2 +
+// jt, the rows being the terms.
+template <int N, int KT, typename T>
+__device__ __forceinline__ void store_piece(const Piece<T>& v, int a, int m, char* rows, char* cols) {
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  if (rows) {
+    const int half = m % 4 / 2, g = m % 2 * 2;
+    char* at = rows + (a / 4 * KT + m / 4) * N * 1024 + half * 8 + (16 * g + a % 4 * 4) * 16;
+    const int turn = row_turn(m / 4);  // below 4, as r
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const t4 x = {v.v[r][4 * k], v.v[r][4 * k + 1], v.v[r][4 * k + 2], v.v[r][4 * k + 3]};
+        bf4 p[N];
+        split_four<N>(x, p);
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          *reinterpret_cast<bf4*>(at + q * 1024 + (16 * k + (r ^ turn)) * 16) = p[q];
+      }
+    }
+  }
+  if (cols) {
+    char* at = cols + (m / 2 * 2 + a / 8) * N * 1024 + a % 8 / 4 * 8 + (16 * (a % 4) + m % 2 * 8) * 16;
+    const int turn = col_turn(m / 2);  // below 8, as c
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const t4 x = {v.v[0][c], v.v[1][c], v.v[2][c], v.v[3][c]};
+      bf4 p[N];
+      split_four<N>(x, p);
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+        *reinterpret_cast<bf4*>(at + q * 1024 + (c ^ turn) * 16) = p[q];
+    }
+  }
+}
+// The same of f32 values.
+template <int N, int KT>
+__device__ __forceinline__ void store_piece(const float (&x)[4][8], int a, int m, char* rows) {
+  Piece<float> v;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v.v[r][c] = x[r][c];
+  store_piece<N, KT, float>(v, a, m, rows, nullptr);
+}
+// A chunk's rows as operand blocks, by all of a workgroup's threads.
+template <typename T, int KT>
+__device__ __forceinline__ void stage(const T* base, int64_t stride, int rows, int width, char* as_rows,
+                                      char* as_cols) {
+  for (int id = threadIdx.x; id < 64 * KT; id += blockDim.x) {
+    Piece<T> v;
+    load_piece<T>(base, stride, rows, width, id / (4 * KT), id % (4 * KT), v);
+    store_piece<kParts<T>, KT, T>(v, id / (4 * KT), id % (4 * KT), as_rows, as_cols);
+  }
+}
+
+// What is prepared for each (sequence, chunk, head): the decays and writing strengths,
+// then operand blocks: (I + A)^-1 and Q K^T . D (forward), or the transposes of both.
+struct Decays {
+  double log[kC];   // base 2, of the gates up to a step; 2^12 less behind each reset
+  float first[kC];  // gamma; -1 behind a reset
+  float last[kC];   // d
+  float w[kC];
+  int resets[kC];   // up to a step
+};
+constexpr int kInvParts = 3;
+template <typename T>
+constexpr int kScoreParts(bool backward) {
+  return backward ? 3 : kOutParts<T>;
+}
+constexpr size_t prep_bytes(int score_parts) {
+  return sizeof(Decays) + (size_t)6 * (kInvParts + score_parts) * 1024;
+}
+size_t prep_bytes_of(int type, bool backward) {
+  return prep_bytes(backward || type == PER_F32 ? 3 : 2);
+}
+
+__device__ __forceinline__ int steps_of(const DeltaArgs& a, int64_t b) {
+  return __builtin_amdgcn_readfirstlane(
+      (int)(a.length ? min(max(a.length[b], (int64_t)0), a.T) : a.T));
+}
+template <typename T>
+__device__ __forceinline__ const T* at(const Seq& s, int64_t b, int64_t t, int64_t h) {
+  return static_cast<const T*>(s.p) + b * s.sb + t * s.st + h * s.sh;
+}
+
+// Quotient and rest of a workgroup's number, in scalar registers.
+__device__ __forceinline__ void divide(uint32_t x, uint32_t by, int& quotient, int& rest) {
+  quotient = __builtin_amdgcn_readfirstlane((int)(x / by));
+  rest = (int)(x - (uint32_t)quotient * by);
+}
+
+// Of the gates of steps j + 1 to i, 0 across a reset.
+__device__ __forceinline__ float decay(const Decays& d, int i, int j) {
+  return __builtin_amdgcn_exp2f((float)(d.log[i] - d.log[j]));
+}
+
+// One workgroup of 4 waves for each (sequence, chunk, head).
+template <typename T, int KT, bool BACKWARD>
+__global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
+  constexpr int N = kParts<T>, NS = kScoreParts<T>(BACKWARD), kPad = 68;
+  __shared__ __attribute__((aligned(16))) char ks[4 * KT * N * 1024];
+  __shared__ __attribute__((aligned(16))) char qs[4 * KT * N * 1024];
+  __shared__ __attribute__((aligned(16))) float lower[kC][kPad];
+  __shared__ __attribute__((aligned(16))) float inv[kC][kPad];
+  __shared__ Decays dec;
+  const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  int b, c, h;
+  divide(blockIdx.x, (uint32_t)a.H, b, h);
+  divide((uint32_t)b, (uint32_t)a.chunks, b, c);
+  const int64_t t0 = (int64_t)c * kC;
+  const int rows = min(kC, steps_of(a, b) - (int)t0);
+  if (rows <= 0) return;
+  char* out = static_cast<char*>(a.prep) + (int64_t)blockIdx.x * prep_bytes(NS);
+  const int hk = h / (a.H / a.HK);
+  stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, ks, nullptr);
+  stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, qs, nullptr);
+  if (wave == 3) {
+    const bool on = lane < rows;
+    const float gate = on ? (float)*at<T>(a.g, b, t0 + lane, h) : 0.0f;
+    const float wt = on ? (float)*at<T>(a.b, b, t0 + lane, h) : 0.0f;
+    const bool reset = on && a.reset && a.reset[b * a.T + t0 + lane];
+    // log f; a gate below 2^-256 is 0 in f32 whatever it is
+    const float lf = fminf(gate, 0.0f) - log1pf(expf(-fabsf(gate)));
+    double log = reset ? -4096.0 : on ? fmax((double)lf * 1.4426950408889634074, -256.0) : 0.0;
+    if (lf != lf && !reset) log = (double)lf;
+    int resets = reset;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const double l = __shfl_up(log, d);
+      const int r = __shfl_up(resets, d);
+      log += lane >= d ? l : 0.0;
+      resets += lane >= d ? r : 0;
+    }
+    const double end = __shfl(log, 63);
+    dec.log[lane] = log;
+    dec.resets[lane] = resets;
+    dec.first[lane] = resets == 0 ? __builtin_amdgcn_exp2f((float)log) : -1.0f;
+    dec.last[lane] = __builtin_amdgcn_exp2f((float)(end - log));
+    dec.w[lane] = on ? 1.0f / (1.0f + expf(-wt)) : 0.0f;
+  }
+  for (int i = threadIdx.x; i < kC * kPad; i += 256) (&inv[0][0])[i] = 0.0f;
+  __syncthreads();
+  for (int i = threadIdx.x; i < (int)sizeof(Decays) / 16; i += 256)
+    reinterpret_cast<f4*>(out)[i] = reinterpret_cast<const f4*>(&dec)[i];
+
+  // 12 pairs of 16 rows and 16 columns, 10 of them on or below the diagonal: A for the
+  // inverse, and scores as halves of blocks, zeros above the diagonal
+  char* scores = out + sizeof(Decays) + 6 * kInvParts * 1024;
+  for (int id = wave; id < 12; id += 4) {
+    const int it = id < 4 ? id / 2 : 2 + (id - 4) / 4, jt = id < 4 ? id % 2 : (id - 4) % 4;
+    f4 kk = {}, qk = {};
+    if (jt <= it) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        bf8 ki[N], kj[N], qi[N];
+        load_rows<N, KT>(ks, it, kt, ki, lane);
+        load_rows<N, KT>(ks, jt, kt, kj, lane);
+        load_rows<N, KT>(qs, it, kt, qi, lane);
+        if (BACKWARD) {  // rows of it, columns of jt
+          kk = mul<2>(ki, kj, kk);
+          qk = mul<2>(qi, kj, qk);
+        } else {
+          kk = mul<2>(kj, ki, kk);
+          qk = mul<2>(kj, qi, qk);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * it + (BACKWARD ? 4 * g + r : n), j = 16 * jt + (BACKWARD ? n : 4 * g + r);
+        const float d = decay(dec, i, j);
+        lower[i][j] = j < i ? dec.w[i] * d * kk[r] : 0.0f;
+        qk[r] = j <= i ? d * qk[r] : 0.0f;
+      }
+    }
+    if (BACKWARD) {  // rows of it are the terms of a row of jt
+      if (it / 2 >= jt / 2 && jt < 4) store_half<NS>(scores, upper_block(jt, it / 2), it % 2, qk, lane);
+    } else {
+      store_half<NS>(scores, lower_block(it, jt / 2), jt % 2, qk, lane);
+    }
+  }
+  __syncthreads();
+
+  // (I + A)^-1: the blocks of 16 on the diagonal by substitution, a column to a lane
+  if (lane < 16) {
+    const int o = 16 * wave;
+    float x[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float s = r == lane ? 1.0f : 0.0f;
+#pragma unroll
+      for (int k = 0; k < r; ++k) s -= lower[o + r][o + k] * x[k];
+      x[r] = s;
+      inv[o + r][o + lane] = s;
+    }
+  }
+  __syncthreads();
+  // and below it X_ij = -X_ii sum_k A_ik X_kj, a column of blocks to a wave
+  {
+    const int j = wave;
+    f4 x[3];
+#pragma unroll
+    for (int step = 0; step < 3; ++step) {
+      const int i = j + 1 + step;
+      if (i < 4) {
+        f4 z = {};
+#pragma unroll
+        for (int s = 0; s <= step; ++s) {
+          const int k = j + s;
+          const f4 p = *reinterpret_cast<const f4*>(&lower[16 * i + n][16 * k + 4 * g]);
+          f4 q;
+          if (s == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) q[r] = inv[16 * j + 4 * g + r][16 * j + n];
+          } else {
+            q = x[s - 1];
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            z = __builtin_amdgcn_mfma_f32_16x16x4f32(p[r], q[r], z, 0, 0, 0);
+        }
+        const f4 p = *reinterpret_cast<const f4*>(&inv[16 * i + n][16 * i + 4 * g]);
+        f4 y = {};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          y = __builtin_amdgcn_mfma_f32_16x16x4f32(p[r], z[r], y, 0, 0, 0);
+        x[step] = -y;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) inv[16 * i + 4 * g + r][16 * j + n] = -y[r];
+      }
+    }
+  }
+  __syncthreads();
+  char* blocks = out + sizeof(Decays);
+  for (int id = wave; id < 6; id += 4) {
+    f4 lo, hi;
+    if (BACKWARD) {
+      const int jt = id < 4 ? id / 2 : id - 2, kt = id < 4 ? id % 2 : 1;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        lo[r] = inv[32 * kt + 4 * g + r][16 * jt + n];
+        hi[r] = inv[32 * kt + 16 + 4 * g + r][16 * jt + n];
+      }
+    } else {
+      const int it = id < 2 ? id : id / 2 + 1, kt = id < 2 ? 0 : id % 2;
+      lo = *reinterpret_cast<const f4*>(&inv[16 * it + n][32 * kt + 4 * g]);
+      hi = *reinterpret_cast<const f4*>(&inv[16 * it + n][32 * kt + 16 + 4 * g]);
+    }
+    bf8 p[kInvParts];
+    split<kInvParts>(lo, hi, p);
+#pragma unroll
+    for (int q = 0; q < kInvParts; ++q)
+      *reinterpret_cast<bf8*>(blocks + (id * kInvParts + q) * 1024 + lane * 16) = p[q];
+  }
+}
+
+// Copies whole 16 bytes from memory to LDS by a workgroup.
+__device__ __forceinline__ void copy16(char* to, const char* from, int bytes) {
+  for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
+    *reinterpret_cast<f4*>(to + i) = *reinterpret_cast<const f4*>(from + i);
+}
+
+// W neighbouring values of a row, 0 past `width`.
+template <typename T, int W>
+__device__ __forceinline__ void load_few(const T* row, int col, int width, float (&v)[W]) {
+  if (col + W <= width) {
+    unpack<T, W>(load_pack<T, W>(row + col), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = col + i < width ? (float)row[col + i] : 0.0f;
+  }
+}
+template <typename T, int W>
+__device__ __forceinline__ void store_few(T* row, int col, int width, const float (&v)[W]) {
+  if (col + W <= width) {
+    store_vals<T, W>(row + col, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (col + i < width) row[col + i] = (T)v[i];
+  }
+}
+
+// A wave's column of a matrix [rows x width] for each lane n, as 16 x 16 results: rows 16 t
+// + 4 g + r of column col.  Through a buffer descriptor that ends with the last row: the
+// unit checks every access against it, so rows past the end read 0 and write nothing
+// without a branch, a row's place is one scalar for the whole wave, and a lane's part of it
+// (its column, past all rows where it has none) one register for all rows.
+template <typename T, int TILES>
+struct Column {
+  __amdgpu_buffer_rsrc_t buffer;
+  uint32_t lane;  // the lane's part
+  int step;       // bytes between rows
+  __device__ __forceinline__ Column(const T* base, int64_t stride, int rows, int col, int width) {
+    step = (int)stride * (int)sizeof(T);
+    asm volatile("" : "+s"(step));  // else the places of all rows are kept from chunk to chunk
+    const int bytes = (rows - 1) * step + width * (int)sizeof(T);
+    buffer = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, rows > 0 ? bytes : 0, 0x00020000);
+    lane = col < width ? (threadIdx.x & 63) / 16 * 4 * (uint32_t)step + (uint32_t)col * (uint32_t)sizeof(T)
+                       : 0xFFFFFFFFu;
+  }
+  __device__ __forceinline__ void load(T (&v)[TILES][4]) const {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (sizeof(T) == 4) {
+          v[t][r] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(buffer, lane, (16 * t + r) * step, 0));
+        } else {
+          v[t][r] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(buffer, lane, (16 * t + r) * step, 0));
+        }
+      }
+  }
+  __device__ __forceinline__ void store(const f4 (&v)[TILES]) const {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (sizeof(T) == 4) {
+          __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (T)v[t][r]), buffer, lane,
+                                                (16 * t + r) * step, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)v[t][r]), buffer, lane,
+                                                (16 * t + r) * step, 0);
+        }
+      }
+  }
+};
+template <typename T, int TILES>
+__device__ __forceinline__ void load_column(const T* base, int64_t stride, int rows, int col, int width,
+                                            T (&v)[TILES][4]) {
+  if (stride >= width) {
+    Column<T, TILES>(base, stride, rows, col, width).load(v);
+    return;
+  }
+  // rows that overlap (an expanded array) do not end with the last
+  asm volatile("" : "+s"(stride), "+s"(rows));
+  const int g = (threadIdx.x & 63) / 16;
+#pragma unroll
+  for (int t = 0; t < TILES; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * t + 4 * g + r;
+      v[t][r] = (T)0.0f;
+      if (row < rows && col < width) v[t][r] = base[row * stride + col];
+    }
+}
+template <typename T, int TILES>
+__device__ __forceinline__ void store_column(T* base, int64_t stride, int rows, int col, int width,
+                                             const f4 (&v)[TILES]) {
+  Column<T, TILES>(base, stride, rows, col, width).store(v);
+}
+template <int TILES>
+__device__ __forceinline__ void load_state(const float* s, int DK, int DV, int col, f4 (&v)[TILES]) {
+  float x[TILES][4] = {};
+  if (s) load_column<float, TILES>(s, DV, DK, col, DV, x);
+#pragma unroll
+  for (int t = 0; t < TILES; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[t][r] = x[t][r];
+}
+// 0, or the unit column with 1 in row `one`.
+template <int TILES>
+__device__ __forceinline__ void unit_state(int one, f4 (&v)[TILES]) {
+  const int g = (threadIdx.x & 63) / 16;
+#pragma unroll
+  for (int t = 0; t < TILES; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[t][r] = 16 * t + 4 * g + r == one ? 1.0f : 0.0f;
+}
+// The rows' values of a chunk, 4 neighbouring ones of each 16.
+__device__ __forceinline__ f4 rows_of(const float (&v)[kC], int it) {
+  return *reinterpret_cast<const f4*>(&v[16 * it + 4 * ((threadIdx.x & 63) / 16)]);
+}
+
+// A state that is not finite stays on its side of a reset: the rows of the chunk on
+// that side (`with`) give 0 to the other rows' sums, where 0 times them would not be 0.
+// Called where the chunk has a reset.
+template <typename F>
+__device__ __forceinline__ void keep_apart(f4 (&x)[4], F with) {
+  const int g = (threadIdx.x & 63) / 16;
+  float bad = 0.0f;
+#pragma unroll
+  for (int it = 0; it < 4; ++it)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (with(16 * it + 4 * g + r) && !__builtin_isfinite(x[it][r])) bad = 1.0f;
+  bad = fmaxf(bad, xor_lanes(bad, 4));
+  bad = fmaxf(bad, xor_lanes(bad, 5));
+#pragma unroll
+  for (int it = 0; it < 4; ++it)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (bad != 0.0f && with(16 * it + 4 * g + r)) x[it][r] = 0.0f;
+}
+
+constexpr int64_t carry_size(int DK, int DV) { return (int64_t)(DK + kC) * DV; }
+
+// What a workgroup of THREADS takes from memory for a chunk, held in registers while
+// the chunk before is computed: pieces of the keys and queries, and what is prepared.
+template <typename T, int KT, int THREADS, int BYTES, bool QUERIES>
+struct Ahead {
+  static constexpr int kAll = (QUERIES ? 128 : 64) * KT;
+  static constexpr int kPieces = (kAll + THREADS - 1) / THREADS;
+  static constexpr int kCopies = (BYTES / 16 + THREADS - 1) / THREADS;
+  Piece<T> piece[kPieces];
+  f4 copy[kCopies];
+
+  // even: rows begin at whole 4 bytes, and hold whole pieces
+  __device__ __forceinline__ void load(const T* ks, int64_t kst, const T* qs, int64_t qst, bool even, int DK,
+                                       int rows, const char* prep) {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      const int id = threadIdx.x + p * THREADS, at = id % (64 * KT), a = at / (4 * KT), m = at % (4 * KT);
+      const int query = __builtin_amdgcn_readfirstlane(id / (64 * KT));
+      if (query > (QUERIES ? 1 : 0)) continue;
+      const T* base = query ? qs : ks;
+      const int64_t stride = query ? qst : kst;
+      if (even) {
+        int step = (int)stride * (int)sizeof(T);
+        const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<T*>(base), 0, (rows - 1) * step + DK * (int)sizeof(T), 0x00020000);
+        const uint32_t lane = 8 * m < DK ? 4 * a * (uint32_t)step + 8 * m * (uint32_t)sizeof(T) : 0xFFFFFFFFu;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (sizeof(T) == 2) {
+            piece[p].v[r] = __builtin_bit_cast(typename Piece<T>::row,
+                                               __builtin_amdgcn_raw_buffer_load_b128(buffer, lane, r * step, 0));
+          } else {
+            typedef T t4 __attribute__((ext_vector_type(4)));
+            const t4 lo = __builtin_bit_cast(t4, __builtin_amdgcn_raw_buffer_load_b128(buffer, lane, r * step, 0));
+            const t4 hi = __builtin_bit_cast(
+                t4, __builtin_amdgcn_raw_buffer_load_b128(buffer, lane, r * step + 16, 0));
+            piece[p].v[r] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          }
+        }
+      } else {
+        int64_t step = stride;
+        int width = DK;
+        asm volatile("" : "+s"(step), "+s"(width));
+        load_piece<T>(base, step, rows, width, a, m, piece[p]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      const uint32_t at = (threadIdx.x + c * THREADS) * 16;
+      if (at < BYTES) copy[c] = *reinterpret_cast<const f4*>(prep + at);
+    }
+  }
+  // which: 1 keys, 2 queries, 3 both
+  __device__ __forceinline__ void store(char* krows, char* kcols, char* qrows, char* qcols, char* prep,
+                                        int which = 3) const {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      const int id = threadIdx.x + p * THREADS, at = id % (64 * KT);
+      const int query = __builtin_amdgcn_readfirstlane(id / (64 * KT));
+      if (query == 0) {
+        if (which & 1)
+          store_piece<kParts<T>, KT, T>(piece[p], at / (4 * KT), at % (4 * KT), krows, kcols);
+      } else if (query == 1 && (which & 2)) {
+        store_piece<kParts<T>, KT, T>(piece[p], at / (4 * KT), at % (4 * KT), qrows, qcols);
+      }
+    }
+    if (which & 1) {
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) {
+        const uint32_t at = (threadIdx.x + c * THREADS) * 16;
+        if (at < BYTES) *reinterpret_cast<f4*>(prep + at) = copy[c];
+      }
+    }
+  }
+};
+// Whether rows of an array begin at whole 4 bytes, are whole pieces, and do not overlap.
+template <typename T>
+__device__ __forceinline__ bool even_rows(const T* p, int64_t stride, int D) {
+  return D % 8 == 0 && stride >= D && (((uint32_t)(uintptr_t)p | (uint32_t)stride * (uint32_t)sizeof(T)) & 3) == 0;
+}
+
+// The states that the segments of a cut time axis begin with (in REVERSE: the gradients
+// behind them), one after the other: S = map S + local, 16 columns to a wave.  A segment
+// with a reset takes nothing over, whatever S holds.
+template <int KT, bool REVERSE>
+__global__ __launch_bounds__(256) void delta_join_kernel(DeltaArgs a, int slices) {
+  const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  int bh, b, h, slice;
+  divide(blockIdx.x, (uint32_t)slices, bh, slice);
+  divide((uint32_t)bh, (uint32_t)a.H, b, h);
+  const int col = (slice * 4 + wave) * 16 + n;
+  const int steps = steps_of(a, b);
+  f4 s[2 * KT];
+  load_state<2 * KT>(a.s0 ? a.s0 + (int64_t)bh * a.DK * a.DV : nullptr, a.DK, a.DV, col, s);
+  for (int k = 0; k < a.segments; ++k) {
+    const int seg = REVERSE ? a.segments - 1 - k : k;
+    const int64_t place = (int64_t)bh * a.segments + seg;
+    store_column<float, 2 * KT>(a.states + place * a.DK * a.DV, a.DV, a.DK, col, a.DV, s);
+    if (k == a.segments - 1) break;
+    float local[2 * KT][4];
+    load_column<float, 2 * KT>(a.locals + place * a.DK * a.DV, a.DV, a.DK, col, a.DV, local);
+    const int from = seg * a.segment_chunks * kC, end = min(steps, from + a.segment_chunks * kC);
+    bool reset = false;
+    if (a.reset)
+      for (int t = from + lane; t < end; t += 64) reset |= a.reset[b * a.T + t] != 0;
+    f4 y[2 * KT];
+#pragma unroll
+    for (int t = 0; t < 2 * KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[t][r] = local[t][r];
+    if (__ballot(reset) == 0) {
+      const float* map = a.maps + place * a.DK * a.DK;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        bf8 sp[3];
+        split<3>(s[2 * kt], s[2 * kt + 1], sp);
+#pragma unroll 2
+        for (int dt = 0; dt < 2 * KT; ++dt) {
+          const int row = 16 * dt + n;
+          float lo[4] = {}, hi[4] = {};
+          if (row < a.DK) {
+            load_few<float, 4>(map + (int64_t)row * a.DK, 32 * kt + 4 * g, a.DK, lo);
+            load_few<float, 4>(map + (int64_t)row * a.DK, 32 * kt + 16 + 4 * g, a.DK, hi);
+          }
+          bf8 mp[3];
+          split<3>(f4{lo[0], lo[1], lo[2], lo[3]}, f4{hi[0], hi[1], hi[2], hi[3]}, mp);
+          y[dt] = mul<2>(mp, sp, y[dt]);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 2 * KT; ++t) s[t] = y[t];
+  }
+}
+
+template <typename F>
+hipError_t by_type(int type, F f) {
+  switch (type) {
+    case PER_F32: return f(Tag<float>{});
+    case PER_BF16: return f(Tag<bf16_t>{});
+    default: return f(Tag<f16_t>{});
+  }
+}
+template <int K>
+struct Size {
+  static constexpr int value = K;
+};
+template <typename F>
+hipError_t by_keys(int DK, F f) {
+  if (DK <= 32) return f(Size<1>{});
+  if (DK <= 64) return f(Size<2>{});
+  return f(Size<4>{});
+}
+
+template <bool BACKWARD>
+hipError_t launch_prepare(const DeltaArgs& a, int type, hipStream_t s) {
+  return by_type(type, [&](auto tag) {
+    return by_keys(a.DK, [&](auto keys) {
+      using T = typename decltype(tag)::type;
+      constexpr int KT = decltype(keys)::value;
+      return enqueue(delta_prepare_kernel<T, KT, BACKWARD>, dim3((uint32_t)(a.B * a.chunks * a.H)),
+                     dim3(256), 0, s, a);
+    });
+  });
+}
+
+// Waves of a workgroup, 16 columns of the state each: up to 128 columns, or 64 where the
+// states are few and twice as many workgroups find a place, or where 8 waves' registers
+// do not hold what a chunk takes (f32, and 128 keys of f16).
+inline int column_waves(const DeltaArgs& a, int type) {
+  if (type == PER_F32 || (type == PER_F16 && a.DK > 64)) return 4;
+  return a.DV <= 64 || a.segments > 1 || a.B * a.H * ((a.DV + 127) / 128) <= 128 ? 4 : 8;
+}
+
+// Join of the segments' maps.
+template <bool REVERSE>
+hipError_t launch_join(const DeltaArgs& a, hipStream_t s) {
+  return by_keys(a.DK, [&](auto keys) {
+    constexpr int KT = decltype(keys)::value;
+    const int slices = (a.DV + 63) / 64;
+    return enqueue(delta_join_kernel<KT, REVERSE>, dim3((uint32_t)(a.B * a.H * slices)), dim3(256), 0, s, a,
+                   slices);
+  });
+}
+
+}  // namespace
+}  // namespace per

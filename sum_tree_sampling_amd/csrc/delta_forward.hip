@@ -1,0 +1,377 @@
+// delta_forward.hip -- the gated delta rule: the forward pass and one step.
+#include "delta_common.h"
+
+namespace per {
+namespace {
+
+// A workgroup has a head of a sequence and 16 columns of its state for each of its waves.
+// While a chunk is computed the next one's operands are on their way in registers; they
+// go to a second place in LDS where there is room for one, so a chunk needs one barrier.
+//
+// LOCAL: what a segment of a cut time axis does to a state, without outputs.  Its value
+// columns begin with a state of 0, and DK further columns, whose values are 0, with the
+// unit columns, so they end as the map that the segment's steps are.
+template <typename T, int KT, int WAVES, bool LOCAL>
+__global__ __launch_bounds__(64 * WAVES)
+__attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 && !LOCAL ? 1 : 4))) void delta_forward_kernel(
+    DeltaArgs a, int slices) {
+  constexpr int N = kParts<T>, NO = kOutParts<T>, WEAK = kWeak<T>;
+  constexpr int kTile = 4 * KT * N * 1024, kPrep = (int)prep_bytes(NO);
+  constexpr int kTaken = LOCAL ? (int)prep_bytes(0) : kPrep;  // of what is prepared
+  constexpr bool kApart = N < 3;  // queries have a place of their own in LDS
+  constexpr int kRoom = (kApart && !LOCAL ? 3 : 2) * kTile + kTaken;
+  constexpr int kSome = 2;  // blocks that are held at a time
+  constexpr bool kTwice = !LOCAL && 2 * kRoom <= 160 * 1024;
+  __shared__ __attribute__((aligned(16))) char room[(kTwice ? 2 : 1) * kRoom];
+  constexpr int kCols = kTile, kQueries = kApart ? 2 * kTile : 0, kReady = kRoom - kTaken;
+  constexpr int kInvs = kReady + (int)sizeof(Decays), kScores = kInvs + 6 * kInvParts * 1024;
+
+  const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  int bh, b, h, hk, slice, rest;
+  divide(blockIdx.x % (uint32_t)(a.B * a.H * slices), (uint32_t)slices, bh, slice);
+  divide((uint32_t)bh, (uint32_t)a.H, b, h);
+  divide((uint32_t)h, (uint32_t)(a.H / a.HK), hk, rest);
+  int seg = 0;
+  if (a.segments > 1) divide((uint32_t)blockIdx.x, (uint32_t)(a.B * a.H * slices), seg, rest);
+  const int64_t place = (int64_t)bh * a.segments + seg;  // of the segment's states
+  // value columns, or in LOCAL unit columns behind them
+  const int behind = LOCAL ? (a.DV + 16 * WAVES - 1) / (16 * WAVES) : slices;
+  const bool unit_columns = LOCAL && slice >= behind;
+  const int col = ((unit_columns ? slice - behind : slice) * WAVES + wave) * 16 + n;
+  const int steps = steps_of(a, b);
+  const int from = seg * a.segment_chunks * kC;
+  const int end = a.segments > 1 ? min(steps, from + a.segment_chunks * kC) : steps;
+  const int64_t unit0 = (int64_t)b * a.chunks * a.H + h;  // the head's first chunk; others lie H apart
+  const T *ks = at<T>(a.k, b, 0, hk), *qs = at<T>(a.q, b, 0, hk), *vs = at<T>(a.v, b, 0, h);
+  const bool even = even_rows(ks, a.k.st, a.DK) && even_rows(qs, a.q.st, a.DK);
+  T* os = const_cast<T*>(at<T>(a.o, b, 0, h));
+
+  f4 s[2 * KT];
+  if constexpr (LOCAL) {
+    unit_state<2 * KT>(unit_columns ? col : -1, s);
+  } else if (a.segments > 1) {
+    load_state<2 * KT>(a.states + place * a.DK * a.DV, a.DK, a.DV, col, s);
+  } else {
+    load_state<2 * KT>(a.s0 ? a.s0 + (int64_t)bh * a.DK * a.DV : nullptr, a.DK, a.DV, col, s);
+  }
+  Ahead<T, KT, 64 * WAVES, kTaken, !LOCAL> ahead;
+  T v[4][4];
+  const int width = unit_columns ? 0 : a.DV;  // no values
+  if (from < end) {
+    ahead.load(ks + (int64_t)from * a.k.st, a.k.st, qs + (int64_t)from * a.q.st, a.q.st, even, a.DK,
+               min(kC, end - from), static_cast<const char*>(a.prep) + (unit0 + from / kC * a.H) * kPrep);
+    load_column<T, 4>(vs + (int64_t)from * a.v.st, a.v.st, min(kC, end - from), col, width, v);
+    ahead.store(room, room + kCols, room + kQueries, nullptr, room + kReady, kApart && !LOCAL ? 3 : 1);
+  }
+  __syncthreads();
+  for (int t0 = from, flip = 0; t0 < end; t0 += kC) {
+    const int rows = min(kC, end - t0), more = min(kC, end - t0 - kC);
+    const int64_t unit = unit0 + t0 / kC * a.H;
+    char* now = room + (kTwice ? flip * kRoom : 0);
+    const Decays& dec = *reinterpret_cast<const Decays*>(now + kReady);
+    const bool resets = __builtin_amdgcn_readfirstlane(dec.resets[kC - 1]) != 0;
+    // one register for all places in LDS
+    uint32_t me = (uint32_t)(now - room) + (uint32_t)lane * 16;
+    asm volatile("" : "+v"(me));
+    f4 r[4];  // V
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[it][i] = (float)v[it][i];
+    Ahead<T, KT, 64 * WAVES, kTaken, !LOCAL> queries;
+    if constexpr (!kApart && !LOCAL) queries = ahead;
+    if (more > 0) {
+      ahead.load(ks + (int64_t)(t0 + kC) * a.k.st, a.k.st, qs + (int64_t)(t0 + kC) * a.q.st, a.q.st, even,
+                 a.DK, more, static_cast<const char*>(a.prep) + (unit + a.H) * kPrep);
+      load_column<T, 4>(vs + (int64_t)(t0 + kC) * a.v.st, a.v.st, more, col, width, v);
+    }
+    float* carry = !LOCAL && a.carries ? a.carries + unit * carry_size(a.DK, a.DV) : nullptr;
+    if (carry) store_column<float, 2 * KT>(carry, a.DV, a.DK, col, a.DV, s);
+
+    // K S and Q S
+    f4 x[4] = {}, y[4] = {};
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      bf8 sp[3], kp[4][N], qp[4][N];
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        lds_rows<N, KT>(room, 0, it, kt, kp[it], me);
+        if constexpr (kApart && !LOCAL) lds_rows<N, KT>(room, kQueries, it, kt, qp[it], me);
+      }
+      split<3>(s[2 * kt], s[2 * kt + 1], sp);
+      mul_each<2>(kp, sp, x);
+      if constexpr (kApart && !LOCAL) mul_each<WEAK>(qp, sp, y);
+    }
+    if constexpr (!kApart && !LOCAL) {
+      __syncthreads();
+      queries.store(nullptr, nullptr, now + kQueries, nullptr, nullptr, 2);
+      __syncthreads();
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        bf8 sp[3], qp[4][N];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) lds_rows<N, KT>(room, kQueries, it, kt, qp[it], me);
+        split<3>(s[2 * kt], s[2 * kt + 1], sp);
+        mul_each<WEAK>(qp, sp, y);
+      }
+    }
+    // w (V - gamma K S)
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const f4 first = rows_of(dec.first, it), w = rows_of(dec.w, it);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[it][i] *= first[i];
+        y[it][i] *= first[i];
+        if (resets && first[i] < 0.0f) x[it][i] = y[it][i] = 0.0f;
+        x[it][i] = w[i] * (r[it][i] - x[it][i]);
+      }
+    }
+    if (resets) keep_apart(x, [&](int i) { return dec.first[i] >= 0.0f; });
+    // U
+    f4 u[4] = {};
+    {
+      bf8 xp[3], p[kSome][kInvParts], q[2][kInvParts];
+      split<3>(x[0], x[1], xp);
+#pragma unroll
+      for (int i0 = 0; i0 < 4; i0 += kSome) {
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) lds_block<kInvParts>(room, kInvs, lower_block(i0 + i, 0), p[i], me);
+        mul_each<2>(p, xp, u + i0);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) lds_block<kInvParts>(room, kInvs, lower_block(i + 2, 1), q[i], me);
+      split<3>(x[2], x[3], xp);
+      mul_each<2>(q, xp, u + 2);
+    }
+    if (carry) store_column<float, 4>(carry + (int64_t)a.DK * a.DV, a.DV, kC, col, a.DV, u);
+    // the outputs
+    if constexpr (!LOCAL) {
+      bf8 p[4][NO], up[NO];
+#pragma unroll
+      for (int it = 0; it < 4; ++it) lds_block<NO>(room, kScores, lower_block(it, 0), p[it], me);
+      split<NO>(u[0], u[1], up);
+      mul_each<WEAK>(p, up, y);
+      bf8 q[2][NO];
+#pragma unroll
+      for (int it = 0; it < 2; ++it) lds_block<NO>(room, kScores, lower_block(it + 2, 1), q[it], me);
+      split<NO>(u[2], u[3], up);
+      mul_each<WEAK>(q, up, y + 2);
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      y[it] = y[it] * a.scale;
+      u[it] = u[it] * rows_of(dec.last, it);
+    }
+    if constexpr (!LOCAL) store_column<T, 4>(os + (int64_t)t0 * a.o.st, a.o.st, rows, col, a.DV, y);
+    // the state behind the chunk
+    const float kept = dec.first[kC - 1];
+#pragma unroll
+    for (int dt = 0; dt < 2 * KT; ++dt) s[dt] = resets ? f4{} : s[dt] * kept;
+#pragma unroll
+    for (int jt = 0; jt < 2; ++jt) {
+      bf8 up[3];
+      split<3>(u[2 * jt], u[2 * jt + 1], up);
+#pragma unroll
+      for (int d0 = 0; d0 < 2 * KT; d0 += kSome) {
+        bf8 p[kSome][N];
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) lds_cols<N>(room, kCols, d0 + i, jt, p[i], me);
+        mul_each<2>(p, up, s + d0);
+      }
+    }
+    if (more > 0) {
+      if (kTwice) {
+        flip ^= 1;
+      } else {
+        __syncthreads();
+      }
+      char* next = room + (kTwice ? flip * kRoom : 0);
+      ahead.store(next, next + kCols, next + kQueries, nullptr, next + kReady, kApart && !LOCAL ? 3 : 1);
+    }
+    __syncthreads();
+  }
+  if constexpr (LOCAL) {
+    float* to = unit_columns ? a.maps + place * a.DK * a.DK : a.locals + place * a.DK * a.DV;
+    const int wide = unit_columns ? a.DK : a.DV;
+    store_column<float, 2 * KT>(to, wide, a.DK, col, wide, s);
+  } else {
+    // the segment that the sequence ends in has the last state; what lies behind is 0
+    const int last = a.segments > 1 && steps > 0 ? (steps - 1) / (a.segment_chunks * kC) : 0;
+    if (a.s_last && seg == last)
+      store_column<float, 2 * KT>(a.s_last + (int64_t)bh * a.DK * a.DV, a.DV, a.DK, col, a.DV, s);
+    const int64_t stop = a.segments > 1 ? min(a.T, (int64_t)from + a.segment_chunks * kC) : a.T;
+    for (int64_t t = max(from, steps) + g; t < stop; t += 4)
+      if (col < a.DV) os[t * a.o.st + col] = (T)0.0f;
+  }
+}
+
+// One step: a workgroup has a head's state, 32 groups of 4 columns by PARTS groups of 16
+// rows, so all of it is asked for at once.  The state is read and written once.
+template <typename T, int PARTS>
+__global__ __launch_bounds__(32 * PARTS) void delta_step_kernel(DeltaArgs a, int slices) {
+  __shared__ float sum[2][PARTS][128];
+  __shared__ float ks[16 * PARTS], qs[16 * PARTS];
+  int bh, b, h, hk, slice, rest;
+  divide(blockIdx.x, (uint32_t)slices, bh, slice);
+  divide((uint32_t)bh, (uint32_t)a.H, b, h);
+  divide((uint32_t)h, (uint32_t)(a.H / a.HK), hk, rest);
+  const int part = threadIdx.x / 32, cl = threadIdx.x % 32 * 4, col = slice * 128 + cl;
+  const float* s = a.s0 + (int64_t)bh * a.DK * a.DV;
+  float v[16][4];
+  const bool reset = a.reset && a.reset[b];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int row = part * 16 + r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[r][i] = 0.0f;
+    if (row < a.DK && !reset) load_few<float, 4>(s + (int64_t)row * a.DV, col, a.DV, v[r]);
+  }
+  {
+    const int i = threadIdx.x;
+    const int c = i % (16 * PARTS);
+    const T* from = i < 16 * PARTS ? at<T>(a.k, b, 0, hk) : at<T>(a.q, b, 0, hk);
+    (i < 16 * PARTS ? ks : qs)[c] = c < a.DK ? (float)from[c] : 0.0f;
+  }
+  float vs[4];
+  load_few<T, 4>(at<T>(a.v, b, 0, h), col, a.DV, vs);
+  const float gate = (float)*at<T>(a.g, b, 0, h), wt = (float)*at<T>(a.b, b, 0, h);
+  const float f = 1.0f / (1.0f + expf(-gate)), w = 1.0f / (1.0f + expf(-wt));
+  __syncthreads();
+  float k[4] = {}, q[4] = {};
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const float kr = ks[part * 16 + r];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[r][i] *= f;
+      k[i] += kr * v[r][i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[0][part][cl + i] = k[i];
+  __syncthreads();
+  float u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x = 0.0f;
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) x += sum[0][p][cl + i];
+    u[i] = col + i < a.DV ? w * (vs[i] - x) : 0.0f;
+  }
+  float* to = a.s_last + (int64_t)bh * a.DK * a.DV;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int row = part * 16 + r;
+    const float kr = ks[row], qr = qs[row];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[r][i] += kr * u[i];
+      q[i] += qr * v[r][i];
+    }
+    if (row < a.DK) store_few<float, 4>(to + (int64_t)row * a.DV, col, a.DV, v[r]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[1][part][cl + i] = q[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 128; i += 32 * PARTS) {
+    const int c = slice * 128 + i;
+    if (c >= a.DV) break;
+    float x = 0.0f;
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) x += sum[1][p][i];
+    const_cast<T*>(at<T>(a.o, b, 0, h))[c] = (T)(a.scale * x);
+  }
+}
+
+template <typename T, int KT>
+struct Columns {
+  static constexpr int most = kParts<T> == 3 || (kParts<T> == 2 && KT == 4) ? 4 : 8;
+  static constexpr auto four = delta_forward_kernel<T, KT, 4, false>;
+  static constexpr auto eight = delta_forward_kernel<T, KT, most, false>;
+};
+
+}  // namespace
+
+// How many segments the time axis is cut into.  A cut costs a second pass over the keys
+// and values (with DK columns more) and a walk over the segments, so it pays where a
+// sequence has many chunks and the chip is far from full.
+void delta_segments(DeltaArgs& a) {
+  a.segments = 1;
+  a.segment_chunks = (int)a.chunks;
+  const int64_t groups = a.B * a.H * ((a.DV + 63) / 64);
+  if (a.chunks < 16 || groups == 0 || groups > 128) return;
+  int64_t n = 4;
+  while (n * n < 2 * a.chunks && n < 64) ++n;  // as long in the walk as in a segment
+  n = std::min(n, std::max<int64_t>(2, 512 / groups));
+  a.segment_chunks = (int)((a.chunks + n - 1) / n);
+  a.segments = (int)((a.chunks + a.segment_chunks - 1) / a.segment_chunks);
+}
+
+size_t delta_workspace(int64_t B, int64_t T, int64_t H, int64_t DK, int64_t DV, int type,
+                       bool backward, DeltaArgs* to, void* ws) {
+  DeltaArgs mine = {};
+  DeltaArgs& a = to ? *to : mine;
+  a.B = B;
+  a.H = (int)H;
+  a.DV = (int)DV;
+  a.chunks = (T + kC - 1) / kC;
+  delta_segments(a);
+  const int64_t units = B * a.chunks * H;
+  const size_t prep = (size_t)units * prep_bytes_of(type, backward);
+  const size_t places = a.segments > 1 ? (size_t)(B * H * a.segments) : 0;
+  const size_t state = ((size_t)(DK * DV) * 4 + 15) / 16 * 16, map = (size_t)(DK * DK) * 4;
+  char* p = static_cast<char*>(ws);
+  auto take = [&](size_t bytes) {
+    float* at = reinterpret_cast<float*>(p);
+    p += (bytes + 15) / 16 * 16;
+    return at;
+  };
+  a.prep = take(prep);
+  a.states = take(places * state);
+  a.locals = take(places * state);
+  a.maps = take(places * map);
+  if (backward) {
+    a.dstate = take((size_t)(units * DK * DV) * 4);
+    a.e = take((size_t)(units * kC * DV) * 4);
+  }
+  return (size_t)(p - static_cast<char*>(ws));
+}
+
+hipError_t launch_delta_forward(const DeltaArgs& a, int type, hipStream_t s) {
+  hipError_t e = a.chunks > 0 ? launch_prepare<false>(a, type, s) : hipSuccess;
+  if (e != hipSuccess) return e;
+  return by_type(type, [&](auto tag) {
+    return by_keys(a.DK, [&](auto keys) {
+      using T = typename decltype(tag)::type;
+      constexpr int KT = decltype(keys)::value;
+      using K = Columns<T, KT>;
+      const uint32_t heads = (uint32_t)(a.B * a.H);
+      if (a.segments > 1) {
+        // the last segment's map is not needed
+        const int slices = (a.DV + 63) / 64 + (a.DK + 63) / 64;
+        hipError_t e = enqueue(delta_forward_kernel<T, KT, 4, true>,
+                               dim3(heads * slices * (a.segments - 1)), dim3(256), 0, s, a, slices);
+        if (e == hipSuccess) e = launch_join<false>(a, s);
+        if (e != hipSuccess) return e;
+      }
+      const int waves = column_waves(a, type), slices = (a.DV + 16 * waves - 1) / (16 * waves);
+      return enqueue(waves == 4 ? K::four : K::eight, dim3(heads * slices * a.segments), dim3(64 * waves), 0,
+                     s, a, slices);
+    });
+  });
+}
+
+hipError_t launch_delta_step(const DeltaArgs& a, int type, hipStream_t s) {
+  const int slices = (a.DV + 127) / 128;
+  return by_type(type, [&](auto tag) {
+    return by_keys(a.DK, [&](auto keys) {
+      constexpr int parts = 2 * decltype(keys)::value;
+      return enqueue(delta_step_kernel<typename decltype(tag)::type, parts>,
+                     dim3((uint32_t)(a.B * a.H * slices)), dim3(32 * parts), 0, s, a, slices);
+    });
+  });
+}
+
+}  // namespace per

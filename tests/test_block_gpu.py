@@ -285,6 +285,50 @@ def test_delta_long(dtype):
     check_delta(dev, host, dtype)
 
 
+@pytest.mark.parametrize("B,T,H,HK,DK,DV,resets", [(2, 1300, 2, 1, 33, 40, 0.0), (1, 1024, 1, 1, 128, 70, 0.002),
+                                                   (3, 1000, 1, 1, 8, 8, 0.01)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_delta_cut(B, T, H, HK, DK, DV, resets, dtype):
+    """Few long sequences, whose time axis is cut, some of them ending early."""
+    host, dev = delta_case(B, T, H, HK, DK, DV, dtype, T, ragged=B > 1, resets=resets)
+    if B > 1:
+        host["length"][0] = T - 3
+        dev["length"] = host["length"].cuda()
+        host, dev = delta_recut(host, dev)
+    check_delta(dev, host, dtype)
+
+
+def delta_recut(host, dev):
+    """NaN past the (changed) ends, and finite values before them."""
+    past = torch.arange(host["q"].shape[1]) >= host["length"][:, None]
+    for x in ("q", "k", "v", "g", "b", "do"):
+        host[x] = torch.where(torch.isnan(host[x]), torch.full_like(host[x], 0.125), host[x])
+        host[x][past] = math.nan
+        dev[x].copy_(host[x])
+    return host, dev
+
+
+def test_delta_cut_masked_states():
+    """A state that is not finite does not pass a reset where the time axis is cut."""
+    p = per()
+    host, dev = delta_case(2, 1100, 1, 1, 32, 48, "f32", 8, resets=0.0)
+    dev["reset"][0, 0] = True
+    dev["reset"][1, 300] = True
+    good = run(p, dev)
+    gg = back(p, dev, good[2])
+    s0 = dev["s0"].clone()
+    s0[0] = math.nan
+    s0[1, 0, 3, 5] = math.inf
+    bad = run(p, dict(dev, s0=s0))
+    assert same(bad[0][0], good[0][0]) and same(bad[1], good[1]) and same(bad[0][1, 300:], good[0][1, 300:])
+    gb = back(p, dict(dev, s0=s0), bad[2])
+    assert all(same(x[0], y[0]) and same(x[1, 300:], y[1, 300:]) for x, y in zip(gb[:5], gg[:5])) and same(gb[5], gg[5])
+    d = dev["ds_last"].clone()
+    d[1] = math.nan
+    gb = back(p, dict(dev, ds_last=d), good[2])
+    assert all(same(x[1, :300], y[1, :300]) for x, y in zip(gb[:5], gg[:5])) and same(gb[5], gg[5])
+
+
 def test_delta_gates_and_strengths():
     """Gates shut and open, strengths of 0 and 1, keys that repeat, a reset at every step."""
     B, T = 4, 150
