@@ -194,21 +194,56 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 && !LOCAL ? 1 : 4))) vo
   }
 }
 
+// A piece of rows that lie dense or apart, by one load for each row where rows begin at
+// whole 4 bytes and `width` is whole pieces.
+template <typename T>
+__device__ __forceinline__ void take_piece(const T* base, int64_t stride, bool even, int rows, int width,
+                                           int a, int m, Piece<T>& v) {
+  if (even) {
+    const int step = (int)stride * (int)sizeof(T);
+    const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<T*>(base), 0, (rows - 1) * step + width * (int)sizeof(T), 0x00020000);
+    const uint32_t lane = 8 * m < width ? 4 * a * (uint32_t)step + 8 * m * (uint32_t)sizeof(T) : 0xFFFFFFFFu;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if constexpr (sizeof(T) == 2) {
+        v.v[r] = __builtin_bit_cast(typename Piece<T>::row,
+                                    __builtin_amdgcn_raw_buffer_load_b128(buffer, lane, r * step, 0));
+      } else {
+        typedef T t4 __attribute__((ext_vector_type(4)));
+        const t4 lo = __builtin_bit_cast(t4, __builtin_amdgcn_raw_buffer_load_b128(buffer, lane, r * step, 0));
+        const t4 hi =
+            __builtin_bit_cast(t4, __builtin_amdgcn_raw_buffer_load_b128(buffer, lane, r * step + 16, 0));
+        v.v[r] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+    }
+  } else {
+    asm volatile("" : "+s"(stride), "+s"(width));
+    load_piece<T>(base, stride, rows, width, a, m, v);
+  }
+}
+
 // dQ, dK and the gradients of gates and strengths, for each (sequence, chunk, head of
 // keys): 8 waves.  What sums over the state's columns takes 64 of them at a time; a wave
-// has 16 columns of dQ and dK (dt) and NI of the chunk's 4 groups of rows.
-template <typename T, int KT>
+// has 16 columns of dQ and dK (dt) and NI of the chunk's 4 groups of rows.  The next 64
+// columns' rows are on their way while these are computed, and the states' while the
+// 64 x 64 products are.
+//
+// SHARED: several value heads to a head of keys, whose dQ and dK are added up.
+template <typename T, int KT, bool SHARED>
 __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
+  // the registers hold either the sums over heads or the next columns' rows
+  constexpr bool kEarly = KT < 4 || !SHARED;
   constexpr int N = kParts<T>, NO = kOutParts<T>, WEAK = kWeak<T>;
   constexpr int kDt = 2 * KT, NI = kDt / 2;
   constexpr int kTile = 4 * KT * N * 1024;
-  constexpr int kStage = (8 * N + 16 * NO) * 1024, kPairs = 20 * NO * 1024;
+  constexpr int kStage = 16 * (N + NO) * 1024, kPairs = 20 * NO * 1024;
   constexpr bool kApart = N < 3;
   __shared__ __attribute__((aligned(16))) char space[kStage > kPairs ? kStage : kPairs];
   __shared__ __attribute__((aligned(16))) char kcols_[kTile], qcols_[kApart ? kTile : 16];
   __shared__ __attribute__((aligned(16))) Decays dec;
-  __shared__ float eu[kC], gv[kC], qd[kDt][kC], ends[8][2];
-  char *dos = space, *us = dos + 8 * N * 1024, *gs = us + 8 * NO * 1024;
+  __shared__ float gu[kC], gv[kC], qd[kDt][kC], ends[8][2];
+  char *us = space, *gs = us + 8 * NO * 1024, *dos = gs + 8 * NO * 1024, *vs = dos + 8 * N * 1024;
   char *da = space, *dt_ = da + 6 * NO * 1024, *mm = dt_ + 6 * NO * 1024;
   char *kcols = kcols_, *qcols = kApart ? qcols_ : kcols_;
 
@@ -216,7 +251,7 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
   int b, c, hk;
   divide(blockIdx.x, (uint32_t)a.HK, b, hk);
   divide((uint32_t)b, (uint32_t)a.chunks, b, c);
-  const int shared = a.H / a.HK;
+  const int shared = SHARED ? a.H / a.HK : 1;
   const int64_t t0 = (int64_t)c * kC;
   const int steps = steps_of(a, b), rows = min(kC, steps - (int)t0);
   const int here = (int)min((int64_t)kC, a.T - t0);  // rows that are written
@@ -232,67 +267,94 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
       const int h = hk * shared + gi;
       const int64_t unit = ((int64_t)b * a.chunks + c) * a.H + h;
       const float* s0 = a.carries + unit * carry_size(a.DK, a.DV);
-      const float* u = s0 + (int64_t)a.DK * a.DV;
       const float* ds = a.dstate + unit * a.DK * a.DV;
-      const float* e = a.e + unit * kC * a.DV;
-      f4 qs[NI] = {}, k1[NI] = {}, k2[NI] = {}, pair[5] = {};
+      // 128 threads each take U, E, dO, V
+      const int pa = wave % 2 * 8 + lane / 8, pm = lane % 8, job = wave / 2;
+      const T* seq = job == 2 ? at<T>(a.o, b, t0, h) : at<T>(a.v, b, t0, h);
+      const int64_t seq_st = job == 2 ? a.o.st : a.v.st;
+      const float* dense = job == 0 ? s0 + (int64_t)a.DK * a.DV : a.e + unit * kC * a.DV;
+      const bool even = job < 2 ? a.DV % 8 == 0 : even_rows(seq, seq_st, a.DV);
+      // f32 pieces and those of the type share their registers
+      struct Raw {
+        f4 v[8];
+      } raw;
+      auto take = [&](int v0) {
+        if (job < 2) {
+          Piece<float> piece;
+          take_piece<float>(dense + v0, a.DV, even, kC, a.DV - v0, pa, pm, piece);
+          raw = __builtin_bit_cast(Raw, piece);
+        } else {
+          Piece<T> piece;
+          take_piece<T>(seq + v0, seq_st, even, rows, a.DV - v0, pa, pm, piece);
+          if constexpr (sizeof(T) == 4) {
+            raw = __builtin_bit_cast(Raw, piece);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) raw.v[r] = __builtin_bit_cast(f4, piece.v[r]);
+          }
+        }
+      };
+      f4 qs[NI] = {}, k1[NI] = {}, k2[NI] = {}, pair[5] = {}, own = {};
       float ss = 0.0f;
       __syncthreads();
       copy16(reinterpret_cast<char*>(&dec), static_cast<const char*>(a.prep) + unit * prep_bytes(3),
              sizeof(Decays));
-      if (threadIdx.x < kC) eu[threadIdx.x] = gv[threadIdx.x] = 0.0f;
+      if (kEarly) take(0);
       if (kApart && gi == 0) {
         stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, nullptr, kcols);
         stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, nullptr, qcols);
       }
       for (int v0 = 0; v0 < a.DV; v0 += 64) {
+        if (!kEarly) take(v0);
         __syncthreads();
-        const int width = a.DV - v0;
-        {
-          // 128 threads each: U; dO; G and the sums E.U; the sums G.V
-          const int pa = wave % 2 * 8 + lane / 8, pm = lane % 8, job = wave / 2;
-          if (job == 0) {
-            Piece<float> x;
-            load_piece<float>(u + v0, a.DV, kC, width, pa, pm, x);
-            store_piece<NO, 2, float>(x, pa, pm, us, nullptr);
-          } else if (job == 1) {
-            Piece<T> x;
-            load_piece<T>(at<T>(a.o, b, t0, h) + v0, a.o.st, rows, width, pa, pm, x);
-            store_piece<N, 2, T>(x, pa, pm, dos, nullptr);
-          } else {
-            Piece<float> p;
-            float x[4][8], y[4][8];
-            load_piece<float>(e + v0, a.DV, kC, width, pa, pm, p);
-            unpack_piece<float>(p, x);
-            if (job == 2) {
-              load_piece<float>(u + v0, a.DV, kC, width, pa, pm, p);
-              unpack_piece<float>(p, y);
-            } else {
-              Piece<T> q;
-              load_piece<T>(at<T>(a.v, b, t0, h) + v0, a.v.st, rows, width, pa, pm, q);
-              unpack_piece<T>(q, y);
+        // the states' 64 columns, rows dcol: two halves of 4 columns for each 32
+        f4 x[4], y[4];
+        if (a.DV % 4 == 0) {
+          const int bytes = a.DK * a.DV * 4;
+          const __amdgpu_buffer_rsrc_t xb =
+              __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(s0), 0, bytes, 0x00020000);
+          const __amdgpu_buffer_rsrc_t yb =
+              __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(ds), 0, bytes, 0x00020000);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int v = v0 + 16 * k + 4 * g;
+            const uint32_t off = v < a.DV && dcol < a.DK ? (uint32_t)(dcol * a.DV + v) * 4 : 0xFFFFFFFFu;
+            x[k] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(xb, off, 0, 0));
+            y[k] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(yb, off, 0, 0));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float p[4] = {}, q[4] = {};
+            if (dcol < a.DK) {
+              load_few<float, 4>(s0 + (int64_t)dcol * a.DV, v0 + 16 * k + 4 * g, a.DV, p);
+              load_few<float, 4>(ds + (int64_t)dcol * a.DV, v0 + 16 * k + 4 * g, a.DV, q);
             }
-            float sum[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float w = dec.w[4 * pa + r];
-              sum[r] = 0.0f;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                sum[r] += x[r][k] * y[r][k];
-                x[r][k] *= w;
-              }
-              if (job == 3) sum[r] *= w;
-#pragma unroll
-              for (int q = 0; q < 3; ++q) sum[r] += xor_lanes(sum[r], q);
-              if (pm == 0) (job == 2 ? eu : gv)[4 * pa + r] += sum[r];
-            }
-            if (job == 2) store_piece<NO, 2>(x, pa, pm, gs);
+            x[k] = f4{p[0], p[1], p[2], p[3]};
+            y[k] = f4{q[0], q[1], q[2], q[3]};
           }
         }
+        if (job < 2) {
+          Piece<float> piece = __builtin_bit_cast(Piece<float>, raw);
+          if (job == 1) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) piece.v[r] *= dec.w[4 * pa + r];
+          }
+          store_piece<NO, 2, float>(piece, pa, pm, job == 0 ? us : gs, nullptr);
+        } else {
+          Piece<T> piece;
+          if constexpr (sizeof(T) == 4) {
+            piece = __builtin_bit_cast(Piece<T>, raw);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) piece.v[r] = __builtin_bit_cast(typename Piece<T>::row, raw.v[r]);
+          }
+          store_piece<N, 2, T>(piece, pa, pm, job == 2 ? dos : vs, nullptr);
+        }
         __syncthreads();
+        if (kEarly && v0 + 64 < a.DV) take(v0 + 64);
         // 64 x 64 products: waves 0 to 3 G U^T, twice for the 16 x 16 on the diagonal (once
-        // for each side of it), waves 4 to 7 dO U^T and its transpose
+        // for each side of it), waves 4 to 7 dO U^T and its transpose; and 16 x 16 of V G^T
 #pragma unroll 1
         for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
@@ -302,42 +364,36 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
               // rows j, columns i: U_j G_i above the diagonal of this result, G_j U_i below
               const int it = wave, jt = p < 2 ? wave : (wave + p - 1) & 3;
               const bool up = p < 2 ? p == 0 : jt < it;
-              bf8 x[NO], y[NO];
-              load_rows<NO, 2>(up ? us : gs, jt, kt, x, lane);
-              load_rows<NO, 2>(up ? gs : us, it, kt, y, lane);
-              pair[p] = mul<WEAK>(x, y, pair[p]);
+              bf8 u[NO], w[NO];
+              load_rows<NO, 2>(up ? us : gs, jt, kt, u, lane);
+              load_rows<NO, 2>(up ? gs : us, it, kt, w, lane);
+              pair[p] = mul<WEAK>(u, w, pair[p]);
             } else {
               const int id = (wave - 4) * 5 + p, k = id % 10;
               const int it = k < 1 ? 0 : k < 3 ? 1 : k < 6 ? 2 : 3, jt = k - it * (it + 1) / 2;
-              bf8 x[NO], y[N];
-              load_rows<NO, 2>(us, jt, kt, x, lane);
-              load_rows<N, 2>(dos, it, kt, y, lane);
-              pair[p] = id < 10 ? mul<WEAK>(x, y, pair[p]) : mul<WEAK>(y, x, pair[p]);
+              bf8 u[NO], w[N];
+              load_rows<NO, 2>(us, jt, kt, u, lane);
+              load_rows<N, 2>(dos, it, kt, w, lane);
+              pair[p] = id < 10 ? mul<WEAK>(u, w, pair[p]) : mul<WEAK>(w, u, pair[p]);
             }
+          }
+          if (wave >= 4) {
+            bf8 u[N], w[NO];
+            load_rows<N, 2>(vs, wave - 4, kt, u, lane);
+            load_rows<NO, 2>(gs, wave - 4, kt, w, lane);
+            own = mul<WEAK>(u, w, own);
           }
         }
         // dO S^T, U dS^T, G S^T
-#pragma unroll 1
+#pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
-          const int v = v0 + 32 * kt + 4 * g;
-          f4 x[2], y[2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float p[4] = {}, q[4] = {};
-            if (dcol < a.DK) {
-              load_few<float, 4>(s0 + (int64_t)dcol * a.DV, v + 16 * k, a.DV, p);
-              load_few<float, 4>(ds + (int64_t)dcol * a.DV, v + 16 * k, a.DV, q);
-            }
+          for (int k = 2 * kt; k < 2 * kt + 2; ++k)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              x[k][r] = p[r];
-              y[k][r] = q[r];
-              ss += p[r] * q[r];
-            }
-          }
+            for (int r = 0; r < 4; ++r) ss += x[k][r] * y[k][r];
           bf8 xp[NO], yp[NO];
-          split<NO>(x[0], x[1], xp);
-          split<NO>(y[0], y[1], yp);
+          split<NO>(x[2 * kt], x[2 * kt + 1], xp);
+          split<NO>(y[2 * kt], y[2 * kt + 1], yp);
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
             __builtin_amdgcn_sched_barrier(0);
@@ -352,7 +408,15 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
         }
       }
       __syncthreads();
-      // the 64 x 64 matrices with their decays, as operands
+      // the 64 x 64 matrices with their decays, as operands; G.U and G.V of each row
+      if (n / 4 == g) {
+        const int row = 16 * (wave & 3) + n;
+        if (wave < 4) {
+          gu[row] = pair[0][n & 3];
+        } else {
+          gv[row] = own[n & 3];
+        }
+      }
       if (wave < 4) {
         const int it = wave;
 #pragma unroll
@@ -462,8 +526,13 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
           for (int q = 0; q < 4; ++q) x += xor_lanes(x, q);
           if (n == 0) qd[dt][16 * it + 4 * g + r] = x;
         }
-        dq[i] += qs[i];
-        dk[i] += k1[i];
+        if (SHARED) {
+          dq[i] += qs[i];
+          dk[i] += k1[i];
+        } else {
+          dq[i] = qs[i];
+          dk[i] = k1[i];
+        }
       }
       // dS . S behind the chunk
       if (i0 > 0) ss = 0.0f;
@@ -505,8 +574,10 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
           const float wt = on ? (float)*at<T>(a.b, b, t0 + lane, h) : 0.0f;
           *const_cast<T*>(at<T>(a.dg, b, t0 + lane, h)) =
               (T)(on && !reset ? (float)z / (1.0f + expf(gate)) : 0.0f);
+          // E.U (1 - w), and G = w E; U is a multiple of w, so nothing is lost where w is 0
+          const float w = dec.w[lane];
           *const_cast<T*>(at<T>(a.db, b, t0 + lane, h)) =
-              (T)(on ? eu[lane] / (1.0f + expf(wt)) : 0.0f);
+              (T)(on && w > 0.0f ? gu[lane] / w / (1.0f + expf(wt)) : 0.0f);
         }
       }
     }
@@ -563,7 +634,8 @@ hipError_t launch_delta_backward(const DeltaArgs& a, int type, hipStream_t s) {
       e = enqueue(waves == 4 ? K::four : K::eight, dim3(heads * slices * a.segments), dim3(64 * waves), 0, s, a,
                   slices);
       if (e != hipSuccess || a.chunks == 0) return e;
-      return enqueue(delta_gradient_kernel<T, KT>, dim3((uint32_t)(a.B * a.chunks * a.HK)), dim3(512), 0, s, a);
+      return enqueue(a.H > a.HK ? delta_gradient_kernel<T, KT, true> : delta_gradient_kernel<T, KT, false>,
+                     dim3((uint32_t)(a.B * a.chunks * a.HK)), dim3(512), 0, s, a);
     });
   });
 }

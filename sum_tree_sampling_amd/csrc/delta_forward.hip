@@ -301,7 +301,7 @@ void delta_segments(DeltaArgs& a) {
   a.segments = 1;
   a.segment_chunks = (int)a.chunks;
   const int64_t groups = a.B * a.H * ((a.DV + 63) / 64);
-  if (a.chunks < 16 || groups == 0 || groups > 128) return;
+  if (a.chunks < 16 || groups == 0 || groups > 64) return;
   int64_t n = 4;
   while (n * n < 2 * a.chunks && n < 64) ++n;  // as long in the walk as in a segment
   n = std::min(n, std::max<int64_t>(2, 512 / groups));
