@@ -74,7 +74,8 @@ struct DeltaArgs {
   int segment_chunks;
   float* states;          // [B x H x segments x DK x DV] that segments begin with
   float* locals;          // [..] what a segment makes of a state of 0
-  float* maps;            // [B x H x segments x DK x DK] what it makes of the unit columns
+  float* maps;            // [B x H x segments x DK x 32, 64 or 128] what it makes of the unit columns
+  int* flags;             // [B x H x segments] whether it has a reset
 };
 size_t delta_workspace(int64_t B, int64_t T, int64_t H, int64_t DK, int64_t DV, int type,
                        bool backward, DeltaArgs* a, void* ws);

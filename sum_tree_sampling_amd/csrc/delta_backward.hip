@@ -39,6 +39,7 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 && !LOCAL ? 1 : 4))) vo
   const bool even = even_rows(ks, a.k.st, a.DK) && even_rows(qs, a.q.st, a.DK);
   T* dvs = const_cast<T*>(at<T>(a.dv, b, 0, h));
 
+  bool cut = false;  // a reset was met
   f4 s[2 * KT];
   if constexpr (LOCAL) {
     unit_state<2 * KT>(unit_columns ? col : -1, s);
@@ -64,6 +65,7 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 && !LOCAL ? 1 : 4))) vo
     char* now = room + (kTwice ? flip * kRoom : 0);
     const Decays& dec = *reinterpret_cast<const Decays*>(now + kReady);
     const bool resets = __builtin_amdgcn_readfirstlane(dec.resets[kC - 1]) != 0;
+    cut |= resets;
     uint32_t me = (uint32_t)(now - room) + (uint32_t)lane * 16;
     asm volatile("" : "+v"(me));
     f4 o[4];
@@ -182,9 +184,11 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 && !LOCAL ? 1 : 4))) vo
     __syncthreads();
   }
   if constexpr (LOCAL) {
-    float* to = unit_columns ? a.maps + place * a.DK * a.DK : a.locals + place * a.DK * a.DV;
-    const int wide = unit_columns ? a.DK : a.DV;
+    // maps have rows of whole 32 columns
+    float* to = unit_columns ? a.maps + place * a.DK * 32 * KT : a.locals + place * a.DK * a.DV;
+    const int wide = unit_columns ? 32 * KT : a.DV;
     store_column<float, 2 * KT>(to, wide, a.DK, col, wide, s);
+    if (slice == 0 && threadIdx.x == 0) a.flags[place] = cut;
   } else {
     if (a.s_last && seg == 0)
       store_column<float, 2 * KT>(a.s_last + (int64_t)bh * a.DK * a.DV, a.DV, a.DK, col, a.DV, s);
@@ -203,7 +207,7 @@ __device__ __forceinline__ void take_piece(const T* base, int64_t stride, bool e
     const int step = (int)stride * (int)sizeof(T);
     const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<T*>(base), 0, (rows - 1) * step + width * (int)sizeof(T), 0x00020000);
-    const uint32_t lane = 8 * m < width ? 4 * a * (uint32_t)step + 8 * m * (uint32_t)sizeof(T) : 0xFFFFFFFFu;
+    const uint32_t lane = 8 * m < width ? 4 * a * (uint32_t)step + 8 * m * (uint32_t)sizeof(T) : kNowhere;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       if constexpr (sizeof(T) == 2) {
@@ -294,6 +298,11 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
           }
         }
       };
+      float gate = 0.0f, wt = 0.0f;
+      if (wave == 0 && lane < rows) {
+        gate = (float)*at<T>(a.g, b, t0 + lane, h);
+        wt = (float)*at<T>(a.b, b, t0 + lane, h);
+      }
       f4 qs[NI] = {}, k1[NI] = {}, k2[NI] = {}, pair[5] = {}, own = {};
       float ss = 0.0f;
       __syncthreads();
@@ -318,7 +327,7 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int v = v0 + 16 * k + 4 * g;
-            const uint32_t off = v < a.DV && dcol < a.DK ? (uint32_t)(dcol * a.DV + v) * 4 : 0xFFFFFFFFu;
+            const uint32_t off = v < a.DV && dcol < a.DK ? (uint32_t)(dcol * a.DV + v) * 4 : kNowhere;
             x[k] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(xb, off, 0, 0));
             y[k] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(yb, off, 0, 0));
           }
@@ -570,8 +579,6 @@ __global__ __launch_bounds__(512) void delta_gradient_kernel(DeltaArgs a) {
         const bool reset = lane == 0 ? mine != 0 : mine != before;
         if (lane < here) {
           const bool on = lane < rows;
-          const float gate = on ? (float)*at<T>(a.g, b, t0 + lane, h) : 0.0f;
-          const float wt = on ? (float)*at<T>(a.b, b, t0 + lane, h) : 0.0f;
           *const_cast<T*>(at<T>(a.dg, b, t0 + lane, h)) =
               (T)(on && !reset ? (float)z / (1.0f + expf(gate)) : 0.0f);
           // E.U (1 - w), and G = w E; U is a multiple of w, so nothing is lost where w is 0

@@ -42,6 +42,9 @@ namespace per {
 namespace {
 
 constexpr int kC = PER_DELTA_CHUNK;
+// A place in a buffer that is out of range: a lane's offset is compared with what the
+// buffer has behind the scalar offset, so the two are never added first.
+constexpr uint32_t kNowhere = 0xFFFFFFFFu;
 typedef bf16_t bf8 __attribute__((ext_vector_type(8)));
 typedef bf16_t bf4 __attribute__((ext_vector_type(4)));
 typedef float f4 __attribute__((ext_vector_type(4)));
@@ -313,11 +316,13 @@ __device__ __forceinline__ float decay(const Decays& d, int i, int j) {
 template <typename T, int KT, bool BACKWARD>
 __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
   constexpr int N = kParts<T>, NS = kScoreParts<T>(BACKWARD), kPad = 68;
-  __shared__ __attribute__((aligned(16))) char ks[4 * KT * N * 1024];
-  __shared__ __attribute__((aligned(16))) char qs[4 * KT * N * 1024];
-  __shared__ __attribute__((aligned(16))) float lower[kC][kPad];
-  __shared__ __attribute__((aligned(16))) float inv[kC][kPad];
-  __shared__ Decays dec;
+  // keys and queries make room for A and its inverse
+  constexpr int kTile = 4 * KT * N * 1024, kMatrix = kC * kPad * 4;
+  __shared__ __attribute__((aligned(16))) char room[2 * kTile > 2 * kMatrix ? 2 * kTile : 2 * kMatrix];
+  __shared__ __attribute__((aligned(16))) Decays dec;
+  char *ks = room, *qs = room + kTile;
+  float(*lower)[kPad] = reinterpret_cast<float(*)[kPad]>(room);
+  float(*inv)[kPad] = reinterpret_cast<float(*)[kPad]>(room + kMatrix);
   const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   int b, c, h;
@@ -328,13 +333,17 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
   if (rows <= 0) return;
   char* out = static_cast<char*>(a.prep) + (int64_t)blockIdx.x * prep_bytes(NS);
   const int hk = h / (a.H / a.HK);
+  const bool on = lane < rows;
+  float gate = 0.0f, wt = 0.0f;
+  bool reset = false;
+  if (wave == 3 && on) {
+    gate = (float)*at<T>(a.g, b, t0 + lane, h);
+    wt = (float)*at<T>(a.b, b, t0 + lane, h);
+    reset = a.reset && a.reset[b * a.T + t0 + lane];
+  }
   stage<T, KT>(at<T>(a.k, b, t0, hk), a.k.st, rows, a.DK, ks, nullptr);
   stage<T, KT>(at<T>(a.q, b, t0, hk), a.q.st, rows, a.DK, qs, nullptr);
   if (wave == 3) {
-    const bool on = lane < rows;
-    const float gate = on ? (float)*at<T>(a.g, b, t0 + lane, h) : 0.0f;
-    const float wt = on ? (float)*at<T>(a.b, b, t0 + lane, h) : 0.0f;
-    const bool reset = on && a.reset && a.reset[b * a.T + t0 + lane];
     // log f; a gate below 2^-256 is 0 in f32 whatever it is
     const float lf = fminf(gate, 0.0f) - log1pf(expf(-fabsf(gate)));
     double log = reset ? -4096.0 : on ? fmax((double)lf * 1.4426950408889634074, -256.0) : 0.0;
@@ -354,7 +363,6 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     dec.last[lane] = __builtin_amdgcn_exp2f((float)(end - log));
     dec.w[lane] = on ? 1.0f / (1.0f + expf(-wt)) : 0.0f;
   }
-  for (int i = threadIdx.x; i < kC * kPad; i += 256) (&inv[0][0])[i] = 0.0f;
   __syncthreads();
   for (int i = threadIdx.x; i < (int)sizeof(Decays) / 16; i += 256)
     reinterpret_cast<f4*>(out)[i] = reinterpret_cast<const f4*>(&dec)[i];
@@ -362,7 +370,10 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
   // 12 pairs of 16 rows and 16 columns, 10 of them on or below the diagonal: A for the
   // inverse, and scores as halves of blocks, zeros above the diagonal
   char* scores = out + sizeof(Decays) + 6 * kInvParts * 1024;
-  for (int id = wave; id < 12; id += 4) {
+  f4 mine[3];
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    const int id = wave + 4 * p;
     const int it = id < 4 ? id / 2 : 2 + (id - 4) / 4, jt = id < 4 ? id % 2 : (id - 4) % 4;
     f4 kk = {}, qk = {};
     if (jt <= it) {
@@ -384,16 +395,31 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
       for (int r = 0; r < 4; ++r) {
         const int i = 16 * it + (BACKWARD ? 4 * g + r : n), j = 16 * jt + (BACKWARD ? n : 4 * g + r);
         const float d = decay(dec, i, j);
-        lower[i][j] = j < i ? dec.w[i] * d * kk[r] : 0.0f;
+        kk[r] = j < i ? dec.w[i] * d * kk[r] : 0.0f;
         qk[r] = j <= i ? d * qk[r] : 0.0f;
       }
     }
+    mine[p] = kk;
     if (BACKWARD) {  // rows of it are the terms of a row of jt
       if (it / 2 >= jt / 2 && jt < 4) store_half<NS>(scores, upper_block(jt, it / 2), it % 2, qk, lane);
     } else {
       store_half<NS>(scores, lower_block(it, jt / 2), jt % 2, qk, lane);
     }
   }
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    const int id = wave + 4 * p;
+    const int it = id < 4 ? id / 2 : 2 + (id - 4) / 4, jt = id < 4 ? id % 2 : (id - 4) % 4;
+    if (jt <= it) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * it + (BACKWARD ? 4 * g + r : n), j = 16 * jt + (BACKWARD ? n : 4 * g + r);
+        lower[i][j] = mine[p][r];
+      }
+    }
+  }
+  for (int i = threadIdx.x; i < kC * kPad; i += 256) (&inv[0][0])[i] = 0.0f;
   __syncthreads();
 
   // (I + A)^-1: the blocks of 16 on the diagonal by substitution, a column to a lane
@@ -512,7 +538,7 @@ struct Column {
     const int bytes = (rows - 1) * step + width * (int)sizeof(T);
     buffer = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, rows > 0 ? bytes : 0, 0x00020000);
     lane = col < width ? (threadIdx.x & 63) / 16 * 4 * (uint32_t)step + (uint32_t)col * (uint32_t)sizeof(T)
-                       : 0xFFFFFFFFu;
+                       : kNowhere;
   }
   __device__ __forceinline__ void load(T (&v)[TILES][4]) const {
 #pragma unroll
@@ -635,7 +661,7 @@ struct Ahead {
         int step = (int)stride * (int)sizeof(T);
         const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<T*>(base), 0, (rows - 1) * step + DK * (int)sizeof(T), 0x00020000);
-        const uint32_t lane = 8 * m < DK ? 4 * a * (uint32_t)step + 8 * m * (uint32_t)sizeof(T) : 0xFFFFFFFFu;
+        const uint32_t lane = 8 * m < DK ? 4 * a * (uint32_t)step + 8 * m * (uint32_t)sizeof(T) : kNowhere;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           if constexpr (sizeof(T) == 2) {
@@ -692,57 +718,78 @@ __device__ __forceinline__ bool even_rows(const T* p, int64_t stride, int D) {
 }
 
 // The states that the segments of a cut time axis begin with (in REVERSE: the gradients
-// behind them), one after the other: S = map S + local, 16 columns to a wave.  A segment
-// with a reset takes nothing over, whatever S holds.
+// behind them), one after the other: S = map S + local.  A workgroup has 16 columns, a
+// quarter of their rows to a wave; the parts of S go round through LDS, and the next
+// segment's map is loaded meanwhile.  A segment with a reset takes nothing over, whatever
+// S holds.
 template <int KT, bool REVERSE>
 __global__ __launch_bounds__(256) void delta_join_kernel(DeltaArgs a, int slices) {
+  constexpr int kTiles = KT == 1 ? 1 : KT / 2;  // of 16 rows for a wave
+  __shared__ __attribute__((aligned(16))) char room[2][KT * 3 * 1024];
   const int lane = threadIdx.x & 63, g = lane / 16, n = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  int bh, b, h, slice;
+  int bh, slice;
   divide(blockIdx.x, (uint32_t)slices, bh, slice);
-  divide((uint32_t)bh, (uint32_t)a.H, b, h);
-  const int col = (slice * 4 + wave) * 16 + n;
-  const int steps = steps_of(a, b);
-  f4 s[2 * KT];
-  load_state<2 * KT>(a.s0 ? a.s0 + (int64_t)bh * a.DK * a.DV : nullptr, a.DK, a.DV, col, s);
+  const int col = slice * 16 + n, row0 = 16 * kTiles * wave;  // the wave's first row
+  const int rows = min(16 * kTiles, a.DK - row0);             // none where it is not above 0
+  const int64_t size = (int64_t)a.DK * a.DV;
+  f4 s[kTiles];
+  load_state<kTiles>(a.s0 ? a.s0 + bh * size + (int64_t)row0 * a.DV : nullptr, rows, a.DV, col, s);
+  auto place = [&](int k) { return (int64_t)bh * a.segments + (REVERSE ? a.segments - 1 - k : k); };
+  f4 map[kTiles][KT][2];
+  float local[kTiles][4];
+  int resets = 0;
+  auto take = [&](int k) {
+    const int64_t at = place(k);
+    const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
+        a.maps + at * a.DK * 32 * KT, 0, a.DK * 32 * KT * 4, 0x00020000);
+    const uint32_t off = (uint32_t)((row0 + n) * 32 * KT + 4 * g) * 4;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          map[t][kt][half] = __builtin_bit_cast(
+              f4, __builtin_amdgcn_raw_buffer_load_b128(buffer, off + ((16 * t * KT + kt) * 32 + 16 * half) * 4, 0, 0));
+        }
+    load_column<float, kTiles>(a.locals + at * size + (int64_t)row0 * a.DV, a.DV, rows, col, a.DV, local);
+    resets = a.flags[at];
+  };
+  take(0);
   for (int k = 0; k < a.segments; ++k) {
-    const int seg = REVERSE ? a.segments - 1 - k : k;
-    const int64_t place = (int64_t)bh * a.segments + seg;
-    store_column<float, 2 * KT>(a.states + place * a.DK * a.DV, a.DV, a.DK, col, a.DV, s);
-    if (k == a.segments - 1) break;
-    float local[2 * KT][4];
-    load_column<float, 2 * KT>(a.locals + place * a.DK * a.DV, a.DV, a.DK, col, a.DV, local);
-    const int from = seg * a.segment_chunks * kC, end = min(steps, from + a.segment_chunks * kC);
-    bool reset = false;
-    if (a.reset)
-      for (int t = from + lane; t < end; t += 64) reset |= a.reset[b * a.T + t] != 0;
-    f4 y[2 * KT];
+    float* to = a.states + place(k) * size + (int64_t)row0 * a.DV;
+    if (k == a.segments - 1) {
+      store_column<float, kTiles>(to, a.DV, rows, col, a.DV, s);
+      break;
+    }
+    char* parts = room[k & 1];
+    f4 y[kTiles];
+    bf8 mp[kTiles][KT][3];
 #pragma unroll
-    for (int t = 0; t < 2 * KT; ++t)
+    for (int t = 0; t < kTiles; ++t) {
+      const int tile = wave * kTiles + t;
+      if (tile < 2 * KT) store_half<3>(parts, tile / 2, tile % 2, s[t], lane);
+      y[t] = f4{local[t][0], local[t][1], local[t][2], local[t][3]};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) y[t][r] = local[t][r];
-    if (__ballot(reset) == 0) {
-      const float* map = a.maps + place * a.DK * a.DK;
+      for (int kt = 0; kt < KT; ++kt) split<3>(map[t][kt][0], map[t][kt][1], mp[t][kt]);
+    }
+    const bool reset = __builtin_amdgcn_readfirstlane(resets) != 0;
+    if (k + 2 < a.segments) take(k + 1);
+    // behind the loads, which are waited for before it
+    store_column<float, kTiles>(to, a.DV, rows, col, a.DV, s);
+    __syncthreads();
+    if (!reset) {
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         bf8 sp[3];
-        split<3>(s[2 * kt], s[2 * kt + 1], sp);
-#pragma unroll 2
-        for (int dt = 0; dt < 2 * KT; ++dt) {
-          const int row = 16 * dt + n;
-          float lo[4] = {}, hi[4] = {};
-          if (row < a.DK) {
-            load_few<float, 4>(map + (int64_t)row * a.DK, 32 * kt + 4 * g, a.DK, lo);
-            load_few<float, 4>(map + (int64_t)row * a.DK, 32 * kt + 16 + 4 * g, a.DK, hi);
-          }
-          bf8 mp[3];
-          split<3>(f4{lo[0], lo[1], lo[2], lo[3]}, f4{hi[0], hi[1], hi[2], hi[3]}, mp);
-          y[dt] = mul<2>(mp, sp, y[dt]);
-        }
+        load_block<3>(parts + kt * 3 * 1024, sp, lane);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) y[t] = mul<2>(mp[t][kt], sp, y[t]);
       }
     }
 #pragma unroll
-    for (int t = 0; t < 2 * KT; ++t) s[t] = y[t];
+    for (int t = 0; t < kTiles; ++t) s[t] = y[t];
   }
 }
 
@@ -790,7 +837,7 @@ template <bool REVERSE>
 hipError_t launch_join(const DeltaArgs& a, hipStream_t s) {
   return by_keys(a.DK, [&](auto keys) {
     constexpr int KT = decltype(keys)::value;
-    const int slices = (a.DV + 63) / 64;
+    const int slices = (a.DV + 15) / 16;
     return enqueue(delta_join_kernel<KT, REVERSE>, dim3((uint32_t)(a.B * a.H * slices)), dim3(256), 0, s, a,
                    slices);
   });

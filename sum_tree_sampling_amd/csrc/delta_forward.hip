@@ -47,6 +47,7 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 && !LOCAL ? 1 : 4))) vo
   const bool even = even_rows(ks, a.k.st, a.DK) && even_rows(qs, a.q.st, a.DK);
   T* os = const_cast<T*>(at<T>(a.o, b, 0, h));
 
+  bool cut = false;  // a reset was met
   f4 s[2 * KT];
   if constexpr (LOCAL) {
     unit_state<2 * KT>(unit_columns ? col : -1, s);
@@ -71,6 +72,7 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 && !LOCAL ? 1 : 4))) vo
     char* now = room + (kTwice ? flip * kRoom : 0);
     const Decays& dec = *reinterpret_cast<const Decays*>(now + kReady);
     const bool resets = __builtin_amdgcn_readfirstlane(dec.resets[kC - 1]) != 0;
+    cut |= resets;
     // one register for all places in LDS
     uint32_t me = (uint32_t)(now - room) + (uint32_t)lane * 16;
     asm volatile("" : "+v"(me));
@@ -193,9 +195,11 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 && !LOCAL ? 1 : 4))) vo
     __syncthreads();
   }
   if constexpr (LOCAL) {
-    float* to = unit_columns ? a.maps + place * a.DK * a.DK : a.locals + place * a.DK * a.DV;
-    const int wide = unit_columns ? a.DK : a.DV;
+    // maps have rows of whole 32 columns
+    float* to = unit_columns ? a.maps + place * a.DK * 32 * KT : a.locals + place * a.DK * a.DV;
+    const int wide = unit_columns ? 32 * KT : a.DV;
     store_column<float, 2 * KT>(to, wide, a.DK, col, wide, s);
+    if (slice == 0 && threadIdx.x == 0) a.flags[place] = cut;
   } else {
     // the segment that the sequence ends in has the last state; what lies behind is 0
     const int last = a.segments > 1 && steps > 0 ? (steps - 1) / (a.segment_chunks * kC) : 0;
@@ -207,81 +211,90 @@ __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 && !LOCAL ? 1 : 4))) vo
   }
 }
 
-// One step: a workgroup has a head's state, 32 groups of 4 columns by PARTS groups of 16
-// rows, so all of it is asked for at once.  The state is read and written once.
-template <typename T, int PARTS>
+// One step: a workgroup has 128 columns of a head's state, 32 groups of 4 columns by PARTS
+// groups of 16 rows, so all of it is asked for at once.  The state is read and written
+// once.  The code is short on purpose (buffer descriptors instead of guards; WHOLE: rows
+// are whole groups of 4 columns): a small call runs it once, and waits for it to come in.
+template <typename T, int PARTS, bool WHOLE>
 __global__ __launch_bounds__(32 * PARTS) void delta_step_kernel(DeltaArgs a, int slices) {
   __shared__ float sum[2][PARTS][128];
-  __shared__ float ks[16 * PARTS], qs[16 * PARTS];
+  __shared__ float ks[2][16 * PARTS];
   int bh, b, h, hk, slice, rest;
   divide(blockIdx.x, (uint32_t)slices, bh, slice);
   divide((uint32_t)bh, (uint32_t)a.H, b, h);
   divide((uint32_t)h, (uint32_t)(a.H / a.HK), hk, rest);
   const int part = threadIdx.x / 32, cl = threadIdx.x % 32 * 4, col = slice * 128 + cl;
-  const float* s = a.s0 + (int64_t)bh * a.DK * a.DV;
-  float v[16][4];
-  const bool reset = a.reset && a.reset[b];
+  const int pitch = a.DV * 4, bytes = a.DK * pitch;
+  const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(a.s0) + (int64_t)bh * a.DK * a.DV, 0, bytes, 0x00020000);
+  const __amdgpu_buffer_rsrc_t to =
+      __builtin_amdgcn_make_buffer_rsrc(a.s_last + (int64_t)bh * a.DK * a.DV, 0, bytes, 0x00020000);
+  uint32_t off[WHOLE ? 1 : 4];
+#pragma unroll
+  for (int i = 0; i < (WHOLE ? 1 : 4); ++i)
+    off[i] = col + i < a.DV ? (uint32_t)(part * 16 * pitch + (col + i) * 4) : kNowhere;
+  f4 v[16];
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
-    const int row = part * 16 + r;
+    if constexpr (WHOLE) {
+      v[r] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(from, off[0], r * pitch, 0));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[r][i] = 0.0f;
-    if (row < a.DK && !reset) load_few<float, 4>(s + (int64_t)row * a.DV, col, a.DV, v[r]);
+      for (int i = 0; i < 4; ++i)
+        v[r][i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(from, off[i], r * pitch, 0));
+    }
   }
   {
-    const int i = threadIdx.x;
-    const int c = i % (16 * PARTS);
-    const T* from = i < 16 * PARTS ? at<T>(a.k, b, 0, hk) : at<T>(a.q, b, 0, hk);
-    (i < 16 * PARTS ? ks : qs)[c] = c < a.DK ? (float)from[c] : 0.0f;
+    const int i = threadIdx.x, c = i % (16 * PARTS);
+    const T* row = i < 16 * PARTS ? at<T>(a.k, b, 0, hk) : at<T>(a.q, b, 0, hk);
+    ks[i / (16 * PARTS)][c] = c < a.DK ? (float)row[c] : 0.0f;
   }
-  float vs[4];
-  load_few<T, 4>(at<T>(a.v, b, 0, h), col, a.DV, vs);
+  f4 x = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col + i < a.DV) x[i] = (float)at<T>(a.v, b, 0, h)[col + i];
   const float gate = (float)*at<T>(a.g, b, 0, h), wt = (float)*at<T>(a.b, b, 0, h);
+  const bool reset = a.reset && a.reset[b];
   const float f = 1.0f / (1.0f + expf(-gate)), w = 1.0f / (1.0f + expf(-wt));
   __syncthreads();
-  float k[4] = {}, q[4] = {};
+  f4 kv = {}, qv = {};
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
-    const float kr = ks[part * 16 + r];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[r][i] *= f;
-      k[i] += kr * v[r][i];
-    }
+    v[r] = reset ? f4{} : v[r] * f;
+    kv += ks[0][part * 16 + r] * v[r];
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) sum[0][part][cl + i] = k[i];
+  *reinterpret_cast<f4*>(&sum[0][part][cl]) = kv;
   __syncthreads();
-  float u[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x = 0.0f;
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p) x += sum[0][p][cl + i];
-    u[i] = col + i < a.DV ? w * (vs[i] - x) : 0.0f;
-  }
-  float* to = a.s_last + (int64_t)bh * a.DK * a.DV;
+  for (int p = 0; p < PARTS; ++p) x -= *reinterpret_cast<const f4*>(&sum[0][p][cl]);
+  x *= w;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
-    const int row = part * 16 + r;
-    const float kr = ks[row], qr = qs[row];
+    v[r] += ks[0][part * 16 + r] * x;
+    qv += ks[1][part * 16 + r] * v[r];
+    if constexpr (WHOLE) {
+      // The row's place is added in the lane: the registers of a 16 byte store at a scalar
+      // offset can be written again too early (seen here), which the compiler does not know.
+      typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+      const uint32_t place = col < a.DV ? off[0] + (uint32_t)(r * pitch) : kNowhere;
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v[r]), to, place, 0, 0);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[r][i] += kr * u[i];
-      q[i] += qr * v[r][i];
+      for (int i = 0; i < 4; ++i) {
+        const float y = v[r][i];  // a cast of a vector's element itself takes the first one
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, y), to, off[i], r * pitch, 0);
+      }
     }
-    if (row < a.DK) store_few<float, 4>(to + (int64_t)row * a.DV, col, a.DV, v[r]);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) sum[1][part][cl + i] = q[i];
+  *reinterpret_cast<f4*>(&sum[1][part][cl]) = qv;
   __syncthreads();
   for (int i = threadIdx.x; i < 128; i += 32 * PARTS) {
     const int c = slice * 128 + i;
     if (c >= a.DV) break;
-    float x = 0.0f;
+    float y = 0.0f;
 #pragma unroll
-    for (int p = 0; p < PARTS; ++p) x += sum[1][p][i];
-    const_cast<T*>(at<T>(a.o, b, 0, h))[c] = (T)(a.scale * x);
+    for (int p = 0; p < PARTS; ++p) y += sum[1][p][i];
+    const_cast<T*>(at<T>(a.o, b, 0, h))[c] = (T)(a.scale * y);
   }
 }
 
@@ -304,7 +317,7 @@ void delta_segments(DeltaArgs& a) {
   if (a.chunks < 16 || groups == 0 || groups > 64) return;
   int64_t n = 4;
   while (n * n < 2 * a.chunks && n < 64) ++n;  // as long in the walk as in a segment
-  n = std::min(n, std::max<int64_t>(2, 512 / groups));
+  n = std::min(n, std::max<int64_t>(2, 256 / groups));  // a workgroup to a CU
   a.segment_chunks = (int)((a.chunks + n - 1) / n);
   a.segments = (int)((a.chunks + a.segment_chunks - 1) / a.segment_chunks);
 }
@@ -321,7 +334,7 @@ size_t delta_workspace(int64_t B, int64_t T, int64_t H, int64_t DK, int64_t DV, 
   const int64_t units = B * a.chunks * H;
   const size_t prep = (size_t)units * prep_bytes_of(type, backward);
   const size_t places = a.segments > 1 ? (size_t)(B * H * a.segments) : 0;
-  const size_t state = ((size_t)(DK * DV) * 4 + 15) / 16 * 16, map = (size_t)(DK * DK) * 4;
+  const size_t state = ((size_t)(DK * DV) * 4 + 15) / 16 * 16, map = (size_t)(DK * (DK <= 32 ? 32 : DK <= 64 ? 64 : 128)) * 4;
   char* p = static_cast<char*>(ws);
   auto take = [&](size_t bytes) {
     float* at = reinterpret_cast<float*>(p);
@@ -332,6 +345,7 @@ size_t delta_workspace(int64_t B, int64_t T, int64_t H, int64_t DK, int64_t DV, 
   a.states = take(places * state);
   a.locals = take(places * state);
   a.maps = take(places * map);
+  a.flags = reinterpret_cast<int*>(take(places * sizeof(int)));
   if (backward) {
     a.dstate = take((size_t)(units * DK * DV) * 4);
     a.e = take((size_t)(units * kC * DV) * 4);
@@ -368,7 +382,8 @@ hipError_t launch_delta_step(const DeltaArgs& a, int type, hipStream_t s) {
   return by_type(type, [&](auto tag) {
     return by_keys(a.DK, [&](auto keys) {
       constexpr int parts = 2 * decltype(keys)::value;
-      return enqueue(delta_step_kernel<typename decltype(tag)::type, parts>,
+      using T = typename decltype(tag)::type;
+      return enqueue(a.DV % 4 == 0 ? delta_step_kernel<T, parts, true> : delta_step_kernel<T, parts, false>,
                      dim3((uint32_t)(a.B * a.H * slices)), dim3(32 * parts), 0, s, a, slices);
     });
   });

@@ -30,26 +30,48 @@ __device__ __forceinline__ uint32_t token_at(const EmbedArgs& a, int64_t n) {
 
 // ---------------------------------------------------------------------- forward
 
-// 2^lg lanes to a row, W columns to a lane at a time.
+// 2^lg lanes to a row and kRows rows one after the other, W columns to a lane at a time;
+// the rows' loads are all on their way before the first is stored.
+constexpr int kRows = 4;
 template <typename F, typename T, int W>
 __global__ __launch_bounds__(256) void embed_forward_kernel(EmbedArgs a, int lg) {
   const uint32_t lane = threadIdx.x & ((1u << lg) - 1);
-  const int64_t n = ((int64_t)blockIdx.x << (8 - lg)) + (threadIdx.x >> lg);
-  if (n >= a.N) return;
-  const uint32_t token = token_at(a, n);
-  const bool there = token < (uint32_t)a.V;
-  const F* from = static_cast<const F*>(a.src) + (there ? (int64_t)token * a.src_stride : 0);
-  T* to = static_cast<T*>(a.dst) + n * a.dst_stride;
+  const int64_t step = (int64_t)256 >> lg;  // rows of the workgroup at a time
+  const int64_t n0 = (int64_t)blockIdx.x * kRows * step + (threadIdx.x >> lg);
   const uint32_t D = (uint32_t)a.D;
-  for (uint32_t col = lane * W; col < D; col += (uint32_t)W << lg) {
-    float v[W];
-    if (col + W <= D) {
-      unpack<F, W>(load_pack<F, W>(from + col), v);
+  uint32_t token[kRows];
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = there ? v[i] * a.scale : 0.0f;
-      store_vals<T, W>(to + col, v);
-    } else {
-      for (uint32_t c = col; c < D; ++c) to[c] = (T)(there ? (float)from[c] * a.scale : 0.0f);
+  for (int r = 0; r < kRows; ++r) token[r] = n0 + r * step < a.N ? token_at(a, n0 + r * step) : (uint32_t)a.V;
+  for (uint32_t col = lane * W; col < D; col += (uint32_t)W << lg) {
+    Pack<F, W> v[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const bool there = token[r] < (uint32_t)a.V;
+      const F* from = static_cast<const F*>(a.src) + (there ? (int64_t)token[r] * a.src_stride : 0);
+      if (col + W <= D) {
+        v[r] = load_pack<F, W>(from + col);
+      } else {
+        const uint32_t last = D - 1 - col;
+#pragma unroll
+        for (uint32_t i = 0; i < W; ++i) v[r].v[i] = from[col + min(i, last)];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (n0 + r * step >= a.N) break;
+      const bool there = token[r] < (uint32_t)a.V;
+      T* to = static_cast<T*>(a.dst) + (n0 + r * step) * a.dst_stride + col;
+      float x[W];
+      unpack<F, W>(v[r], x);
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = there ? x[i] * a.scale : 0.0f;
+      if (col + W <= D) {
+        store_vals<T, W>(to, x);
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (col + i < D) to[i] = (T)x[i];
+      }
     }
   }
 }
@@ -424,7 +446,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, uint32_t sl
 
 // A token that begins in a chunk and goes on in others: a workgroup adds its parts in the
 // chunks' order, a run of them to each of its waves.  Most find nothing to do.
-constexpr int kJoinWaves = 8;
+constexpr int kJoinWaves = 16;
 template <typename G>
 __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs a, uint32_t slices,
                                                                     int64_t chunks) {
@@ -438,14 +460,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs a
   const uint32_t key = a.keys[i1], last = a.keys[i1 - 1], head = a.keys[i0];
   const uint32_t past = first > 0 ? a.keys[i0 - 1] : 0xFFFFFFFFu;
   if (key >= (uint32_t)a.V || last != key || (head == key && past == key)) return;
-  // chunks behind the first that begin with the token
+  // chunks behind the first that begin with the token: they follow each other
   int64_t more = 1;
   for (;;) {
-    const int64_t c = first + 1 + more + lane;
-    const uint64_t on = __ballot(c < chunks && a.keys[min(c, chunks - 1) << a.lg_rows] == key);
-    const int n = on == ~0ull ? 64 : __builtin_ctzll(~on);
+    const int64_t c = first + 1 + more + threadIdx.x;
+    const int n = __syncthreads_count(c < chunks && a.keys[min(c, chunks - 1) << a.lg_rows] == key);
     more += n;
-    if (n < 64) break;
+    if (n < 64 * kJoinWaves) break;
   }
   // part 1 of the first chunk, then part 0 of the others
   const int64_t per = (more + kJoinWaves) / kJoinWaves;  // of more + 1 parts
@@ -469,7 +490,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs a
       add(part + a.D);
       j = 1;
     }
-#pragma unroll 8
+#pragma unroll 16
     for (; j < hi; ++j) add(part + j * 2 * a.D);
   }
 #pragma unroll
@@ -536,7 +557,7 @@ hipError_t launch_embed_forward(const EmbedArgs& a, int table_type, int out_type
       constexpr int W = sizeof(F) == 4 && sizeof(T) == 4 ? 4 : 8;
       int lg = 0;
       while (lg < 8 && ((int64_t)W << lg) < a.D) ++lg;
-      const int64_t rows = 256 >> lg;
+      const int64_t rows = kRows * (256 >> lg);
       return enqueue(embed_forward_kernel<F, T, W>, dim3((uint32_t)((a.N + rows - 1) / rows)),
                      dim3(256), 0, s, a, lg);
     });

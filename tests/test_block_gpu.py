@@ -485,6 +485,22 @@ def test_delta_step(B, H, HK, DK, DV, dtype):
     assert torch.isfinite(o3.float()).all() and torch.isfinite(s3).all()
 
 
+def test_delta_step_fills_the_chip():
+    """Every store of a state waits behind many others."""
+    p = per()
+    B, H, D = 256, 16, 128
+    host, dev = delta_case(1, 1, H, H, D, D, "f32", 12)
+    want = O.delta_all(*(host[x] for x in "qkvgb"), s0=host["s0"], scale=host["scale"])
+    tol = O.delta_tolerance(O.delta_size(*(host[x] for x in "qkvgb"), s0=host["s0"], scale=host["scale"]), want,
+                            torch.float32)
+    one = [dev[x][:, 0].expand(B, *dev[x].shape[2:]) for x in "qkvgb"]
+    s0 = dev["s0"].repeat(B, 1, 1, 1)
+    for _ in range(3):
+        o, s = p.per_delta_step(*one, s0, scale=dev["scale"], s_out=torch.empty_like(s0))
+        assert same(s, s[:1].expand_as(s)) and same(o, o[:1].expand_as(o))
+        assert_close(s[0], want["s"][0], tol["s"][0], "s")
+
+
 def test_delta_steps_follow_the_sequence():
     p = per()
     B, T, H, D = 2, 70, 2, 32
