@@ -244,17 +244,20 @@ __global__ __launch_bounds__(32 * PARTS) void delta_step_kernel(DeltaArgs a, int
         v[r][i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(from, off[i], r * pitch, 0));
     }
   }
-  {
-    const int i = threadIdx.x, c = i % (16 * PARTS);
-    const T* row = i < 16 * PARTS ? at<T>(a.k, b, 0, hk) : at<T>(a.q, b, 0, hk);
-    ks[i / (16 * PARTS)][c] = c < a.DK ? (float)row[c] : 0.0f;
-  }
-  f4 x = {};
+  // no load waits for another: places past an end read the last value
+  const int kq = threadIdx.x, kc = kq % (16 * PARTS);
+  const T* row = kq < 16 * PARTS ? at<T>(a.k, b, 0, hk) : at<T>(a.q, b, 0, hk);
+  const T* values = at<T>(a.v, b, 0, h);
+  const T one = row[min(kc, a.DK - 1)];
+  T few[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (col + i < a.DV) x[i] = (float)at<T>(a.v, b, 0, h)[col + i];
+  for (int i = 0; i < 4; ++i) few[i] = values[min(col + i, a.DV - 1)];
   const float gate = (float)*at<T>(a.g, b, 0, h), wt = (float)*at<T>(a.b, b, 0, h);
   const bool reset = a.reset && a.reset[b];
+  ks[kq / (16 * PARTS)][kc] = kc < a.DK ? (float)one : 0.0f;
+  f4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = col + i < a.DV ? (float)few[i] : 0.0f;
   const float f = 1.0f / (1.0f + expf(-gate)), w = 1.0f / (1.0f + expf(-wt));
   __syncthreads();
   f4 kv = {}, qv = {};

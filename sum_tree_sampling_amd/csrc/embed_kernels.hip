@@ -446,12 +446,10 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, uint32_t sl
 
 // A token that begins in a chunk and goes on in others: a workgroup adds its parts in the
 // chunks' order, a run of them to each of its waves.  Most find nothing to do.
-constexpr int kJoinWaves = 16;
-template <typename G>
-__global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs a, uint32_t slices,
-                                                                    int64_t chunks) {
+template <typename G, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void embed_join_kernel(EmbedArgs a, uint32_t slices, int64_t chunks) {
   constexpr int W = 4;
-  __shared__ float sum[kJoinWaves][64][W];
+  __shared__ float sum[WAVES][64][W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int64_t first = blockIdx.x / slices;
   const uint32_t col = ((uint32_t)(blockIdx.x % slices) * 64 + lane) * W;
@@ -466,10 +464,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs a
     const int64_t c = first + 1 + more + threadIdx.x;
     const int n = __syncthreads_count(c < chunks && a.keys[min(c, chunks - 1) << a.lg_rows] == key);
     more += n;
-    if (n < 64 * kJoinWaves) break;
+    if (n < 64 * WAVES) break;
   }
   // part 1 of the first chunk, then part 0 of the others
-  const int64_t per = (more + kJoinWaves) / kJoinWaves;  // of more + 1 parts
+  const int64_t per = (more + WAVES) / WAVES;  // of more + 1 parts
   const int64_t lo = wave * per, hi = min(more + 1, lo + per);
   float acc[W] = {};
   if (col < D) {
@@ -498,7 +496,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs a
   __syncthreads();
   if (wave == 0 && col < D) {
 #pragma unroll
-    for (int w = 1; w < kJoinWaves; ++w)
+    for (int w = 1; w < WAVES; ++w)
 #pragma unroll
       for (int i = 0; i < W; ++i) acc[i] += sum[w][lane][i];
     write_sum<G, W>(a, key, col, acc);
@@ -608,8 +606,9 @@ hipError_t launch_embed_backward(EmbedArgs a, int dout_type, int grad_type, hipS
     });
     if (e != hipSuccess || chunks < 2) return e;
     const uint32_t slices = (uint32_t)((a.D + 255) / 256);
-    return enqueue(embed_join_kernel<G>, dim3((uint32_t)((chunks - 1) * slices)),
-                   dim3(64 * kJoinWaves), 0, s, a, slices, chunks);
+    const int waves = chunks > a.V ? 16 : 4;
+    return enqueue(waves == 16 ? embed_join_kernel<G, 16> : embed_join_kernel<G, 4>,
+                   dim3((uint32_t)((chunks - 1) * slices)), dim3(64 * waves), 0, s, a, slices, chunks);
   });
 }
 
