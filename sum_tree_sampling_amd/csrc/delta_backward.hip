@@ -4,7 +4,9 @@
 namespace per {
 namespace {
 
-// Backward in time: dS behind each chunk, E, and dV.
+// Backward in time: dS behind each chunk, E, and dV.  As the forward pass it is bound by a
+// chain of products in each chunk: 225 us for 32 sequences of 512 steps, 16 heads of 128 x
+// 128 bf16.
 template <typename T, int KT, int WAVES, bool LOCAL>
 __global__ __launch_bounds__(64 * WAVES)
 __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES == 4 && !LOCAL ? 1 : 4))) void delta_reverse_kernel(
@@ -232,6 +234,11 @@ __device__ __forceinline__ void take_piece(const T* base, int64_t stride, bool e
 // has 16 columns of dQ and dK (dt) and NI of the chunk's 4 groups of rows.  The next 64
 // columns' rows are on their way while these are computed, and the states' while the
 // 64 x 64 products are.
+//
+// 457 us for 32 sequences of 512 steps, 16 heads of 128 x 128 bf16 on 8 heads of keys: 27
+// us for each chunk and head, of which its 190 KB at an equal share of the copy's rate are
+// 10.  One workgroup fills a CU (240 registers a wave), so loads that are not asked for
+// ahead, the barriers and the way from one head to the next show.
 //
 // SHARED: several value heads to a head of keys, whose dQ and dK are added up.
 template <typename T, int KT, bool SHARED>

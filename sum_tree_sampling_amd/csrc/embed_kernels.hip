@@ -7,6 +7,12 @@
 // inside one chunk is written at once; what chunks share goes to the workspace, and a
 // second launch adds a token's parts in order, so a token that is half of all rows is
 // summed by as many waves as the others.  No sum is made with atomics.
+//
+// Memory bounds the large calls: 65536 tokens of 65536 x 1024 (f32 table and gradient,
+// bf16 rows) take 50 us forward (293 MB, 5.9 TB/s) and 94 us for the sums (402 MB, 4.3
+// TB/s, rows in the tokens' order), beside 22 us of sorting (four launches, each 2 to 7)
+// and 9 us of joins.  20001 x 333 f32 of 501 tokens, 40 % of them one, take 10 us forward
+// and 12 + 10 + 16: five launches in order, each a chain of dependent loads.
 #include <algorithm>
 
 #include "block_internal.h"
@@ -31,7 +37,8 @@ __device__ __forceinline__ uint32_t token_at(const EmbedArgs& a, int64_t n) {
 // ---------------------------------------------------------------------- forward
 
 // 2^lg lanes to a row and kRows rows one after the other, W columns to a lane at a time;
-// the rows' loads are all on their way before the first is stored.
+// the rows' loads are all on their way before the first is stored (20001 x 333 f32: 9.8
+// us, and 10.5 with one row at a time).
 constexpr int kRows = 4;
 template <typename F, typename T, int W>
 __global__ __launch_bounds__(256) void embed_forward_kernel(EmbedArgs a, int lg) {
@@ -118,30 +125,21 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* space)
   return base + s - v;
 }
 
-// Up to 1024 * ITEMS tokens by one workgroup, all passes in LDS.
-template <int ITEMS>
+// Up to kSmall tokens by one workgroup, all passes in LDS, a token to a thread.
+constexpr int64_t kSmall = 1024;
 __global__ __launch_bounds__(1024) void embed_sort_small_kernel(EmbedArgs a, int bits, int passes) {
   __shared__ uint32_t cnt[16][kBins];
-  __shared__ uint32_t keys[1024 * ITEMS], pos[1024 * ITEMS];
+  __shared__ uint32_t keys[kSmall], pos[kSmall];
   __shared__ uint32_t space[16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-  const uint32_t N = (uint32_t)a.N;
-  uint32_t k[ITEMS], p[ITEMS], r[ITEMS];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    p[i] = (uint32_t)(wave * ITEMS + i) * 64 + lane;
-    k[i] = p[i] < N ? token_at(a, p[i]) : 0;
-  }
+  const int wave = threadIdx.x / 64;
+  const bool valid = threadIdx.x < (uint32_t)a.N;
+  uint32_t p = threadIdx.x, k = valid ? token_at(a, p) : 0;
+  const uint32_t mask = (1u << bits) - 1;
   for (int pass = 0; pass < passes; ++pass) {
-    const uint32_t mask = (1u << bits) - 1;
     const int shift = pass * bits;
     for (int j = threadIdx.x; j < 16 * kBins; j += 1024) (&cnt[0][0])[j] = 0;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const bool valid = (uint32_t)(wave * ITEMS + i) * 64 + lane < N;
-      r[i] = wave_rank(k[i] >> shift & mask, valid, bits, cnt[wave]);
-    }
+    const uint32_t rank = wave_rank(k >> shift & mask, valid, bits, cnt[wave]);
     __syncthreads();
     uint32_t total = 0;
     if (threadIdx.x < kBins) {
@@ -158,37 +156,27 @@ __global__ __launch_bounds__(1024) void embed_sort_small_kernel(EmbedArgs a, int
       for (int w = 0; w < 16; ++w) cnt[w][threadIdx.x] += base;
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const bool valid = (uint32_t)(wave * ITEMS + i) * 64 + lane < N;
-      if (valid) {
-        const uint32_t to = cnt[wave][k[i] >> shift & mask] + r[i];
-        keys[to] = k[i];
-        pos[to] = p[i];
-      }
+    if (valid) {
+      const uint32_t to = cnt[wave][k >> shift & mask] + rank;
+      keys[to] = k;
+      pos[to] = p;
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const uint32_t at = (uint32_t)(wave * ITEMS + i) * 64 + lane;
-      if (at < N) {
-        k[i] = keys[at];
-        p[i] = pos[at];
-      }
+    if (valid) {
+      k = keys[threadIdx.x];
+      p = pos[threadIdx.x];
     }
   }
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const uint32_t at = (uint32_t)(wave * ITEMS + i) * 64 + lane;
-    if (at < N) {
-      a.keys[at] = k[i];
-      a.pos[at] = p[i];
-    }
+  if (valid) {
+    a.keys[threadIdx.x] = k;
+    a.pos[threadIdx.x] = p;
   }
 }
 
 // More of them: a block has `per` consecutive items, and each pass is two launches, the
-// digits' counts of each block and the scatter.
+// digits' counts of each block and the scatter.  With 8 tokens to a thread one workgroup
+// could sort 8192, but takes longer than these four launches (the whole gradient of 50000 x
+// 64 f32: 2049 tokens 24.4 and 23.1 us, 8192 tokens 28.7 and 25.4).
 constexpr int kSortThreads = 1024, kSortTile = 1024;  // a wave has 64 items of a tile
 
 __device__ __forceinline__ uint32_t sort_key(const EmbedArgs& a, const uint32_t* keys, int64_t n) {
@@ -445,7 +433,10 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, uint32_t sl
 }
 
 // A token that begins in a chunk and goes on in others: a workgroup adds its parts in the
-// chunks' order, a run of them to each of its waves.  Most find nothing to do.
+// chunks' order, a run of them to each of its waves.  Most find nothing to do.  16 waves
+// where there are more chunks than tokens, so that a token has many parts (1251 chunks of
+// 501 tokens: 16.2 us, 21 with 4 waves that add 8 parts at a time), else 4, which come and go faster
+// (1024 chunks of 65536 tokens: 8.8 us, 23.5 with 16).
 template <typename G, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void embed_join_kernel(EmbedArgs a, uint32_t slices, int64_t chunks) {
   constexpr int W = 4;
@@ -512,8 +503,6 @@ hipError_t by_type(int type, F f) {
   }
 }
 
-constexpr int64_t kSmall = 8192;  // tokens that one workgroup sorts
-
 // Blocks of a sorting pass.
 int64_t sort_blocks(int64_t N) { return std::min<int64_t>(256, (N + kSortTile - 1) / kSortTile); }
 
@@ -568,11 +557,7 @@ hipError_t launch_embed_backward(EmbedArgs a, int dout_type, int grad_type, hipS
   const int passes = (all + 8) / 9, bits = (all + passes - 1) / passes;
   hipError_t e = hipSuccess;
   if (a.N > 0 && a.N <= kSmall) {
-    if (a.N <= 1024) {
-      e = enqueue(embed_sort_small_kernel<1>, dim3(1), dim3(1024), 0, s, a, bits, passes);
-    } else {
-      e = enqueue(embed_sort_small_kernel<8>, dim3(1), dim3(1024), 0, s, a, bits, passes);
-    }
+    e = enqueue(embed_sort_small_kernel, dim3(1), dim3(1024), 0, s, a, bits, passes);
   } else if (a.N > 0) {
     const int64_t blocks = sort_blocks(a.N);
     const int64_t per = ((a.N + blocks - 1) / blocks + kSortTile - 1) / kSortTile * kSortTile;

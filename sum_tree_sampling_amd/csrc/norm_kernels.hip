@@ -8,6 +8,11 @@
 // Backward, a group of lanes walks over rows and keeps its columns' sums for the
 // weight and the bias in registers; a block's sums go to memory once, and a second
 // launch adds the blocks in order.
+//
+// Memory bounds the large calls: 65536 x 2048 bf16 take 104 us forward (5.2 TB/s) and 161
+// us backward (5.0 TB/s, a large copy reaches 4.84), and 8 us for the join of 1536 blocks.
+// Small ones wait for their launches and loads: 4095 x 1001 f16 take 8 + 12 + 4 us, 512 x
+// 1024 f32 forward 4.8.
 #include <algorithm>
 
 #include "block_internal.h"
@@ -465,7 +470,10 @@ constexpr uint32_t longest(int type) { return 2u * 1024 * (type == PER_F32 ? 4 :
 }  // namespace
 
 // Blocks of the backward pass: enough to fill the chip, few enough that their sums
-// are little next to the rows.
+// are little next to the rows.  Rows of 128 to 256 packs go to 256 threads and 6 blocks of
+// a CU, whose registers leave room for as many: with a wave to a row of 4 packs a lane
+// 65536 x 2048 bf16 took 221 us, so 161; with 5 blocks to a CU, and the rest in a second
+// round, 200 to 225.
 size_t norm_workspace(int64_t N, int64_t D, int type, NormArgs* a, void* ws) {
   const uint32_t vec = type == PER_F32 ? 4 : 8;
   const int64_t rows = D <= 128 * vec ? 4 : 1;  // rows that a block has at once
