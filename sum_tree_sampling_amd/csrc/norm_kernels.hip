@@ -469,15 +469,24 @@ constexpr uint32_t longest(int type) { return 2u * 1024 * (type == PER_F32 ? 4 :
 
 }  // namespace
 
-// Blocks of the backward pass: enough to fill the chip, few enough that their sums
-// are little next to the rows.  Rows of 128 to 256 packs go to 256 threads and 6 blocks of
-// a CU, whose registers leave room for as many: with a wave to a row of 4 packs a lane
-// 65536 x 2048 bf16 took 221 us, so 161; with 5 blocks to a CU, and the rest in a second
-// round, 200 to 225.
+// Blocks of the backward pass: enough to fill the chip, few enough that their sums are
+// little next to the rows (bf16, us):
+//   65536 x 1024   1024 blocks 80,  512 blocks 103
+//    4095 x 1001   1024 blocks 18.7, 512 blocks 15.8, 256 blocks 18.1 (f16)
+//    2000 x 1024    512 blocks 14.3, 256 blocks 10.4
+//    1000 x 2048   1000 blocks 20.4, 256 blocks 11.4
+// Rows of 128 to 256 packs go to 256 threads and 6 blocks of a CU, whose registers leave
+// room for as many: with a wave to a row of 4 packs a lane 65536 x 2048 bf16 took 221 us,
+// so 161; with 5 blocks to a CU, and the rest in a second round, 200 to 225.
 size_t norm_workspace(int64_t N, int64_t D, int type, NormArgs* a, void* ws) {
   const uint32_t vec = type == PER_F32 ? 4 : 8;
   const int64_t rows = D <= 128 * vec ? 4 : 1;  // rows that a block has at once
-  const int64_t most = D <= 128 * vec ? 512 : D <= 256 * vec ? 1536 : D <= 1024 * vec ? 512 : 256;
+  int64_t most = 256;
+  if (D <= 128 * vec) {
+    most = N <= 2048 ? 256 : N <= 16384 ? 512 : 1024;
+  } else if (D <= 1024 * vec) {
+    most = std::clamp<int64_t>(N / 4, 256, D <= 256 * vec ? 1536 : 512);
+  }
   const int64_t blocks = N == 0 ? 0 : std::min(most, (N + rows - 1) / rows);
   const size_t part = (size_t)blocks * 2 * (size_t)D * 4;
   if (a) {
